@@ -116,6 +116,16 @@ enum { KVR_DTYPE_BF16 = 0, KVR_DTYPE_FP32 = 1 };
  * written).  Half the stitch's traffic; the output is the same, bit for bit. */
 #define KVR_PREFILL_SKIP_PREFIX_CACHE 2u
 
+/* kvr_key_weights flag: add to the weights that are there instead of replacing
+ * them. */
+#define KVR_WEIGHTS_ACCUMULATE 1u
+
+/* kvr_evict flag: keys are moved bit for bit, keeping the rotation they have
+ * (a cache of composite positions, whose rows are not at positions equal to
+ * their row); by default a key that moves from row r to row i is turned by
+ * i - r positions. */
+#define KVR_EVICT_KEEP_ROTATION 1u
+
 typedef struct kvr_pool *kvr_pool_t;
 
 /*
@@ -314,6 +324,119 @@ KVR_API kvr_status kvr_prefill(kvr_pool_t pool, int32_t batch, const int32_t *sp
                                uint32_t flags, const int32_t *q_offsets, const void *q,
                                const void *kq, const void *vq, void *out, float softmax_scale,
                                void *stream);
+
+/*
+ * kvr_shared_query_attention -- query attention over a prefix that a group of
+ * requests shares.
+ *
+ * Requests answered from the same retrieved spans have the same stitched
+ * prefix (CoinRAG blog section 2.3, C_ctx).  It is stitched once, into a block
+ * of its own (kvr_assemble with one request per group), and each request keeps
+ * a block of what follows it: its earlier query and decoded tokens.  Group g's
+ * requests are group_offsets[g] .. group_offsets[g+1]-1; its prefix block
+ * holds P_g rows.  Request b of group g owns S_b rows, at positions
+ * P_g .. P_g + S_b - 1.  Query token t sits at position P_g + S_b + t: the call
+ * rotates its query heads and its key there, appends its key and value at own
+ * row S_b + t, and computes
+ *   O[l, q_offsets[b]+t, h] = sum_j softmax_j(scale * <q, k_j>) v_j
+ * over the P_g prefix rows and own rows 0..S_b + t.  The result is that of
+ * kvr_query_attention on a cache holding both one behind the other, up to
+ * rounding order; the prefix is read once for the group, not once per request.
+ *
+ *   group_offsets  host [n_groups+1], non-decreasing, group_offsets[0] = 0;
+ *                  batch = group_offsets[n_groups]
+ *   prefix_offsets host [n_groups+1] rows: group g's block of the prefix
+ *                  caches, laid out as in kvr_assemble
+ *   prefix_len     host [n_groups] P_g (0: the group shares nothing)
+ *   prefix_k, prefix_v  device, read only (NULL if every P_g is 0)
+ *   cache_offsets  host [batch+1] rows: the requests' own blocks; need
+ *                  S_b + Lq_b <= R_b
+ *   own_len        host [batch] S_b
+ *   q_offsets, q, kq, vq, out, softmax_scale as in kvr_query_attention
+ *
+ * Requests without query tokens, and rows of a block behind its last query
+ * row, are left as they are.  A batch of at most 64 requests passes its tables
+ * inside the kernels' parameters.
+ * On a stream that is being captured the call returns KVR_ERR_UNSUPPORTED when
+ * it would have to bind the pool, upload tables or use library scratch.
+ * Errors: KVR_ERR_INVALID_ARG (also: the caches or `out` overlap the prefix),
+ * KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA; kvr_check reports
+ * KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for kvr_query_attention.
+ */
+KVR_API kvr_status kvr_shared_query_attention(kvr_pool_t pool, int32_t n_groups, const int32_t *group_offsets,
+                                              const int64_t *prefix_offsets, const int32_t *prefix_len,
+                                              const void *prefix_k, const void *prefix_v,
+                                              const int64_t *cache_offsets, const int32_t *own_len,
+                                              const int32_t *q_offsets, const void *q, const void *kq,
+                                              const void *vq, void *cache_k, void *cache_v, void *out,
+                                              float softmax_scale, void *stream);
+
+/*
+ * kvr_key_weights -- the attention weight that each cached key receives.
+ *
+ * For every (layer, kv-head) block and row j < P_b + Lq_b of request b:
+ *   weights[j] = sum over query tokens t and the G query heads of the kv head
+ *                of softmax_j(scale * <rot(q, P_b + t), k_j>), j <= P_b + t,
+ * the probabilities of kvr_query_attention with the same arguments, summed
+ * over its query rows: after that call, with the same prefix_len, q_offsets
+ * and q, the cache holds the keys these sums run over.  Queries are rotated in
+ * fp32 and not rounded to the cache's type; sums are fp32.
+ *
+ *   weights  device fp32, one value per cache row: request b's block starts at
+ *            element cache_offsets[b] * n_layers * n_kv_heads, inside it
+ *            [n_layers][n_kv_heads][R_b].  Rows 0..P_b + Lq_b - 1 are written
+ *            (or, with KVR_WEIGHTS_ACCUMULATE, added to); rows behind them are
+ *            left as they are.  A request without query tokens gets zeros (or
+ *            nothing is added).
+ *   flags    0 or KVR_WEIGHTS_ACCUMULATE
+ * The other arguments mean what they mean in kvr_query_attention; cache_k is
+ * read only.  On a stream that is being captured the call returns
+ * KVR_ERR_UNSUPPORTED when it would have to bind the pool or upload tables
+ * (more than 64 requests).
+ * Errors: KVR_ERR_INVALID_ARG, KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED,
+ * KVR_ERR_CUDA; kvr_check reports KVR_ERR_DEVICE_CHECK for a query row whose
+ * softmax denominator is not finite and positive.
+ */
+KVR_API kvr_status kvr_key_weights(kvr_pool_t pool, int32_t batch, const int64_t *cache_offsets,
+                                   const int32_t *prefix_len, const int32_t *q_offsets, const void *q,
+                                   const void *cache_k, float *weights, float softmax_scale, uint32_t flags,
+                                   void *stream);
+
+/*
+ * kvr_evict -- cut each request's cache to its heaviest rows.
+ *
+ * Of the kv_len[b] rows that every (layer, kv-head) block of request b holds,
+ * the first n_first, the last n_recent and the rows of largest weight between
+ * them stay, k_b = min(keep[b], kv_len[b]) in all, each block choosing its own
+ * (equal weights: the lowest row stays; a NaN weighs less than any number).
+ * They keep their order: row kept[i] moves to row i, its value and weight
+ * copied, its key turned by i - kept[i], so that the kept rows again form one
+ * contiguous prefix at positions 0..k_b - 1 and kvr_query_attention carries on
+ * with prefix_len = k_b (rounded to the cache's type once more).  A block of
+ * own rows behind a shared prefix (kvr_shared_query_attention) is evicted the
+ * same way.
+ *
+ *   weights      device fp32, laid out as in kvr_key_weights
+ *   dst_offsets  host [batch+1] rows: the blocks of dst_k, dst_v and
+ *                dst_weights; need R'_b >= k_b.  The call works in place when
+ *                a destination is its source with equal offsets; otherwise
+ *                destinations and sources must not overlap.
+ *   dst_weights  device fp32 or NULL: row i of a block gets the weight of row
+ *                kept[i], rows k_b..R'_b - 1 get 0
+ *   kept         device int32: request b's rows start at element
+ *                (k_0 + .. + k_b-1) * n_layers * n_kv_heads, inside it
+ *                [n_layers][n_kv_heads][k_b], ascending
+ *   flags        0 or KVR_EVICT_KEEP_ROTATION
+ * Rows k_b.. of the destination's keys and values are left as they are.
+ * Capture: as kvr_key_weights.
+ * Errors: KVR_ERR_INVALID_ARG (also: keep[b] < n_first + n_recent, or
+ * overlapping arguments), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED,
+ * KVR_ERR_CUDA.
+ */
+KVR_API kvr_status kvr_evict(kvr_pool_t pool, int32_t batch, const int64_t *cache_offsets, const int32_t *kv_len,
+                             const int32_t *keep, int32_t n_first, int32_t n_recent, const float *weights,
+                             const void *cache_k, const void *cache_v, const int64_t *dst_offsets, void *dst_k,
+                             void *dst_v, float *dst_weights, int32_t *kept, uint32_t flags, void *stream);
 
 /* Attention kernels a pool can select (kvr_attention_path). */
 enum { KVR_PATH_UNBOUND = -1, KVR_PATH_CUDA_CORES = 0, KVR_PATH_TCGEN05 = 1 };

@@ -19,6 +19,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <string>
 #include <vector>
 
@@ -1243,6 +1244,468 @@ extern "C" kvr_status kvr_prefill(kvr_pool_t p, int32_t batch, const int32_t *sp
     if (ap.slot)
         cudaEventRecord(ap.slot->done, s);
     return st;
+}
+
+// ---------------------------------------------------------------------------
+// shared prefixes, key weights, eviction
+// ---------------------------------------------------------------------------
+namespace {
+
+// One shared-prefix call: its request table, and the append of the query
+// tokens' keys and values.
+struct SharedPlan {
+    std::vector<DevShared> rq;
+    int32_t max_lq = 0;
+    SharedTable tab;
+    AssembleTables atab;
+};
+
+// A C entry point lets no exception out (the tables are std::vectors).
+template <typename F>
+kvr_status guarded(F &&f)
+{
+    try {
+        return f();
+    } catch (const std::exception &e) {
+        return fail(KVR_ERR_CUDA, "host allocation failed: %s", e.what());
+    }
+}
+
+// A call on a stream that is being captured may only enqueue kernels: binding
+// the pool, staging slots and scratch wait, allocate or are reused by later
+// calls, which a replayed graph would not see.
+kvr_status check_capture(const kvr_pool &p, cudaStream_t s, bool kernels_only, const char *why)
+{
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &c) != cudaSuccess) {
+        cudaGetLastError();
+        if (p.ready)   // no GPU, or a legacy stream beside a capture: the launch itself will report it
+            return KVR_OK;
+        c = cudaStreamCaptureStatusNone;
+    }
+    if (c == cudaStreamCaptureStatusNone)
+        return KVR_OK;
+    if (!p.ready)
+        return fail(KVR_ERR_UNSUPPORTED, "the stream is being captured: bind the pool first (kvr_pool_reserve)");
+    if (!kernels_only)
+        return fail(KVR_ERR_UNSUPPORTED, "the stream is being captured: %s", why);
+    return KVR_OK;
+}
+
+// The table `rows` on the device, through the next staging slot (whose event
+// the caller records after the kernels that read it).
+kvr_status upload_table(kvr_pool *p, const void *rows, size_t bytes, cudaStream_t s, Slot **slot)
+{
+    kvr_status st;
+    if ((st = p->acquire(bytes, bytes, slot)) != KVR_OK)
+        return st;
+    std::memcpy((*slot)->host, rows, bytes);
+    const cudaError_t e = cudaMemcpyAsync((*slot)->dev, (*slot)->host, bytes, cudaMemcpyHostToDevice, s);
+    cudaEventRecord((*slot)->done, s);
+    (*slot)->used = true;
+    return e == cudaSuccess ? KVR_OK : cuda_fail(e, "table upload");
+}
+
+struct Range {
+    const char *lo, *hi;
+    bool meets(const Range &o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
+};
+Range range_of(const void *p, int64_t first, int64_t last, int64_t bytes)
+{
+    const char *c = static_cast<const char *>(p);
+    return c ? Range{c + first * bytes, c + last * bytes} : Range{nullptr, nullptr};
+}
+
+}  // namespace
+
+extern "C" kvr_status kvr_shared_query_attention(kvr_pool_t p, int32_t n_groups, const int32_t *group_offsets,
+                                                 const int64_t *prefix_offsets, const int32_t *prefix_len,
+                                                 const void *prefix_k, const void *prefix_v,
+                                                 const int64_t *cache_offsets, const int32_t *own_len,
+                                                 const int32_t *q_offsets, const void *q, const void *kq,
+                                                 const void *vq, void *cache_k, void *cache_v, void *out,
+                                                 float softmax_scale, void *stream)
+{
+    if (!p)
+        return fail(KVR_ERR_INVALID_ARG, "pool is NULL");
+    if (n_groups < 0)
+        return fail(KVR_ERR_INVALID_ARG, "n_groups %d", n_groups);
+    if (n_groups == 0)
+        return KVR_OK;
+    NvtxRange call("kvr_shared_query_attention");
+    return guarded([&]() -> kvr_status {
+        kvr_status st;
+        if ((st = check_offsets32(group_offsets, n_groups, "group_offsets")) != KVR_OK)
+            return st;
+        const int32_t batch = group_offsets[n_groups];
+        if (batch == 0)
+            return KVR_OK;
+        if ((st = check_cache_offsets(prefix_offsets, n_groups)) != KVR_OK ||
+            (st = check_cache_offsets(cache_offsets, batch)) != KVR_OK ||
+            (st = check_offsets32(q_offsets, batch, "q_offsets")) != KVR_OK)
+            return st;
+        if (!prefix_len || !own_len)
+            return fail(KVR_ERR_INVALID_ARG, "prefix_len / own_len is NULL");
+        if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale))
+            return fail(KVR_ERR_INVALID_ARG, "softmax_scale %g", (double)softmax_scale);
+        bool any_prefix = false;
+        for (int g = 0; g < n_groups; ++g) {
+            if (prefix_len[g] < 0 || prefix_len[g] > prefix_offsets[g + 1] - prefix_offsets[g])
+                return fail(KVR_ERR_OUT_OF_RANGE, "group %d: prefix %d rows outside its block of %lld", g, prefix_len[g],
+                            (long long)(prefix_offsets[g + 1] - prefix_offsets[g]));
+            any_prefix = any_prefix || prefix_len[g] > 0;
+        }
+        const int L = p->d.n_layers, H = p->d.n_kv_heads, Hq = p->d.n_q_heads, D = p->d.head_dim, LH = L * H;
+        const int32_t T = q_offsets[batch];
+        SharedPlan pl;
+        pl.rq.reserve(batch);
+        for (int g = 0; g < n_groups; ++g)
+            for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b) {
+                const int64_t cap = cache_offsets[b + 1] - cache_offsets[b];
+                const int32_t lq = q_offsets[b + 1] - q_offsets[b];
+                if (own_len[b] < 0 || (int64_t)own_len[b] + lq > cap)
+                    return fail(KVR_ERR_OUT_OF_RANGE, "request %d: own rows %d + query %d > cache block %lld", b,
+                                own_len[b], lq, (long long)cap);
+                if ((int64_t)prefix_len[g] + own_len[b] + lq > kMaxPosition)
+                    return fail(KVR_ERR_OUT_OF_RANGE, "request %d: positions beyond 2^24", b);
+                DevShared r{};
+                r.cache_row0 = cache_offsets[b] * LH;
+                r.pre_row0 = prefix_offsets[g] * LH;
+                r.cap = (int32_t)cap;
+                r.own = own_len[b];
+                r.pre_cap = (int32_t)(prefix_offsets[g + 1] - prefix_offsets[g]);
+                r.pre_len = prefix_len[g];
+                r.q_off = q_offsets[b];
+                r.q_len = lq;
+                pl.rq.push_back(r);
+                pl.max_lq = std::max(pl.max_lq, lq);
+            }
+        if (T == 0)
+            return KVR_OK;
+        const void *ptrs[] = {q, kq, vq, cache_k, cache_v, out};
+        for (const void *x : ptrs)
+            if (!x || !aligned16(x))
+                return fail(KVR_ERR_INVALID_ARG, "q / kq / vq / cache / out NULL or not 16-byte aligned");
+        if (any_prefix && (!prefix_k || !prefix_v || !aligned16(prefix_k) || !aligned16(prefix_v)))
+            return fail(KVR_ERR_INVALID_ARG, "prefix_k / prefix_v NULL or not 16-byte aligned");
+        const int64_t own_rows[2] = {cache_offsets[0] * LH, cache_offsets[batch] * LH};
+        const int64_t pre_rows[2] = {prefix_offsets[0] * LH, prefix_offsets[n_groups] * LH};
+        const int64_t row_bytes = (int64_t)D * p->elt();
+        const Range dst[3] = {range_of(cache_k, own_rows[0], own_rows[1], row_bytes),
+                              range_of(cache_v, own_rows[0], own_rows[1], row_bytes),
+                              range_of(out, 0, (int64_t)L * T * Hq, row_bytes)};
+        const Range src[2] = {range_of(prefix_k, pre_rows[0], pre_rows[1], row_bytes),
+                              range_of(prefix_v, pre_rows[0], pre_rows[1], row_bytes)};
+        for (const Range &d : dst)
+            for (const Range &x : src)
+                if (any_prefix && d.meets(x))
+                    return fail(KVR_ERR_INVALID_ARG, "the cache or the output overlaps the shared prefix");
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if ((st = check_capture(*p, s, batch <= kInlineEntries, "a call of more than 64 requests uploads its tables")) !=
+                KVR_OK ||
+            (st = ensure_device(p)) != KVR_OK)
+            return st;
+        DeviceGuard g(p->device);
+
+        // the query tokens' keys and values become own rows S_b .. S_b + Lq - 1,
+        // turned by their positions P_g + S_b + t
+        std::vector<DevSpan> ap;
+        std::vector<DevLocal> al;
+        for (const DevShared &r : pl.rq) {
+            if (r.q_len == 0)
+                continue;
+            DevSpan d{};
+            d.dst_row0 = r.cache_row0;
+            d.src = KVR_SRC_LOCAL | (int32_t)al.size();
+            d.len = r.q_len;
+            d.row = r.own;
+            d.pos0 = d.delta = r.pre_len + r.own;
+            d.cap = r.cap;
+            d.dstep = 1;
+            ap.push_back(d);
+            const int64_t off = (int64_t)r.q_off * H * row_bytes;
+            al.push_back(DevLocal{static_cast<const char *>(kq) + off, static_cast<const char *>(vq) + off,
+                                  (int64_t)T * H * D, D, (int64_t)H * D, r.q_len});
+        }
+        AssembleArgs a{};
+        a.rope = p->rope;
+        a.cache_k = cache_k;
+        a.cache_v = cache_v;
+        a.n_layers = L;
+        a.n_heads = H;
+        a.upc = 1;
+        a.interleaved = (p->d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
+        SharedArgs sa{};
+        sa.rope = p->rope;
+        sa.q = q;
+        sa.kq = kq;
+        sa.vq = vq;
+        sa.prefix_k = prefix_k;
+        sa.prefix_v = prefix_v;
+        sa.cache_k = cache_k;
+        sa.cache_v = cache_v;
+        sa.out = out;
+        sa.n_reqs = batch;
+        sa.n_layers = L;
+        sa.n_q_heads = Hq;
+        sa.n_kv_heads = H;
+        sa.total_q = T;
+        sa.max_q_len = pl.max_lq;
+        sa.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
+        sa.interleaved = a.interleaved;
+        sa.err = p->err;
+        Slot *slot = nullptr;
+        const bool inl = batch <= kInlineEntries;
+        if (inl) {
+            std::memcpy(pl.tab.reqs, pl.rq.data(), pl.rq.size() * sizeof(DevShared));
+            std::memcpy(pl.atab.spans, ap.data(), ap.size() * sizeof(DevSpan));
+            std::memcpy(pl.atab.locals, al.data(), al.size() * sizeof(DevLocal));
+        } else {
+            const size_t off_sp = align16(pl.rq.size() * sizeof(DevShared));
+            const size_t off_lc = off_sp + align16(ap.size() * sizeof(DevSpan));
+            std::vector<char> rows(off_lc + al.size() * sizeof(DevLocal));
+            std::memcpy(rows.data(), pl.rq.data(), pl.rq.size() * sizeof(DevShared));
+            std::memcpy(rows.data() + off_sp, ap.data(), ap.size() * sizeof(DevSpan));
+            std::memcpy(rows.data() + off_lc, al.data(), al.size() * sizeof(DevLocal));
+            if ((st = upload_table(p, rows.data(), rows.size(), s, &slot)) != KVR_OK)
+                return st;
+            const char *dv = static_cast<const char *>(slot->dev);
+            sa.reqs = reinterpret_cast<const DevShared *>(dv);
+            a.spans = reinterpret_cast<const DevSpan *>(dv + off_sp);
+            a.locals = reinterpret_cast<const DevLocal *>(dv + off_lc);
+        }
+        p->mark(2, s);
+        cudaError_t e = launch_assemble(a, p->d.dtype, D, (int)ap.size(), s, inl ? &pl.atab : nullptr);
+        p->mark(3, s);
+        if (e == cudaSuccess) {
+            NvtxRange r("kvr.k_shared_simt");
+            p->mark(4, s);
+            e = launch_shared_simt(sa, pl.tab, p->d.dtype, D, s);
+            p->mark(5, s);
+        }
+        if (slot)
+            cudaEventRecord(slot->done, s);
+        return e == cudaSuccess ? KVR_OK : cuda_fail(e, "shared-prefix attention launch");
+    });
+}
+
+extern "C" kvr_status kvr_key_weights(kvr_pool_t p, int32_t batch, const int64_t *cache_offsets,
+                                      const int32_t *prefix_len, const int32_t *q_offsets, const void *q,
+                                      const void *cache_k, float *weights, float softmax_scale, uint32_t flags,
+                                      void *stream)
+{
+    if (!p)
+        return fail(KVR_ERR_INVALID_ARG, "pool is NULL");
+    if (batch < 0)
+        return fail(KVR_ERR_INVALID_ARG, "batch %d", batch);
+    if (flags & ~(uint32_t)KVR_WEIGHTS_ACCUMULATE)
+        return fail(KVR_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if (batch == 0)
+        return KVR_OK;
+    NvtxRange call("kvr_key_weights");
+    return guarded([&]() -> kvr_status {
+        kvr_status st;
+        if ((st = check_cache_offsets(cache_offsets, batch)) != KVR_OK ||
+            (st = check_offsets32(q_offsets, batch, "q_offsets")) != KVR_OK)
+            return st;
+        if (!prefix_len)
+            return fail(KVR_ERR_INVALID_ARG, "prefix_len is NULL");
+        if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale))
+            return fail(KVR_ERR_INVALID_ARG, "softmax_scale %g", (double)softmax_scale);
+        const int L = p->d.n_layers, H = p->d.n_kv_heads, Hq = p->d.n_q_heads, D = p->d.head_dim, LH = L * H;
+        const int32_t T = q_offsets[batch];
+        const bool accumulate = flags & KVR_WEIGHTS_ACCUMULATE;
+        std::vector<DevReq> rq(batch);
+        WeightsArgs a{};
+        for (int b = 0; b < batch; ++b) {
+            const int64_t cap = cache_offsets[b + 1] - cache_offsets[b];
+            const int32_t lq = q_offsets[b + 1] - q_offsets[b];
+            if (prefix_len[b] < 0 || (int64_t)prefix_len[b] + lq > cap)
+                return fail(KVR_ERR_OUT_OF_RANGE, "request %d: prefix %d + query %d > cache block %lld", b, prefix_len[b],
+                            lq, (long long)cap);
+            rq[b] = DevReq{};
+            rq[b].cache_row0 = cache_offsets[b] * LH;
+            rq[b].cap = (int32_t)cap;
+            rq[b].prefix = prefix_len[b];
+            rq[b].q_off = q_offsets[b];
+            rq[b].q_len = lq;
+            a.max_rows = std::max(a.max_rows, prefix_len[b] + lq);
+            a.max_q_len = std::max(a.max_q_len, lq);
+        }
+        if (a.max_rows == 0 || (T == 0 && accumulate))
+            return KVR_OK;
+        if (!cache_k || !aligned16(cache_k) || (T > 0 && (!q || !aligned16(q))))
+            return fail(KVR_ERR_INVALID_ARG, "q / cache_k NULL or not 16-byte aligned");
+        if (!weights || (reinterpret_cast<uintptr_t>(weights) & 3))
+            return fail(KVR_ERR_INVALID_ARG, "weights NULL or not 4-byte aligned");
+        const int64_t r0 = cache_offsets[0] * LH, r1 = cache_offsets[batch] * LH, row_bytes = (int64_t)D * p->elt();
+        const Range wr = range_of(weights, r0, r1, 4);
+        if (wr.meets(range_of(cache_k, r0, r1, row_bytes)) ||
+            (T > 0 && wr.meets(range_of(q, 0, (int64_t)L * T * Hq, row_bytes))))
+            return fail(KVR_ERR_INVALID_ARG, "weights overlap the cache or the queries");
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const bool inl = batch <= kInlineEntries;
+        if ((st = check_capture(*p, s, inl, "a call of more than 64 requests uploads its tables")) != KVR_OK ||
+            (st = ensure_device(p)) != KVR_OK)
+            return st;
+        DeviceGuard g(p->device);
+        a.rope = p->rope;
+        a.q = q;
+        a.cache_k = cache_k;
+        a.weights = weights;
+        a.n_reqs = batch;
+        a.n_layers = L;
+        a.n_q_heads = Hq;
+        a.n_kv_heads = H;
+        a.total_q = T;
+        a.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
+        a.interleaved = (p->d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
+        a.accumulate = accumulate ? 1 : 0;
+        a.err = p->err;
+        ReqTable tab;
+        Slot *slot = nullptr;
+        if (inl) {
+            std::memcpy(tab.reqs, rq.data(), rq.size() * sizeof(DevReq));
+        } else {
+            if ((st = upload_table(p, rq.data(), rq.size() * sizeof(DevReq), s, &slot)) != KVR_OK)
+                return st;
+            a.reqs = static_cast<const DevReq *>(slot->dev);
+        }
+        cudaError_t e;
+        {
+            NvtxRange r("kvr.k_key_weights");
+            e = launch_weights_simt(a, tab, p->d.dtype, D, s);
+        }
+        if (slot)
+            cudaEventRecord(slot->done, s);
+        return e == cudaSuccess ? KVR_OK : cuda_fail(e, "key weights launch");
+    });
+}
+
+extern "C" kvr_status kvr_evict(kvr_pool_t p, int32_t batch, const int64_t *cache_offsets, const int32_t *kv_len,
+                                const int32_t *keep, int32_t n_first, int32_t n_recent, const float *weights,
+                                const void *cache_k, const void *cache_v, const int64_t *dst_offsets, void *dst_k,
+                                void *dst_v, float *dst_weights, int32_t *kept, uint32_t flags, void *stream)
+{
+    if (!p)
+        return fail(KVR_ERR_INVALID_ARG, "pool is NULL");
+    if (batch < 0)
+        return fail(KVR_ERR_INVALID_ARG, "batch %d", batch);
+    if (flags & ~(uint32_t)KVR_EVICT_KEEP_ROTATION)
+        return fail(KVR_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if (n_first < 0 || n_recent < 0)
+        return fail(KVR_ERR_INVALID_ARG, "n_first %d, n_recent %d", n_first, n_recent);
+    if (batch == 0)
+        return KVR_OK;
+    NvtxRange call("kvr_evict");
+    return guarded([&]() -> kvr_status {
+        kvr_status st;
+        if ((st = check_cache_offsets(cache_offsets, batch)) != KVR_OK ||
+            (st = check_cache_offsets(dst_offsets, batch)) != KVR_OK)
+            return st;
+        if (!kv_len || !keep)
+            return fail(KVR_ERR_INVALID_ARG, "kv_len / keep is NULL");
+        const int LH = p->d.n_layers * p->d.n_kv_heads, D = p->d.head_dim;
+        std::vector<DevEvict> rq(batch);
+        EvictArgs a{};
+        int64_t kept0 = 0, chunks = 0;
+        for (int b = 0; b < batch; ++b) {
+            const int64_t cap = cache_offsets[b + 1] - cache_offsets[b], dcap = dst_offsets[b + 1] - dst_offsets[b];
+            if (kv_len[b] < 0 || kv_len[b] > cap)
+                return fail(KVR_ERR_OUT_OF_RANGE, "request %d: %d rows outside its block of %lld", b, kv_len[b],
+                            (long long)cap);
+            if (keep[b] < 0 || (int64_t)n_first + n_recent > keep[b])
+                return fail(KVR_ERR_INVALID_ARG, "request %d: keep %d < n_first %d + n_recent %d", b, keep[b], n_first,
+                            n_recent);
+            const int32_t k = std::min(keep[b], kv_len[b]);
+            if (k > dcap)
+                return fail(KVR_ERR_OUT_OF_RANGE, "request %d: %d kept rows > destination block %lld", b, k,
+                            (long long)dcap);
+            DevEvict r{};
+            r.src_row0 = cache_offsets[b] * LH;
+            r.dst_row0 = dst_offsets[b] * LH;
+            r.kept0 = kept0;
+            r.src_cap = (int32_t)cap;
+            r.dst_cap = (int32_t)dcap;
+            r.n = kv_len[b];
+            r.keep = k;
+            r.chunk0 = (int32_t)std::min<int64_t>(chunks, INT32_MAX);
+            rq[b] = r;
+            kept0 += (int64_t)k * LH;
+            chunks += (int64_t)LH * std::max(1, (k + kEvictChunk - 1) / kEvictChunk);
+            a.max_n = std::max(a.max_n, kv_len[b]);
+        }
+        if (chunks > INT32_MAX)
+            return fail(KVR_ERR_UNSUPPORTED, "too many rows to move in one call");
+        const int64_t s0 = cache_offsets[0] * LH, s1 = cache_offsets[batch] * LH;
+        const int64_t d0 = dst_offsets[0] * LH, d1 = dst_offsets[batch] * LH, row_bytes = (int64_t)D * p->elt();
+        if (s0 == s1 && d0 == d1)
+            return KVR_OK;
+        if (s0 < s1 && (!cache_k || !cache_v || !weights || !aligned16(cache_k) || !aligned16(cache_v)))
+            return fail(KVR_ERR_INVALID_ARG, "cache_k / cache_v NULL or not 16-byte aligned, or weights NULL");
+        if (kept0 > 0 && (!dst_k || !dst_v || !kept || !aligned16(dst_k) || !aligned16(dst_v)))
+            return fail(KVR_ERR_INVALID_ARG, "dst_k / dst_v NULL or not 16-byte aligned, or kept NULL");
+        if ((reinterpret_cast<uintptr_t>(weights) & 3) || (reinterpret_cast<uintptr_t>(dst_weights) & 3) ||
+            (reinterpret_cast<uintptr_t>(kept) & 3))
+            return fail(KVR_ERR_INVALID_ARG, "weights / dst_weights / kept not 4-byte aligned");
+        // each destination is apart from everything else, or is its own source, block for block
+        const bool same = std::equal(cache_offsets, cache_offsets + batch + 1, dst_offsets);
+        const Range src[3] = {range_of(cache_k, s0, s1, row_bytes), range_of(cache_v, s0, s1, row_bytes),
+                              range_of(weights, s0, s1, 4)};
+        const Range dst[4] = {range_of(dst_k, d0, d1, row_bytes), range_of(dst_v, d0, d1, row_bytes),
+                              range_of(dst_weights, d0, d1, 4), range_of(kept, 0, kept0, 4)};
+        for (int i = 0; i < 4; ++i) {
+            for (int j = 0; j < 3; ++j) {
+                if (i == j && same && dst[i].lo == src[j].lo) {
+                    if (dst[i].meets(src[j]))
+                        a.in_place = 1;
+                } else if (dst[i].meets(src[j])) {
+                    return fail(KVR_ERR_INVALID_ARG, "a destination overlaps a source (only the same block is evicted in place)");
+                }
+            }
+            for (int j = 0; j < i; ++j)
+                if (dst[i].meets(dst[j]))
+                    return fail(KVR_ERR_INVALID_ARG, "destinations overlap");
+        }
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        const bool inl = batch <= kInlineEntries;
+        if ((st = check_capture(*p, s, inl, "a call of more than 64 requests uploads its tables")) != KVR_OK ||
+            (st = ensure_device(p)) != KVR_OK)
+            return st;
+        DeviceGuard g(p->device);
+        a.rope = p->rope;
+        a.weights = weights;
+        a.cache_k = cache_k;
+        a.cache_v = cache_v;
+        a.dst_k = dst_k;
+        a.dst_v = dst_v;
+        a.dst_weights = dst_weights;
+        a.kept = kept;
+        a.n_reqs = batch;
+        a.units = LH;
+        a.n_first = n_first;
+        a.n_recent = n_recent;
+        a.n_chunks = (int32_t)chunks;
+        a.interleaved = (p->d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
+        a.keep_rotation = (flags & KVR_EVICT_KEEP_ROTATION) ? 1 : 0;
+        EvictTable tab;
+        Slot *slot = nullptr;
+        if (inl) {
+            std::memcpy(tab.reqs, rq.data(), rq.size() * sizeof(DevEvict));
+        } else {
+            if ((st = upload_table(p, rq.data(), rq.size() * sizeof(DevEvict), s, &slot)) != KVR_OK)
+                return st;
+            a.reqs = static_cast<const DevEvict *>(slot->dev);
+        }
+        cudaError_t e;
+        {
+            NvtxRange r("kvr.k_evict");
+            e = launch_evict(a, tab, p->d.dtype, D, s);
+        }
+        if (slot)
+            cudaEventRecord(slot->done, s);
+        return e == cudaSuccess ? KVR_OK : cuda_fail(e, "eviction launch");
+    });
 }
 
 // ---------------------------------------------------------------------------

@@ -94,6 +94,54 @@ __device__ __forceinline__ void rotate_bf16x8_il(uint4 &lo, uint4 &hi, const flo
     }
 }
 
+// 16-byte vectors of E elements, rotation of a (lo, hi) pair of vectors.
+template <typename T>
+struct Vec;
+
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int E = 8;
+    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
+    {
+        if (il)
+            rotate_bf16x8_il(lo, hi, c, s);
+        else
+            rotate_bf16x8(lo, hi, c, s);
+    }
+};
+
+template <>
+struct Vec<float> {
+    static constexpr int E = 4;
+    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
+    {
+        float *x = reinterpret_cast<float *>(&lo);
+        float *y = reinterpret_cast<float *>(&hi);
+        if (il) {
+            // pairs (x0, x1), (x2, x3) of lo with c[0], c[1]; of hi with c[2], c[3]
+            float *v[2] = {x, y};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float a0 = v[h][2 * p], a1 = v[h][2 * p + 1];
+                    const float cc = c[2 * h + p], ss = s[2 * h + p];
+                    v[h][2 * p] = fmaf(a0, cc, -a1 * ss);
+                    v[h][2 * p + 1] = fmaf(a0, ss, a1 * cc);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float xo = fmaf(x[e], c[e], -y[e] * s[e]);
+            const float yo = fmaf(x[e], s[e], y[e] * c[e]);
+            x[e] = xo;
+            y[e] = yo;
+        }
+    }
+};
+
 // Pair index of the e-th (cos, sin) of a thread that owns 16-byte chunk j of
 // both row halves (E elements per chunk, head dim D): half-split pairs are
 // elements (jE + e, D/2 + jE + e); interleaved pairs are whole inside a
@@ -244,6 +292,89 @@ struct QueryPrologueArgs {
     int32_t interleaved;        // RoPE pairs (x_2i, x_2i+1)
 };
 
+// ---- query attention over a prefix shared by a group of requests ----
+// Per-request data (64 bytes): the request's own cache block, as DevReq, and
+// the prefix block of its group.
+struct alignas(16) DevShared {
+    int64_t cache_row0;  // own block: cache_offsets[b] * L * H_kv
+    int64_t pre_row0;    // prefix block: prefix_offsets[g] * L * H_kv
+    int32_t cap;         // own rows per (layer, kv-head) block
+    int32_t own;         // own rows that hold data before the call
+    int32_t pre_cap;     // rows per (layer, kv-head) block of the prefix
+    int32_t pre_len;     // P_g; query token t sits at position P_g + own + t
+    int32_t q_off, q_len;
+    int32_t pad_[6];
+};
+static_assert(sizeof(DevShared) == 64, "shared-prefix request table layout");
+struct SharedTable {
+    DevShared reqs[kInlineEntries];
+};
+struct SharedArgs {
+    const DevShared *reqs;      // NULL: the SharedTable parameter
+    const float2 *rope;
+    const void *q, *kq, *vq;
+    const void *prefix_k, *prefix_v;
+    void *cache_k, *cache_v;
+    void *out;
+    int32_t n_reqs;
+    int32_t n_layers, n_q_heads, n_kv_heads;
+    int32_t total_q;            // T
+    int32_t max_q_len;
+    float scale_log2;
+    int32_t interleaved;
+    int *err;
+};
+
+// ---- attention weight per cached key ----
+struct WeightsArgs {
+    const DevReq *reqs;         // NULL: the ReqTable parameter
+    const float2 *rope;
+    const void *q;              // [L][T][Hq][D], not rotated
+    const void *cache_k;
+    float *weights;             // the cache's blocks, one float a row
+    int32_t n_reqs;
+    int32_t n_layers, n_q_heads, n_kv_heads;
+    int32_t total_q;
+    int32_t max_rows;           // largest P_b + Lq_b of the batch
+    int32_t max_q_len;
+    float scale_log2;
+    int32_t interleaved;
+    int32_t accumulate;
+    int *err;
+};
+
+// ---- eviction of a cache's lightest rows ----
+// Per-request data (64 bytes).
+struct alignas(16) DevEvict {
+    int64_t src_row0;    // cache_offsets[b] * L * H_kv
+    int64_t dst_row0;    // dst_offsets[b] * L * H_kv
+    int64_t kept0;       // first entry of the request's kept rows
+    int32_t src_cap, dst_cap;
+    int32_t n, keep;     // rows held, rows to keep (keep <= n)
+    int32_t chunk0;      // first (unit, row chunk) of the request (move kernel)
+    int32_t pad_[5];
+};
+static_assert(sizeof(DevEvict) == 64, "eviction table layout");
+struct EvictTable {
+    DevEvict reqs[kInlineEntries];
+};
+struct EvictArgs {
+    const DevEvict *reqs;       // NULL: the EvictTable parameter
+    const float2 *rope;
+    const float *weights;
+    const void *cache_k, *cache_v;
+    void *dst_k, *dst_v;
+    float *dst_weights;         // or NULL
+    int32_t *kept;
+    int32_t n_reqs, units;      // units: L * H_kv
+    int32_t n_first, n_recent;
+    int32_t max_n;              // largest n of the batch
+    int32_t n_chunks;           // (unit, row chunk) pieces of the batch (move kernel)
+    int32_t interleaved;
+    int32_t keep_rotation;      // keys are copied as they are
+    int32_t in_place;
+};
+
 // ---- launchers (each returns the cudaGetLastError of its launch) ----
 cudaError_t launch_rope_tables(float2 *tab, int head_dim, double theta, cudaStream_t s);
 // `inl` (optional) carries the span and local tables; a.spans / a.locals are
@@ -317,6 +448,11 @@ cudaError_t launch_wait_selftest(int *err, unsigned long long limit_ns, cudaStre
 // the next one launch that way
 cudaError_t launch_decode_attention(const AttnArgs &a, const ReqTable &rt, const void *tmap_k, const void *tmap_v,
                                     const DecodeIO &io, bool pdl, cudaStream_t s);
+cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, cudaStream_t s);
+// Rows of one piece of the eviction's move kernel.
+constexpr int kEvictChunk = 64;
+cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, cudaStream_t s);
 // Whether `n_sms` CTAs of the attention kernel (either variant) can be
 // resident at once as two-CTA clusters.
 bool attention_tc_pairs_fit(int n_sms);

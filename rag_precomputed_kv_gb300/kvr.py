@@ -22,6 +22,8 @@ KVR_DTYPE_FP32 = 1
 KVR_SRC_LOCAL = 1 << 30
 KVR_POSITIONS_COMPOSITE = 1
 KVR_PREFILL_SKIP_PREFIX_CACHE = 2
+KVR_WEIGHTS_ACCUMULATE = 1
+KVR_EVICT_KEEP_ROTATION = 1
 KVR_POOL_KEYS_UNROTATED = 1
 KVR_POOL_ROPE_INTERLEAVED = 2
 
@@ -30,7 +32,8 @@ STATUS = {0: "KVR_OK", 1: "KVR_ERR_INVALID_ARG", 2: "KVR_ERR_OUT_OF_RANGE", 3: "
 
 EXPORTED = ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_query_attention",
             "kvr_prefill", "kvr_check", "kvr_status_string", "kvr_last_error", "kvr_attention_path",
-            "kvr_set_timing_events", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve")
+            "kvr_set_timing_events", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
+            "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict")
 PATH_UNBOUND, PATH_CUDA_CORES, PATH_TCGEN05 = -1, 0, 1
 
 
@@ -76,6 +79,9 @@ def load(path: str = LIB_PATH):
     lib.kvr_query_attention.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp]
     lib.kvr_prefill.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, ctypes.c_uint32,
                                 vp, vp, vp, vp, vp, ctypes.c_float, vp]
+    lib.kvr_shared_query_attention.argtypes = [vp, i32] + [vp] * 14 + [ctypes.c_float, vp]
+    lib.kvr_key_weights.argtypes = [vp, i32] + [vp] * 6 + [ctypes.c_float, ctypes.c_uint32, vp]
+    lib.kvr_evict.argtypes = [vp, i32, vp, vp, vp, i32, i32] + [vp] * 8 + [ctypes.c_uint32, vp]
     lib.kvr_check.argtypes = [vp, vp]
     lib.kvr_assemble_noalloc.argtypes = [ctypes.POINTER(PoolDesc), i32, vp, vp, vp, i32, vp, vp, vp, vp, vp,
                                          vp, ctypes.c_uint32, vp]
@@ -89,7 +95,8 @@ def load(path: str = LIB_PATH):
     lib.kvr_attention_path.argtypes = [vp]
     lib.kvr_attention_path.restype = ctypes.c_int32
     for name in ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_query_attention",
-                 "kvr_prefill", "kvr_check", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve"):
+                 "kvr_prefill", "kvr_check", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
+                 "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -117,6 +124,18 @@ def _i32(a) -> np.ndarray:
 
 def _i64(a) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=np.int64))
+
+
+def _sized(name: str, a: np.ndarray, n: int) -> np.ndarray:
+    if a.ndim != 1 or len(a) != n:
+        raise ValueError(f"{name} must hold {n} values, got shape {a.shape}")
+    return a
+
+
+def _check_f32(t, name: str):
+    import torch
+    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 tensor")
 
 
 def _np_ptr(a: Optional[np.ndarray]):
@@ -249,6 +268,66 @@ class Pool:
         _raise(load().kvr_query_attention(self._h, len(qo) - 1, _np_ptr(co), _np_ptr(pl), _np_ptr(qo),
                                           _ptr(q), _ptr(kq), _ptr(vq), _ptr(cache_k), _ptr(cache_v),
                                           _ptr(out), float(softmax_scale), _stream_ptr(stream)))
+
+    def shared_query_attention(self, group_offsets, prefix_offsets, prefix_len, prefix_k, prefix_v, cache_offsets,
+                               own_len, q_offsets, q, kq, vq, cache_k, cache_v, out, softmax_scale: float = 0.0,
+                               stream=None):
+        """kvr_shared_query_attention: query attention of groups of requests,
+        each over its group's shared prefix block (``prefix_k``, ``prefix_v``,
+        read only) and the requests' own rows, to which the query K/V are
+        appended; writes ``out``."""
+        go = _i32(group_offsets)
+        n, batch = len(go) - 1, int(go[-1])
+        po, pl = _sized("prefix_offsets", _i64(prefix_offsets), n + 1), _sized("prefix_len", _i32(prefix_len), n)
+        co, ol = _sized("cache_offsets", _i64(cache_offsets), batch + 1), _sized("own_len", _i32(own_len), batch)
+        qo = _sized("q_offsets", _i32(q_offsets), batch + 1)
+        _raise(load().kvr_shared_query_attention(self._h, n, _np_ptr(go), _np_ptr(po), _np_ptr(pl),
+                                                 _ptr(prefix_k), _ptr(prefix_v), _np_ptr(co), _np_ptr(ol), _np_ptr(qo),
+                                                 _ptr(q), _ptr(kq), _ptr(vq), _ptr(cache_k), _ptr(cache_v), _ptr(out),
+                                                 float(softmax_scale), _stream_ptr(stream)))
+
+    def key_weights(self, cache_offsets, prefix_len, q_offsets, q, cache_k, weights, softmax_scale: float = 0.0,
+                    accumulate: bool = False, stream=None):
+        """kvr_key_weights: the attention weight each cached key receives from
+        the query tokens (fp32, one value per cache row), written to
+        ``weights`` or, with ``accumulate``, added to it."""
+        _check_f32(weights, "weights")
+        qo = _i32(q_offsets)
+        n = len(qo) - 1
+        co, pl = _sized("cache_offsets", _i64(cache_offsets), n + 1), _sized("prefix_len", _i32(prefix_len), n)
+        _raise(load().kvr_key_weights(self._h, n, _np_ptr(co), _np_ptr(pl), _np_ptr(qo), _ptr(q),
+                                      _ptr(cache_k), _ptr(weights), float(softmax_scale),
+                                      KVR_WEIGHTS_ACCUMULATE if accumulate else 0, _stream_ptr(stream)))
+
+    def evict(self, cache_offsets, kv_len, keep, weights, cache_k, cache_v, kept, dst_offsets=None, dst_k=None,
+              dst_v=None, dst_weights=None, n_first: int = 0, n_recent: int = 0, keep_rotation: bool = False,
+              stream=None):
+        """kvr_evict: keep the ``keep[b]`` heaviest rows of each block (the
+        first ``n_first`` and last ``n_recent`` always), moved to rows 0.. with
+        their keys turned to the new positions; ``kept`` (int32) receives the
+        rows.  Without ``dst_k`` the cache and the weights are evicted in
+        place.  Returns the rows each request holds afterwards (numpy int32)."""
+        import torch
+        _check_f32(weights, "weights")
+        if dst_k is None:
+            if dst_v is not None or dst_weights is not None or dst_offsets is not None:
+                raise ValueError("dst_offsets, dst_v and dst_weights go with dst_k")
+            dst_offsets, dst_k, dst_v, dst_weights = cache_offsets, cache_k, cache_v, weights
+        elif dst_offsets is None:
+            raise ValueError("dst_k needs dst_offsets")
+        if dst_weights is not None:
+            _check_f32(dst_weights, "dst_weights")
+        if kept is not None and (kept.dtype != torch.int32 or not kept.is_contiguous()):
+            raise ValueError("kept must be a contiguous int32 tensor")
+        kl = _i32(kv_len)
+        n = len(kl)
+        kp, co = _sized("keep", _i32(keep), n), _sized("cache_offsets", _i64(cache_offsets), n + 1)
+        do = _sized("dst_offsets", _i64(dst_offsets), n + 1)
+        _raise(load().kvr_evict(self._h, n, _np_ptr(co), _np_ptr(kl), _np_ptr(kp), int(n_first), int(n_recent),
+                                _ptr(weights), _ptr(cache_k), _ptr(cache_v), _np_ptr(do), _ptr(dst_k), _ptr(dst_v),
+                                _ptr(dst_weights), _ptr(kept), KVR_EVICT_KEEP_ROTATION if keep_rotation else 0,
+                                _stream_ptr(stream)))
+        return np.minimum(kl, kp)
 
     @property
     def attention_path(self) -> int:
