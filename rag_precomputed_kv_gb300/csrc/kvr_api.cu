@@ -1562,6 +1562,11 @@ extern "C" kvr_status kvr_key_weights(kvr_pool_t p, int32_t batch, const int64_t
         a.interleaved = (p->d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
         a.accumulate = accumulate ? 1 : 0;
         a.err = p->err;
+        // the tensor cores' TMA coordinates are 32-bit rows
+        const bool tc = use_tensor_cores(*p) && r1 <= (int64_t)INT32_MAX - 256;
+        CUtensorMap mk;
+        if (tc && (st = encode_cache_map(*p, const_cast<void *>(cache_k), r1, &mk)) != KVR_OK)
+            return st;
         ReqTable tab;
         Slot *slot = nullptr;
         if (inl) {
@@ -1574,7 +1579,7 @@ extern "C" kvr_status kvr_key_weights(kvr_pool_t p, int32_t batch, const int64_t
         cudaError_t e;
         {
             NvtxRange r("kvr.k_key_weights");
-            e = launch_weights_simt(a, tab, p->d.dtype, D, s);
+            e = tc ? launch_weights_tc(a, tab, &mk, p->n_sms, s) : launch_weights_simt(a, tab, p->d.dtype, D, s);
         }
         if (slot)
             cudaEventRecord(slot->done, s);

@@ -47,6 +47,56 @@ cudaError_t launch_rope_tables(float2 *tab, int head_dim, double theta, cudaStre
     return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// 16-byte vectors of E elements, rotation of a (lo, hi) pair of vectors
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Vec;
+
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int E = 8;
+    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
+    {
+        if (il)
+            rotate_bf16x8_il(lo, hi, c, s);
+        else
+            rotate_bf16x8(lo, hi, c, s);
+    }
+};
+
+template <>
+struct Vec<float> {
+    static constexpr int E = 4;
+    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
+    {
+        float *x = reinterpret_cast<float *>(&lo);
+        float *y = reinterpret_cast<float *>(&hi);
+        if (il) {
+            // pairs (x0, x1), (x2, x3) of lo with c[0], c[1]; of hi with c[2], c[3]
+            float *v[2] = {x, y};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float a0 = v[h][2 * p], a1 = v[h][2 * p + 1];
+                    const float cc = c[2 * h + p], ss = s[2 * h + p];
+                    v[h][2 * p] = fmaf(a0, cc, -a1 * ss);
+                    v[h][2 * p + 1] = fmaf(a0, ss, a1 * cc);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float xo = fmaf(x[e], c[e], -y[e] * s[e]);
+            const float yo = fmaf(x[e], s[e], y[e] * c[e]);
+            x[e] = xo;
+            y[e] = yo;
+        }
+    }
+};
+
 __device__ __forceinline__ uint4 ld_stream(const void *p)
 {
     uint4 r;

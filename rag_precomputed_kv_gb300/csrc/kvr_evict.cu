@@ -36,6 +36,54 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+// 16-byte vectors of E elements of a row, rotation of a (lo, hi) pair of them.
+template <typename T>
+struct RowVec;
+
+template <>
+struct RowVec<__nv_bfloat16> {
+    static constexpr int E = 8;
+    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
+    {
+        if (il)
+            rotate_bf16x8_il(lo, hi, c, s);
+        else
+            rotate_bf16x8(lo, hi, c, s);
+    }
+};
+
+template <>
+struct RowVec<float> {
+    static constexpr int E = 4;
+    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
+    {
+        float *x = reinterpret_cast<float *>(&lo);
+        float *y = reinterpret_cast<float *>(&hi);
+        if (il) {
+            // pairs (x0, x1), (x2, x3) of lo with c[0], c[1]; of hi with c[2], c[3]
+            float *v[2] = {x, y};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float a0 = v[h][2 * p], a1 = v[h][2 * p + 1];
+                    const float cc = c[2 * h + p], ss = s[2 * h + p];
+                    v[h][2 * p] = fmaf(a0, cc, -a1 * ss);
+                    v[h][2 * p + 1] = fmaf(a0, ss, a1 * cc);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float xo = fmaf(x[e], c[e], -y[e] * s[e]);
+            const float yo = fmaf(x[e], s[e], y[e] * c[e]);
+            x[e] = xo;
+            y[e] = yo;
+        }
+    }
+};
+
 }  // namespace
 
 // One CTA per (request, unit).  The threshold is found 8 bits at a time: a
@@ -160,7 +208,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kMoveThreads)
     k_evict_move(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
 {
-    constexpr int E = Vec<T>::E, H2 = D / 2, TPR = H2 / E, RPP = kMoveThreads / TPR;
+    constexpr int E = RowVec<T>::E, H2 = D / 2, TPR = H2 / E, RPP = kMoveThreads / TPR;
     constexpr int NR = (kEvictChunk + RPP - 1) / RPP;   // rows of a thread
     const DevEvict *reqs = a.reqs ? a.reqs : rt.reqs;
     int b, lh, c_first, c_end;
@@ -237,7 +285,7 @@ __global__ void __launch_bounds__(kMoveThreads)
                     cs[e] = r.x;
                     sn[e] = r.y;
                 }
-                Vec<T>::rotate(k[x][0], k[x][1], cs, sn, a.interleaved);
+                RowVec<T>::rotate(k[x][0], k[x][1], cs, sn, a.interleaved);
             }
             const int64_t o = (int64_t)i * D + j * E;
             *reinterpret_cast<uint4 *>(dk + o) = k[x][0];

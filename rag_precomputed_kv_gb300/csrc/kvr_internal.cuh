@@ -94,54 +94,6 @@ __device__ __forceinline__ void rotate_bf16x8_il(uint4 &lo, uint4 &hi, const flo
     }
 }
 
-// 16-byte vectors of E elements, rotation of a (lo, hi) pair of vectors.
-template <typename T>
-struct Vec;
-
-template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int E = 8;
-    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
-    {
-        if (il)
-            rotate_bf16x8_il(lo, hi, c, s);
-        else
-            rotate_bf16x8(lo, hi, c, s);
-    }
-};
-
-template <>
-struct Vec<float> {
-    static constexpr int E = 4;
-    __device__ static void rotate(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
-    {
-        float *x = reinterpret_cast<float *>(&lo);
-        float *y = reinterpret_cast<float *>(&hi);
-        if (il) {
-            // pairs (x0, x1), (x2, x3) of lo with c[0], c[1]; of hi with c[2], c[3]
-            float *v[2] = {x, y};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float a0 = v[h][2 * p], a1 = v[h][2 * p + 1];
-                    const float cc = c[2 * h + p], ss = s[2 * h + p];
-                    v[h][2 * p] = fmaf(a0, cc, -a1 * ss);
-                    v[h][2 * p + 1] = fmaf(a0, ss, a1 * cc);
-                }
-            }
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float xo = fmaf(x[e], c[e], -y[e] * s[e]);
-            const float yo = fmaf(x[e], s[e], y[e] * c[e]);
-            x[e] = xo;
-            y[e] = yo;
-        }
-    }
-};
-
 // Pair index of the e-th (cos, sin) of a thread that owns 16-byte chunk j of
 // both row halves (E elements per chunk, head dim D): half-split pairs are
 // elements (jE + e, D/2 + jE + e); interleaved pairs are whole inside a
@@ -450,6 +402,9 @@ cudaError_t launch_decode_attention(const AttnArgs &a, const ReqTable &rt, const
                                     const DecodeIO &io, bool pdl, cudaStream_t s);
 cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, cudaStream_t s);
+// bf16, head_dim 128: the tensor-core kernel; `tmap_k` points to the CUtensorMap
+// of the cache's keys ([rows, head_dim], 64 x 128 boxes).
+cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const void *tmap_k, int n_sms, cudaStream_t s);
 // Rows of one piece of the eviction's move kernel.
 constexpr int kEvictChunk = 64;
 cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, cudaStream_t s);

@@ -1,0 +1,569 @@
+// kvr_key_weights_tc.cu -- attention weight per cached key on the tensor cores
+// (bf16, head_dim 128).
+//
+// For every (request, layer, kv-head) and key row j < n = P_b + Lq_b:
+//     w[j] (+)= sum over query rows r of exp2(c s_rj - lse_r),  s_rj = <rot(q_r), k_j>,
+//     lse_r = log2 sum_j exp2(c s_rj),                          c = scale log2(e),
+// a query row r being one of the G heads of one query token.
+//
+// The scores are computed the other way round, S^T = K Q^T: a 128-key tile is
+// the M side of tcgen05.mma and the NQ query rows its N side.  A thread then
+// owns a key (a TMEM lane): the sum over queries that makes a weight runs
+// inside the thread, a decode step's few rows cost a narrow MMA instead of 128
+// padded ones, and rows of the cache behind n stay in their own lanes.  Only
+// the queries' denominators cross lanes, once per CTA.
+//
+// Every weight needs its rows' denominators over all keys before it can be
+// summed.  So that K is read once, the scores stay in TMEM in between: a CTA
+// holds 256 columns, 256 / NQ tiles, and the CTAs of a cluster split a unit's
+// key tiles and exchange their rows' (max, sum) through distributed shared
+// memory.  Tiles beyond what TMEM holds are processed first, for their
+// statistics only, and loaded again at the end.
+//
+// Rotated queries are split into three bf16 terms (8 + 8 + 8 bits: all of the
+// fp32 rotation's), three accumulating MMAs, so that the weights are fp32
+// results; a decode step is bound by the HBM read of K, and a window of 64
+// rows by exp2, so the two extra products cost no time there.
+//
+// Two CTAs per SM (110 KB of shared memory, 256 TMEM columns each): one loads
+// while the other is in its prologue or exchange.  Warps 0-3 rotate the
+// queries and run the softmax passes; warp 4 issues the TMA loads (16 KB
+// panels: 128 keys x 64 dims); warp 5 the MMAs.  All waits are bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kvr_tc_common.cuh"
+
+namespace kvr {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kWtThreads = 192;
+constexpr int kWtD = 128;
+constexpr int kWtTile = 128;                 // keys per tile
+constexpr int kWtPanel = kWtTile * 64 * 2;   // 16 KB: 128 keys x 64 dims
+constexpr int kWtTmemCols = 256;
+constexpr int kWtMaxCluster = 8;
+// a row that has seen no key yet: finite, so that the first score is far above
+// it and sets the reference, and a masked -inf stays -inf
+constexpr float kWtUnset = -1e30f;
+constexpr float kWtHeadroom = 60.f;          // log2 units above the reference before it moves
+
+template <int NQ>
+struct WtCfg {
+    static constexpr int kSlots = NQ == 16 ? 6 : NQ == 32 ? 5 : 3;   // K panels in flight
+    static constexpr int kKept = kWtTmemCols / NQ;                   // tiles whose scores stay in TMEM
+    static constexpr int kQTerm = NQ * kWtD * 2;                     // one bf16 term of the query rows
+    static constexpr int kOffRing = 3 * kQTerm;
+    static constexpr int kOffBar = kOffRing + kSlots * kWtPanel;
+    // full[slots], empty[slots], s_full[kept], s_free[kept], q_full, q_empty, peers, drain
+    static constexpr int kNumBars = 2 * kSlots + 2 * kKept + 4;
+    static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // TMEM address, abort flag
+    static constexpr int kOffRef = (kOffMisc + 8 + 15) & ~15;        // [4][NQ] reference per warp
+    static constexpr int kOffStat = kOffRef + 4 * NQ * 4;            // [4][NQ] (reference, sum) per warp
+    static constexpr int kOffFin = kOffStat + 4 * NQ * 8;            // [NQ] lse
+    static constexpr int kOffPeer = kOffFin + NQ * 4;                // [2][kWtMaxCluster][NQ] (max, sum)
+    static constexpr int kSmem = kOffPeer + 2 * kWtMaxCluster * NQ * 8;
+    static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
+};
+
+// Order-preserving integer of a float (a warp's maximum by one integer reduction).
+__device__ __forceinline__ int f_key(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_f(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+// Sums over the warp of NV values per lane; lane i gets value i % NV's (NV <= 32).
+template <int NV>
+__device__ __forceinline__ float warp_sums(float *v, int lane)
+{
+    int o = 16;
+#pragma unroll
+    for (int n = NV; n > 1; n >>= 1, o >>= 1) {
+        // lanes with bit `o` take the upper half of the values
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = up ? v[n / 2 + i] : v[i], give = up ? v[i] : v[n / 2 + i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    float r = v[0];
+#pragma unroll
+    for (; o > 0; o >>= 1)
+        r += __shfl_xor_sync(0xffffffffu, r, o);
+    return r;
+}
+// The value that warp_sums<NV> leaves in `lane`.
+template <int NV>
+__device__ __forceinline__ int warp_sums_index(int lane)
+{
+    int idx = 0, o = 16;
+#pragma unroll
+    for (int n = NV; n > 1; n >>= 1, o >>= 1)
+        idx += (lane & o) ? n / 2 : 0;
+    return idx;
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Bounded wait that sees what other CTAs of the cluster released before arriving.
+__device__ __forceinline__ bool wait_peers(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok)
+            return true;
+        if (*abort_flag || globaltimer() - t0 > kWaitNs)
+            return false;
+    }
+}
+
+}  // namespace
+
+template <int NQ>
+__global__ void __launch_bounds__(kWtThreads, 2)
+    k_key_weights_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ WeightsArgs a,
+                     const __grid_constant__ ReqTable rt, const int n_cluster)
+{
+    using C = WtCfg<NQ>;
+    constexpr int BL = NQ < 32 ? NQ : 32;   // columns per TMEM read
+    constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NQ >> 3) << 17) |
+                                ((uint32_t)(kWtTile >> 4) << 24);
+    extern __shared__ __align__(1024) uint8_t wt_smem[];
+    const uint32_t sbase = smem_u32(wt_smem);
+    auto bar = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
+    constexpr int bFull = 0, bEmpty = C::kSlots, bSFull = 2 * C::kSlots, bSFree = bSFull + C::kKept,
+                  bQFull = bSFree + C::kKept, bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bQFull + 3;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(wt_smem + C::kOffMisc + 4);
+    float *s_ref = reinterpret_cast<float *>(wt_smem + C::kOffRef);
+    float2 *s_stat = reinterpret_cast<float2 *>(wt_smem + C::kOffStat);
+    float *s_fin = reinterpret_cast<float *>(wt_smem + C::kOffFin);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = a.n_layers * a.n_kv_heads;
+    const int rank = (int)(blockIdx.x % (unsigned)n_cluster), unit_i = (int)(blockIdx.x / (unsigned)n_cluster);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kNumBars; ++i) {
+            const bool wg = (i >= bSFree && i < bSFree + C::kKept) || i == bQFull;
+            mbar_init(bar(i), wg ? 128u : i == bPeers ? (uint32_t)(n_cluster * NQ) : 1u);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5)
+        tmem_alloc(sbase + C::kOffMisc, kWtTmemCols);
+    if (warp == 4 && lane == 0)
+        prefetch_tmap(&tmk);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync();   // the peers' barriers are initialised before any remote arrive
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(wt_smem + C::kOffMisc);
+    pdl_wait_prerequisites();
+
+    const DevReq *reqs = a.reqs ? a.reqs : rt.reqs;
+    const DevReq rq = reqs[unit_i / units];
+    const int lh = unit_i % units;
+    const int G = a.n_q_heads / a.n_kv_heads;
+    const int m_rows = rq.q_len * G, n = rq.prefix + rq.q_len;
+    const int n_rb = (m_rows + NQ - 1) / NQ;                 // row blocks
+    const int nt = (n + kWtTile - 1) / kWtTile;
+    const int t_lo = (int)((int64_t)rank * nt / n_cluster), t_hi = (int)((int64_t)(rank + 1) * nt / n_cluster);
+    const int T = t_hi - t_lo;                               // this CTA's key tiles
+    const int n_redo = max(0, T - C::kKept);                 // loaded a second time, for each row block
+    const int64_t blk = rq.cache_row0 + (int64_t)lh * rq.cap;
+    // job i of a row block: tiles T-1 .. 0 for the statistics, then kKept .. T-1 again
+    auto job_tile = [&](int i) { return i < T ? T - 1 - i : C::kKept + (i - T); };
+    const int n_jobs = T + n_redo;
+
+    if (warp < 4) {
+        const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const float sc = a.scale_log2;
+        float *wp = a.weights + blk;
+        uint32_t full_par = 0;   // parity of the next wait on s_full[slot]
+        bool ok = true;
+        if (m_rows == 0 && !a.accumulate)   // a sum over no queries
+            for (int j = t_lo * kWtTile + (int)threadIdx.x; j < min(n, t_hi * kWtTile); j += 128)
+                wp[j] = 0.f;
+        for (int rb = 0; rb < n_rb && ok; ++rb) {
+            const int r0 = rb * NQ, nr = min(NQ, m_rows - r0);
+            if (rb > 0 && !mbar_wait(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            // ---- the row block's queries: rotated, split in three bf16 terms ----
+#pragma unroll 1
+            for (int it = threadIdx.x; it < NQ * 8; it += 128) {
+                const int row = it >> 3, j = it & 7;
+                float v[16];   // elements 8j..8j+7 and 64+8j..64+8j+7
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] = 0.f;
+                if (row < nr) {
+                    const int t = (r0 + row) / G, g = (r0 + row) - t * G;
+                    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
+                                              (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + g) * kWtD + 8 * j;
+                    const uint4 u[2] = {*reinterpret_cast<const uint4 *>(qp), *reinterpret_cast<const uint4 *>(qp + 64)};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t w4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            v[8 * k + 2 * e] = __uint_as_float(w4[e] << 16);
+                            v[8 * k + 2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 cs = rope_cs(a.rope, kWtD / 2, rq.prefix + t, rope_pair(a.interleaved, kWtD, 8, j, e));
+                        float x0, x1;
+                        if (a.interleaved) {
+                            x0 = v[2 * e];
+                            x1 = v[2 * e + 1];
+                        } else {
+                            x0 = v[e];
+                            x1 = v[8 + e];
+                        }
+                        const float y0 = fmaf(x0, cs.x, -x1 * cs.y), y1 = fmaf(x0, cs.y, x1 * cs.x);
+                        if (a.interleaved) {
+                            v[2 * e] = y0;
+                            v[2 * e + 1] = y1;
+                        } else {
+                            v[e] = y0;
+                            v[8 + e] = y1;
+                        }
+                    }
+                }
+                const uint32_t dst = sbase + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4));
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &x0 = v[8 * k + 2 * e], &x1 = v[8 * k + 2 * e + 1];
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+                            w4[e] = *reinterpret_cast<const uint32_t *>(&b);
+                            x0 -= __low2float(b);    // exact: what the term leaves
+                            x1 -= __high2float(b);
+                        }
+                        st_shared_v4(dst + (uint32_t)(term * C::kQTerm + k * (C::kQTerm / 2)), w4[0], w4[1], w4[2], w4[3]);
+                    }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar(bQFull));
+
+            // scores of TMEM slot `slot`, columns 32 q .., in log2 units; keys that a
+            // row does not see are -inf.  lim: the first column that sees this key.
+            auto load = [&](int slot, int q, float *s) {
+                const uint32_t at = lane_base + (uint32_t)(slot * NQ + q * 32);
+                if constexpr (BL == 16)
+                    tmem_ld16(at, s);
+                else
+                    tmem_ld32(at, s);
+                tmem_wait_ld();
+            };
+            auto mask = [&](int lim, int q, float *s) {
+#pragma unroll
+                for (int c = 0; c < BL; ++c)
+                    s[c] = q * 32 + c >= lim ? s[c] : -INFINITY;
+            };
+
+            // ---- pass 1: each row's reference and sum over this warp's keys ----
+            float ls[NQ];
+#pragma unroll
+            for (int c = 0; c < NQ; ++c)
+                ls[c] = 0.f;
+            float *ref = s_ref + warp * NQ;
+            for (int c = lane; c < NQ; c += 32)
+                ref[c] = kWtUnset;
+            __syncwarp();
+            for (int i = 0; i < T; ++i) {
+                const int t = T - 1 - i, slot = t % C::kKept;
+                if (!mbar_wait(bar(bSFull + slot), (full_par >> slot) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                full_par ^= 1u << slot;
+                tc_fence_after();
+                const int j0 = (t_lo + t) * kWtTile, j = j0 + (int)threadIdx.x;
+                const bool edge = j0 + kWtTile > rq.prefix + 1;   // some key is not seen by every row
+                const int lim = !edge ? 0 : j >= n ? NQ : (j - rq.prefix) * G - r0;
+#pragma unroll
+                for (int q = 0; q < NQ / BL; ++q) {
+                    float s[BL];
+                    load(slot, q, s);
+                    if (edge)
+                        mask(lim, q, s);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < BL; ++c) {
+                        s[c] *= sc;
+                        mx = fmaxf(mx, s[c] - ref[q * 32 + c]);
+                    }
+                    if (__any_sync(0xffffffffu, mx > kWtHeadroom)) {
+                        // a first key, or one far above the reference: the rows'
+                        // references move up to this tile's maxima
+#pragma unroll
+                        for (int c = 0; c < BL; ++c) {
+                            const float old = ref[q * 32 + c];
+                            const float m = key_f(__reduce_max_sync(0xffffffffu, f_key(s[c])));
+                            if (m > old) {
+                                ls[q * 32 + c] = old == kWtUnset ? 0.f : ls[q * 32 + c] * ex2(old - m);
+                                __syncwarp();
+                                if (lane == 0)
+                                    ref[q * 32 + c] = m;
+                                __syncwarp();
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < BL; ++c)
+                        ls[q * 32 + c] += ex2(s[c] - ref[q * 32 + c]);
+                }
+                if (t >= C::kKept) {
+                    tc_fence_before();
+                    mbar_arrive(bar(bSFree + slot));
+                }
+            }
+            if (!ok)
+                break;
+#pragma unroll
+            for (int q = 0; q < NQ / BL; ++q) {
+                const float r = warp_sums<BL>(ls + q * 32, lane);
+                const int c = q * 32 + warp_sums_index<BL>(lane);
+                s_stat[warp * NQ + c] = make_float2(ref[c], r);
+            }
+            softmax_sync();
+            // ---- the CTA's (max, sum) of row c to every CTA of the cluster ----
+            const uint32_t peer = sbase + C::kOffPeer + (uint32_t)((rb & 1) * kWtMaxCluster * NQ * 8);
+            if (threadIdx.x < NQ) {
+                const int c = threadIdx.x;
+                float M = kWtUnset, L = 0.f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    M = fmaxf(M, s_stat[x * NQ + c].x);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float2 v = s_stat[x * NQ + c];
+                    L += v.y != 0.f ? v.y * ex2(v.x - M) : 0.f;
+                }
+                for (int x = 0; x < n_cluster; ++x) {
+                    const uint32_t dst = mapa_rank(peer + (uint32_t)((rank * NQ + c) * 8), (uint32_t)x);
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(M), "f"(L) : "memory");
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                     mapa_rank(bar(bPeers), (uint32_t)x))
+                                 : "memory");
+                }
+                if (wait_peers(bar(bPeers), (uint32_t)rb & 1, abort_flag)) {
+                    float Mt = kWtUnset, Lt = 0.f;
+                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + C::kOffPeer) + (rb & 1) * kWtMaxCluster * NQ + c;
+                    for (int x = 0; x < n_cluster; ++x)
+                        Mt = fmaxf(Mt, pv[x * NQ].x);
+                    for (int x = 0; x < n_cluster; ++x) {   // in rank order: one rounding order
+                        const float2 v = pv[x * NQ];
+                        Lt += v.y != 0.f ? v.y * ex2(v.x - Mt) : 0.f;
+                    }
+                    s_fin[c] = Mt + log2f(Lt);
+                    if (c < nr && rank == 0 && !(Lt > 0.f && Lt < INFINITY))
+                        atomicCAS(a.err, kDevOk, kDevBadInput);
+                } else {
+                    give_up(a.err, abort_flag);
+                }
+            }
+            softmax_sync();
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            // ---- pass 2: the weights of this thread's keys ----
+            const bool add = rb > 0 || a.accumulate;
+            for (int t = 0; t < T; ++t) {
+                const int slot = t % C::kKept;
+                const int j0 = (t_lo + t) * kWtTile, j = j0 + (int)threadIdx.x;
+                float w = add && j < n ? wp[j] : 0.f;
+                if (t >= C::kKept) {
+                    if (!mbar_wait(bar(bSFull + slot), (full_par >> slot) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    full_par ^= 1u << slot;
+                    tc_fence_after();
+                }
+                const bool edge = j0 + kWtTile > rq.prefix + 1;
+                const int lim = !edge ? 0 : j >= n ? NQ : (j - rq.prefix) * G - r0;
+                float sum = 0.f;
+#pragma unroll
+                for (int q = 0; q < NQ / BL; ++q) {
+                    float s[BL];
+                    load(slot, q, s);
+                    if (edge)
+                        mask(lim, q, s);
+                    float p4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < BL; ++c)
+                        p4[c & 3] += q * 32 + c < nr ? ex2(fmaf(s[c], sc, -s_fin[q * 32 + c])) : 0.f;
+                    sum += (p4[0] + p4[1]) + (p4[2] + p4[3]);
+                }
+                tc_fence_before();
+                mbar_arrive(bar(bSFree + slot));
+                if (j < n)
+                    wp[j] = w + sum;
+            }
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+    } else if (warp == 4) {
+        if (lane == 0) {
+            bool ok = true;
+            int k = 0;   // panels issued
+            for (int rb = 0; rb < n_rb && ok; ++rb)
+                for (int i = 0; i < n_jobs && ok; ++i) {
+                    const int row = (int)(blk + (int64_t)(t_lo + job_tile(i)) * kWtTile);
+                    for (int p = 0; p < 2; ++p, ++k) {
+                        const int s = k % C::kSlots;
+                        if (k >= C::kSlots && !mbar_wait(bar(bEmpty + s), (uint32_t)(k / C::kSlots - 1) & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_expect_tx(bar(bFull + s), kWtPanel);
+                        tma_load_2d(sbase + (uint32_t)(C::kOffRing + s * kWtPanel), &tmk, 64 * p, row, bar(bFull + s));
+                    }
+                }
+            if (!ok)
+                give_up(a.err, abort_flag);
+            // every issued copy lands before the CTA leaves
+            for (int x = k > C::kSlots ? k - C::kSlots : 0; x < k; ++x)
+                mbar_drain(bar(bFull + x % C::kSlots), (uint32_t)(x / C::kSlots) & 1);
+        }
+    } else {
+        const uint32_t lead = elect_one();
+        const uint64_t d0 = sdesc(sbase, 16, 1024);
+        const uint32_t lo = (uint32_t)d0, hi = (uint32_t)(d0 >> 32);
+        uint32_t used = 0, free_par = 0;   // per score slot
+        bool ok = true;
+        int k = 0;
+        for (int rb = 0; rb < n_rb && ok; ++rb) {
+            if (!mbar_wait(bar(bQFull), (uint32_t)rb & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            for (int i = 0; i < n_jobs && ok; ++i) {
+                const int slot = job_tile(i) % C::kKept;
+                if ((used >> slot) & 1) {
+                    if (!mbar_wait(bar(bSFree + slot), (free_par >> slot) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    free_par ^= 1u << slot;
+                }
+                used |= 1u << slot;
+                for (int p = 0; p < 2; ++p, ++k) {
+                    const int s = k % C::kSlots;
+                    if (!mbar_wait(bar(bFull + s), (uint32_t)(k / C::kSlots) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t ka = lo + ((uint32_t)(C::kOffRing + s * kWtPanel) >> 4);
+#pragma unroll
+                    for (int term = 0; term < 3; ++term) {
+                        const uint32_t qb = lo + ((uint32_t)(term * C::kQTerm + p * (C::kQTerm / 2)) >> 4);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma_ss(lead, tmem + (uint32_t)(slot * NQ), desc_with_lo(ka + 2 * x, hi), desc_with_lo(qb + 2 * x, hi),
+                                   kIdesc, p > 0 || term > 0 || x > 0);
+                    }
+                    umma_commit(lead, bar(bEmpty + s));
+                }
+                if (ok)
+                    umma_commit(lead, bar(bSFull + slot));
+            }
+            umma_commit(lead, bar(bQEmpty));
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+        // all issued MMAs complete before TMEM is released
+        umma_commit(lead, bar(bDrain));
+        mbar_drain(bar(bDrain), 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no CTA leaves while a peer may still write to its shared memory
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kWtTmemCols);
+    }
+}
+
+template <int NQ>
+static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
+{
+    using C = WtCfg<NQ>;
+    static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(k_key_weights_tc<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            attr_set[dev].store(true, std::memory_order_release);
+    }
+    const int64_t units = (int64_t)a.n_reqs * a.n_layers * a.n_kv_heads;
+    const int tiles = (a.max_rows + kWtTile - 1) / kWtTile;
+    // as many CTAs as hold the longest request's scores in TMEM; more while the
+    // grid does not fill the SMs and a CTA keeps four tiles
+    int c = 1;
+    while (c < kWtMaxCluster && (tiles > c * C::kKept || (units * c < 2 * n_sms && tiles >= 8 * c)))
+        c *= 2;
+    if (units * c > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * c));
+    cfg.blockDim = dim3(kWtThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)c;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_key_weights_tc<NQ>, tmk, a, rt, c);
+}
+
+cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const void *tmap_k, int n_sms, cudaStream_t s)
+{
+    const CUtensorMap &m = *static_cast<const CUtensorMap *>(tmap_k);
+    const int64_t rows = (int64_t)a.max_q_len * (a.n_q_heads / a.n_kv_heads);
+    if (rows <= 16)
+        return launch_nq<16>(a, rt, m, n_sms, s);
+    if (rows <= 32)
+        return launch_nq<32>(a, rt, m, n_sms, s);
+    return launch_nq<64>(a, rt, m, n_sms, s);
+}
+
+}  // namespace kvr
