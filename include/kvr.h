@@ -45,6 +45,9 @@
  *          head_dim * 2 bytes of device memory (T = query tokens of the
  *          call).  A call with more than the scratch holds waits for the
  *          previous call's attention, frees it and allocates it larger.
+ *          kvr_shared_query_attention uses the same scratch, and beside it up
+ *          to 1 GiB for partial results, grown the same way (134 KB for each
+ *          256 query rows of a group, (layer, kv-head) and slice).
  *       5. A pool in pinned host memory: the first kvr_prefill on it creates
  *          an internal stream and its events (kept until unregister).
  *     kvr_pool_reserve makes 3 and 4 happen up front: afterwards, calls

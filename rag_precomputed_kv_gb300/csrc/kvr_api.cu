@@ -122,6 +122,10 @@ struct kvr_pool {
     size_t q_rot_cap = 0;
     cudaEvent_t q_rot_done = nullptr;
     bool q_rot_used = false;
+    // partial results of the shared-prefix attention (grown on demand; used
+    // and reused with the query scratch)
+    void *part = nullptr;
+    size_t part_cap = 0;
     // a pool in pinned host memory: kvr_prefill stitches it by layer groups on
     // a second stream, each group's attention overlapping the next group's
     // stitch (which reads over the CPU-GPU link)
@@ -190,6 +194,25 @@ struct kvr_pool {
         }
         if (!s.done && (e = cudaEventCreateWithFlags(&s.done, cudaEventDisableTiming)) != cudaSuccess)
             return cuda_fail(e, "staging event");
+        return KVR_OK;
+    }
+
+    // The partial-result scratch with at least `bytes`, likewise.
+    kvr_status grow_part_scratch(size_t bytes)
+    {
+        if (part_cap >= bytes)
+            return KVR_OK;
+        NvtxRange r("kvr.part_scratch_alloc");
+        cudaError_t e;
+        if (q_rot_used && (e = cudaEventSynchronize(q_rot_done)) != cudaSuccess)
+            return cuda_fail(e, "partial result scratch wait");
+        if (part)
+            cudaFree(part);
+        part = nullptr;
+        part_cap = 0;
+        if ((e = cudaMalloc(&part, bytes)) != cudaSuccess)
+            return cuda_fail(e, "partial result scratch");
+        part_cap = bytes;
         return KVR_OK;
     }
 
@@ -323,6 +346,8 @@ extern "C" kvr_status kvr_pool_unregister(kvr_pool_t p)
     }
     if (p->q_rot)
         cudaFree(p->q_rot);
+    if (p->part)
+        cudaFree(p->part);
     if (p->side) {
         cudaStreamSynchronize(p->side);
         cudaStreamDestroy(p->side);
@@ -708,6 +733,23 @@ kvr_status encode_gather_map(const kvr_pool &p, const void *base, CUtensorMap *m
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(KVR_ERR_CUDA, "cuTensorMapEncodeTiled (pool values) failed (%d)", (int)r);
+    return KVR_OK;
+}
+
+// [rows, D] at `base` with a box of 64 columns x `box_rows` rows.
+kvr_status encode_rows_map(const kvr_pool &p, const void *base, int64_t rows, uint32_t box_rows, CUtensorMap *m)
+{
+    if (!p.encode)
+        return fail(KVR_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled not available");
+    const cuuint64_t dims[2] = {(cuuint64_t)p.d.head_dim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.d.head_dim * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = p.encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(KVR_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return KVR_OK;
 }
 
@@ -1258,7 +1300,13 @@ struct SharedPlan {
     int32_t max_lq = 0;
     SharedTable tab;
     AssembleTables atab;
+    std::vector<DevGroup> gr;   // tensor-core path
+    GroupTable gtab;
 };
+
+// Partial results of the prefix part that one launch may hold; a call with
+// more goes through its (layer, kv-head) units in slices.
+constexpr int64_t kMaxPartBytes = int64_t(1) << 30;
 
 // A C entry point lets no exception out (the tables are std::vectors).
 template <typename F>
@@ -1314,6 +1362,182 @@ Range range_of(const void *p, int64_t first, int64_t last, int64_t bytes)
 {
     const char *c = static_cast<const char *>(p);
     return c ? Range{c + first * bytes, c + last * bytes} : Range{nullptr, nullptr};
+}
+
+// The CUDA-core path: the query tokens' keys and values become own rows
+// S_b .. S_b + Lq - 1, turned by their positions P_g + S_b + t (an assemble of
+// un-rotated request-local sources), then the attention.
+kvr_status shared_simt(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, cudaStream_t s)
+{
+    const int H = sa.n_kv_heads, D = p->d.head_dim;
+    std::vector<DevSpan> ap;
+    std::vector<DevLocal> al;
+    for (const DevShared &r : pl.rq) {
+        if (r.q_len == 0)
+            continue;
+        DevSpan d{};
+        d.dst_row0 = r.cache_row0;
+        d.src = KVR_SRC_LOCAL | (int32_t)al.size();
+        d.len = r.q_len;
+        d.row = r.own;
+        d.pos0 = d.delta = r.pre_len + r.own;
+        d.cap = r.cap;
+        d.dstep = 1;
+        ap.push_back(d);
+        const int64_t off = (int64_t)r.q_off * H * D * p->elt();
+        al.push_back(DevLocal{static_cast<const char *>(sa.kq) + off, static_cast<const char *>(sa.vq) + off,
+                              (int64_t)sa.total_q * H * D, D, (int64_t)H * D, r.q_len});
+    }
+    AssembleArgs a{};
+    a.rope = p->rope;
+    a.cache_k = sa.cache_k;
+    a.cache_v = sa.cache_v;
+    a.n_layers = sa.n_layers;
+    a.n_heads = H;
+    a.upc = 1;
+    a.interleaved = sa.interleaved;
+    Slot *slot = nullptr;
+    const bool inl = sa.n_reqs <= kInlineEntries;
+    kvr_status st;
+    if (inl) {
+        std::memcpy(pl.tab.reqs, pl.rq.data(), pl.rq.size() * sizeof(DevShared));
+        std::memcpy(pl.atab.spans, ap.data(), ap.size() * sizeof(DevSpan));
+        std::memcpy(pl.atab.locals, al.data(), al.size() * sizeof(DevLocal));
+    } else {
+        const size_t off_sp = align16(pl.rq.size() * sizeof(DevShared));
+        const size_t off_lc = off_sp + align16(ap.size() * sizeof(DevSpan));
+        std::vector<char> rows(off_lc + al.size() * sizeof(DevLocal));
+        std::memcpy(rows.data(), pl.rq.data(), pl.rq.size() * sizeof(DevShared));
+        std::memcpy(rows.data() + off_sp, ap.data(), ap.size() * sizeof(DevSpan));
+        std::memcpy(rows.data() + off_lc, al.data(), al.size() * sizeof(DevLocal));
+        if ((st = upload_table(p, rows.data(), rows.size(), s, &slot)) != KVR_OK)
+            return st;
+        const char *dv = static_cast<const char *>(slot->dev);
+        sa.reqs = reinterpret_cast<const DevShared *>(dv);
+        a.spans = reinterpret_cast<const DevSpan *>(dv + off_sp);
+        a.locals = reinterpret_cast<const DevLocal *>(dv + off_lc);
+    }
+    p->mark(2, s);
+    cudaError_t e = launch_assemble(a, p->d.dtype, D, (int)ap.size(), s, inl ? &pl.atab : nullptr);
+    p->mark(3, s);
+    if (e == cudaSuccess) {
+        NvtxRange r("kvr.k_shared_simt");
+        p->mark(4, s);
+        e = launch_shared_simt(sa, pl.tab, p->d.dtype, D, s);
+        p->mark(5, s);
+    }
+    if (slot)
+        cudaEventRecord(slot->done, s);
+    return e == cudaSuccess ? KVR_OK : cuda_fail(e, "shared-prefix attention launch");
+}
+
+// The tensor-core path: rotation and append, then, slice by slice of the
+// units, the prefix part and the own part.
+kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_groups, const int32_t *group_offsets,
+                     const int64_t *prefix_offsets, const int32_t *prefix_len, bool any_prefix, const int32_t *q_offsets,
+                     int64_t own_rows, int64_t pre_rows, cudaStream_t s)
+{
+    const int L = sa.n_layers, H = sa.n_kv_heads, Hq = sa.n_q_heads, D = p->d.head_dim, LH = L * H, G = Hq / H;
+    SharedPrefixArgs pa{};
+    pa.group = G;
+    pa.total_q = sa.total_q;
+    pa.scale_log2 = sa.scale_log2;
+    pa.err = p->err;
+    // groups with prefix and tokens first, numbered pair by pair; the others behind them
+    pl.gr.reserve(n_groups);
+    std::vector<int32_t> place(n_groups);
+    for (int pass = 0; pass < 2; ++pass)
+        for (int g = 0; g < n_groups; ++g) {
+            const int32_t t0 = q_offsets[group_offsets[g]], t1 = q_offsets[group_offsets[g + 1]];
+            const bool active = prefix_len[g] > 0 && t1 > t0;
+            if (active != (pass == 0))
+                continue;
+            if ((int64_t)(t1 - t0) * G > INT32_MAX - 256)
+                return fail(KVR_ERR_UNSUPPORTED, "group %d: too many query rows", g);
+            DevGroup d{};
+            d.pre_row0 = prefix_offsets[g] * LH;
+            d.item0 = pa.unit_blocks;
+            d.w0 = pa.unit_pairs;
+            d.pre_cap = (int32_t)(prefix_offsets[g + 1] - prefix_offsets[g]);
+            d.pre_len = prefix_len[g];
+            d.q_off = t0;
+            d.rows = (t1 - t0) * G;
+            if (active) {
+                d.nt = (d.pre_len + 127) / 128;
+                d.mb = (d.rows + 255) / 256;
+                pa.unit_blocks += d.mb;
+                pa.unit_pairs += (int64_t)d.mb * d.nt;
+            }
+            place[g] = (int32_t)pl.gr.size();
+            pl.gr.push_back(d);
+        }
+    for (int g = 0; g < n_groups; ++g)
+        for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
+            pl.rq[b].group = place[g];
+    pa.n_groups = n_groups;
+
+    // slices whose partial results fit kMaxPartBytes
+    int lh_slice = LH;
+    if (pa.unit_blocks > 0) {
+        const int64_t fit = (kMaxPartBytes / kSharedPartBytes - p->n_sms) / pa.unit_blocks;
+        const int64_t n = (LH + std::max<int64_t>(1, fit) - 1) / std::max<int64_t>(1, fit);
+        lh_slice = (int)((LH + n - 1) / n);
+    }
+    kvr_status st;
+    cudaError_t e;
+    const int64_t q_rows = (int64_t)L * sa.total_q * Hq;
+    if ((st = p->grow_query_scratch((size_t)q_rows * D * 2)) != KVR_OK ||
+        (pa.unit_blocks > 0 &&
+         (st = p->grow_part_scratch((size_t)(lh_slice * pa.unit_blocks + p->n_sms) * kSharedPartBytes)) != KVR_OK))
+        return st;
+    pa.part = static_cast<float *>(p->part);
+    pa.q_rot = p->q_rot;
+    CUtensorMap mq, mpk, mpv, mk, mv;
+    if ((st = encode_rows_map(*p, p->q_rot, q_rows, 128, &mq)) != KVR_OK ||
+        (any_prefix && ((st = encode_rows_map(*p, sa.prefix_k, pre_rows, 128, &mpk)) != KVR_OK ||
+                        (st = encode_rows_map(*p, sa.prefix_v, pre_rows, 128, &mpv)) != KVR_OK)) ||
+        (st = encode_rows_map(*p, sa.cache_k, own_rows, 32, &mk)) != KVR_OK ||
+        (st = encode_rows_map(*p, sa.cache_v, own_rows, 32, &mv)) != KVR_OK)
+        return st;
+    // the previous call's attention must be done with the scratch
+    if (p->q_rot_used && (e = cudaStreamWaitEvent(s, p->q_rot_done, 0)) != cudaSuccess)
+        return cuda_fail(e, "query scratch ordering");
+    Slot *slot = nullptr;
+    if (sa.n_reqs <= kInlineEntries && n_groups <= kInlineEntries) {
+        std::memcpy(pl.tab.reqs, pl.rq.data(), pl.rq.size() * sizeof(DevShared));
+        std::memcpy(pl.gtab.groups, pl.gr.data(), pl.gr.size() * sizeof(DevGroup));
+    } else {
+        const size_t off = pl.rq.size() * sizeof(DevShared);
+        std::vector<char> rows(off + pl.gr.size() * sizeof(DevGroup));
+        std::memcpy(rows.data(), pl.rq.data(), off);
+        std::memcpy(rows.data() + off, pl.gr.data(), pl.gr.size() * sizeof(DevGroup));
+        if ((st = upload_table(p, rows.data(), rows.size(), s, &slot)) != KVR_OK)
+            return st;
+        sa.reqs = static_cast<const DevShared *>(slot->dev);
+        pa.groups = reinterpret_cast<const DevGroup *>(static_cast<const char *>(slot->dev) + off);
+    }
+    SharedTcArgs t{&sa, &pl.tab, &pa, &pl.gtab, &mq, any_prefix ? &mpk : nullptr, any_prefix ? &mpv : nullptr, &mk, &mv};
+    p->mark(2, s);
+    {
+        NvtxRange r("kvr.k_shared_prologue");
+        e = launch_shared_prologue(sa, pl.tab, p->q_rot, p->n_sms, s);
+    }
+    p->mark(3, s);
+    p->mark(4, s);
+    for (int lh = 0; lh < LH && e == cudaSuccess; lh += lh_slice) {
+        NvtxRange r("kvr.k_shared_prefix_own");
+        pa.lh_base = lh;
+        pa.lh_count = std::min(lh_slice, LH - lh);
+        pa.total = pa.lh_count * pa.unit_pairs;
+        pa.n_ctas = (int32_t)std::min<int64_t>(p->n_sms, pa.total);
+        e = launch_shared_tc(t, !p->timed, s);
+    }
+    p->mark(5, s);
+    cudaEventRecord(p->q_rot_done, s);
+    p->q_rot_used = true;
+    if (slot)
+        cudaEventRecord(slot->done, s);
+    return e == cudaSuccess ? KVR_OK : cuda_fail(e, "shared-prefix attention launch");
 }
 
 }  // namespace
@@ -1401,40 +1625,15 @@ extern "C" kvr_status kvr_shared_query_attention(kvr_pool_t p, int32_t n_groups,
                 if (any_prefix && d.meets(x))
                     return fail(KVR_ERR_INVALID_ARG, "the cache or the output overlaps the shared prefix");
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if ((st = check_capture(*p, s, batch <= kInlineEntries, "a call of more than 64 requests uploads its tables")) !=
-                KVR_OK ||
+        const bool may_tc = attention_tc_supported(p->d.dtype, D);
+        if ((st = check_capture(*p, s, !may_tc && batch <= kInlineEntries,
+                                "the call uses library scratch, or uploads the tables of more than 64 requests")) != KVR_OK ||
             (st = ensure_device(p)) != KVR_OK)
             return st;
         DeviceGuard g(p->device);
-
-        // the query tokens' keys and values become own rows S_b .. S_b + Lq - 1,
-        // turned by their positions P_g + S_b + t
-        std::vector<DevSpan> ap;
-        std::vector<DevLocal> al;
-        for (const DevShared &r : pl.rq) {
-            if (r.q_len == 0)
-                continue;
-            DevSpan d{};
-            d.dst_row0 = r.cache_row0;
-            d.src = KVR_SRC_LOCAL | (int32_t)al.size();
-            d.len = r.q_len;
-            d.row = r.own;
-            d.pos0 = d.delta = r.pre_len + r.own;
-            d.cap = r.cap;
-            d.dstep = 1;
-            ap.push_back(d);
-            const int64_t off = (int64_t)r.q_off * H * row_bytes;
-            al.push_back(DevLocal{static_cast<const char *>(kq) + off, static_cast<const char *>(vq) + off,
-                                  (int64_t)T * H * D, D, (int64_t)H * D, r.q_len});
-        }
-        AssembleArgs a{};
-        a.rope = p->rope;
-        a.cache_k = cache_k;
-        a.cache_v = cache_v;
-        a.n_layers = L;
-        a.n_heads = H;
-        a.upc = 1;
-        a.interleaved = (p->d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
+        const bool tc = use_tensor_cores(*p);
+        if (tc && std::max({own_rows[1], pre_rows[1], (int64_t)L * T * Hq}) > (int64_t)INT32_MAX - 256)
+            return fail(KVR_ERR_UNSUPPORTED, "cache, prefix or query rows exceed the int32 TMA coordinate range");
         SharedArgs sa{};
         sa.rope = p->rope;
         sa.q = q;
@@ -1452,40 +1651,12 @@ extern "C" kvr_status kvr_shared_query_attention(kvr_pool_t p, int32_t n_groups,
         sa.total_q = T;
         sa.max_q_len = pl.max_lq;
         sa.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
-        sa.interleaved = a.interleaved;
+        sa.interleaved = (p->d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
         sa.err = p->err;
-        Slot *slot = nullptr;
-        const bool inl = batch <= kInlineEntries;
-        if (inl) {
-            std::memcpy(pl.tab.reqs, pl.rq.data(), pl.rq.size() * sizeof(DevShared));
-            std::memcpy(pl.atab.spans, ap.data(), ap.size() * sizeof(DevSpan));
-            std::memcpy(pl.atab.locals, al.data(), al.size() * sizeof(DevLocal));
-        } else {
-            const size_t off_sp = align16(pl.rq.size() * sizeof(DevShared));
-            const size_t off_lc = off_sp + align16(ap.size() * sizeof(DevSpan));
-            std::vector<char> rows(off_lc + al.size() * sizeof(DevLocal));
-            std::memcpy(rows.data(), pl.rq.data(), pl.rq.size() * sizeof(DevShared));
-            std::memcpy(rows.data() + off_sp, ap.data(), ap.size() * sizeof(DevSpan));
-            std::memcpy(rows.data() + off_lc, al.data(), al.size() * sizeof(DevLocal));
-            if ((st = upload_table(p, rows.data(), rows.size(), s, &slot)) != KVR_OK)
-                return st;
-            const char *dv = static_cast<const char *>(slot->dev);
-            sa.reqs = reinterpret_cast<const DevShared *>(dv);
-            a.spans = reinterpret_cast<const DevSpan *>(dv + off_sp);
-            a.locals = reinterpret_cast<const DevLocal *>(dv + off_lc);
-        }
-        p->mark(2, s);
-        cudaError_t e = launch_assemble(a, p->d.dtype, D, (int)ap.size(), s, inl ? &pl.atab : nullptr);
-        p->mark(3, s);
-        if (e == cudaSuccess) {
-            NvtxRange r("kvr.k_shared_simt");
-            p->mark(4, s);
-            e = launch_shared_simt(sa, pl.tab, p->d.dtype, D, s);
-            p->mark(5, s);
-        }
-        if (slot)
-            cudaEventRecord(slot->done, s);
-        return e == cudaSuccess ? KVR_OK : cuda_fail(e, "shared-prefix attention launch");
+        if (tc)
+            return shared_tc(p, pl, sa, n_groups, group_offsets, prefix_offsets, prefix_len, any_prefix, q_offsets,
+                             own_rows[1], pre_rows[1], s);
+        return shared_simt(p, pl, sa, s);
     });
 }
 

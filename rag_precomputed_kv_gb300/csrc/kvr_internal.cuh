@@ -255,7 +255,8 @@ struct alignas(16) DevShared {
     int32_t pre_cap;     // rows per (layer, kv-head) block of the prefix
     int32_t pre_len;     // P_g; query token t sits at position P_g + own + t
     int32_t q_off, q_len;
-    int32_t pad_[6];
+    int32_t group;       // index into the group table (tensor-core path)
+    int32_t pad_[5];
 };
 static_assert(sizeof(DevShared) == 64, "shared-prefix request table layout");
 struct SharedTable {
@@ -275,6 +276,53 @@ struct SharedArgs {
     float scale_log2;
     int32_t interleaved;
     int *err;
+};
+
+// Per-group data (64 bytes) of the tensor-core path: the packed query rows of
+// the group's tokens are consecutive, and meet the prefix in blocks of 256.
+// The (block, key tile) pairs of a (layer, kv-head) unit are numbered group by
+// group; groups without prefix or tokens come last in the table, with nt 0 and
+// the unit's number of pairs as w0.
+struct alignas(16) DevGroup {
+    int64_t pre_row0;    // prefix_offsets[g] * L * H_kv
+    int64_t item0;       // the group's first 256-row block of a unit
+    int64_t w0;          // the group's first (block, key tile) pair of a unit
+    int32_t pre_cap, pre_len;
+    int32_t q_off;       // first token
+    int32_t rows;        // tokens x G
+    int32_t nt;          // 128-key tiles of the prefix
+    int32_t mb;          // 256-row blocks
+    int32_t pad_[4];
+};
+static_assert(sizeof(DevGroup) == 64, "group table layout");
+struct GroupTable {
+    DevGroup groups[kInlineEntries];
+};
+// Bytes of one partial result of the prefix part (a block's rows of one CTA:
+// 256 x 128 fp32 and 256 maxima and sums).
+constexpr int64_t kSharedPartBytes = 256 * 128 * 4 + 256 * 8;
+struct SharedPrefixArgs {
+    const DevGroup *groups;     // NULL: the GroupTable parameter
+    int32_t n_groups;
+    int32_t group;              // G
+    int32_t total_q;
+    int32_t lh_base, lh_count;  // the slice of (layer, kv-head) units of this launch
+    int32_t n_ctas;             // stretches that the pairs are cut in
+    int64_t unit_pairs, unit_blocks;   // pairs, blocks of one unit
+    int64_t total;              // pairs of the slice: lh_count * unit_pairs
+    float *part;                // (blocks + n_ctas) partial results
+    const void *q_rot;          // [L][Hkv][T][G][D], rotated
+    float scale_log2;
+    int *err;
+};
+struct SharedTcArgs {
+    const SharedArgs *base;
+    const SharedTable *reqs;
+    const SharedPrefixArgs *prefix;
+    const GroupTable *groups;
+    // host CUtensorMaps: packed queries and prefix (64 x 128 boxes; the prefix's
+    // NULL when nothing is shared), own caches (64 x 32 boxes)
+    const void *tmap_q, *tmap_pk, *tmap_pv, *tmap_k, *tmap_v;
 };
 
 // ---- attention weight per cached key ----
@@ -401,6 +449,10 @@ cudaError_t launch_wait_selftest(int *err, unsigned long long limit_ns, cudaStre
 cudaError_t launch_decode_attention(const AttnArgs &a, const ReqTable &rt, const void *tmap_k, const void *tmap_v,
                                     const DecodeIO &io, bool pdl, cudaStream_t s);
 cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, cudaStream_t s);
+// bf16, head_dim 128: rotation and append, then the prefix part and the own part
+// of a slice of the units.
+cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, int n_sms, cudaStream_t s);
+cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s);
 cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, cudaStream_t s);
 // bf16, head_dim 128: the tensor-core kernel; `tmap_k` points to the CUtensorMap
 // of the cache's keys ([rows, head_dim], 64 x 128 boxes).

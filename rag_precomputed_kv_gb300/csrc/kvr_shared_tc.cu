@@ -1,0 +1,902 @@
+// kvr_shared_tc.cu -- query attention over a prefix shared by a group of
+// requests, on the tensor cores (bf16, head_dim 128).
+//
+// O_r = (sum_j e^{s_rj} v_j) / (sum_j e^{s_rj}) over the shared prefix rows and
+// the request's own rows (CoinRAG blog section 2.3: KV_M(q; C_ctx), with C_ctx
+// the same for the whole group).  The sums over a set of keys, each with its
+// own maximum m (sum e^{s - m} v, sum e^{s - m}), add after scaling by
+// e^{m - max}, so the two parts are computed apart:
+//
+//   k_shared_prologue  rotates the query heads at P_g + S_b + t into a packed
+//                      scratch [layer][kv-head][token][G][D], and appends the
+//                      keys (rotated) and values at own row S_b + t.
+//   k_shared_prefix    the prefix part.  The packed rows of a whole group are
+//                      consecutive: M = tokens of the group x G rows meet each
+//                      prefix tile once, in blocks of 256 rows.  tcgen05, as
+//                      the query-prefill attention: two 128-row tiles A and B
+//                      per CTA, S and P and O in TMEM.  A block of at most 128
+//                      rows (a decode step of a few requests) is bound by the
+//                      reads of K and V, not by the MMAs: then A and B hold the
+//                      same rows and take alternate key tiles, so that one
+//                      tile's softmax overlaps the other's.  The work, all
+//                      (block, key tile) pairs of the call in a row, is cut in
+//                      equal stretches, one per SM; a block that a stretch ends
+//                      in has several partial results.
+//   k_shared_own       the own part, and the sum of everything.  One CTA per
+//                      (request, layer, kv-head, row tile); at a few rows per
+//                      request this streams the own rows through register-
+//                      resident warp MMAs (as the decode step), then adds the
+//                      prefix's partial results and writes the output.
+//
+// Values behind the last prefix row are zeroed in shared memory before the
+// P V product that reaches them (a masked key's weight is 0, but 0 x NaN is
+// NaN), so the blocks' spare rows are neither read as data nor written.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <utility>
+
+#include "kvr_decode_common.cuh"
+#include "kvr_tc_common.cuh"
+
+namespace kvr {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kSpThreads = 384;
+constexpr int kSpRegsLaunch = 168, kSpRegsSoftmax = 200, kSpRegsOther = 104;
+static_assert(2 * 128 * kSpRegsSoftmax + 128 * kSpRegsOther <= kSpThreads * kSpRegsLaunch, "register split");
+constexpr int kSpD = 128;
+constexpr int kSpTile = 128;                        // keys per tile, rows per query tile
+constexpr int kSpSlots = 5;                         // K/V ring
+constexpr int kSpTileBytes = kSpTile * kSpD * 2;    // 32 KB
+constexpr int kSpPanel = kSpTileBytes / 2;
+constexpr int kSpTmemCols = 512;
+__host__ __device__ constexpr uint32_t sp_col_s(int x) { return 128u * (uint32_t)x; }
+__host__ __device__ constexpr uint32_t sp_col_o(int x) { return 256u + 128u * (uint32_t)x; }
+constexpr float kSpRescale = 8.0f;
+
+constexpr int kSpOffQ = 0;
+constexpr int kSpOffKV = 2 * kSpTileBytes;
+constexpr int kSpOffBar = kSpOffKV + kSpSlots * kSpTileBytes;
+constexpr int kSbFull = 0, kSbEmpty = kSbFull + kSpSlots, kSbS = kSbEmpty + kSpSlots, kSbP = kSbS + 2, kSbO = kSbP + 2,
+              kSbOEmpty = kSbO + 2, kSbQ = kSbOEmpty + 2, kSbQEmpty = kSbQ + 1, kSbDrain = kSbQEmpty + 1,
+              kSbNum = kSbDrain + 1;
+constexpr int kSpOffMisc = kSpOffBar + 8 * kSbNum;
+constexpr int kSpSmem = kSpOffMisc + 16 + 1024;     // + alignment slack
+static_assert(kSpSmem <= 227 * 1024, "shared memory budget");
+
+constexpr uint32_t kSpIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kSpTile >> 3) << 17) |
+                               ((uint32_t)(kSpTile >> 4) << 24);
+constexpr uint32_t kSpIdescPV = kSpIdescS | (1u << 16);   // V is MN-major
+
+// A partial result of one block and one CTA: per tile x, O as float4
+// [column / 4][row] (lanes are rows: coalesced), then (max, sum) [row].
+constexpr int64_t kPartO = 2 * 128 * 128;                        // floats
+constexpr int64_t kPartFloats = kPartO + 2 * 128 * 2;
+static_assert(kPartFloats * 4 == kSharedPartBytes, "partial result layout");
+
+__device__ __forceinline__ float4 *part_o(float *part, int64_t slot, int x)
+{
+    return reinterpret_cast<float4 *>(part + slot * kPartFloats) + x * (128 * 32);
+}
+__device__ __forceinline__ float2 *part_ml(float *part, int64_t slot, int x)
+{
+    return reinterpret_cast<float2 *>(part + slot * kPartFloats + kPartO) + x * 128;
+}
+
+// Stretch c of the call's `total` (block, key tile) pairs starts here.
+__device__ __forceinline__ int64_t stretch_start(int64_t total, int n, int c) { return total * c / n; }
+// The stretch that holds pair w.
+__device__ __forceinline__ int stretch_of(int64_t total, int n, int64_t w)
+{
+    int c = (int)(w * n / total);
+    while (stretch_start(total, n, c + 1) <= w)
+        ++c;
+    while (stretch_start(total, n, c) > w)
+        --c;
+    return c;
+}
+
+// One block's part in a CTA's stretch.
+struct Seg {
+    DevGroup g;
+    int lh;          // (layer, kv-head), within the call's slice
+    int row0;        // first packed row of the block in the group
+    int rows;        // rows of the block (<= 256)
+    bool dual;       // <= 128 rows: tiles A and B take alternate key tiles
+    int jb, je;      // key tiles
+    int64_t item;    // block index in the call
+    int64_t next;    // the stretch's next pair
+};
+
+__device__ __forceinline__ Seg seg_at(const SharedPrefixArgs &a, const DevGroup *groups, int64_t w, int64_t w_end)
+{
+    Seg s;
+    s.lh = (int)(w / a.unit_pairs);
+    const int64_t in_unit = w - (int64_t)s.lh * a.unit_pairs;
+    int lo = 0, hi = a.n_groups - 1;
+    while (lo < hi) {   // the last group whose first pair in the unit is <= w (one with tiles)
+        const int mid = (lo + hi + 1) >> 1;
+        if (groups[mid].w0 <= in_unit)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    s.g = groups[lo];
+    const int blk = (int)((in_unit - s.g.w0) / s.g.nt);
+    s.jb = (int)(in_unit - s.g.w0 - (int64_t)blk * s.g.nt);
+    s.je = (int)min((int64_t)s.g.nt, s.jb + (w_end - w));
+    s.next = w + (s.je - s.jb);
+    s.item = (int64_t)s.lh * a.unit_blocks + s.g.item0 + blk;
+    s.row0 = blk * 256;
+    s.rows = min(256, s.g.rows - s.row0);
+    s.dual = s.rows <= 128;
+    return s;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kSpThreads, 1)
+    k_shared_prefix(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ SharedPrefixArgs a,
+                    const __grid_constant__ GroupTable gt)
+{
+    const DevGroup *groups = a.groups ? a.groups : gt.groups;
+    extern __shared__ uint8_t sp_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(sp_smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + kSpOffBar + 8u * (uint32_t)i; };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSpOffMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t w_begin = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x),
+                  w_end = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x + 1);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSbNum; ++i)
+            mbar_init(bar(i), (i >= kSbP && i < kSbP + 2) || (i >= kSbOEmpty && i < kSbOEmpty + 2) ? 128u : 1u);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9)
+        tmem_alloc(sbase + kSpOffMisc, kSpTmemCols);
+    if (warp == 8 && lane == 0) {
+        prefetch_tmap(&tmq);
+        prefetch_tmap(&tmk);
+        prefetch_tmap(&tmv);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kSpOffMisc);
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSpRegsSoftmax));
+        pdl_wait_prerequisites();   // (the partial results' scratch may still be read by the call before)
+        const int x = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float sc = a.scale_log2;
+        int s_cnt = 0, o_cnt = 0;
+        bool ok = true;
+        for (int64_t w = w_begin; w < w_end && ok;) {
+            const Seg sg = seg_at(a, groups, w, w_end);
+            w = sg.next;
+            const int j0 = sg.jb + (sg.dual ? x : 0), step = sg.dual ? 2 : 1;
+            const bool row_ok = (sg.dual ? r : x * 128 + r) < sg.rows;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = j0; j < sg.je; j += step) {
+                if (!mbar_wait(bar(kSbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++s_cnt;
+                tc_fence_after();
+                float s[kSpTile];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    tmem_ld32(lane_base + sp_col_s(x) + 32 * q, s + 32 * q);
+                tmem_wait_ld();
+                const int lim = sg.g.pre_len - j * kSpTile;   // keys of the tile that exist
+                if (lim < kSpTile) {
+#pragma unroll
+                    for (int c = 0; c < kSpTile; ++c)
+                        s[c] = (c < lim) ? s[c] : -INFINITY;
+                }
+                float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int c = 4; c < kSpTile; c += 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        m4[k] = fmaxf(m4[k], s[c + k]);
+                }
+                const float mxs = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+                // lazy maximum: O and l are rescaled only when it grows by more than
+                // the threshold
+                float corr = 1.f;
+                if (j == j0) {
+                    m_run = mxs;
+                } else if (mxs > m_run + kSpRescale) {
+                    corr = ex2(m_run - mxs);
+                    m_run = mxs;
+                }
+                const float nm = m_run == -INFINITY ? 0.f : -m_run;   // (a score of -inf in every key)
+                float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float p0 = ex2(fmaf(s[32 * q + 2 * i], sc, nm)), p1 = ex2(fmaf(s[32 * q + 2 * i + 1], sc, nm));
+                        sum4[(2 * i) & 3] += p0;
+                        sum4[(2 * i + 1) & 3] += p1;
+                        pk[i] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(lane_base + sp_col_s(x) + 16 * q, pk);
+                }
+                l_run = l_run * corr + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+                if (corr != 1.f) {
+                    // the commit that signalled this S covers the P V before it: O is stable
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float o[32];
+                        tmem_ld32(lane_base + sp_col_o(x) + 32 * q, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] *= corr;
+                        tmem_st32(lane_base + sp_col_o(x) + 32 * q, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(kSbP + x));
+            }
+            if (!ok)
+                break;
+            // the partial result: O (relative to m), m, l
+            const int64_t slot = sg.item + blockIdx.x;
+            if (row_ok)
+                part_ml(a.part, slot, x)[r] = make_float2(m_run, l_run);
+            if (j0 >= sg.je)
+                continue;   // no key tile for B: its maximum is -inf, its sum 0
+            if (!mbar_wait(bar(kSbO + x), (uint32_t)o_cnt & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            ++o_cnt;
+            tc_fence_after();
+            float4 *po = part_o(a.part, slot, x) + r;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float o[32];
+                tmem_ld32(lane_base + sp_col_o(x) + 32 * q, o);
+                tmem_wait_ld();
+                if (row_ok) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        po[(8 * q + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar(kSbOEmpty + x));
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+    } else if (warp == 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSpRegsOther));
+        if (lane == 0) {
+            // the prefix is not written by the kernel before (the prologue), so its
+            // tiles are loaded ahead of the wait for it; the packed queries are not
+            bool ok = true, waited = false;
+            int tt = 0, nq = 0;
+            for (int64_t w = w_begin; w < w_end && ok;) {
+                const Seg sg = seg_at(a, groups, w, w_end);
+                w = sg.next;
+                const int64_t kv0 = sg.g.pre_row0 + (int64_t)(a.lh_base + sg.lh) * sg.g.pre_cap;
+                const int n_loads = 2 * (sg.je - sg.jb);
+                for (int i = 0; i <= n_loads && ok; ++i) {
+                    if (i == 2) {   // the queries after the first K and V tile
+                        if (!waited) {
+                            pdl_wait_prerequisites();
+                            waited = true;
+                        }
+                        if (nq > 0 && !mbar_wait(bar(kSbQEmpty), (uint32_t)(nq - 1) & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        const int nx = sg.dual ? 1 : 2;
+                        const int q0 = (int)(((int64_t)(a.lh_base + sg.lh) * a.total_q + sg.g.q_off) * a.group + sg.row0);
+                        mbar_expect_tx(bar(kSbQ), (uint32_t)(nx * kSpTileBytes));
+                        for (int x = 0; x < nx; ++x) {
+                            const uint32_t dst = sbase + (uint32_t)(kSpOffQ + x * kSpTileBytes);
+                            tma_load_2d(dst, &tmq, 0, q0 + x * kSpTile, bar(kSbQ));
+                            tma_load_2d(dst + kSpPanel, &tmq, 64, q0 + x * kSpTile, bar(kSbQ));
+                        }
+                        ++nq;
+                    }
+                    if (i == n_loads)
+                        break;
+                    const int slot = tt % kSpSlots;
+                    if (tt >= kSpSlots && !mbar_wait(bar(kSbEmpty + slot), (uint32_t)(tt / kSpSlots - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + (uint32_t)(kSpOffKV + slot * kSpTileBytes);
+                    const CUtensorMap *map = (i & 1) ? &tmv : &tmk;
+                    const int row = (int)(kv0 + (int64_t)(sg.jb + (i >> 1)) * kSpTile);
+                    mbar_expect_tx(bar(kSbFull + slot), kSpTileBytes);
+                    tma_load_2d(dst, map, 0, row, bar(kSbFull + slot));
+                    tma_load_2d(dst + kSpPanel, map, 64, row, bar(kSbFull + slot));
+                    ++tt;
+                }
+            }
+            if (!ok)
+                give_up(a.err, abort_flag);
+            for (int k = tt > kSpSlots ? tt - kSpSlots : 0; k < tt; ++k)
+                mbar_drain(bar(kSbFull + k % kSpSlots), (uint32_t)(k / kSpSlots) & 1);
+            if (nq > 0)
+                mbar_drain(bar(kSbQ), (uint32_t)(nq - 1) & 1);
+        }
+    } else if (warp == 9) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSpRegsOther));
+        const uint32_t lead = elect_one();
+        int tt = 0, nq = 0, p_cnt[2] = {0, 0}, oe_cnt[2] = {0, 0};
+        bool o_used[2] = {false, false}, ok = true;
+        const uint64_t d_k = sdesc(sbase, 16, 1024), d_v = sdesc(sbase, kSpPanel, 1024);
+        const uint32_t lo_k = (uint32_t)d_k, hi_k = (uint32_t)(d_k >> 32), lo_v = (uint32_t)d_v, hi_v = (uint32_t)(d_v >> 32);
+        auto wait_kv = [&](int k) -> bool {
+            if (!mbar_wait(bar(kSbFull + k % kSpSlots), (uint32_t)(k / kSpSlots) & 1, abort_flag))
+                return false;
+            tc_fence_after();
+            return true;
+        };
+        // S_x = Q_qx K^T with K the ring's load k
+        auto issue_s = [&](int x, int qx, int k) {
+            const uint32_t qa = lo_k + ((uint32_t)(kSpOffQ + qx * kSpTileBytes) >> 4);
+            const uint32_t kb = lo_k + ((uint32_t)(kSpOffKV + (k % kSpSlots) * kSpTileBytes) >> 4);
+#pragma unroll
+            for (int i = 0; i < kSpD / 16; ++i) {
+                const uint32_t off = (uint32_t)((i >> 2) * kSpPanel + (i & 3) * 32) >> 4;
+                mma_ss(lead, tmem + sp_col_s(x), desc_with_lo(qa + off, hi_k), desc_with_lo(kb + off, hi_k), kSpIdescS, i > 0);
+            }
+            umma_commit(lead, bar(kSbS + x));
+        };
+        auto issue_pv = [&](int x, int k, uint32_t acc0) {
+            const uint32_t vb = lo_v + ((uint32_t)(kSpOffKV + (k % kSpSlots) * kSpTileBytes) >> 4);
+#pragma unroll
+            for (int i = 0; i < kSpTile / 16; ++i)
+                mma_ts(lead, tmem + sp_col_o(x), tmem + sp_col_s(x) + 8 * i, desc_with_lo(vb + ((i * 2048) >> 4), hi_v),
+                       kSpIdescPV, i > 0 ? 1u : acc0);
+        };
+        for (int64_t w = w_begin; w < w_end && ok;) {
+            const Seg sg = seg_at(a, groups, w, w_end);
+            w = sg.next;
+            const int K = sg.je - sg.jb, step = sg.dual ? 2 : 1;
+            // V tile i of the segment: landed, its rows behind the prefix zeroed
+            auto wait_v = [&](int i) -> bool {
+                if (!wait_kv(tt + 2 * i + 1))
+                    return false;
+                const int lim = sg.g.pre_len - (sg.jb + i) * kSpTile;
+                if (lim < kSpTile) {
+                    const uint32_t v = sbase + (uint32_t)(kSpOffKV + ((tt + 2 * i + 1) % kSpSlots) * kSpTileBytes);
+                    for (int c = lim * 8 + lane; c < kSpTile * 8; c += 32) {
+                        st_shared_v4(v + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
+                        st_shared_v4(v + kSpPanel + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                return true;
+            };
+            auto o_free = [&](int x) -> bool {
+                if (o_used[x]) {
+                    if (!mbar_wait(bar(kSbOEmpty + x), (uint32_t)oe_cnt[x] & 1, abort_flag))
+                        return false;
+                    ++oe_cnt[x];
+                    o_used[x] = false;
+                }
+                return true;
+            };
+            if (!mbar_wait(bar(kSbQ), (uint32_t)nq & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            ++nq;
+            tc_fence_after();
+            // the first S of each tile
+            for (int x = 0; x < 2 && ok; ++x) {
+                const int i = sg.dual ? x : 0;
+                if (i >= K)
+                    continue;
+                if (!o_free(x) || ((sg.dual || x == 0) && !wait_kv(tt + 2 * i))) {
+                    ok = false;
+                    break;
+                }
+                issue_s(x, sg.dual ? 0 : x, tt + 2 * i);
+                if (sg.dual)
+                    umma_commit(lead, bar(kSbEmpty + (tt + 2 * i) % kSpSlots));
+            }
+            if (!ok)
+                break;
+            if (!sg.dual)
+                umma_commit(lead, bar(kSbEmpty + tt % kSpSlots));
+            if (K <= step)
+                umma_commit(lead, bar(kSbQEmpty));
+            for (int i = 0; i < K && ok; ++i) {
+                bool v_ready = false, k_ready = false;
+                const bool more = i + step < K;
+                for (int x = sg.dual ? i & 1 : 0; x < (sg.dual ? (i & 1) + 1 : 2); ++x) {
+                    if (!mbar_wait(bar(kSbP + x), (uint32_t)p_cnt[x] & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    ++p_cnt[x];
+                    if (!v_ready && !(v_ready = wait_v(i))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    issue_pv(x, tt + 2 * i + 1, i >= step);
+                    if (!more) {
+                        umma_commit(lead, bar(kSbO + x));
+                        o_used[x] = true;
+                    } else {
+                        if (!k_ready && !(k_ready = wait_kv(tt + 2 * (i + step)))) {
+                            ok = false;
+                            break;
+                        }
+                        issue_s(x, sg.dual ? 0 : x, tt + 2 * (i + step));
+                    }
+                }
+                if (!ok)
+                    break;
+                if (more && i + step + 1 == K)
+                    umma_commit(lead, bar(kSbQEmpty));   // the segment's last S is issued
+                umma_commit(lead, bar(kSbEmpty + (tt + 2 * i + 1) % kSpSlots));
+                if (more)
+                    umma_commit(lead, bar(kSbEmpty + (tt + 2 * (i + step)) % kSpSlots));
+            }
+            tt += 2 * K;
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+        umma_commit(lead, bar(kSbDrain));
+        mbar_drain(bar(kSbDrain), 0);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSpRegsOther));
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kSpTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the query side
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kPrTokens = 16;                // query tokens per piece
+constexpr int kPrThreads = 8 * kPrTokens;    // 8 threads a token: elements [8j, 8j + 8) and [64 + 8j, ..)
+
+__device__ __forceinline__ void rotate_row(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
+{
+    if (il)
+        rotate_bf16x8_il(lo, hi, c, s);
+    else
+        rotate_bf16x8(lo, hi, c, s);
+}
+}  // namespace
+
+// Pieces of (request, 16 tokens, layer, kv-head), a grid-stride loop.
+__global__ void __launch_bounds__(kPrThreads)
+    k_shared_prologue(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt, __nv_bfloat16 *q_rot)
+{
+    constexpr int D = kSpD, H2 = D / 2, E = 8;
+    const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
+    const int n_chunks = (a.max_q_len + kPrTokens - 1) / kPrTokens;
+    const int64_t n_rc = (int64_t)a.n_reqs * n_chunks, n_items = n_rc * a.n_layers * a.n_kv_heads;
+    const int G = a.n_q_heads / a.n_kv_heads, j = threadIdx.x & 7;
+    const int64_t T = a.total_q;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q), *kq = static_cast<const __nv_bfloat16 *>(a.kq),
+                        *vq = static_cast<const __nv_bfloat16 *>(a.vq);
+    __nv_bfloat16 *ck = static_cast<__nv_bfloat16 *>(a.cache_k), *cv = static_cast<__nv_bfloat16 *>(a.cache_v);
+    pdl_launch_dependents();   // the attention kernel sets up, and loads prefix tiles, meanwhile
+    for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
+        const int64_t rc = it % n_rc;
+        const int lh = (int)(it / n_rc);
+        const DevShared rq = reqs[rc / n_chunks];
+        const int t = (int)(rc % n_chunks) * kPrTokens + (int)(threadIdx.x >> 3);
+        if (t >= rq.q_len)
+            continue;
+        const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
+        const int64_t tok = l * T + rq.q_off + t;
+        float c[E], s[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float2 cs = rope_cs(a.rope, H2, rq.pre_len + rq.own + t, rope_pair(a.interleaved, D, E, j, e));
+            c[e] = cs.x;
+            s[e] = cs.y;
+        }
+        const int64_t src = (tok * a.n_kv_heads + h) * D + j * E;
+        uint4 klo = *reinterpret_cast<const uint4 *>(kq + src), khi = *reinterpret_cast<const uint4 *>(kq + src + H2);
+        const uint4 vlo = *reinterpret_cast<const uint4 *>(vq + src), vhi = *reinterpret_cast<const uint4 *>(vq + src + H2);
+        rotate_row(klo, khi, c, s, a.interleaved);
+        const int64_t dst = (rq.cache_row0 + (int64_t)lh * rq.cap + rq.own + t) * D + j * E;
+        *reinterpret_cast<uint4 *>(ck + dst) = klo;
+        *reinterpret_cast<uint4 *>(ck + dst + H2) = khi;
+        *reinterpret_cast<uint4 *>(cv + dst) = vlo;
+        *reinterpret_cast<uint4 *>(cv + dst + H2) = vhi;
+        const int64_t q_src = (tok * a.n_q_heads + (int64_t)h * G) * D + j * E;
+        const int64_t q_dst = ((int64_t)lh * T + rq.q_off + t) * G * D + j * E;
+        for (int g = 0; g < G; ++g) {
+            uint4 lo = *reinterpret_cast<const uint4 *>(q + q_src + (int64_t)g * D);
+            uint4 hi = *reinterpret_cast<const uint4 *>(q + q_src + (int64_t)g * D + H2);
+            rotate_row(lo, hi, c, s, a.interleaved);
+            *reinterpret_cast<uint4 *>(q_rot + q_dst + (int64_t)g * D) = lo;
+            *reinterpret_cast<uint4 *>(q_rot + q_dst + (int64_t)g * D + H2) = hi;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the own part and the sum
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kOwThreads = 128;
+constexpr int kOwTile = 128;                        // keys per tile, loaded 32 rows at a time
+constexpr int kOwOffBar = 2 * dec::kDecTileBytes;   // K tile, V tile
+constexpr int kOwSmem = kOwOffBar + 16 + 1024;      // + alignment slack
+constexpr int kOwRowsMax = 64;
+// the states (m, l, O [rows][128]) over the tiles at the end
+static_assert(4 * 16 * 2 * 4 + 4 * 16 * kSpD * 4 <= 2 * dec::kDecTileBytes, "state area");
+}  // namespace
+
+// kSplit: the CTA's rows are one MMA row tile (<= 16) and each warp takes 32
+// keys of a tile; otherwise each warp has a row tile of its own and takes all
+// 128 keys.
+template <bool kSplit>
+__global__ void __launch_bounds__(kOwThreads)
+    k_shared_own(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                 const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
+                 const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt, const int n_row_tiles)
+{
+    using namespace dec;
+    constexpr int kRows = kSplit ? 16 : kOwRowsMax;
+    extern __shared__ uint8_t ow_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ow_smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = dec_smem_u32(smem), kt = sbase, vt = sbase + kDecTileBytes, full = sbase + kOwOffBar;
+    const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
+    const DevGroup *groups = pa.groups ? pa.groups : gt.groups;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = pa.group;
+    int64_t bi = blockIdx.x;
+    const int tile = (int)(bi % n_row_tiles);
+    bi /= n_row_tiles;
+    const int lh_s = (int)(bi % pa.lh_count), lh = pa.lh_base + lh_s;
+    const DevShared rq = reqs[bi / pa.lh_count];
+    const int m_rows = rq.q_len * G, r0 = tile * kRows;
+    volatile int *cta_err = reinterpret_cast<volatile int *>(smem + kOwOffBar + 8);
+    if (threadIdx.x == 0) {
+        dec_mbar_init(full, 1);
+        *cta_err = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_wait_prerequisites();
+    if (r0 >= m_rows)
+        return;   // uniform over the CTA
+    const int rows = min(kRows, m_rows - r0);
+    const int n_keys = rq.own + (r0 + rows - 1) / G + 1;   // of the last row
+    const int n_t = (n_keys + kOwTile - 1) / kOwTile;
+    const int64_t kv_row0 = rq.cache_row0 + (int64_t)lh * rq.cap;
+
+    auto issue = [&](int j) {   // thread 0
+        const int n32 = min(4, (n_keys - j * kOwTile + 31) >> 5);
+        dec_expect_tx(full, (uint32_t)(n32 * 32 * kSpD * 2 * 2));
+        for (int i = 0; i < n32; ++i) {
+            const int row = (int)(kv_row0 + (int64_t)j * kOwTile + 32 * i);
+            const uint32_t d = (uint32_t)(i * 32 * 128);
+            dec_tma_load(kt + d, &tmk, 0, row, full);
+            dec_tma_load(kt + kDecPanel + d, &tmk, 64, row, full);
+            dec_tma_load(vt + d, &tmv, 0, row, full);
+            dec_tma_load(vt + kDecPanel + d, &tmv, 64, row, full);
+        }
+    };
+    if (threadIdx.x == 0)
+        issue(0);
+
+    // query fragments (A operand): rows q_lo, q_lo + 8 of this warp's row tile
+    const int rt0 = kSplit ? 0 : 16 * warp;              // first CTA row of the warp's row tile
+    const int ra = rt0 + (lane >> 2), rb = ra + 8, cq = (lane & 3) * 2;
+    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(pa.q_rot) +
+                              (((int64_t)lh * a.total_q + rq.q_off) * G + r0) * kSpD;
+    uint32_t qa[8][4];
+#pragma unroll
+    for (int kb = 0; kb < 8; ++kb) {
+        const int c0 = kb * 16 + cq;
+        auto ld2 = [&](int r, int c) -> uint32_t {
+            return r < rows ? *reinterpret_cast<const uint32_t *>(qp + (int64_t)r * kSpD + c) : 0u;
+        };
+        qa[kb][0] = ld2(ra, c0);
+        qa[kb][1] = ld2(rb, c0);
+        qa[kb][2] = ld2(ra, c0 + 8);
+        qa[kb][3] = ld2(rb, c0 + 8);
+    }
+    // keys that the two rows see
+    const int see[2] = {ra < rows ? rq.own + (r0 + ra) / G + 1 : 0, rb < rows ? rq.own + (r0 + rb) / G + 1 : 0};
+
+    const float sc = a.scale_log2;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float o[16][4];
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+        o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int j = 0; j < n_t; ++j) {
+        if (!dec_wait(full, (uint32_t)j & 1))
+            *cta_err = 1;
+        const int kk0 = j * kOwTile, n_here = min(kOwTile, n_keys - kk0);
+        // V rows behind the last key are zero (32-row groups that were loaded)
+        const int n_ld = (n_here + 31) & ~31;
+        for (int idx = threadIdx.x; idx < (n_ld - n_here) * 16; idx += kOwThreads) {
+            const int row = n_here + (idx >> 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vt + sw_off(row, idx & 15)), "r"(0u) : "memory");
+        }
+        __syncthreads();
+        if (*cta_err) {   // the same for every thread
+            if (threadIdx.x == 0) {
+                atomicCAS(a.err, kDevOk, kDevTimeout);
+                mbar_drain(full, (uint32_t)j & 1);
+            }
+            return;
+        }
+        for (int key0 = kSplit ? 32 * warp : 0; key0 < (kSplit ? min(32 * warp + 1, n_here) : n_here); key0 += 32) {
+            float c[4][4];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb)
+                c[nb][0] = c[nb][1] = c[nb][2] = c[nb][3] = 0.f;
+#pragma unroll
+            for (int nb = 0; nb < 4; nb += 2) {
+#pragma unroll
+                for (int kb = 0; kb < 8; ++kb) {
+                    const int mi = lane >> 3;
+                    const int key = key0 + 8 * (nb + (mi >> 1)) + (lane & 7);
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4(kt + sw_off(key, 2 * kb + (mi & 1)), b0, b1, b2, b3);
+                    mma_bf16(c[nb], qa[kb], b0, b1);
+                    mma_bf16(c[nb + 1], qa[kb], b2, b3);
+                }
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = kk0 + key0 + 8 * nb + cq + (e & 1);
+                    c[nb][e] = kk < see[e >> 1] ? c[nb][e] * sc : -INFINITY;
+                    mx[e >> 1] = fmaxf(mx[e >> 1], c[nb][e]);
+                }
+            }
+            float corr[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                const float m_new = fmaxf(m_run[h], mx[h]);
+                corr[h] = m_new == -INFINITY ? 1.f : dec_ex2(m_run[h] - m_new);
+                m_run[h] = m_new;
+            }
+            const float nm[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
+            float sum[2] = {0.f, 0.f};
+            uint32_t p[2][4];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+                const float p0 = dec_ex2(c[nb][0] + nm[0]), p1 = dec_ex2(c[nb][1] + nm[0]);
+                const float p2 = dec_ex2(c[nb][2] + nm[1]), p3 = dec_ex2(c[nb][3] + nm[1]);
+                sum[0] += p0 + p1;
+                sum[1] += p2 + p3;
+                p[nb >> 1][(nb & 1) * 2 + 0] = pack2(p0, p1);
+                p[nb >> 1][(nb & 1) * 2 + 1] = pack2(p2, p3);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+                l_run[h] = l_run[h] * corr[h] + sum[h];
+            }
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                o[n][0] *= corr[0];
+                o[n][1] *= corr[0];
+                o[n][2] *= corr[1];
+                o[n][3] *= corr[1];
+            }
+#pragma unroll
+            for (int kb2 = 0; kb2 < 2; ++kb2) {
+#pragma unroll
+                for (int n = 0; n < 16; n += 2) {
+                    const int mi = lane >> 3;
+                    const int key = key0 + 16 * kb2 + 8 * (mi & 1) + (lane & 7);
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4_t(vt + sw_off(key, n + (mi >> 1)), b0, b1, b2, b3);
+                    mma_bf16(o[n], p[kb2], b0, b1);
+                    mma_bf16(o[n + 1], p[kb2], b2, b3);
+                }
+            }
+        }
+        __syncthreads();   // the tile is consumed
+        if (threadIdx.x == 0 && j + 1 < n_t)
+            issue(j + 1);
+    }
+    // the warps' states [4 x 16] over the tiles
+    float *mm = reinterpret_cast<float *>(smem), *ll = mm + 64, *oo = ll + 64;
+    const int sa = 16 * warp + (lane >> 2), sb = sa + 8;
+    if ((lane & 3) == 0) {
+        mm[sa] = m_run[0];
+        mm[sb] = m_run[1];
+        ll[sa] = l_run[0];
+        ll[sb] = l_run[1];
+    }
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+        const int col = 8 * n + cq;
+        *reinterpret_cast<float2 *>(oo + sa * kSpD + col) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2 *>(oo + sb * kSpD + col) = make_float2(o[n][2], o[n][3]);
+    }
+    __syncthreads();
+    // 8 threads a row, 16 columns each: own states (in warp order), then the
+    // prefix's partial results (in stretch order)
+    const DevGroup g = groups[rq.group];
+    const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
+    for (int row = threadIdx.x >> 3; row < rows; row += kOwThreads / 8) {
+        const int c0 = 16 * (threadIdx.x & 7);
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < (kSplit ? 4 : 1); ++w)
+            M = fmaxf(M, mm[w * 16 + row]);
+        int64_t s_lo = 0;
+        int n_slots = 0, x_lo = 0, x_hi = 0, pr = 0;
+        if (g.nt > 0) {
+            const int gr = (rq.q_off - g.q_off) * G + r0 + row, blk = gr >> 8, in = gr & 255;
+            const bool dual = min(256, g.rows - 256 * blk) <= 128;
+            const int64_t it = (int64_t)lh_s * pa.unit_blocks + g.item0 + blk;
+            const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.nt;
+            const int ca = stretch_of(pa.total, pa.n_ctas, w0), cb = stretch_of(pa.total, pa.n_ctas, w0 + g.nt - 1);
+            s_lo = it + ca;
+            n_slots = cb - ca + 1;
+            x_lo = dual ? 0 : in >> 7;
+            x_hi = dual ? 1 : x_lo;
+            pr = in & 127;
+            for (int i = 0; i < n_slots; ++i)
+                for (int x = x_lo; x <= x_hi; ++x)
+                    M = fmaxf(M, part_ml(pa.part, s_lo + i, x)[pr].x);
+        }
+        const float Mr = M == -INFINITY ? 0.f : M;
+        float L = 0.f, acc[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < (kSplit ? 4 : 1); ++w) {
+            const int st = w * 16 + row;
+            const float wt = dec_ex2(mm[st] - Mr);
+            L += ll[st] * wt;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[e] += oo[st * kSpD + c0 + e] * wt;
+        }
+        for (int i = 0; i < n_slots; ++i)
+            for (int x = x_lo; x <= x_hi; ++x) {
+                const float2 v = part_ml(pa.part, s_lo + i, x)[pr];
+                if (v.y == 0.f)   // no key of this part counts
+                    continue;
+                const float wt = dec_ex2(v.x - Mr);
+                L += v.y * wt;
+                const float4 *po = part_o(pa.part, s_lo + i, x) + pr;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 f = po[(c0 / 4 + e) * 128];
+                    acc[4 * e] += f.x * wt;
+                    acc[4 * e + 1] += f.y * wt;
+                    acc[4 * e + 2] += f.z * wt;
+                    acc[4 * e + 3] += f.w * wt;
+                }
+            }
+        if (!(L > 0.f && L < INFINITY) && (threadIdx.x & 7) == 0)
+            atomicCAS(a.err, kDevOk, kDevBadInput);
+        const float inv = 1.f / L;
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            pk[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        const int t = (r0 + row) / G, gg = r0 + row - t * G;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                             (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + gg) * kSpD + c0;
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+static cudaError_t shared_attrs()
+{
+    static std::atomic<bool> done[64] = {};   // per device (host threads may race: same values)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire)))
+        return e;
+    // the register split must fit what the CTA is launched with, or the
+    // softmax warpgroups' increase would wait forever
+    cudaFuncAttributes fa{};
+    if ((e = cudaFuncGetAttributes(&fa, k_shared_prefix)) != cudaSuccess)
+        return e;
+    if (fa.numRegs != kSpRegsLaunch)
+        return cudaErrorInvalidConfiguration;
+    if ((e = cudaFuncSetAttribute(k_shared_prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(k_shared_own<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwSmem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(k_shared_own<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwSmem)) != cudaSuccess)
+        return e;
+    if (dev < 64)
+        done[dev].store(true, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <typename... P, typename... A>
+static cudaError_t launch_pdl(void (*k)(P...), int64_t grid, int block, int smem, bool pdl, cudaStream_t s, A &&...args)
+{
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, std::forward<A>(args)...);
+}
+
+cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, int n_sms, cudaStream_t s)
+{
+    const int64_t n_items = (int64_t)a.n_reqs * ((a.max_q_len + kPrTokens - 1) / kPrTokens) * a.n_layers * a.n_kv_heads;
+    return launch_pdl(k_shared_prologue, std::min<int64_t>(n_items, (int64_t)n_sms * 8), kPrThreads, 0, false, s, a, rt,
+                      static_cast<__nv_bfloat16 *>(q_rot));
+}
+
+cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s)
+{
+    cudaError_t e = shared_attrs();
+    if (e != cudaSuccess)
+        return e;
+    const SharedArgs &a = *t.base;
+    const SharedPrefixArgs &pa = *t.prefix;
+    static const CUtensorMap no_map{};
+    auto map = [](const void *m) -> const CUtensorMap & { return m ? *static_cast<const CUtensorMap *>(m) : no_map; };
+    if (pa.total > 0) {
+        e = launch_pdl(k_shared_prefix, pa.n_ctas, kSpThreads, kSpSmem, pdl, s, map(t.tmap_q), map(t.tmap_pk),
+                       map(t.tmap_pv), pa, *t.groups);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int rows = a.max_q_len * pa.group;
+    const bool split = rows <= 16;
+    const int n_row_tiles = split ? 1 : (rows + kOwRowsMax - 1) / kOwRowsMax;
+    const int64_t grid = (int64_t)a.n_reqs * pa.lh_count * n_row_tiles;
+    if (split)
+        return launch_pdl(k_shared_own<true>, grid, kOwThreads, kOwSmem, pdl, s, map(t.tmap_k), map(t.tmap_v), a, *t.reqs,
+                          pa, *t.groups, n_row_tiles);
+    return launch_pdl(k_shared_own<false>, grid, kOwThreads, kOwSmem, pdl, s, map(t.tmap_k), map(t.tmap_v), a, *t.reqs, pa,
+                      *t.groups, n_row_tiles);
+}
+
+}  // namespace kvr
