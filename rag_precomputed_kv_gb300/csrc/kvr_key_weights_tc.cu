@@ -114,6 +114,68 @@ __device__ __forceinline__ int warp_sums_index(int lane)
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+// Query rows r0 .. r0 + nr - 1 of a unit, rotated in fp32 and split into TERMS
+// bf16 terms (what a term leaves goes to the next), written as K-major
+// 128B-swizzled operands of `rows` rows: two 64-dim panels a term.  Rows past
+// nr are zero.  128 threads; a thread takes 8 RoPE pairs of a row at a time.
+template <int TERMS>
+__device__ __forceinline__ void prepare_queries(const WeightsArgs &a, const DevReq &rq, int l, int h, int G, int r0, int nr,
+                                                int rows, uint32_t dst0, uint32_t term_bytes)
+{
+#pragma unroll 2
+    for (int it = threadIdx.x; it < rows * 8; it += 128) {
+        const int row = it >> 3, j = it & 7;
+        float v[16];   // elements 8j..8j+7 and 64+8j..64+8j+7
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            v[e] = 0.f;
+        if (row < nr) {
+            const int t = (r0 + row) / G, g = (r0 + row) - t * G;
+            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
+                                      (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + g) * kWtD + 8 * j;
+            const uint4 u[2] = {*reinterpret_cast<const uint4 *>(qp), *reinterpret_cast<const uint4 *>(qp + 64)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t w4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[8 * k + 2 * e] = __uint_as_float(w4[e] << 16);
+                    v[8 * k + 2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 cs = rope_cs(a.rope, kWtD / 2, rq.prefix + t, rope_pair(a.interleaved, kWtD, 8, j, e));
+                const float x0 = a.interleaved ? v[2 * e] : v[e], x1 = a.interleaved ? v[2 * e + 1] : v[8 + e];
+                const float y0 = fmaf(x0, cs.x, -x1 * cs.y), y1 = fmaf(x0, cs.y, x1 * cs.x);
+                if (a.interleaved) {
+                    v[2 * e] = y0;
+                    v[2 * e + 1] = y1;
+                } else {
+                    v[e] = y0;
+                    v[8 + e] = y1;
+                }
+            }
+        }
+        const uint32_t dst = dst0 + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4));
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float &x0 = v[8 * k + 2 * e], &x1 = v[8 * k + 2 * e + 1];
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+                    w4[e] = *reinterpret_cast<const uint32_t *>(&b);
+                    x0 -= __low2float(b);    // exact: what the term leaves
+                    x1 -= __high2float(b);
+                }
+                st_shared_v4(dst + (uint32_t)term * term_bytes + (uint32_t)k * (term_bytes / 2), w4[0], w4[1], w4[2], w4[3]);
+            }
+    }
+}
+
 // Bounded wait that sees what other CTAs of the cluster released before arriving.
 __device__ __forceinline__ bool wait_peers(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
@@ -210,65 +272,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 break;
             }
             // ---- the row block's queries: rotated, split in three bf16 terms ----
-#pragma unroll 1
-            for (int it = threadIdx.x; it < NQ * 8; it += 128) {
-                const int row = it >> 3, j = it & 7;
-                float v[16];   // elements 8j..8j+7 and 64+8j..64+8j+7
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    v[e] = 0.f;
-                if (row < nr) {
-                    const int t = (r0 + row) / G, g = (r0 + row) - t * G;
-                    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
-                                              (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + g) * kWtD + 8 * j;
-                    const uint4 u[2] = {*reinterpret_cast<const uint4 *>(qp), *reinterpret_cast<const uint4 *>(qp + 64)};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t w4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            v[8 * k + 2 * e] = __uint_as_float(w4[e] << 16);
-                            v[8 * k + 2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 cs = rope_cs(a.rope, kWtD / 2, rq.prefix + t, rope_pair(a.interleaved, kWtD, 8, j, e));
-                        float x0, x1;
-                        if (a.interleaved) {
-                            x0 = v[2 * e];
-                            x1 = v[2 * e + 1];
-                        } else {
-                            x0 = v[e];
-                            x1 = v[8 + e];
-                        }
-                        const float y0 = fmaf(x0, cs.x, -x1 * cs.y), y1 = fmaf(x0, cs.y, x1 * cs.x);
-                        if (a.interleaved) {
-                            v[2 * e] = y0;
-                            v[2 * e + 1] = y1;
-                        } else {
-                            v[e] = y0;
-                            v[8 + e] = y1;
-                        }
-                    }
-                }
-                const uint32_t dst = sbase + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4));
-#pragma unroll
-                for (int term = 0; term < 3; ++term)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t w4[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float &x0 = v[8 * k + 2 * e], &x1 = v[8 * k + 2 * e + 1];
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-                            w4[e] = *reinterpret_cast<const uint32_t *>(&b);
-                            x0 -= __low2float(b);    // exact: what the term leaves
-                            x1 -= __high2float(b);
-                        }
-                        st_shared_v4(dst + (uint32_t)(term * C::kQTerm + k * (C::kQTerm / 2)), w4[0], w4[1], w4[2], w4[3]);
-                    }
-            }
+            prepare_queries<3>(a, rq, l, h, G, r0, nr, NQ, sbase, (uint32_t)C::kQTerm);
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
 
@@ -515,6 +519,320 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     }
 }
 
+// ---------------------------------------------------------------------------
+// windows: more than 32 query rows
+// ---------------------------------------------------------------------------
+// At many rows the scores of a unit do not fit TMEM and exp2, not the read of
+// K, bounds the kernel.  So K is streamed twice (the second time mostly from
+// L2) and each pass takes the orientation in which its sum stays inside a
+// thread: S = Q K^T for the rows' denominators (a thread owns a query row),
+// S^T = K Q^T for the weights (a thread owns a key); the two operands' shared
+// memory is the same.  Two bf16 query terms: the weight of a key sums over all
+// the rows, which averages the 2^-17 that they leave.  Blocks of 128 rows; a
+// unit's tiles are split over a cluster only when there are too few units to
+// fill the SMs.
+namespace {
+constexpr int kWwSlots = 3;
+constexpr int kWwQTerm = 128 * kWtD * 2;
+constexpr int kWwOffRing = 2 * kWwQTerm;
+constexpr int kWwOffBar = kWwOffRing + kWwSlots * kWtPanel;
+constexpr int kWwNumBars = 2 * kWwSlots + 4 + 4;   // full, empty, s_full[2], s_free[2], q_full, q_empty, peers, drain
+constexpr int kWwOffMisc = kWwOffBar + 8 * kWwNumBars;
+constexpr int kWwOffFin = (kWwOffMisc + 8 + 15) & ~15;         // [128] lse
+constexpr int kWwSmem = kWwOffFin + 128 * 4;
+constexpr int kWwOffPeer = kWwSmem;                            // [2][kWtMaxCluster][128] (max, sum), clusters only
+constexpr int kWwSmemCluster = kWwOffPeer + 2 * kWtMaxCluster * 128 * 8;
+static_assert(kWwSmem <= 113 * 1024, "two CTAs per SM");
+}  // namespace
+
+__global__ void __launch_bounds__(kWtThreads, 2)
+    k_key_weights_window(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ WeightsArgs a,
+                         const __grid_constant__ ReqTable rt, const int n_cluster)
+{
+    constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kWtTile >> 4) << 24);
+    extern __shared__ __align__(1024) uint8_t wt_smem[];
+    const uint32_t sbase = smem_u32(wt_smem);
+    auto bar = [&](int i) { return sbase + kWwOffBar + 8u * (uint32_t)i; };
+    constexpr int bFull = 0, bEmpty = kWwSlots, bSFull = 2 * kWwSlots, bSFree = bSFull + 2, bQFull = bSFree + 2,
+                  bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bQFull + 3;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(wt_smem + kWwOffMisc + 4);
+    float *s_fin = reinterpret_cast<float *>(wt_smem + kWwOffFin);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = a.n_layers * a.n_kv_heads;
+    const int rank = (int)(blockIdx.x % (unsigned)n_cluster), unit_i = (int)(blockIdx.x / (unsigned)n_cluster);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWwNumBars; ++i)
+            mbar_init(bar(i), (i >= bSFree && i < bSFree + 2) || i == bQFull ? 128u : i == bPeers ? (uint32_t)(n_cluster * 128) : 1u);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 5)
+        tmem_alloc(sbase + kWwOffMisc, kWtTmemCols);
+    if (warp == 4 && lane == 0)
+        prefetch_tmap(&tmk);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync();   // the peers' barriers are initialised before any remote arrive
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(wt_smem + kWwOffMisc);
+
+    const DevReq *reqs = a.reqs ? a.reqs : rt.reqs;
+    const DevReq rq = reqs[unit_i / units];
+    const int lh = unit_i % units;
+    const int G = a.n_q_heads / a.n_kv_heads;
+    const int m_rows = rq.q_len * G, n = rq.prefix + rq.q_len;
+    const int n_rb = (m_rows + 127) / 128;
+    const int nt = (n + kWtTile - 1) / kWtTile;
+    const int t_lo = (int)((int64_t)rank * nt / n_cluster), t_hi = (int)((int64_t)(rank + 1) * nt / n_cluster);
+    const int T = t_hi - t_lo;
+    const int64_t blk = rq.cache_row0 + (int64_t)lh * rq.cap;
+    // job i of a row block: tiles 0 .. T-1, then T-1 .. 0; scores in TMEM half i & 1
+    auto job_tile = [&](int i) { return i < T ? i : 2 * T - 1 - i; };
+
+    if (warp < 4) {
+        const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const float sc = a.scale_log2;
+        float *wp = a.weights + blk;
+        int job = 0;   // over all row blocks (2 T is even: the halves alternate on)
+        bool ok = true;
+        if (m_rows == 0 && !a.accumulate)
+            for (int j = t_lo * kWtTile + (int)threadIdx.x; j < min(n, t_hi * kWtTile); j += 128)
+                wp[j] = 0.f;
+        for (int rb = 0; rb < n_rb && ok; ++rb) {
+            const int r0 = rb * 128, nr = min(128, m_rows - r0);
+            if (rb > 0 && !mbar_wait(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            prepare_queries<2>(a, rq, l, h, G, r0, nr, 128, sbase, (uint32_t)kWwQTerm);
+            fence_proxy_async_smem();
+            mbar_arrive(bar(bQFull));
+
+            // ---- pass 1: this thread's query row over the CTA's keys ----
+            const int r = threadIdx.x;
+            const int see = rq.prefix + (r0 + min(r, nr - 1)) / G + 1;   // keys the row sees
+            float m = kWtUnset, lsum = 0.f;
+            for (int i = 0; i < T; ++i, ++job) {
+                const int half = job & 1;
+                if (!mbar_wait(bar(bSFull + half), (uint32_t)(job >> 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (warp * 32 < nr) {
+                    const int lim = see - (t_lo + i) * kWtTile;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float s[32];
+                        tmem_ld32(lane_base + (uint32_t)(half * 128 + q * 32), s);
+                        tmem_wait_ld();
+                        if (lim < kWtTile) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                s[c] = q * 32 + c < lim ? s[c] : -INFINITY;
+                        }
+                        float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                        for (int c = 4; c < 32; ++c)
+                            m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+                        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+                        if (mx > m + 8.f) {   // (the reference need not be the maximum)
+                            lsum = lsum == 0.f ? 0.f : lsum * ex2(m - mx);
+                            m = mx;
+                        }
+                        float a4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            a4[c & 3] += ex2(fmaf(s[c], sc, -m));
+                        lsum += (a4[0] + a4[1]) + (a4[2] + a4[3]);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(bar(bSFree + half));
+            }
+            if (!ok)
+                break;
+            float M = m, L = lsum;
+            if (n_cluster > 1) {
+                const uint32_t peer = sbase + kWwOffPeer + (uint32_t)((rb & 1) * kWtMaxCluster * 128 * 8);
+                for (int x = 0; x < n_cluster; ++x) {
+                    const uint32_t dst = mapa_rank(peer + (uint32_t)((rank * 128 + r) * 8), (uint32_t)x);
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(m), "f"(lsum) : "memory");
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                     mapa_rank(bar(bPeers), (uint32_t)x))
+                                 : "memory");
+                }
+                if (wait_peers(bar(bPeers), (uint32_t)rb & 1, abort_flag)) {
+                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + kWwOffPeer) + (rb & 1) * kWtMaxCluster * 128 + r;
+                    M = kWtUnset;
+                    L = 0.f;
+                    for (int x = 0; x < n_cluster; ++x)
+                        M = fmaxf(M, pv[x * 128].x);
+                    for (int x = 0; x < n_cluster; ++x) {   // in rank order: one rounding order
+                        const float2 v = pv[x * 128];
+                        L += v.y != 0.f ? v.y * ex2(v.x - M) : 0.f;
+                    }
+                } else {
+                    give_up(a.err, abort_flag);
+                }
+            }
+            softmax_sync();   // (the row block before has read its denominators)
+            s_fin[r] = r < nr ? M + log2f(L) : 0.f;   // (rows that pad the block: any finite value)
+            if (r < nr && rank == 0 && !(L > 0.f && L < INFINITY))
+                atomicCAS(a.err, kDevOk, kDevBadInput);
+            softmax_sync();
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            // ---- pass 2: the weights of this thread's keys ----
+            const bool add = rb > 0 || a.accumulate;
+            const int nb = (nr + 31) >> 5;   // 32-row blocks of queries
+            for (int i = 0; i < T; ++i, ++job) {
+                const int half = job & 1;
+                const int j0 = (t_lo + T - 1 - i) * kWtTile, j = j0 + (int)threadIdx.x;
+                const float w = add && j < n ? wp[j] : 0.f;
+                if (!mbar_wait(bar(bSFull + half), (uint32_t)(job >> 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const bool edge = j0 + kWtTile > rq.prefix + 1;
+                const int lim = !edge ? 0 : j >= n ? 128 : (j - rq.prefix) * G - r0;   // the first row that sees the key
+                float sum = 0.f;
+#pragma unroll 1
+                for (int q = 0; q < nb; ++q) {
+                    float s[32];
+                    tmem_ld32(lane_base + (uint32_t)(half * 128 + q * 32), s);
+                    tmem_wait_ld();
+                    const int hi = nr - q * 32;
+                    if (edge || hi < 32) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            s[c] = q * 32 + c >= lim && c < hi ? s[c] : -INFINITY;
+                    }
+                    float p4[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float4 *fin = reinterpret_cast<const float4 *>(s_fin + q * 32);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 f = fin[c];
+                        p4[0] += ex2(fmaf(s[4 * c], sc, -f.x));
+                        p4[1] += ex2(fmaf(s[4 * c + 1], sc, -f.y));
+                        p4[2] += ex2(fmaf(s[4 * c + 2], sc, -f.z));
+                        p4[3] += ex2(fmaf(s[4 * c + 3], sc, -f.w));
+                    }
+                    sum += (p4[0] + p4[1]) + (p4[2] + p4[3]);
+                }
+                tc_fence_before();
+                mbar_arrive(bar(bSFree + half));
+                if (j < n)
+                    wp[j] = w + sum;
+            }
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+    } else if (warp == 4) {
+        if (lane == 0) {
+            bool ok = true;
+            int k = 0;   // panels issued
+            for (int rb = 0; rb < n_rb && ok; ++rb)
+                for (int i = 0; i < 2 * T && ok; ++i) {
+                    const int row = (int)(blk + (int64_t)(t_lo + job_tile(i)) * kWtTile);
+                    for (int p = 0; p < 2; ++p, ++k) {
+                        const int s = k % kWwSlots;
+                        if (k >= kWwSlots && !mbar_wait(bar(bEmpty + s), (uint32_t)(k / kWwSlots - 1) & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_expect_tx(bar(bFull + s), kWtPanel);
+                        tma_load_2d(sbase + (uint32_t)(kWwOffRing + s * kWtPanel), &tmk, 64 * p, row, bar(bFull + s));
+                    }
+                }
+            if (!ok)
+                give_up(a.err, abort_flag);
+            for (int x = k > kWwSlots ? k - kWwSlots : 0; x < k; ++x)
+                mbar_drain(bar(bFull + x % kWwSlots), (uint32_t)(x / kWwSlots) & 1);
+        }
+    } else {
+        const uint32_t lead = elect_one();
+        const uint64_t d0 = sdesc(sbase, 16, 1024);
+        const uint32_t lo = (uint32_t)d0, hi = (uint32_t)(d0 >> 32);
+        bool ok = true;
+        int k = 0, job = 0;
+        for (int rb = 0; rb < n_rb && ok; ++rb) {
+            if (!mbar_wait(bar(bQFull), (uint32_t)rb & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            const int nr = min(128, m_rows - rb * 128);
+            const uint32_t idesc_t = kIdescBase | ((uint32_t)(((nr + 31) & ~31) >> 3) << 17);   // S^T: N = rows
+            const uint32_t idesc_s = kIdescBase | ((uint32_t)(kWtTile >> 3) << 17);             // S: N = keys
+            for (int i = 0; i < 2 * T && ok; ++i, ++job) {
+                const int half = job & 1;
+                if (job >= 2 && !mbar_wait(bar(bSFree + half), (uint32_t)((job >> 1) - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const bool second = i >= T;
+                for (int p = 0; p < 2; ++p, ++k) {
+                    const int s = k % kWwSlots;
+                    if (!mbar_wait(bar(bFull + s), (uint32_t)(k / kWwSlots) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t ka = lo + ((uint32_t)(kWwOffRing + s * kWtPanel) >> 4);
+#pragma unroll
+                    for (int term = 0; term < 2; ++term) {
+                        const uint32_t qb = lo + ((uint32_t)(term * kWwQTerm + p * (kWwQTerm / 2)) >> 4);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mma_ss(lead, tmem + (uint32_t)(half * 128), desc_with_lo((second ? ka : qb) + 2 * x, hi),
+                                   desc_with_lo((second ? qb : ka) + 2 * x, hi), second ? idesc_t : idesc_s,
+                                   p > 0 || term > 0 || x > 0);
+                    }
+                    umma_commit(lead, bar(bEmpty + s));
+                }
+                if (ok)
+                    umma_commit(lead, bar(bSFull + half));
+            }
+            umma_commit(lead, bar(bQEmpty));
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+        umma_commit(lead, bar(bDrain));
+        mbar_drain(bar(bDrain), 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no CTA leaves while a peer may still write to its shared memory
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kWtTmemCols);
+    }
+}
+
+static cudaError_t launch_cluster(void (*k)(const CUtensorMap, const WeightsArgs, const ReqTable, const int), int64_t grid,
+                                  int smem, int c, cudaStream_t s, const CUtensorMap &tmk, const WeightsArgs &a,
+                                  const ReqTable &rt)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kWtThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)c;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, tmk, a, rt, c);
+}
+
 template <int NQ>
 static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
 {
@@ -525,8 +843,9 @@ static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUt
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(k_key_weights_tc<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(k_key_weights_tc<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) !=
+                cudaSuccess ||
+            (e = cudaFuncSetAttribute(k_key_weights_tc<NQ>, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
             return e;
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
@@ -540,19 +859,32 @@ static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUt
         c *= 2;
     if (units * c > 0x7fffffff)
         return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * c));
-    cfg.blockDim = dim3(kWtThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)c;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_key_weights_tc<NQ>, tmk, a, rt, c);
+    return launch_cluster(k_key_weights_tc<NQ>, units * c, C::kSmem, c, s, tmk, a, rt);
+}
+
+static cudaError_t launch_window(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
+{
+    static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(k_key_weights_window, cudaFuncAttributeMaxDynamicSharedMemorySize, kWwSmemCluster)) !=
+                cudaSuccess ||
+            (e = cudaFuncSetAttribute(k_key_weights_window, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
+            return e;
+        if (dev < 64)
+            attr_set[dev].store(true, std::memory_order_release);
+    }
+    const int64_t units = (int64_t)a.n_reqs * a.n_layers * a.n_kv_heads;
+    const int tiles = (a.max_rows + kWtTile - 1) / kWtTile;
+    int c = 1;   // split a unit's tiles while the grid leaves SMs idle (one CTA per SM then)
+    while (c < kWtMaxCluster && units * c * 2 <= n_sms && tiles >= 4 * c)
+        c *= 2;
+    if (units * c > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    return launch_cluster(k_key_weights_window, units * c, c > 1 ? kWwSmemCluster : kWwSmem, c, s, tmk, a, rt);
 }
 
 cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const void *tmap_k, int n_sms, cudaStream_t s)
@@ -563,7 +895,7 @@ cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const vo
         return launch_nq<16>(a, rt, m, n_sms, s);
     if (rows <= 32)
         return launch_nq<32>(a, rt, m, n_sms, s);
-    return launch_nq<64>(a, rt, m, n_sms, s);
+    return launch_window(a, rt, m, n_sms, s);
 }
 
 }  // namespace kvr
