@@ -1492,6 +1492,10 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         return st;
     pa.part = static_cast<float *>(p->part);
     pa.q_rot = p->q_rot;
+    int32_t max_own = 1;
+    for (const DevShared &r : pl.rq)
+        if (r.q_len > 0)
+            max_own = std::max(max_own, r.own + r.q_len);
     CUtensorMap mq, mpk, mpv, mk, mv;
     if ((st = encode_rows_map(*p, p->q_rot, q_rows, 128, &mq)) != KVR_OK ||
         (any_prefix && ((st = encode_rows_map(*p, sa.prefix_k, pre_rows, 128, &mpk)) != KVR_OK ||
@@ -1516,11 +1520,12 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         sa.reqs = static_cast<const DevShared *>(slot->dev);
         pa.groups = reinterpret_cast<const DevGroup *>(static_cast<const char *>(slot->dev) + off);
     }
-    SharedTcArgs t{&sa, &pl.tab, &pa, &pl.gtab, &mq, any_prefix ? &mpk : nullptr, any_prefix ? &mpv : nullptr, &mk, &mv};
+    SharedTcArgs t{&sa, &pl.tab, &pa, &pl.gtab, &mq, any_prefix ? &mpk : nullptr, any_prefix ? &mpv : nullptr,
+                   &mk, &mv, p->n_sms, max_own};
     p->mark(2, s);
     {
         NvtxRange r("kvr.k_shared_prologue");
-        e = launch_shared_prologue(sa, pl.tab, p->q_rot, p->n_sms, s);
+        e = launch_shared_prologue(sa, pl.tab, p->q_rot, s);
     }
     p->mark(3, s);
     p->mark(4, s);
@@ -1530,6 +1535,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         pa.lh_count = std::min(lh_slice, LH - lh);
         pa.total = pa.lh_count * pa.unit_pairs;
         pa.n_ctas = (int32_t)std::min<int64_t>(p->n_sms, pa.total);
+        pa.ratio = pa.total > 0 ? (float)((double)pa.n_ctas / (double)pa.total) : 0.f;
         e = launch_shared_tc(t, !p->timed, s);
     }
     p->mark(5, s);

@@ -310,6 +310,7 @@ struct SharedPrefixArgs {
     int32_t n_ctas;             // stretches that the pairs are cut in
     int64_t unit_pairs, unit_blocks;   // pairs, blocks of one unit
     int64_t total;              // pairs of the slice: lh_count * unit_pairs
+    float ratio;                // n_ctas / total
     float *part;                // (blocks + n_ctas) partial results
     const void *q_rot;          // [L][Hkv][T][G][D], rotated
     float scale_log2;
@@ -321,8 +322,10 @@ struct SharedTcArgs {
     const SharedPrefixArgs *prefix;
     const GroupTable *groups;
     // host CUtensorMaps: packed queries and prefix (64 x 128 boxes; the prefix's
-    // NULL when nothing is shared), own caches (64 x 32 boxes)
+    // NULL when nothing is shared), own caches (64 x 32)
     const void *tmap_q, *tmap_pk, *tmap_pv, *tmap_k, *tmap_v;
+    int32_t n_sms;
+    int32_t max_own_keys;       // the longest own part (own rows and query tokens) of a request with tokens
 };
 
 // ---- attention weight per cached key ----
@@ -451,7 +454,7 @@ cudaError_t launch_decode_attention(const AttnArgs &a, const ReqTable &rt, const
 cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, cudaStream_t s);
 // bf16, head_dim 128: rotation and append, then the prefix part and the own part
 // of a slice of the units.
-cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, int n_sms, cudaStream_t s);
+cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, cudaStream_t s);
 cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s);
 cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, cudaStream_t s);
 // bf16, head_dim 128: the tensor-core kernel; `tmap_k` points to the CUtensorMap

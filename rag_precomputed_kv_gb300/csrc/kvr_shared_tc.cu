@@ -91,14 +91,16 @@ __device__ __forceinline__ float2 *part_ml(float *part, int64_t slot, int x)
 
 // Stretch c of the call's `total` (block, key tile) pairs starts here.
 __device__ __forceinline__ int64_t stretch_start(int64_t total, int n, int c) { return total * c / n; }
-// The stretch that holds pair w.
-__device__ __forceinline__ int stretch_of(int64_t total, int n, int64_t w)
+// The stretch that holds pair w: the last c with total * c / n <= w, that is
+// total * c < n (w + 1); `ratio` = n / total gives it within one.
+__device__ __forceinline__ int stretch_of(int64_t total, int n, float ratio, int64_t w)
 {
-    int c = (int)(w * n / total);
-    while (stretch_start(total, n, c + 1) <= w)
-        ++c;
-    while (stretch_start(total, n, c) > w)
+    int c = min((int)((float)w * ratio), n - 1);
+    const int64_t lim = (int64_t)n * (w + 1);
+    while (total * c >= lim)
         --c;
+    while (total * (c + 1) < lim)
+        ++c;
     return c;
 }
 
@@ -177,6 +179,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSpRegsSoftmax));
         pdl_wait_prerequisites();   // (the partial results' scratch may still be read by the call before)
+        // the own part may be set up now, and load what the prologue, now done, wrote
+        pdl_launch_dependents();
         const int x = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = a.scale_log2;
@@ -481,8 +485,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
 // the query side
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int kPrTokens = 16;                // query tokens per piece
-constexpr int kPrThreads = 8 * kPrTokens;    // 8 threads a token: elements [8j, 8j + 8) and [64 + 8j, ..)
+constexpr int kPrPairs = 16;                // (layer, token, kv-head) triples per CTA
+constexpr int kPrThreads = 8 * kPrPairs;    // 8 threads each: elements [8j, 8j + 8) and [64 + 8j, ..)
 
 __device__ __forceinline__ void rotate_row(uint4 &lo, uint4 &hi, const float *c, const float *s, bool il)
 {
@@ -493,55 +497,52 @@ __device__ __forceinline__ void rotate_row(uint4 &lo, uint4 &hi, const float *c,
 }
 }  // namespace
 
-// Pieces of (request, 16 tokens, layer, kv-head), a grid-stride loop.
+// One CTA: kPrPairs consecutive (layer, token, kv-head) triples of a request, in
+// the order of the query tensor.
 __global__ void __launch_bounds__(kPrThreads)
-    k_shared_prologue(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt, __nv_bfloat16 *q_rot)
+    k_shared_prologue(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
+                      __nv_bfloat16 *__restrict__ q_rot, const int n_chunks)
 {
     constexpr int D = kSpD, H2 = D / 2, E = 8;
     const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
-    const int n_chunks = (a.max_q_len + kPrTokens - 1) / kPrTokens;
-    const int64_t n_rc = (int64_t)a.n_reqs * n_chunks, n_items = n_rc * a.n_layers * a.n_kv_heads;
-    const int G = a.n_q_heads / a.n_kv_heads, j = threadIdx.x & 7;
-    const int64_t T = a.total_q;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q), *kq = static_cast<const __nv_bfloat16 *>(a.kq),
-                        *vq = static_cast<const __nv_bfloat16 *>(a.vq);
-    __nv_bfloat16 *ck = static_cast<__nv_bfloat16 *>(a.cache_k), *cv = static_cast<__nv_bfloat16 *>(a.cache_v);
     pdl_launch_dependents();   // the attention kernel sets up, and loads prefix tiles, meanwhile
-    for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
-        const int64_t rc = it % n_rc;
-        const int lh = (int)(it / n_rc);
-        const DevShared rq = reqs[rc / n_chunks];
-        const int t = (int)(rc % n_chunks) * kPrTokens + (int)(threadIdx.x >> 3);
-        if (t >= rq.q_len)
-            continue;
-        const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
-        const int64_t tok = l * T + rq.q_off + t;
-        float c[E], s[E];
+    const DevShared rq = reqs[blockIdx.x / (unsigned)n_chunks];
+    const int i = (int)(blockIdx.x % (unsigned)n_chunks) * kPrPairs + (int)(threadIdx.x >> 3), j = threadIdx.x & 7;
+    const int H = a.n_kv_heads, G = a.n_q_heads / H;
+    if (i >= rq.q_len * a.n_layers * H)
+        return;
+    const int h = i % H, lt = i / H, l = lt / rq.q_len, t = lt - l * rq.q_len, lh = l * H + h;
+    const int64_t T = a.total_q, tok = l * T + rq.q_off + t;
+    const __nv_bfloat16 *__restrict__ q = static_cast<const __nv_bfloat16 *>(a.q);
+    const __nv_bfloat16 *__restrict__ kq = static_cast<const __nv_bfloat16 *>(a.kq);
+    const __nv_bfloat16 *__restrict__ vq = static_cast<const __nv_bfloat16 *>(a.vq);
+    __nv_bfloat16 *ck = static_cast<__nv_bfloat16 *>(a.cache_k), *cv = static_cast<__nv_bfloat16 *>(a.cache_v);
+    const int64_t src = (tok * H + h) * D + j * E;
+    uint4 klo = *reinterpret_cast<const uint4 *>(kq + src), khi = *reinterpret_cast<const uint4 *>(kq + src + H2);
+    const uint4 vlo = *reinterpret_cast<const uint4 *>(vq + src), vhi = *reinterpret_cast<const uint4 *>(vq + src + H2);
+    float c[E], s[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float2 cs = rope_cs(a.rope, H2, rq.pre_len + rq.own + t, rope_pair(a.interleaved, D, E, j, e));
-            c[e] = cs.x;
-            s[e] = cs.y;
-        }
-        const int64_t src = (tok * a.n_kv_heads + h) * D + j * E;
-        uint4 klo = *reinterpret_cast<const uint4 *>(kq + src), khi = *reinterpret_cast<const uint4 *>(kq + src + H2);
-        const uint4 vlo = *reinterpret_cast<const uint4 *>(vq + src), vhi = *reinterpret_cast<const uint4 *>(vq + src + H2);
-        rotate_row(klo, khi, c, s, a.interleaved);
-        const int64_t dst = (rq.cache_row0 + (int64_t)lh * rq.cap + rq.own + t) * D + j * E;
-        *reinterpret_cast<uint4 *>(ck + dst) = klo;
-        *reinterpret_cast<uint4 *>(ck + dst + H2) = khi;
-        *reinterpret_cast<uint4 *>(cv + dst) = vlo;
-        *reinterpret_cast<uint4 *>(cv + dst + H2) = vhi;
-        const int64_t q_src = (tok * a.n_q_heads + (int64_t)h * G) * D + j * E;
-        const int64_t q_dst = ((int64_t)lh * T + rq.q_off + t) * G * D + j * E;
-        for (int g = 0; g < G; ++g) {
-            uint4 lo = *reinterpret_cast<const uint4 *>(q + q_src + (int64_t)g * D);
-            uint4 hi = *reinterpret_cast<const uint4 *>(q + q_src + (int64_t)g * D + H2);
-            rotate_row(lo, hi, c, s, a.interleaved);
-            *reinterpret_cast<uint4 *>(q_rot + q_dst + (int64_t)g * D) = lo;
-            *reinterpret_cast<uint4 *>(q_rot + q_dst + (int64_t)g * D + H2) = hi;
-        }
+    for (int e = 0; e < E; ++e) {
+        const float2 cs = rope_cs(a.rope, H2, rq.pre_len + rq.own + t, rope_pair(a.interleaved, D, E, j, e));
+        c[e] = cs.x;
+        s[e] = cs.y;
     }
+    const int64_t q_src = (tok * a.n_q_heads + (int64_t)h * G) * D + j * E;
+    const int64_t q_dst = ((int64_t)lh * T + rq.q_off + t) * G * D + j * E;
+#pragma unroll 4
+    for (int g = 0; g < G; ++g) {
+        uint4 lo = *reinterpret_cast<const uint4 *>(q + q_src + (int64_t)g * D);
+        uint4 hi = *reinterpret_cast<const uint4 *>(q + q_src + (int64_t)g * D + H2);
+        rotate_row(lo, hi, c, s, a.interleaved);
+        *reinterpret_cast<uint4 *>(q_rot + q_dst + (int64_t)g * D) = lo;
+        *reinterpret_cast<uint4 *>(q_rot + q_dst + (int64_t)g * D + H2) = hi;
+    }
+    rotate_row(klo, khi, c, s, a.interleaved);
+    const int64_t dst = (rq.cache_row0 + (int64_t)lh * rq.cap + rq.own + t) * D + j * E;
+    *reinterpret_cast<uint4 *>(ck + dst) = klo;
+    *reinterpret_cast<uint4 *>(ck + dst + H2) = khi;
+    *reinterpret_cast<uint4 *>(cv + dst) = vlo;
+    *reinterpret_cast<uint4 *>(cv + dst + H2) = vhi;
 }
 
 // ---------------------------------------------------------------------------
@@ -549,70 +550,122 @@ __global__ void __launch_bounds__(kPrThreads)
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kOwThreads = 128;
-constexpr int kOwTile = 128;                        // keys per tile, loaded 32 rows at a time
-constexpr int kOwOffBar = 2 * dec::kDecTileBytes;   // K tile, V tile
-constexpr int kOwSmem = kOwOffBar + 16 + 1024;      // + alignment slack
 constexpr int kOwRowsMax = 64;
-// the states (m, l, O [rows][128]) over the tiles at the end
-static_assert(4 * 16 * 2 * 4 + 4 * 16 * kSpD * 4 <= 2 * dec::kDecTileBytes, "state area");
+constexpr int kOwTileMax = 128;   // keys per tile
+// Shared memory of k_shared_own_rows: K and V tile ([tile_keys][128], two
+// 128B-swizzled panels each; the rows' final states reuse it), the rows'
+// PartRefs, the barrier.
+__host__ __device__ constexpr int ow_off_ref(int tile_keys)
+{
+    return tile_keys * 512 > kOwRowsMax * (kSpD + 2) * 4 ? tile_keys * 512 : kOwRowsMax * (kSpD + 2) * 4;
+}
+__host__ __device__ constexpr int ow_bytes(int tile_keys) { return ow_off_ref(tile_keys) + kOwRowsMax * 16 + 16 + 1024; }
+
+// Where the partial results of one row lie: slots [slot, slot + n), tiles x0..x1,
+// row pr of each.
+struct PartRef {
+    int64_t slot;
+    int n, where;    // where: pr | x0 << 8 | x1 << 9
+    __device__ __forceinline__ int pr() const { return where & 127; }
+    __device__ __forceinline__ int x0() const { return (where >> 8) & 1; }
+    __device__ __forceinline__ int x1() const { return (where >> 9) & 1; }
+};
+static_assert(sizeof(PartRef) == 16, "row reference");
+
+__device__ __forceinline__ PartRef part_ref(const SharedPrefixArgs &pa, const DevGroup &g, int lh_s, int group_row)
+{
+    PartRef r{0, 0, 0};
+    if (g.nt == 0)
+        return r;
+    const int blk = group_row >> 8, in = group_row & 255;
+    const bool dual = min(256, g.rows - 256 * blk) <= 128;
+    const int64_t it = (int64_t)lh_s * pa.unit_blocks + g.item0 + blk;
+    const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.nt;
+    const int ca = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0);
+    const int cb = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0 + g.nt - 1);
+    r.slot = it + ca;
+    r.n = cb - ca + 1;
+    const int x0 = dual ? 0 : in >> 7, x1 = dual ? 1 : x0;
+    r.where = (in & 127) | x0 << 8 | x1 << 9;
+    return r;
+}
+
+// Bounded wait that reads the timer only when the phase is not complete yet (a
+// %globaltimer read costs some 600 cycles).
+__device__ __forceinline__ bool own_wait(uint32_t bar, uint32_t parity)
+{
+    return mbar_try_wait(bar, parity) || mbar_drain(bar, parity);
+}
+
+// Adds a partial sum (relative to maximum m, denominator l) to a running one.
+__device__ __forceinline__ void add_state(float &M, float &L, float *acc, float m, float l, const float *o)
+{
+    if (l == 0.f)   // no key counts
+        return;
+    const float n = fmaxf(M, m), a = L == 0.f ? 0.f : dec::dec_ex2(M - n), b = dec::dec_ex2(m - n);
+    L = L * a + l * b;
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        acc[e] = acc[e] * a + o[e] * b;
+    M = n;
+}
 }  // namespace
 
-// kSplit: the CTA's rows are one MMA row tile (<= 16) and each warp takes 32
-// keys of a tile; otherwise each warp has a row tile of its own and takes all
-// 128 keys.
-template <bool kSplit>
-__global__ void __launch_bounds__(kOwThreads)
-    k_shared_own(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+// More than 16 query rows a request: a CTA per (request, unit, 64 rows); each
+// warp has an MMA row tile of its own and takes all keys of a tile.
+__global__ void __launch_bounds__(kOwThreads, 3)
+    k_shared_own_rows(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                  const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
-                 const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt, const int n_row_tiles)
+                 const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt, const int n_row_tiles,
+                 const int tile_keys)
 {
     using namespace dec;
-    constexpr int kRows = kSplit ? 16 : kOwRowsMax;
     extern __shared__ uint8_t ow_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ow_smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sbase = dec_smem_u32(smem), kt = sbase, vt = sbase + kDecTileBytes, full = sbase + kOwOffBar;
+    const int panel = tile_keys * 128, kOwTile = tile_keys, off_ref = ow_off_ref(tile_keys), off_bar = off_ref + kOwRowsMax * 16;
+    const uint32_t sbase = dec_smem_u32(smem), kt = sbase, vt = sbase + 2 * panel, full = sbase + off_bar;
+    volatile int *cta_err = reinterpret_cast<volatile int *>(smem + off_bar + 8);
+    auto sw = [&](int r, int c) { return (uint32_t)((c >> 3) * panel + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
     const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
     const DevGroup *groups = pa.groups ? pa.groups : gt.groups;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = pa.group;
-    int64_t bi = blockIdx.x;
-    const int tile = (int)(bi % n_row_tiles);
-    bi /= n_row_tiles;
-    const int lh_s = (int)(bi % pa.lh_count), lh = pa.lh_base + lh_s;
-    const DevShared rq = reqs[bi / pa.lh_count];
-    const int m_rows = rq.q_len * G, r0 = tile * kRows;
-    volatile int *cta_err = reinterpret_cast<volatile int *>(smem + kOwOffBar + 8);
-    if (threadIdx.x == 0) {
-        dec_mbar_init(full, 1);
-        *cta_err = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncthreads();
-    pdl_wait_prerequisites();
+    unsigned bi = blockIdx.x;
+    const int tile = (int)(bi % (unsigned)n_row_tiles);
+    bi /= (unsigned)n_row_tiles;
+    const int lh_s = (int)(bi % (unsigned)pa.lh_count), lh = pa.lh_base + lh_s;
+    const DevShared rq = reqs[bi / (unsigned)pa.lh_count];
+    const int m_rows = rq.q_len * G, r0 = tile * kOwRowsMax;
     if (r0 >= m_rows)
         return;   // uniform over the CTA
-    const int rows = min(kRows, m_rows - r0);
+    const int rows = min(kOwRowsMax, m_rows - r0);
     const int n_keys = rq.own + (r0 + rows - 1) / G + 1;   // of the last row
     const int n_t = (n_keys + kOwTile - 1) / kOwTile;
     const int64_t kv_row0 = rq.cache_row0 + (int64_t)lh * rq.cap;
 
     auto issue = [&](int j) {   // thread 0
-        const int n32 = min(4, (n_keys - j * kOwTile + 31) >> 5);
+        const int n32 = min(kOwTile >> 5, (n_keys - j * kOwTile + 31) >> 5);
         dec_expect_tx(full, (uint32_t)(n32 * 32 * kSpD * 2 * 2));
         for (int i = 0; i < n32; ++i) {
             const int row = (int)(kv_row0 + (int64_t)j * kOwTile + 32 * i);
             const uint32_t d = (uint32_t)(i * 32 * 128);
             dec_tma_load(kt + d, &tmk, 0, row, full);
-            dec_tma_load(kt + kDecPanel + d, &tmk, 64, row, full);
+            dec_tma_load(kt + panel + d, &tmk, 64, row, full);
             dec_tma_load(vt + d, &tmv, 0, row, full);
-            dec_tma_load(vt + kDecPanel + d, &tmv, 64, row, full);
+            dec_tma_load(vt + panel + d, &tmv, 64, row, full);
         }
     };
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
+        dec_mbar_init(full, 1);
+        *cta_err = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        pdl_wait_prerequisites();
         issue(0);
-
-    // query fragments (A operand): rows q_lo, q_lo + 8 of this warp's row tile
-    const int rt0 = kSplit ? 0 : 16 * warp;              // first CTA row of the warp's row tile
+    } else {
+        pdl_wait_prerequisites();
+    }
+    // query fragments (A operand): rows ra, rb of this warp's row tile
+    const int rt0 = 16 * warp;              // first CTA row of the warp's row tile
     const int ra = rt0 + (lane >> 2), rb = ra + 8, cq = (lane & 3) * 2;
     const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(pa.q_rot) +
                               (((int64_t)lh * a.total_q + rq.q_off) * G + r0) * kSpD;
@@ -628,6 +681,14 @@ __global__ void __launch_bounds__(kOwThreads)
         qa[kb][2] = ld2(ra, c0 + 8);
         qa[kb][3] = ld2(rb, c0 + 8);
     }
+    // where the prefix's partial results lie, while the tile is on its way
+    {
+        const DevGroup g = groups[rq.group];
+        const int g_row0 = (rq.q_off - g.q_off) * G + r0;
+        if ((int)threadIdx.x < rows)
+            reinterpret_cast<PartRef *>(smem + off_ref)[threadIdx.x] = part_ref(pa, g, lh_s, g_row0 + (int)threadIdx.x);
+    }
+    __syncthreads();   // the barrier is initialised
     // keys that the two rows see
     const int see[2] = {ra < rows ? rq.own + (r0 + ra) / G + 1 : 0, rb < rows ? rq.own + (r0 + rb) / G + 1 : 0};
 
@@ -638,14 +699,14 @@ __global__ void __launch_bounds__(kOwThreads)
     for (int n = 0; n < 16; ++n)
         o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     for (int j = 0; j < n_t; ++j) {
-        if (!dec_wait(full, (uint32_t)j & 1))
+        if (!own_wait(full, (uint32_t)j & 1))
             *cta_err = 1;
         const int kk0 = j * kOwTile, n_here = min(kOwTile, n_keys - kk0);
         // V rows behind the last key are zero (32-row groups that were loaded)
         const int n_ld = (n_here + 31) & ~31;
         for (int idx = threadIdx.x; idx < (n_ld - n_here) * 16; idx += kOwThreads) {
             const int row = n_here + (idx >> 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vt + sw_off(row, idx & 15)), "r"(0u) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vt + sw(row, idx & 15)), "r"(0u) : "memory");
         }
         __syncthreads();
         if (*cta_err) {   // the same for every thread
@@ -655,7 +716,7 @@ __global__ void __launch_bounds__(kOwThreads)
             }
             return;
         }
-        for (int key0 = kSplit ? 32 * warp : 0; key0 < (kSplit ? min(32 * warp + 1, n_here) : n_here); key0 += 32) {
+        for (int key0 = 0; key0 < n_here; key0 += 32) {
             float c[4][4];
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb)
@@ -667,7 +728,7 @@ __global__ void __launch_bounds__(kOwThreads)
                     const int mi = lane >> 3;
                     const int key = key0 + 8 * (nb + (mi >> 1)) + (lane & 7);
                     uint32_t b0, b1, b2, b3;
-                    ldsm_x4(kt + sw_off(key, 2 * kb + (mi & 1)), b0, b1, b2, b3);
+                    ldsm_x4(kt + sw(key, 2 * kb + (mi & 1)), b0, b1, b2, b3);
                     mma_bf16(c[nb], qa[kb], b0, b1);
                     mma_bf16(c[nb + 1], qa[kb], b2, b3);
                 }
@@ -723,7 +784,7 @@ __global__ void __launch_bounds__(kOwThreads)
                     const int mi = lane >> 3;
                     const int key = key0 + 16 * kb2 + 8 * (mi & 1) + (lane & 7);
                     uint32_t b0, b1, b2, b3;
-                    ldsm_x4_t(vt + sw_off(key, n + (mi >> 1)), b0, b1, b2, b3);
+                    ldsm_x4_t(vt + sw(key, n + (mi >> 1)), b0, b1, b2, b3);
                     mma_bf16(o[n], p[kb2], b0, b1);
                     mma_bf16(o[n + 1], p[kb2], b2, b3);
                 }
@@ -733,81 +794,44 @@ __global__ void __launch_bounds__(kOwThreads)
         if (threadIdx.x == 0 && j + 1 < n_t)
             issue(j + 1);
     }
-    // the warps' states [4 x 16] over the tiles
-    float *mm = reinterpret_cast<float *>(smem), *ll = mm + 64, *oo = ll + 64;
-    const int sa = 16 * warp + (lane >> 2), sb = sa + 8;
+
+    // the own states over the tiles: [row][128], then (max, sum)
+    float *oo = reinterpret_cast<float *>(smem);
+    float2 *ml = reinterpret_cast<float2 *>(oo + kOwRowsMax * kSpD);
     if ((lane & 3) == 0) {
-        mm[sa] = m_run[0];
-        mm[sb] = m_run[1];
-        ll[sa] = l_run[0];
-        ll[sb] = l_run[1];
+        ml[ra] = make_float2(m_run[0], l_run[0]);
+        ml[rb] = make_float2(m_run[1], l_run[1]);
     }
 #pragma unroll
     for (int n = 0; n < 16; ++n) {
         const int col = 8 * n + cq;
-        *reinterpret_cast<float2 *>(oo + sa * kSpD + col) = make_float2(o[n][0], o[n][1]);
-        *reinterpret_cast<float2 *>(oo + sb * kSpD + col) = make_float2(o[n][2], o[n][3]);
+        *reinterpret_cast<float2 *>(oo + ra * kSpD + col) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2 *>(oo + rb * kSpD + col) = make_float2(o[n][2], o[n][3]);
     }
     __syncthreads();
-    // 8 threads a row, 16 columns each: own states (in warp order), then the
-    // prefix's partial results (in stretch order)
-    const DevGroup g = groups[rq.group];
+    // 8 threads a row, 16 columns each: the own state, then the prefix's
     const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
-    for (int row = threadIdx.x >> 3; row < rows; row += kOwThreads / 8) {
-        const int c0 = 16 * (threadIdx.x & 7);
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < (kSplit ? 4 : 1); ++w)
-            M = fmaxf(M, mm[w * 16 + row]);
-        int64_t s_lo = 0;
-        int n_slots = 0, x_lo = 0, x_hi = 0, pr = 0;
-        if (g.nt > 0) {
-            const int gr = (rq.q_off - g.q_off) * G + r0 + row, blk = gr >> 8, in = gr & 255;
-            const bool dual = min(256, g.rows - 256 * blk) <= 128;
-            const int64_t it = (int64_t)lh_s * pa.unit_blocks + g.item0 + blk;
-            const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.nt;
-            const int ca = stretch_of(pa.total, pa.n_ctas, w0), cb = stretch_of(pa.total, pa.n_ctas, w0 + g.nt - 1);
-            s_lo = it + ca;
-            n_slots = cb - ca + 1;
-            x_lo = dual ? 0 : in >> 7;
-            x_hi = dual ? 1 : x_lo;
-            pr = in & 127;
-            for (int i = 0; i < n_slots; ++i)
-                for (int x = x_lo; x <= x_hi; ++x)
-                    M = fmaxf(M, part_ml(pa.part, s_lo + i, x)[pr].x);
-        }
-        const float Mr = M == -INFINITY ? 0.f : M;
-        float L = 0.f, acc[16];
+    const int c0 = 16 * (threadIdx.x & 7);
+    auto own_state = [&](int row, float &M, float &L, float *acc) {
+        M = -INFINITY;
+        L = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             acc[e] = 0.f;
+        const float2 v = ml[row];
+        float f[16];
 #pragma unroll
-        for (int w = 0; w < (kSplit ? 4 : 1); ++w) {
-            const int st = w * 16 + row;
-            const float wt = dec_ex2(mm[st] - Mr);
-            L += ll[st] * wt;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                acc[e] += oo[st * kSpD + c0 + e] * wt;
+        for (int e = 0; e < 16; e += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(oo + row * kSpD + c0 + e);
+            f[e] = u.x;
+            f[e + 1] = u.y;
+            f[e + 2] = u.z;
+            f[e + 3] = u.w;
         }
-        for (int i = 0; i < n_slots; ++i)
-            for (int x = x_lo; x <= x_hi; ++x) {
-                const float2 v = part_ml(pa.part, s_lo + i, x)[pr];
-                if (v.y == 0.f)   // no key of this part counts
-                    continue;
-                const float wt = dec_ex2(v.x - Mr);
-                L += v.y * wt;
-                const float4 *po = part_o(pa.part, s_lo + i, x) + pr;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 f = po[(c0 / 4 + e) * 128];
-                    acc[4 * e] += f.x * wt;
-                    acc[4 * e + 1] += f.y * wt;
-                    acc[4 * e + 2] += f.z * wt;
-                    acc[4 * e + 3] += f.w * wt;
-                }
-            }
-        if (!(L > 0.f && L < INFINITY) && (threadIdx.x & 7) == 0)
+        add_state(M, L, acc, v.x, v.y, f);
+    };
+    auto put = [&](int row, float L, const float *acc) {
+        if (!(L > 0.f && L < INFINITY) && c0 == 0)
             atomicCAS(a.err, kDevOk, kDevBadInput);
         const float inv = 1.f / L;
         uint32_t pk[8];
@@ -819,6 +843,332 @@ __global__ void __launch_bounds__(kOwThreads)
                              (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + gg) * kSpD + c0;
         *reinterpret_cast<uint4 *>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+    };
+    // the first partial result of each of the thread's rows is loaded ahead
+    constexpr int NR = kOwRowsMax / (kOwThreads / 8);
+    PartRef ref[NR];
+    float2 v1[NR];
+    float4 f1[NR][4];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+        const int row = (int)(threadIdx.x >> 3) + k * (kOwThreads / 8);
+        ref[k].n = 0;
+        if (row < rows)
+            ref[k] = reinterpret_cast<const PartRef *>(smem + off_ref)[row];
+        if (ref[k].n > 0) {
+            v1[k] = part_ml(pa.part, ref[k].slot, ref[k].x0())[ref[k].pr()];
+            const float4 *po = part_o(pa.part, ref[k].slot, ref[k].x0()) + ref[k].pr() + c0 * 32;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f1[k][e] = po[e * 128];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+        const int row = (int)(threadIdx.x >> 3) + k * (kOwThreads / 8);
+        if (row >= rows)
+            break;
+        float M, L, acc[16];
+        own_state(row, M, L, acc);
+        auto add = [&](const float2 &v, const float4 *u) {
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[4 * e] = u[e].x;
+                f[4 * e + 1] = u[e].y;
+                f[4 * e + 2] = u[e].z;
+                f[4 * e + 3] = u[e].w;
+            }
+            add_state(M, L, acc, v.x, v.y, f);
+        };
+        if (ref[k].n > 0)
+            add(v1[k], f1[k]);
+        for (int i = 0; i < ref[k].n; ++i)
+            for (int x = ref[k].x0(); x <= ref[k].x1(); ++x) {   // in stretch order
+                if (i == 0 && x == ref[k].x0())
+                    continue;
+                const float2 v = part_ml(pa.part, ref[k].slot + i, x)[ref[k].pr()];
+                const float4 *po = part_o(pa.part, ref[k].slot + i, x) + ref[k].pr() + c0 * 32;
+                float4 u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] = po[e * 128];
+                add(v, u);
+            }
+        put(row, L, acc);
+    }
+}
+
+// At most 16 query rows a request (a decode step): the own rows are a stream of
+// short pieces, one per (request, unit), and a piece's work is a chain of short
+// dependent steps.  So every warp works by itself, on a consecutive stretch of
+// pieces: its lane 0 loads the K and V rows 32 keys at a time, two steps ahead
+// (across pieces), the warp runs S, softmax and P V of a step in registers, adds
+// the prefix's partial results at the end of a piece and writes its rows.  Six
+// warps per SM, 32 KB of tiles each.
+namespace {
+constexpr int kOdWarps = 6;
+constexpr int kOdThreads = 32 * kOdWarps;
+constexpr int kOdTile = 32;
+constexpr int kOdPanel = kOdTile * 128;           // 32 keys x 64 dims
+constexpr int kOdStage = 4 * kOdPanel;            // K, then V: two panels each
+constexpr int kOdOffBar = kOdWarps * 2 * kOdStage;
+constexpr int kOdSmem = kOdOffBar + kOdWarps * 2 * 8 + 1024;   // + alignment slack
+
+// 16-byte chunk c of row r of a tile
+__device__ __forceinline__ uint32_t od_off(int r, int c)
+{
+    return (uint32_t)((c >> 3) * kOdPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+}  // namespace
+
+__global__ void __launch_bounds__(kOdThreads, 1)
+    k_shared_own_decode(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                        const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
+                        const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt)
+{
+    using namespace dec;
+    extern __shared__ uint8_t od_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(od_smem_raw) + 1023) & ~uintptr_t(1023));
+    const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
+    const DevGroup *groups = pa.groups ? pa.groups : gt.groups;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tiles = dec_smem_u32(smem) + (uint32_t)(warp * 2 * kOdStage);
+    const uint32_t full0 = dec_smem_u32(smem) + (uint32_t)(kOdOffBar + warp * 16);
+    const int G = pa.group, n_items = a.n_reqs * pa.lh_count;
+    // the pieces of this warp; neighbours go to different SMs when there are few
+    const int n_w = (int)gridDim.x * kOdWarps, w = warp * (int)gridDim.x + (int)blockIdx.x;
+    const int it0 = (int)((int64_t)n_items * w / n_w), it1 = (int)((int64_t)n_items * (w + 1) / n_w);
+
+    if (lane == 0) {
+        dec_mbar_init(full0, 1);
+        dec_mbar_init(full0 + 8, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tmap(&tmk);
+        prefetch_tmap(&tmv);
+    }
+    __syncwarp();
+    // Behind a prefix part, which let this kernel start only after the prologue
+    // was done, only the partial results have to be waited for.
+    bool waited = pa.total == 0;
+    if (waited)
+        pdl_wait_prerequisites();
+
+    // the next step to load: tile `lj` of piece `li`
+    int li = it0, lj = 0, l_keys = 0, n_issued = 0;
+    int64_t l_row0 = 0;
+    auto load_piece = [&]() {   // the first piece from li on with keys to load
+        for (; li < it1; ++li) {
+            const DevShared &r = reqs[li / pa.lh_count];
+            if (r.q_len > 0) {
+                l_keys = r.own + r.q_len;
+                l_row0 = r.cache_row0 + (int64_t)(pa.lh_base + li % pa.lh_count) * r.cap;
+                return;
+            }
+        }
+    };
+    load_piece();
+    auto issue = [&]() {
+        if (li >= it1)
+            return;
+        if (lane == 0) {
+            const uint32_t bar = full0 + 8u * (uint32_t)(n_issued & 1), dst = tiles + (uint32_t)((n_issued & 1) * kOdStage);
+            const int row = (int)(l_row0 + (int64_t)lj * kOdTile);
+            dec_expect_tx(bar, kOdStage);
+            dec_tma_load(dst, &tmk, 0, row, bar);
+            dec_tma_load(dst + kOdPanel, &tmk, 64, row, bar);
+            dec_tma_load(dst + 2 * kOdPanel, &tmv, 0, row, bar);
+            dec_tma_load(dst + 3 * kOdPanel, &tmv, 64, row, bar);
+        }
+        ++n_issued;
+        if (++lj * kOdTile >= l_keys) {
+            ++li;
+            lj = 0;
+            load_piece();
+        }
+    };
+    issue();
+    issue();
+
+    // rows ra, rb and columns cq, cq + 1 (+ 8) of the MMA fragments
+    const int ra = lane >> 2, rb = ra + 8, cq = (lane & 3) * 2, mi = lane >> 3;
+    const float sc = a.scale_log2;
+    int k = 0;   // steps done
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+        const DevShared rq = reqs[it / pa.lh_count];
+        if (rq.q_len == 0)
+            continue;
+        const int lh_s = it % pa.lh_count, lh = pa.lh_base + lh_s, m_rows = rq.q_len * G;
+        const int n_keys = rq.own + rq.q_len, n_t = (n_keys + kOdTile - 1) / kOdTile;
+        const int see[2] = {ra < m_rows ? rq.own + ra / G + 1 : 0, rb < m_rows ? rq.own + rb / G + 1 : 0};
+        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(pa.q_rot) + ((int64_t)lh * a.total_q + rq.q_off) * G * kSpD;
+        uint32_t qa[8][4];
+#pragma unroll
+        for (int kb = 0; kb < 8; ++kb) {
+            auto ld2 = [&](int r, int c) -> uint32_t {
+                return r < m_rows ? *reinterpret_cast<const uint32_t *>(qp + r * kSpD + c) : 0u;
+            };
+            qa[kb][0] = ld2(ra, kb * 16 + cq);
+            qa[kb][1] = ld2(rb, kb * 16 + cq);
+            qa[kb][2] = ld2(ra, kb * 16 + cq + 8);
+            qa[kb][3] = ld2(rb, kb * 16 + cq + 8);
+        }
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        float o[16][4];
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        for (int j = 0; j < n_t; ++j, ++k) {
+            const uint32_t kt = tiles + (uint32_t)((k & 1) * kOdStage), vt = kt + 2 * kOdPanel;
+            ok = own_wait(full0 + 8u * (uint32_t)(k & 1), (uint32_t)(k >> 1) & 1);
+            if (!(ok = __all_sync(0xffffffffu, ok)))
+                break;
+            const int n_here = n_keys - j * kOdTile;
+            if (n_here < kOdTile) {   // V rows behind the last key are zero
+                for (int idx = lane; idx < (kOdTile - n_here) * 16; idx += 32)
+                    st_shared_v4(vt + od_off(n_here + (idx >> 4), idx & 15), 0u, 0u, 0u, 0u);
+                __syncwarp();
+            }
+            float c[4][4];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb)
+                c[nb][0] = c[nb][1] = c[nb][2] = c[nb][3] = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < 8; ++kb) {
+#pragma unroll
+                for (int nb = 0; nb < 4; nb += 2) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4(kt + od_off(8 * (nb + (mi >> 1)) + (lane & 7), 2 * kb + (mi & 1)), b0, b1, b2, b3);
+                    mma_bf16(c[nb], qa[kb], b0, b1);
+                    mma_bf16(c[nb + 1], qa[kb], b2, b3);
+                }
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int kk = j * kOdTile + 8 * nb + cq + (e & 1);
+                    c[nb][e] = kk < see[e >> 1] ? c[nb][e] * sc : -INFINITY;
+                    mx[e >> 1] = fmaxf(mx[e >> 1], c[nb][e]);
+                }
+            }
+            float corr[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                const float m_new = fmaxf(m_run[h], mx[h]);
+                corr[h] = m_new == -INFINITY ? 1.f : dec_ex2(m_run[h] - m_new);
+                m_run[h] = m_new;
+            }
+            const float nm[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
+            float sum[2] = {0.f, 0.f};
+            uint32_t p[2][4];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+                const float p0 = dec_ex2(c[nb][0] + nm[0]), p1 = dec_ex2(c[nb][1] + nm[0]);
+                const float p2 = dec_ex2(c[nb][2] + nm[1]), p3 = dec_ex2(c[nb][3] + nm[1]);
+                sum[0] += p0 + p1;
+                sum[1] += p2 + p3;
+                p[nb >> 1][(nb & 1) * 2 + 0] = pack2(p0, p1);
+                p[nb >> 1][(nb & 1) * 2 + 1] = pack2(p2, p3);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)   // (this lane's keys only: added up over the quad at the end)
+                l_run[h] = l_run[h] * corr[h] + sum[h];
+            if (j > 0) {
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    o[n][0] *= corr[0];
+                    o[n][1] *= corr[0];
+                    o[n][2] *= corr[1];
+                    o[n][3] *= corr[1];
+                }
+            }
+#pragma unroll
+            for (int kb2 = 0; kb2 < 2; ++kb2) {
+#pragma unroll
+                for (int n = 0; n < 16; n += 2) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4_t(vt + od_off(16 * kb2 + 8 * (mi & 1) + (lane & 7), n + (mi >> 1)), b0, b1, b2, b3);
+                    mma_bf16(o[n], p[kb2], b0, b1);
+                    mma_bf16(o[n + 1], p[kb2], b2, b3);
+                }
+            }
+            if (n_here < kOdTile)
+                fence_proxy_async_smem();   // the zeroed rows, before the stage's next TMA write
+            __syncwarp();
+            issue();
+        }
+        if (!ok)
+            break;
+        // the prefix's partial results, in stretch order
+        if (!waited) {
+            pdl_wait_prerequisites();
+            waited = true;
+        }
+        const DevGroup g = groups[rq.group];
+        const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int r = hh ? rb : ra;
+            float L = l_run[hh];
+            L += __shfl_xor_sync(0xffffffffu, L, 1);
+            L += __shfl_xor_sync(0xffffffffu, L, 2);
+            if (r >= m_rows)
+                continue;
+            const PartRef pr = part_ref(pa, g, lh_s, (rq.q_off - g.q_off) * G + r);
+            const int two = pr.x1() - pr.x0(), n = pr.n << two;
+            float M = L == 0.f ? -INFINITY : m_run[hh];   // (a sum of 0: no key counts)
+            for (int i = 0; i < n; ++i) {
+                const float2 v = part_ml(pa.part, pr.slot + (i >> two), pr.x0() + (i & two))[pr.pr()];
+                M = v.y == 0.f ? M : fmaxf(M, v.x);
+            }
+            const float w_own = L == 0.f ? 0.f : dec_ex2(m_run[hh] - M);
+            L *= w_own;
+#pragma unroll
+            for (int nn = 0; nn < 16; ++nn) {
+                o[nn][2 * hh] *= w_own;
+                o[nn][2 * hh + 1] *= w_own;
+            }
+            for (int i = 0; i < n; ++i) {
+                const int64_t slot = pr.slot + (i >> two);
+                const int x = pr.x0() + (i & two);
+                const float2 v = part_ml(pa.part, slot, x)[pr.pr()];
+                if (v.y == 0.f)   // (its O is undefined)
+                    continue;
+                const float wt = dec_ex2(v.x - M);
+                L += v.y * wt;
+                const float *po = reinterpret_cast<const float *>(part_o(pa.part, slot, x) + (cq >> 2) * 128 + pr.pr()) + (cq & 3);
+                float2 f[16];
+#pragma unroll
+                for (int nn = 0; nn < 16; ++nn)
+                    f[nn] = *reinterpret_cast<const float2 *>(po + nn * 2 * 128 * 4);
+#pragma unroll
+                for (int nn = 0; nn < 16; ++nn) {
+                    o[nn][2 * hh] = fmaf(f[nn].x, wt, o[nn][2 * hh]);
+                    o[nn][2 * hh + 1] = fmaf(f[nn].y, wt, o[nn][2 * hh + 1]);
+                }
+            }
+            if ((lane & 3) == 0 && !(L > 0.f && L < INFINITY))
+                atomicCAS(a.err, kDevOk, kDevBadInput);
+            const float inv = 1.f / L;
+            const int tk = r / G;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                                 (((int64_t)l * a.total_q + rq.q_off + tk) * a.n_q_heads + h * G + (r - tk * G)) * kSpD + cq;
+#pragma unroll
+            for (int nn = 0; nn < 16; ++nn)
+                *reinterpret_cast<uint32_t *>(dst + 8 * nn) = pack2(o[nn][2 * hh] * inv, o[nn][2 * hh + 1] * inv);
+        }
+        __syncwarp();
+    }
+    if (!ok) {   // nothing is in flight when the CTA leaves
+        for (int x = k; x < n_issued; ++x)
+            mbar_drain(full0 + 8u * (uint32_t)(x & 1), (uint32_t)(x >> 1) & 1);
+        if (lane == 0)
+            atomicCAS(a.err, kDevOk, kDevTimeout);
     }
 }
 
@@ -840,8 +1190,9 @@ static cudaError_t shared_attrs()
     if (fa.numRegs != kSpRegsLaunch)
         return cudaErrorInvalidConfiguration;
     if ((e = cudaFuncSetAttribute(k_shared_prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmem)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(k_shared_own<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwSmem)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(k_shared_own<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwSmem)) != cudaSuccess)
+        (e = cudaFuncSetAttribute(k_shared_own_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, ow_bytes(kOwTileMax))) !=
+            cudaSuccess ||
+        (e = cudaFuncSetAttribute(k_shared_own_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, kOdSmem)) != cudaSuccess)
         return e;
     if (dev < 64)
         done[dev].store(true, std::memory_order_release);
@@ -866,11 +1217,11 @@ static cudaError_t launch_pdl(void (*k)(P...), int64_t grid, int block, int smem
     return cudaLaunchKernelEx(&cfg, k, std::forward<A>(args)...);
 }
 
-cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, int n_sms, cudaStream_t s)
+cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, cudaStream_t s)
 {
-    const int64_t n_items = (int64_t)a.n_reqs * ((a.max_q_len + kPrTokens - 1) / kPrTokens) * a.n_layers * a.n_kv_heads;
-    return launch_pdl(k_shared_prologue, std::min<int64_t>(n_items, (int64_t)n_sms * 8), kPrThreads, 0, false, s, a, rt,
-                      static_cast<__nv_bfloat16 *>(q_rot));
+    const int64_t n_chunks = ((int64_t)a.max_q_len * a.n_layers * a.n_kv_heads + kPrPairs - 1) / kPrPairs;
+    return launch_pdl(k_shared_prologue, a.n_reqs * n_chunks, kPrThreads, 0, false, s, a, rt,
+                      static_cast<__nv_bfloat16 *>(q_rot), (int)n_chunks);
 }
 
 cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s)
@@ -889,14 +1240,20 @@ cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s)
             return e;
     }
     const int rows = a.max_q_len * pa.group;
-    const bool split = rows <= 16;
-    const int n_row_tiles = split ? 1 : (rows + kOwRowsMax - 1) / kOwRowsMax;
-    const int64_t grid = (int64_t)a.n_reqs * pa.lh_count * n_row_tiles;
-    if (split)
-        return launch_pdl(k_shared_own<true>, grid, kOwThreads, kOwSmem, pdl, s, map(t.tmap_k), map(t.tmap_v), a, *t.reqs,
-                          pa, *t.groups, n_row_tiles);
-    return launch_pdl(k_shared_own<false>, grid, kOwThreads, kOwSmem, pdl, s, map(t.tmap_k), map(t.tmap_v), a, *t.reqs, pa,
-                      *t.groups, n_row_tiles);
+    if (rows <= 16) {
+        const int64_t items = (int64_t)a.n_reqs * pa.lh_count;
+        if (items > 0x7fffffff)
+            return cudaErrorInvalidValue;
+        return launch_pdl(k_shared_own_decode, std::min<int64_t>(items, t.n_sms), kOdThreads, kOdSmem, pdl, s, map(t.tmap_k),
+                          map(t.tmap_v), a, *t.reqs, pa, *t.groups);
+    }
+    // tiles that just hold the longest own part, cut evenly (a smaller tile
+    // leaves room for more CTAs per SM)
+    const int n_tiles = (t.max_own_keys + kOwTileMax - 1) / kOwTileMax;
+    const int tile_keys = ((t.max_own_keys + n_tiles - 1) / n_tiles + 31) & ~31;
+    const int n_row_tiles = (rows + kOwRowsMax - 1) / kOwRowsMax;
+    return launch_pdl(k_shared_own_rows, (int64_t)a.n_reqs * pa.lh_count * n_row_tiles, kOwThreads, ow_bytes(tile_keys), pdl, s,
+                      map(t.tmap_k), map(t.tmap_v), a, *t.reqs, pa, *t.groups, n_row_tiles, tile_keys);
 }
 
 }  // namespace kvr
