@@ -212,12 +212,13 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 }
                 float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int c = 4; c < kSpTile; c += 4) {
+                for (int c = 4; c + 4 < kSpTile; c += 8) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        m4[k] = fmaxf(m4[k], s[c + k]);
+                        m4[k] = max3(m4[k], s[c + 2 * k], s[c + 2 * k + 1]);
                 }
-                const float mxs = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+                const float mxs = max3(max3(m4[0], m4[1], m4[2]), m4[3],
+                                       max3(max3(s[kSpTile - 4], s[kSpTile - 3], s[kSpTile - 2]), s[kSpTile - 1], m4[0])) * sc;
                 // lazy maximum: O and l are rescaled only when it grows by more than
                 // the threshold
                 float corr = 1.f;
@@ -228,20 +229,27 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                     m_run = mxs;
                 }
                 const float nm = m_run == -INFINITY ? 0.f : -m_run;   // (a score of -inf in every key)
-                float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = pk2(sc, sc), nm2 = pk2(nm, nm);
+                uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float p0 = ex2(fmaf(s[32 * q + 2 * i], sc, nm)), p1 = ex2(fmaf(s[32 * q + 2 * i + 1], sc, nm));
-                        sum4[(2 * i) & 3] += p0;
-                        sum4[(2 * i + 1) & 3] += p1;
+                        float x0, x1;
+                        unpk2(fma2(pk2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), sc2, nm2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        acc[i & 1] = add2(acc[i & 1], pk2(p0, p1));
                         pk[i] = pack_bf16(p0, p1);
                     }
                     tmem_st16(lane_base + sp_col_s(x) + 16 * q, pk);
                 }
-                l_run = l_run * corr + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+                {
+                    float a0, a1, b0, b1;
+                    unpk2(acc[0], a0, a1);
+                    unpk2(acc[1], b0, b1);
+                    l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
+                }
                 if (corr != 1.f) {
                     // the commit that signalled this S covers the P V before it: O is stable
 #pragma unroll
@@ -553,13 +561,8 @@ constexpr int kOwThreads = 128;
 constexpr int kOwRowsMax = 64;
 constexpr int kOwTileMax = 128;   // keys per tile
 // Shared memory of k_shared_own_rows: K and V tile ([tile_keys][128], two
-// 128B-swizzled panels each; the rows' final states reuse it), the rows'
-// PartRefs, the barrier.
-__host__ __device__ constexpr int ow_off_ref(int tile_keys)
-{
-    return tile_keys * 512 > kOwRowsMax * (kSpD + 2) * 4 ? tile_keys * 512 : kOwRowsMax * (kSpD + 2) * 4;
-}
-__host__ __device__ constexpr int ow_bytes(int tile_keys) { return ow_off_ref(tile_keys) + kOwRowsMax * 16 + 16 + 1024; }
+// 128B-swizzled panels each), the barrier.
+__host__ __device__ constexpr int ow_bytes(int tile_keys) { return tile_keys * 512 + 16 + 1024; }
 
 // Where the partial results of one row lie: slots [slot, slot + n), tiles x0..x1,
 // row pr of each.
@@ -597,32 +600,117 @@ __device__ __forceinline__ bool own_wait(uint32_t bar, uint32_t parity)
     return mbar_try_wait(bar, parity) || mbar_drain(bar, parity);
 }
 
-// Adds a partial sum (relative to maximum m, denominator l) to a running one.
-__device__ __forceinline__ void add_state(float &M, float &L, float *acc, float m, float l, const float *o)
+// The end of a row tile: adds the prefix's partial results (in stretch order) to
+// the warp's own states and writes the rows.  Lane: columns 8n + cq, + 1 of row
+// r_first of the request and of row r_first + 8 (fragment layout); l_run holds
+// the lane's keys only.
+__device__ __forceinline__ void finish_rows(const SharedArgs &a, const SharedPrefixArgs &pa, const DevGroup &g,
+                                            const DevShared &rq, int lh_s, int r_first, int m_rows, float (&o)[16][4],
+                                            const float *m_run, const float *l_run)
 {
-    if (l == 0.f)   // no key counts
-        return;
-    const float n = fmaxf(M, m), a = L == 0.f ? 0.f : dec::dec_ex2(M - n), b = dec::dec_ex2(m - n);
-    L = L * a + l * b;
+    const int lane = threadIdx.x & 31, cq = (lane & 3) * 2, G = pa.group;
+    const int lh = pa.lh_base + lh_s, l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
+    float L[2], M[2];
+    PartRef pr[2];
+    int n[2], two[2];
+    float2 v0[2];   // (max, sum) of the first partial result
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        acc[e] = acc[e] * a + o[e] * b;
-    M = n;
+    for (int hh = 0; hh < 2; ++hh) {
+        const int r = r_first + 8 * hh;
+        L[hh] = l_run[hh];
+        L[hh] += __shfl_xor_sync(0xffffffffu, L[hh], 1);
+        L[hh] += __shfl_xor_sync(0xffffffffu, L[hh], 2);
+        pr[hh] = PartRef{0, 0, 0};
+        if (r < m_rows)
+            pr[hh] = part_ref(pa, g, lh_s, (rq.q_off - g.q_off) * G + r);
+        two[hh] = pr[hh].x1() - pr[hh].x0();
+        n[hh] = pr[hh].n << two[hh];
+        v0[hh] = n[hh] > 0 ? part_ml(pa.part, pr[hh].slot, pr[hh].x0())[pr[hh].pr()] : make_float2(-INFINITY, 0.f);
+    }
+    auto part_state = [&](int hh, int i) -> float2 {
+        return i == 0 ? v0[hh] : part_ml(pa.part, pr[hh].slot + (i >> two[hh]), pr[hh].x0() + (i & two[hh]))[pr[hh].pr()];
+    };
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        M[hh] = L[hh] == 0.f ? -INFINITY : m_run[hh];   // (a sum of 0: no key counts)
+        for (int i = 0; i < n[hh]; ++i) {
+            const float2 v = part_state(hh, i);
+            M[hh] = v.y == 0.f ? M[hh] : fmaxf(M[hh], v.x);
+        }
+        const float w_own = L[hh] == 0.f ? 0.f : dec::dec_ex2(m_run[hh] - M[hh]);
+        L[hh] *= w_own;
+#pragma unroll
+        for (int nn = 0; nn < 16; ++nn) {
+            o[nn][2 * hh] *= w_own;
+            o[nn][2 * hh + 1] *= w_own;
+        }
+    }
+    for (int i = 0; i < max(n[0], n[1]); ++i) {
+        float wt[2];
+        const float *po[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            wt[hh] = 0.f;
+            po[hh] = nullptr;
+            if (i >= n[hh])
+                continue;
+            const float2 v = part_state(hh, i);
+            if (v.y == 0.f)   // (its O is undefined)
+                continue;
+            wt[hh] = dec::dec_ex2(v.x - M[hh]);
+            L[hh] += v.y * wt[hh];
+            po[hh] = reinterpret_cast<const float *>(part_o(pa.part, pr[hh].slot + (i >> two[hh]), pr[hh].x0() + (i & two[hh])) +
+                                                     (cq >> 2) * 128 + pr[hh].pr()) + (cq & 3);
+        }
+#pragma unroll
+        for (int n0 = 0; n0 < 16; n0 += 8) {   // both rows' loads before their use
+            float2 f[2][8];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int nn = 0; nn < 8; ++nn)
+                    f[hh][nn] = po[hh] ? *reinterpret_cast<const float2 *>(po[hh] + (n0 + nn) * 2 * 128 * 4) : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int nn = 0; nn < 8; ++nn) {
+                    o[n0 + nn][2 * hh] = fmaf(f[hh][nn].x, wt[hh], o[n0 + nn][2 * hh]);
+                    o[n0 + nn][2 * hh + 1] = fmaf(f[hh][nn].y, wt[hh], o[n0 + nn][2 * hh + 1]);
+                }
+        }
+    }
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        const int r = r_first + 8 * hh;
+        if (r >= m_rows)
+            continue;
+        if ((lane & 3) == 0 && !(L[hh] > 0.f && L[hh] < INFINITY))
+            atomicCAS(a.err, kDevOk, kDevBadInput);
+        const float inv = 1.f / L[hh];
+        const int tk = r / G;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                             (((int64_t)l * a.total_q + rq.q_off + tk) * a.n_q_heads + h * G + (r - tk * G)) * kSpD + cq;
+#pragma unroll
+        for (int nn = 0; nn < 16; ++nn)
+            *reinterpret_cast<uint32_t *>(dst + 8 * nn) = dec::pack2(o[nn][2 * hh] * inv, o[nn][2 * hh + 1] * inv);
+    }
 }
 }  // namespace
 
-// More than 16 query rows a request: a CTA per (request, unit, 64 rows); each
-// warp has an MMA row tile of its own and takes all keys of a tile.
+// More than 16 query rows a request: a CTA takes `tiles_per_cta` groups of 64
+// rows of a (request, unit); each warp has an MMA row tile of its own and takes
+// all keys of a tile.  Own parts of one tile are loaded once per CTA, and its
+// warps then go through their rows independently.
 __global__ void __launch_bounds__(kOwThreads, 3)
     k_shared_own_rows(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                  const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
-                 const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt, const int n_row_tiles,
-                 const int tile_keys)
+                 const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt, const int n_chunks,
+                 const int tiles_per_cta, const int tile_keys)
 {
     using namespace dec;
     extern __shared__ uint8_t ow_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ow_smem_raw) + 1023) & ~uintptr_t(1023));
-    const int panel = tile_keys * 128, kOwTile = tile_keys, off_ref = ow_off_ref(tile_keys), off_bar = off_ref + kOwRowsMax * 16;
+    const int panel = tile_keys * 128, kOwTile = tile_keys, off_bar = 4 * panel;
     const uint32_t sbase = dec_smem_u32(smem), kt = sbase, vt = sbase + 2 * panel, full = sbase + off_bar;
     volatile int *cta_err = reinterpret_cast<volatile int *>(smem + off_bar + 8);
     auto sw = [&](int r, int c) { return (uint32_t)((c >> 3) * panel + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
@@ -631,17 +719,18 @@ __global__ void __launch_bounds__(kOwThreads, 3)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = pa.group;
     unsigned bi = blockIdx.x;
-    const int tile = (int)(bi % (unsigned)n_row_tiles);
-    bi /= (unsigned)n_row_tiles;
+    const int chunk = (int)(bi % (unsigned)n_chunks);
+    bi /= (unsigned)n_chunks;
     const int lh_s = (int)(bi % (unsigned)pa.lh_count), lh = pa.lh_base + lh_s;
     const DevShared rq = reqs[bi / (unsigned)pa.lh_count];
-    const int m_rows = rq.q_len * G, r0 = tile * kOwRowsMax;
-    if (r0 >= m_rows)
+    const int m_rows = rq.q_len * G;
+    const int r_first = chunk * tiles_per_cta * kOwRowsMax, r_last = min(m_rows, r_first + tiles_per_cta * kOwRowsMax);
+    if (r_first >= m_rows)
         return;   // uniform over the CTA
-    const int rows = min(kOwRowsMax, m_rows - r0);
-    const int n_keys = rq.own + (r0 + rows - 1) / G + 1;   // of the last row
-    const int n_t = (n_keys + kOwTile - 1) / kOwTile;
+    auto keys_to = [&](int r_end) { return rq.own + (r_end - 1) / G + 1; };   // keys of the rows before r_end
+    const bool once = keys_to(r_last) <= kOwTile;
     const int64_t kv_row0 = rq.cache_row0 + (int64_t)lh * rq.cap;
+    int n_keys = keys_to(once ? r_last : min(r_last, r_first + kOwRowsMax));
 
     auto issue = [&](int j) {   // thread 0
         const int n32 = min(kOwTile >> 5, (n_keys - j * kOwTile + 31) >> 5);
@@ -664,238 +753,142 @@ __global__ void __launch_bounds__(kOwThreads, 3)
     } else {
         pdl_wait_prerequisites();
     }
-    // query fragments (A operand): rows ra, rb of this warp's row tile
-    const int rt0 = 16 * warp;              // first CTA row of the warp's row tile
-    const int ra = rt0 + (lane >> 2), rb = ra + 8, cq = (lane & 3) * 2;
-    const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(pa.q_rot) +
-                              (((int64_t)lh * a.total_q + rq.q_off) * G + r0) * kSpD;
-    uint32_t qa[8][4];
-#pragma unroll
-    for (int kb = 0; kb < 8; ++kb) {
-        const int c0 = kb * 16 + cq;
-        auto ld2 = [&](int r, int c) -> uint32_t {
-            return r < rows ? *reinterpret_cast<const uint32_t *>(qp + (int64_t)r * kSpD + c) : 0u;
-        };
-        qa[kb][0] = ld2(ra, c0);
-        qa[kb][1] = ld2(rb, c0);
-        qa[kb][2] = ld2(ra, c0 + 8);
-        qa[kb][3] = ld2(rb, c0 + 8);
-    }
-    // where the prefix's partial results lie, while the tile is on its way
-    {
-        const DevGroup g = groups[rq.group];
-        const int g_row0 = (rq.q_off - g.q_off) * G + r0;
-        if ((int)threadIdx.x < rows)
-            reinterpret_cast<PartRef *>(smem + off_ref)[threadIdx.x] = part_ref(pa, g, lh_s, g_row0 + (int)threadIdx.x);
-    }
     __syncthreads();   // the barrier is initialised
-    // keys that the two rows see
-    const int see[2] = {ra < rows ? rq.own + (r0 + ra) / G + 1 : 0, rb < rows ? rq.own + (r0 + rb) / G + 1 : 0};
-
     const float sc = a.scale_log2;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    float o[16][4];
-#pragma unroll
-    for (int n = 0; n < 16; ++n)
-        o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    for (int j = 0; j < n_t; ++j) {
-        if (!own_wait(full, (uint32_t)j & 1))
-            *cta_err = 1;
-        const int kk0 = j * kOwTile, n_here = min(kOwTile, n_keys - kk0);
-        // V rows behind the last key are zero (32-row groups that were loaded)
-        const int n_ld = (n_here + 31) & ~31;
-        for (int idx = threadIdx.x; idx < (n_ld - n_here) * 16; idx += kOwThreads) {
-            const int row = n_here + (idx >> 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vt + sw(row, idx & 15)), "r"(0u) : "memory");
+    const int rt0 = 16 * warp;   // the warp's row tile in a group
+    const int ra = rt0 + (lane >> 2), rb = ra + 8, cq = (lane & 3) * 2;
+    int step = 0;   // tiles loaded
+    for (int r0 = r_first; r0 < r_last; r0 += kOwRowsMax) {
+        const int rows = min(kOwRowsMax, r_last - r0);
+        if (!once && r0 > r_first) {
+            n_keys = keys_to(r0 + rows);
+            if (threadIdx.x == 0)
+                issue(0);
         }
-        __syncthreads();
-        if (*cta_err) {   // the same for every thread
-            if (threadIdx.x == 0) {
-                atomicCAS(a.err, kDevOk, kDevTimeout);
-                mbar_drain(full, (uint32_t)j & 1);
+        const int n_t = (n_keys + kOwTile - 1) / kOwTile;
+        // query fragments (A operand): rows ra, rb of this warp's row tile
+        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(pa.q_rot) +
+                                  (((int64_t)lh * a.total_q + rq.q_off) * G + r0) * kSpD;
+        uint32_t qa[8][4];
+#pragma unroll
+        for (int kb = 0; kb < 8; ++kb) {
+            const int c0 = kb * 16 + cq;
+            auto ld2 = [&](int r, int c) -> uint32_t {
+                return r < rows ? *reinterpret_cast<const uint32_t *>(qp + (int64_t)r * kSpD + c) : 0u;
+            };
+            qa[kb][0] = ld2(ra, c0);
+            qa[kb][1] = ld2(rb, c0);
+            qa[kb][2] = ld2(ra, c0 + 8);
+            qa[kb][3] = ld2(rb, c0 + 8);
+        }
+        // keys that the two rows see
+        const int see[2] = {ra < rows ? rq.own + (r0 + ra) / G + 1 : 0, rb < rows ? rq.own + (r0 + rb) / G + 1 : 0};
+        const int see_warp = rt0 < rows ? rq.own + (r0 + min(rt0 + 15, rows - 1)) / G + 1 : 0;
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        float o[16][4];
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        for (int j = 0; j < n_t; ++j) {
+            const int kk0 = j * kOwTile, n_here = min(kOwTile, n_keys - kk0);
+            if (!once || r0 == r_first) {
+                if (!own_wait(full, (uint32_t)step & 1))
+                    *cta_err = 1;
+                // V rows behind the last key are zero (32-row groups that were loaded)
+                const int n_ld = (n_here + 31) & ~31;
+                for (int idx = threadIdx.x; idx < (n_ld - n_here) * 16; idx += kOwThreads)
+                    st_shared_v4(vt + sw(n_here + (idx >> 4), idx & 15), 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();   // (before the tile's next TMA write)
+                __syncthreads();
+                if (*cta_err) {   // the same for every thread
+                    if (threadIdx.x == 0) {
+                        atomicCAS(a.err, kDevOk, kDevTimeout);
+                        mbar_drain(full, (uint32_t)step & 1);
+                    }
+                    return;
+                }
+                ++step;
             }
-            return;
-        }
-        for (int key0 = 0; key0 < n_here; key0 += 32) {
-            float c[4][4];
+            const int n_warp = min(n_here, see_warp - kk0);   // keys that some row of the warp sees
+            for (int key0 = 0; key0 < n_warp; key0 += 32) {
+                float c[4][4];
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb)
-                c[nb][0] = c[nb][1] = c[nb][2] = c[nb][3] = 0.f;
+                for (int nb = 0; nb < 4; ++nb)
+                    c[nb][0] = c[nb][1] = c[nb][2] = c[nb][3] = 0.f;
 #pragma unroll
-            for (int nb = 0; nb < 4; nb += 2) {
+                for (int nb = 0; nb < 4; nb += 2) {
 #pragma unroll
-                for (int kb = 0; kb < 8; ++kb) {
-                    const int mi = lane >> 3;
-                    const int key = key0 + 8 * (nb + (mi >> 1)) + (lane & 7);
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4(kt + sw(key, 2 * kb + (mi & 1)), b0, b1, b2, b3);
-                    mma_bf16(c[nb], qa[kb], b0, b1);
-                    mma_bf16(c[nb + 1], qa[kb], b2, b3);
+                    for (int kb = 0; kb < 8; ++kb) {
+                        const int mi = lane >> 3;
+                        const int key = key0 + 8 * (nb + (mi >> 1)) + (lane & 7);
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4(kt + sw(key, 2 * kb + (mi & 1)), b0, b1, b2, b3);
+                        mma_bf16(c[nb], qa[kb], b0, b1);
+                        mma_bf16(c[nb + 1], qa[kb], b2, b3);
+                    }
+                }
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int kk = kk0 + key0 + 8 * nb + cq + (e & 1);
+                        c[nb][e] = kk < see[e >> 1] ? c[nb][e] * sc : -INFINITY;
+                        mx[e >> 1] = fmaxf(mx[e >> 1], c[nb][e]);
+                    }
+                }
+                float corr[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                    const float m_new = fmaxf(m_run[h], mx[h]);
+                    corr[h] = m_new == -INFINITY ? 1.f : dec_ex2(m_run[h] - m_new);
+                    m_run[h] = m_new;
+                }
+                const float nm[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
+                float sum[2] = {0.f, 0.f};
+                uint32_t p[2][4];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+                    const float p0 = dec_ex2(c[nb][0] + nm[0]), p1 = dec_ex2(c[nb][1] + nm[0]);
+                    const float p2 = dec_ex2(c[nb][2] + nm[1]), p3 = dec_ex2(c[nb][3] + nm[1]);
+                    sum[0] += p0 + p1;
+                    sum[1] += p2 + p3;
+                    p[nb >> 1][(nb & 1) * 2 + 0] = pack2(p0, p1);
+                    p[nb >> 1][(nb & 1) * 2 + 1] = pack2(p2, p3);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)   // (this lane's keys only)
+                    l_run[h] = l_run[h] * corr[h] + sum[h];
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    o[n][0] *= corr[0];
+                    o[n][1] *= corr[0];
+                    o[n][2] *= corr[1];
+                    o[n][3] *= corr[1];
+                }
+#pragma unroll
+                for (int kb2 = 0; kb2 < 2; ++kb2) {
+#pragma unroll
+                    for (int n = 0; n < 16; n += 2) {
+                        const int mi = lane >> 3;
+                        const int key = key0 + 16 * kb2 + 8 * (mi & 1) + (lane & 7);
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4_t(vt + sw(key, n + (mi >> 1)), b0, b1, b2, b3);
+                        mma_bf16(o[n], p[kb2], b0, b1);
+                        mma_bf16(o[n + 1], p[kb2], b2, b3);
+                    }
                 }
             }
-            float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int kk = kk0 + key0 + 8 * nb + cq + (e & 1);
-                    c[nb][e] = kk < see[e >> 1] ? c[nb][e] * sc : -INFINITY;
-                    mx[e >> 1] = fmaxf(mx[e >> 1], c[nb][e]);
-                }
-            }
-            float corr[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                const float m_new = fmaxf(m_run[h], mx[h]);
-                corr[h] = m_new == -INFINITY ? 1.f : dec_ex2(m_run[h] - m_new);
-                m_run[h] = m_new;
-            }
-            const float nm[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
-            float sum[2] = {0.f, 0.f};
-            uint32_t p[2][4];
-#pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                const float p0 = dec_ex2(c[nb][0] + nm[0]), p1 = dec_ex2(c[nb][1] + nm[0]);
-                const float p2 = dec_ex2(c[nb][2] + nm[1]), p3 = dec_ex2(c[nb][3] + nm[1]);
-                sum[0] += p0 + p1;
-                sum[1] += p2 + p3;
-                p[nb >> 1][(nb & 1) * 2 + 0] = pack2(p0, p1);
-                p[nb >> 1][(nb & 1) * 2 + 1] = pack2(p2, p3);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
-                sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
-                l_run[h] = l_run[h] * corr[h] + sum[h];
-            }
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-                o[n][0] *= corr[0];
-                o[n][1] *= corr[0];
-                o[n][2] *= corr[1];
-                o[n][3] *= corr[1];
-            }
-#pragma unroll
-            for (int kb2 = 0; kb2 < 2; ++kb2) {
-#pragma unroll
-                for (int n = 0; n < 16; n += 2) {
-                    const int mi = lane >> 3;
-                    const int key = key0 + 16 * kb2 + 8 * (mi & 1) + (lane & 7);
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4_t(vt + sw(key, n + (mi >> 1)), b0, b1, b2, b3);
-                    mma_bf16(o[n], p[kb2], b0, b1);
-                    mma_bf16(o[n + 1], p[kb2], b2, b3);
-                }
+            if (!once) {
+                __syncthreads();   // the tile is consumed
+                if (threadIdx.x == 0 && j + 1 < n_t)
+                    issue(j + 1);
             }
         }
-        __syncthreads();   // the tile is consumed
-        if (threadIdx.x == 0 && j + 1 < n_t)
-            issue(j + 1);
-    }
 
-    // the own states over the tiles: [row][128], then (max, sum)
-    float *oo = reinterpret_cast<float *>(smem);
-    float2 *ml = reinterpret_cast<float2 *>(oo + kOwRowsMax * kSpD);
-    if ((lane & 3) == 0) {
-        ml[ra] = make_float2(m_run[0], l_run[0]);
-        ml[rb] = make_float2(m_run[1], l_run[1]);
-    }
-#pragma unroll
-    for (int n = 0; n < 16; ++n) {
-        const int col = 8 * n + cq;
-        *reinterpret_cast<float2 *>(oo + ra * kSpD + col) = make_float2(o[n][0], o[n][1]);
-        *reinterpret_cast<float2 *>(oo + rb * kSpD + col) = make_float2(o[n][2], o[n][3]);
-    }
-    __syncthreads();
-    // 8 threads a row, 16 columns each: the own state, then the prefix's
-    const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
-    const int c0 = 16 * (threadIdx.x & 7);
-    auto own_state = [&](int row, float &M, float &L, float *acc) {
-        M = -INFINITY;
-        L = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-            acc[e] = 0.f;
-        const float2 v = ml[row];
-        float f[16];
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const float4 u = *reinterpret_cast<const float4 *>(oo + row * kSpD + c0 + e);
-            f[e] = u.x;
-            f[e + 1] = u.y;
-            f[e + 2] = u.z;
-            f[e + 3] = u.w;
-        }
-        add_state(M, L, acc, v.x, v.y, f);
-    };
-    auto put = [&](int row, float L, const float *acc) {
-        if (!(L > 0.f && L < INFINITY) && c0 == 0)
-            atomicCAS(a.err, kDevOk, kDevBadInput);
-        const float inv = 1.f / L;
-        uint32_t pk[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            pk[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        const int t = (r0 + row) / G, gg = r0 + row - t * G;
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                             (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + gg) * kSpD + c0;
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-    };
-    // the first partial result of each of the thread's rows is loaded ahead
-    constexpr int NR = kOwRowsMax / (kOwThreads / 8);
-    PartRef ref[NR];
-    float2 v1[NR];
-    float4 f1[NR][4];
-#pragma unroll
-    for (int k = 0; k < NR; ++k) {
-        const int row = (int)(threadIdx.x >> 3) + k * (kOwThreads / 8);
-        ref[k].n = 0;
-        if (row < rows)
-            ref[k] = reinterpret_cast<const PartRef *>(smem + off_ref)[row];
-        if (ref[k].n > 0) {
-            v1[k] = part_ml(pa.part, ref[k].slot, ref[k].x0())[ref[k].pr()];
-            const float4 *po = part_o(pa.part, ref[k].slot, ref[k].x0()) + ref[k].pr() + c0 * 32;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                f1[k][e] = po[e * 128];
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < NR; ++k) {
-        const int row = (int)(threadIdx.x >> 3) + k * (kOwThreads / 8);
-        if (row >= rows)
-            break;
-        float M, L, acc[16];
-        own_state(row, M, L, acc);
-        auto add = [&](const float2 &v, const float4 *u) {
-            float f[16];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[4 * e] = u[e].x;
-                f[4 * e + 1] = u[e].y;
-                f[4 * e + 2] = u[e].z;
-                f[4 * e + 3] = u[e].w;
-            }
-            add_state(M, L, acc, v.x, v.y, f);
-        };
-        if (ref[k].n > 0)
-            add(v1[k], f1[k]);
-        for (int i = 0; i < ref[k].n; ++i)
-            for (int x = ref[k].x0(); x <= ref[k].x1(); ++x) {   // in stretch order
-                if (i == 0 && x == ref[k].x0())
-                    continue;
-                const float2 v = part_ml(pa.part, ref[k].slot + i, x)[ref[k].pr()];
-                const float4 *po = part_o(pa.part, ref[k].slot + i, x) + ref[k].pr() + c0 * 32;
-                float4 u[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] = po[e * 128];
-                add(v, u);
-            }
-        put(row, L, acc);
+        finish_rows(a, pa, groups[rq.group], rq, lh_s, r0 + ra, r0 + rows, o, m_run, l_run);
     }
 }
 
@@ -1104,64 +1097,11 @@ __global__ void __launch_bounds__(kOdThreads, 1)
         }
         if (!ok)
             break;
-        // the prefix's partial results, in stretch order
-        if (!waited) {
+        if (!waited) {   // the prefix's partial results
             pdl_wait_prerequisites();
             waited = true;
         }
-        const DevGroup g = groups[rq.group];
-        const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int r = hh ? rb : ra;
-            float L = l_run[hh];
-            L += __shfl_xor_sync(0xffffffffu, L, 1);
-            L += __shfl_xor_sync(0xffffffffu, L, 2);
-            if (r >= m_rows)
-                continue;
-            const PartRef pr = part_ref(pa, g, lh_s, (rq.q_off - g.q_off) * G + r);
-            const int two = pr.x1() - pr.x0(), n = pr.n << two;
-            float M = L == 0.f ? -INFINITY : m_run[hh];   // (a sum of 0: no key counts)
-            for (int i = 0; i < n; ++i) {
-                const float2 v = part_ml(pa.part, pr.slot + (i >> two), pr.x0() + (i & two))[pr.pr()];
-                M = v.y == 0.f ? M : fmaxf(M, v.x);
-            }
-            const float w_own = L == 0.f ? 0.f : dec_ex2(m_run[hh] - M);
-            L *= w_own;
-#pragma unroll
-            for (int nn = 0; nn < 16; ++nn) {
-                o[nn][2 * hh] *= w_own;
-                o[nn][2 * hh + 1] *= w_own;
-            }
-            for (int i = 0; i < n; ++i) {
-                const int64_t slot = pr.slot + (i >> two);
-                const int x = pr.x0() + (i & two);
-                const float2 v = part_ml(pa.part, slot, x)[pr.pr()];
-                if (v.y == 0.f)   // (its O is undefined)
-                    continue;
-                const float wt = dec_ex2(v.x - M);
-                L += v.y * wt;
-                const float *po = reinterpret_cast<const float *>(part_o(pa.part, slot, x) + (cq >> 2) * 128 + pr.pr()) + (cq & 3);
-                float2 f[16];
-#pragma unroll
-                for (int nn = 0; nn < 16; ++nn)
-                    f[nn] = *reinterpret_cast<const float2 *>(po + nn * 2 * 128 * 4);
-#pragma unroll
-                for (int nn = 0; nn < 16; ++nn) {
-                    o[nn][2 * hh] = fmaf(f[nn].x, wt, o[nn][2 * hh]);
-                    o[nn][2 * hh + 1] = fmaf(f[nn].y, wt, o[nn][2 * hh + 1]);
-                }
-            }
-            if ((lane & 3) == 0 && !(L > 0.f && L < INFINITY))
-                atomicCAS(a.err, kDevOk, kDevBadInput);
-            const float inv = 1.f / L;
-            const int tk = r / G;
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                 (((int64_t)l * a.total_q + rq.q_off + tk) * a.n_q_heads + h * G + (r - tk * G)) * kSpD + cq;
-#pragma unroll
-            for (int nn = 0; nn < 16; ++nn)
-                *reinterpret_cast<uint32_t *>(dst + 8 * nn) = pack2(o[nn][2 * hh] * inv, o[nn][2 * hh + 1] * inv);
-        }
+        finish_rows(a, pa, groups[rq.group], rq, lh_s, ra, m_rows, o, m_run, l_run);
         __syncwarp();
     }
     if (!ok) {   // nothing is in flight when the CTA leaves
@@ -1251,9 +1191,14 @@ cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s)
     // leaves room for more CTAs per SM)
     const int n_tiles = (t.max_own_keys + kOwTileMax - 1) / kOwTileMax;
     const int tile_keys = ((t.max_own_keys + n_tiles - 1) / n_tiles + 31) & ~31;
-    const int n_row_tiles = (rows + kOwRowsMax - 1) / kOwRowsMax;
-    return launch_pdl(k_shared_own_rows, (int64_t)a.n_reqs * pa.lh_count * n_row_tiles, kOwThreads, ow_bytes(tile_keys), pdl, s,
-                      map(t.tmap_k), map(t.tmap_v), a, *t.reqs, pa, *t.groups, n_row_tiles, tile_keys);
+    // row groups per CTA: all of a (request, unit)'s, while that leaves three
+    // CTAs per SM
+    const int n_groups = (rows + kOwRowsMax - 1) / kOwRowsMax;
+    const int64_t units = (int64_t)a.n_reqs * pa.lh_count;
+    const int per_cta = (int)std::min<int64_t>(n_groups, std::max<int64_t>(1, units * n_groups / (3 * (int64_t)t.n_sms)));
+    const int n_chunks = (n_groups + per_cta - 1) / per_cta;
+    return launch_pdl(k_shared_own_rows, units * n_chunks, kOwThreads, ow_bytes(tile_keys), pdl, s, map(t.tmap_k), map(t.tmap_v),
+                      a, *t.reqs, pa, *t.groups, n_chunks, per_cta, tile_keys);
 }
 
 }  // namespace kvr
