@@ -109,7 +109,8 @@ struct kvr_pool {
     kvr_pool_desc d{};
     int device = 0;
     int cc = 0;               // compute capability, major * 10 + minor
-    float2 *rope = nullptr;   // RoPE tables
+    float2 *rope = nullptr;   // RoPE tables, then the pairs' frequencies in turns
+    float2 *rope_turns = nullptr;
     int *err = nullptr;       // device error word
     Slot slots[kSlots];
     int next = 0;
@@ -296,12 +297,15 @@ static kvr_status ensure_device(kvr_pool *p)
     p->cc = maj * 10 + min;
     cudaDeviceGetAttribute(&p->n_sms, cudaDevAttrMultiProcessorCount, p->device);
     const size_t tab = sizeof(float2) * 2 * kRopeSplit * (p->d.head_dim / 2);
-    if ((e = cudaMalloc(&p->rope, tab)) != cudaSuccess ||
+    if ((e = cudaMalloc(&p->rope, tab + sizeof(float2) * (p->d.head_dim / 2))) != cudaSuccess ||
         (e = cudaMalloc(&p->err, sizeof(int))) != cudaSuccess ||
         (e = cudaMemset(p->err, 0, sizeof(int))) != cudaSuccess ||
         (e = launch_rope_tables(p->rope, p->d.head_dim, p->d.rope_theta, 0)) != cudaSuccess ||
+        (e = launch_rope_turns(p->rope + 2 * kRopeSplit * (p->d.head_dim / 2), p->d.head_dim, p->d.rope_theta, 0)) !=
+            cudaSuccess ||
         (e = cudaStreamSynchronize(0)) != cudaSuccess)
         return cuda_fail(e, "pool device setup");
+    p->rope_turns = p->rope + 2 * kRopeSplit * (p->d.head_dim / 2);
     cudaDriverEntryPointQueryResult q;
     void *fn = nullptr;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
@@ -1856,6 +1860,7 @@ extern "C" kvr_status kvr_evict(kvr_pool_t p, int32_t batch, const int64_t *cach
             return st;
         DeviceGuard g(p->device);
         a.rope = p->rope;
+        a.rope_turns = p->rope_turns;
         a.weights = weights;
         a.cache_k = cache_k;
         a.cache_v = cache_v;
@@ -1882,7 +1887,7 @@ extern "C" kvr_status kvr_evict(kvr_pool_t p, int32_t batch, const int64_t *cach
         cudaError_t e;
         {
             NvtxRange r("kvr.k_evict");
-            e = launch_evict(a, tab, p->d.dtype, D, s);
+            e = launch_evict(a, tab, p->d.dtype, D, p->n_sms, s);
         }
         if (slot)
             cudaEventRecord(slot->done, s);

@@ -22,17 +22,17 @@ namespace kvr {
 
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMoveThreads = 256;
 
 // Integer key in the order of the weights: NaN lowest, then -inf .. +inf, both
-// zeros alike.
-__device__ __forceinline__ uint32_t weight_key(float w)
+// zeros alike.  Two more values: kNoRow below all of them, for places past the
+// rows, and kAlways above, for rows that stay whatever they weigh.
+constexpr uint32_t kNoRow = 0u, kNanKey = 1u, kMaxKey = 0xff800000u, kAlways = 0xffffffffu;
+__device__ __forceinline__ uint32_t weight_key(uint32_t bits)
 {
-    if (w != w)
-        return 0u;
-    const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
+    if ((bits & 0x7fffffffu) > 0x7f800000u)
+        return kNanKey;
+    const uint32_t u = bits == 0x80000000u ? 0u : bits;
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
@@ -86,121 +86,282 @@ struct RowVec<float> {
 
 }  // namespace
 
-// One CTA per (request, unit).  The threshold is found 8 bits at a time: a
-// histogram of the candidates' next digit, and the digit in which the k-th
-// largest falls.  Each warp then owns one consecutive stretch of rows, counts
-// what it keeps, and writes its rows behind the warps before it.
-__global__ void __launch_bounds__(kSelThreads)
+// One CTA of TH threads per (request, unit).  The threshold is found 11, 11 and
+// 10 bits at a time: a histogram of the candidates' next digit, and the digit in
+// which the k-th largest falls (11 bits: a float's exponent and two bits of its
+// fraction, so that heavy-tailed weights already spread over many bins).  Once
+// at most kRankMax candidates are left, each counts the candidates before it,
+// (weight, then lower row) deciding.  With many rows the shared-memory atomics
+// of the first histogram dominate: there an eighth of the rows is counted first,
+// and then only the rows in the digits that the k-th largest can lie in.
+// Warp w owns rows [32 R' w, 32 R' (w + 1)), R' = ceil(n / TH); it counts what it
+// keeps and writes its rows behind the warps before it.  The rows' keys are read
+// once, R per thread in registers; with R = 0 every pass reads them again.
+constexpr int kRankMax = 256;
+
+template <int TH, int R>
+__global__ void __launch_bounds__(TH, 1)
     k_evict_select(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
 {
+    constexpr int NW = TH / 32, BPT = 2048 / TH;   // warps, bins of a thread
     const DevEvict *reqs = a.reqs ? a.reqs : rt.reqs;
     const int b = (int)(blockIdx.x / (unsigned)a.units), lh = (int)(blockIdx.x % (unsigned)a.units);
     const DevEvict rq = reqs[b];
     int32_t *kept = a.kept + rq.kept0 + (int64_t)lh * rq.keep;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();   // (the move kernel waits for this grid)
     if (rq.keep == rq.n) {
-        for (int i = threadIdx.x; i < rq.n; i += kSelThreads)
+        for (int i = threadIdx.x; i < rq.n; i += TH)
             kept[i] = i;
         return;
     }
     const float *w = a.weights + rq.src_row0 + (int64_t)lh * rq.src_cap;
     const int lo = a.n_first, hi = rq.n - a.n_recent;   // rows that compete
     const int k = rq.keep - a.n_first - a.n_recent;     // how many of them stay
+    const int n_r = (rq.n + TH - 1) / TH, row0 = warp * 32 * n_r + lane;
 
-    __shared__ int hist[256];
-    __shared__ uint32_t s_digit;
-    __shared__ int s_left;
-    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
-    uint32_t prefix = 0;   // the threshold's leading digits
-    int left = k;          // how many of the rows with those digits stay
-    for (int shift = 24; shift >= 0 && k > 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += kSelThreads)
-            hist[i] = 0;
-        __syncthreads();
-        for (int i = lo + (int)threadIdx.x; i < hi; i += kSelThreads) {
-            const uint32_t key = weight_key(w[i]);
-            if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&hist[(key >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l holds digits 255 - 8l .. 248 - 8l (descending)
-            int c[8], sum = 0;
+    __shared__ int hist[2048];
+    __shared__ int s_warp[NW], s_eq[NW];
+    __shared__ int s_found[3];                  // digit, rank in it (1 based), candidates in it
+    __shared__ int s_n;
+    __shared__ uint2 s_cand[kRankMax];          // (key, row)
+    __shared__ uint2 s_last;                    // the last candidate that stays
+    auto bits_of = [&](int r) -> uint32_t {
+        const int i = row0 + 32 * r;
+        return i < rq.n ? __float_as_uint(w[i]) : 0u;
+    };
+    auto key_of = [&](int r, uint32_t bits) -> uint32_t {
+        const int i = row0 + 32 * r;
+        return i >= rq.n ? kNoRow : i < lo || i >= hi ? kAlways : weight_key(bits);
+    };
+    uint32_t key[R > 0 ? R : 1];
+    if constexpr (R > 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                c[e] = hist[255 - 8 * lane - e];
-                sum += c[e];
-            }
-            int incl = sum;
+        for (int r = 0; r < R; ++r)   // all loads before the first use
+            key[r] = r < n_r ? bits_of(r) : 0u;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += v;
-            }
-            int above = incl - sum;   // rows of larger digits
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (above < left && left <= above + c[e]) {
-                    s_digit = 255 - 8 * lane - e;
-                    s_left = left - above;
-                }
-                above += c[e];
-            }
-        }
-        __syncthreads();
-        prefix |= s_digit << shift;
-        left = s_left;
-        __syncthreads();
+        for (int r = 0; r < R; ++r)
+            key[r] = r < n_r ? key_of(r, key[r]) : kNoRow;
     }
-    // `left` rows with key == prefix stay, the lowest ones; all with key > prefix
-    const int seg = (rq.n + kSelThreads - 1) / kSelThreads * 32;   // rows of a warp
-    const int r0 = warp * seg, r1 = min(rq.n, r0 + seg);
-    auto cls = [&](int i, bool &gt, bool &eq) {
-        gt = eq = false;
-        if (i >= r1)
-            return;
-        if (i < lo || i >= hi) {
-            gt = true;
-        } else if (k > 0) {
-            const uint32_t key = weight_key(w[i]);
-            gt = key > prefix;
-            eq = key == prefix;
+    // f(row, its key) for every row of the thread, in row order (step 8: an eighth of them)
+    auto each = [&](auto &&f) {
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < n_r)
+                    f(row0 + 32 * r, key[r]);
+        } else {
+#pragma unroll 4
+            for (int r = 0; r < n_r; ++r)
+                f(row0 + 32 * r, key_of(r, bits_of(r)));
         }
     };
-    int n_gt = 0, n_eq = 0;
-    for (int i0 = r0; i0 < r1; i0 += 32) {
-        bool gt, eq;
-        cls(i0 + lane, gt, eq);
-        n_gt += __popc(__ballot_sync(0xffffffffu, gt));
-        n_eq += __popc(__ballot_sync(0xffffffffu, eq));
+    auto each8 = [&](auto &&f) {
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int r = 0; r < R; r += 8)
+                if (r < n_r)
+                    f(row0 + 32 * r, key[r]);
+        } else {
+            for (int r = 0; r < n_r; r += 8)
+                f(row0 + 32 * r, key_of(r, bits_of(r)));
+        }
+    };
+    auto clear = [&] {
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2048; i += TH)
+            hist[i] = 0;
+        if (threadIdx.x == 0)
+            s_found[0] = -1;
+        __syncthreads();
+    };
+    auto block_sum_before = [&](int v, int &total) -> int {   // sum over the threads before this one
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += u;
+        }
+        if (lane == 31)
+            s_warp[warp] = incl;
+        __syncthreads();
+        int before = 0;
+        total = 0;
+        for (int x = 0; x < NW; ++x) {
+            before += x < warp ? s_warp[x] : 0;
+            total += s_warp[x];
+        }
+        __syncthreads();
+        return before + incl - v;
+    };
+    // The histogram's digit in which the `rank`-th largest falls (-1: none), from
+    // the largest digit down; thread t holds digits 2047 - BPT t and below.
+    auto find = [&](int above, int total, int rank) -> int {
+        const int d0 = 2047 - BPT * (int)threadIdx.x;
+        int run = above;
+#pragma unroll
+        for (int e = 0; e < BPT; ++e) {
+            const int c = hist[d0 - e];
+            if (run < rank && rank <= run + c) {
+                s_found[0] = d0 - e;
+                s_found[1] = rank - run;
+                s_found[2] = c;
+            }
+            run += c;
+        }
+        __syncthreads();
+        return s_found[0];
+    };
+    auto bins_before = [&](int &total) -> int {
+        int sum = 0;
+#pragma unroll
+        for (int e = 0; e < BPT; ++e)
+            sum += hist[2047 - BPT * (int)threadIdx.x - e];
+        return block_sum_before(sum, total);
+    };
+
+    int n_always = 0;      // of this thread's rows
+    each([&](int, uint32_t x) { n_always += x == kAlways; });
+    uint32_t prefix = 0;   // the threshold's leading digits
+    int left = k;          // how many of the rows with those digits stay
+    bool ranked = false;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        constexpr int kShift[3] = {21, 10, 0};
+        const int shift = kShift[pass], above_bits = pass == 0 ? 31 : kShift[pass == 0 ? 0 : pass - 1];
+        if (k == 0 || ranked)
+            break;
+        int d_lo = 0, d_hi = 2047, above = 0, total = 0;
+        bool whole = true;
+        if (pass == 0 && n_r >= 8) {
+            clear();
+            each8([&](int, uint32_t x) {
+                if (x - 1u < kMaxKey)   // kNanKey .. kMaxKey
+                    atomicAdd(&hist[x >> 21], 1);
+            });
+            __syncthreads();
+            const int before = bins_before(total);
+            // the sample's rank, and six standard deviations on both sides
+            const float est = (float)k * (float)total / (float)(hi - lo), dev = 6.f * sqrtf((float)total) * 0.5f + 2.f;
+            const int r_hi = (int)(est - dev), r_lo = (int)(est + dev);
+            if (r_hi >= 1)
+                d_hi = find(before, total, r_hi);
+            __syncthreads();
+            if (r_lo <= total)
+                d_lo = find(before, total, r_lo);
+            whole = d_lo == 0 && d_hi == 2047;
+        }
+        for (;;) {
+            clear();
+            int n_above = 0;
+            if (pass == 0) {
+                const uint32_t k_lo = max(kNanKey, (uint32_t)d_lo << 21), k_hi = min(kMaxKey, ((uint32_t)d_hi << 21) | 0x1fffffu);
+                each([&](int, uint32_t x) {
+                    n_above += x > k_hi;
+                    if (x - k_lo <= k_hi - k_lo)
+                        atomicAdd(&hist[x >> 21], 1);
+                });
+                n_above -= n_always;
+            } else {
+                each([&](int, uint32_t x) {
+                    if (x != kNoRow && (x >> above_bits) == (prefix >> above_bits))
+                        atomicAdd(&hist[(x >> shift) & 2047], 1);
+                });
+            }
+            __syncthreads();
+            if (!whole) {
+                block_sum_before(n_above, above);
+            }
+            const int before = bins_before(total);
+            if (find(above + before, total, left) >= 0)
+                break;
+            d_lo = 0;   // outside the sample's digits (they are six deviations wide): count all
+            d_hi = 2047;
+            whole = true;
+            above = 0;
+        }
+        prefix |= (uint32_t)s_found[0] << shift;
+        left = s_found[1];
+        const int n_cand = s_found[2];
+        if (n_cand <= kRankMax) {
+            ranked = true;
+            if (threadIdx.x == 0)
+                s_n = 0;
+            __syncthreads();
+            each([&](int i, uint32_t x) {
+                if (x != kNoRow && (x >> shift) == (prefix >> shift)) {
+                    const int c = atomicAdd(&s_n, 1);
+                    if (c < kRankMax)
+                        s_cand[c] = make_uint2(x, (uint32_t)i);
+                }
+            });
+            __syncthreads();
+            for (int c = threadIdx.x; c < n_cand; c += TH) {
+                const uint2 me = s_cand[c];
+                int rank = 0;
+                for (int o = 0; o < n_cand; ++o) {
+                    const uint2 v = s_cand[o];
+                    rank += v.x > me.x || (v.x == me.x && v.y < me.y);
+                }
+                if (rank == left - 1)
+                    s_last = me;
+            }
+            __syncthreads();
+        }
     }
+    // Kept: keys above the threshold (kAlways among them); of the keys equal to it
+    // those up to row s_last.y (ranked), or the `left` lowest rows
+    const uint32_t thr = k == 0 ? kAlways - 1u : ranked ? s_last.x : prefix;
+    const int last_row = ranked ? (int)s_last.y : -1;
+    const bool ties = k > 0 && !ranked;
+    int n_gt = 0, n_eq = 0;
+    each([&](int i, uint32_t x) {
+        n_gt += x > thr || (x == thr && i <= last_row);
+        n_eq += x == thr;
+    });
+    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+    __syncthreads();
     if (lane == 0) {
-        s_gt[warp] = n_gt;
-        s_eq[warp] = n_eq;
+        s_warp[warp] = n_gt;
+        s_eq[warp] = ties ? n_eq : 0;
     }
     __syncthreads();
     int gt_before = 0, eq_before = 0;
     for (int x = 0; x < warp; ++x) {
-        gt_before += s_gt[x];
+        gt_before += s_warp[x];
         eq_before += s_eq[x];
     }
     const unsigned below = (1u << lane) - 1u;
-    for (int i0 = r0; i0 < r1; i0 += 32) {
-        bool gt, eq;
-        cls(i0 + lane, gt, eq);
-        const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-        const int g = gt_before + __popc(bg & below), e = eq_before + __popc(be & below);
-        if (gt || (eq && e < left))
-            kept[g + min(e, left)] = i0 + lane;
-        gt_before += __popc(bg);
-        eq_before += __popc(be);
+    if (!ties) {
+        each([&](int i, uint32_t x) {
+            const bool gt = x > thr || (x == thr && i <= last_row);
+            const unsigned bg = __ballot_sync(0xffffffffu, gt);
+            if (gt)
+                kept[gt_before + __popc(bg & below)] = i;
+            gt_before += __popc(bg);
+        });
+    } else {
+        each([&](int i, uint32_t x) {
+            const bool gt = x > thr, eq = x == thr;
+            const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+            const int g = gt_before + __popc(bg & below), e = eq_before + __popc(be & below);
+            if (gt || (eq && e < left))
+                kept[g + min(e, left)] = i;
+            gt_before += __popc(bg);
+            eq_before += __popc(be);
+        });
     }
 }
 
 // A piece is kEvictChunk kept rows of one unit.  TPR threads a row, thread j
 // holding 16-byte vector j of each row half (so that both halves of a RoPE
-// pair are in one thread).  To another block, every piece is a CTA.  In place,
+// pair are in one thread).  A bf16 key's angles are computed, not read: a moved
+// row's (cos, sin) table row would be 512 bytes beside the 512 of its K and V.
+// The turn delta * w_i / 2 pi is reduced exactly (an fp32 product with the
+// frequency in two words), and sin and cos of the rest are good to 2^-20, far
+// below the bf16 result's 2^-9.  To another block, every piece is a CTA.  In place,
 // a CTA walks its unit's pieces in order: a piece's sources lie at or behind
 // its own rows, so once the piece is read (barrier), writing it only
 // overwrites rows that were read before.
@@ -242,6 +403,16 @@ __global__ void __launch_bounds__(kMoveThreads)
     const float *sw = a.weights + src0;
     float *dw = a.dst_weights ? a.dst_weights + dst0 : nullptr;
     const int j = threadIdx.x % TPR, rr = threadIdx.x / TPR;
+    float f_hi[E], f_lo[E];   // the thread's pairs' frequencies in turns
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float2 f = __ldg(a.rope_turns + rope_pair(a.interleaved, D, E, j, e));
+            f_hi[e] = f.x;
+            f_lo[e] = f.y;
+        }
+    }
+    pdl_wait_prerequisites();   // the kept rows
     for (int c = c_first; c < c_end; ++c) {
         uint4 k[NR][2], v[NR][2];
         int src[NR];
@@ -281,9 +452,15 @@ __global__ void __launch_bounds__(kMoveThreads)
                 float cs[E], sn[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const float2 r = rope_cs(a.rope, H2, delta, rope_pair(a.interleaved, D, E, j, e));
-                    cs[e] = r.x;
-                    sn[e] = r.y;
+                    if constexpr (sizeof(T) == 2) {
+                        const float fd = (float)delta, q = rintf(fd * f_hi[e]);
+                        const float turn = fmaf(fd, f_lo[e], fmaf(fd, f_hi[e], -q));   // in [-1/2, 1/2], to 2^-24
+                        __sincosf(turn * 6.283185307179586f, &sn[e], &cs[e]);
+                    } else {
+                        const float2 r = rope_cs(a.rope, H2, delta, rope_pair(a.interleaved, D, E, j, e));
+                        cs[e] = r.x;
+                        sn[e] = r.y;
+                    }
                 }
                 RowVec<T>::rotate(k[x][0], k[x][1], cs, sn, a.interleaved);
             }
@@ -303,26 +480,55 @@ __global__ void __launch_bounds__(kMoveThreads)
     }
 }
 
-cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, cudaStream_t s)
+cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s)
 {
     const int64_t ctas = (int64_t)a.n_reqs * a.units;
     const int64_t move = a.in_place ? ctas : a.n_chunks;
     if (ctas > 0x7fffffff || move > 0x7fffffff)
         return cudaErrorInvalidValue;
-    k_evict_select<<<(unsigned)ctas, kSelThreads, 0, s>>>(a, rt);
+    // Small CTAs when there are several units per SM (eight resident hide each
+    // other's barriers), large ones when a unit has an SM to itself.
+    const bool small = a.max_n <= 24 * 256 && ctas >= 4 * (int64_t)n_sms;
+    const int threads = small ? 256 : 1024, r = (a.max_n + threads - 1) / threads;
+    auto select = small ? (r <= 8 ? k_evict_select<256, 8> : k_evict_select<256, 24>)
+                        : r <= 4 ? k_evict_select<1024, 4> : r <= 12 ? k_evict_select<1024, 12>
+                        : r <= 36 ? k_evict_select<1024, 36> : k_evict_select<1024, 0>;
+    select<<<(unsigned)ctas, threads, 0, s>>>(a, rt);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    if (dtype == KVR_DTYPE_BF16 && head_dim == 128)
-        k_evict_move<__nv_bfloat16, 128><<<(unsigned)move, kMoveThreads, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_BF16 && head_dim == 64)
-        k_evict_move<__nv_bfloat16, 64><<<(unsigned)move, kMoveThreads, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_FP32 && head_dim == 128)
-        k_evict_move<float, 128><<<(unsigned)move, kMoveThreads, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_FP32 && head_dim == 64)
-        k_evict_move<float, 64><<<(unsigned)move, kMoveThreads, 0, s>>>(a, rt);
+    void (*k)(const EvictArgs, const EvictTable) = nullptr;
+    if (dtype == KVR_DTYPE_BF16)
+        k = head_dim == 128 ? k_evict_move<__nv_bfloat16, 128> : head_dim == 64 ? k_evict_move<__nv_bfloat16, 64> : nullptr;
     else
+        k = head_dim == 128 ? k_evict_move<float, 128> : head_dim == 64 ? k_evict_move<float, 64> : nullptr;
+    if (!k)
         return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)move);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a, rt);
+}
+
+// w_i / 2 pi in two floats (value and what it leaves), pairs 0 .. half - 1.
+__global__ void k_rope_turns(float2 *turns, int half, double theta)
+{
+    const int i = threadIdx.x;
+    if (i < half) {
+        const double f = pow(theta, -(double)i / (double)half) / 6.283185307179586476925286766559;
+        turns[i] = make_float2((float)f, (float)(f - (double)(float)f));
+    }
+}
+
+cudaError_t launch_rope_turns(float2 *turns, int head_dim, double theta, cudaStream_t s)
+{
+    k_rope_turns<<<1, 64, 0, s>>>(turns, head_dim / 2, theta);
     return cudaGetLastError();
 }
 

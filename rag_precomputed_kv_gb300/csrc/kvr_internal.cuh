@@ -364,6 +364,7 @@ struct EvictTable {
 struct EvictArgs {
     const DevEvict *reqs;       // NULL: the EvictTable parameter
     const float2 *rope;
+    const float2 *rope_turns;   // w_i / 2 pi in two words
     const float *weights;
     const void *cache_k, *cache_v;
     void *dst_k, *dst_v;
@@ -462,7 +463,8 @@ cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dt
 cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const void *tmap_k, int n_sms, cudaStream_t s);
 // Rows of one piece of the eviction's move kernel.
 constexpr int kEvictChunk = 64;
-cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_rope_turns(float2 *turns, int head_dim, double theta, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s);
 // Whether `n_sms` CTAs of the attention kernel (either variant) can be
 // resident at once as two-CTA clusters.
 bool attention_tc_pairs_fit(int n_sms);
