@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvr_internal.cuh"
 
@@ -96,10 +97,14 @@ struct RowVec<float> {
 // and then only the rows in the digits that the k-th largest can lie in.
 // Warp w owns rows [32 R' w, 32 R' (w + 1)), R' = ceil(n / TH); it counts what it
 // keeps and writes its rows behind the warps before it.  The rows' keys are read
-// once, R per thread in registers; with R = 0 every pass reads them again.
+// once, into shared memory (kept in registers, the passes over them were
+// unrolled code that runs once, at the speed of instruction fetches: 65 us
+// against 33 for 256 units of 33,504 rows); a unit of more rows than fit there
+// reads them in every pass.
 constexpr int kRankMax = 256;
+constexpr int kSelSmemRows = 48 * 1024;   // 192 KB
 
-template <int TH, int R>
+template <int TH, bool kSmem>
 __global__ void __launch_bounds__(TH, 1)
     k_evict_select(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
 {
@@ -134,39 +139,29 @@ __global__ void __launch_bounds__(TH, 1)
         const int i = row0 + 32 * r;
         return i >= rq.n ? kNoRow : i < lo || i >= hi ? kAlways : weight_key(bits);
     };
-    uint32_t key[R > 0 ? R : 1];
-    if constexpr (R > 0) {
+    extern __shared__ uint32_t keys[];   // [warp][R'][lane]
+    uint32_t *mine = keys + row0;
+    if constexpr (kSmem) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < n_r; r0 += 8) {   // eight loads in flight
+            uint32_t u[8];
 #pragma unroll
-        for (int r = 0; r < R; ++r)   // all loads before the first use
-            key[r] = r < n_r ? bits_of(r) : 0u;
+            for (int r = 0; r < 8; ++r)
+                u[r] = r0 + r < n_r ? bits_of(r0 + r) : 0u;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            key[r] = r < n_r ? key_of(r, key[r]) : kNoRow;
+            for (int r = 0; r < 8; ++r)
+                if (r0 + r < n_r)
+                    mine[32 * (r0 + r)] = key_of(r0 + r, u[r]);
+        }
     }
-    // f(row, its key) for every row of the thread, in row order (step 8: an eighth of them)
-    auto each = [&](auto &&f) {
-        if constexpr (R > 0) {
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < n_r)
-                    f(row0 + 32 * r, key[r]);
-        } else {
+    // f(row, its key) for every row of the thread, in row order (or every eighth)
+    auto each_n = [&](int step, auto &&f) {
 #pragma unroll 4
-            for (int r = 0; r < n_r; ++r)
-                f(row0 + 32 * r, key_of(r, bits_of(r)));
-        }
+        for (int r = 0; r < n_r; r += step)
+            f(row0 + 32 * r, kSmem ? mine[32 * r] : key_of(r, bits_of(r)));
     };
-    auto each8 = [&](auto &&f) {
-        if constexpr (R > 0) {
-#pragma unroll
-            for (int r = 0; r < R; r += 8)
-                if (r < n_r)
-                    f(row0 + 32 * r, key[r]);
-        } else {
-            for (int r = 0; r < n_r; r += 8)
-                f(row0 + 32 * r, key_of(r, bits_of(r)));
-        }
-    };
+    auto each = [&](auto &&f) { each_n(1, f); };
+    auto each8 = [&](auto &&f) { each_n(8, f); };
     auto clear = [&] {
         __syncthreads();
         for (int i = threadIdx.x; i < 2048; i += TH)
@@ -489,12 +484,24 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
     // Small CTAs when there are several units per SM (eight resident hide each
     // other's barriers), large ones when a unit has an SM to itself.
     const bool small = a.max_n <= 24 * 256 && ctas >= 4 * (int64_t)n_sms;
-    const int threads = small ? 256 : 1024, r = (a.max_n + threads - 1) / threads;
-    auto select = small ? (r <= 8 ? k_evict_select<256, 8> : k_evict_select<256, 24>)
-                        : r <= 4 ? k_evict_select<1024, 4> : r <= 12 ? k_evict_select<1024, 12>
-                        : r <= 36 ? k_evict_select<1024, 36> : k_evict_select<1024, 0>;
-    select<<<(unsigned)ctas, threads, 0, s>>>(a, rt);
-    cudaError_t e = cudaGetLastError();
+    const int threads = small ? 256 : 1024;
+    const int rows = (a.max_n + threads - 1) / threads * threads;   // of keys in shared memory
+    const bool smem = rows <= kSelSmemRows;
+    auto select = small ? k_evict_select<256, true> : smem ? k_evict_select<1024, true> : k_evict_select<1024, false>;
+    static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(k_evict_select<1024, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemRows * 4)) !=
+            cudaSuccess)
+            return e;
+        if (dev < 64)
+            attr_set[dev].store(true, std::memory_order_release);
+    }
+    select<<<(unsigned)ctas, threads, smem ? rows * 4 : 0, s>>>(a, rt);
+    e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     void (*k)(const EvictArgs, const EvictTable) = nullptr;
