@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kWThreads)
 #pragma unroll
             for (int r = 0; r < kWRows; ++r)
                 s[r] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
             for (int d = 0; d < D; d += E) {
                 float f[E];
                 unpack16<T>(*reinterpret_cast<const uint4 *>(kp + (int64_t)j * D + d), f);
@@ -114,14 +114,15 @@ __global__ void __launch_bounds__(kWThreads)
             for (int r = 0; r < kWRows; ++r)
                 s[r] = (r >= r_min && r < nr) ? s[r] * a.scale_log2 : -INFINITY;
         };
-        float m[kWRows], ls[kWRows];
+        // a cache of at most one key a thread keeps its scores between the passes
+        const bool one = n <= kWThreads;
+        float s[kWRows], m[kWRows], ls[kWRows];
 #pragma unroll
         for (int r = 0; r < kWRows; ++r) {
             m[r] = -INFINITY;
             ls[r] = 0.f;
         }
         for (int j = threadIdx.x; j < n; j += kWThreads) {
-            float s[kWRows];
             scores(j, s);
 #pragma unroll
             for (int r = 0; r < kWRows; ++r) {
@@ -163,8 +164,9 @@ __global__ void __launch_bounds__(kWThreads)
         }
         __syncthreads();
         for (int j = threadIdx.x; j < n; j += kWThreads) {
-            float s[kWRows], sum = 0.f;
-            scores(j, s);
+            float sum = 0.f;
+            if (!one)
+                scores(j, s);
 #pragma unroll
             for (int r = 0; r < kWRows; ++r)
                 if (s[r] != -INFINITY)

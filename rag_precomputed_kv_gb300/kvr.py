@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional, Sequence
 
 import numpy as np
@@ -126,10 +127,21 @@ def _i64(a) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=np.int64))
 
 
-def _sized(name: str, a: np.ndarray, n: int) -> np.ndarray:
-    if a.ndim != 1 or len(a) != n:
-        raise ValueError(f"{name} must hold {n} values, got shape {a.shape}")
-    return a
+def _ints(name: str, a, code: str, n: Optional[int] = None):
+    """``a`` as a C array of int32 ("i") or int64 ("q"): (keep-alive, address,
+    length); ``n``: the length it must have.  Lists take the short way, which
+    costs a tenth of numpy's."""
+    if isinstance(a, (list, tuple)):
+        c = array(code, a)
+        addr, m = c.buffer_info()
+    else:
+        c = np.ascontiguousarray(a, dtype=np.int32 if code == "i" else np.int64)
+        if c.ndim != 1:
+            raise ValueError(f"{name} must be one-dimensional, got shape {c.shape}")
+        addr, m = c.ctypes.data, len(c)
+    if n is not None and m != n:
+        raise ValueError(f"{name} must hold {n} values, got {m}")
+    return c, addr, m
 
 
 def _check_f32(t, name: str):
@@ -139,7 +151,7 @@ def _check_f32(t, name: str):
 
 
 def _np_ptr(a: Optional[np.ndarray]):
-    return None if a is None else a.ctypes.data_as(ctypes.c_void_p)
+    return None if a is None else a.ctypes.data
 
 
 def _span_args(span_offsets, spans, cache_offsets, locals_):
@@ -276,15 +288,14 @@ class Pool:
         each over its group's shared prefix block (``prefix_k``, ``prefix_v``,
         read only) and the requests' own rows, to which the query K/V are
         appended; writes ``out``."""
-        go = _i32(group_offsets)
-        n, batch = len(go) - 1, int(go[-1])
-        po, pl = _sized("prefix_offsets", _i64(prefix_offsets), n + 1), _sized("prefix_len", _i32(prefix_len), n)
-        co, ol = _sized("cache_offsets", _i64(cache_offsets), batch + 1), _sized("own_len", _i32(own_len), batch)
-        qo = _sized("q_offsets", _i32(q_offsets), batch + 1)
-        _raise(load().kvr_shared_query_attention(self._h, n, _np_ptr(go), _np_ptr(po), _np_ptr(pl),
-                                                 _ptr(prefix_k), _ptr(prefix_v), _np_ptr(co), _np_ptr(ol), _np_ptr(qo),
-                                                 _ptr(q), _ptr(kq), _ptr(vq), _ptr(cache_k), _ptr(cache_v), _ptr(out),
-                                                 float(softmax_scale), _stream_ptr(stream)))
+        go = _ints("group_offsets", group_offsets, "i")
+        n, batch = go[2] - 1, int(group_offsets[-1])
+        po, pl = _ints("prefix_offsets", prefix_offsets, "q", n + 1), _ints("prefix_len", prefix_len, "i", n)
+        co, ol = _ints("cache_offsets", cache_offsets, "q", batch + 1), _ints("own_len", own_len, "i", batch)
+        qo = _ints("q_offsets", q_offsets, "i", batch + 1)
+        _raise(load().kvr_shared_query_attention(self._h, n, go[1], po[1], pl[1], _ptr(prefix_k), _ptr(prefix_v), co[1],
+                                                 ol[1], qo[1], _ptr(q), _ptr(kq), _ptr(vq), _ptr(cache_k), _ptr(cache_v),
+                                                 _ptr(out), float(softmax_scale), _stream_ptr(stream)))
 
     def key_weights(self, cache_offsets, prefix_len, q_offsets, q, cache_k, weights, softmax_scale: float = 0.0,
                     accumulate: bool = False, stream=None):
@@ -292,12 +303,12 @@ class Pool:
         the query tokens (fp32, one value per cache row), written to
         ``weights`` or, with ``accumulate``, added to it."""
         _check_f32(weights, "weights")
-        qo = _i32(q_offsets)
-        n = len(qo) - 1
-        co, pl = _sized("cache_offsets", _i64(cache_offsets), n + 1), _sized("prefix_len", _i32(prefix_len), n)
-        _raise(load().kvr_key_weights(self._h, n, _np_ptr(co), _np_ptr(pl), _np_ptr(qo), _ptr(q),
-                                      _ptr(cache_k), _ptr(weights), float(softmax_scale),
-                                      KVR_WEIGHTS_ACCUMULATE if accumulate else 0, _stream_ptr(stream)))
+        qo = _ints("q_offsets", q_offsets, "i")
+        n = qo[2] - 1
+        co, pl = _ints("cache_offsets", cache_offsets, "q", n + 1), _ints("prefix_len", prefix_len, "i", n)
+        _raise(load().kvr_key_weights(self._h, n, co[1], pl[1], qo[1], _ptr(q), _ptr(cache_k), _ptr(weights),
+                                      float(softmax_scale), KVR_WEIGHTS_ACCUMULATE if accumulate else 0,
+                                      _stream_ptr(stream)))
 
     def evict(self, cache_offsets, kv_len, keep, weights, cache_k, cache_v, kept, dst_offsets=None, dst_k=None,
               dst_v=None, dst_weights=None, n_first: int = 0, n_recent: int = 0, keep_rotation: bool = False,
@@ -319,15 +330,14 @@ class Pool:
             _check_f32(dst_weights, "dst_weights")
         if kept is not None and (kept.dtype != torch.int32 or not kept.is_contiguous()):
             raise ValueError("kept must be a contiguous int32 tensor")
-        kl = _i32(kv_len)
-        n = len(kl)
-        kp, co = _sized("keep", _i32(keep), n), _sized("cache_offsets", _i64(cache_offsets), n + 1)
-        do = _sized("dst_offsets", _i64(dst_offsets), n + 1)
-        _raise(load().kvr_evict(self._h, n, _np_ptr(co), _np_ptr(kl), _np_ptr(kp), int(n_first), int(n_recent),
-                                _ptr(weights), _ptr(cache_k), _ptr(cache_v), _np_ptr(do), _ptr(dst_k), _ptr(dst_v),
-                                _ptr(dst_weights), _ptr(kept), KVR_EVICT_KEEP_ROTATION if keep_rotation else 0,
-                                _stream_ptr(stream)))
-        return np.minimum(kl, kp)
+        kl = _ints("kv_len", kv_len, "i")
+        n = kl[2]
+        kp, co = _ints("keep", keep, "i", n), _ints("cache_offsets", cache_offsets, "q", n + 1)
+        do = _ints("dst_offsets", dst_offsets, "q", n + 1)
+        _raise(load().kvr_evict(self._h, n, co[1], kl[1], kp[1], int(n_first), int(n_recent), _ptr(weights), _ptr(cache_k),
+                                _ptr(cache_v), do[1], _ptr(dst_k), _ptr(dst_v), _ptr(dst_weights), _ptr(kept),
+                                KVR_EVICT_KEEP_ROTATION if keep_rotation else 0, _stream_ptr(stream)))
+        return np.minimum(kl[0], kp[0], dtype=np.int32)
 
     @property
     def attention_path(self) -> int:
