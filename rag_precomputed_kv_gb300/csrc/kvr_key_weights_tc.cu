@@ -14,11 +14,12 @@
 // the queries' denominators cross lanes, once per CTA.
 //
 // Every weight needs its rows' denominators over all keys before it can be
-// summed.  So that K is read once, the scores stay in TMEM in between: a CTA
-// holds 256 columns, 256 / NQ tiles, and the CTAs of a cluster split a unit's
-// key tiles and exchange their rows' (max, sum) through distributed shared
-// memory.  Tiles beyond what TMEM holds are processed first, for their
-// statistics only, and loaded again at the end.
+// summed.  So that K is read once, the scores stay in TMEM in between: of a
+// CTA's 256 columns 64 take the products, and 192 hold the scores of 192 / NC
+// tiles (NC: the query rows, padded to 4, 8, 16 or 32), and the CTAs of a
+// cluster split a unit's key tiles and exchange their rows' (max, sum) through
+// distributed shared memory.  Tiles beyond what TMEM holds are processed first,
+// for their statistics only, and loaded again at the end.
 //
 // Rotated queries are split into three bf16 terms (8 + 8 + 8 bits: all of the
 // fp32 rotation's), three accumulating MMAs, so that the weights are fp32
@@ -48,21 +49,24 @@ constexpr int kWtD = 128;
 constexpr int kWtTile = 128;                 // keys per tile
 constexpr int kWtPanel = kWtTile * 64 * 2;   // 16 KB: 128 keys x 64 dims
 constexpr int kWtTmemCols = 256;
-constexpr int kWtMaxCluster = 8;
+constexpr int kWtMaxCluster = 8;   // (16 CTAs, not portable: 1.31 ms against 1.03 on two 33k-token caches)
 // a row that has seen no key yet: finite, so that the first score is far above
 // it and sets the reference, and a masked -inf stays -inf
 constexpr float kWtUnset = -1e30f;
 constexpr float kWtHeadroom = 60.f;          // log2 units above the reference before it moves
 
-template <int NQ>
+// NQ: columns of the S^T product (query rows, padded); NC: columns of them that
+// are kept of a tile (4, 8, 16 or 32: query rows padded less).
+template <int NQ, int NC>
 struct WtCfg {
-    static constexpr int kSlots = NQ == 16 ? 6 : NQ == 32 ? 5 : 3;   // K panels in flight
-    static constexpr int kKept = kWtTmemCols / NQ;                   // tiles whose scores stay in TMEM
+    static constexpr int kSlots = NQ == 16 ? 6 : 5;                  // K panels in flight
+    static constexpr int kStages = 64 / NQ;                          // products in TMEM that wait for pass 1
+    static constexpr int kKept = (kWtTmemCols - 64) / NC;            // tiles whose scores stay in TMEM behind them
     static constexpr int kQTerm = NQ * kWtD * 2;                     // one bf16 term of the query rows
     static constexpr int kOffRing = 3 * kQTerm;
     static constexpr int kOffBar = kOffRing + kSlots * kWtPanel;
-    // full[slots], empty[slots], s_full[kept], s_free[kept], q_full, q_empty, peers, drain
-    static constexpr int kNumBars = 2 * kSlots + 2 * kKept + 4;
+    // full[slots], empty[slots], s_full[stages], s_free[stages], q_full, q_empty, peers, drain
+    static constexpr int kNumBars = 2 * kSlots + 2 * kStages + 4;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // TMEM address, abort flag
     static constexpr int kOffRef = (kOffMisc + 8 + 15) & ~15;        // [4][NQ] reference per warp
     static constexpr int kOffStat = kOffRef + 4 * NQ * 4;            // [4][NQ] (reference, sum) per warp
@@ -198,20 +202,19 @@ __device__ __forceinline__ bool wait_peers(uint32_t bar, uint32_t parity, volati
 
 }  // namespace
 
-template <int NQ>
+template <int NQ, int NC>
 __global__ void __launch_bounds__(kWtThreads, 2)
     k_key_weights_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ WeightsArgs a,
                      const __grid_constant__ ReqTable rt, const int n_cluster)
 {
-    using C = WtCfg<NQ>;
-    constexpr int BL = NQ < 32 ? NQ : 32;   // columns per TMEM read
+    using C = WtCfg<NQ, NC>;
     constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NQ >> 3) << 17) |
                                 ((uint32_t)(kWtTile >> 4) << 24);
     extern __shared__ __align__(1024) uint8_t wt_smem[];
     const uint32_t sbase = smem_u32(wt_smem);
     auto bar = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
-    constexpr int bFull = 0, bEmpty = C::kSlots, bSFull = 2 * C::kSlots, bSFree = bSFull + C::kKept,
-                  bQFull = bSFree + C::kKept, bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bQFull + 3;
+    constexpr int bFull = 0, bEmpty = C::kSlots, bSFull = 2 * C::kSlots, bSFree = bSFull + C::kStages,
+                  bQFull = bSFree + C::kStages, bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bQFull + 3;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(wt_smem + C::kOffMisc + 4);
     float *s_ref = reinterpret_cast<float *>(wt_smem + C::kOffRef);
     float2 *s_stat = reinterpret_cast<float2 *>(wt_smem + C::kOffStat);
@@ -223,8 +226,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
-            const bool wg = (i >= bSFree && i < bSFree + C::kKept) || i == bQFull;
-            mbar_init(bar(i), wg ? 128u : i == bPeers ? (uint32_t)(n_cluster * NQ) : 1u);
+            const bool wg = (i >= bSFree && i < bSFree + C::kStages) || i == bQFull;
+            mbar_init(bar(i), wg ? 128u : i == bPeers ? (uint32_t)(n_cluster * NC) : 1u);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -251,7 +254,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     const int T = t_hi - t_lo;                               // this CTA's key tiles
     const int n_redo = max(0, T - C::kKept);                 // loaded a second time, for each row block
     const int64_t blk = rq.cache_row0 + (int64_t)lh * rq.cap;
-    // job i of a row block: tiles T-1 .. 0 for the statistics, then kKept .. T-1 again
+    // job i of a row block: tiles T-1 .. 0 for the statistics, then kKept .. T-1
+    // again; its product goes to stage (job of the CTA) % kStages
     auto job_tile = [&](int i) { return i < T ? T - 1 - i : C::kKept + (i - T); };
     const int n_jobs = T + n_redo;
 
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
         const float sc = a.scale_log2;
         float *wp = a.weights + blk;
-        uint32_t full_par = 0;   // parity of the next wait on s_full[slot]
+        int job = 0;
         bool ok = true;
         if (m_rows == 0 && !a.accumulate)   // a sum over no queries
             for (int j = t_lo * kWtTile + (int)threadIdx.x; j < min(n, t_hi * kWtTile); j += 128)
@@ -276,91 +280,110 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
 
-            // scores of TMEM slot `slot`, columns 32 q .., in log2 units; keys that a
-            // row does not see are -inf.  lim: the first column that sees this key.
-            auto load = [&](int slot, int q, float *s) {
-                const uint32_t at = lane_base + (uint32_t)(slot * NQ + q * 32);
-                if constexpr (BL == 16)
+            // NC columns at a TMEM address; keys that a row does not see are -inf.
+            // lim: the first column that sees this key.
+            auto load = [&](uint32_t at, float *s) {
+                if constexpr (NC == 4)
+                    tmem_ld4(at, s);
+                else if constexpr (NC == 8)
+                    tmem_ld8(at, s);
+                else if constexpr (NC == 16)
                     tmem_ld16(at, s);
                 else
                     tmem_ld32(at, s);
                 tmem_wait_ld();
             };
-            auto mask = [&](int lim, int q, float *s) {
-#pragma unroll
-                for (int c = 0; c < BL; ++c)
-                    s[c] = q * 32 + c >= lim ? s[c] : -INFINITY;
+            auto keep = [&](uint32_t at, const float *s) {
+                if constexpr (NC == 4)
+                    tmem_st4(at, s);
+                else if constexpr (NC == 8)
+                    tmem_st8(at, s);
+                else if constexpr (NC == 16)
+                    tmem_st16(at, reinterpret_cast<const uint32_t *>(s));
+                else
+                    tmem_st32(at, s);
             };
+            auto job_at = [&](int jb) { return lane_base + (uint32_t)((jb % C::kStages) * NQ); };
+            auto wait_job = [&](int jb) -> bool {
+                if (!mbar_wait(bar(bSFull + jb % C::kStages), (uint32_t)(jb / C::kStages) & 1, abort_flag))
+                    return false;
+                tc_fence_after();
+                return true;
+            };
+            auto free_job = [&](int jb) {
+                tc_fence_before();
+                mbar_arrive(bar(bSFree + jb % C::kStages));
+            };
+            auto mask = [&](int lim, float *s) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    s[c] = c >= lim ? s[c] : -INFINITY;
+            };
+            // scores kept of tile t
+            auto kept_at = [&](int t) { return lane_base + (uint32_t)(64 + t * NC); };
 
             // ---- pass 1: each row's reference and sum over this warp's keys ----
-            float ls[NQ];
+            float ls[NC];
 #pragma unroll
-            for (int c = 0; c < NQ; ++c)
+            for (int c = 0; c < NC; ++c)
                 ls[c] = 0.f;
             float *ref = s_ref + warp * NQ;
-            for (int c = lane; c < NQ; c += 32)
-                ref[c] = kWtUnset;
+            if (lane < NC)
+                ref[lane] = kWtUnset;
             __syncwarp();
-            for (int i = 0; i < T; ++i) {
-                const int t = T - 1 - i, slot = t % C::kKept;
-                if (!mbar_wait(bar(bSFull + slot), (full_par >> slot) & 1, abort_flag)) {
+            for (int i = 0; i < T; ++i, ++job) {
+                const int t = T - 1 - i;
+                if (!wait_job(job)) {
                     ok = false;
                     break;
                 }
-                full_par ^= 1u << slot;
-                tc_fence_after();
                 const int j0 = (t_lo + t) * kWtTile, j = j0 + (int)threadIdx.x;
                 const bool edge = j0 + kWtTile > rq.prefix + 1;   // some key is not seen by every row
-                const int lim = !edge ? 0 : j >= n ? NQ : (j - rq.prefix) * G - r0;
+                float s[NC];
+                load(job_at(job), s);
+                if (t < C::kKept)   // uniform
+                    keep(kept_at(t), s);
+                free_job(job);
+                if (edge)
+                    mask(j >= n ? NC : (j - rq.prefix) * G - r0, s);
+                float mx = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < NQ / BL; ++q) {
-                    float s[BL];
-                    load(slot, q, s);
-                    if (edge)
-                        mask(lim, q, s);
-                    float mx = -INFINITY;
+                for (int c = 0; c < NC; ++c) {
+                    s[c] *= sc;
+                    mx = fmaxf(mx, s[c] - ref[c]);
+                }
+                if (__any_sync(0xffffffffu, mx > kWtHeadroom)) {
+                    // a first key, or one far above the reference: the rows'
+                    // references move up to this tile's maxima
 #pragma unroll
-                    for (int c = 0; c < BL; ++c) {
-                        s[c] *= sc;
-                        mx = fmaxf(mx, s[c] - ref[q * 32 + c]);
-                    }
-                    if (__any_sync(0xffffffffu, mx > kWtHeadroom)) {
-                        // a first key, or one far above the reference: the rows'
-                        // references move up to this tile's maxima
-#pragma unroll
-                        for (int c = 0; c < BL; ++c) {
-                            const float old = ref[q * 32 + c];
-                            const float m = key_f(__reduce_max_sync(0xffffffffu, f_key(s[c])));
-                            if (m > old) {
-                                ls[q * 32 + c] = old == kWtUnset ? 0.f : ls[q * 32 + c] * ex2(old - m);
-                                __syncwarp();
-                                if (lane == 0)
-                                    ref[q * 32 + c] = m;
-                                __syncwarp();
-                            }
+                    for (int c = 0; c < NC; ++c) {
+                        const float old = ref[c];
+                        const float m = key_f(__reduce_max_sync(0xffffffffu, f_key(s[c])));
+                        if (m > old) {   // the same in all lanes
+                            ls[c] = old == kWtUnset ? 0.f : ls[c] * ex2(old - m);
+                            __syncwarp();
+                            if (lane == 0)
+                                ref[c] = m;
+                            __syncwarp();
                         }
                     }
+                }
 #pragma unroll
-                    for (int c = 0; c < BL; ++c)
-                        ls[q * 32 + c] += ex2(s[c] - ref[q * 32 + c]);
-                }
-                if (t >= C::kKept) {
-                    tc_fence_before();
-                    mbar_arrive(bar(bSFree + slot));
-                }
+                for (int c = 0; c < NC; ++c)
+                    ls[c] += ex2(s[c] - ref[c]);
             }
             if (!ok)
                 break;
-#pragma unroll
-            for (int q = 0; q < NQ / BL; ++q) {
-                const float r = warp_sums<BL>(ls + q * 32, lane);
-                const int c = q * 32 + warp_sums_index<BL>(lane);
+            tmem_wait_st();
+            {
+                const float r = warp_sums<NC>(ls, lane);
+                const int c = warp_sums_index<NC>(lane);
                 s_stat[warp * NQ + c] = make_float2(ref[c], r);
             }
             softmax_sync();
             // ---- the CTA's (max, sum) of row c to every CTA of the cluster ----
             const uint32_t peer = sbase + C::kOffPeer + (uint32_t)((rb & 1) * kWtMaxCluster * NQ * 8);
-            if (threadIdx.x < NQ) {
+            if (threadIdx.x < NC) {
                 const int c = threadIdx.x;
                 float M = kWtUnset, L = 0.f;
 #pragma unroll
@@ -402,36 +425,26 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             // ---- pass 2: the weights of this thread's keys ----
             const bool add = rb > 0 || a.accumulate;
             for (int t = 0; t < T; ++t) {
-                const int slot = t % C::kKept;
                 const int j0 = (t_lo + t) * kWtTile, j = j0 + (int)threadIdx.x;
-                float w = add && j < n ? wp[j] : 0.f;
-                if (t >= C::kKept) {
-                    if (!mbar_wait(bar(bSFull + slot), (full_par >> slot) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    full_par ^= 1u << slot;
-                    tc_fence_after();
+                const float w = add && j < n ? wp[j] : 0.f;
+                const bool redo = t >= C::kKept;
+                if (redo && !wait_job(job)) {
+                    ok = false;
+                    break;
                 }
-                const bool edge = j0 + kWtTile > rq.prefix + 1;
-                const int lim = !edge ? 0 : j >= n ? NQ : (j - rq.prefix) * G - r0;
-                float sum = 0.f;
-#pragma unroll
-                for (int q = 0; q < NQ / BL; ++q) {
-                    float s[BL];
-                    load(slot, q, s);
-                    if (edge)
-                        mask(lim, q, s);
-                    float p4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < BL; ++c)
-                        p4[c & 3] += q * 32 + c < nr ? ex2(fmaf(s[c], sc, -s_fin[q * 32 + c])) : 0.f;
-                    sum += (p4[0] + p4[1]) + (p4[2] + p4[3]);
+                float s[NC], p4[4] = {0.f, 0.f, 0.f, 0.f};
+                load(redo ? job_at(job) : kept_at(t), s);
+                if (redo) {
+                    free_job(job);
+                    ++job;
                 }
-                tc_fence_before();
-                mbar_arrive(bar(bSFree + slot));
+                if (j0 + kWtTile > rq.prefix + 1)
+                    mask(j >= n ? NC : (j - rq.prefix) * G - r0, s);
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    p4[c & 3] += c < nr ? ex2(fmaf(s[c], sc, -s_fin[c])) : 0.f;
                 if (j < n)
-                    wp[j] = w + sum;
+                    wp[j] = w + ((p4[0] + p4[1]) + (p4[2] + p4[3]));
             }
         }
         if (!ok)
@@ -463,24 +476,19 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         const uint32_t lead = elect_one();
         const uint64_t d0 = sdesc(sbase, 16, 1024);
         const uint32_t lo = (uint32_t)d0, hi = (uint32_t)(d0 >> 32);
-        uint32_t used = 0, free_par = 0;   // per score slot
         bool ok = true;
-        int k = 0;
+        int k = 0, job = 0;
         for (int rb = 0; rb < n_rb && ok; ++rb) {
             if (!mbar_wait(bar(bQFull), (uint32_t)rb & 1, abort_flag)) {
                 ok = false;
                 break;
             }
-            for (int i = 0; i < n_jobs && ok; ++i) {
-                const int slot = job_tile(i) % C::kKept;
-                if ((used >> slot) & 1) {
-                    if (!mbar_wait(bar(bSFree + slot), (free_par >> slot) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    free_par ^= 1u << slot;
+            for (int i = 0; i < n_jobs && ok; ++i, ++job) {
+                const int stage = job % C::kStages;
+                if (job >= C::kStages && !mbar_wait(bar(bSFree + stage), (uint32_t)(job / C::kStages - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
                 }
-                used |= 1u << slot;
                 for (int p = 0; p < 2; ++p, ++k) {
                     const int s = k % C::kSlots;
                     if (!mbar_wait(bar(bFull + s), (uint32_t)(k / C::kSlots) & 1, abort_flag)) {
@@ -494,13 +502,13 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                         const uint32_t qb = lo + ((uint32_t)(term * C::kQTerm + p * (C::kQTerm / 2)) >> 4);
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            mma_ss(lead, tmem + (uint32_t)(slot * NQ), desc_with_lo(ka + 2 * x, hi), desc_with_lo(qb + 2 * x, hi),
+                            mma_ss(lead, tmem + (uint32_t)(stage * NQ), desc_with_lo(ka + 2 * x, hi), desc_with_lo(qb + 2 * x, hi),
                                    kIdesc, p > 0 || term > 0 || x > 0);
                     }
                     umma_commit(lead, bar(bEmpty + s));
                 }
                 if (ok)
-                    umma_commit(lead, bar(bSFull + slot));
+                    umma_commit(lead, bar(bSFull + stage));
             }
             umma_commit(lead, bar(bQEmpty));
         }
@@ -533,6 +541,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
 // fill the SMs.
 namespace {
 constexpr int kWwSlots = 3;
+constexpr int kWwMaxCluster = 8;
 constexpr int kWwQTerm = 128 * kWtD * 2;
 constexpr int kWwOffRing = 2 * kWwQTerm;
 constexpr int kWwOffBar = kWwOffRing + kWwSlots * kWtPanel;
@@ -540,8 +549,8 @@ constexpr int kWwNumBars = 2 * kWwSlots + 4 + 4;   // full, empty, s_full[2], s_
 constexpr int kWwOffMisc = kWwOffBar + 8 * kWwNumBars;
 constexpr int kWwOffFin = (kWwOffMisc + 8 + 15) & ~15;         // [128] lse
 constexpr int kWwSmem = kWwOffFin + 128 * 4;
-constexpr int kWwOffPeer = kWwSmem;                            // [2][kWtMaxCluster][128] (max, sum), clusters only
-constexpr int kWwSmemCluster = kWwOffPeer + 2 * kWtMaxCluster * 128 * 8;
+constexpr int kWwOffPeer = kWwSmem;                            // [2][kWwMaxCluster][128] (max, sum), clusters only
+constexpr int kWwSmemCluster = kWwOffPeer + 2 * kWwMaxCluster * 128 * 8;
 static_assert(kWwSmem <= 113 * 1024, "two CTAs per SM");
 }  // namespace
 
@@ -656,7 +665,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 break;
             float M = m, L = lsum;
             if (n_cluster > 1) {
-                const uint32_t peer = sbase + kWwOffPeer + (uint32_t)((rb & 1) * kWtMaxCluster * 128 * 8);
+                const uint32_t peer = sbase + kWwOffPeer + (uint32_t)((rb & 1) * kWwMaxCluster * 128 * 8);
                 for (int x = 0; x < n_cluster; ++x) {
                     const uint32_t dst = mapa_rank(peer + (uint32_t)((rank * 128 + r) * 8), (uint32_t)x);
                     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(m), "f"(lsum) : "memory");
@@ -665,7 +674,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                                  : "memory");
                 }
                 if (wait_peers(bar(bPeers), (uint32_t)rb & 1, abort_flag)) {
-                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + kWwOffPeer) + (rb & 1) * kWtMaxCluster * 128 + r;
+                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + kWwOffPeer) + (rb & 1) * kWwMaxCluster * 128 + r;
                     M = kWtUnset;
                     L = 0.f;
                     for (int x = 0; x < n_cluster; ++x)
@@ -833,19 +842,19 @@ static cudaError_t launch_cluster(void (*k)(const CUtensorMap, const WeightsArgs
     return cudaLaunchKernelEx(&cfg, k, tmk, a, rt, c);
 }
 
-template <int NQ>
+template <int NQ, int NC>
 static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
 {
-    using C = WtCfg<NQ>;
+    using C = WtCfg<NQ, NC>;
     static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(k_key_weights_tc<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) !=
+        if ((e = cudaFuncSetAttribute(k_key_weights_tc<NQ, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) !=
                 cudaSuccess ||
-            (e = cudaFuncSetAttribute(k_key_weights_tc<NQ>, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
+            (e = cudaFuncSetAttribute(k_key_weights_tc<NQ, NC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
             return e;
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
@@ -853,13 +862,14 @@ static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUt
     const int64_t units = (int64_t)a.n_reqs * a.n_layers * a.n_kv_heads;
     const int tiles = (a.max_rows + kWtTile - 1) / kWtTile;
     // as many CTAs as hold the longest request's scores in TMEM; more while the
-    // grid does not fill the SMs and a CTA keeps four tiles
+    // grid stays within two CTAs per SM and a CTA keeps four tiles (one request
+    // of 2,657 rows and 112 units: 28 us with clusters of 2, 34 with 4)
     int c = 1;
-    while (c < kWtMaxCluster && (tiles > c * C::kKept || (units * c < 2 * n_sms && tiles >= 8 * c)))
+    while (c < kWtMaxCluster && (tiles > c * C::kKept || (units * c <= n_sms && tiles >= 8 * c)))
         c *= 2;
     if (units * c > 0x7fffffff)
         return cudaErrorInvalidValue;
-    return launch_cluster(k_key_weights_tc<NQ>, units * c, C::kSmem, c, s, tmk, a, rt);
+    return launch_cluster(k_key_weights_tc<NQ, NC>, units * c, C::kSmem, c, s, tmk, a, rt);
 }
 
 static cudaError_t launch_window(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
@@ -880,7 +890,7 @@ static cudaError_t launch_window(const WeightsArgs &a, const ReqTable &rt, const
     const int64_t units = (int64_t)a.n_reqs * a.n_layers * a.n_kv_heads;
     const int tiles = (a.max_rows + kWtTile - 1) / kWtTile;
     int c = 1;   // split a unit's tiles while the grid leaves SMs idle (one CTA per SM then)
-    while (c < kWtMaxCluster && units * c * 2 <= n_sms && tiles >= 4 * c)
+    while (c < kWwMaxCluster && units * c * 2 <= n_sms && tiles >= 4 * c)
         c *= 2;
     if (units * c > 0x7fffffff)
         return cudaErrorInvalidValue;
@@ -891,10 +901,14 @@ cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const vo
 {
     const CUtensorMap &m = *static_cast<const CUtensorMap *>(tmap_k);
     const int64_t rows = (int64_t)a.max_q_len * (a.n_q_heads / a.n_kv_heads);
+    if (rows <= 4)
+        return launch_nq<16, 4>(a, rt, m, n_sms, s);
+    if (rows <= 8)
+        return launch_nq<16, 8>(a, rt, m, n_sms, s);
     if (rows <= 16)
-        return launch_nq<16>(a, rt, m, n_sms, s);
+        return launch_nq<16, 16>(a, rt, m, n_sms, s);
     if (rows <= 32)
-        return launch_nq<32>(a, rt, m, n_sms, s);
+        return launch_nq<32, 32>(a, rt, m, n_sms, s);
     return launch_window(a, rt, m, n_sms, s);
 }
 

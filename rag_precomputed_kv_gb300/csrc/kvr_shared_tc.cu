@@ -191,6 +191,9 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             w = sg.next;
             const int j0 = sg.jb + (sg.dual ? x : 0), step = sg.dual ? 2 : 1;
             const bool row_ok = (sg.dual ? r : x * 128 + r) < sg.rows;
+            // a warp without rows of its own only keeps the barriers going: what it
+            // leaves in its lanes of P meets its own lanes of O alone
+            const bool idle = (sg.dual ? 0 : x * 128) + (warp & 3) * 32 >= sg.rows;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = j0; j < sg.je; j += step) {
                 if (!mbar_wait(bar(kSbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
@@ -199,6 +202,11 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 }
                 ++s_cnt;
                 tc_fence_after();
+                if (idle) {
+                    tc_fence_before();
+                    mbar_arrive(bar(kSbP + x));
+                    continue;
+                }
                 float s[kSpTile];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -600,32 +608,48 @@ __device__ __forceinline__ bool own_wait(uint32_t bar, uint32_t parity)
     return mbar_try_wait(bar, parity) || mbar_drain(bar, parity);
 }
 
+// What the end of a row tile needs to know of the prefix's partial results of
+// its two rows, looked up ahead of the row tile's work.
+struct RowParts {
+    PartRef pr[2];
+    float2 v0[2];   // (max, sum) of the first partial result
+};
+__device__ __forceinline__ RowParts row_parts(const SharedPrefixArgs &pa, const DevGroup &g, const DevShared &rq, int lh_s,
+                                              int r_first, int m_rows)
+{
+    RowParts p;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        const int r = r_first + 8 * hh;
+        p.pr[hh] = PartRef{0, 0, 0};
+        if (r < m_rows)
+            p.pr[hh] = part_ref(pa, g, lh_s, (rq.q_off - g.q_off) * pa.group + r);
+        p.v0[hh] = p.pr[hh].n > 0 ? part_ml(pa.part, p.pr[hh].slot, p.pr[hh].x0())[p.pr[hh].pr()] : make_float2(-INFINITY, 0.f);
+    }
+    return p;
+}
+
 // The end of a row tile: adds the prefix's partial results (in stretch order) to
 // the warp's own states and writes the rows.  Lane: columns 8n + cq, + 1 of row
 // r_first of the request and of row r_first + 8 (fragment layout); l_run holds
 // the lane's keys only.
-__device__ __forceinline__ void finish_rows(const SharedArgs &a, const SharedPrefixArgs &pa, const DevGroup &g,
+__device__ __forceinline__ void finish_rows(const SharedArgs &a, const SharedPrefixArgs &pa, const RowParts &rp,
                                             const DevShared &rq, int lh_s, int r_first, int m_rows, float (&o)[16][4],
                                             const float *m_run, const float *l_run)
 {
     const int lane = threadIdx.x & 31, cq = (lane & 3) * 2, G = pa.group;
     const int lh = pa.lh_base + lh_s, l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
     float L[2], M[2];
-    PartRef pr[2];
+    const PartRef (&pr)[2] = rp.pr;
+    const float2 (&v0)[2] = rp.v0;
     int n[2], two[2];
-    float2 v0[2];   // (max, sum) of the first partial result
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-        const int r = r_first + 8 * hh;
         L[hh] = l_run[hh];
         L[hh] += __shfl_xor_sync(0xffffffffu, L[hh], 1);
         L[hh] += __shfl_xor_sync(0xffffffffu, L[hh], 2);
-        pr[hh] = PartRef{0, 0, 0};
-        if (r < m_rows)
-            pr[hh] = part_ref(pa, g, lh_s, (rq.q_off - g.q_off) * G + r);
         two[hh] = pr[hh].x1() - pr[hh].x0();
         n[hh] = pr[hh].n << two[hh];
-        v0[hh] = n[hh] > 0 ? part_ml(pa.part, pr[hh].slot, pr[hh].x0())[pr[hh].pr()] : make_float2(-INFINITY, 0.f);
     }
     auto part_state = [&](int hh, int i) -> float2 {
         return i == 0 ? v0[hh] : part_ml(pa.part, pr[hh].slot + (i >> two[hh]), pr[hh].x0() + (i & two[hh]))[pr[hh].pr()];
@@ -888,7 +912,8 @@ __global__ void __launch_bounds__(kOwThreads, 3)
             }
         }
 
-        finish_rows(a, pa, groups[rq.group], rq, lh_s, r0 + ra, r0 + rows, o, m_run, l_run);
+        const RowParts parts = row_parts(pa, groups[rq.group], rq, lh_s, r0 + ra, r0 + rows);
+        finish_rows(a, pa, parts, rq, lh_s, r0 + ra, r0 + rows, o, m_run, l_run);
     }
 }
 
@@ -897,10 +922,10 @@ __global__ void __launch_bounds__(kOwThreads, 3)
 // dependent steps.  So every warp works by itself, on a consecutive stretch of
 // pieces: its lane 0 loads the K and V rows 32 keys at a time, two steps ahead
 // (across pieces), the warp runs S, softmax and P V of a step in registers, adds
-// the prefix's partial results at the end of a piece and writes its rows.  Six
+// the prefix's partial results at the end of a piece and writes its rows.  Seven
 // warps per SM, 32 KB of tiles each.
 namespace {
-constexpr int kOdWarps = 6;
+constexpr int kOdWarps = 7;
 constexpr int kOdThreads = 32 * kOdWarps;
 constexpr int kOdTile = 32;
 constexpr int kOdPanel = kOdTile * 128;           // 32 keys x 64 dims
@@ -1007,6 +1032,11 @@ __global__ void __launch_bounds__(kOdThreads, 1)
             qa[kb][2] = ld2(ra, kb * 16 + cq + 8);
             qa[kb][3] = ld2(rb, kb * 16 + cq + 8);
         }
+        if (!waited) {   // for the prefix's partial results
+            pdl_wait_prerequisites();
+            waited = true;
+        }
+        const RowParts parts = row_parts(pa, groups[rq.group], rq, lh_s, ra, m_rows);
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
         float o[16][4];
 #pragma unroll
@@ -1097,11 +1127,7 @@ __global__ void __launch_bounds__(kOdThreads, 1)
         }
         if (!ok)
             break;
-        if (!waited) {   // the prefix's partial results
-            pdl_wait_prerequisites();
-            waited = true;
-        }
-        finish_rows(a, pa, groups[rq.group], rq, lh_s, ra, m_rows, o, m_run, l_run);
+        finish_rows(a, pa, parts, rq, lh_s, ra, m_rows, o, m_run, l_run);
         __syncwarp();
     }
     if (!ok) {   // nothing is in flight when the CTA leaves
