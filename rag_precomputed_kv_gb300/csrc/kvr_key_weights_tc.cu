@@ -15,16 +15,17 @@
 //
 // Every weight needs its rows' denominators over all keys before it can be
 // summed.  So that K is read once, the scores stay in TMEM in between: of a
-// CTA's 256 columns 64 take the products, and 192 hold the scores of 192 / NC
-// tiles (NC: the query rows, padded to 4, 8, 16 or 32), and the CTAs of a
-// cluster split a unit's key tiles and exchange their rows' (max, sum) through
+// CTA's 256 columns some 64 to 96 take the products, and the others hold the
+// scores of tiles, one column a query row (48 tiles at up to 4 rows, 24 at 8, 10
+// at 16, 5 at 32), and the CTAs of a cluster split a unit's key tiles and exchange their rows' (max, sum) through
 // distributed shared memory.  Tiles beyond what TMEM holds are processed first,
 // for their statistics only, and loaded again at the end.
 //
 // Rotated queries are split into three bf16 terms (8 + 8 + 8 bits: all of the
-// fp32 rotation's), three accumulating MMAs, so that the weights are fp32
-// results; a decode step is bound by the HBM read of K, and a window of 64
-// rows by exp2, so the two extra products cost no time there.
+// fp32 rotation's), so that the weights are fp32 results.  The terms stand side
+// by side on the N side, and their products are added in registers: an MMA this
+// narrow is bound by reading its 128-key operand from shared memory, once for
+// the three.
 //
 // Two CTAs per SM (110 KB of shared memory, 256 TMEM columns each): one loads
 // while the other is in its prologue or exchange.  Warps 0-3 rotate the
@@ -55,24 +56,25 @@ constexpr int kWtMaxCluster = 8;   // (16 CTAs, not portable: 1.31 ms against 1.
 constexpr float kWtUnset = -1e30f;
 constexpr float kWtHeadroom = 60.f;          // log2 units above the reference before it moves
 
-// NQ: columns of the S^T product (query rows, padded); NC: columns of them that
-// are kept of a tile (4, 8, 16 or 32: query rows padded less).
-template <int NQ, int NC>
+// NC: query rows, padded to 4, 8, 16 or 32.
+template <int NC>
 struct WtCfg {
-    static constexpr int kSlots = NQ == 16 ? 6 : 5;                  // K panels in flight
-    static constexpr int kStages = 64 / NQ;                          // products in TMEM that wait for pass 1
-    static constexpr int kKept = (kWtTmemCols - 64) / NC;            // tiles whose scores stay in TMEM behind them
-    static constexpr int kQTerm = NQ * kWtD * 2;                     // one bf16 term of the query rows
-    static constexpr int kOffRing = 3 * kQTerm;
+    static constexpr int kTermRows = NC < 8 ? 8 : NC;                // rows of a query term in the MMA operand
+    static constexpr int NQ = (3 * kTermRows + 15) & ~15;            // columns of the S^T product: the three terms side by side
+    static constexpr int kSlots = NC == 32 ? 5 : 6;                  // K panels in flight
+    static constexpr int kStages = NC == 32 ? 1 : 2;                 // products in TMEM that wait for pass 1
+    static constexpr int kKept = (kWtTmemCols - kStages * NQ) / NC;  // tiles whose scores stay in TMEM behind them
+    static constexpr int kQPanel = NQ * 128;                         // the terms' rows x 64 dims
+    static constexpr int kOffRing = 2 * kQPanel;
     static constexpr int kOffBar = kOffRing + kSlots * kWtPanel;
     // full[slots], empty[slots], s_full[stages], s_free[stages], q_full, q_empty, peers, drain
     static constexpr int kNumBars = 2 * kSlots + 2 * kStages + 4;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // TMEM address, abort flag
-    static constexpr int kOffRef = (kOffMisc + 8 + 15) & ~15;        // [4][NQ] reference per warp
-    static constexpr int kOffStat = kOffRef + 4 * NQ * 4;            // [4][NQ] (reference, sum) per warp
-    static constexpr int kOffFin = kOffStat + 4 * NQ * 8;            // [NQ] lse
-    static constexpr int kOffPeer = kOffFin + NQ * 4;                // [2][kWtMaxCluster][NQ] (max, sum)
-    static constexpr int kSmem = kOffPeer + 2 * kWtMaxCluster * NQ * 8;
+    static constexpr int kOffRef = (kOffMisc + 8 + 15) & ~15;        // [4][NC] reference per warp
+    static constexpr int kOffStat = kOffRef + 4 * NC * 4;            // [4][NC] (reference, sum) per warp
+    static constexpr int kOffFin = kOffStat + 4 * NC * 8;            // [NC] lse
+    static constexpr int kOffPeer = kOffFin + NC * 4;                // [2][kWtMaxCluster][NC] (max, sum)
+    static constexpr int kSmem = kOffPeer + 2 * kWtMaxCluster * NC * 8;
     static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -120,11 +122,11 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;"
 
 // Query rows r0 .. r0 + nr - 1 of a unit, rotated in fp32 and split into TERMS
 // bf16 terms (what a term leaves goes to the next), written as K-major
-// 128B-swizzled operands of `rows` rows: two 64-dim panels a term.  Rows past
-// nr are zero.  128 threads; a thread takes 8 RoPE pairs of a row at a time.
+// 128B-swizzled operands of `rows` rows (a multiple of 8): two 64-dim panels a
+// term.  Rows past nr are zero.  128 threads; a thread takes 8 RoPE pairs of a row at a time.
 template <int TERMS>
 __device__ __forceinline__ void prepare_queries(const WeightsArgs &a, const DevReq &rq, int l, int h, int G, int r0, int nr,
-                                                int rows, uint32_t dst0, uint32_t term_bytes)
+                                                int rows, uint32_t dst0, uint32_t term_bytes, uint32_t panel_bytes)
 {
 #pragma unroll 2
     for (int it = threadIdx.x; it < rows * 8; it += 128) {
@@ -175,7 +177,7 @@ __device__ __forceinline__ void prepare_queries(const WeightsArgs &a, const DevR
                     x0 -= __low2float(b);    // exact: what the term leaves
                     x1 -= __high2float(b);
                 }
-                st_shared_v4(dst + (uint32_t)term * term_bytes + (uint32_t)k * (term_bytes / 2), w4[0], w4[1], w4[2], w4[3]);
+                st_shared_v4(dst + (uint32_t)term * term_bytes + (uint32_t)k * panel_bytes, w4[0], w4[1], w4[2], w4[3]);
             }
     }
 }
@@ -202,12 +204,13 @@ __device__ __forceinline__ bool wait_peers(uint32_t bar, uint32_t parity, volati
 
 }  // namespace
 
-template <int NQ, int NC>
+template <int NC>
 __global__ void __launch_bounds__(kWtThreads, 2)
     k_key_weights_tc(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ WeightsArgs a,
                      const __grid_constant__ ReqTable rt, const int n_cluster)
 {
-    using C = WtCfg<NQ, NC>;
+    using C = WtCfg<NC>;
+    constexpr int NQ = C::NQ;
     constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NQ >> 3) << 17) |
                                 ((uint32_t)(kWtTile >> 4) << 24);
     extern __shared__ __align__(1024) uint8_t wt_smem[];
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     const int lh = unit_i % units;
     const int G = a.n_q_heads / a.n_kv_heads;
     const int m_rows = rq.q_len * G, n = rq.prefix + rq.q_len;
-    const int n_rb = (m_rows + NQ - 1) / NQ;                 // row blocks
+    const int n_rb = (m_rows + NC - 1) / NC;                 // row blocks
     const int nt = (n + kWtTile - 1) / kWtTile;
     const int t_lo = (int)((int64_t)rank * nt / n_cluster), t_hi = (int)((int64_t)(rank + 1) * nt / n_cluster);
     const int T = t_hi - t_lo;                               // this CTA's key tiles
@@ -270,13 +273,13 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             for (int j = t_lo * kWtTile + (int)threadIdx.x; j < min(n, t_hi * kWtTile); j += 128)
                 wp[j] = 0.f;
         for (int rb = 0; rb < n_rb && ok; ++rb) {
-            const int r0 = rb * NQ, nr = min(NQ, m_rows - r0);
+            const int r0 = rb * NC, nr = min(NC, m_rows - r0);
             if (rb > 0 && !mbar_wait(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             // ---- the row block's queries: rotated, split in three bf16 terms ----
-            prepare_queries<3>(a, rq, l, h, G, r0, nr, NQ, sbase, (uint32_t)C::kQTerm);
+            prepare_queries<3>(a, rq, l, h, G, r0, nr, C::kTermRows, sbase, (uint32_t)(C::kTermRows * 128), (uint32_t)C::kQPanel);
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
 
@@ -291,7 +294,6 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                     tmem_ld16(at, s);
                 else
                     tmem_ld32(at, s);
-                tmem_wait_ld();
             };
             auto keep = [&](uint32_t at, const float *s) {
                 if constexpr (NC == 4)
@@ -303,7 +305,18 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 else
                     tmem_st32(at, s);
             };
-            auto job_at = [&](int jb) { return lane_base + (uint32_t)((jb % C::kStages) * NQ); };
+            // a product: the sum of the three terms'
+            auto load_job = [&](int jb, float *s) {
+                const uint32_t at = lane_base + (uint32_t)((jb % C::kStages) * NQ);
+                float mid[NC], low[NC];
+                load(at, s);
+                load(at + C::kTermRows, mid);
+                load(at + 2 * C::kTermRows, low);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    s[c] += mid[c] + low[c];
+            };
             auto wait_job = [&](int jb) -> bool {
                 if (!mbar_wait(bar(bSFull + jb % C::kStages), (uint32_t)(jb / C::kStages) & 1, abort_flag))
                     return false;
@@ -320,14 +333,14 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                     s[c] = c >= lim ? s[c] : -INFINITY;
             };
             // scores kept of tile t
-            auto kept_at = [&](int t) { return lane_base + (uint32_t)(64 + t * NC); };
+            auto kept_at = [&](int t) { return lane_base + (uint32_t)(C::kStages * NQ + t * NC); };
 
             // ---- pass 1: each row's reference and sum over this warp's keys ----
             float ls[NC];
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 ls[c] = 0.f;
-            float *ref = s_ref + warp * NQ;
+            float *ref = s_ref + warp * NC;
             if (lane < NC)
                 ref[lane] = kWtUnset;
             __syncwarp();
@@ -340,7 +353,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 const int j0 = (t_lo + t) * kWtTile, j = j0 + (int)threadIdx.x;
                 const bool edge = j0 + kWtTile > rq.prefix + 1;   // some key is not seen by every row
                 float s[NC];
-                load(job_at(job), s);
+                load_job(job, s);
                 if (t < C::kKept)   // uniform
                     keep(kept_at(t), s);
                 free_job(job);
@@ -378,24 +391,24 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             {
                 const float r = warp_sums<NC>(ls, lane);
                 const int c = warp_sums_index<NC>(lane);
-                s_stat[warp * NQ + c] = make_float2(ref[c], r);
+                s_stat[warp * NC + c] = make_float2(ref[c], r);
             }
             softmax_sync();
             // ---- the CTA's (max, sum) of row c to every CTA of the cluster ----
-            const uint32_t peer = sbase + C::kOffPeer + (uint32_t)((rb & 1) * kWtMaxCluster * NQ * 8);
+            const uint32_t peer = sbase + C::kOffPeer + (uint32_t)((rb & 1) * kWtMaxCluster * NC * 8);
             if (threadIdx.x < NC) {
                 const int c = threadIdx.x;
                 float M = kWtUnset, L = 0.f;
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    M = fmaxf(M, s_stat[x * NQ + c].x);
+                    M = fmaxf(M, s_stat[x * NC + c].x);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float2 v = s_stat[x * NQ + c];
+                    const float2 v = s_stat[x * NC + c];
                     L += v.y != 0.f ? v.y * ex2(v.x - M) : 0.f;
                 }
                 for (int x = 0; x < n_cluster; ++x) {
-                    const uint32_t dst = mapa_rank(peer + (uint32_t)((rank * NQ + c) * 8), (uint32_t)x);
+                    const uint32_t dst = mapa_rank(peer + (uint32_t)((rank * NC + c) * 8), (uint32_t)x);
                     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(M), "f"(L) : "memory");
                     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                                      mapa_rank(bar(bPeers), (uint32_t)x))
@@ -403,11 +416,11 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 }
                 if (wait_peers(bar(bPeers), (uint32_t)rb & 1, abort_flag)) {
                     float Mt = kWtUnset, Lt = 0.f;
-                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + C::kOffPeer) + (rb & 1) * kWtMaxCluster * NQ + c;
+                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + C::kOffPeer) + (rb & 1) * kWtMaxCluster * NC + c;
                     for (int x = 0; x < n_cluster; ++x)
-                        Mt = fmaxf(Mt, pv[x * NQ].x);
+                        Mt = fmaxf(Mt, pv[x * NC].x);
                     for (int x = 0; x < n_cluster; ++x) {   // in rank order: one rounding order
-                        const float2 v = pv[x * NQ];
+                        const float2 v = pv[x * NC];
                         Lt += v.y != 0.f ? v.y * ex2(v.x - Mt) : 0.f;
                     }
                     s_fin[c] = Mt + log2f(Lt);
@@ -433,10 +446,13 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                     break;
                 }
                 float s[NC], p4[4] = {0.f, 0.f, 0.f, 0.f};
-                load(redo ? job_at(job) : kept_at(t), s);
                 if (redo) {
+                    load_job(job, s);
                     free_job(job);
                     ++job;
+                } else {
+                    load(kept_at(t), s);
+                    tmem_wait_ld();
                 }
                 if (j0 + kWtTile > rq.prefix + 1)
                     mask(j >= n ? NC : (j - rq.prefix) * G - r0, s);
@@ -497,14 +513,11 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                     }
                     tc_fence_after();
                     const uint32_t ka = lo + ((uint32_t)(C::kOffRing + s * kWtPanel) >> 4);
+                    const uint32_t qb = lo + ((uint32_t)(p * C::kQPanel) >> 4);
 #pragma unroll
-                    for (int term = 0; term < 3; ++term) {
-                        const uint32_t qb = lo + ((uint32_t)(term * C::kQTerm + p * (C::kQTerm / 2)) >> 4);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mma_ss(lead, tmem + (uint32_t)(stage * NQ), desc_with_lo(ka + 2 * x, hi), desc_with_lo(qb + 2 * x, hi),
-                                   kIdesc, p > 0 || term > 0 || x > 0);
-                    }
+                    for (int x = 0; x < 4; ++x)
+                        mma_ss(lead, tmem + (uint32_t)(stage * NQ), desc_with_lo(ka + 2 * x, hi), desc_with_lo(qb + 2 * x, hi),
+                               kIdesc, p > 0 || x > 0);
                     umma_commit(lead, bar(bEmpty + s));
                 }
                 if (ok)
@@ -615,7 +628,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 ok = false;
                 break;
             }
-            prepare_queries<2>(a, rq, l, h, G, r0, nr, 128, sbase, (uint32_t)kWwQTerm);
+            prepare_queries<2>(a, rq, l, h, G, r0, nr, 128, sbase, (uint32_t)kWwQTerm, (uint32_t)(kWwQTerm / 2));
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
 
@@ -842,19 +855,19 @@ static cudaError_t launch_cluster(void (*k)(const CUtensorMap, const WeightsArgs
     return cudaLaunchKernelEx(&cfg, k, tmk, a, rt, c);
 }
 
-template <int NQ, int NC>
+template <int NC>
 static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
 {
-    using C = WtCfg<NQ, NC>;
+    using C = WtCfg<NC>;
     static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(k_key_weights_tc<NQ, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) !=
+        if ((e = cudaFuncSetAttribute(k_key_weights_tc<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) !=
                 cudaSuccess ||
-            (e = cudaFuncSetAttribute(k_key_weights_tc<NQ, NC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
+            (e = cudaFuncSetAttribute(k_key_weights_tc<NC>, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
             return e;
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
@@ -869,7 +882,7 @@ static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUt
         c *= 2;
     if (units * c > 0x7fffffff)
         return cudaErrorInvalidValue;
-    return launch_cluster(k_key_weights_tc<NQ, NC>, units * c, C::kSmem, c, s, tmk, a, rt);
+    return launch_cluster(k_key_weights_tc<NC>, units * c, C::kSmem, c, s, tmk, a, rt);
 }
 
 static cudaError_t launch_window(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
@@ -902,13 +915,13 @@ cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const vo
     const CUtensorMap &m = *static_cast<const CUtensorMap *>(tmap_k);
     const int64_t rows = (int64_t)a.max_q_len * (a.n_q_heads / a.n_kv_heads);
     if (rows <= 4)
-        return launch_nq<16, 4>(a, rt, m, n_sms, s);
+        return launch_nq<4>(a, rt, m, n_sms, s);
     if (rows <= 8)
-        return launch_nq<16, 8>(a, rt, m, n_sms, s);
+        return launch_nq<8>(a, rt, m, n_sms, s);
     if (rows <= 16)
-        return launch_nq<16, 16>(a, rt, m, n_sms, s);
+        return launch_nq<16>(a, rt, m, n_sms, s);
     if (rows <= 32)
-        return launch_nq<32, 32>(a, rt, m, n_sms, s);
+        return launch_nq<32>(a, rt, m, n_sms, s);
     return launch_window(a, rt, m, n_sms, s);
 }
 
