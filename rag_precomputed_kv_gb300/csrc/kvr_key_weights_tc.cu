@@ -122,38 +122,58 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;"
 
 // Query rows r0 .. r0 + nr - 1 of a unit, rotated in fp32 and split into TERMS
 // bf16 terms (what a term leaves goes to the next), written as K-major
-// 128B-swizzled operands of `rows` rows (a multiple of 8): two 64-dim panels a
-// term.  Rows past nr are zero.  128 threads; a thread takes 8 RoPE pairs of a row at a time.
-template <int TERMS>
+// 128B-swizzled operands of ROWS rows (a multiple of 8): two 64-dim panels a
+// term.  Rows past nr are zero.  128 threads; thread: RoPE pairs 8j .. 8j + 7,
+// j = thread % 8, of rows thread / 8 + 16 k, four rows at a time, all their loads
+// before the first use (one row at a time, a window's 128 rows took 17,000
+// cycles, nearly all of it latency).
+template <int TERMS, int ROWS>
 __device__ __forceinline__ void prepare_queries(const WeightsArgs &a, const DevReq &rq, int l, int h, int G, int r0, int nr,
-                                                int rows, uint32_t dst0, uint32_t term_bytes, uint32_t panel_bytes)
+                                                uint32_t dst0, uint32_t term_bytes, uint32_t panel_bytes)
 {
-#pragma unroll 2
-    for (int it = threadIdx.x; it < rows * 8; it += 128) {
-        const int row = it >> 3, j = it & 7;
-        float v[16];   // elements 8j..8j+7 and 64+8j..64+8j+7
+    constexpr int U = ROWS >= 64 ? 4 : 1;
+    const int j = threadIdx.x & 7;
+#pragma unroll 1
+    for (int row0 = threadIdx.x >> 3; row0 < ROWS; row0 += 16 * U) {
+        uint4 u[U][2];
+        float2 cs[U][8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            v[e] = 0.f;
-        if (row < nr) {
-            const int t = (r0 + row) / G, g = (r0 + row) - t * G;
-            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
-                                      (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + g) * kWtD + 8 * j;
-            const uint4 u[2] = {*reinterpret_cast<const uint4 *>(qp), *reinterpret_cast<const uint4 *>(qp + 64)};
+        for (int k = 0; k < U; ++k) {
+            const int row = row0 + 16 * k;
+            u[k][0] = u[k][1] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t w4[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+            for (int e = 0; e < 8; ++e)
+                cs[k][e] = make_float2(1.f, 0.f);
+            if (row < nr) {
+                const int t = (r0 + row) / G, g = (r0 + row) - t * G;
+                const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
+                                          (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + g) * kWtD + 8 * j;
+                u[k][0] = *reinterpret_cast<const uint4 *>(qp);
+                u[k][1] = *reinterpret_cast<const uint4 *>(qp + 64);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    cs[k][e] = rope_cs(a.rope, kWtD / 2, rq.prefix + t, rope_pair(a.interleaved, kWtD, 8, j, e));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int row = row0 + 16 * k;
+            if (row >= ROWS)
+                break;
+            float v[16];   // elements 8j..8j+7 and 64+8j..64+8j+7
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t w4[4] = {u[k][x].x, u[k][x].y, u[k][x].z, u[k][x].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    v[8 * k + 2 * e] = __uint_as_float(w4[e] << 16);
-                    v[8 * k + 2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
+                    v[8 * x + 2 * e] = __uint_as_float(w4[e] << 16);
+                    v[8 * x + 2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
                 }
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float2 cs = rope_cs(a.rope, kWtD / 2, rq.prefix + t, rope_pair(a.interleaved, kWtD, 8, j, e));
                 const float x0 = a.interleaved ? v[2 * e] : v[e], x1 = a.interleaved ? v[2 * e + 1] : v[8 + e];
-                const float y0 = fmaf(x0, cs.x, -x1 * cs.y), y1 = fmaf(x0, cs.y, x1 * cs.x);
+                const float y0 = fmaf(x0, cs[k][e].x, -x1 * cs[k][e].y), y1 = fmaf(x0, cs[k][e].y, x1 * cs[k][e].x);
                 if (a.interleaved) {
                     v[2 * e] = y0;
                     v[2 * e + 1] = y1;
@@ -162,23 +182,23 @@ __device__ __forceinline__ void prepare_queries(const WeightsArgs &a, const DevR
                     v[8 + e] = y1;
                 }
             }
-        }
-        const uint32_t dst = dst0 + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4));
+            const uint32_t dst = dst0 + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4));
 #pragma unroll
-        for (int term = 0; term < TERMS; ++term)
+            for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t w4[4];
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t w4[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float &x0 = v[8 * k + 2 * e], &x1 = v[8 * k + 2 * e + 1];
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-                    w4[e] = *reinterpret_cast<const uint32_t *>(&b);
-                    x0 -= __low2float(b);    // exact: what the term leaves
-                    x1 -= __high2float(b);
+                    for (int e = 0; e < 4; ++e) {
+                        float &x0 = v[8 * x + 2 * e], &x1 = v[8 * x + 2 * e + 1];
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+                        w4[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        x0 -= __low2float(b);    // exact: what the term leaves
+                        x1 -= __high2float(b);
+                    }
+                    st_shared_v4(dst + (uint32_t)term * term_bytes + (uint32_t)x * panel_bytes, w4[0], w4[1], w4[2], w4[3]);
                 }
-                st_shared_v4(dst + (uint32_t)term * term_bytes + (uint32_t)k * panel_bytes, w4[0], w4[1], w4[2], w4[3]);
-            }
+        }
     }
 }
 
@@ -279,7 +299,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 break;
             }
             // ---- the row block's queries: rotated, split in three bf16 terms ----
-            prepare_queries<3>(a, rq, l, h, G, r0, nr, C::kTermRows, sbase, (uint32_t)(C::kTermRows * 128), (uint32_t)C::kQPanel);
+            prepare_queries<3, C::kTermRows>(a, rq, l, h, G, r0, nr, sbase, (uint32_t)(C::kTermRows * 128), (uint32_t)C::kQPanel);
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
 
@@ -437,9 +457,19 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             }
             // ---- pass 2: the weights of this thread's keys ----
             const bool add = rb > 0 || a.accumulate;
+            // (the weights to add to are read eight tiles ahead)
+            float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             for (int t = 0; t < T; ++t) {
                 const int j0 = (t_lo + t) * kWtTile, j = j0 + (int)threadIdx.x;
-                const float w = add && j < n ? wp[j] : 0.f;
+                if (add && (t & 7) == 0) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        old[x] = t + x < T && j + x * kWtTile < n ? wp[j + x * kWtTile] : 0.f;
+                }
+                const float w = old[0];
+#pragma unroll
+                for (int x = 0; x < 7; ++x)
+                    old[x] = old[x + 1];
                 const bool redo = t >= C::kKept;
                 if (redo && !wait_job(job)) {
                     ok = false;
@@ -560,7 +590,7 @@ constexpr int kWwOffRing = 2 * kWwQTerm;
 constexpr int kWwOffBar = kWwOffRing + kWwSlots * kWtPanel;
 constexpr int kWwNumBars = 2 * kWwSlots + 4 + 4;   // full, empty, s_full[2], s_free[2], q_full, q_empty, peers, drain
 constexpr int kWwOffMisc = kWwOffBar + 8 * kWwNumBars;
-constexpr int kWwOffFin = (kWwOffMisc + 8 + 15) & ~15;         // [128] lse
+constexpr int kWwOffFin = (kWwOffMisc + 8 + 15) & ~15;         // [128] -lse
 constexpr int kWwSmem = kWwOffFin + 128 * 4;
 constexpr int kWwOffPeer = kWwSmem;                            // [2][kWwMaxCluster][128] (max, sum), clusters only
 constexpr int kWwSmemCluster = kWwOffPeer + 2 * kWwMaxCluster * 128 * 8;
@@ -628,7 +658,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 ok = false;
                 break;
             }
-            prepare_queries<2>(a, rq, l, h, G, r0, nr, 128, sbase, (uint32_t)kWwQTerm, (uint32_t)(kWwQTerm / 2));
+            prepare_queries<2, 128>(a, rq, l, h, G, r0, nr, sbase, (uint32_t)kWwQTerm, (uint32_t)(kWwQTerm / 2));
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
 
@@ -645,11 +675,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 tc_fence_after();
                 if (warp * 32 < nr) {
                     const int lim = see - (t_lo + i) * kWtTile;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float s[32];
-                        tmem_ld32(lane_base + (uint32_t)(half * 128 + q * 32), s);
-                        tmem_wait_ld();
+                    const uint32_t at = lane_base + (uint32_t)(half * 128);
+                    auto block = [&](int q, float *s) {
                         if (lim < kWtTile) {
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
@@ -657,19 +684,42 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                         }
                         float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                        for (int c = 4; c < 32; ++c)
-                            m4[c & 3] = fmaxf(m4[c & 3], s[c]);
-                        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+                        for (int c = 4; c < 28; c += 8)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                m4[x] = max3(m4[x], s[c + 2 * x], s[c + 2 * x + 1]);
+                        const float mx = max3(max3(m4[0], m4[1], s[28]), max3(m4[2], m4[3], s[29]), fmaxf(s[30], s[31])) * sc;
                         if (mx > m + 8.f) {   // (the reference need not be the maximum)
                             lsum = lsum == 0.f ? 0.f : lsum * ex2(m - mx);
                             m = mx;
                         }
-                        float a4[4] = {0.f, 0.f, 0.f, 0.f};
+                        const uint64_t sc2 = pk2(sc, sc), nm2 = pk2(-m, -m);
+                        uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            a4[c & 3] += ex2(fmaf(s[c], sc, -m));
-                        lsum += (a4[0] + a4[1]) + (a4[2] + a4[3]);
-                    }
+                        for (int c = 0; c < 16; ++c) {
+                            float x0, x1;
+                            unpk2(fma2(pk2(s[2 * c], s[2 * c + 1]), sc2, nm2), x0, x1);
+                            acc[c & 1] = add2(acc[c & 1], pk2(ex2(x0), ex2(x1)));
+                        }
+                        float a0, a1, b0, b1;
+                        unpk2(acc[0], a0, a1);
+                        unpk2(acc[1], b0, b1);
+                        lsum += (a0 + a1) + (b0 + b1);
+                    };
+                    // the next 32 columns are on their way while these are summed
+                    float sa[32], sb[32];
+                    tmem_ld32(at, sa);
+                    tmem_wait_ld();
+                    tmem_ld32(at + 32, sb);
+                    block(0, sa);
+                    tmem_wait_ld();
+                    tmem_ld32(at + 64, sa);
+                    block(1, sb);
+                    tmem_wait_ld();
+                    tmem_ld32(at + 96, sb);
+                    block(2, sa);
+                    tmem_wait_ld();
+                    block(3, sb);
                 }
                 tc_fence_before();
                 mbar_arrive(bar(bSFree + half));
@@ -701,7 +751,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 }
             }
             softmax_sync();   // (the row block before has read its denominators)
-            s_fin[r] = r < nr ? M + log2f(L) : 0.f;   // (rows that pad the block: any finite value)
+            s_fin[r] = r < nr ? -(M + log2f(L)) : 0.f;   // (rows that pad the block: any finite value)
             if (r < nr && rank == 0 && !(L > 0.f && L < INFINITY))
                 atomicCAS(a.err, kDevOk, kDevBadInput);
             softmax_sync();
@@ -723,30 +773,52 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 tc_fence_after();
                 const bool edge = j0 + kWtTile > rq.prefix + 1;
                 const int lim = !edge ? 0 : j >= n ? 128 : (j - rq.prefix) * G - r0;   // the first row that sees the key
-                float sum = 0.f;
-#pragma unroll 1
-                for (int q = 0; q < nb; ++q) {
-                    float s[32];
-                    tmem_ld32(lane_base + (uint32_t)(half * 128 + q * 32), s);
-                    tmem_wait_ld();
+                uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+                const uint64_t sc2 = pk2(sc, sc);
+                const uint32_t at = lane_base + (uint32_t)(half * 128);
+                auto block = [&](int q, float *s) {
                     const int hi = nr - q * 32;
                     if (edge || hi < 32) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             s[c] = q * 32 + c >= lim && c < hi ? s[c] : -INFINITY;
                     }
-                    float p4[4] = {0.f, 0.f, 0.f, 0.f};
-                    const float4 *fin = reinterpret_cast<const float4 *>(s_fin + q * 32);
+                    const float4 *fin = reinterpret_cast<const float4 *>(s_fin + q * 32);   // -lse
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const float4 f = fin[c];
-                        p4[0] += ex2(fmaf(s[4 * c], sc, -f.x));
-                        p4[1] += ex2(fmaf(s[4 * c + 1], sc, -f.y));
-                        p4[2] += ex2(fmaf(s[4 * c + 2], sc, -f.z));
-                        p4[3] += ex2(fmaf(s[4 * c + 3], sc, -f.w));
+                        float x0, x1, x2, x3;
+                        unpk2(fma2(pk2(s[4 * c], s[4 * c + 1]), sc2, pk2(f.x, f.y)), x0, x1);
+                        unpk2(fma2(pk2(s[4 * c + 2], s[4 * c + 3]), sc2, pk2(f.z, f.w)), x2, x3);
+                        acc[0] = add2(acc[0], pk2(ex2(x0), ex2(x1)));
+                        acc[1] = add2(acc[1], pk2(ex2(x2), ex2(x3)));
                     }
-                    sum += (p4[0] + p4[1]) + (p4[2] + p4[3]);
+                };
+                float sa[32], sb[32];
+                tmem_ld32(at, sa);
+                tmem_wait_ld();
+                if (nb > 1)   // the next 32 rows are on their way while these are summed
+                    tmem_ld32(at + 32, sb);
+                block(0, sa);
+                tmem_wait_ld();
+                if (nb > 1) {
+                    if (nb > 2)
+                        tmem_ld32(at + 64, sa);
+                    block(1, sb);
+                    tmem_wait_ld();
+                    if (nb > 2) {
+                        if (nb > 3)
+                            tmem_ld32(at + 96, sb);
+                        block(2, sa);
+                        tmem_wait_ld();
+                        if (nb > 3)
+                            block(3, sb);
+                    }
                 }
+                float a0, a1, b0, b1;
+                unpk2(acc[0], a0, a1);
+                unpk2(acc[1], b0, b1);
+                const float sum = (a0 + a1) + (b0 + b1);
                 tc_fence_before();
                 mbar_arrive(bar(bSFree + half));
                 if (j < n)
