@@ -120,86 +120,117 @@ __device__ __forceinline__ int warp_sums_index(int lane)
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+// (cos, sin) of pairs 8j .. 8j + 7 at position pos (interleaved: 4j .. 4j + 3 and
+// 32 + 4j .. 32 + 4j + 3), as rope_cs, by 16-byte loads.
+__device__ __forceinline__ void rope_cs8(const float2 *__restrict__ tab, int pos, int j, bool il, float2 *cs)
+{
+    const int p0 = il ? 4 * j : 8 * j, p1 = il ? 32 + 4 * j : 8 * j + 4;
+    auto load = [&](int row, float4 *f) {
+        const float2 *r = tab + row * (kWtD / 2);
+        f[0] = __ldg(reinterpret_cast<const float4 *>(r + p0));
+        f[1] = __ldg(reinterpret_cast<const float4 *>(r + p0) + 1);
+        f[2] = __ldg(reinterpret_cast<const float4 *>(r + p1));
+        f[3] = __ldg(reinterpret_cast<const float4 *>(r + p1) + 1);
+    };
+    float4 f[4];
+    load(kRopeSplit + (pos & (kRopeSplit - 1)), f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        cs[2 * e] = make_float2(f[e].x, f[e].y);
+        cs[2 * e + 1] = make_float2(f[e].z, f[e].w);
+    }
+    if (pos >= kRopeSplit) {
+        load(pos >> 12, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float hx = e & 1 ? f[e >> 1].z : f[e >> 1].x, hy = e & 1 ? f[e >> 1].w : f[e >> 1].y;
+            cs[e] = make_float2(fmaf(hx, cs[e].x, -hy * cs[e].y), fmaf(hy, cs[e].x, hx * cs[e].y));
+        }
+    }
+}
+
 // Query rows r0 .. r0 + nr - 1 of a unit, rotated in fp32 and split into TERMS
 // bf16 terms (what a term leaves goes to the next), written as K-major
 // 128B-swizzled operands of ROWS rows (a multiple of 8): two 64-dim panels a
 // term.  Rows past nr are zero.  128 threads; thread: RoPE pairs 8j .. 8j + 7,
-// j = thread % 8, of rows thread / 8 + 16 k, four rows at a time, all their loads
-// before the first use (one row at a time, a window's 128 rows took 17,000
-// cycles, nearly all of it latency).
+// j = thread % 8, of a token's heads, four heads at a time (their angles are the
+// same, and shared memory leaves next to no L1 that would keep a table row
+// between them: a row at a time, a window's 128 rows took 17,000 cycles).
 template <int TERMS, int ROWS>
 __device__ __forceinline__ void prepare_queries(const WeightsArgs &a, const DevReq &rq, int l, int h, int G, int r0, int nr,
                                                 uint32_t dst0, uint32_t term_bytes, uint32_t panel_bytes)
 {
-    constexpr int U = ROWS >= 64 ? 4 : 1;
-    const int j = threadIdx.x & 7;
+    const int j = threadIdx.x & 7, t_a = r0 / G, n_tok = (r0 + nr - 1) / G - t_a + 1;
+    for (int it = threadIdx.x >> 3; it < n_tok; it += 16) {
+        const int t = t_a + it;
+        const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
+                                  (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G) * kWtD + 8 * j;
+        const int row_t = t * G - r0;   // the row of head 0 (negative: in the block before)
+        float2 cs[8];
+        rope_cs8(a.rope, rq.prefix + t, j, a.interleaved, cs);
 #pragma unroll 1
-    for (int row0 = threadIdx.x >> 3; row0 < ROWS; row0 += 16 * U) {
-        uint4 u[U][2];
-        float2 cs[U][8];
+        for (int g0 = max(0, -row_t); g0 < G && row_t + g0 < nr; g0 += 4) {
+            uint4 u[4][2];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int row = row0 + 16 * k;
-            u[k][0] = u[k][1] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                cs[k][e] = make_float2(1.f, 0.f);
-            if (row < nr) {
-                const int t = (r0 + row) / G, g = (r0 + row) - t * G;
-                const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
-                                          (((int64_t)l * a.total_q + rq.q_off + t) * a.n_q_heads + h * G + g) * kWtD + 8 * j;
-                u[k][0] = *reinterpret_cast<const uint4 *>(qp);
-                u[k][1] = *reinterpret_cast<const uint4 *>(qp + 64);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    cs[k][e] = rope_cs(a.rope, kWtD / 2, rq.prefix + t, rope_pair(a.interleaved, kWtD, 8, j, e));
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int row = row0 + 16 * k;
-            if (row >= ROWS)
-                break;
-            float v[16];   // elements 8j..8j+7 and 64+8j..64+8j+7
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint32_t w4[4] = {u[k][x].x, u[k][x].y, u[k][x].z, u[k][x].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[8 * x + 2 * e] = __uint_as_float(w4[e] << 16);
-                    v[8 * x + 2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
-                }
+            for (int k = 0; k < 4; ++k) {
+                const bool in = g0 + k < G && row_t + g0 + k < nr;
+                const __nv_bfloat16 *p = qp + (in ? g0 + k : g0) * kWtD;
+                u[k][0] = *reinterpret_cast<const uint4 *>(p);
+                u[k][1] = *reinterpret_cast<const uint4 *>(p + 64);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x0 = a.interleaved ? v[2 * e] : v[e], x1 = a.interleaved ? v[2 * e + 1] : v[8 + e];
-                const float y0 = fmaf(x0, cs[k][e].x, -x1 * cs[k][e].y), y1 = fmaf(x0, cs[k][e].y, x1 * cs[k][e].x);
-                if (a.interleaved) {
-                    v[2 * e] = y0;
-                    v[2 * e + 1] = y1;
-                } else {
-                    v[e] = y0;
-                    v[8 + e] = y1;
-                }
-            }
-            const uint32_t dst = dst0 + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4));
-#pragma unroll
-            for (int term = 0; term < TERMS; ++term)
+            for (int k = 0; k < 4; ++k) {
+                const int row = row_t + g0 + k;
+                if (g0 + k >= G || row >= nr)
+                    break;
+                float v[16];   // elements 8j..8j+7 and 64+8j..64+8j+7
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    uint32_t w4[4];
+                    const uint32_t w4[4] = {u[k][x].x, u[k][x].y, u[k][x].z, u[k][x].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float &x0 = v[8 * x + 2 * e], &x1 = v[8 * x + 2 * e + 1];
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
-                        w4[e] = *reinterpret_cast<const uint32_t *>(&b);
-                        x0 -= __low2float(b);    // exact: what the term leaves
-                        x1 -= __high2float(b);
+                        v[8 * x + 2 * e] = __uint_as_float(w4[e] << 16);
+                        v[8 * x + 2 * e + 1] = __uint_as_float(w4[e] & 0xffff0000u);
                     }
-                    st_shared_v4(dst + (uint32_t)term * term_bytes + (uint32_t)x * panel_bytes, w4[0], w4[1], w4[2], w4[3]);
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x0 = a.interleaved ? v[2 * e] : v[e], x1 = a.interleaved ? v[2 * e + 1] : v[8 + e];
+                    const float y0 = fmaf(x0, cs[e].x, -x1 * cs[e].y), y1 = fmaf(x0, cs[e].y, x1 * cs[e].x);
+                    if (a.interleaved) {
+                        v[2 * e] = y0;
+                        v[2 * e + 1] = y1;
+                    } else {
+                        v[e] = y0;
+                        v[8 + e] = y1;
+                    }
+                }
+                const uint32_t dst = dst0 + (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4));
+#pragma unroll
+                for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &x0 = v[8 * x + 2 * e], &x1 = v[8 * x + 2 * e + 1];
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+                            w4[e] = *reinterpret_cast<const uint32_t *>(&b);
+                            x0 -= __low2float(b);    // exact: what the term leaves
+                            x1 -= __high2float(b);
+                        }
+                        st_shared_v4(dst + (uint32_t)term * term_bytes + (uint32_t)x * panel_bytes, w4[0], w4[1], w4[2], w4[3]);
+                    }
+            }
         }
     }
+    for (int row = nr + (int)(threadIdx.x >> 3); row < ROWS; row += 16)
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                st_shared_v4(dst0 + (uint32_t)(row * 128 + (j << 4)) + (uint32_t)term * term_bytes + (uint32_t)x * panel_bytes, 0u,
+                             0u, 0u, 0u);
 }
 
 // Bounded wait that sees what other CTAs of the cluster released before arriving.
