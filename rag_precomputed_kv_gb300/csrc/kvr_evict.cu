@@ -139,29 +139,41 @@ __global__ void __launch_bounds__(TH, 1)
         const int i = row0 + 32 * r;
         return i >= rq.n ? kNoRow : i < lo || i >= hi ? kAlways : weight_key(bits);
     };
-    extern __shared__ uint32_t keys[];   // [warp][R'][lane]
-    uint32_t *mine = keys + row0;
+    // keys: [warp][r / 4][lane] of four rows r .. r + 3 of the lane
+    extern __shared__ uint4 keys[];
+    const int n_q = (n_r + 3) / 4;
+    uint4 *mine = keys + warp * 32 * n_q + lane;
+    auto quad_of = [&](int q) -> uint4 {   // from global memory
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u[e] = 4 * q + e < n_r ? bits_of(4 * q + e) : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u[e] = 4 * q + e < n_r ? key_of(4 * q + e, u[e]) : kNoRow;
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    };
     if constexpr (kSmem) {
-#pragma unroll 1
-        for (int r0 = 0; r0 < n_r; r0 += 8) {   // eight loads in flight
-            uint32_t u[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                u[r] = r0 + r < n_r ? bits_of(r0 + r) : 0u;
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r0 + r < n_r)
-                    mine[32 * (r0 + r)] = key_of(r0 + r, u[r]);
-        }
+#pragma unroll 4
+        for (int q = 0; q < n_q; ++q)   // (sixteen loads in flight)
+            mine[32 * q] = quad_of(q);
     }
     // f(row, its key) for every row of the thread, in row order (or every eighth)
-    auto each_n = [&](int step, auto &&f) {
-#pragma unroll 4
-        for (int r = 0; r < n_r; r += step)
-            f(row0 + 32 * r, kSmem ? mine[32 * r] : key_of(r, bits_of(r)));
+    auto each = [&](auto &&f) {
+#pragma unroll 2
+        for (int q = 0; q < n_q; ++q) {
+            const uint4 x = kSmem ? mine[32 * q] : quad_of(q);
+            const int i = row0 + 128 * q;
+            f(i, x.x);
+            f(i + 32, x.y);
+            f(i + 64, x.z);
+            f(i + 96, x.w);
+        }
     };
-    auto each = [&](auto &&f) { each_n(1, f); };
-    auto each8 = [&](auto &&f) { each_n(8, f); };
+    auto each8 = [&](auto &&f) {
+        for (int q = 0; q < n_q; q += 2)
+            f(row0 + 128 * q, kSmem ? mine[32 * q].x : quad_of(q).x);
+    };
     auto clear = [&] {
         __syncthreads();
         for (int i = threadIdx.x; i < 2048; i += TH)
@@ -216,8 +228,6 @@ __global__ void __launch_bounds__(TH, 1)
         return block_sum_before(sum, total);
     };
 
-    int n_always = 0;      // of this thread's rows
-    each([&](int, uint32_t x) { n_always += x == kAlways; });
     uint32_t prefix = 0;   // the threshold's leading digits
     int left = k;          // how many of the rows with those digits stay
     bool ranked = false;
@@ -257,7 +267,6 @@ __global__ void __launch_bounds__(TH, 1)
                     if (x - k_lo <= k_hi - k_lo)
                         atomicAdd(&hist[x >> 21], 1);
                 });
-                n_above -= n_always;
             } else {
                 each([&](int, uint32_t x) {
                     if (x != kNoRow && (x >> above_bits) == (prefix >> above_bits))
@@ -267,6 +276,7 @@ __global__ void __launch_bounds__(TH, 1)
             __syncthreads();
             if (!whole) {
                 block_sum_before(n_above, above);
+                above -= a.n_first + a.n_recent;   // (kAlways is above every digit)
             }
             const int before = bins_before(total);
             if (find(above + before, total, left) >= 0)
@@ -280,17 +290,26 @@ __global__ void __launch_bounds__(TH, 1)
         left = s_found[1];
         const int n_cand = s_found[2];
         if (n_cand <= kRankMax) {
+            // collected, with each warp's count of the keys above the digit; then the
+            // ones among the candidates that stay are added to their warps' counts
             ranked = true;
             if (threadIdx.x == 0)
                 s_n = 0;
             __syncthreads();
+            const uint32_t digit = prefix >> shift;
+            int n_gt = 0;
             each([&](int i, uint32_t x) {
-                if (x != kNoRow && (x >> shift) == (prefix >> shift)) {
+                const uint32_t d = x >> shift;
+                n_gt += d > digit;
+                if (d == digit && x != kNoRow) {
                     const int c = atomicAdd(&s_n, 1);
                     if (c < kRankMax)
                         s_cand[c] = make_uint2(x, (uint32_t)i);
                 }
             });
+            n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+            if (lane == 0)
+                s_warp[warp] = n_gt;
             __syncthreads();
             for (int c = threadIdx.x; c < n_cand; c += TH) {
                 const uint2 me = s_cand[c];
@@ -299,6 +318,8 @@ __global__ void __launch_bounds__(TH, 1)
                     const uint2 v = s_cand[o];
                     rank += v.x > me.x || (v.x == me.x && v.y < me.y);
                 }
+                if (rank < left)
+                    atomicAdd(&s_warp[(int)me.y / (32 * n_r)], 1);
                 if (rank == left - 1)
                     s_last = me;
             }
@@ -310,23 +331,25 @@ __global__ void __launch_bounds__(TH, 1)
     const uint32_t thr = k == 0 ? kAlways - 1u : ranked ? s_last.x : prefix;
     const int last_row = ranked ? (int)s_last.y : -1;
     const bool ties = k > 0 && !ranked;
-    int n_gt = 0, n_eq = 0;
-    each([&](int i, uint32_t x) {
-        n_gt += x > thr || (x == thr && i <= last_row);
-        n_eq += x == thr;
-    });
-    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
-    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
-    __syncthreads();
-    if (lane == 0) {
-        s_warp[warp] = n_gt;
-        s_eq[warp] = ties ? n_eq : 0;
+    if (!ranked) {
+        int n_gt = 0, n_eq = 0;
+        each([&](int, uint32_t x) {
+            n_gt += x > thr;
+            n_eq += x == thr;
+        });
+        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+        n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+        __syncthreads();
+        if (lane == 0) {
+            s_warp[warp] = n_gt;
+            s_eq[warp] = ties ? n_eq : 0;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     int gt_before = 0, eq_before = 0;
     for (int x = 0; x < warp; ++x) {
         gt_before += s_warp[x];
-        eq_before += s_eq[x];
+        eq_before += ranked ? 0 : s_eq[x];
     }
     const unsigned below = (1u << lane) - 1u;
     if (!ties) {
@@ -485,7 +508,7 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
     // other's barriers), large ones when a unit has an SM to itself.
     const bool small = a.max_n <= 24 * 256 && ctas >= 4 * (int64_t)n_sms;
     const int threads = small ? 256 : 1024;
-    const int rows = (a.max_n + threads - 1) / threads * threads;   // of keys in shared memory
+    const int rows = (a.max_n + 4 * threads - 1) / (4 * threads) * 4 * threads;   // of keys in shared memory
     const bool smem = rows <= kSelSmemRows;
     auto select = small ? k_evict_select<256, true> : smem ? k_evict_select<1024, true> : k_evict_select<1024, false>;
     static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)

@@ -885,12 +885,14 @@ __global__ void __launch_bounds__(kOwThreads, 3)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)   // (this lane's keys only)
                     l_run[h] = l_run[h] * corr[h] + sum[h];
+                if (j > 0 || key0 > 0) {   // (nothing to rescale in the first block)
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    o[n][0] *= corr[0];
-                    o[n][1] *= corr[0];
-                    o[n][2] *= corr[1];
-                    o[n][3] *= corr[1];
+                    for (int n = 0; n < 16; ++n) {
+                        o[n][0] *= corr[0];
+                        o[n][1] *= corr[0];
+                        o[n][2] *= corr[1];
+                        o[n][3] *= corr[1];
+                    }
                 }
 #pragma unroll
                 for (int kb2 = 0; kb2 < 2; ++kb2) {
