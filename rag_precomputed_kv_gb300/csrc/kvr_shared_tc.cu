@@ -36,6 +36,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 #include <utility>
 
 #include "kvr_decode_common.cuh"
@@ -609,11 +610,26 @@ __device__ __forceinline__ bool own_wait(uint32_t bar, uint32_t parity)
 }
 
 // What the end of a row tile needs to know of the prefix's partial results of
-// its two rows, looked up ahead of the row tile's work.
+// its rows (NH: row r_first, and r_first + 8 too), looked up ahead of the row
+// tile's work.
 struct RowParts {
     PartRef pr[2];
-    float2 v0[2];   // (max, sum) of the first partial result
+    float2 v[2][2];   // (max, sum) of the first two partial results (none: -inf, 0)
+
+    __device__ __forceinline__ int two(int hh) const { return pr[hh].x1() - pr[hh].x0(); }
+    __device__ __forceinline__ int n(int hh) const { return pr[hh].n << two(hh); }
+    __device__ __forceinline__ float2 ml(const SharedPrefixArgs &pa, int hh, int i) const
+    {
+        return part_ml(pa.part, pr[hh].slot + (i >> two(hh)), pr[hh].x0() + (i & two(hh)))[pr[hh].pr()];
+    }
+    // columns cq, cq + 1 of partial result i; the next 8 columns are 1024 floats on
+    __device__ __forceinline__ const float *o(const SharedPrefixArgs &pa, int hh, int i, int cq) const
+    {
+        return reinterpret_cast<const float *>(part_o(pa.part, pr[hh].slot + (i >> two(hh)), pr[hh].x0() + (i & two(hh))) +
+                                               (cq >> 2) * 128 + pr[hh].pr()) + (cq & 3);
+    }
 };
+template <int NH>
 __device__ __forceinline__ RowParts row_parts(const SharedPrefixArgs &pa, const DevGroup &g, const DevShared &rq, int lh_s,
                                               int r_first, int m_rows)
 {
@@ -622,95 +638,103 @@ __device__ __forceinline__ RowParts row_parts(const SharedPrefixArgs &pa, const 
     for (int hh = 0; hh < 2; ++hh) {
         const int r = r_first + 8 * hh;
         p.pr[hh] = PartRef{0, 0, 0};
-        if (r < m_rows)
+        if (hh < NH && r < m_rows)
             p.pr[hh] = part_ref(pa, g, lh_s, (rq.q_off - g.q_off) * pa.group + r);
-        p.v0[hh] = p.pr[hh].n > 0 ? part_ml(pa.part, p.pr[hh].slot, p.pr[hh].x0())[p.pr[hh].pr()] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            p.v[hh][i] = hh < NH && i < p.n(hh) ? p.ml(pa, hh, i) : make_float2(-INFINITY, 0.f);
     }
     return p;
 }
 
+// The O of the first two partial results of a row tile's first row half, in
+// registers ahead of their use.
+template <int NH>
+struct EarlyO {
+    float2 f[2][16];
+    __device__ __forceinline__ void load(const SharedPrefixArgs &pa, const RowParts &rp, int cq)
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // (a result whose sum is 0 has an undefined O: read, where it exists, and not used)
+            const float *po = i < rp.n(0) ? rp.o(pa, 0, i, cq) : nullptr;
+#pragma unroll
+            for (int nn = 0; nn < 16; ++nn)
+                f[i][nn] = po ? *reinterpret_cast<const float2 *>(po + nn * 1024) : make_float2(0.f, 0.f);
+        }
+    }
+};
+struct NoEarlyO {};
+
 // The end of a row tile: adds the prefix's partial results (in stretch order) to
 // the warp's own states and writes the rows.  Lane: columns 8n + cq, + 1 of row
-// r_first of the request and of row r_first + 8 (fragment layout); l_run holds
-// the lane's keys only.
+// r_first of the request and (NH 2) of row r_first + 8 (fragment layout); l_run
+// holds the lane's keys only.
+template <int NH, typename Early>
 __device__ __forceinline__ void finish_rows(const SharedArgs &a, const SharedPrefixArgs &pa, const RowParts &rp,
-                                            const DevShared &rq, int lh_s, int r_first, int m_rows, float (&o)[16][4],
-                                            const float *m_run, const float *l_run)
+                                            const Early &early, const DevShared &rq, int lh_s, int r_first, int m_rows,
+                                            float (&o)[16][4], const float *m_run, const float *l_run)
 {
+    constexpr bool kEarly = !std::is_same<Early, NoEarlyO>::value;
     const int lane = threadIdx.x & 31, cq = (lane & 3) * 2, G = pa.group;
     const int lh = pa.lh_base + lh_s, l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
-    float L[2], M[2];
-    const PartRef (&pr)[2] = rp.pr;
-    const float2 (&v0)[2] = rp.v0;
-    int n[2], two[2];
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        L[hh] = l_run[hh];
-        L[hh] += __shfl_xor_sync(0xffffffffu, L[hh], 1);
-        L[hh] += __shfl_xor_sync(0xffffffffu, L[hh], 2);
-        two[hh] = pr[hh].x1() - pr[hh].x0();
-        n[hh] = pr[hh].n << two[hh];
-    }
-    auto part_state = [&](int hh, int i) -> float2 {
-        return i == 0 ? v0[hh] : part_ml(pa.part, pr[hh].slot + (i >> two[hh]), pr[hh].x0() + (i & two[hh]))[pr[hh].pr()];
-    };
+    for (int hh = 0; hh < NH; ++hh) {
+        const int r = r_first + 8 * hh, n = rp.n(hh);
+        float L = l_run[hh];
+        L += __shfl_xor_sync(0xffffffffu, L, 1);
+        L += __shfl_xor_sync(0xffffffffu, L, 2);
+        if (r >= m_rows)
+            continue;
+        auto state = [&](int i) -> float2 { return i < 2 ? rp.v[hh][i] : rp.ml(pa, hh, i); };
+        float M = L == 0.f ? -INFINITY : m_run[hh];   // (a sum of 0: no key counts)
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        M[hh] = L[hh] == 0.f ? -INFINITY : m_run[hh];   // (a sum of 0: no key counts)
-        for (int i = 0; i < n[hh]; ++i) {
-            const float2 v = part_state(hh, i);
-            M[hh] = v.y == 0.f ? M[hh] : fmaxf(M[hh], v.x);
+        for (int i = 0; i < 2; ++i)
+            M = rp.v[hh][i].y == 0.f ? M : fmaxf(M, rp.v[hh][i].x);
+        for (int i = 2; i < n; ++i) {
+            const float2 v = state(i);
+            M = v.y == 0.f ? M : fmaxf(M, v.x);
         }
-        const float w_own = L[hh] == 0.f ? 0.f : dec::dec_ex2(m_run[hh] - M[hh]);
-        L[hh] *= w_own;
+        const float w_own = L == 0.f ? 0.f : dec::dec_ex2(m_run[hh] - M);
+        L *= w_own;
 #pragma unroll
         for (int nn = 0; nn < 16; ++nn) {
             o[nn][2 * hh] *= w_own;
             o[nn][2 * hh + 1] *= w_own;
         }
-    }
-    for (int i = 0; i < max(n[0], n[1]); ++i) {
-        float wt[2];
-        const float *po[2];
+        auto add = [&](float2 v, const float2 (&f)[16]) {
+            const float wt = dec::dec_ex2(v.x - M);
+            L += v.y * wt;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            wt[hh] = 0.f;
-            po[hh] = nullptr;
-            if (i >= n[hh])
-                continue;
-            const float2 v = part_state(hh, i);
+            for (int nn = 0; nn < 16; ++nn) {
+                o[nn][2 * hh] = fmaf(f[nn].x, wt, o[nn][2 * hh]);
+                o[nn][2 * hh + 1] = fmaf(f[nn].y, wt, o[nn][2 * hh + 1]);
+            }
+        };
+        int i = 0;
+        if constexpr (kEarly) {
+            if (hh == 0) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (rp.v[0][x].y != 0.f)
+                        add(rp.v[0][x], early.f[x]);
+                i = 2;
+            }
+        }
+        for (; i < n; ++i) {
+            const float2 v = state(i);
             if (v.y == 0.f)   // (its O is undefined)
                 continue;
-            wt[hh] = dec::dec_ex2(v.x - M[hh]);
-            L[hh] += v.y * wt[hh];
-            po[hh] = reinterpret_cast<const float *>(part_o(pa.part, pr[hh].slot + (i >> two[hh]), pr[hh].x0() + (i & two[hh])) +
-                                                     (cq >> 2) * 128 + pr[hh].pr()) + (cq & 3);
+            const float *po = rp.o(pa, hh, i, cq);
+            float2 f[16];
+#pragma unroll
+            for (int nn = 0; nn < 16; ++nn)
+                f[nn] = *reinterpret_cast<const float2 *>(po + nn * 1024);
+            add(v, f);
         }
-#pragma unroll
-        for (int n0 = 0; n0 < 16; n0 += 8) {   // both rows' loads before their use
-            float2 f[2][8];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int nn = 0; nn < 8; ++nn)
-                    f[hh][nn] = po[hh] ? *reinterpret_cast<const float2 *>(po[hh] + (n0 + nn) * 2 * 128 * 4) : make_float2(0.f, 0.f);
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int nn = 0; nn < 8; ++nn) {
-                    o[n0 + nn][2 * hh] = fmaf(f[hh][nn].x, wt[hh], o[n0 + nn][2 * hh]);
-                    o[n0 + nn][2 * hh + 1] = fmaf(f[hh][nn].y, wt[hh], o[n0 + nn][2 * hh + 1]);
-                }
-        }
-    }
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        const int r = r_first + 8 * hh;
-        if (r >= m_rows)
-            continue;
-        if ((lane & 3) == 0 && !(L[hh] > 0.f && L[hh] < INFINITY))
+        if ((lane & 3) == 0 && !(L > 0.f && L < INFINITY))
             atomicCAS(a.err, kDevOk, kDevBadInput);
-        const float inv = 1.f / L[hh];
+        const float inv = 1.f / L;
         const int tk = r / G;
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
                              (((int64_t)l * a.total_q + rq.q_off + tk) * a.n_q_heads + h * G + (r - tk * G)) * kSpD + cq;
@@ -914,8 +938,8 @@ __global__ void __launch_bounds__(kOwThreads, 3)
             }
         }
 
-        const RowParts parts = row_parts(pa, groups[rq.group], rq, lh_s, r0 + ra, r0 + rows);
-        finish_rows(a, pa, parts, rq, lh_s, r0 + ra, r0 + rows, o, m_run, l_run);
+        const RowParts parts = row_parts<2>(pa, groups[rq.group], rq, lh_s, r0 + ra, r0 + rows);
+        finish_rows<2>(a, pa, parts, NoEarlyO{}, rq, lh_s, r0 + ra, r0 + rows, o, m_run, l_run);
     }
 }
 
@@ -942,6 +966,8 @@ __device__ __forceinline__ uint32_t od_off(int r, int c)
 }
 }  // namespace
 
+// kTwo: more than 8 query rows (both halves of an MMA row tile hold some)
+template <bool kTwo>
 __global__ void __launch_bounds__(kOdThreads, 1)
     k_shared_own_decode(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                         const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
@@ -1011,34 +1037,47 @@ __global__ void __launch_bounds__(kOdThreads, 1)
     issue();
 
     // rows ra, rb and columns cq, cq + 1 (+ 8) of the MMA fragments
+    constexpr int NH = kTwo ? 2 : 1;   // row halves with rows in them
     const int ra = lane >> 2, rb = ra + 8, cq = (lane & 3) * 2, mi = lane >> 3;
     const float sc = a.scale_log2;
-    int k = 0;   // steps done
-    bool ok = true;
-    for (int it = it0; it < it1 && ok; ++it) {
-        const DevShared rq = reqs[it / pa.lh_count];
-        if (rq.q_len == 0)
-            continue;
-        const int lh_s = it % pa.lh_count, lh = pa.lh_base + lh_s, m_rows = rq.q_len * G;
-        const int n_keys = rq.own + rq.q_len, n_t = (n_keys + kOdTile - 1) / kOdTile;
-        const int see[2] = {ra < m_rows ? rq.own + ra / G + 1 : 0, rb < m_rows ? rq.own + rb / G + 1 : 0};
+    // the piece `it`, its packed queries as the MMA's A operand
+    DevShared rq{};
+    uint32_t qa[8][4];
+    auto load_queries = [&](int it) {
+        rq = reqs[it / pa.lh_count];
+        const int m_rows = rq.q_len * G, lh = pa.lh_base + it % pa.lh_count;
         const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(pa.q_rot) + ((int64_t)lh * a.total_q + rq.q_off) * G * kSpD;
-        uint32_t qa[8][4];
 #pragma unroll
         for (int kb = 0; kb < 8; ++kb) {
             auto ld2 = [&](int r, int c) -> uint32_t {
                 return r < m_rows ? *reinterpret_cast<const uint32_t *>(qp + r * kSpD + c) : 0u;
             };
             qa[kb][0] = ld2(ra, kb * 16 + cq);
-            qa[kb][1] = ld2(rb, kb * 16 + cq);
+            qa[kb][1] = kTwo ? ld2(rb, kb * 16 + cq) : 0u;
             qa[kb][2] = ld2(ra, kb * 16 + cq + 8);
-            qa[kb][3] = ld2(rb, kb * 16 + cq + 8);
+            qa[kb][3] = kTwo ? ld2(rb, kb * 16 + cq + 8) : 0u;
         }
-        if (!waited) {   // for the prefix's partial results
-            pdl_wait_prerequisites();
-            waited = true;
+    };
+    if (it0 < it1)
+        load_queries(it0);
+    if (!waited)   // for the prefix's partial results
+        pdl_wait_prerequisites();
+    int k = 0;   // steps done
+    bool ok = true;
+    for (int it = it0; it < it1 && ok; ++it) {
+        if (rq.q_len == 0) {
+            if (it + 1 < it1)
+                load_queries(it + 1);
+            continue;
         }
-        const RowParts parts = row_parts(pa, groups[rq.group], rq, lh_s, ra, m_rows);
+        const DevShared req = rq;
+        const int lh_s = it % pa.lh_count, m_rows = req.q_len * G;
+        const int n_keys = req.own + req.q_len, n_t = (n_keys + kOdTile - 1) / kOdTile;
+        const int see[2] = {ra < m_rows ? req.own + ra / G + 1 : 0, rb < m_rows ? req.own + rb / G + 1 : 0};
+        // the first two partial results of the rows are on their way meanwhile
+        const RowParts parts = row_parts<NH>(pa, groups[req.group], req, lh_s, ra, m_rows);
+        EarlyO<NH> early;
+        early.load(pa, parts, cq);
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
         float o[16][4];
 #pragma unroll
@@ -1069,48 +1108,48 @@ __global__ void __launch_bounds__(kOdThreads, 1)
                     mma_bf16(c[nb + 1], qa[kb], b2, b3);
                 }
             }
-            float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int kk = j * kOdTile + 8 * nb + cq + (e & 1);
-                    c[nb][e] = kk < see[e >> 1] ? c[nb][e] * sc : -INFINITY;
-                    mx[e >> 1] = fmaxf(mx[e >> 1], c[nb][e]);
-                }
-            }
-            float corr[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                const float m_new = fmaxf(m_run[h], mx[h]);
-                corr[h] = m_new == -INFINITY ? 1.f : dec_ex2(m_run[h] - m_new);
-                m_run[h] = m_new;
-            }
-            const float nm[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
-            float sum[2] = {0.f, 0.f};
+            float corr[2], nm[2];
             uint32_t p[2][4];
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                const float p0 = dec_ex2(c[nb][0] + nm[0]), p1 = dec_ex2(c[nb][1] + nm[0]);
-                const float p2 = dec_ex2(c[nb][2] + nm[1]), p3 = dec_ex2(c[nb][3] + nm[1]);
-                sum[0] += p0 + p1;
-                sum[1] += p2 + p3;
-                p[nb >> 1][(nb & 1) * 2 + 0] = pack2(p0, p1);
-                p[nb >> 1][(nb & 1) * 2 + 1] = pack2(p2, p3);
-            }
+            for (int h = 0; h < NH; ++h) {
+                float mx = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)   // (this lane's keys only: added up over the quad at the end)
-                l_run[h] = l_run[h] * corr[h] + sum[h];
+                for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int kk = j * kOdTile + 8 * nb + cq + e;
+                        float &s = c[nb][2 * h + e];
+                        s = kk < see[h] ? s * sc : -INFINITY;
+                        mx = fmaxf(mx, s);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m_new = fmaxf(m_run[h], mx);
+                corr[h] = m_new == -INFINITY ? 1.f : dec_ex2(m_run[h] - m_new);
+                m_run[h] = m_new;
+                nm[h] = m_new == -INFINITY ? 0.f : -m_new;
+                float sum = 0.f;
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+                    const float p0 = dec_ex2(c[nb][2 * h] + nm[h]), p1 = dec_ex2(c[nb][2 * h + 1] + nm[h]);
+                    sum += p0 + p1;
+                    p[nb >> 1][(nb & 1) * 2 + h] = pack2(p0, p1);
+                }
+                l_run[h] = l_run[h] * corr[h] + sum;   // (this lane's keys only: added up over the quad at the end)
+            }
+            if (!kTwo) {   // the other row half: no rows, no weights
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    p[x][1] = p[x][3] = 0u;
+            }
             if (j > 0) {
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                    o[n][0] *= corr[0];
-                    o[n][1] *= corr[0];
-                    o[n][2] *= corr[1];
-                    o[n][3] *= corr[1];
-                }
+                for (int n = 0; n < 16; ++n)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        o[n][2 * h] *= corr[h];
+                        o[n][2 * h + 1] *= corr[h];
+                    }
             }
 #pragma unroll
             for (int kb2 = 0; kb2 < 2; ++kb2) {
@@ -1129,7 +1168,9 @@ __global__ void __launch_bounds__(kOdThreads, 1)
         }
         if (!ok)
             break;
-        finish_rows(a, pa, parts, rq, lh_s, ra, m_rows, o, m_run, l_run);
+        if (it + 1 < it1)
+            load_queries(it + 1);   // on their way during the end of this piece
+        finish_rows<NH>(a, pa, parts, early, req, lh_s, ra, m_rows, o, m_run, l_run);
         __syncwarp();
     }
     if (!ok) {   // nothing is in flight when the CTA leaves
@@ -1160,7 +1201,9 @@ static cudaError_t shared_attrs()
     if ((e = cudaFuncSetAttribute(k_shared_prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmem)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(k_shared_own_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, ow_bytes(kOwTileMax))) !=
             cudaSuccess ||
-        (e = cudaFuncSetAttribute(k_shared_own_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, kOdSmem)) != cudaSuccess)
+        (e = cudaFuncSetAttribute(k_shared_own_decode<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOdSmem)) !=
+            cudaSuccess ||
+        (e = cudaFuncSetAttribute(k_shared_own_decode<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOdSmem)) != cudaSuccess)
         return e;
     if (dev < 64)
         done[dev].store(true, std::memory_order_release);
@@ -1212,7 +1255,7 @@ cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s)
         const int64_t items = (int64_t)a.n_reqs * pa.lh_count;
         if (items > 0x7fffffff)
             return cudaErrorInvalidValue;
-        return launch_pdl(k_shared_own_decode, std::min<int64_t>(items, t.n_sms), kOdThreads, kOdSmem, pdl, s, map(t.tmap_k),
+        return launch_pdl(rows <= 8 ? k_shared_own_decode<false> : k_shared_own_decode<true>, std::min<int64_t>(items, t.n_sms), kOdThreads, kOdSmem, pdl, s, map(t.tmap_k),
                           map(t.tmap_v), a, *t.reqs, pa, *t.groups);
     }
     // tiles that just hold the longest own part, cut evenly (a smaller tile
