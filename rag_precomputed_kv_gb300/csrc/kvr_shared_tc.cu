@@ -12,21 +12,22 @@
 //                      keys (rotated) and values at own row S_b + t.
 //   k_shared_prefix    the prefix part.  The packed rows of a whole group are
 //                      consecutive: M = tokens of the group x G rows meet each
-//                      prefix tile once, in blocks of 256 rows.  tcgen05, as
-//                      the query-prefill attention: two 128-row tiles A and B
-//                      per CTA, S and P and O in TMEM.  A block of at most 128
-//                      rows (a decode step of a few requests) is bound by the
-//                      reads of K and V, not by the MMAs: then A and B hold the
-//                      same rows and take alternate key tiles, so that one
-//                      tile's softmax overlaps the other's.  The work, all
+//                      prefix tile once, in blocks of up to 256 rows.
+//                      tcgen05, as the query-prefill attention: 128-row tiles
+//                      A and B per CTA, S and P and O in TMEM.  The work, all
 //                      (block, key tile) pairs of the call in a row, is cut in
 //                      equal stretches, one per SM; a block that a stretch ends
 //                      in has several partial results.
-//   k_shared_own       the own part, and the sum of everything.  One CTA per
-//                      (request, layer, kv-head, row tile); at a few rows per
-//                      request this streams the own rows through register-
-//                      resident warp MMAs (as the decode step), then adds the
-//                      prefix's partial results and writes the output.
+//   k_shared_own_*     the own part, and the sum of everything: the own rows
+//                      through register-resident warp MMAs (as the decode
+//                      step), then the prefix's partial results are added and
+//                      the output written.
+//
+// A block of at most 128 rows (a decode step of a few requests) uses tile A
+// alone: its time is the reads of K and V.  (Both tiles on the same rows and
+// alternate key tiles, so that one's softmax overlaps the other's: 736 us
+// against 695 for 64 rows on 33,248 prefix rows and 256 units, 105 against 95
+// for 7 rows on 8,256 and 112 units: twice the partial results, for nothing.)
 //
 // Values behind the last prefix row are zeroed in shared memory before the
 // P V product that reaches them (a masked key's weight is 0, but 0 x NaN is
@@ -111,7 +112,7 @@ struct Seg {
     int lh;          // (layer, kv-head), within the call's slice
     int row0;        // first packed row of the block in the group
     int rows;        // rows of the block (<= 256)
-    bool dual;       // <= 128 rows: tiles A and B take alternate key tiles
+    int nx;          // its 128-row tiles: A, or A and B
     int jb, je;      // key tiles
     int64_t item;    // block index in the call
     int64_t next;    // the stretch's next pair
@@ -138,7 +139,7 @@ __device__ __forceinline__ Seg seg_at(const SharedPrefixArgs &a, const DevGroup 
     s.item = (int64_t)s.lh * a.unit_blocks + s.g.item0 + blk;
     s.row0 = blk * 256;
     s.rows = min(256, s.g.rows - s.row0);
-    s.dual = s.rows <= 128;
+    s.nx = s.rows > 128 ? 2 : 1;
     return s;
 }
 
@@ -190,13 +191,14 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         for (int64_t w = w_begin; w < w_end && ok;) {
             const Seg sg = seg_at(a, groups, w, w_end);
             w = sg.next;
-            const int j0 = sg.jb + (sg.dual ? x : 0), step = sg.dual ? 2 : 1;
-            const bool row_ok = (sg.dual ? r : x * 128 + r) < sg.rows;
+            if (x >= sg.nx)
+                continue;
+            const bool row_ok = x * 128 + r < sg.rows;
             // a warp without rows of its own only keeps the barriers going: what it
             // leaves in its lanes of P meets its own lanes of O alone
-            const bool idle = (sg.dual ? 0 : x * 128) + (warp & 3) * 32 >= sg.rows;
+            const bool idle = x * 128 + (warp & 3) * 32 >= sg.rows;
             float m_run = -INFINITY, l_run = 0.f;
-            for (int j = j0; j < sg.je; j += step) {
+            for (int j = sg.jb; j < sg.je; ++j) {
                 if (!mbar_wait(bar(kSbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
                     ok = false;
                     break;
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 // lazy maximum: O and l are rescaled only when it grows by more than
                 // the threshold
                 float corr = 1.f;
-                if (j == j0) {
+                if (j == sg.jb) {
                     m_run = mxs;
                 } else if (mxs > m_run + kSpRescale) {
                     corr = ex2(m_run - mxs);
@@ -282,8 +284,6 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             const int64_t slot = sg.item + blockIdx.x;
             if (row_ok)
                 part_ml(a.part, slot, x)[r] = make_float2(m_run, l_run);
-            if (j0 >= sg.je)
-                continue;   // no key tile for B: its maximum is -inf, its sum 0
             if (!mbar_wait(bar(kSbO + x), (uint32_t)o_cnt & 1, abort_flag)) {
                 ok = false;
                 break;
@@ -329,10 +329,9 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                             ok = false;
                             break;
                         }
-                        const int nx = sg.dual ? 1 : 2;
                         const int q0 = (int)(((int64_t)(a.lh_base + sg.lh) * a.total_q + sg.g.q_off) * a.group + sg.row0);
-                        mbar_expect_tx(bar(kSbQ), (uint32_t)(nx * kSpTileBytes));
-                        for (int x = 0; x < nx; ++x) {
+                        mbar_expect_tx(bar(kSbQ), (uint32_t)(sg.nx * kSpTileBytes));
+                        for (int x = 0; x < sg.nx; ++x) {
                             const uint32_t dst = sbase + (uint32_t)(kSpOffQ + x * kSpTileBytes);
                             tma_load_2d(dst, &tmq, 0, q0 + x * kSpTile, bar(kSbQ));
                             tma_load_2d(dst + kSpPanel, &tmq, 64, q0 + x * kSpTile, bar(kSbQ));
@@ -375,9 +374,9 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             tc_fence_after();
             return true;
         };
-        // S_x = Q_qx K^T with K the ring's load k
-        auto issue_s = [&](int x, int qx, int k) {
-            const uint32_t qa = lo_k + ((uint32_t)(kSpOffQ + qx * kSpTileBytes) >> 4);
+        // S_x = Q_x K^T with K the ring's load k
+        auto issue_s = [&](int x, int k) {
+            const uint32_t qa = lo_k + ((uint32_t)(kSpOffQ + x * kSpTileBytes) >> 4);
             const uint32_t kb = lo_k + ((uint32_t)(kSpOffKV + (k % kSpSlots) * kSpTileBytes) >> 4);
 #pragma unroll
             for (int i = 0; i < kSpD / 16; ++i) {
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         for (int64_t w = w_begin; w < w_end && ok;) {
             const Seg sg = seg_at(a, groups, w, w_end);
             w = sg.next;
-            const int K = sg.je - sg.jb, step = sg.dual ? 2 : 1;
+            const int K = sg.je - sg.jb;
             // V tile i of the segment: landed, its rows behind the prefix zeroed
             auto wait_v = [&](int i) -> bool {
                 if (!wait_kv(tt + 2 * i + 1))
@@ -429,57 +428,53 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             ++nq;
             tc_fence_after();
             // the first S of each tile
-            for (int x = 0; x < 2 && ok; ++x) {
-                const int i = sg.dual ? x : 0;
-                if (i >= K)
-                    continue;
-                if (!o_free(x) || ((sg.dual || x == 0) && !wait_kv(tt + 2 * i))) {
-                    ok = false;
-                    break;
-                }
-                issue_s(x, sg.dual ? 0 : x, tt + 2 * i);
-                if (sg.dual)
-                    umma_commit(lead, bar(kSbEmpty + (tt + 2 * i) % kSpSlots));
+            ok = wait_kv(tt);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                ok = ok && (x >= sg.nx || o_free(x));
+                if (ok && x < sg.nx)
+                    issue_s(x, tt);
             }
             if (!ok)
                 break;
-            if (!sg.dual)
-                umma_commit(lead, bar(kSbEmpty + tt % kSpSlots));
-            if (K <= step)
+            umma_commit(lead, bar(kSbEmpty + tt % kSpSlots));
+            if (K == 1)
                 umma_commit(lead, bar(kSbQEmpty));
             for (int i = 0; i < K && ok; ++i) {
-                bool v_ready = false, k_ready = false;
-                const bool more = i + step < K;
-                for (int x = sg.dual ? i & 1 : 0; x < (sg.dual ? (i & 1) + 1 : 2); ++x) {
+                const bool more = i + 1 < K;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x >= sg.nx)
+                        break;
                     if (!mbar_wait(bar(kSbP + x), (uint32_t)p_cnt[x] & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
                     ++p_cnt[x];
-                    if (!v_ready && !(v_ready = wait_v(i))) {
+                    if (x == 0 && !wait_v(i)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    issue_pv(x, tt + 2 * i + 1, i >= step);
+                    issue_pv(x, tt + 2 * i + 1, i > 0);
                     if (!more) {
                         umma_commit(lead, bar(kSbO + x));
                         o_used[x] = true;
                     } else {
-                        if (!k_ready && !(k_ready = wait_kv(tt + 2 * (i + step)))) {
+                        if (x == 0 && !wait_kv(tt + 2 * i + 2)) {
                             ok = false;
                             break;
                         }
-                        issue_s(x, sg.dual ? 0 : x, tt + 2 * (i + step));
+                        issue_s(x, tt + 2 * i + 2);
                     }
                 }
                 if (!ok)
                     break;
-                if (more && i + step + 1 == K)
+                if (i + 2 == K)
                     umma_commit(lead, bar(kSbQEmpty));   // the segment's last S is issued
                 umma_commit(lead, bar(kSbEmpty + (tt + 2 * i + 1) % kSpSlots));
                 if (more)
-                    umma_commit(lead, bar(kSbEmpty + (tt + 2 * (i + step)) % kSpSlots));
+                    umma_commit(lead, bar(kSbEmpty + (tt + 2 * i + 2) % kSpSlots));
             }
             tt += 2 * K;
         }
@@ -573,32 +568,26 @@ constexpr int kOwTileMax = 128;   // keys per tile
 // 128B-swizzled panels each), the barrier.
 __host__ __device__ constexpr int ow_bytes(int tile_keys) { return tile_keys * 512 + 16 + 1024; }
 
-// Where the partial results of one row lie: slots [slot, slot + n), tiles x0..x1,
-// row pr of each.
+// Where the partial results of one row lie: slots [slot, slot + n), row `in` of
+// each (of its two tiles).
 struct PartRef {
     int64_t slot;
-    int n, where;    // where: pr | x0 << 8 | x1 << 9
-    __device__ __forceinline__ int pr() const { return where & 127; }
-    __device__ __forceinline__ int x0() const { return (where >> 8) & 1; }
-    __device__ __forceinline__ int x1() const { return (where >> 9) & 1; }
+    int n, in;
 };
-static_assert(sizeof(PartRef) == 16, "row reference");
 
 __device__ __forceinline__ PartRef part_ref(const SharedPrefixArgs &pa, const DevGroup &g, int lh_s, int group_row)
 {
     PartRef r{0, 0, 0};
     if (g.nt == 0)
         return r;
-    const int blk = group_row >> 8, in = group_row & 255;
-    const bool dual = min(256, g.rows - 256 * blk) <= 128;
+    const int blk = group_row >> 8;
     const int64_t it = (int64_t)lh_s * pa.unit_blocks + g.item0 + blk;
     const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.nt;
     const int ca = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0);
     const int cb = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0 + g.nt - 1);
     r.slot = it + ca;
     r.n = cb - ca + 1;
-    const int x0 = dual ? 0 : in >> 7, x1 = dual ? 1 : x0;
-    r.where = (in & 127) | x0 << 8 | x1 << 9;
+    r.in = group_row & 255;
     return r;
 }
 
@@ -616,17 +605,16 @@ struct RowParts {
     PartRef pr[2];
     float2 v[2][2];   // (max, sum) of the first two partial results (none: -inf, 0)
 
-    __device__ __forceinline__ int two(int hh) const { return pr[hh].x1() - pr[hh].x0(); }
-    __device__ __forceinline__ int n(int hh) const { return pr[hh].n << two(hh); }
+    __device__ __forceinline__ int n(int hh) const { return pr[hh].n; }
     __device__ __forceinline__ float2 ml(const SharedPrefixArgs &pa, int hh, int i) const
     {
-        return part_ml(pa.part, pr[hh].slot + (i >> two(hh)), pr[hh].x0() + (i & two(hh)))[pr[hh].pr()];
+        return part_ml(pa.part, pr[hh].slot + i, pr[hh].in >> 7)[pr[hh].in & 127];
     }
     // columns cq, cq + 1 of partial result i; the next 8 columns are 1024 floats on
     __device__ __forceinline__ const float *o(const SharedPrefixArgs &pa, int hh, int i, int cq) const
     {
-        return reinterpret_cast<const float *>(part_o(pa.part, pr[hh].slot + (i >> two(hh)), pr[hh].x0() + (i & two(hh))) +
-                                               (cq >> 2) * 128 + pr[hh].pr()) + (cq & 3);
+        return reinterpret_cast<const float *>(part_o(pa.part, pr[hh].slot + i, pr[hh].in >> 7) + (cq >> 2) * 128 +
+                                               (pr[hh].in & 127)) + (cq & 3);
     }
 };
 template <int NH>
@@ -649,7 +637,6 @@ __device__ __forceinline__ RowParts row_parts(const SharedPrefixArgs &pa, const 
 
 // The O of the first two partial results of a row tile's first row half, in
 // registers ahead of their use.
-template <int NH>
 struct EarlyO {
     float2 f[2][16];
     __device__ __forceinline__ void load(const SharedPrefixArgs &pa, const RowParts &rp, int cq)
@@ -1076,7 +1063,7 @@ __global__ void __launch_bounds__(kOdThreads, 1)
         const int see[2] = {ra < m_rows ? req.own + ra / G + 1 : 0, rb < m_rows ? req.own + rb / G + 1 : 0};
         // the first two partial results of the rows are on their way meanwhile
         const RowParts parts = row_parts<NH>(pa, groups[req.group], req, lh_s, ra, m_rows);
-        EarlyO<NH> early;
+        EarlyO early;
         early.load(pa, parts, cq);
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
         float o[16][4];
