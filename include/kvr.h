@@ -46,8 +46,9 @@
  *          call).  A call with more than the scratch holds waits for the
  *          previous call's attention, frees it and allocates it larger.
  *          kvr_shared_query_attention uses the same scratch, and beside it up
- *          to 1 GiB for partial results, grown the same way (134 KB for each
- *          256 query rows of a group, (layer, kv-head) and slice).
+ *          to 1 GiB for partial results, grown the same way (133 KB for each
+ *          256 query rows of a group and (layer, kv-head), and for each SM;
+ *          more than 1 GiB only where one (layer, kv-head) needs it).
  *       5. A pool in pinned host memory: the first kvr_prefill on it creates
  *          an internal stream and its events (kept until unregister).
  *     kvr_pool_reserve makes 3 and 4 happen up front: afterwards, calls
@@ -362,7 +363,11 @@ KVR_API kvr_status kvr_prefill(kvr_pool_t pool, int32_t batch, const int32_t *sp
  * inside the kernels' parameters.
  * On a stream that is being captured the call returns KVR_ERR_UNSUPPORTED when
  * it would have to bind the pool, upload tables or use library scratch.
- * Errors: KVR_ERR_INVALID_ARG (also: the caches or `out` overlap the prefix),
+ * A NaN or an infinity among a request's new values may reach every query token
+ * of that request's call (a weight of 0 times it is NaN), on other requests it
+ * has no effect; neither has what a block holds behind its last row.
+ * Errors: KVR_ERR_INVALID_ARG (also: the caches or `out` overlap the prefix or
+ * each other),
  * KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA; kvr_check reports
  * KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for kvr_query_attention.
  */

@@ -1634,6 +1634,10 @@ extern "C" kvr_status kvr_shared_query_attention(kvr_pool_t p, int32_t n_groups,
             for (const Range &x : src)
                 if (any_prefix && d.meets(x))
                     return fail(KVR_ERR_INVALID_ARG, "the cache or the output overlaps the shared prefix");
+        for (int i = 0; i < 3; ++i)
+            for (int j = 0; j < i; ++j)
+                if (dst[i].meets(dst[j]))
+                    return fail(KVR_ERR_INVALID_ARG, "the caches and the output overlap");
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const bool may_tc = attention_tc_supported(p->d.dtype, D);
         if ((st = check_capture(*p, s, !may_tc && batch <= kInlineEntries,

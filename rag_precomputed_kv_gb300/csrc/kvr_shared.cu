@@ -12,8 +12,8 @@
 // query token, query head), the keys split in four stretches; each lane holds
 // head_dim / 32 elements; eight keys at a time, so that their loads and
 // reductions over the warp overlap; online softmax in fp32, the warps' states
-// added in warp order.  (One warp per row, four keys at a time: 45 us against 8
-// on a 200-row cache, all of it latency.)
+// added in warp order.  (One warp per row, four keys at a time: 47 us a call
+// against 20.6 on three requests with 200 rows each, all of it latency.)
 #include <cuda_bf16.h>
 
 #include "kvr_internal.cuh"
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(128)
     const int tok = (int)((w / Hq) % a.total_q);
     const int l = (int)(w / Hq / a.total_q);
 
-    // the request of this token: the last one that starts at or before it and has tokens
+    // the request of this token: the last one that starts at or before it
     int lo = 0, hi = a.n_reqs - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -55,8 +55,6 @@ __global__ void __launch_bounds__(128)
         else
             hi = mid - 1;
     }
-    while (lo > 0 && reqs[lo].q_len == 0)
-        --lo;
     const DevShared rq = reqs[lo];
     const int t = tok - rq.q_off;
     const int pos = rq.pre_len + rq.own + t;

@@ -55,6 +55,7 @@ def shared(lib, h, go=(0, 2), po=(0, 100), pl=(90,), co=(0, 20, 40), own=(3, 4),
     (dict(q=None), 1), (dict(q=C + 2), 1), (dict(kq=None), 1), (dict(ck=Dp + 8), 1), (dict(out=None), 1),
     (dict(pk=None), 1), (dict(pv=Bp + 2), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
     (dict(scale=float("inf")), 1), (dict(ck=A), 1), (dict(out=Bp), 1), (dict(cv=A + 128 * 2 * 4 * 99), 1),
+    (dict(cv=Dp), 1), (dict(cv=Dp + 128 * 2 * 4 * 39), 1), (dict(out=E + 64), 1),
 ])
 def test_shared_query_attention_refuses(lib, pool, kw, status):
     assert shared(lib, pool, **kw) == status

@@ -92,8 +92,9 @@ def _check_attention(got, ref, A, qk, n, dtype, D):
 # shared prefix
 # ---------------------------------------------------------------------------
 def _shared_case(L, H, G, D, dtype, groups, prefix, own, q, il=False, theta=THETA, scale=0.0, seed=1, spread=1.0,
-                 stream=None, spare=3, pool=None, dev_q=True):
-    """groups: requests per group; prefix per group; own and q per request."""
+                 stream=None, spare=3, pool=None, check=None):
+    """groups: requests per group; prefix per group; own and q per request.
+    check: the requests whose results are compared (None: all)."""
     import torch
     B, LH, T = sum(groups), L * H, int(sum(q))
     go, po = _starts(groups).astype(np.int32), _starts([p + 2 for p in prefix])
@@ -119,10 +120,11 @@ def _shared_case(L, H, G, D, dtype, groups, prefix, own, q, il=False, theta=THET
     pool.check()
     sc = scale if scale > 0 else D ** -0.5
     e2 = n2 = 0.0
-    outn = to_np64(out)
     for g in range(len(groups)):
         Kp, Vp = (to_np64(_block(x, po, g, LH))[:, :prefix[g]] for x in (pk, pv))
         for b in range(int(go[g]), int(go[g + 1])):
+            if check is not None and b not in check:
+                continue
             S, lq, a = own[b], q[b], int(qo[b])
             gk, gv = to_np64(_block(ck, co, b, LH)), to_np64(_block(cv, co, b, LH))
             wk, wv = to_np64(_block(ck0, co, b, LH)), to_np64(_block(cv0, co, b, LH))
@@ -135,13 +137,13 @@ def _shared_case(L, H, G, D, dtype, groups, prefix, own, q, il=False, theta=THET
             kr = oracle.rope(np.moveaxis(kq, 2, 1).reshape(LH, lq, D), pos[None, :], theta, il)
             assert k_within_tolerance(gk[:, S:S + lq], kr, dtype, il)[0]
             assert np.array_equal(gv[:, S:S + lq], np.moveaxis(vq, 2, 1).reshape(LH, lq, D))
-            qr = oracle.rope(to_np64(Q[:, a:a + lq]), pos[None, :, None], theta, il)
+            qr, outn = oracle.rope(to_np64(Q[:, a:a + lq]), pos[None, :, None], theta, il), to_np64(out[:, a:a + lq])
             for u in range(LH):
                 l, h = divmod(u, H)
                 K = np.concatenate([Kp[u], gk[u, :S], kr[u]])
                 V = np.concatenate([Vp[u], gv[u, :S + lq]])
                 ref, A, qk, _ = _attention_ref(K, V, qr[l, :, h * G:(h + 1) * G], 0, prefix[g] + S, sc)
-                x, y = _check_attention(outn[l, a:a + lq, h * G:(h + 1) * G], ref, A, qk, len(K), dtype, D)
+                x, y = _check_attention(outn[l, :, h * G:(h + 1) * G], ref, A, qk, len(K), dtype, D)
                 e2, n2 = e2 + x, n2 + y
     rel = (e2 / max(n2, 1e-300)) ** 0.5
     assert rel <= (3 ** 0.5 * 2.0 ** -8 if dtype == "bf16" else 2.0 ** -17), rel
@@ -185,6 +187,14 @@ def test_shared_prefix_interleaved_pairs_far_positions_and_scale(dtype, D):
 def test_shared_prefix_query_rows_at_tile_edges(rows):
     """All requests of a group in one (layer, kv-head)'s query rows: G = 1."""
     _shared_case(1, 1, 1, 128, "bf16", groups=[rows], prefix=[260], own=[i % 3 for i in range(rows)], q=[1] * rows)
+
+
+def test_shared_prefix_in_slices():
+    """More than 1 GiB of partial results (64 units x 128 blocks of 256 rows):
+    the units go through in two slices."""
+    n = 4096
+    _shared_case(8, 8, 8, 128, "bf16", groups=[n], prefix=[130], own=[i % 3 for i in range(n)], q=[1] * n,
+                 check=(0, 1, 1500, 2047, 4095))
 
 
 def test_shared_prefix_large_scores():
@@ -322,6 +332,13 @@ def test_key_weights(name, L, H, G, D, dtype):
 @pytest.mark.parametrize("q", [1, 5, 40])
 def test_key_weights_group_sizes(G, q):
     _weights_case(1, 1, G, 128, "bf16", prefix=[333, 1500], q=[q, 1], accumulate=q == 5)
+
+
+@pytest.mark.parametrize("G,q,n", [(4, 1, 50000), (8, 1, 25500), (16, 1, 11000), (16, 2, 6200), (32, 1, 6000)])
+def test_key_weights_of_more_keys_than_tmem_holds(G, q, n):
+    """The tiles beyond what eight CTAs keep (6,144 keys each at up to 4 rows,
+    down to 640 at 32) are loaded twice; a second, short request beside it."""
+    _weights_case(1, 1, G, 128, "bf16", prefix=[n - q, 40], q=[q, 1], accumulate=G == 8)
 
 
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp32", 64)])
@@ -470,6 +487,29 @@ def test_evict_ties_and_special_weights(kind):
 
     for in_place in (False, True):
         _evict_case(1, 2, 128, "bf16", [1500, 200], [700, 60], 5, 7, weights=weights, in_place=in_place)
+
+
+def test_evict_more_rows_than_shared_memory_holds():
+    _evict_case(1, 1, 64, "bf16", [50001], [20000], 4, 64)
+    _evict_case(1, 1, 64, "bf16", [60000], [333], 4, 64, in_place=True)
+
+
+@pytest.mark.parametrize("heavy", [True, False])
+@pytest.mark.parametrize("L,H,B,n,threads", [(1, 2, 1, 20000, 1024), (4, 8, 20, 3100, 256), (1, 1, 1, 51000, 1024)])
+def test_evict_weights_unlike_their_sample(heavy, L, H, B, n, threads):
+    """A first count of an eighth of the rows says where the threshold lies;
+    here just those rows are the heavy (light) ones, and it lies elsewhere."""
+    import torch
+
+    def weights(w, co, LH):
+        n_r = -(-n // threads)
+        i = torch.arange(n, device="cuda")
+        counted = (i % (32 * n_r)) // 32 % 8 == 0
+        for b in range(B):
+            blk = _block(w, co, b, LH)[:, :n]
+            blk.mul_(torch.where(counted == heavy, 1e6, 1e-6))
+
+    _evict_case(L, H, 64, "bf16", [n] * B, [n // 2] * B, 3, 5, weights=weights)
 
 
 # ---------------------------------------------------------------------------
