@@ -99,7 +99,7 @@ struct RowVec<float> {
 // keeps and writes its rows behind the warps before it.  The rows' keys are read
 // once, into shared memory (kept in registers, the passes over them were
 // unrolled code that runs once, at the speed of instruction fetches: 65 us
-// against 33 for 256 units of 33,504 rows); a unit of more rows than fit there
+// against 52 for 256 units of 33,504 rows); a unit of more rows than fit there
 // reads them in every pass.
 constexpr int kRankMax = 256;
 constexpr int kSelSmemRows = 48 * 1024;   // 192 KB
@@ -504,9 +504,11 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
     const int64_t move = a.in_place ? ctas : a.n_chunks;
     if (ctas > 0x7fffffff || move > 0x7fffffff)
         return cudaErrorInvalidValue;
-    // Small CTAs when there are several units per SM (eight resident hide each
-    // other's barriers), large ones when a unit has an SM to itself.
-    const bool small = a.max_n <= 24 * 256 && ctas >= 4 * (int64_t)n_sms;
+    // Small CTAs when there are several units per SM (up to eight resident hide
+    // each other's barriers), large ones when a unit has an SM to itself: 1,344
+    // rows, 4,608 units: 417 us a call against 510; 2,656 rows: 336 units 70.5
+    // against 74, 224 units alike, 112 units 31.3 against 28.8.
+    const bool small = a.max_n <= 24 * 256 && ctas >= 2 * (int64_t)n_sms;
     const int threads = small ? 256 : 1024;
     const int rows = (a.max_n + 4 * threads - 1) / (4 * threads) * 4 * threads;   // of keys in shared memory
     const bool smem = rows <= kSelSmemRows;

@@ -64,17 +64,18 @@ struct WtCfg {
     static constexpr int kSlots = NC == 32 ? 5 : 6;                  // K panels in flight
     static constexpr int kStages = NC == 32 ? 1 : 2;                 // products in TMEM that wait for pass 1
     static constexpr int kKept = (kWtTmemCols - kStages * NQ) / NC;  // tiles whose scores stay in TMEM behind them
+    static constexpr int kMaxCluster = NC == 32 ? 4 : kWtMaxCluster;
     static constexpr int kQPanel = NQ * 128;                         // the terms' rows x 64 dims
     static constexpr int kOffRing = 2 * kQPanel;
     static constexpr int kOffBar = kOffRing + kSlots * kWtPanel;
-    // full[slots], empty[slots], s_full[stages], s_free[stages], q_full, q_empty, peers, drain
-    static constexpr int kNumBars = 2 * kSlots + 2 * kStages + 4;
+    // full[slots], empty[slots], s_full[stages], s_free[stages], q_full, peers, drain
+    static constexpr int kNumBars = 2 * kSlots + 2 * kStages + 3;
     static constexpr int kOffMisc = kOffBar + 8 * kNumBars;          // TMEM address, abort flag
     static constexpr int kOffRef = (kOffMisc + 8 + 15) & ~15;        // [4][NC] reference per warp
     static constexpr int kOffStat = kOffRef + 4 * NC * 4;            // [4][NC] (reference, sum) per warp
     static constexpr int kOffFin = kOffStat + 4 * NC * 8;            // [NC] lse
-    static constexpr int kOffPeer = kOffFin + NC * 4;                // [2][kWtMaxCluster][NC] (max, sum)
-    static constexpr int kSmem = kOffPeer + 2 * kWtMaxCluster * NC * 8;
+    static constexpr int kOffPeer = kOffFin + NC * 4;                // [kMaxCluster][NC] (max, sum)
+    static constexpr int kSmem = kOffPeer + kMaxCluster * NC * 8;
     static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     const uint32_t sbase = smem_u32(wt_smem);
     auto bar = [&](int i) { return sbase + C::kOffBar + 8u * (uint32_t)i; };
     constexpr int bFull = 0, bEmpty = C::kSlots, bSFull = 2 * C::kSlots, bSFree = bSFull + C::kStages,
-                  bQFull = bSFree + C::kStages, bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bQFull + 3;
+                  bQFull = bSFree + C::kStages, bPeers = bQFull + 1, bDrain = bQFull + 2;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(wt_smem + C::kOffMisc + 4);
     float *s_ref = reinterpret_cast<float *>(wt_smem + C::kOffRef);
     float2 *s_stat = reinterpret_cast<float2 *>(wt_smem + C::kOffStat);
@@ -302,16 +303,15 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     const int lh = unit_i % units;
     const int G = a.n_q_heads / a.n_kv_heads;
     const int m_rows = rq.q_len * G, n = rq.prefix + rq.q_len;
-    const int n_rb = (m_rows + NC - 1) / NC;                 // row blocks
     const int nt = (n + kWtTile - 1) / kWtTile;
     const int t_lo = (int)((int64_t)rank * nt / n_cluster), t_hi = (int)((int64_t)(rank + 1) * nt / n_cluster);
     const int T = t_hi - t_lo;                               // this CTA's key tiles
-    const int n_redo = max(0, T - C::kKept);                 // loaded a second time, for each row block
+    const int n_redo = max(0, T - C::kKept);                 // loaded a second time
     const int64_t blk = rq.cache_row0 + (int64_t)lh * rq.cap;
-    // job i of a row block: tiles T-1 .. 0 for the statistics, then kKept .. T-1
-    // again; its product goes to stage (job of the CTA) % kStages
+    // job i: tiles T-1 .. 0 for the statistics, then kKept .. T-1 again; its
+    // product goes to stage i % kStages
     auto job_tile = [&](int i) { return i < T ? T - 1 - i : C::kKept + (i - T); };
-    const int n_jobs = T + n_redo;
+    const int n_jobs = m_rows > 0 ? T + n_redo : 0;
 
     if (warp < 4) {
         const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
@@ -323,14 +323,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         if (m_rows == 0 && !a.accumulate)   // a sum over no queries
             for (int j = t_lo * kWtTile + (int)threadIdx.x; j < min(n, t_hi * kWtTile); j += 128)
                 wp[j] = 0.f;
-        for (int rb = 0; rb < n_rb && ok; ++rb) {
-            const int r0 = rb * NC, nr = min(NC, m_rows - r0);
-            if (rb > 0 && !mbar_wait(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag)) {
-                ok = false;
-                break;
-            }
-            // ---- the row block's queries: rotated, split in three bf16 terms ----
-            prepare_queries<3, C::kTermRows>(a, rq, l, h, G, r0, nr, sbase, (uint32_t)(C::kTermRows * 128), (uint32_t)C::kQPanel);
+        if (m_rows > 0) {   // the same for the whole cluster; at most NC rows
+            // ---- the queries: rotated, split in three bf16 terms ----
+            prepare_queries<3, C::kTermRows>(a, rq, l, h, G, 0, m_rows, sbase, (uint32_t)(C::kTermRows * 128), (uint32_t)C::kQPanel);
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
 
@@ -409,7 +404,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                     keep(kept_at(t), s);
                 free_job(job);
                 if (edge)
-                    mask(j >= n ? NC : (j - rq.prefix) * G - r0, s);
+                    mask(j >= n ? NC : (j - rq.prefix) * G, s);
                 float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
@@ -436,8 +431,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 for (int c = 0; c < NC; ++c)
                     ls[c] += ex2(s[c] - ref[c]);
             }
+            // (a thread whose wait ran out goes on to the barriers below with the others)
             if (!ok)
-                break;
+                give_up(a.err, abort_flag);
             tmem_wait_st();
             {
                 const float r = warp_sums<NC>(ls, lane);
@@ -446,7 +442,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             }
             softmax_sync();
             // ---- the CTA's (max, sum) of row c to every CTA of the cluster ----
-            const uint32_t peer = sbase + C::kOffPeer + (uint32_t)((rb & 1) * kWtMaxCluster * NC * 8);
+            const uint32_t peer = sbase + C::kOffPeer;
             if (threadIdx.x < NC) {
                 const int c = threadIdx.x;
                 float M = kWtUnset, L = 0.f;
@@ -465,9 +461,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                                      mapa_rank(bar(bPeers), (uint32_t)x))
                                  : "memory");
                 }
-                if (wait_peers(bar(bPeers), (uint32_t)rb & 1, abort_flag)) {
+                if (wait_peers(bar(bPeers), 0, abort_flag)) {
                     float Mt = kWtUnset, Lt = 0.f;
-                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + C::kOffPeer) + (rb & 1) * kWtMaxCluster * NC + c;
+                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + C::kOffPeer) + c;
                     for (int x = 0; x < n_cluster; ++x)
                         Mt = fmaxf(Mt, pv[x * NC].x);
                     for (int x = 0; x < n_cluster; ++x) {   // in rank order: one rounding order
@@ -475,24 +471,21 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                         Lt += v.y != 0.f ? v.y * ex2(v.x - Mt) : 0.f;
                     }
                     s_fin[c] = Mt + log2f(Lt);
-                    if (c < nr && rank == 0 && !(Lt > 0.f && Lt < INFINITY))
+                    if (c < m_rows && rank == 0 && !(Lt > 0.f && Lt < INFINITY))
                         atomicCAS(a.err, kDevOk, kDevBadInput);
                 } else {
                     give_up(a.err, abort_flag);
                 }
             }
             softmax_sync();
-            if (*abort_flag) {
+            if (*abort_flag)
                 ok = false;
-                break;
-            }
             // ---- pass 2: the weights of this thread's keys ----
-            const bool add = rb > 0 || a.accumulate;
             // (the weights to add to are read eight tiles ahead)
             float old[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            for (int t = 0; t < T; ++t) {
+            for (int t = 0; t < T && ok; ++t) {
                 const int j0 = (t_lo + t) * kWtTile, j = j0 + (int)threadIdx.x;
-                if (add && (t & 7) == 0) {
+                if (a.accumulate && (t & 7) == 0) {
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         old[x] = t + x < T && j + x * kWtTile < n ? wp[j + x * kWtTile] : 0.f;
@@ -516,10 +509,10 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                     tmem_wait_ld();
                 }
                 if (j0 + kWtTile > rq.prefix + 1)
-                    mask(j >= n ? NC : (j - rq.prefix) * G - r0, s);
+                    mask(j >= n ? NC : (j - rq.prefix) * G, s);
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    p4[c & 3] += c < nr ? ex2(fmaf(s[c], sc, -s_fin[c])) : 0.f;
+                    p4[c & 3] += c < m_rows ? ex2(fmaf(s[c], sc, -s_fin[c])) : 0.f;
                 if (j < n)
                     wp[j] = w + ((p4[0] + p4[1]) + (p4[2] + p4[3]));
             }
@@ -530,19 +523,18 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         if (lane == 0) {
             bool ok = true;
             int k = 0;   // panels issued
-            for (int rb = 0; rb < n_rb && ok; ++rb)
-                for (int i = 0; i < n_jobs && ok; ++i) {
-                    const int row = (int)(blk + (int64_t)(t_lo + job_tile(i)) * kWtTile);
-                    for (int p = 0; p < 2; ++p, ++k) {
-                        const int s = k % C::kSlots;
-                        if (k >= C::kSlots && !mbar_wait(bar(bEmpty + s), (uint32_t)(k / C::kSlots - 1) & 1, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_expect_tx(bar(bFull + s), kWtPanel);
-                        tma_load_2d(sbase + (uint32_t)(C::kOffRing + s * kWtPanel), &tmk, 64 * p, row, bar(bFull + s));
+            for (int i = 0; i < n_jobs && ok; ++i) {
+                const int row = (int)(blk + (int64_t)(t_lo + job_tile(i)) * kWtTile);
+                for (int p = 0; p < 2; ++p, ++k) {
+                    const int s = k % C::kSlots;
+                    if (k >= C::kSlots && !mbar_wait(bar(bEmpty + s), (uint32_t)(k / C::kSlots - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
                     }
+                    mbar_expect_tx(bar(bFull + s), kWtPanel);
+                    tma_load_2d(sbase + (uint32_t)(C::kOffRing + s * kWtPanel), &tmk, 64 * p, row, bar(bFull + s));
                 }
+            }
             if (!ok)
                 give_up(a.err, abort_flag);
             // every issued copy lands before the CTA leaves
@@ -553,38 +545,31 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         const uint32_t lead = elect_one();
         const uint64_t d0 = sdesc(sbase, 16, 1024);
         const uint32_t lo = (uint32_t)d0, hi = (uint32_t)(d0 >> 32);
-        bool ok = true;
-        int k = 0, job = 0;
-        for (int rb = 0; rb < n_rb && ok; ++rb) {
-            if (!mbar_wait(bar(bQFull), (uint32_t)rb & 1, abort_flag)) {
+        bool ok = n_jobs == 0 || mbar_wait(bar(bQFull), 0, abort_flag);
+        int k = 0;
+        for (int i = 0; i < n_jobs && ok; ++i) {
+            const int stage = i % C::kStages;
+            if (i >= C::kStages && !mbar_wait(bar(bSFree + stage), (uint32_t)(i / C::kStages - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
-            for (int i = 0; i < n_jobs && ok; ++i, ++job) {
-                const int stage = job % C::kStages;
-                if (job >= C::kStages && !mbar_wait(bar(bSFree + stage), (uint32_t)(job / C::kStages - 1) & 1, abort_flag)) {
+            for (int p = 0; p < 2; ++p, ++k) {
+                const int s = k % C::kSlots;
+                if (!mbar_wait(bar(bFull + s), (uint32_t)(k / C::kSlots) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
-                for (int p = 0; p < 2; ++p, ++k) {
-                    const int s = k % C::kSlots;
-                    if (!mbar_wait(bar(bFull + s), (uint32_t)(k / C::kSlots) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t ka = lo + ((uint32_t)(C::kOffRing + s * kWtPanel) >> 4);
-                    const uint32_t qb = lo + ((uint32_t)(p * C::kQPanel) >> 4);
+                tc_fence_after();
+                const uint32_t ka = lo + ((uint32_t)(C::kOffRing + s * kWtPanel) >> 4);
+                const uint32_t qb = lo + ((uint32_t)(p * C::kQPanel) >> 4);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        mma_ss(lead, tmem + (uint32_t)(stage * NQ), desc_with_lo(ka + 2 * x, hi), desc_with_lo(qb + 2 * x, hi),
-                               kIdesc, p > 0 || x > 0);
-                    umma_commit(lead, bar(bEmpty + s));
-                }
-                if (ok)
-                    umma_commit(lead, bar(bSFull + stage));
+                for (int x = 0; x < 4; ++x)
+                    mma_ss(lead, tmem + (uint32_t)(stage * NQ), desc_with_lo(ka + 2 * x, hi), desc_with_lo(qb + 2 * x, hi), kIdesc,
+                           p > 0 || x > 0);
+                umma_commit(lead, bar(bEmpty + s));
             }
-            umma_commit(lead, bar(bQEmpty));
+            if (ok)
+                umma_commit(lead, bar(bSFull + stage));
         }
         if (!ok)
             give_up(a.err, abort_flag);
@@ -621,7 +606,7 @@ constexpr int kWwOffRing = 2 * kWwQTerm;
 constexpr int kWwOffBar = kWwOffRing + kWwSlots * kWtPanel;
 constexpr int kWwNumBars = 2 * kWwSlots + 4 + 4;   // full, empty, s_full[2], s_free[2], q_full, q_empty, peers, drain
 constexpr int kWwOffMisc = kWwOffBar + 8 * kWwNumBars;
-constexpr int kWwOffFin = (kWwOffMisc + 8 + 15) & ~15;         // [128] -lse
+constexpr int kWwOffFin = (kWwOffMisc + 12 + 15) & ~15;         // [128] -lse
 constexpr int kWwSmem = kWwOffFin + 128 * 4;
 constexpr int kWwOffPeer = kWwSmem;                            // [2][kWwMaxCluster][128] (max, sum), clusters only
 constexpr int kWwSmemCluster = kWwOffPeer + 2 * kWwMaxCluster * 128 * 8;
@@ -638,7 +623,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     auto bar = [&](int i) { return sbase + kWwOffBar + 8u * (uint32_t)i; };
     constexpr int bFull = 0, bEmpty = kWwSlots, bSFull = 2 * kWwSlots, bSFree = bSFull + 2, bQFull = bSFree + 2,
                   bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bQFull + 3;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(wt_smem + kWwOffMisc + 4);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(wt_smem + kWwOffMisc + 4), *abort_seen = abort_flag + 1;
     float *s_fin = reinterpret_cast<float *>(wt_smem + kWwOffFin);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int units = a.n_layers * a.n_kv_heads;
@@ -647,7 +632,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWwNumBars; ++i)
             mbar_init(bar(i), (i >= bSFree && i < bSFree + 2) || i == bQFull ? 128u : i == bPeers ? (uint32_t)(n_cluster * 128) : 1u);
-        *abort_flag = 0;
+        *abort_flag = *abort_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 5)
@@ -683,12 +668,11 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         if (m_rows == 0 && !a.accumulate)
             for (int j = t_lo * kWtTile + (int)threadIdx.x; j < min(n, t_hi * kWtTile); j += 128)
                 wp[j] = 0.f;
-        for (int rb = 0; rb < n_rb && ok; ++rb) {
+        // (a thread whose wait ran out still passes every barrier of the 128, until
+        // all of them leave together)
+        for (int rb = 0; rb < n_rb; ++rb) {
             const int r0 = rb * 128, nr = min(128, m_rows - r0);
-            if (rb > 0 && !mbar_wait(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag)) {
-                ok = false;
-                break;
-            }
+            ok = ok && (rb == 0 || mbar_wait(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag));
             prepare_queries<2, 128>(a, rq, l, h, G, r0, nr, sbase, (uint32_t)kWwQTerm, (uint32_t)(kWwQTerm / 2));
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
@@ -697,7 +681,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             const int r = threadIdx.x;
             const int see = rq.prefix + (r0 + min(r, nr - 1)) / G + 1;   // keys the row sees
             float m = kWtUnset, lsum = 0.f;
-            for (int i = 0; i < T; ++i, ++job) {
+            for (int i = 0; i < T && ok; ++i, ++job) {
                 const int half = job & 1;
                 if (!mbar_wait(bar(bSFull + half), (uint32_t)(job >> 1) & 1, abort_flag)) {
                     ok = false;
@@ -756,7 +740,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 mbar_arrive(bar(bSFree + half));
             }
             if (!ok)
-                break;
+                give_up(a.err, abort_flag);
             float M = m, L = lsum;
             if (n_cluster > 1) {
                 const uint32_t peer = sbase + kWwOffPeer + (uint32_t)((rb & 1) * kWwMaxCluster * 128 * 8);
@@ -785,15 +769,17 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             s_fin[r] = r < nr ? -(M + log2f(L)) : 0.f;   // (rows that pad the block: any finite value)
             if (r < nr && rank == 0 && !(L > 0.f && L < INFINITY))
                 atomicCAS(a.err, kDevOk, kDevBadInput);
+            if (threadIdx.x == 0)
+                *abort_seen = *abort_flag;
             softmax_sync();
-            if (*abort_flag) {
+            if (*abort_seen) {   // the same for all 128 threads
                 ok = false;
                 break;
             }
             // ---- pass 2: the weights of this thread's keys ----
             const bool add = rb > 0 || a.accumulate;
             const int nb = (nr + 31) >> 5;   // 32-row blocks of queries
-            for (int i = 0; i < T; ++i, ++job) {
+            for (int i = 0; i < T && ok; ++i, ++job) {
                 const int half = job & 1;
                 const int j0 = (t_lo + T - 1 - i) * kWtTile, j = j0 + (int)threadIdx.x;
                 const float w = add && j < n ? wp[j] : 0.f;
@@ -977,11 +963,16 @@ static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUt
     }
     const int64_t units = (int64_t)a.n_reqs * a.n_layers * a.n_kv_heads;
     const int tiles = (a.max_rows + kWtTile - 1) / kWtTile;
-    // as many CTAs as hold the longest request's scores in TMEM; more while the
-    // grid stays within two CTAs per SM and a CTA keeps four tiles (one request
-    // of 2,657 rows and 112 units: 28 us with clusters of 2, 34 with 4)
+    // A cluster's CTAs together keep more scores in TMEM, but each pays its
+    // prologue and exchange: the cluster grows while the longest request's scores
+    // do not fit and a CTA keeps ten tiles (288 units: 16 rows, 11 tiles: 25 us
+    // with one CTA, 31 with two; 47 tiles: 116, 108, 100 and 128 with 1, 2, 4 and
+    // 8; 258 tiles: 669, 654, 616 and 590.  32 rows: 4 CTAs at most, 258 tiles:
+    // 651 with 4, 692 with 8).  And it grows while SMs would be idle and a CTA
+    // keeps four tiles (112 units of 21 tiles: 28 us with 2, 34 with 4).
     int c = 1;
-    while (c < kWtMaxCluster && (tiles > c * C::kKept || (units * c <= n_sms && tiles >= 8 * c)))
+    while (c < C::kMaxCluster &&
+           ((tiles > c * C::kKept && tiles >= 20 * c) || (units * c <= n_sms && tiles >= 8 * c)))
         c *= 2;
     if (units * c > 0x7fffffff)
         return cudaErrorInvalidValue;
