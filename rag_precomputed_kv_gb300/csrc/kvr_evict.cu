@@ -8,10 +8,15 @@
 // from row kept[i] to row i is turned by i - kept[i], the same re-rotation
 // that stitched it (CoinRAG blog section 2.3); values and weights are copied.
 //
-// Two kernels.  k_evict_select finds each unit's kept rows: the threshold
-// weight by a radix select over order-preserving integer keys, then the rows
-// at or above it in order.  k_evict_move gathers the kept rows: a pure HBM
-// stream like the stitch.
+// First a unit's kept rows: the threshold weight by a radix select over
+// order-preserving integer keys, then the rows at or above it in order, a chain
+// of short passes bound by their latency.  Then the kept rows are gathered: an
+// HBM stream like the stitch.  With many units of few rows both in one kernel
+// (k_evict_unit), else a kernel each (k_evict_select, k_evict_move).
+// Measured (bf16, head_dim 128): 4,608 units of 1,344 rows to 512: 370 us, of
+// which 362 are the rows' and weights' bytes at the copy rate; 256 units of
+// 33,504 rows to 4,096: 52 us + 167 us (6.6 TB/s); 112 units of 2,656 rows to
+// 1,024: 9 us + 19 us (6.3 TB/s).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -24,6 +29,13 @@ namespace kvr {
 namespace {
 
 constexpr int kMoveThreads = 256;
+constexpr int kSelThreads = 1024;
+// CTAs per SM that the registers must leave room for (a bf16 row of 128: 82
+// registers, two CTAs, 241 us a call for 256 units of 33,504 rows; three 219,
+// four 233)
+template <typename T, int D>
+constexpr int kMoveCtas = sizeof(T) * D > 256 ? 2 : 3;   // (fp32 rows of 128 need 126 registers)
+__host__ __device__ constexpr int evict_chunks(int keep) { return keep > 0 ? (keep + kEvictChunk - 1) / kEvictChunk : 1; }
 
 // Integer key in the order of the weights: NaN lowest, then -inf .. +inf, both
 // zeros alike.  Two more values: kNoRow below all of them, for places past the
@@ -105,16 +117,11 @@ constexpr int kRankMax = 256;
 constexpr int kSelSmemRows = 48 * 1024;   // 192 KB
 
 template <int TH, bool kSmem>
-__global__ void __launch_bounds__(TH, 1)
-    k_evict_select(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
+__device__ __forceinline__ void select_rows(const EvictArgs &a, const DevEvict rq, int lh)
 {
     constexpr int NW = TH / 32, BPT = 2048 / TH;   // warps, bins of a thread
-    const DevEvict *reqs = a.reqs ? a.reqs : rt.reqs;
-    const int b = (int)(blockIdx.x / (unsigned)a.units), lh = (int)(blockIdx.x % (unsigned)a.units);
-    const DevEvict rq = reqs[b];
     int32_t *kept = a.kept + rq.kept0 + (int64_t)lh * rq.keep;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_launch_dependents();   // (the move kernel waits for this grid)
     if (rq.keep == rq.n) {
         for (int i = threadIdx.x; i < rq.n; i += TH)
             kept[i] = i;
@@ -373,47 +380,30 @@ __global__ void __launch_bounds__(TH, 1)
     }
 }
 
-// A piece is kEvictChunk kept rows of one unit.  TPR threads a row, thread j
+template <bool kSmem>
+__global__ void __launch_bounds__(kSelThreads, 1)
+    k_evict_select(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
+{
+    pdl_launch_dependents();   // (the move kernel waits for this grid)
+    const int b = (int)(blockIdx.x / (unsigned)a.units);
+    select_rows<kSelThreads, kSmem>(a, (a.reqs ? a.reqs : rt.reqs)[b], (int)(blockIdx.x % (unsigned)a.units));
+}
+
+// Rows c_first * kEvictChunk .. of unit lh: pieces of kEvictChunk kept rows.  TPR threads a row, thread j
 // holding 16-byte vector j of each row half (so that both halves of a RoPE
 // pair are in one thread).  A bf16 key's angles are computed, not read: a moved
 // row's (cos, sin) table row would be 512 bytes beside the 512 of its K and V.
 // The turn delta * w_i / 2 pi is reduced exactly (an fp32 product with the
 // frequency in two words), and sin and cos of the rest are good to 2^-20, far
-// below the bf16 result's 2^-9.  To another block, every piece is a CTA.  In place,
-// a CTA walks its unit's pieces in order: a piece's sources lie at or behind
-// its own rows, so once the piece is read (barrier), writing it only
-// overwrites rows that were read before.
-template <typename T, int D>
-__global__ void __launch_bounds__(kMoveThreads)
-    k_evict_move(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
+// below the bf16 result's 2^-9.  In place, a CTA walks its unit's pieces in
+// order: a piece's sources lie at or behind its own rows, so once the piece is
+// read (barrier), writing it only overwrites rows that were read before.
+// `wait` is called before the kept rows are read.
+template <typename T, int D, typename Wait>
+__device__ __forceinline__ void move_rows(const EvictArgs &a, const DevEvict rq, int lh, int c_first, int c_end, Wait &&wait)
 {
     constexpr int E = RowVec<T>::E, H2 = D / 2, TPR = H2 / E, RPP = kMoveThreads / TPR;
     constexpr int NR = (kEvictChunk + RPP - 1) / RPP;   // rows of a thread
-    const DevEvict *reqs = a.reqs ? a.reqs : rt.reqs;
-    int b, lh, c_first, c_end;
-    if (a.in_place) {
-        b = (int)(blockIdx.x / (unsigned)a.units);
-        lh = (int)(blockIdx.x % (unsigned)a.units);
-        c_first = 0;
-        c_end = max(1, (reqs[b].keep + kEvictChunk - 1) / kEvictChunk);
-    } else {
-        int lo = 0, hi = a.n_reqs - 1;
-        while (lo < hi) {   // the last request whose first piece is <= blockIdx.x
-            const int mid = (lo + hi + 1) >> 1;
-            if (reqs[mid].chunk0 <= (int)blockIdx.x)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        b = lo;
-        const int n_c = max(1, (reqs[b].keep + kEvictChunk - 1) / kEvictChunk);
-        const int local = (int)blockIdx.x - reqs[b].chunk0;
-        lh = local / n_c;
-        c_first = local - lh * n_c;
-        c_end = c_first + 1;
-    }
-    const DevEvict rq = reqs[b];
-    const int n_chunks = max(1, (rq.keep + kEvictChunk - 1) / kEvictChunk);
     const int32_t *kept = a.kept + rq.kept0 + (int64_t)lh * rq.keep;
     const int64_t src0 = rq.src_row0 + (int64_t)lh * rq.src_cap, dst0 = rq.dst_row0 + (int64_t)lh * rq.dst_cap;
     const T *sk = static_cast<const T *>(a.cache_k) + src0 * D, *sv = static_cast<const T *>(a.cache_v) + src0 * D;
@@ -430,7 +420,7 @@ __global__ void __launch_bounds__(kMoveThreads)
             f_lo[e] = f.y;
         }
     }
-    pdl_wait_prerequisites();   // the kept rows
+    wait();
     for (int c = c_first; c < c_end; ++c) {
         uint4 k[NR][2], v[NR][2];
         int src[NR];
@@ -490,12 +480,56 @@ __global__ void __launch_bounds__(kMoveThreads)
         }
     }
     // the rows behind the kept ones start at no weight
-    if (dw && c_end == n_chunks) {
+    if (dw && c_end == evict_chunks(rq.keep)) {
         if (a.in_place)
             __syncthreads();
         for (int i = rq.keep + (int)threadIdx.x; i < rq.dst_cap; i += kMoveThreads)
             dw[i] = 0.f;
     }
+}
+
+// To another block, every piece is a CTA; in place, every unit.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas<T, D>)
+    k_evict_move(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
+{
+    const DevEvict *reqs = a.reqs ? a.reqs : rt.reqs;
+    int b, lh, c_first, c_end;
+    if (a.in_place) {
+        b = (int)(blockIdx.x / (unsigned)a.units);
+        lh = (int)(blockIdx.x % (unsigned)a.units);
+        c_first = 0;
+        c_end = evict_chunks(reqs[b].keep);
+    } else {
+        int lo = 0, hi = a.n_reqs - 1;
+        while (lo < hi) {   // the last request whose first piece is <= blockIdx.x
+            const int mid = (lo + hi + 1) >> 1;
+            if (reqs[mid].chunk0 <= (int)blockIdx.x)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        b = lo;
+        const int n_c = evict_chunks(reqs[b].keep);
+        const int local = (int)blockIdx.x - reqs[b].chunk0;
+        lh = local / n_c;
+        c_first = local - lh * n_c;
+        c_end = c_first + 1;
+    }
+    move_rows<T, D>(a, reqs[b], lh, c_first, c_end, [] { pdl_wait_prerequisites(); });
+}
+
+// Both in one: a CTA of 256 threads selects a unit's rows and moves them.  With
+// several units per SM one's selection, a chain of short dependent steps,
+// overlaps the others' traffic.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas<T, D>)
+    k_evict_unit(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
+{
+    const int b = (int)(blockIdx.x / (unsigned)a.units), lh = (int)(blockIdx.x % (unsigned)a.units);
+    const DevEvict rq = (a.reqs ? a.reqs : rt.reqs)[b];
+    select_rows<kMoveThreads, true>(a, rq, lh);
+    move_rows<T, D>(a, rq, lh, 0, evict_chunks(rq.keep), [] { __syncthreads(); });
 }
 
 cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s)
@@ -504,38 +538,47 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
     const int64_t move = a.in_place ? ctas : a.n_chunks;
     if (ctas > 0x7fffffff || move > 0x7fffffff)
         return cudaErrorInvalidValue;
-    // Small CTAs when there are several units per SM (up to eight resident hide
-    // each other's barriers), large ones when a unit has an SM to itself: 1,344
-    // rows, 4,608 units: 417 us a call against 510; 2,656 rows: 336 units 70.5
-    // against 74, 224 units alike, 112 units 31.3 against 28.8.
-    const bool small = a.max_n <= 24 * 256 && ctas >= 2 * (int64_t)n_sms;
-    const int threads = small ? 256 : 1024;
-    const int rows = (a.max_n + 4 * threads - 1) / (4 * threads) * 4 * threads;   // of keys in shared memory
+    using Kernel = void (*)(const EvictArgs, const EvictTable);
+    auto pick = [&](Kernel b128, Kernel b64, Kernel f128, Kernel f64) -> Kernel {
+        if (head_dim != 128 && head_dim != 64)
+            return nullptr;
+        return dtype == KVR_DTYPE_BF16 ? (head_dim == 128 ? b128 : b64) : (head_dim == 128 ? f128 : f64);
+    };
+    auto smem_rows = [&](int threads) { return (a.max_n + 4 * threads - 1) / (4 * threads) * 4 * threads; };   // keys there
+    // One kernel where there are two units per SM or more and their keys leave
+    // room for three CTAs: 4,608 units of 1,344 rows 370 us a call, 531 in two
+    // kernels; 336 units of 2,656 rows 73 against 76; 224 units 52 against 53; 112
+    // units 39 against 29 (a CTA each cannot move them at full rate).
+    if (a.max_n <= 24 * 256 && ctas >= 2 * (int64_t)n_sms) {
+        const Kernel k = pick(k_evict_unit<__nv_bfloat16, 128>, k_evict_unit<__nv_bfloat16, 64>, k_evict_unit<float, 128>,
+                              k_evict_unit<float, 64>);
+        if (!k)
+            return cudaErrorInvalidValue;
+        k<<<(unsigned)ctas, kMoveThreads, smem_rows(kMoveThreads) * 4, s>>>(a, rt);
+        return cudaGetLastError();
+    }
+    const int rows = smem_rows(kSelThreads);
     const bool smem = rows <= kSelSmemRows;
-    auto select = small ? k_evict_select<256, true> : smem ? k_evict_select<1024, true> : k_evict_select<1024, false>;
     static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(k_evict_select<1024, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemRows * 4)) !=
+        if ((e = cudaFuncSetAttribute(k_evict_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemRows * 4)) !=
             cudaSuccess)
             return e;
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
     }
-    select<<<(unsigned)ctas, threads, smem ? rows * 4 : 0, s>>>(a, rt);
+    const Kernel k = pick(k_evict_move<__nv_bfloat16, 128>, k_evict_move<__nv_bfloat16, 64>, k_evict_move<float, 128>,
+                          k_evict_move<float, 64>);
+    if (!k)
+        return cudaErrorInvalidValue;
+    (smem ? k_evict_select<true> : k_evict_select<false>)<<<(unsigned)ctas, kSelThreads, smem ? rows * 4 : 0, s>>>(a, rt);
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    void (*k)(const EvictArgs, const EvictTable) = nullptr;
-    if (dtype == KVR_DTYPE_BF16)
-        k = head_dim == 128 ? k_evict_move<__nv_bfloat16, 128> : head_dim == 64 ? k_evict_move<__nv_bfloat16, 64> : nullptr;
-    else
-        k = head_dim == 128 ? k_evict_move<float, 128> : head_dim == 64 ? k_evict_move<float, 64> : nullptr;
-    if (!k)
-        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)move);
     cfg.blockDim = dim3(kMoveThreads);
