@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                     s[c] += mid[c] + low[c];
             };
             auto wait_job = [&](int jb) -> bool {
-                if (!mbar_wait(bar(bSFull + jb % C::kStages), (uint32_t)(jb / C::kStages) & 1, abort_flag))
+                if (!mbar_wait_warp(bar(bSFull + jb % C::kStages), (uint32_t)(jb / C::kStages) & 1, abort_flag))
                     return false;
                 tc_fence_after();
                 return true;
@@ -545,17 +545,17 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         const uint32_t lead = elect_one();
         const uint64_t d0 = sdesc(sbase, 16, 1024);
         const uint32_t lo = (uint32_t)d0, hi = (uint32_t)(d0 >> 32);
-        bool ok = n_jobs == 0 || mbar_wait(bar(bQFull), 0, abort_flag);
+        bool ok = n_jobs == 0 || mbar_wait_warp(bar(bQFull), 0, abort_flag);
         int k = 0;
         for (int i = 0; i < n_jobs && ok; ++i) {
             const int stage = i % C::kStages;
-            if (i >= C::kStages && !mbar_wait(bar(bSFree + stage), (uint32_t)(i / C::kStages - 1) & 1, abort_flag)) {
+            if (i >= C::kStages && !mbar_wait_warp(bar(bSFree + stage), (uint32_t)(i / C::kStages - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             for (int p = 0; p < 2; ++p, ++k) {
                 const int s = k % C::kSlots;
-                if (!mbar_wait(bar(bFull + s), (uint32_t)(k / C::kSlots) & 1, abort_flag)) {
+                if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(k / C::kSlots) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         // all of them leave together)
         for (int rb = 0; rb < n_rb; ++rb) {
             const int r0 = rb * 128, nr = min(128, m_rows - r0);
-            ok = ok && (rb == 0 || mbar_wait(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag));
+            ok = ok && (rb == 0 || mbar_wait_warp(bar(bQEmpty), (uint32_t)(rb - 1) & 1, abort_flag));
             prepare_queries<2, 128>(a, rq, l, h, G, r0, nr, sbase, (uint32_t)kWwQTerm, (uint32_t)(kWwQTerm / 2));
             fence_proxy_async_smem();
             mbar_arrive(bar(bQFull));
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             float m = kWtUnset, lsum = 0.f;
             for (int i = 0; i < T && ok; ++i, ++job) {
                 const int half = job & 1;
-                if (!mbar_wait(bar(bSFull + half), (uint32_t)(job >> 1) & 1, abort_flag)) {
+                if (!mbar_wait_warp(bar(bSFull + half), (uint32_t)(job >> 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 const int half = job & 1;
                 const int j0 = (t_lo + T - 1 - i) * kWtTile, j = j0 + (int)threadIdx.x;
                 const float w = add && j < n ? wp[j] : 0.f;
-                if (!mbar_wait(bar(bSFull + half), (uint32_t)(job >> 1) & 1, abort_flag)) {
+                if (!mbar_wait_warp(bar(bSFull + half), (uint32_t)(job >> 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
         bool ok = true;
         int k = 0, job = 0;
         for (int rb = 0; rb < n_rb && ok; ++rb) {
-            if (!mbar_wait(bar(bQFull), (uint32_t)rb & 1, abort_flag)) {
+            if (!mbar_wait_warp(bar(bQFull), (uint32_t)rb & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -882,14 +882,14 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             const uint32_t idesc_s = kIdescBase | ((uint32_t)(kWtTile >> 3) << 17);             // S: N = keys
             for (int i = 0; i < 2 * T && ok; ++i, ++job) {
                 const int half = job & 1;
-                if (job >= 2 && !mbar_wait(bar(bSFree + half), (uint32_t)((job >> 1) - 1) & 1, abort_flag)) {
+                if (job >= 2 && !mbar_wait_warp(bar(bSFree + half), (uint32_t)((job >> 1) - 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
                 const bool second = i >= T;
                 for (int p = 0; p < 2; ++p, ++k) {
                     const int s = k % kWwSlots;
-                    if (!mbar_wait(bar(bFull + s), (uint32_t)(k / kWwSlots) & 1, abort_flag)) {
+                    if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(k / kWwSlots) & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
