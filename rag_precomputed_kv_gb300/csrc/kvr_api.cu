@@ -1447,9 +1447,11 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
     pa.total_q = sa.total_q;
     pa.scale_log2 = sa.scale_log2;
     pa.err = p->err;
-    // groups with prefix and tokens first, numbered pair by pair; the others behind them
+    // groups with prefix and tokens first; the others behind them
     pl.gr.reserve(n_groups);
     std::vector<int32_t> place(n_groups);
+    int64_t own_tiles = 0, blocks = 0;   // of a unit: own key tiles that the 256-row blocks meet
+    bool all_active = true;
     for (int pass = 0; pass < 2; ++pass)
         for (int g = 0; g < n_groups; ++g) {
             const int32_t t0 = q_offsets[group_offsets[g]], t1 = q_offsets[group_offsets[g + 1]];
@@ -1460,21 +1462,46 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
                 return fail(KVR_ERR_UNSUPPORTED, "group %d: too many query rows", g);
             DevGroup d{};
             d.pre_row0 = prefix_offsets[g] * LH;
-            d.item0 = pa.unit_blocks;
-            d.w0 = pa.unit_pairs;
             d.pre_cap = (int32_t)(prefix_offsets[g + 1] - prefix_offsets[g]);
             d.pre_len = prefix_len[g];
             d.q_off = t0;
             d.rows = (t1 - t0) * G;
             if (active) {
-                d.nt = (d.pre_len + 127) / 128;
+                d.nt = d.pairs = (d.pre_len + 127) / 128;
                 d.mb = (d.rows + 255) / 256;
-                pa.unit_blocks += d.mb;
-                pa.unit_pairs += (int64_t)d.mb * d.nt;
+                blocks += d.mb;
+                // the block that meets most own tiles
+                int b = group_offsets[g], most = 0;
+                for (int m = 0; m < d.mb; ++m) {
+                    const int32_t first = t0 + m * 256 / G;
+                    const int32_t end = t0 + (std::min(d.rows, m * 256 + 256) - 1) / G + 1;
+                    int n = 0;
+                    while (pl.rq[b].q_off + pl.rq[b].q_len <= first)
+                        ++b;
+                    for (int i = b; i < group_offsets[g + 1] && pl.rq[i].q_off < end; ++i)
+                        if (pl.rq[i].q_len > 0)
+                            n += (pl.rq[i].own + std::min(pl.rq[i].q_len, end - pl.rq[i].q_off) + 127) / 128;
+                    own_tiles += n;
+                    most = std::max(most, n);
+                }
+                d.most_own = most;
+            } else if (t1 > t0) {
+                all_active = false;
             }
             place[g] = (int32_t)pl.gr.size();
             pl.gr.push_back(d);
         }
+    // Whole blocks, own keys and all, in one kernel
+    const bool whole = all_active && blocks * LH >= 8 * (int64_t)p->n_sms && own_tiles <= 6 * blocks;
+    // the (block, key tile) pairs, numbered group by group
+    for (DevGroup &d : pl.gr) {
+        if (whole && d.mb > 0)
+            d.pairs = d.nt + d.most_own;
+        d.item0 = pa.unit_blocks;
+        d.w0 = pa.unit_pairs;
+        pa.unit_blocks += d.mb;
+        pa.unit_pairs += (int64_t)d.mb * d.pairs;
+    }
     for (int g = 0; g < n_groups; ++g)
         for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
             pl.rq[b].group = place[g];
@@ -1482,7 +1509,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
 
     // slices whose partial results fit kMaxPartBytes
     int lh_slice = LH;
-    if (pa.unit_blocks > 0) {
+    if (pa.unit_blocks > 0 && !whole) {
         const int64_t fit = (kMaxPartBytes / kSharedPartBytes - p->n_sms) / pa.unit_blocks;
         const int64_t n = (LH + std::max<int64_t>(1, fit) - 1) / std::max<int64_t>(1, fit);
         lh_slice = (int)((LH + n - 1) / n);
@@ -1491,7 +1518,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
     cudaError_t e;
     const int64_t q_rows = (int64_t)L * sa.total_q * Hq;
     if ((st = p->grow_query_scratch((size_t)q_rows * D * 2)) != KVR_OK ||
-        (pa.unit_blocks > 0 &&
+        (pa.unit_blocks > 0 && !whole &&
          (st = p->grow_part_scratch((size_t)(lh_slice * pa.unit_blocks + p->n_sms) * kSharedPartBytes)) != KVR_OK))
         return st;
     pa.part = static_cast<float *>(p->part);
@@ -1504,8 +1531,8 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
     if ((st = encode_rows_map(*p, p->q_rot, q_rows, 128, &mq)) != KVR_OK ||
         (any_prefix && ((st = encode_rows_map(*p, sa.prefix_k, pre_rows, 128, &mpk)) != KVR_OK ||
                         (st = encode_rows_map(*p, sa.prefix_v, pre_rows, 128, &mpv)) != KVR_OK)) ||
-        (st = encode_rows_map(*p, sa.cache_k, own_rows, 32, &mk)) != KVR_OK ||
-        (st = encode_rows_map(*p, sa.cache_v, own_rows, 32, &mv)) != KVR_OK)
+        (st = encode_rows_map(*p, sa.cache_k, own_rows, whole ? 128 : 32, &mk)) != KVR_OK ||
+        (st = encode_rows_map(*p, sa.cache_v, own_rows, whole ? 128 : 32, &mv)) != KVR_OK)
         return st;
     // the previous call's attention must be done with the scratch
     if (p->q_rot_used && (e = cudaStreamWaitEvent(s, p->q_rot_done, 0)) != cudaSuccess)
@@ -1525,7 +1552,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         pa.groups = reinterpret_cast<const DevGroup *>(static_cast<const char *>(slot->dev) + off);
     }
     SharedTcArgs t{&sa, &pl.tab, &pa, &pl.gtab, &mq, any_prefix ? &mpk : nullptr, any_prefix ? &mpv : nullptr,
-                   &mk, &mv, p->n_sms, max_own};
+                   &mk, &mv, p->n_sms, whole, max_own};
     p->mark(2, s);
     {
         NvtxRange r("kvr.k_shared_prologue");

@@ -292,7 +292,9 @@ struct alignas(16) DevGroup {
     int32_t rows;        // tokens x G
     int32_t nt;          // 128-key tiles of the prefix
     int32_t mb;          // 256-row blocks
-    int32_t pad_[4];
+    int32_t pairs;       // pairs of a block: nt, or (whole) nt and the own tiles of the block that meets most
+    int32_t most_own;    // own tiles of that block
+    int32_t pad_[2];
 };
 static_assert(sizeof(DevGroup) == 64, "group table layout");
 struct GroupTable {
@@ -323,8 +325,10 @@ struct SharedTcArgs {
     const GroupTable *groups;
     // host CUtensorMaps: packed queries and prefix (64 x 128 boxes; the prefix's
     // NULL when nothing is shared), own caches (64 x 32)
+    // (whole: 64 x 128)
     const void *tmap_q, *tmap_pk, *tmap_pv, *tmap_k, *tmap_v;
     int32_t n_sms;
+    bool whole;                 // the prefix kernel takes whole blocks, and their rows' own keys too
     int32_t max_own_keys;       // the longest own part (own rows and query tokens) of a request with tokens
 };
 

@@ -132,9 +132,9 @@ __device__ __forceinline__ Seg seg_at(const SharedPrefixArgs &a, const DevGroup 
             hi = mid - 1;
     }
     s.g = groups[lo];
-    const int blk = (int)((in_unit - s.g.w0) / s.g.nt);
-    s.jb = (int)(in_unit - s.g.w0 - (int64_t)blk * s.g.nt);
-    s.je = (int)min((int64_t)s.g.nt, s.jb + (w_end - w));
+    const int blk = (int)((in_unit - s.g.w0) / s.g.pairs);
+    s.jb = (int)(in_unit - s.g.w0 - (int64_t)blk * s.g.pairs);
+    s.je = (int)min((int64_t)s.g.pairs, s.jb + (w_end - w));
     s.next = w + (s.je - s.jb);
     s.item = (int64_t)s.lh * a.unit_blocks + s.g.item0 + blk;
     s.row0 = blk * 256;
@@ -143,22 +143,78 @@ __device__ __forceinline__ Seg seg_at(const SharedPrefixArgs &a, const DevGroup 
     return s;
 }
 
-}  // namespace
+// The own key tiles that a whole block meets: request by request, those of the
+// requests that its rows belong to, as far as the block's last row sees.
+struct OwnTiles {
+    int b, k;        // request, key tile
+    int t_end;       // token behind the block's last
 
-__global__ void __launch_bounds__(kSpThreads, 1)
-    k_shared_prefix(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ SharedPrefixArgs a,
-                    const __grid_constant__ GroupTable gt)
+    __device__ __forceinline__ int keys(const DevShared &r) const { return r.own + min(r.q_len, t_end - r.q_off); }
+    __device__ __forceinline__ void skip_empty(const DevShared *reqs, int n_reqs)
+    {
+        while (b < n_reqs && reqs[b].q_len == 0)
+            ++b;
+    }
+    // the block's first tile; returns how many there are
+    __device__ __forceinline__ int first(const DevShared *reqs, int n_reqs, const Seg &s, int G)
+    {
+        const int t0 = s.g.q_off + s.row0 / G;
+        t_end = s.g.q_off + (s.row0 + s.rows - 1) / G + 1;
+        int lo = 0, hi = n_reqs - 1;
+        while (lo < hi) {   // the last request that starts at or before the first token
+            const int mid = (lo + hi + 1) >> 1;
+            if (reqs[mid].q_off <= t0)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        int n = 0;
+        for (b = lo; b < n_reqs && reqs[b].q_off < t_end; ++b)
+            n += reqs[b].q_len > 0 ? (keys(reqs[b]) + kSpTile - 1) / kSpTile : 0;
+        b = lo;
+        k = 0;
+        return n;
+    }
+    __device__ __forceinline__ void next(const DevShared *reqs, int n_reqs)
+    {
+        if (++k * kSpTile >= keys(reqs[b])) {
+            ++b;
+            k = 0;
+            skip_empty(reqs, n_reqs);
+        }
+    }
+};
+
+// kWhole: stretches of whole blocks, whose own keys follow the prefix's, and
+// whose rows are written as the output; else partial results of the prefix.
+template <bool kWhole>
+__device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                                            const SharedPrefixArgs &a, const DevGroup *groups, const CUtensorMap &tmok,
+                                            const CUtensorMap &tmov, const SharedArgs *sa, const DevShared *reqs)
 {
-    const DevGroup *groups = a.groups ? a.groups : gt.groups;
     extern __shared__ uint8_t sp_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(sp_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return sbase + kSpOffBar + 8u * (uint32_t)i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSpOffMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t w_begin = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x),
-                  w_end = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x + 1);
+    int64_t w_begin = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x);
+    const int64_t w_end = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x + 1);
+    // the block that holds pair w (whole: all of it, with its own tiles)
+    auto block_at = [&](int64_t w, OwnTiles &ot) -> Seg {
+        Seg s = seg_at(a, groups, w, w_end);
+        if constexpr (kWhole) {
+            s.next = w + s.g.pairs;
+            s.je = s.g.nt + ot.first(reqs, sa->n_reqs, s, a.group);
+        }
+        return s;
+    };
+    if constexpr (kWhole) {   // from the first block that begins in the stretch on
+        if (w_begin < w_end) {
+            const Seg s = seg_at(a, groups, w_begin, w_end);
+            w_begin += s.jb > 0 ? s.g.pairs - s.jb : 0;
+        }
+    }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSbNum; ++i)
@@ -189,7 +245,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         int s_cnt = 0, o_cnt = 0;
         bool ok = true;
         for (int64_t w = w_begin; w < w_end && ok;) {
-            const Seg sg = seg_at(a, groups, w, w_end);
+            OwnTiles ot;
+            const Seg sg = block_at(w, ot);
             w = sg.next;
             if (x >= sg.nx)
                 continue;
@@ -197,9 +254,10 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             // a warp without rows of its own only keeps the barriers going: what it
             // leaves in its lanes of P meets its own lanes of O alone
             const bool idle = x * 128 + (warp & 3) * 32 >= sg.rows;
+            const int tok = kWhole ? sg.g.q_off + (sg.row0 + x * 128 + r) / a.group : 0;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = sg.jb; j < sg.je; ++j) {
-                if (!mbar_wait(bar(kSbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
+                if (!mbar_wait_warp(bar(kSbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -215,7 +273,15 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 for (int q = 0; q < 4; ++q)
                     tmem_ld32(lane_base + sp_col_s(x) + 32 * q, s + 32 * q);
                 tmem_wait_ld();
-                const int lim = sg.g.pre_len - j * kSpTile;   // keys of the tile that exist
+                int lim = sg.g.pre_len - j * kSpTile;   // keys of the tile that exist
+                if constexpr (kWhole) {
+                    if (j >= sg.g.nt) {   // that the row sees: none of another request's
+                        const DevShared &rq = reqs[ot.b];
+                        const int t = tok - rq.q_off;
+                        lim = t >= 0 && t < rq.q_len ? rq.own + t + 1 - ot.k * kSpTile : 0;
+                        ot.next(reqs, sa->n_reqs);
+                    }
+                }
                 if (lim < kSpTile) {
 #pragma unroll
                     for (int c = 0; c < kSpTile; ++c)
@@ -239,6 +305,9 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                     corr = ex2(m_run - mxs);
                     m_run = mxs;
                 }
+                // (all lanes together: tcgen05 loads and stores under a lane's own
+                // condition may never return)
+                const bool rescale = __any_sync(0xffffffffu, corr != 1.f);
                 const float nm = m_run == -INFINITY ? 0.f : -m_run;   // (a score of -inf in every key)
                 const uint64_t sc2 = pk2(sc, sc), nm2 = pk2(nm, nm);
                 uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
@@ -261,7 +330,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                     unpk2(acc[1], b0, b1);
                     l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
                 }
-                if (corr != 1.f) {
+                if (rescale) {
                     // the commit that signalled this S covers the P V before it: O is stable
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -282,14 +351,40 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 break;
             // the partial result: O (relative to m), m, l
             const int64_t slot = sg.item + blockIdx.x;
-            if (row_ok)
+            if (!kWhole && row_ok)
                 part_ml(a.part, slot, x)[r] = make_float2(m_run, l_run);
-            if (!mbar_wait(bar(kSbO + x), (uint32_t)o_cnt & 1, abort_flag)) {
+            if (!mbar_wait_warp(bar(kSbO + x), (uint32_t)o_cnt & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             ++o_cnt;
             tc_fence_after();
+            if constexpr (kWhole) {   // the row's output
+                const int lh = a.lh_base + sg.lh, l = lh / sa->n_kv_heads, h = lh - l * sa->n_kv_heads;
+                const int g = sg.row0 + x * 128 + r - (tok - sg.g.q_off) * a.group;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(sa->out) +
+                                                       (((int64_t)l * a.total_q + tok) * sa->n_q_heads + h * a.group + g) * kSpD);
+                const float inv = 1.f / l_run;
+                if (row_ok && !(l_run > 0.f && l_run < INFINITY))
+                    atomicCAS(a.err, kDevOk, kDevBadInput);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float o[32];
+                    tmem_ld32(lane_base + sp_col_o(x) + 32 * q, o);
+                    tmem_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[4 * q + i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                                        pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                                        pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                                        pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(bar(kSbOEmpty + x));
+                continue;
+            }
             float4 *po = part_o(a.part, slot, x) + r;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -315,7 +410,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             bool ok = true, waited = false;
             int tt = 0, nq = 0;
             for (int64_t w = w_begin; w < w_end && ok;) {
-                const Seg sg = seg_at(a, groups, w, w_end);
+                OwnTiles ot;
+                const Seg sg = block_at(w, ot);
                 w = sg.next;
                 const int64_t kv0 = sg.g.pre_row0 + (int64_t)(a.lh_base + sg.lh) * sg.g.pre_cap;
                 const int n_loads = 2 * (sg.je - sg.jb);
@@ -347,7 +443,16 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                     }
                     const uint32_t dst = sbase + (uint32_t)(kSpOffKV + slot * kSpTileBytes);
                     const CUtensorMap *map = (i & 1) ? &tmv : &tmk;
-                    const int row = (int)(kv0 + (int64_t)(sg.jb + (i >> 1)) * kSpTile);
+                    int row = (int)(kv0 + (int64_t)(sg.jb + (i >> 1)) * kSpTile);
+                    if constexpr (kWhole) {
+                        if ((i >> 1) >= sg.g.nt) {
+                            const DevShared &rq = reqs[ot.b];
+                            map = (i & 1) ? &tmov : &tmok;
+                            row = (int)(rq.cache_row0 + (int64_t)(a.lh_base + sg.lh) * rq.cap + ot.k * kSpTile);
+                            if (i & 1)
+                                ot.next(reqs, sa->n_reqs);
+                        }
+                    }
                     mbar_expect_tx(bar(kSbFull + slot), kSpTileBytes);
                     tma_load_2d(dst, map, 0, row, bar(kSbFull + slot));
                     tma_load_2d(dst + kSpPanel, map, 64, row, bar(kSbFull + slot));
@@ -369,7 +474,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         const uint64_t d_k = sdesc(sbase, 16, 1024), d_v = sdesc(sbase, kSpPanel, 1024);
         const uint32_t lo_k = (uint32_t)d_k, hi_k = (uint32_t)(d_k >> 32), lo_v = (uint32_t)d_v, hi_v = (uint32_t)(d_v >> 32);
         auto wait_kv = [&](int k) -> bool {
-            if (!mbar_wait(bar(kSbFull + k % kSpSlots), (uint32_t)(k / kSpSlots) & 1, abort_flag))
+            if (!mbar_wait_warp(bar(kSbFull + k % kSpSlots), (uint32_t)(k / kSpSlots) & 1, abort_flag))
                 return false;
             tc_fence_after();
             return true;
@@ -392,15 +497,38 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 mma_ts(lead, tmem + sp_col_o(x), tmem + sp_col_s(x) + 8 * i, desc_with_lo(vb + ((i * 2048) >> 4), hi_v),
                        kSpIdescPV, i > 0 ? 1u : acc0);
         };
+        // An own tile's P V, for rows lo .. hi - 1 of tile x alone: another
+        // request's rows have weights of 0, but 0 x NaN would reach them.
+        auto issue_pv_rows = [&](int x, int k, int lo, int hi) {
+            const uint32_t vb = lo_v + ((uint32_t)(kSpOffKV + (k % kSpSlots) * kSpTileBytes) >> 4);
+            uint32_t off[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int a0 = min(32, max(0, lo - 32 * i)), a1 = min(32, max(0, hi - 32 * i));
+                const uint32_t below_lo = a0 == 32 ? ~0u : (1u << a0) - 1u, below_hi = a1 == 32 ? ~0u : (1u << a1) - 1u;
+                off[i] = ~(below_hi & ~below_lo);
+            }
+#pragma unroll
+            for (int i = 0; i < kSpTile / 16; ++i)
+                mma_ts_rows(lead, tmem + sp_col_o(x), tmem + sp_col_s(x) + 8 * i,
+                            desc_with_lo(vb + ((i * 2048) >> 4), hi_v), kSpIdescPV, 1u, off);
+        };
         for (int64_t w = w_begin; w < w_end && ok;) {
-            const Seg sg = seg_at(a, groups, w, w_end);
+            OwnTiles ot;
+            const Seg sg = block_at(w, ot);
             w = sg.next;
             const int K = sg.je - sg.jb;
             // V tile i of the segment: landed, its rows behind the prefix zeroed
             auto wait_v = [&](int i) -> bool {
                 if (!wait_kv(tt + 2 * i + 1))
                     return false;
-                const int lim = sg.g.pre_len - (sg.jb + i) * kSpTile;
+                int lim = sg.g.pre_len - (sg.jb + i) * kSpTile;
+                if constexpr (kWhole) {
+                    if (i >= sg.g.nt) {
+                        const DevShared &rq = reqs[ot.b];
+                        lim = rq.own + rq.q_len - ot.k * kSpTile;
+                    }
+                }
                 if (lim < kSpTile) {
                     const uint32_t v = sbase + (uint32_t)(kSpOffKV + ((tt + 2 * i + 1) % kSpSlots) * kSpTileBytes);
                     for (int c = lim * 8 + lane; c < kSpTile * 8; c += 32) {
@@ -414,14 +542,14 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             };
             auto o_free = [&](int x) -> bool {
                 if (o_used[x]) {
-                    if (!mbar_wait(bar(kSbOEmpty + x), (uint32_t)oe_cnt[x] & 1, abort_flag))
+                    if (!mbar_wait_warp(bar(kSbOEmpty + x), (uint32_t)oe_cnt[x] & 1, abort_flag))
                         return false;
                     ++oe_cnt[x];
                     o_used[x] = false;
                 }
                 return true;
             };
-            if (!mbar_wait(bar(kSbQ), (uint32_t)nq & 1, abort_flag)) {
+            if (!mbar_wait_warp(bar(kSbQ), (uint32_t)nq & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -446,7 +574,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     if (x >= sg.nx)
                         break;
-                    if (!mbar_wait(bar(kSbP + x), (uint32_t)p_cnt[x] & 1, abort_flag)) {
+                    if (!mbar_wait_warp(bar(kSbP + x), (uint32_t)p_cnt[x] & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -456,7 +584,13 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    issue_pv(x, tt + 2 * i + 1, i > 0);
+                    if (kWhole && i >= sg.g.nt) {
+                        const DevShared &rq = reqs[ot.b];
+                        const int lo = (rq.q_off - sg.g.q_off) * a.group - sg.row0 - x * kSpTile;
+                        issue_pv_rows(x, tt + 2 * i + 1, lo, lo + rq.q_len * a.group);
+                    } else {
+                        issue_pv(x, tt + 2 * i + 1, i > 0);
+                    }
                     if (!more) {
                         umma_commit(lead, bar(kSbO + x));
                         o_used[x] = true;
@@ -470,6 +604,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
                 }
                 if (!ok)
                     break;
+                if (kWhole && i >= sg.g.nt)
+                    ot.next(reqs, sa->n_reqs);
                 if (i + 2 == K)
                     umma_commit(lead, bar(kSbQEmpty));   // the segment's last S is issued
                 umma_commit(lead, bar(kSbEmpty + (tt + 2 * i + 1) % kSpSlots));
@@ -491,6 +627,26 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kSpTmemCols);
     }
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kSpThreads, 1)
+    k_shared_prefix(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ SharedPrefixArgs a,
+                    const __grid_constant__ GroupTable gt)
+{
+    prefix_part<false>(tmq, tmk, tmv, a, a.groups ? a.groups : gt.groups, tmk, tmv, nullptr, nullptr);
+}
+
+__global__ void __launch_bounds__(kSpThreads, 1)
+    k_shared_whole(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                   const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmok,
+                   const __grid_constant__ CUtensorMap tmov, const __grid_constant__ SharedPrefixArgs a,
+                   const __grid_constant__ GroupTable gt, const __grid_constant__ SharedArgs sa,
+                   const __grid_constant__ SharedTable rt)
+{
+    prefix_part<true>(tmq, tmk, tmv, a, a.groups ? a.groups : gt.groups, tmok, tmov, &sa, sa.reqs ? sa.reqs : rt.reqs);
 }
 
 // ---------------------------------------------------------------------------
@@ -582,7 +738,7 @@ __device__ __forceinline__ PartRef part_ref(const SharedPrefixArgs &pa, const De
         return r;
     const int blk = group_row >> 8;
     const int64_t it = (int64_t)lh_s * pa.unit_blocks + g.item0 + blk;
-    const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.nt;
+    const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.pairs;
     const int ca = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0);
     const int cb = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0 + g.nt - 1);
     r.slot = it + ca;
@@ -1180,12 +1336,14 @@ static cudaError_t shared_attrs()
         return e;
     // the register split must fit what the CTA is launched with, or the
     // softmax warpgroups' increase would wait forever
-    cudaFuncAttributes fa{};
-    if ((e = cudaFuncGetAttributes(&fa, k_shared_prefix)) != cudaSuccess)
+    cudaFuncAttributes fa{}, fw{};
+    if ((e = cudaFuncGetAttributes(&fa, k_shared_prefix)) != cudaSuccess ||
+        (e = cudaFuncGetAttributes(&fw, k_shared_whole)) != cudaSuccess)
         return e;
-    if (fa.numRegs != kSpRegsLaunch)
+    if (fa.numRegs != kSpRegsLaunch || fw.numRegs != kSpRegsLaunch)
         return cudaErrorInvalidConfiguration;
     if ((e = cudaFuncSetAttribute(k_shared_prefix, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(k_shared_whole, cudaFuncAttributeMaxDynamicSharedMemorySize, kSpSmem)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(k_shared_own_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, ow_bytes(kOwTileMax))) !=
             cudaSuccess ||
         (e = cudaFuncSetAttribute(k_shared_own_decode<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOdSmem)) !=
@@ -1231,6 +1389,9 @@ cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s)
     const SharedPrefixArgs &pa = *t.prefix;
     static const CUtensorMap no_map{};
     auto map = [](const void *m) -> const CUtensorMap & { return m ? *static_cast<const CUtensorMap *>(m) : no_map; };
+    if (t.whole)
+        return launch_pdl(k_shared_whole, pa.n_ctas, kSpThreads, kSpSmem, pdl, s, map(t.tmap_q), map(t.tmap_pk),
+                          map(t.tmap_pv), map(t.tmap_k), map(t.tmap_v), pa, *t.groups, a, *t.reqs);
     if (pa.total > 0) {
         e = launch_pdl(k_shared_prefix, pa.n_ctas, kSpThreads, kSpSmem, pdl, s, map(t.tmap_q), map(t.tmap_pk),
                        map(t.tmap_pv), pa, *t.groups);

@@ -62,14 +62,15 @@ def _block(flat, offsets, b, LH):
 def _attention_ref(K, V, q, first_pos, n_own_before, scale):
     """K, V [n, D] fp64; q [Lq, G, D] rotated; token t sees rows < n_own_before + t + 1.
     Returns o, and per output the bound's ingredients A and sum |q k| (max over keys)."""
-    Lq = q.shape[0]
-    s = np.einsum("tgd,nd->tgn", q, K) * scale
-    vis = np.arange(K.shape[0])[None, :] <= n_own_before + np.arange(Lq)[:, None]
+    Lq, G, n = q.shape[0], q.shape[1], K.shape[0]
+    rows = lambda x, y: (x.reshape(Lq * G, -1) @ y).reshape(Lq, G, -1)
+    s = rows(q, K.T) * scale
+    vis = np.arange(n)[None, :] <= n_own_before + np.arange(Lq)[:, None]
     s = np.where(vis[:, None], s, -np.inf)
     p = np.exp(s - s.max(-1, keepdims=True))
     p /= p.sum(-1, keepdims=True)
-    qk = np.where(vis[:, None], np.einsum("tgd,nd->tgn", np.abs(q), np.abs(K)), 0.0) * scale
-    return (np.einsum("tgn,nd->tgd", p, V), np.einsum("tgn,nd->tgd", p, np.abs(V)), qk, p)
+    qk = np.where(vis[:, None], rows(np.abs(q), np.abs(K).T), 0.0) * scale
+    return rows(p, V), rows(p, np.abs(V)), qk, p
 
 
 def _check_attention(got, ref, A, qk, n, dtype, D):
@@ -189,6 +190,42 @@ def test_shared_prefix_query_rows_at_tile_edges(rows):
     _shared_case(1, 1, 1, 128, "bf16", groups=[rows], prefix=[260], own=[i % 3 for i in range(rows)], q=[1] * rows)
 
 
+# enough blocks of 256 query rows for every SM: prefix and own keys in one kernel
+WHOLE = {
+    "two-groups": dict(G=4, L=19, groups=[3, 2], prefix=[200, 385], own=[0, 3, 300, 128, 1], q=[100, 130, 33, 150, 99]),
+    "odd-heads": dict(G=7, L=16, groups=[1, 3], prefix=[1, 129], own=[127, 0, 40, 5], q=[128, 64, 1, 190]),
+    "some-without-tokens": dict(G=16, L=19, groups=[2, 0, 3], prefix=[64, 9, 128], own=[7, 2, 0, 9, 129], q=[150, 0, 0, 127, 1]),
+    "one-row-blocks": dict(G=1, L=24, groups=[1] * 8, prefix=[300 + i for i in range(8)], own=list(range(8)), q=[1] * 8),
+}
+
+
+@pytest.mark.parametrize("name", WHOLE)
+def test_shared_prefix_of_many_query_blocks(name):
+    c = dict(WHOLE[name])
+    L, G = c.pop("L"), c.pop("G")
+    _shared_case(L, 8, G, 128, "bf16", **c)
+
+
+def test_shared_prefix_of_many_query_blocks_keeps_requests_apart():
+    """What is not a number in one request's values and keys reaches none of the
+    others, which share its blocks of query rows."""
+    import torch
+    q = [100, 30, 70, 33, 200, 79]
+    pool, args, _ = _shared_case(19, 8, 4, 128, "bf16", groups=[6], prefix=[200], own=[5, 0, 9, 130, 1, 2], q=q, check=(1,))
+    want = args[-1].clone()
+    qo = _starts(q)
+    a, b = int(qo[2]), int(qo[3])
+    args[9][:, a + 3:b, :, 5] = float("nan")
+    args[10][:, a:b, :, ::3] = float("inf")
+    args[10][:, a:b, :, 1] = float("nan")
+    pool.shared_query_attention(*args)
+    torch.cuda.synchronize()
+    got = args[-1]
+    for x, y in ((0, a), (b, int(qo[-1]))):
+        assert torch.equal(got[:, x:y], want[:, x:y])
+    assert not torch.isfinite(got[:, a:b]).all()
+
+
 def test_shared_prefix_in_slices():
     """More than 1 GiB of partial results (64 units x 128 blocks of 256 rows):
     the units go through in two slices."""
@@ -220,6 +257,31 @@ def test_shared_prefix_large_scores():
     pool.check()
     kr = oracle.rope(to_np64(kq), np.full((1, 2, 1), float(P)), THETA)
     for b in range(2):
+        for h in range(H):
+            Kf = np.concatenate([to_np64(K[h]), kr[0, b, h][None]])
+            Vf = np.concatenate([to_np64(V[h]), to_np64(vq[0, b, h])[None]])
+            ref, A, qk, _ = _attention_ref(Kf, Vf, qr[:, b, h * G:(h + 1) * G], 0, P, D ** -0.5)
+            _check_attention(to_np64(out[:, b, h * G:(h + 1) * G]), ref, A, qk, P + 1, "bf16", D)
+
+
+@pytest.mark.parametrize("rows", [24, 200])
+def test_shared_prefix_of_growing_scores(rows):
+    """Prefix keys of growing length: every row's maximum moves, at tiles of its own."""
+    import torch
+    L, H, G, D, P, B = 1, 2, 4, 128, 900, rows // 4
+    pool = _pool(L, H, G, D, "bf16")
+    K, V = _randn(1, (H, P, D), "bf16"), _randn(2, (H, P, D), "bf16")
+    K = (K.float() * torch.linspace(0.05, 6.0, P, device="cuda")[None, :, None]).to(K.dtype)
+    q, kq, vq = _randn(3, (L, B, H * G, D), "bf16"), _randn(4, (L, B, H, D), "bf16"), _randn(5, (L, B, H, D), "bf16")
+    ck = torch.full((B * H * 2, D), float("nan"), device="cuda", dtype=torch.bfloat16)
+    cv, out = ck.clone(), torch.empty_like(q)
+    pool.shared_query_attention([0, B], [0, P], [P], K.reshape(-1, D), V.reshape(-1, D), np.arange(B + 1) * 2, [0] * B,
+                                np.arange(B + 1), q, kq, vq, ck, cv, out)
+    torch.cuda.synchronize()
+    pool.check()
+    pos = np.full((1, 1, 1), float(P))
+    qr, kr = oracle.rope(to_np64(q), pos, THETA), oracle.rope(to_np64(kq), pos, THETA)
+    for b in range(B):
         for h in range(H):
             Kf = np.concatenate([to_np64(K[h]), kr[0, b, h][None]])
             Vf = np.concatenate([to_np64(V[h]), to_np64(vq[0, b, h])[None]])
