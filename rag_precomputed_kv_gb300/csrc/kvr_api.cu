@@ -1491,8 +1491,15 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
             place[g] = (int32_t)pl.gr.size();
             pl.gr.push_back(d);
         }
-    // Whole blocks, own keys and all, in one kernel
-    const bool whole = all_active && blocks * LH >= 8 * (int64_t)p->n_sms && own_tiles <= 6 * blocks;
+    // One kernel for whole blocks, their own keys and the output, where blocks are
+    // well filled, enough for all SMs, and meet few own tiles: 16 requests of 64
+    // tokens x 7 heads on 2,592 shared rows, 112 units: 995 us against 1,061 with
+    // partial results and an own part; 8 of 70 x 4 on 400 rows, 288 units: 352
+    // against 450.  Blocks of few rows wait for each tile in turn: 8 groups of one
+    // 4-row request on 2,000 rows: 451 against 391.  Four own tiles a block: 238
+    // against 222 for 16 requests of 20 x 4 rows on 500.
+    const bool whole = all_active && q_offsets[sa.n_reqs] * (int64_t)G >= 128 * blocks &&
+                       blocks * LH >= 4 * (int64_t)p->n_sms && own_tiles <= 3 * blocks;
     // the (block, key tile) pairs, numbered group by group
     for (DevGroup &d : pl.gr) {
         if (whole && d.mb > 0)

@@ -18,6 +18,9 @@
 //                      (block, key tile) pairs of the call in a row, is cut in
 //                      equal stretches, one per SM; a block that a stretch ends
 //                      in has several partial results.
+//   k_shared_whole     the same for whole blocks, whose rows' own keys follow
+//                      the prefix's, tile by tile, request by request; it
+//                      writes the output.  Nothing else is launched then.
 //   k_shared_own_*     the own part, and the sum of everything: the own rows
 //                      through register-resident warp MMAs (as the decode
 //                      step), then the prefix's partial results are added and
@@ -29,9 +32,16 @@
 // against 695 for 64 rows on 33,248 prefix rows and 256 units, 105 against 95
 // for 7 rows on 8,256 and 112 units: twice the partial results, for nothing.)
 //
-// Values behind the last prefix row are zeroed in shared memory before the
-// P V product that reaches them (a masked key's weight is 0, but 0 x NaN is
-// NaN), so the blocks' spare rows are neither read as data nor written.
+// Values behind the last row are zeroed in shared memory before the P V product
+// that reaches them (a masked key's weight is 0, but 0 x NaN is NaN), so the
+// blocks' spare rows are neither read as data nor written; an own tile's
+// product leaves the O rows of other requests out.
+//
+// Measured on whole calls (bf16, head_dim 128): 64 rows on 33,248 prefix rows,
+// 256 units: k_shared_prefix 606 us, 7.2 TB/s of K and V; 256 rows on 8,256, 288
+// units: 213 us, 1.46 PFLOP/s, and 166 us for 64 requests' own rows;
+// 7,168 rows on 2,592, 112 units: k_shared_whole 925 us, 1.18 PFLOP/s, behind 80
+// us of k_shared_prologue (6.7 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
