@@ -1447,10 +1447,10 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
     pa.total_q = sa.total_q;
     pa.scale_log2 = sa.scale_log2;
     pa.err = p->err;
-    // groups with prefix and tokens first; the others behind them
+    // groups with prefix and tokens first, numbered pair by pair; the others behind them
     pl.gr.reserve(n_groups);
     std::vector<int32_t> place(n_groups);
-    int64_t own_tiles = 0, blocks = 0;   // of a unit: own key tiles that the 256-row blocks meet
+    int64_t own_tiles = 0;   // that the 256-row blocks of a unit meet
     bool all_active = true;
     for (int pass = 0; pass < 2; ++pass)
         for (int g = 0; g < n_groups; ++g) {
@@ -1467,26 +1467,26 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
             d.q_off = t0;
             d.rows = (t1 - t0) * G;
             if (active) {
-                d.nt = d.pairs = (d.pre_len + 127) / 128;
+                d.nt = (d.pre_len + 127) / 128;
                 d.mb = (d.rows + 255) / 256;
-                blocks += d.mb;
-                // the block that meets most own tiles
-                int b = group_offsets[g], most = 0;
+                d.item0 = pa.unit_blocks;
+                d.w0 = pa.unit_pairs;
+                pa.unit_blocks += d.mb;
+                pa.unit_pairs += (int64_t)d.mb * d.nt;
+                int b = group_offsets[g];
                 for (int m = 0; m < d.mb; ++m) {
                     const int32_t first = t0 + m * 256 / G;
                     const int32_t end = t0 + (std::min(d.rows, m * 256 + 256) - 1) / G + 1;
-                    int n = 0;
                     while (pl.rq[b].q_off + pl.rq[b].q_len <= first)
                         ++b;
                     for (int i = b; i < group_offsets[g + 1] && pl.rq[i].q_off < end; ++i)
                         if (pl.rq[i].q_len > 0)
-                            n += (pl.rq[i].own + std::min(pl.rq[i].q_len, end - pl.rq[i].q_off) + 127) / 128;
-                    own_tiles += n;
-                    most = std::max(most, n);
+                            own_tiles += (pl.rq[i].own + std::min(pl.rq[i].q_len, end - pl.rq[i].q_off) + 127) / 128;
                 }
-                d.most_own = most;
-            } else if (t1 > t0) {
-                all_active = false;
+            } else {
+                d.item0 = pa.unit_blocks;
+                d.w0 = pa.unit_pairs;
+                all_active = all_active && t1 == t0;
             }
             place[g] = (int32_t)pl.gr.size();
             pl.gr.push_back(d);
@@ -1498,17 +1498,8 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
     // against 450.  Blocks of few rows wait for each tile in turn: 8 groups of one
     // 4-row request on 2,000 rows: 451 against 391.  Four own tiles a block: 238
     // against 222 for 16 requests of 20 x 4 rows on 500.
-    const bool whole = all_active && q_offsets[sa.n_reqs] * (int64_t)G >= 128 * blocks &&
-                       blocks * LH >= 4 * (int64_t)p->n_sms && own_tiles <= 3 * blocks;
-    // the (block, key tile) pairs, numbered group by group
-    for (DevGroup &d : pl.gr) {
-        if (whole && d.mb > 0)
-            d.pairs = d.nt + d.most_own;
-        d.item0 = pa.unit_blocks;
-        d.w0 = pa.unit_pairs;
-        pa.unit_blocks += d.mb;
-        pa.unit_pairs += (int64_t)d.mb * d.pairs;
-    }
+    const bool whole = all_active && sa.total_q * (int64_t)G >= 128 * pa.unit_blocks &&
+                       pa.unit_blocks * LH >= 4 * (int64_t)p->n_sms && own_tiles <= 3 * pa.unit_blocks;
     for (int g = 0; g < n_groups; ++g)
         for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
             pl.rq[b].group = place[g];
@@ -1571,7 +1562,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         NvtxRange r("kvr.k_shared_prefix_own");
         pa.lh_base = lh;
         pa.lh_count = std::min(lh_slice, LH - lh);
-        pa.total = pa.lh_count * pa.unit_pairs;
+        pa.total = pa.lh_count * (whole ? pa.unit_blocks : pa.unit_pairs);
         pa.n_ctas = (int32_t)std::min<int64_t>(p->n_sms, pa.total);
         pa.ratio = pa.total > 0 ? (float)((double)pa.n_ctas / (double)pa.total) : 0.f;
         e = launch_shared_tc(t, !p->timed, s);

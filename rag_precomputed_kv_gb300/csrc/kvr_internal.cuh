@@ -292,9 +292,7 @@ struct alignas(16) DevGroup {
     int32_t rows;        // tokens x G
     int32_t nt;          // 128-key tiles of the prefix
     int32_t mb;          // 256-row blocks
-    int32_t pairs;       // pairs of a block: nt, or (whole) nt and the own tiles of the block that meets most
-    int32_t most_own;    // own tiles of that block
-    int32_t pad_[2];
+    int32_t pad_[4];
 };
 static_assert(sizeof(DevGroup) == 64, "group table layout");
 struct GroupTable {
@@ -311,7 +309,7 @@ struct SharedPrefixArgs {
     int32_t lh_base, lh_count;  // the slice of (layer, kv-head) units of this launch
     int32_t n_ctas;             // stretches that the pairs are cut in
     int64_t unit_pairs, unit_blocks;   // pairs, blocks of one unit
-    int64_t total;              // pairs of the slice: lh_count * unit_pairs
+    int64_t total;              // pairs (whole: blocks) of the slice: lh_count times a unit's
     float ratio;                // n_ctas / total
     float *part;                // (blocks + n_ctas) partial results
     const void *q_rot;          // [L][Hkv][T][G][D], rotated

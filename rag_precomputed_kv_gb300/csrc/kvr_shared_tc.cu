@@ -125,7 +125,14 @@ struct Seg {
     int nx;          // its 128-row tiles: A, or A and B
     int jb, je;      // key tiles
     int64_t item;    // block index in the call
-    int64_t next;    // the stretch's next pair
+    int64_t next;    // the stretch's next pair (whole: the CTA's next block)
+
+    __device__ __forceinline__ void set_rows(int blk)
+    {
+        row0 = blk * 256;
+        rows = min(256, g.rows - row0);
+        nx = rows > 128 ? 2 : 1;
+    }
 };
 
 __device__ __forceinline__ Seg seg_at(const SharedPrefixArgs &a, const DevGroup *groups, int64_t w, int64_t w_end)
@@ -142,14 +149,35 @@ __device__ __forceinline__ Seg seg_at(const SharedPrefixArgs &a, const DevGroup 
             hi = mid - 1;
     }
     s.g = groups[lo];
-    const int blk = (int)((in_unit - s.g.w0) / s.g.pairs);
-    s.jb = (int)(in_unit - s.g.w0 - (int64_t)blk * s.g.pairs);
-    s.je = (int)min((int64_t)s.g.pairs, s.jb + (w_end - w));
+    const int blk = (int)((in_unit - s.g.w0) / s.g.nt);
+    s.jb = (int)(in_unit - s.g.w0 - (int64_t)blk * s.g.nt);
+    s.je = (int)min((int64_t)s.g.nt, s.jb + (w_end - w));
     s.next = w + (s.je - s.jb);
     s.item = (int64_t)s.lh * a.unit_blocks + s.g.item0 + blk;
-    s.row0 = blk * 256;
-    s.rows = min(256, s.g.rows - s.row0);
-    s.nx = s.rows > 128 ? 2 : 1;
+    s.set_rows(blk);
+    return s;
+}
+
+// Whole block i of the call, with all tiles of the prefix.
+__device__ __forceinline__ Seg block_at(const SharedPrefixArgs &a, const DevGroup *groups, int64_t i, int step)
+{
+    Seg s;
+    s.lh = (int)(i / a.unit_blocks);
+    const int64_t in_unit = i - (int64_t)s.lh * a.unit_blocks;
+    int lo = 0, hi = a.n_groups - 1;
+    while (lo < hi) {   // the last group whose first block in the unit is <= i (one with blocks)
+        const int mid = (lo + hi + 1) >> 1;
+        if (groups[mid].item0 <= in_unit)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    s.g = groups[lo];
+    s.jb = 0;
+    s.je = s.g.nt;
+    s.next = i + step;
+    s.item = i;
+    s.set_rows((int)(in_unit - s.g.item0));
     return s;
 }
 
@@ -195,8 +223,11 @@ struct OwnTiles {
     }
 };
 
-// kWhole: stretches of whole blocks, whose own keys follow the prefix's, and
-// whose rows are written as the output; else partial results of the prefix.
+// kWhole: whole blocks, whose own keys follow the prefix's, and whose rows are
+// written as the output, else stretches of pairs and partial results of the
+// prefix.  Whole blocks go round the CTAs one by one: those of a unit, which read
+// the same prefix, run at the same time (consecutive blocks in a CTA: 1.7 GB read
+// from DRAM for 0.25 GB of prefix and queries).
 template <bool kWhole>
 __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                             const SharedPrefixArgs &a, const DevGroup *groups, const CUtensorMap &tmok,
@@ -208,23 +239,17 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
     auto bar = [&](int i) { return sbase + kSpOffBar + 8u * (uint32_t)i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSpOffMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t w_begin = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x);
-    const int64_t w_end = stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x + 1);
-    // the block that holds pair w (whole: all of it, with its own tiles)
-    auto block_at = [&](int64_t w, OwnTiles &ot) -> Seg {
-        Seg s = seg_at(a, groups, w, w_end);
+    const int64_t w_begin = kWhole ? blockIdx.x : stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x);
+    const int64_t w_end = kWhole ? a.total : stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x + 1);
+    auto seg = [&](int64_t w, OwnTiles &ot) -> Seg {
         if constexpr (kWhole) {
-            s.next = w + s.g.pairs;
-            s.je = s.g.nt + ot.first(reqs, sa->n_reqs, s, a.group);
+            Seg s = block_at(a, groups, w, (int)gridDim.x);
+            s.je += ot.first(reqs, sa->n_reqs, s, a.group);
+            return s;
+        } else {
+            return seg_at(a, groups, w, w_end);
         }
-        return s;
     };
-    if constexpr (kWhole) {   // from the first block that begins in the stretch on
-        if (w_begin < w_end) {
-            const Seg s = seg_at(a, groups, w_begin, w_end);
-            w_begin += s.jb > 0 ? s.g.pairs - s.jb : 0;
-        }
-    }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSbNum; ++i)
@@ -256,7 +281,7 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
         bool ok = true;
         for (int64_t w = w_begin; w < w_end && ok;) {
             OwnTiles ot;
-            const Seg sg = block_at(w, ot);
+            const Seg sg = seg(w, ot);
             w = sg.next;
             if (x >= sg.nx)
                 continue;
@@ -421,7 +446,7 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
             int tt = 0, nq = 0;
             for (int64_t w = w_begin; w < w_end && ok;) {
                 OwnTiles ot;
-                const Seg sg = block_at(w, ot);
+                const Seg sg = seg(w, ot);
                 w = sg.next;
                 const int64_t kv0 = sg.g.pre_row0 + (int64_t)(a.lh_base + sg.lh) * sg.g.pre_cap;
                 const int n_loads = 2 * (sg.je - sg.jb);
@@ -525,7 +550,7 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
         };
         for (int64_t w = w_begin; w < w_end && ok;) {
             OwnTiles ot;
-            const Seg sg = block_at(w, ot);
+            const Seg sg = seg(w, ot);
             w = sg.next;
             const int K = sg.je - sg.jb;
             // V tile i of the segment: landed, its rows behind the prefix zeroed
@@ -748,7 +773,7 @@ __device__ __forceinline__ PartRef part_ref(const SharedPrefixArgs &pa, const De
         return r;
     const int blk = group_row >> 8;
     const int64_t it = (int64_t)lh_s * pa.unit_blocks + g.item0 + blk;
-    const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.pairs;
+    const int64_t w0 = (int64_t)lh_s * pa.unit_pairs + g.w0 + (int64_t)blk * g.nt;
     const int ca = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0);
     const int cb = stretch_of(pa.total, pa.n_ctas, pa.ratio, w0 + g.nt - 1);
     r.slot = it + ca;
