@@ -1493,13 +1493,19 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         }
     // One kernel for whole blocks, their own keys and the output, where blocks are
     // well filled, enough for all SMs, and meet few own tiles: 16 requests of 64
-    // tokens x 7 heads on 2,592 shared rows, 112 units: 995 us against 1,061 with
-    // partial results and an own part; 8 of 70 x 4 on 400 rows, 288 units: 352
-    // against 450.  Blocks of few rows wait for each tile in turn: 8 groups of one
+    // tokens x 7 heads on 2,592 shared rows, 112 units: 925 us against 1,070 with
+    // partial results and an own part; 8 of 70 x 4 on 400 rows, 288 units: 338
+    // against 443.  Blocks of few rows wait for each tile in turn: 8 groups of one
     // 4-row request on 2,000 rows: 451 against 391.  Four own tiles a block: 238
     // against 222 for 16 requests of 20 x 4 rows on 500.
     const bool whole = all_active && sa.total_q * (int64_t)G >= 128 * pa.unit_blocks &&
                        pa.unit_blocks * LH >= 4 * (int64_t)p->n_sms && own_tiles <= 3 * pa.unit_blocks;
+    // Consecutive blocks of a CTA: one where the prefix is long, so that a unit's
+    // blocks run side by side and read it once from DRAM (21 tiles: 925 us with runs
+    // of 1, 936 of 4, 959 with one run; 47: 1,052, 1,080, 1,112); some 32 tiles'
+    // worth where it is short and the next block's first loads count (4 tiles: 388
+    // us with 1, 347 with 4, 338 with 8; 7: 846, 817, 804; 12: 268, 261, 262).
+    pa.run = (int32_t)std::max<int64_t>(1, pa.unit_pairs > 0 ? 32 * pa.unit_blocks / pa.unit_pairs : 1);
     for (int g = 0; g < n_groups; ++g)
         for (int b = group_offsets[g]; b < group_offsets[g + 1]; ++b)
             pl.rq[b].group = place[g];

@@ -311,6 +311,7 @@ struct SharedPrefixArgs {
     int64_t unit_pairs, unit_blocks;   // pairs, blocks of one unit
     int64_t total;              // pairs (whole: blocks) of the slice: lh_count times a unit's
     float ratio;                // n_ctas / total
+    int32_t run;                // whole: consecutive blocks of a CTA
     float *part;                // (blocks + n_ctas) partial results
     const void *q_rot;          // [L][Hkv][T][G][D], rotated
     float scale_log2;

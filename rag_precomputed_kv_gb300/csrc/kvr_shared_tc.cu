@@ -158,10 +158,20 @@ __device__ __forceinline__ Seg seg_at(const SharedPrefixArgs &a, const DevGroup 
     return s;
 }
 
-// Whole block i of the call, with all tiles of the prefix.
-__device__ __forceinline__ Seg block_at(const SharedPrefixArgs &a, const DevGroup *groups, int64_t i, int step)
+// The whole blocks of CTA c of n: runs of a.run blocks go round the CTAs, what is
+// left over is cut in equal stretches.
+__device__ __forceinline__ int64_t blocks_of(const SharedPrefixArgs &a, int n, int c)
+{
+    const int64_t rounds = a.total / ((int64_t)n * a.run), rest = a.total - rounds * n * a.run;
+    return rounds * a.run + stretch_start(rest, n, c + 1) - stretch_start(rest, n, c);
+}
+// The w-th of them, with all tiles of the prefix.
+__device__ __forceinline__ Seg block_at(const SharedPrefixArgs &a, const DevGroup *groups, int64_t w, int n, int c)
 {
     Seg s;
+    const int64_t rounds = a.total / ((int64_t)n * a.run), q = w / a.run;
+    const int64_t i = q < rounds ? (q * n + c) * a.run + (w - q * a.run)
+                                 : rounds * n * a.run + stretch_start(a.total - rounds * n * a.run, n, c) + (w - rounds * a.run);
     s.lh = (int)(i / a.unit_blocks);
     const int64_t in_unit = i - (int64_t)s.lh * a.unit_blocks;
     int lo = 0, hi = a.n_groups - 1;
@@ -175,7 +185,7 @@ __device__ __forceinline__ Seg block_at(const SharedPrefixArgs &a, const DevGrou
     s.g = groups[lo];
     s.jb = 0;
     s.je = s.g.nt;
-    s.next = i + step;
+    s.next = w + 1;
     s.item = i;
     s.set_rows((int)(in_unit - s.g.item0));
     return s;
@@ -225,9 +235,9 @@ struct OwnTiles {
 
 // kWhole: whole blocks, whose own keys follow the prefix's, and whose rows are
 // written as the output, else stretches of pairs and partial results of the
-// prefix.  Whole blocks go round the CTAs one by one: those of a unit, which read
-// the same prefix, run at the same time (consecutive blocks in a CTA: 1.7 GB read
-// from DRAM for 0.25 GB of prefix and queries).
+// prefix.  Whole blocks go round the CTAs in short runs: those of a unit, which
+// read the same prefix, run at the same time (all of a CTA's blocks in a row: 1.7
+// GB read from DRAM for 0.25 GB of prefix and queries).
 template <bool kWhole>
 __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                                             const SharedPrefixArgs &a, const DevGroup *groups, const CUtensorMap &tmok,
@@ -239,11 +249,12 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
     auto bar = [&](int i) { return sbase + kSpOffBar + 8u * (uint32_t)i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSpOffMisc + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t w_begin = kWhole ? blockIdx.x : stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x);
-    const int64_t w_end = kWhole ? a.total : stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x + 1);
+    const int64_t w_begin = kWhole ? 0 : stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x);
+    const int64_t w_end = kWhole ? blocks_of(a, (int)gridDim.x, (int)blockIdx.x)
+                                 : stretch_start(a.total, (int)gridDim.x, (int)blockIdx.x + 1);
     auto seg = [&](int64_t w, OwnTiles &ot) -> Seg {
         if constexpr (kWhole) {
-            Seg s = block_at(a, groups, w, (int)gridDim.x);
+            Seg s = block_at(a, groups, w, (int)gridDim.x, (int)blockIdx.x);
             s.je += ot.first(reqs, sa->n_reqs, s, a.group);
             return s;
         } else {
