@@ -13,7 +13,7 @@
 // of short passes bound by their latency.  Then the kept rows are gathered: an
 // HBM stream like the stitch.  With many units of few rows both in one kernel
 // (k_evict_unit), else a kernel each (k_evict_select, k_evict_move).
-// Measured (bf16, head_dim 128): 4,608 units of 1,344 rows to 512: 370 us, of
+// Measured (bf16, head_dim 128): 4,608 units of 1,044 to 1,344 rows to 512: 370 us, of
 // which 362 are the rows' and weights' bytes at the copy rate; 256 units of
 // 33,504 rows to 4,096: 52 us + 167 us (6.6 TB/s); 112 units of 2,656 rows to
 // 1,024: 9 us + 19 us (6.3 TB/s).
@@ -546,7 +546,7 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
     };
     auto smem_rows = [&](int threads) { return (a.max_n + 4 * threads - 1) / (4 * threads) * 4 * threads; };   // keys there
     // One kernel where there are two units per SM or more and their keys leave
-    // room for three CTAs: 4,608 units of 1,344 rows 370 us a call, 531 in two
+    // room for three CTAs: 4,608 units of up to 1,344 rows 370 us a call, 531 in two
     // kernels; 336 units of 2,656 rows 73 against 76; 224 units 52 against 53; 112
     // units 39 against 29 (a CTA each cannot move them at full rate).
     if (a.max_n <= 24 * 256 && ctas >= 2 * (int64_t)n_sms) {

@@ -17,9 +17,10 @@
 // summed.  So that K is read once, the scores stay in TMEM in between: of a
 // CTA's 256 columns some 64 to 96 take the products, and the others hold the
 // scores of tiles, one column a query row (48 tiles at up to 4 rows, 24 at 8, 10
-// at 16, 5 at 32), and the CTAs of a cluster split a unit's key tiles and exchange their rows' (max, sum) through
-// distributed shared memory.  Tiles beyond what TMEM holds are processed first,
-// for their statistics only, and loaded again at the end.
+// at 16, 5 at 32); the CTAs of a cluster split a unit's key tiles and exchange
+// their rows' (max, sum) through distributed shared memory.  Tiles beyond what
+// TMEM holds are processed first, for their statistics only, and loaded again at
+// the end.
 //
 // Rotated queries are split into three bf16 terms (8 + 8 + 8 bits: all of the
 // fp32 rotation's), so that the weights are fp32 results.  The terms stand side
@@ -31,6 +32,11 @@
 // while the other is in its prologue or exchange.  Warps 0-3 rotate the
 // queries and run the softmax passes; warp 4 issues the TMA loads (16 KB
 // panels: 128 keys x 64 dims); warp 5 the MMAs.  All waits are bounded.
+//
+// Bound by the one read of K where it is long: 4 rows, 33,281 keys, 512 units:
+// 725 us, 6.0 TB/s.  A short unit is latency: 7 rows, 2,657 keys, 112 units: 23
+// us a call, 3.3 TB/s (setup and rotation 4 us, then two passes and an exchange
+// that only the SM's other CTA overlaps).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -589,15 +595,19 @@ __global__ void __launch_bounds__(kWtThreads, 2)
 // ---------------------------------------------------------------------------
 // windows: more than 32 query rows
 // ---------------------------------------------------------------------------
-// At many rows the scores of a unit do not fit TMEM and exp2, not the read of
-// K, bounds the kernel.  So K is streamed twice (the second time mostly from
-// L2) and each pass takes the orientation in which its sum stays inside a
+// At many rows the scores of a unit do not fit TMEM, and the products, not the
+// read of K, bound the kernel.  So K is streamed twice (the second time mostly
+// from L2) and each pass takes the orientation in which its sum stays inside a
 // thread: S = Q K^T for the rows' denominators (a thread owns a query row),
 // S^T = K Q^T for the weights (a thread owns a key); the two operands' shared
 // memory is the same.  Two bf16 query terms: the weight of a key sums over all
 // the rows, which averages the 2^-17 that they leave.  Blocks of 128 rows; a
 // unit's tiles are split over a cluster only when there are too few units to
-// fill the SMs.
+// fill the SMs.  128 rows, 969 to 1,248 keys, 4,608 units: 491 us; the 2 x 2
+// products are 340 us at the tensor rate, and a fifth of a CTA's time is setup,
+// rotation and exit, which only the SM's other CTA overlaps.  (32 rows cost it
+// 434 us on 16 requests of 1,300 keys, the kernel above 388; that one, with 128
+// rows' scores in TMEM, would keep one tile.)
 namespace {
 constexpr int kWwSlots = 3;
 constexpr int kWwMaxCluster = 8;

@@ -39,9 +39,16 @@
 //
 // Measured on whole calls (bf16, head_dim 128): 64 rows on 33,248 prefix rows,
 // 256 units: k_shared_prefix 606 us, 7.2 TB/s of K and V; 256 rows on 8,256, 288
-// units: 213 us, 1.46 PFLOP/s, and 166 us for 64 requests' own rows;
-// 7,168 rows on 2,592, 112 units: k_shared_whole 925 us, 1.18 PFLOP/s, behind 80
+// units: 213 us, 1.46 PFLOP/s, and 166 us for 64 requests' own rows (4.6 TB/s);
+// 6,328 rows on 2,592, 112 units: k_shared_whole 850 us, 1.12 PFLOP/s, behind 80
 // us of k_shared_prologue (6.7 TB/s).
+//
+// Rounded to bf16 on the way, as the query prefill and the decode step do it: the
+// rotated queries (the cached keys are) and each probability, because both are
+// operands of a product with bf16 keys or values.  With the output's own rounding
+// that is 0.0029 of the output's norm, against 0.0017 for the last alone; two
+// bf16 terms for the queries would add half of all products, for the
+// probabilities another half.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -934,10 +941,14 @@ __device__ __forceinline__ void finish_rows(const SharedArgs &a, const SharedPre
 }
 }  // namespace
 
-// More than 16 query rows a request: a CTA takes `tiles_per_cta` groups of 64
-// rows of a (request, unit); each warp has an MMA row tile of its own and takes
-// all keys of a tile.  Own parts of one tile are loaded once per CTA, and its
-// warps then go through their rows independently.
+// More than 16 query rows a request (an MMA row tile of the kernel below): a CTA
+// takes `tiles_per_cta` groups of 64 rows of a (request, unit); each warp has a
+// row tile of its own and takes all keys of a tile.  Own parts of one tile are
+// loaded once per CTA, and its warps then go through their rows independently.
+// Bound by the reads of queries and partial results: 708,736 rows of 49 to 64
+// keys: 225 us, 3.5 TB/s.  (With 4 rows a request, three of four warps are idle: a
+// step of 64 requests on 8,256 rows takes 491 us with it, 391 with the kernel
+// below.)
 __global__ void __launch_bounds__(kOwThreads, 3)
     k_shared_own_rows(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                  const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
@@ -1138,7 +1149,9 @@ __global__ void __launch_bounds__(kOwThreads, 3)
 // pieces: its lane 0 loads the K and V rows 32 keys at a time, two steps ahead
 // (across pieces), the warp runs S, softmax and P V of a step in registers, adds
 // the prefix's partial results at the end of a piece and writes its rows.  Seven
-// warps per SM, 32 KB of tiles each.
+// warps per SM, 32 KB of tiles each.  64 requests of 32 to 128 rows, 288 units:
+// 166 us, 4.6 TB/s of K and V (a CTA a piece took 291).  With at most 8 query rows the upper half of
+// the MMA row tile is left out: 391 us a call against 400.
 namespace {
 constexpr int kOdWarps = 7;
 constexpr int kOdThreads = 32 * kOdWarps;
