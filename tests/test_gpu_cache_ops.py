@@ -195,6 +195,8 @@ WHOLE = {
     "two-groups": dict(G=4, L=19, groups=[3, 2], prefix=[200, 385], own=[0, 3, 300, 128, 1], q=[100, 130, 33, 150, 99]),
     "odd-heads": dict(G=7, L=16, groups=[1, 3], prefix=[1, 129], own=[127, 0, 40, 5], q=[128, 64, 1, 190]),
     "some-without-tokens": dict(G=16, L=19, groups=[2, 0, 3], prefix=[64, 9, 128], own=[7, 2, 0, 9, 129], q=[150, 0, 0, 127, 1]),
+    "many-requests": dict(G=8, L=2, groups=[40, 30], prefix=[140, 385], own=[i % 7 for i in range(70)],
+                          q=[20 + i % 5 for i in range(70)]),
     "one-row-blocks": dict(G=1, L=24, groups=[1] * 8, prefix=[300 + i for i in range(8)], own=list(range(8)), q=[1] * 8),
 }
 
@@ -204,6 +206,11 @@ def test_shared_prefix_of_many_query_blocks(name):
     c = dict(WHOLE[name])
     L, G = c.pop("L"), c.pop("G")
     _shared_case(L, 8, G, 128, "bf16", **c)
+
+
+@pytest.mark.parametrize("q", [[1, 1], [3, 1]])
+def test_shared_prefix_of_more_heads_than_a_tile_has_rows(q):
+    _shared_case(1, 1, 130, 128, "bf16", groups=[2], prefix=[300], own=[0, 70], q=q)
 
 
 def test_shared_prefix_of_many_query_blocks_keeps_requests_apart():
@@ -390,7 +397,7 @@ def test_key_weights(name, L, H, G, D, dtype):
     _weights_case(L, H, G, D, dtype, **WEIGHTS[name], accumulate=name in ("decode", "long", "some-without-tokens"))
 
 
-@pytest.mark.parametrize("G", [1, 7, 8, 16, 17, 32])
+@pytest.mark.parametrize("G", [1, 7, 8, 16, 17, 32, 130])
 @pytest.mark.parametrize("q", [1, 5, 40])
 def test_key_weights_group_sizes(G, q):
     _weights_case(1, 1, G, 128, "bf16", prefix=[333, 1500], q=[q, 1], accumulate=q == 5)
@@ -767,3 +774,56 @@ def test_evict_and_weights_on_another_stream_and_in_a_graph():
     for x, y in zip((w, kept, dk, dv, dw), want):
         assert torch.equal(x, y)
     pool.check()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "fp32"), (128, "bf16")])
+def test_shared_prefix_in_a_graph(D, dtype):
+    """The CUDA-core path is kernels alone and can be captured; the tensor-core
+    path uses the pool's scratch and says so, and the capture stays usable."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    pool, args, _ = _shared_case(1, 2, 2, D, dtype, groups=[2], prefix=[140], own=[3, 0], q=[1, 1])
+    want = args[-1].clone()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    if dtype == "bf16":
+        with torch.cuda.graph(g, stream=s):
+            args[-1].zero_()
+            with pytest.raises(kvr.KvrError) as e:
+                pool.shared_query_attention(*args)
+        assert e.value.status == 3
+        pool.shared_query_attention(*args)
+    else:
+        with torch.cuda.graph(g, stream=s):
+            pool.shared_query_attention(*args)
+        args[-1].zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    pool.check()
+    assert torch.equal(args[-1], want)
+
+
+def test_caches_beyond_32_bit_offsets():
+    """Blocks that begin 2^31 elements into their tensors give what they give at the start."""
+    import torch
+    L, H, G, D, far, n = 1, 1, 4, 128, (1 << 24) + 77, 400
+    pool = _pool(L, H, G, D, "bf16")
+    near = [_randn(i, (n, D), "bf16") for i in (1, 2)]
+    big = [torch.empty((far + n, D), device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    pk, pv = _randn(3, (200, D), "bf16"), _randn(4, (200, D), "bf16")
+    q, kq, vq = _randn(5, (L, 1, G, D), "bf16"), _randn(6, (L, 1, H, D), "bf16"), _randn(7, (L, 1, H, D), "bf16")
+    got = []
+    for ck, cv, o in ((*[x.clone() for x in near], 0), (*big, far)):
+        if o:
+            ck[o:], cv[o:] = near[0], near[1]
+        w = torch.zeros(o + n, device="cuda")
+        kept = torch.empty(100, device="cuda", dtype=torch.int32)
+        out = torch.empty_like(q)
+        co = [o, o + n]
+        pool.shared_query_attention([0, 1], [0, 200], [200], pk, pv, co, [n - 10], [0, 1], q, kq, vq, ck, cv, out)
+        pool.key_weights(co, [n - 10], [0, 1], q, ck, w)
+        pool.evict(co, [n - 9], [100], w, ck, cv, kept, n_first=3, n_recent=5)
+        torch.cuda.synchronize()
+        pool.check()
+        got.append([x.clone() for x in (out, w[o:], kept, ck[o:], cv[o:])])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
