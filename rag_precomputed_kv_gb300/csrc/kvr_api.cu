@@ -1427,7 +1427,7 @@ kvr_status shared_simt(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, cudaStream_t
     if (e == cudaSuccess) {
         NvtxRange r("kvr.k_shared_simt");
         p->mark(4, s);
-        e = launch_shared_simt(sa, pl.tab, p->d.dtype, D, s);
+        e = launch_shared_simt(sa, pl.tab, p->d.dtype, D, p->n_sms, s);
         p->mark(5, s);
     }
     if (slot)
@@ -1560,7 +1560,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
     p->mark(2, s);
     {
         NvtxRange r("kvr.k_shared_prologue");
-        e = launch_shared_prologue(sa, pl.tab, p->q_rot, s);
+        e = launch_shared_prologue(sa, pl.tab, p->q_rot, !p->timed, s);
     }
     p->mark(3, s);
     p->mark(4, s);
@@ -1795,7 +1795,7 @@ extern "C" kvr_status kvr_key_weights(kvr_pool_t p, int32_t batch, const int64_t
         cudaError_t e;
         {
             NvtxRange r("kvr.k_key_weights");
-            e = tc ? launch_weights_tc(a, tab, &mk, p->n_sms, s) : launch_weights_simt(a, tab, p->d.dtype, D, s);
+            e = tc ? launch_weights_tc(a, tab, &mk, p->n_sms, s) : launch_weights_simt(a, tab, p->d.dtype, D, p->n_sms, s);
         }
         if (slot)
             cudaEventRecord(slot->done, s);

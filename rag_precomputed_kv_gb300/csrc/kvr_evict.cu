@@ -384,6 +384,7 @@ template <bool kSmem>
 __global__ void __launch_bounds__(kSelThreads, 1)
     k_evict_select(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
 {
+    pdl_wait_prerequisites();
     pdl_launch_dependents();   // (the move kernel waits for this grid)
     const int b = (int)(blockIdx.x / (unsigned)a.units);
     select_rows<kSelThreads, kSmem>(a, (a.reqs ? a.reqs : rt.reqs)[b], (int)(blockIdx.x % (unsigned)a.units));
@@ -526,6 +527,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas<T, D>)
     k_evict_unit(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
 {
+    pdl_wait_prerequisites();
     const int b = (int)(blockIdx.x / (unsigned)a.units), lh = (int)(blockIdx.x % (unsigned)a.units);
     const DevEvict rq = (a.reqs ? a.reqs : rt.reqs)[b];
     select_rows<kMoveThreads, true>(a, rq, lh);
@@ -554,8 +556,7 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
                               k_evict_unit<float, 64>);
         if (!k)
             return cudaErrorInvalidValue;
-        k<<<(unsigned)ctas, kMoveThreads, smem_rows(kMoveThreads) * 4, s>>>(a, rt);
-        return cudaGetLastError();
+        return launch_pdl(k, ctas, kMoveThreads, smem_rows(kMoveThreads) * 4, true, s, a, rt);
     }
     const int rows = smem_rows(kSelThreads);
     const bool smem = rows <= kSelSmemRows;
@@ -575,20 +576,8 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
                           k_evict_move<float, 64>);
     if (!k)
         return cudaErrorInvalidValue;
-    (smem ? k_evict_select<true> : k_evict_select<false>)<<<(unsigned)ctas, kSelThreads, smem ? rows * 4 : 0, s>>>(a, rt);
-    e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)move);
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, a, rt);
+    e = launch_pdl(smem ? k_evict_select<true> : k_evict_select<false>, ctas, kSelThreads, smem ? rows * 4 : 0, true, s, a, rt);
+    return e == cudaSuccess ? launch_pdl(k, move, kMoveThreads, 0, true, s, a, rt) : e;
 }
 
 // w_i / 2 pi in two floats (value and what it leaves), pairs 0 .. half - 1.

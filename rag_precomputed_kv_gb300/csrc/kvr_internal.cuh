@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "../../include/kvr.h"
 
 #ifdef __CUDACC__
@@ -244,6 +246,49 @@ struct QueryPrologueArgs {
     int32_t interleaved;        // RoPE pairs (x_2i, x_2i+1)
 };
 
+// A launch whose kernel may set up before the kernel before it is done (it waits
+// with pdl_wait_prerequisites); pdl false: a plain one.
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*k)(P...), int64_t grid, int block, int smem, bool pdl, cudaStream_t s, A &&...args)
+{
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, std::forward<A>(args)...);
+}
+
+// The same in clusters of c CTAs.
+template <typename... P, typename... A>
+inline cudaError_t launch_cluster(void (*k)(P...), int64_t grid, int block, int smem, int c, cudaStream_t s, A &&...args)
+{
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k, std::forward<A>(args)...);
+}
+
 // ---- query attention over a prefix shared by a group of requests ----
 // Per-request data (64 bytes): the request's own cache block, as DevReq, and
 // the prefix block of its group.
@@ -455,12 +500,12 @@ cudaError_t launch_wait_selftest(int *err, unsigned long long limit_ns, cudaStre
 // the next one launch that way
 cudaError_t launch_decode_attention(const AttnArgs &a, const ReqTable &rt, const void *tmap_k, const void *tmap_v,
                                     const DecodeIO &io, bool pdl, cudaStream_t s);
-cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s);
 // bf16, head_dim 128: rotation and append, then the prefix part and the own part
 // of a slice of the units.
-cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, cudaStream_t s);
+cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, bool pdl, cudaStream_t s);
 cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s);
-cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s);
 // bf16, head_dim 128: the tensor-core kernel; `tmap_k` points to the CUtensorMap
 // of the cache's keys ([rows, head_dim], 64 x 128 boxes).
 cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const void *tmap_k, int n_sms, cudaStream_t s);

@@ -6,25 +6,31 @@
 // the probabilities of the query attention (CoinRAG blog section 2.3,
 // KV_M(q; C_ctx)) summed over the queries: what each cached row was read for.
 //
-// The path for fp32 caches and head_dim 64.  One CTA per (request, unit); 16
-// query rows at a time, rotated into shared memory; a thread owns the keys
-// j = tid + 256 i and computes a key's 16 scores from one read of its row.
-// Two passes over the keys: the rows' maxima and sums, then the weights, so
-// nothing of the size (rows x keys) is stored, and every weight is summed by
-// one thread in row order.
+// The path for fp32 caches and head_dim 64.  A cluster of up to eight CTAs per
+// (request, unit) splits its keys; 32 query rows at a time, rotated into shared
+// memory; a thread owns a key and eight of the rows (with fewer rows there are
+// more keys at a time), and computes their scores from one read of the key's row.
+// Two passes over the keys: the rows' maxima and sums, which the CTAs exchange
+// through distributed shared memory, then the weights, so nothing of the size
+// (rows x keys) is stored; the threads of a key add their parts in row order.
 //
-// Bound by latency at the sizes it is for: 16 tokens x 2 heads on 219 keys, two
-// units: 26.7 us a call, two CTAs of two passes over three row blocks.
+// Bound by latency at the sizes it is for: FIG
+#include <cuda.h>
 #include <cuda_bf16.h>
 
-#include "kvr_internal.cuh"
+#include <algorithm>
+
+#include "kvr_tc_common.cuh"
 
 namespace kvr {
 
 namespace {
 
-constexpr int kWThreads = 256;
-constexpr int kWRows = 16;
+constexpr int kWThreads = 1024;
+constexpr int kWPer = 8;              // rows of a thread
+constexpr int kWRows = 4 * kWPer;     // rows at a time, by at most four threads of a key
+constexpr int kWMaxCluster = 8;
+__host__ __device__ constexpr int w_groups(int rows) { return rows > 2 * kWPer ? 4 : rows > kWPer ? 2 : 1; }
 
 template <typename T>
 __device__ __forceinline__ void unpack16(const uint4 &u, float *f);
@@ -54,32 +60,41 @@ __device__ __forceinline__ float w_to_f(__nv_bfloat16 x) { return __bfloat162flo
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kWThreads)
-    k_key_weights_simt(const __grid_constant__ WeightsArgs a, const __grid_constant__ ReqTable rt)
+    k_key_weights_simt(const __grid_constant__ WeightsArgs a, const __grid_constant__ ReqTable rt, const int n_cluster)
 {
     constexpr int E = 16 / (int)sizeof(T), H2 = D / 2;
+    pdl_wait_prerequisites();
     const DevReq *reqs = a.reqs ? a.reqs : rt.reqs;
     const int units = a.n_layers * a.n_kv_heads;
-    const DevReq rq = reqs[blockIdx.x / (unsigned)units];
-    const int lh = (int)(blockIdx.x % (unsigned)units);
+    const int rank = (int)(blockIdx.x % (unsigned)n_cluster), unit_i = (int)(blockIdx.x / (unsigned)n_cluster);
+    const DevReq rq = reqs[unit_i / units];
+    const int lh = unit_i % units;
     const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
     const int G = a.n_q_heads / a.n_kv_heads;
     const int m_rows = rq.q_len * G, n = rq.prefix + rq.q_len;
+    const int j_lo = (int)((int64_t)n * rank / n_cluster), j_hi = (int)((int64_t)n * (rank + 1) / n_cluster);
     const int64_t blk = rq.cache_row0 + (int64_t)lh * rq.cap;
     const T *kp = static_cast<const T *>(a.cache_k) + blk * D;
     float *w = a.weights + blk;
 
     __shared__ __align__(16) float sq[kWRows][D];
-    __shared__ float red_m[kWThreads / 32][kWRows], red_l[kWThreads / 32][kWRows], fin_m[kWRows], fin_i[kWRows];
+    __shared__ float red_m[kWThreads / 32][kWPer], red_l[kWThreads / 32][kWPer], fin_m[kWRows], fin_i[kWRows];
+    __shared__ float part[kWThreads];
+    __shared__ float2 peers[2][kWMaxCluster][kWRows];   // (max, sum) of the cluster's CTAs, by turns
 
     if (m_rows == 0) {   // a sum over no queries
         if (!a.accumulate)
-            for (int j = threadIdx.x; j < n; j += kWThreads)
+            for (int j = j_lo + threadIdx.x; j < j_hi; j += kWThreads)
                 w[j] = 0.f;
         return;
     }
-    for (int r0 = 0; r0 < m_rows; r0 += kWRows) {
-        const int nr = min(kWRows, m_rows - r0);
-        // the batch's query rows, rotated, times the scale (log2 units)
+    if (n_cluster > 1)
+        tc::cluster_sync();   // (the CTAs of a cluster have started: their shared memory may be written)
+    int turn = 0;
+    for (int r0 = 0; r0 < m_rows; r0 += kWRows, turn ^= 1) {
+        const int nr = min(kWRows, m_rows - r0), ng = w_groups(nr), keys = kWThreads / ng;
+        const int lane_key = threadIdx.x % keys, row0 = threadIdx.x / keys * kWPer;
+        // the batch's query rows, rotated
         for (int x = threadIdx.x; x < kWRows * H2; x += kWThreads) {
             const int r = x / H2, i = x - r * H2;
             float x0 = 0.f, x1 = 0.f;
@@ -99,36 +114,36 @@ __global__ void __launch_bounds__(kWThreads)
         __syncthreads();
         auto scores = [&](int j, float *s) {
 #pragma unroll
-            for (int r = 0; r < kWRows; ++r)
+            for (int r = 0; r < kWPer; ++r)
                 s[r] = 0.f;
-#pragma unroll 8
+#pragma unroll(16 / E)   // (more spill)
             for (int d = 0; d < D; d += E) {
                 float f[E];
                 unpack16<T>(*reinterpret_cast<const uint4 *>(kp + (int64_t)j * D + d), f);
 #pragma unroll
-                for (int r = 0; r < kWRows; ++r)
+                for (int r = 0; r < kWPer; ++r)
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        s[r] = fmaf(sq[r][d + e], f[e], s[r]);
+                        s[r] = fmaf(sq[row0 + r][d + e], f[e], s[r]);
             }
             // rows that do not see the key: their token lies before it
             const int r_min = (j - rq.prefix) * G - r0;
 #pragma unroll
-            for (int r = 0; r < kWRows; ++r)
-                s[r] = (r >= r_min && r < nr) ? s[r] * a.scale_log2 : -INFINITY;
+            for (int r = 0; r < kWPer; ++r)
+                s[r] = (row0 + r >= r_min && row0 + r < nr) ? s[r] * a.scale_log2 : -INFINITY;
         };
-        // a cache of at most one key a thread keeps its scores between the passes
-        const bool one = n <= kWThreads;
-        float s[kWRows], m[kWRows], ls[kWRows];
+        // at most one key a thread: its scores are kept between the passes
+        const bool one = j_hi - j_lo <= keys;
+        float s[kWPer], m[kWPer], ls[kWPer];
 #pragma unroll
-        for (int r = 0; r < kWRows; ++r) {
+        for (int r = 0; r < kWPer; ++r) {
             m[r] = -INFINITY;
             ls[r] = 0.f;
         }
-        for (int j = threadIdx.x; j < n; j += kWThreads) {
+        for (int j = j_lo + lane_key; j < j_hi; j += keys) {
             scores(j, s);
 #pragma unroll
-            for (int r = 0; r < kWRows; ++r) {
+            for (int r = 0; r < kWPer; ++r) {
                 if (s[r] != -INFINITY) {   // (NaN scores go through)
                     const float mn = fmaxf(m[r], s[r]);
                     ls[r] = ls[r] * exp2f(m[r] - mn) + exp2f(s[r] - mn);
@@ -137,7 +152,7 @@ __global__ void __launch_bounds__(kWThreads)
             }
         }
 #pragma unroll
-        for (int r = 0; r < kWRows; ++r) {
+        for (int r = 0; r < kWPer; ++r) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const float mo = __shfl_xor_sync(0xffffffffu, m[r], o), lo = __shfl_xor_sync(0xffffffffu, ls[r], o);
@@ -152,50 +167,81 @@ __global__ void __launch_bounds__(kWThreads)
             }
         }
         __syncthreads();
-        if (threadIdx.x < kWRows) {
-            const int r = threadIdx.x;
-            float mm = -INFINITY, ll = 0.f;
-            for (int x = 0; x < kWThreads / 32; ++x)
-                mm = fmaxf(mm, red_m[x][r]);
-            for (int x = 0; x < kWThreads / 32; ++x)
-                if (red_l[x][r] != 0.f)
-                    ll += red_l[x][r] * (red_m[x][r] == -INFINITY ? 1.f : exp2f(red_m[x][r] - mm));
-            fin_m[r] = mm == -INFINITY ? 0.f : mm;
-            fin_i[r] = 1.f / ll;
-            if (r < nr && !(ll > 0.f && ll < INFINITY))
+        // (max, sum) pairs added in order
+        auto join = [](float2 &x, float2 v) {
+            if (v.y == 0.f)   // no key
+                return;
+            const float mn = fmaxf(x.x, v.x);
+            x.y = (x.y == 0.f ? 0.f : x.y * (mn == -INFINITY ? 1.f : exp2f(x.x - mn))) +
+                  v.y * (mn == -INFINITY ? 1.f : exp2f(v.x - mn));
+            x.x = mn;
+        };
+        const int row = threadIdx.x;
+        float2 st = make_float2(-INFINITY, 0.f);
+        if (row < ng * kWPer) {
+            const int n_w = keys / 32, w0 = row / kWPer * n_w;
+            for (int x = w0; x < w0 + n_w; ++x)
+                join(st, make_float2(red_m[x][row % kWPer], red_l[x][row % kWPer]));
+        }
+        if (n_cluster > 1) {
+            if (row < kWRows)
+                for (int x = 0; x < n_cluster; ++x) {
+                    const uint32_t dst = tc::mapa_rank(tc::smem_u32(&peers[turn][rank][row]), (uint32_t)x);
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(st.x), "f"(st.y) : "memory");
+                }
+            // (by the time a CTA writes a turn's places again, all have passed the
+            // other turn's barrier, behind their reads of this one's)
+            tc::cluster_sync();
+            st = make_float2(-INFINITY, 0.f);
+            if (row < kWRows)
+                for (int x = 0; x < n_cluster; ++x)
+                    join(st, peers[turn][x][row]);
+        }
+        if (row < kWRows) {
+            fin_m[row] = st.x == -INFINITY ? 0.f : st.x;
+            fin_i[row] = 1.f / st.y;
+            if (row < nr && rank == 0 && !(st.y > 0.f && st.y < INFINITY))
                 atomicCAS(a.err, kDevOk, kDevBadInput);
         }
         __syncthreads();
-        for (int j = threadIdx.x; j < n; j += kWThreads) {
+        for (int j0 = j_lo; j0 < j_hi; j0 += keys) {
+            const int j = j0 + lane_key;
             float sum = 0.f;
-            if (!one)
-                scores(j, s);
+            if (j < j_hi) {
+                if (!one)
+                    scores(j, s);
 #pragma unroll
-            for (int r = 0; r < kWRows; ++r)
-                if (s[r] != -INFINITY)
-                    sum = fmaf(exp2f(s[r] - fin_m[r]), fin_i[r], sum);
-            w[j] = (r0 > 0 || a.accumulate ? w[j] : 0.f) + sum;
+                for (int r = 0; r < kWPer; ++r)
+                    if (s[r] != -INFINITY)
+                        sum = fmaf(exp2f(s[r] - fin_m[row0 + r]), fin_i[row0 + r], sum);
+            }
+            part[threadIdx.x] = sum;
+            __syncthreads();
+            if (row0 == 0 && j < j_hi) {
+                float all = part[lane_key];
+                for (int g = 1; g < ng; ++g)
+                    all += part[g * keys + lane_key];
+                w[j] = (r0 > 0 || a.accumulate ? w[j] : 0.f) + all;
+            }
+            __syncthreads();
         }
-        __syncthreads();   // the batch's queries and statistics are read
     }
 }
 
-cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, cudaStream_t s)
+cudaError_t launch_weights_simt(const WeightsArgs &a, const ReqTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s)
 {
-    const int64_t ctas = (int64_t)a.n_reqs * a.n_layers * a.n_kv_heads;
-    if (ctas > 0x7fffffff)
+    using Kernel = void (*)(const WeightsArgs, const ReqTable, const int);
+    const Kernel k = head_dim == 128 ? (dtype == KVR_DTYPE_BF16 ? k_key_weights_simt<__nv_bfloat16, 128> : k_key_weights_simt<float, 128>)
+                     : head_dim == 64 ? (dtype == KVR_DTYPE_BF16 ? k_key_weights_simt<__nv_bfloat16, 64> : k_key_weights_simt<float, 64>)
+                                      : nullptr;
+    if (!k)
         return cudaErrorInvalidValue;
-    if (dtype == KVR_DTYPE_BF16 && head_dim == 128)
-        k_key_weights_simt<__nv_bfloat16, 128><<<(unsigned)ctas, kWThreads, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_BF16 && head_dim == 64)
-        k_key_weights_simt<__nv_bfloat16, 64><<<(unsigned)ctas, kWThreads, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_FP32 && head_dim == 128)
-        k_key_weights_simt<float, 128><<<(unsigned)ctas, kWThreads, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_FP32 && head_dim == 64)
-        k_key_weights_simt<float, 64><<<(unsigned)ctas, kWThreads, 0, s>>>(a, rt);
-    else
-        return cudaErrorInvalidValue;
-    return cudaGetLastError();
+    const int64_t units = (int64_t)a.n_reqs * a.n_layers * a.n_kv_heads;
+    const int keys = kWThreads / w_groups((int)std::min<int64_t>(kWRows, (int64_t)a.max_q_len * (a.n_q_heads / a.n_kv_heads)));
+    int c = 1;   // keys of a unit to more CTAs while SMs are idle and a thread has more than one key
+    while (c < kWMaxCluster && units * c * 2 <= n_sms && a.max_rows > c * keys)
+        c *= 2;
+    return launch_cluster(k, units * c, kWThreads, 0, c, s, a, rt, c);
 }
 
 }  // namespace kvr

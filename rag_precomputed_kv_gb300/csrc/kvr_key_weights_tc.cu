@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     tc_fence_after();
     cluster_sync();   // the peers' barriers are initialised before any remote arrive
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(wt_smem + kWwOffMisc);
+    pdl_wait_prerequisites();
 
     const DevReq *reqs = a.reqs ? a.reqs : rt.reqs;
     const DevReq rq = reqs[unit_i / units];
@@ -935,25 +936,6 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     }
 }
 
-static cudaError_t launch_cluster(void (*k)(const CUtensorMap, const WeightsArgs, const ReqTable, const int), int64_t grid,
-                                  int smem, int c, cudaStream_t s, const CUtensorMap &tmk, const WeightsArgs &a,
-                                  const ReqTable &rt)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kWtThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)c;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, tmk, a, rt, c);
-}
-
 template <int NC>
 static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
 {
@@ -984,9 +966,7 @@ static cudaError_t launch_nq(const WeightsArgs &a, const ReqTable &rt, const CUt
     while (c < C::kMaxCluster &&
            ((tiles > c * C::kKept && tiles >= 20 * c) || (units * c <= n_sms && tiles >= 8 * c)))
         c *= 2;
-    if (units * c > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    return launch_cluster(k_key_weights_tc<NC>, units * c, C::kSmem, c, s, tmk, a, rt);
+    return launch_cluster(k_key_weights_tc<NC>, units * c, kWtThreads, C::kSmem, c, s, tmk, a, rt, c);
 }
 
 static cudaError_t launch_window(const WeightsArgs &a, const ReqTable &rt, const CUtensorMap &tmk, int n_sms, cudaStream_t s)
@@ -1009,9 +989,7 @@ static cudaError_t launch_window(const WeightsArgs &a, const ReqTable &rt, const
     int c = 1;   // split a unit's tiles while the grid leaves SMs idle (one CTA per SM then)
     while (c < kWwMaxCluster && units * c * 2 <= n_sms && tiles >= 4 * c)
         c *= 2;
-    if (units * c > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    return launch_cluster(k_key_weights_window, units * c, c > 1 ? kWwSmemCluster : kWwSmem, c, s, tmk, a, rt);
+    return launch_cluster(k_key_weights_window, units * c, kWtThreads, c > 1 ? kWwSmemCluster : kWwSmem, c, s, tmk, a, rt, c);
 }
 
 cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const void *tmap_k, int n_sms, cudaStream_t s)

@@ -8,12 +8,12 @@
 // were appended at own row S_b + t, and it attends to the P_g prefix rows and
 // to own rows 0..S_b + t.
 //
-// The path for fp32 caches and head_dim 64.  One CTA of four warps per (layer,
-// query token, query head), the keys split in four stretches; each lane holds
+// The path for fp32 caches and head_dim 64.  One CTA per (layer,
+// query token, query head), the keys split in as many stretches as it has warps; each lane holds
 // head_dim / 32 elements; eight keys at a time, so that their loads and
 // reductions over the warp overlap; online softmax in fp32, the warps' states
-// added in warp order.  (One warp per row, four keys at a time: 47 us a call
-// against 20.6 on three requests with 200 rows each, all of it latency.)
+// added in warp order.  Three requests with 200 rows each: 11.4 us a call,
+// all of it latency (four warps a row 18.6; one, four keys at a time, 47).
 #include <cuda_bf16.h>
 
 #include "kvr_internal.cuh"
@@ -33,10 +33,11 @@ __device__ __forceinline__ __nv_bfloat16 sh_from_f<__nv_bfloat16>(float x) { ret
 
 }  // namespace
 
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
+template <typename T, int D, int kShWarps>
+__global__ void __launch_bounds__(32 * kShWarps)
     k_shared_simt(const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt)
 {
+    pdl_wait_prerequisites();
     const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
     constexpr int PL = D / 32, KU = 8;
     const int64_t w = blockIdx.x;
@@ -133,15 +134,15 @@ __global__ void __launch_bounds__(128)
             m = mn;
         }
     };
-    // warp x: the x-th quarter of the prefix rows and of the own rows
+    // warp x: the x-th stretch of the prefix rows and of the own rows
     const int64_t pre = (rq.pre_row0 + (int64_t)lh * rq.pre_cap) * D, own = (rq.cache_row0 + (int64_t)lh * rq.cap) * D;
     const int n_own = rq.own + t + 1;
     if (rq.pre_len > 0)
         attend(static_cast<const T *>(a.prefix_k) + pre, static_cast<const T *>(a.prefix_v) + pre,
-               (int)((int64_t)rq.pre_len * warp / 4), (int)((int64_t)rq.pre_len * (warp + 1) / 4));
-    attend(static_cast<const T *>(a.cache_k) + own, static_cast<const T *>(a.cache_v) + own, (int)((int64_t)n_own * warp / 4),
-           (int)((int64_t)n_own * (warp + 1) / 4));
-    __shared__ float s_m[4], s_l[4], s_acc[4][D];
+               (int)((int64_t)rq.pre_len * warp / kShWarps), (int)((int64_t)rq.pre_len * (warp + 1) / kShWarps));
+    attend(static_cast<const T *>(a.cache_k) + own, static_cast<const T *>(a.cache_v) + own, (int)((int64_t)n_own * warp / kShWarps),
+           (int)((int64_t)n_own * (warp + 1) / kShWarps));
+    __shared__ float s_m[kShWarps], s_l[kShWarps], s_acc[kShWarps][D];
     if (lane == 0) {
         s_m[warp] = m;
         s_l[warp] = lsum;
@@ -152,11 +153,11 @@ __global__ void __launch_bounds__(128)
     __syncthreads();
     float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < kShWarps; ++x)
         M = fmaxf(M, s_l[x] == 0.f ? -INFINITY : s_m[x]);   // (a sum of 0: no key counts)
-    float wx[4];
+    float wx[kShWarps];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < kShWarps; ++x) {
         wx[x] = s_l[x] == 0.f ? 0.f : exp2f(s_m[x] - M);
         L += s_l[x] * wx[x];
     }
@@ -167,30 +168,29 @@ __global__ void __launch_bounds__(128)
     if ((int)threadIdx.x < D) {
         float o = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < kShWarps; ++x)
             o = fmaf(s_acc[x][threadIdx.x], wx[x], o);
         op[threadIdx.x] = sh_from_f<T>(o * inv);
     }
 }
 
-cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, cudaStream_t s)
+template <int kShWarps>
+static cudaError_t launch_w(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, int64_t blocks, cudaStream_t s)
 {
+    using Kernel = void (*)(const SharedArgs, const SharedTable);
+    const Kernel k = head_dim == 128 ? (dtype == KVR_DTYPE_BF16 ? k_shared_simt<__nv_bfloat16, 128, kShWarps> : k_shared_simt<float, 128, kShWarps>)
+                     : head_dim == 64 ? (dtype == KVR_DTYPE_BF16 ? k_shared_simt<__nv_bfloat16, 64, kShWarps> : k_shared_simt<float, 64, kShWarps>)
+                                      : nullptr;
+    return k ? launch_pdl(k, blocks, 32 * kShWarps, 0, true, s, a, rt) : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_shared_simt(const SharedArgs &a, const SharedTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s)
+{
+    // Sixteen warps a row where rows are few, four where they fill the SMs: 32 rows
+    // of 2,000 keys 37 us a call against 123; 1,280 rows of 750 keys 74 against 62.
     const int64_t blocks = (int64_t)a.n_layers * a.total_q * a.n_q_heads;
-    if (blocks == 0)
-        return cudaSuccess;
-    if (blocks > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    if (dtype == KVR_DTYPE_BF16 && head_dim == 128)
-        k_shared_simt<__nv_bfloat16, 128><<<(unsigned)blocks, 128, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_BF16 && head_dim == 64)
-        k_shared_simt<__nv_bfloat16, 64><<<(unsigned)blocks, 128, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_FP32 && head_dim == 128)
-        k_shared_simt<float, 128><<<(unsigned)blocks, 128, 0, s>>>(a, rt);
-    else if (dtype == KVR_DTYPE_FP32 && head_dim == 64)
-        k_shared_simt<float, 64><<<(unsigned)blocks, 128, 0, s>>>(a, rt);
-    else
-        return cudaErrorInvalidValue;
-    return cudaGetLastError();
+    return blocks <= 2 * (int64_t)n_sms ? launch_w<16>(a, rt, dtype, head_dim, blocks, s)
+                                        : launch_w<4>(a, rt, dtype, head_dim, blocks, s);
 }
 
 }  // namespace kvr

@@ -726,6 +726,7 @@ __global__ void __launch_bounds__(kPrThreads)
 {
     constexpr int D = kSpD, H2 = D / 2, E = 8;
     const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
+    pdl_wait_prerequisites();
     pdl_launch_dependents();   // the attention kernel sets up, and loads prefix tiles, meanwhile
     const DevShared rq = reqs[blockIdx.x / (unsigned)n_chunks];
     const int i = (int)(blockIdx.x % (unsigned)n_chunks) * kPrPairs + (int)(threadIdx.x >> 3), j = threadIdx.x & 7;
@@ -1414,28 +1415,10 @@ static cudaError_t shared_attrs()
     return cudaSuccess;
 }
 
-template <typename... P, typename... A>
-static cudaError_t launch_pdl(void (*k)(P...), int64_t grid, int block, int smem, bool pdl, cudaStream_t s, A &&...args)
-{
-    if (grid > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)block);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k, std::forward<A>(args)...);
-}
-
-cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, cudaStream_t s)
+cudaError_t launch_shared_prologue(const SharedArgs &a, const SharedTable &rt, void *q_rot, bool pdl, cudaStream_t s)
 {
     const int64_t n_chunks = ((int64_t)a.max_q_len * a.n_layers * a.n_kv_heads + kPrPairs - 1) / kPrPairs;
-    return launch_pdl(k_shared_prologue, a.n_reqs * n_chunks, kPrThreads, 0, false, s, a, rt,
+    return launch_pdl(k_shared_prologue, a.n_reqs * n_chunks, kPrThreads, 0, pdl, s, a, rt,
                       static_cast<__nv_bfloat16 *>(q_rot), (int)n_chunks);
 }
 
