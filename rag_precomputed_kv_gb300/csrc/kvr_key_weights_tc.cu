@@ -34,8 +34,8 @@
 // panels: 128 keys x 64 dims); warp 5 the MMAs.  All waits are bounded.
 //
 // Bound by the one read of K where it is long: 4 rows, 33,281 keys, 512 units:
-// 725 us, 6.0 TB/s.  A short unit is latency: 7 rows, 2,657 keys, 112 units: 23
-// us a call, 3.3 TB/s (setup and rotation 4 us, then two passes and an exchange
+// 725 us, 6.0 TB/s.  A short unit is latency: 7 rows, 2,657 keys, 112 units: 21
+// us a call, 3.7 TB/s (setup and rotation 4 us, then two passes and an exchange
 // that only the SM's other CTA overlaps).
 #include <cuda.h>
 #include <cuda_bf16.h>
