@@ -34,7 +34,7 @@
 // panels: 128 keys x 64 dims); warp 5 the MMAs.  All waits are bounded.
 //
 // Bound by the one read of K where it is long: 4 rows, 33,281 keys, 512 units:
-// 725 us, 6.0 TB/s.  A short unit is latency: 7 rows, 2,657 keys, 112 units: 21
+// 715 us, 6.1 TB/s.  A short unit is latency: 7 rows, 2,657 keys, 112 units: 21
 // us a call, 3.7 TB/s (setup and rotation 4 us, then two passes and an exchange
 // that only the SM's other CTA overlaps).
 #include <cuda.h>
@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    cluster_sync();   // the peers' barriers are initialised before any remote arrive
+    if (n_cluster > 1)
+        cluster_sync();   // the peers' barriers are initialised before any remote arrive
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(wt_smem + C::kOffMisc);
     pdl_wait_prerequisites();
 
@@ -585,7 +586,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // no CTA leaves while a peer may still write to its shared memory
+    if (n_cluster > 1)
+        cluster_sync();   // no CTA leaves while a peer may still write to its shared memory
     if (warp == 5) {
         tc_fence_after();
         tmem_dealloc(tmem, kWtTmemCols);
@@ -603,10 +605,10 @@ __global__ void __launch_bounds__(kWtThreads, 2)
 // memory is the same.  Two bf16 query terms: the weight of a key sums over all
 // the rows, which averages the 2^-17 that they leave.  Blocks of 128 rows; a
 // unit's tiles are split over a cluster only when there are too few units to
-// fill the SMs.  128 rows, 969 to 1,248 keys, 4,608 units: 491 us; the 2 x 2
+// fill the SMs.  128 rows, 969 to 1,248 keys, 4,608 units: 483 us; the 2 x 2
 // products are 340 us at the tensor rate, and a fifth of a CTA's time is setup,
 // rotation and exit, which only the SM's other CTA overlaps.  (32 rows cost it
-// 434 us on 16 requests of 1,300 keys, the kernel above 388; that one, with 128
+// 434 us on 16 requests of 1,300 keys, the kernel above 375; that one, with 128
 // rows' scores in TMEM, would keep one tile.)
 namespace {
 constexpr int kWwSlots = 3;
@@ -652,7 +654,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    cluster_sync();   // the peers' barriers are initialised before any remote arrive
+    if (n_cluster > 1)
+        cluster_sync();   // the peers' barriers are initialised before any remote arrive
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(wt_smem + kWwOffMisc);
     pdl_wait_prerequisites();
 
@@ -929,7 +932,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();   // no CTA leaves while a peer may still write to its shared memory
+    if (n_cluster > 1)
+        cluster_sync();   // no CTA leaves while a peer may still write to its shared memory
     if (warp == 5) {
         tc_fence_after();
         tmem_dealloc(tmem, kWtTmemCols);
