@@ -51,10 +51,11 @@
  *          more than 1 GiB only where one (layer, kv-head) needs it).
  *       5. A pool in pinned host memory: the first kvr_prefill on it creates
  *          an internal stream and its events (kept until unregister).
- *     kvr_pool_reserve makes 3 and 4 happen up front: afterwards, calls
- *     within the reserved sizes allocate nothing and wait only in the one
- *     case of 3 (8 calls with uploaded tables still queued).  kvr_pool_unregister
- *     synchronizes the handle's work before it frees.
+ *     kvr_pool_reserve makes 3 and 4 happen up front, but for the partial
+ *     results: afterwards, calls within the reserved sizes allocate nothing
+ *     and wait only in the one case of 3 (8 calls with uploaded tables still
+ *     queued).  kvr_pool_unregister synchronizes the handle's work before it
+ *     frees.
  *   - Every failure is a returned kvr_status; nothing aborts or traps.  Host
  *     validation runs before any launch, so an error status from validation
  *     means nothing was enqueued.  kvr_last_error() gives a one-line reason.
