@@ -1492,14 +1492,23 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
             pl.gr.push_back(d);
         }
     // One kernel for whole blocks, their own keys and the output, where blocks are
-    // well filled, enough for all SMs, and meet few own tiles: 16 requests of 64
-    // tokens x 7 heads on 2,592 shared rows, 112 units: 925 us against 1,070 with
-    // partial results and an own part; 8 of 70 x 4 on 400 rows, 288 units: 338
-    // against 443.  Blocks of few rows wait for each tile in turn: 8 groups of one
-    // 4-row request on 2,000 rows: 451 against 391.  Four own tiles a block: 238
-    // against 222 for 16 requests of 20 x 4 rows on 500.
-    const bool whole = all_active && sa.total_q * (int64_t)G >= 128 * pa.unit_blocks &&
-                       pa.unit_blocks * LH >= 4 * (int64_t)p->n_sms && own_tiles <= 3 * pa.unit_blocks;
+    // well filled, meet few own tiles, and come out even over the SMs: in units of
+    // a key tile (2 us for 256 rows), a round of whole blocks costs its tiles and
+    // 1.7 more, and partial results with an own part cost 1.15 a tile, 6.3 a block
+    // and 6 a call.  Measured on 2 x 8 requests of 64 tokens x 7 heads on 2,592
+    // rows, 26 blocks a unit, n units: n = 4: 54 us against 59; 8 (1.4 blocks an
+    // SM, two rounds): 101 against 96; 16: 151 against 184; 112: 928 against 1,070.
+    // 8 of 70 x 4 on 400 rows, 288 units: 338 against 443.  Blocks of few rows wait
+    // for each tile in turn: 8 groups of one 4-row request on 2,000 rows: 451
+    // against 391.  Four own tiles a block: 292 against 222 for 16 requests of 20 x
+    // 4 rows on 500.
+    bool whole = false;
+    if (all_active && pa.unit_blocks > 0 && sa.total_q * (int64_t)G >= 128 * pa.unit_blocks &&
+        own_tiles <= 3 * pa.unit_blocks) {
+        const double per_sm = (double)(pa.unit_blocks * LH) / p->n_sms;
+        const double nt = (double)pa.unit_pairs / pa.unit_blocks, own = (double)own_tiles / pa.unit_blocks;
+        whole = std::ceil(per_sm) * (nt + own + 1.7) <= per_sm * (1.15 * nt + 6.3) + 6.;
+    }
     // Consecutive blocks of a CTA: one where the prefix is long, so that a unit's
     // blocks run side by side and read it once from DRAM (21 tiles: 925 us with runs
     // of 1, 936 of 4, 959 with one run; 47: 1,052, 1,080, 1,112); some 32 tiles'
