@@ -162,6 +162,8 @@ SHARED = {
     "empty-groups": dict(groups=[0, 2, 0, 1], prefix=[9, 257, 0, 40], own=[3, 4, 5], q=[1, 2, 1]),
     "nothing-shared": dict(groups=[2], prefix=[0], own=[140, 3], q=[1, 9]),
     "queries": dict(groups=[2, 2], prefix=[200, 385], own=[0, 3, 130, 0], q=[7, 33, 1, 64]),
+    "short-queries": dict(groups=[12, 9], prefix=[700, 260], own=[7 * i % 40 for i in range(21)], q=[5 + i % 4 for i in range(21)]),
+    "short-queries-long-own": dict(groups=[5], prefix=[700], own=[260, 0, 391, 127, 128], q=[9, 5, 8, 12, 7]),
     "long-queries": dict(groups=[2], prefix=[150], own=[0, 40], q=[150, 271]),
     "many": dict(groups=[40, 30], prefix=[140, 64], own=[i % 7 for i in range(70)], q=[1 + (i % 5 == 0) for i in range(70)]),
 }
