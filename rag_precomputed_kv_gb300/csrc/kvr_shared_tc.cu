@@ -41,7 +41,7 @@
 // 256 units: k_shared_prefix 606 us, 7.2 TB/s of K and V; 256 rows on 8,256, 288
 // units: 213 us, 1.46 PFLOP/s, and 166 us for 64 requests' own rows (4.6 TB/s);
 // 6,328 rows on 2,592, 112 units: k_shared_whole 850 us, 1.12 PFLOP/s, behind 80
-// us of k_shared_prologue (6.7 TB/s).
+// us of k_shared_prologue (5.8 TB/s).
 //
 // Rounded to bf16 on the way, as the query prefill and the decode step do it: the
 // rotated queries (the cached keys are) and each probability, because both are
