@@ -1151,8 +1151,11 @@ __global__ void __launch_bounds__(kOwThreads, 3)
 // (across pieces), the warp runs S, softmax and P V of a step in registers, adds
 // the prefix's partial results at the end of a piece and writes its rows.  Seven
 // warps per SM, 32 KB of tiles each.  64 requests of 32 to 128 rows, 288 units:
-// 166 us, 4.6 TB/s of K and V (a CTA a piece took 291).  With at most 8 query rows the upper half of
-// the MMA row tile is left out: 391 us a call against 400.
+// 166 us, 4.6 TB/s of K and V (a CTA a piece took 291), bound by the chain of a
+// piece's steps: loads, three steps on average, partial results, output.  More
+// warps have fewer registers: twelve, 16 KB each, without the early loads of the
+// partial results, make the call 409 us instead of 394.  With at most 8 query
+// rows the upper half of the MMA row tile is left out: 391 us a call against 400.
 namespace {
 constexpr int kOdWarps = 7;
 constexpr int kOdThreads = 32 * kOdWarps;
