@@ -900,6 +900,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     corr = ex2(m_run - mxs);
                     m_run = mxs;
                 }
+                // (a warp's lanes rescale together: tcgen05 loads and stores under a
+                // lane's own condition may never return)
+                const bool rescale = __any_sync(0xffffffffu, corr != 1.f);
                 // a row that sees no key of the item's first tile sees none of
                 // the item (p = 0 throughout, m stays -inf)
                 const float nm = m_run == -INFINITY ? 0.f : -m_run;
@@ -926,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum = (a0 + a1) + (b0 + b1);
                 }
                 l_run = l_run * corr + sum;
-                if (corr != 1.f) {
+                if (rescale) {
                     // the commit that signalled S_x(j) covers PV_x(j-1): O_x is stable
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {

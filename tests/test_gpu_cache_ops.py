@@ -298,6 +298,32 @@ def test_shared_prefix_of_growing_scores(rows):
             _check_attention(to_np64(out[:, b, h * G:(h + 1) * G]), ref, A, qk, P + 1, "bf16", D)
 
 
+def test_query_attention_of_growing_scores():
+    """The same through the query prefill on a cache of its own."""
+    import torch
+    L, H, G, D, P, B, lq = 1, 2, 4, 128, 900, 2, 20
+    pool, R = _pool(L, H, G, D, "bf16"), 930
+    ck, cv = _randn(1, (B * H * R, D), "bf16"), _randn(2, (B * H * R, D), "bf16")
+    scale = torch.cat([torch.linspace(0.05, 6.0, P, device="cuda"), torch.zeros(R - P, device="cuda")])
+    ck = (ck.float().view(B * H, R, D) * scale[None, :, None]).to(ck.dtype).view(-1, D)
+    q, kq, vq = _randn(3, (L, B * lq, H * G, D), "bf16"), _randn(4, (L, B * lq, H, D), "bf16"), _randn(5, (L, B * lq, H, D), "bf16")
+    out = torch.empty_like(q)
+    pool.query_attention(np.arange(B + 1) * R, [P] * B, np.arange(B + 1) * lq, q, kq, vq, ck, cv, out)
+    torch.cuda.synchronize()
+    pool.check()
+    pos = P + np.arange(lq, dtype=np.float64)
+    for b in range(B):
+        sl = slice(b * lq, (b + 1) * lq)
+        qr = oracle.rope(to_np64(q[:, sl]), pos[None, :, None], THETA)
+        kr = oracle.rope(to_np64(kq[:, sl]), pos[None, :, None], THETA)
+        for h in range(H):
+            blk = slice((b * H + h) * R, (b * H + h) * R + P)
+            K = np.concatenate([to_np64(ck[blk]), kr[0, :, h]])
+            V = np.concatenate([to_np64(cv[blk]), to_np64(vq[0, sl, h])])
+            ref, A, qk, _ = _attention_ref(K, V, qr[0, :, h * G:(h + 1) * G], 0, P, D ** -0.5)
+            _check_attention(to_np64(out[0, sl, h * G:(h + 1) * G]), ref, A, qk, len(K), "bf16", D)
+
+
 def test_shared_prefix_flags_bad_input():
     import torch
     from rag_precomputed_kv_gb300 import kvr
