@@ -1864,6 +1864,7 @@ extern "C" kvr_status kvr_evict(kvr_pool_t p, int32_t batch, const int64_t *cach
             kept0 += (int64_t)k * LH;
             chunks += (int64_t)LH * std::max(1, (k + kEvictChunk - 1) / kEvictChunk);
             a.max_n = std::max(a.max_n, kv_len[b]);
+            a.max_keep = std::max(a.max_keep, k);
         }
         if (chunks > INT32_MAX)
             return fail(KVR_ERR_UNSUPPORTED, "too many rows to move in one call");

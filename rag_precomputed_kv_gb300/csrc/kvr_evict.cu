@@ -11,7 +11,7 @@
 // First a unit's kept rows: the threshold weight by a radix select over
 // order-preserving integer keys, then the rows at or above it in order, a chain
 // of short passes bound by their latency.  Then the kept rows are gathered: an
-// HBM stream like the stitch.  With many units of few rows both in one kernel
+// HBM stream like the stitch.  With many units or few rows both in one kernel
 // (k_evict_unit), else a kernel each (k_evict_select, k_evict_move).
 // Measured (bf16, head_dim 128): 4,608 units of 1,044 to 1,344 rows to 512: 370 us, of
 // which 362 are the rows' and weights' bytes at the copy rate; 256 units of
@@ -547,11 +547,14 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
         return dtype == KVR_DTYPE_BF16 ? (head_dim == 128 ? b128 : b64) : (head_dim == 128 ? f128 : f64);
     };
     auto smem_rows = [&](int threads) { return (a.max_n + 4 * threads - 1) / (4 * threads) * 4 * threads; };   // keys there
-    // One kernel where there are two units per SM or more and their keys leave
-    // room for three CTAs: 4,608 units of up to 1,344 rows 370 us a call, 531 in two
-    // kernels; 336 units of 2,656 rows 73 against 76; 224 units 52 against 53; 112
-    // units 39 against 29 (a CTA each cannot move them at full rate).
-    if (a.max_n <= 24 * 256 && ctas >= 2 * (int64_t)n_sms) {
+    // One kernel where units' keys leave room for three CTAs per SM and a CTA's rows
+    // do not last beyond the others': any with two units per SM, 1,024 rows with one,
+    // 256 with fewer.  4,608 units of up to 1,344 rows to 512: 370 us a call, 531 in
+    // two kernels; 224 units, 300 to 150: 8.9 against 16.0, 1,300 to 512: 26 against
+    // 31, 2,600 to 1,024: alike; 112 units, 300 to 150: 6.8 against 9.2, 650 to 450:
+    // 16.4 against 15.1, 2,600 to 1,024: 37 against 27.
+    const int most = ctas >= 2 * (int64_t)n_sms ? a.max_n : ctas >= n_sms ? 1024 : 256;
+    if (a.max_n <= 24 * 256 && a.max_keep <= most) {
         const Kernel k = pick(k_evict_unit<__nv_bfloat16, 128>, k_evict_unit<__nv_bfloat16, 64>, k_evict_unit<float, 128>,
                               k_evict_unit<float, 64>);
         if (!k)

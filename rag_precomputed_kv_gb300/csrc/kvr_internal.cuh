@@ -421,6 +421,7 @@ struct EvictArgs {
     int32_t n_reqs, units;      // units: L * H_kv
     int32_t n_first, n_recent;
     int32_t max_n;              // largest n of the batch
+    int32_t max_keep;           // most rows kept of a request
     int32_t n_chunks;           // (unit, row chunk) pieces of the batch (move kernel)
     int32_t interleaved;
     int32_t keep_rotation;      // keys are copied as they are

@@ -584,6 +584,7 @@ def test_evict_ties_and_special_weights(kind):
 
     for in_place in (False, True):
         _evict_case(1, 2, 128, "bf16", [1500, 200], [700, 60], 5, 7, weights=weights, in_place=in_place)
+        _evict_case(1, 2, 128, "bf16", [1500, 200], [170, 60], 5, 7, weights=weights, in_place=in_place)
 
 
 def test_evict_more_rows_than_shared_memory_holds():
