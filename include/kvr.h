@@ -347,6 +347,8 @@ KVR_API kvr_status kvr_prefill(kvr_pool_t pool, int32_t batch, const int32_t *sp
  * over the P_g prefix rows and own rows 0..S_b + t.  The result is that of
  * kvr_query_attention on a cache holding both one behind the other, up to
  * rounding order; the prefix is read once for the group, not once per request.
+ * (On the tensor cores rotated queries and probabilities are rounded to bf16,
+ * as there.)
  *
  *   group_offsets  host [n_groups+1], non-decreasing, group_offsets[0] = 0;
  *                  batch = group_offsets[n_groups]
@@ -368,8 +370,8 @@ KVR_API kvr_status kvr_prefill(kvr_pool_t pool, int32_t batch, const int32_t *sp
  * of that request's call (a weight of 0 times it is NaN), on other requests it
  * has no effect; neither has what a block holds behind its last row.
  * Errors: KVR_ERR_INVALID_ARG (also: the caches or `out` overlap the prefix or
- * each other),
- * KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA; kvr_check reports
+ * each other), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;
+ * kvr_check reports
  * KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for kvr_query_attention.
  */
 KVR_API kvr_status kvr_shared_query_attention(kvr_pool_t pool, int32_t n_groups, const int32_t *group_offsets,
