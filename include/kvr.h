@@ -371,8 +371,8 @@ KVR_API kvr_status kvr_prefill(kvr_pool_t pool, int32_t batch, const int32_t *sp
  * has no effect; neither has what a block holds behind its last row.
  * Errors: KVR_ERR_INVALID_ARG (also: the caches or `out` overlap the prefix or
  * each other), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;
- * kvr_check reports
- * KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for kvr_query_attention.
+ * kvr_check reports KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for
+ * kvr_query_attention.
  */
 KVR_API kvr_status kvr_shared_query_attention(kvr_pool_t pool, int32_t n_groups, const int32_t *group_offsets,
                                               const int64_t *prefix_offsets, const int32_t *prefix_len,
