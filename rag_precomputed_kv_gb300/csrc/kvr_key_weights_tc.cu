@@ -616,7 +616,7 @@ constexpr int kWwMaxCluster = 8;
 constexpr int kWwQTerm = 128 * kWtD * 2;
 constexpr int kWwOffRing = 2 * kWwQTerm;
 constexpr int kWwOffBar = kWwOffRing + kWwSlots * kWtPanel;
-constexpr int kWwNumBars = 2 * kWwSlots + 4 + 4;   // full, empty, s_full[2], s_free[2], q_full, q_empty, peers, drain
+constexpr int kWwNumBars = 2 * kWwSlots + 4 + 5;   // full, empty, s_full[2], s_free[2], q_full, q_empty, peers[2], drain
 constexpr int kWwOffMisc = kWwOffBar + 8 * kWwNumBars;
 constexpr int kWwOffFin = (kWwOffMisc + 12 + 15) & ~15;         // [128] -lse
 constexpr int kWwSmem = kWwOffFin + 128 * 4;
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     const uint32_t sbase = smem_u32(wt_smem);
     auto bar = [&](int i) { return sbase + kWwOffBar + 8u * (uint32_t)i; };
     constexpr int bFull = 0, bEmpty = kWwSlots, bSFull = 2 * kWwSlots, bSFree = bSFull + 2, bQFull = bSFree + 2,
-                  bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bQFull + 3;
+                  bQEmpty = bQFull + 1, bPeers = bQFull + 2, bDrain = bPeers + 2;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(wt_smem + kWwOffMisc + 4), *abort_seen = abort_flag + 1;
     float *s_fin = reinterpret_cast<float *>(wt_smem + kWwOffFin);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -643,7 +643,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWwNumBars; ++i)
-            mbar_init(bar(i), (i >= bSFree && i < bSFree + 2) || i == bQFull ? 128u : i == bPeers ? (uint32_t)(n_cluster * 128) : 1u);
+            mbar_init(bar(i), (i >= bSFree && i < bSFree + 2) || i == bQFull  ? 128u
+                              : i >= bPeers && i < bPeers + 2 ? (uint32_t)(n_cluster * 128)
+                                                              : 1u);
         *abort_flag = *abort_seen = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -757,16 +759,23 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 give_up(a.err, abort_flag);
             float M = m, L = lsum;
             if (n_cluster > 1) {
-                const uint32_t peer = sbase + kWwOffPeer + (uint32_t)((rb & 1) * kWwMaxCluster * 128 * 8);
+                // Row blocks take two barriers and two sets of places by turns.  A phase that
+                // is complete here says that every thread has arrived here, not at the other
+                // CTAs: with one barrier, this CTA's arrivals for block rb + 1 could count at a
+                // CTA that a slower thread's arrival for rb has yet to reach.  With two, the
+                // arrivals for rb + 2 come after a wait for rb + 1, which every thread joins
+                // only after its arrivals for rb.
+                const int turn = rb & 1;
+                const uint32_t peer = sbase + kWwOffPeer + (uint32_t)(turn * kWwMaxCluster * 128 * 8);
                 for (int x = 0; x < n_cluster; ++x) {
                     const uint32_t dst = mapa_rank(peer + (uint32_t)((rank * 128 + r) * 8), (uint32_t)x);
                     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(m), "f"(lsum) : "memory");
                     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                                     mapa_rank(bar(bPeers), (uint32_t)x))
+                                     mapa_rank(bar(bPeers + turn), (uint32_t)x))
                                  : "memory");
                 }
-                if (wait_peers(bar(bPeers), (uint32_t)rb & 1, abort_flag)) {
-                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + kWwOffPeer) + (rb & 1) * kWwMaxCluster * 128 + r;
+                if (wait_peers(bar(bPeers + turn), (uint32_t)(rb >> 1) & 1, abort_flag)) {
+                    const float2 *pv = reinterpret_cast<const float2 *>(wt_smem + kWwOffPeer) + turn * kWwMaxCluster * 128 + r;
                     M = kWtUnset;
                     L = 0.f;
                     for (int x = 0; x < n_cluster; ++x)

@@ -160,3 +160,43 @@ def test_python_binding_checks_lengths_and_types():
             p.evict([0, 8], [4], [2], x, x, x, x.int(), dst_v=x, stream=0)
     finally:
         p.close()
+
+
+def _exchange_goes_wrong(ctas, blocks, bars):
+    """Whether some order of steps lets a CTA read a pair that has not come.
+    One thread a CTA; per row block it writes its pair to every CTA and arrives
+    at that CTA's barrier, in turn, then waits for its own barrier's phase and
+    reads all pairs.  Row block b uses barrier b % bars and its phase b // bars,
+    of which a wait sees the parity alone, and the places b % 2."""
+    state = (((0, 0),) * ctas, (((0, ctas),) * bars,) * ctas, (((-1,) * ctas,) * 2,) * ctas)
+    seen, todo = {state}, [state]
+    put = lambda t, i, x: t[:i] + (x,) + t[i + 1:]
+    while todo:
+        threads, barriers, places = todo.pop()
+        for t, (b, x) in enumerate(threads):
+            if b == blocks:
+                continue
+            k = b % bars
+            if x < ctas:    # write to CTA x, arrive there
+                done, left = barriers[x][k]
+                done, left = (done + 1, ctas) if left == 1 else (done, left - 1)
+                new = (put(threads, t, (b, x + 1)), put(barriers, x, put(barriers[x], k, (done, left))),
+                       put(places, x, put(places[x], b % 2, put(places[x][b % 2], t, b))))
+            else:
+                if barriers[t][k][0] % 2 == (b // bars) % 2:
+                    continue    # the phase is not complete
+                if any(p != b for p in places[t][b % 2]):
+                    return True
+                new = (put(threads, t, (b + 1, 0)), barriers, places)
+            if new not in seen:
+                seen.add(new)
+                todo.append(new)
+    return False
+
+
+def test_exchange_of_row_sums_between_ctas():
+    """The window kernel's exchange: one barrier for all row blocks lets a CTA go
+    on without a pair as soon as three CTAs take part; two by turns do not."""
+    assert _exchange_goes_wrong(3, 2, 1)
+    for ctas, blocks in ((2, 5), (3, 4), (4, 3)):
+        assert not _exchange_goes_wrong(ctas, blocks, 2)
