@@ -62,7 +62,10 @@
 // Every mbarrier wait is bounded (2 s of %globaltimer); on expiry the CTA
 // records KVR_ERR_TIMEOUT in the pool's error word, all roles leave their
 // loops, in-flight copies and MMAs are drained (again bounded) and TMEM is
-// freed before the CTA exits.
+// freed before the CTA exits.  A wait may run out for one lane and not for
+// another, and tcgen05 loads and stores, votes and shuffles wait for all 32: a
+// warp's lanes go on together and leave where they vote, at the rescale of a key
+// tile and at the next item's geometry (a vote at each wait: 1.5 % slower).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -210,14 +213,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-// Generic-proxy writes to shared memory become visible to the async proxy
-// (the tensor core reads its operands through it).
 // Fetch a tensor map (a kernel parameter) ahead of its first copy.
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Generic-proxy writes to shared memory become visible to the async proxy
+// (the tensor core reads its operands through it).
 __device__ __forceinline__ void fence_proxy_async_smem()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -774,9 +777,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // geometry of this CTA's k-th item: slot k & 1 of the shared-memory ring
     auto geo_slot = [&](int k) { return reinterpret_cast<Geo *>(smem + kOffGeo + (k & 1) * kGeoBytes); };
     // consumer warps: wait for item k's geometry (then read its fields and
-    // release the slot with geo_done)
-    auto geo_wait = [&](int k) -> const Geo * {
-        if (!mbar_wait(bar(kBarGeoFull + (k & 1)), (uint32_t)(k >> 1) & 1u, abort_flag))
+    // release the slot with geo_done); `ok`: no wait of this lane has run out.
+    // All lanes get the slot, or none
+    auto geo_wait = [&](int k, bool ok) -> const Geo * {
+        if (!__all_sync(0xffffffffu, ok && mbar_wait(bar(kBarGeoFull + (k & 1)), (uint32_t)(k >> 1) & 1u, abort_flag)))
             return nullptr;
         return geo_slot(k);
     };
@@ -843,8 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int G = a.n_q_heads / a.n_kv_heads;
         int s_cnt = 0, o_cnt = 0, gk = 0;
         bool ok = true;
-        for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x, ++gk) {
-            const Geo *gp = geo_wait(gk);
+        for (int it = blockIdx.x; it < n_items; it += gridDim.x, ++gk) {
+            const Geo *gp = geo_wait(gk, ok);
             if (!gp) {
                 ok = false;
                 break;
@@ -864,10 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = gp->prefix + t;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = jb; j < nx; ++j) {
-                if (!mbar_wait(bar(kBarSFull + x), s_cnt & 1, abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait(bar(kBarSFull + x), s_cnt & 1, abort_flag);   // (voted on at the rescale)
                 ++s_cnt;
                 tc_fence_after();
                 float s[kTileN];
@@ -900,9 +901,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     corr = ex2(m_run - mxs);
                     m_run = mxs;
                 }
-                // (a warp's lanes rescale together: tcgen05 loads and stores under a
-                // lane's own condition may never return)
-                const bool rescale = __any_sync(0xffffffffu, corr != 1.f);
+                // (a warp's lanes rescale, and leave, together: tcgen05 loads and stores
+                // under a lane's own condition may never return)
+                const bool rescale = __any_sync(0xffffffffu, corr != 1.f || !ok);
                 // a row that sees no key of the item's first tile sees none of
                 // the item (p = 0 throughout, m stays -inf)
                 const float nm = m_run == -INFINITY ? 0.f : -m_run;
@@ -930,6 +931,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 l_run = l_run * corr + sum;
                 if (rescale) {
+                    if (__any_sync(0xffffffffu, !ok)) {
+                        tmem_wait_st();
+                        ok = false;
+                        break;
+                    }
                     // the commit that signalled S_x(j) covers PV_x(j-1): O_x is stable
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -953,10 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             geo_done(gk);
             // epilogue: O / l -> bf16 -> out[l][q_off + t][h*G + g][:], read from
             // TMEM 64 columns at a time (a whole row of O in registers spills)
-            if (!mbar_wait(bar(kBarOFull + x), o_cnt & 1, abort_flag)) {
-                ok = false;
-                break;
-            }
+            ok = mbar_wait(bar(kBarOFull + x), o_cnt & 1, abort_flag);   // (voted on at the next item)
             ++o_cnt;
             tc_fence_after();
             const uint32_t o_tm = lane_base + col_o(x);
@@ -972,10 +975,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t peer_o = sbase + kOffPeerO, peer_ml = sbase + kOffPeerML;
             if (split2 && !merger) {
                 // the partner's ring and Q tiles are free once its MMAs are done
-                if (!mbar_wait_cluster(bar(kBarPeerFree), 0, abort_flag)) {
-                    ok = false;
+                ok = __all_sync(0xffffffffu, ok && mbar_wait_cluster(bar(kBarPeerFree), 0, abort_flag));
+                if (!ok)
                     break;
-                }
                 const uint32_t peer = (uint32_t)x;
                 float amax = 0.f;
 #pragma unroll
@@ -1021,10 +1023,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float w0 = 1.f, w1 = 0.f, p_scale = 0.f;
             if (merger) {
-                if (!mbar_wait_cluster(bar(kBarPeerData), 0, abort_flag)) {
-                    ok = false;
+                ok = __all_sync(0xffffffffu, ok && mbar_wait_cluster(bar(kBarPeerData), 0, abort_flag));
+                if (!ok)
                     break;
-                }
                 const float mp = ld_shared_f32(peer_ml + (uint32_t)r * 4);
                 const float lp = ld_shared_f32(peer_ml + (uint32_t)(kTileM + r) * 4);
                 p_scale = ld_shared_f32(peer_ml + (uint32_t)(2 * kTileM + r) * 4);
@@ -1475,8 +1476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return wait_kv(k);
             };
             int gk = 0;
-            for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x, ++gk) {
-                const Geo *gp = geo_wait(gk);
+            // (within an item lanes need not keep together: one that lost a wait goes
+            // to the next item's vote)
+            for (int it = blockIdx.x; it < n_items; it += gridDim.x, ++gk) {
+                const Geo *gp = geo_wait(gk, ok);
                 if (!gp) {
                     ok = false;
                     break;
@@ -1495,7 +1498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 peer_wait = half >= 0 && (n_tiles + 1) / 2 < (half ? nt1 : nt0) ? half : -1;
                 if (!mbar_wait(bar(kBarQFull), nq & 1, abort_flag) || !wait_kv(tt)) {
                     ok = false;
-                    break;
+                    continue;
                 }
                 ++nq;
                 // a tile's first S of the item waits until the epilogue of its
@@ -1516,7 +1519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         issue_s(x, tt % kSlots);
                     }
                 if (!ok)
-                    break;
+                    continue;
                 if (je - jb == 1)
                     umma_commit(lead, bar(kBarQEmpty));
                 umma_commit(lead, bar(kBarEmpty + tt % kSlots));
@@ -1620,12 +1623,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(kBarGathered + prev_b));
             prev_b = -1;
         };
-        for (int it = blockIdx.x; it < n_items && ok; it += gridDim.x, ++gk) {
+        for (int it = blockIdx.x; it < n_items; it += gridDim.x, ++gk) {
             int jb, je, prefix, n_valid, cap, l, h, s0, s_end;
             bool tma_v;
             int64_t kv_row0;
             {
-                const Geo *gp = geo_wait(gk);
+                const Geo *gp = geo_wait(gk, ok);
                 if (!gp) {
                     ok = false;
                     break;
@@ -1660,7 +1663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cur = lo;
                 }
             }
-            for (int j = jb; j < je && ok; ++j, tt += 2) {
+            for (int j = jb; j < je; ++j, tt += 2) {
                 if (!v_gathered(j, prefix, cap, tma_v))
                     continue;
                 // the source of this lane's two rows (0: zeros)
@@ -1692,8 +1695,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (prev_b >= 0 && j != prev_j + 1)
                     release(1);
                 if (!mbar_wait(bar(kBarGatherJob + b), nj[b] & 1, abort_flag)) {
-                    ok = false;
-                    break;
+                    ok = false;   // (voted on at the next item; no later wait lasts)
+                    *abort_flag = 1;
                 }
                 ++nj[b];
                 const uint32_t vb = sbase + kOffKV + sv * kTileBytes + chunk_off;

@@ -1,0 +1,47 @@
+"""Waits of the kernels that run warp-wide instructions, read in their sources.
+
+A bounded wait may give up, and its lanes may do so one by one.  Code of a whole
+warp that goes on to votes, shuffles or tcgen05 loads needs one answer for all
+lanes, or the lanes that go on wait for the others for good: no run shows that
+unless a wait runs out, so it is read off the source.
+"""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "rag_precomputed_kv_gb300", "csrc")
+ROLE = re.compile(r"^    (?:\} else )?if \((?:kV && )?warp (==|<|>=) (\d+)\) \{|^    \} else \{", re.M)
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def _roles(text):
+    """(condition, text) of each warp role of the file's kernels."""
+    m = list(ROLE.finditer(text))
+    return [((a.group(1), a.group(2)), text[a.end():b.start() if b else len(text)]) for a, b in zip(m, m[1:] + [None])]
+
+
+PLAIN = re.compile(r"\bmbar_wait(?:_cluster)?\(")
+
+
+def test_attention_roles_leave_together():
+    """k_attention_tc: a lane that lost a wait takes part in its warp's votes and
+    leaves at one of them with the others, never before."""
+    roles = dict(reversed(_roles(_source("kvr_attention_tc.cu"))))   # (the first of each condition)
+    for cond in (("<", "8"), ("==", "9"), (">=", "10")):
+        text = roles[cond]
+        item = text[text.index("for (int it = blockIdx.x; it < n_items; it"):]
+        # every item starts with a vote that knows of the waits before it
+        assert re.match(r"for \([^)]*\) \{\s*(int [^;]*;\s*bool [^;]*;\s*int64_t [^;]*;\s*\{\s*)?"
+                        r"const Geo \*gp = geo_wait\(gk, ok\);\s*if \(!gp\)", item), item[:300]
+        if cond != ("==", "9"):   # (no lane of the MMA warp needs another within an item)
+            for m in PLAIN.finditer(item):
+                line = item[item.rindex("\n", 0, m.start()):item.index("\n", m.end())]
+                after = item[item.index("\n", m.end()):][:120]
+                assert "__all_sync(" in line or "ok = mbar_wait(" in line or re.match(r"\s*ok = false;\s*\*abort_flag = 1;\s*\}", after), line
+    softmax = roles["<", "8"]
+    assert "__any_sync(0xffffffffu, corr != 1.f || !ok)" in softmax and "if (__any_sync(0xffffffffu, !ok))" in softmax
+    body = roles["==", "9"][roles["==", "9"].index("geo_done(gk)") + 12:]
+    assert not re.search(r"(?<!mbar)_sync\(|__syncwarp|tmem_(ld|st)", body)
