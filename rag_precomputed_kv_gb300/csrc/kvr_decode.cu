@@ -218,10 +218,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     bool ok = true;
     for (int j = 0; j < n_t; ++j) {
         const int s = j % kDecStages;
-        if (!dec_wait(full(s), (uint32_t)((j / kDecStages) & 1))) {
-            ok = false;
+        // (one answer for the warp: what follows needs all its lanes)
+        if (!(ok = __all_sync(0xffffffffu, ok && dec_wait(full(s), (uint32_t)((j / kDecStages) & 1)))))
             break;
-        }
         const uint32_t kt = sbase + (uint32_t)(s * kDecStageBytes), vt = kt + kDecTileBytes;
         const int key0 = 32 * warp;   // this warp's 32 keys of the tile
         if (j == n_t - 1) {
@@ -329,12 +328,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // this stage is consumed; thread 0 refills it kDecStages tiles ahead
         dec_mbar_arrive(empty(s));
         if (threadIdx.x == 0 && j + kDecStages < n_t) {
-            if (!dec_wait(empty(s), (uint32_t)((j / kDecStages) & 1))) {
-                ok = false;
-                break;
+            ok = dec_wait(empty(s), (uint32_t)((j / kDecStages) & 1));   // (voted on at the next tile)
+            if (ok) {
+                issue(j + kDecStages);
+                ++n_issued;
             }
-            issue(j + kDecStages);
-            ++n_issued;
         }
     }
     if (!ok)

@@ -45,3 +45,13 @@ def test_attention_roles_leave_together():
     assert "__any_sync(0xffffffffu, corr != 1.f || !ok)" in softmax and "if (__any_sync(0xffffffffu, !ok))" in softmax
     body = roles["==", "9"][roles["==", "9"].index("geo_done(gk)") + 12:]
     assert not re.search(r"(?<!mbar)_sync\(|__syncwarp|tmem_(ld|st)", body)
+
+
+def test_decode_warps_wait_with_one_answer():
+    """k_decode_attention: a tile's wait is voted on, thread 0's wait for a free
+    stage with the next tile's."""
+    text = _source("kvr_decode.cu")
+    loop = text[text.index("for (int j = 0; j < n_t; ++j) {"):text.index("if (!ok)\n        *cta_err = 1;")]
+    waits = [loop[loop.rindex("\n", 0, m.start()):m.end()] for m in re.finditer(r"\bdec_wait\(", loop)]
+    assert len(waits) == 2 and "__all_sync(0xffffffffu, ok && " in waits[0] and "ok = dec_wait(" in waits[1]
+    assert loop.count("break;") == 1
