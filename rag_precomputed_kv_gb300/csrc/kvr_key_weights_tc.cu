@@ -485,7 +485,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
                 }
             }
             softmax_sync();
-            if (*abort_flag)
+            // (one answer for the warp's tcgen05 loads: a peer or another role may set the
+            // flag between two lanes' reads)
+            if (__any_sync(0xffffffffu, *abort_flag != 0))
                 ok = false;
             // ---- pass 2: the weights of this thread's keys ----
             // (the weights to add to are read eight tiles ahead)

@@ -55,3 +55,13 @@ def test_decode_warps_wait_with_one_answer():
     waits = [loop[loop.rindex("\n", 0, m.start()):m.end()] for m in re.finditer(r"\bdec_wait\(", loop)]
     assert len(waits) == 2 and "__all_sync(0xffffffffu, ok && " in waits[0] and "ok = dec_wait(" in waits[1]
     assert loop.count("break;") == 1
+
+
+def test_key_weight_warps_read_the_abort_flag_with_one_answer():
+    """Both tensor-core kernels: lanes that go on to tcgen05 loads agree on whether
+    the CTA gave up (a vote, or one thread's reading of it)."""
+    text = _source("kvr_key_weights_tc.cu")
+    reads = [m.group(0).strip() for m in re.finditer(r"[^\n]*\*abort_(?:flag|seen)\b[^\n]*", text[text.index("template <int NC>\n__global__"):])]
+    reads = [r for r in reads if not r.startswith("volatile int")]
+    assert reads == ["*abort_flag = 0;", "if (__any_sync(0xffffffffu, *abort_flag != 0))", "*abort_flag = *abort_seen = 0;",
+                     "*abort_seen = *abort_flag;", "if (*abort_seen) {"]
