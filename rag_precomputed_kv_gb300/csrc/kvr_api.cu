@@ -111,7 +111,8 @@ struct kvr_pool {
     int cc = 0;               // compute capability, major * 10 + minor
     float2 *rope = nullptr;   // RoPE tables, then the pairs' frequencies in turns
     float2 *rope_turns = nullptr;
-    int *err = nullptr;       // device error word
+    int *err = nullptr;       // device error word, then the shared-prefix calls' relay words
+    uint32_t shared_calls = 0;   // shared-prefix calls on the tensor cores so far
     Slot slots[kSlots];
     int next = 0;
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -298,8 +299,8 @@ static kvr_status ensure_device(kvr_pool *p)
     cudaDeviceGetAttribute(&p->n_sms, cudaDevAttrMultiProcessorCount, p->device);
     const size_t tab = sizeof(float2) * 2 * kRopeSplit * (p->d.head_dim / 2);
     if ((e = cudaMalloc(&p->rope, tab + sizeof(float2) * (p->d.head_dim / 2))) != cudaSuccess ||
-        (e = cudaMalloc(&p->err, sizeof(int))) != cudaSuccess ||
-        (e = cudaMemset(p->err, 0, sizeof(int))) != cudaSuccess ||
+        (e = cudaMalloc(&p->err, 3 * sizeof(int))) != cudaSuccess ||
+        (e = cudaMemset(p->err, 0, 3 * sizeof(int))) != cudaSuccess ||
         (e = launch_rope_tables(p->rope, p->d.head_dim, p->d.rope_theta, 0)) != cudaSuccess ||
         (e = launch_rope_turns(p->rope + 2 * kRopeSplit * (p->d.head_dim / 2), p->d.head_dim, p->d.rope_theta, 0)) !=
             cudaSuccess ||
@@ -1443,6 +1444,8 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
 {
     const int L = sa.n_layers, H = sa.n_kv_heads, Hq = sa.n_q_heads, D = p->d.head_dim, LH = L * H, G = Hq / H;
     SharedPrefixArgs pa{};
+    sa.relay = pa.relay = reinterpret_cast<uint32_t *>(p->err + 1);
+    sa.call = pa.call = ++p->shared_calls;
     pa.group = G;
     pa.total_q = sa.total_q;
     pa.scale_log2 = sa.scale_log2;

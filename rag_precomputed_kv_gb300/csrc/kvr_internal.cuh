@@ -321,6 +321,10 @@ struct SharedArgs {
     float scale_log2;
     int32_t interleaved;
     int *err;
+    // tensor-core path: relay[0] holds `call` once a CTA of the prologue has waited for the
+    // work before the call, relay[1] once one of the prefix part has waited for the prologue
+    uint32_t *relay;
+    uint32_t call;              // number of the pool's call, from 1 on
 };
 
 // Per-group data (64 bytes) of the tensor-core path: the packed query rows of
@@ -361,6 +365,8 @@ struct SharedPrefixArgs {
     const void *q_rot;          // [L][Hkv][T][G][D], rotated
     float scale_log2;
     int *err;
+    uint32_t *relay;            // as in SharedArgs
+    uint32_t call;
 };
 struct SharedTcArgs {
     const SharedArgs *base;

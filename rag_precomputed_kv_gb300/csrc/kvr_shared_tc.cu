@@ -291,6 +291,8 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSpRegsSoftmax));
         pdl_wait_prerequisites();   // (the partial results' scratch may still be read by the call before)
         // the own part may be set up now, and load what the prologue, now done, wrote
+        if (!kWhole && blockIdx.x == 0 && threadIdx.x == 0)
+            relay_store(a.relay + 1, a.call);
         pdl_launch_dependents();
         const int x = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -458,9 +460,12 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
     } else if (warp == 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSpRegsOther));
         if (lane == 0) {
-            // the prefix is not written by the kernel before (the prologue), so its
-            // tiles are loaded ahead of the wait for it; the packed queries are not
-            bool ok = true, waited = false;
+            // The kernel before (the prologue) does not write the prefix: once it passed on
+            // that what came before the call is done, the first tiles, and the tables, are
+            // read ahead of the wait for it; the packed queries are not.
+            bool ok = true, waited = !relay_seen(a.relay, a.call);
+            if (waited)
+                pdl_wait_prerequisites();
             int tt = 0, nq = 0;
             for (int64_t w = w_begin; w < w_end && ok;) {
                 OwnTiles ot;
@@ -521,6 +526,7 @@ __device__ __forceinline__ void prefix_part(const CUtensorMap &tmq, const CUtens
         }
     } else if (warp == 9) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSpRegsOther));
+        pdl_wait_prerequisites();   // (it reads the tables)
         const uint32_t lead = elect_one();
         int tt = 0, nq = 0, p_cnt[2] = {0, 0}, oe_cnt[2] = {0, 0};
         bool o_used[2] = {false, false}, ok = true;
@@ -727,6 +733,8 @@ __global__ void __launch_bounds__(kPrThreads)
     constexpr int D = kSpD, H2 = D / 2, E = 8;
     const DevShared *reqs = a.reqs ? a.reqs : rt.reqs;
     pdl_wait_prerequisites();
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        relay_store(a.relay, a.call);
     pdl_launch_dependents();   // the attention kernel sets up, and loads prefix tiles, meanwhile
     const DevShared rq = reqs[blockIdx.x / (unsigned)n_chunks];
     const int i = (int)(blockIdx.x % (unsigned)n_chunks) * kPrPairs + (int)(threadIdx.x >> 3), j = threadIdx.x & 7;
@@ -1200,9 +1208,13 @@ __global__ void __launch_bounds__(kOdThreads, 1)
         prefetch_tmap(&tmv);
     }
     __syncwarp();
-    // Behind a prefix part, which let this kernel start only after the prologue
-    // was done, only the partial results have to be waited for.
+    // Behind a prefix part that passed on that the prologue is done, only the partial
+    // results have to be waited for.
     bool waited = pa.total == 0;
+    if (!waited) {
+        waited = lane == 0 && !relay_seen(pa.relay + 1, pa.call);
+        waited = __shfl_sync(0xffffffffu, waited, 0);
+    }
     if (waited)
         pdl_wait_prerequisites();
 

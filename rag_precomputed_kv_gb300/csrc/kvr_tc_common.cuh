@@ -108,6 +108,21 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// A grid that waited for the ones before it passes on that it did: `word` gets the call's
+// number.  A later grid that reads the number may read what those wrote (release and
+// acquire add up what each grid has seen), through the async proxy too.
+__device__ __forceinline__ void relay_store(uint32_t *word, uint32_t call)
+{
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(word), "r"(call) : "memory");
+}
+__device__ __forceinline__ bool relay_seen(const uint32_t *word, uint32_t call)
+{
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    return v == call;
+}
+
 // Generic-proxy writes to shared memory become visible to the async proxy.
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

@@ -65,3 +65,29 @@ def test_key_weight_warps_read_the_abort_flag_with_one_answer():
     reads = [r for r in reads if not r.startswith("volatile int")]
     assert reads == ["*abort_flag = 0;", "if (__any_sync(0xffffffffu, *abort_flag != 0))", "*abort_flag = *abort_seen = 0;",
                      "*abort_seen = *abort_flag;", "if (*abort_seen) {"]
+
+
+def test_shared_prefix_kernels_read_what_they_may():
+    """A programmatic launch promises what earlier kernels wrote to a grid that
+    waited itself.  A role of the shared-prefix kernels that reads ahead of its wait
+    has first seen that an earlier grid passed its own wait on."""
+    text = _source("kvr_shared_tc.cu")
+    roles = dict(reversed(_roles(text)))
+    wait, flat = "pdl_wait_prerequisites();", lambda s: re.sub(r"\s+", " ", s)
+    softmax, load, mma = (flat(roles[c]) for c in (("<", "8"), ("==", "8"), ("==", "9")))
+    for role in (softmax, mma):
+        before = role.split(wait, 1)[0]
+        assert "seg(" not in before and "mbar_wait" not in before and "tmem_" not in before
+    seen = "waited = !relay_seen(a.relay, a.call); if (waited) " + wait
+    assert seen in load and not re.search(r"seg\(|tma_load_2d\(", load[:load.index(seen)])
+    assert softmax.index(wait) < softmax.index("relay_store(a.relay + 1, a.call);") < softmax.index("pdl_launch_dependents();")
+
+    def kernel(name):
+        start = text.index("    " + name)
+        return flat(text[start:text.index("\n}\n", start)])
+    own = kernel("k_shared_own_decode(")
+    seen = "waited = lane == 0 && !relay_seen(pa.relay + 1, pa.call); waited = __shfl_sync(0xffffffffu, waited, 0); } if (waited) " + wait
+    assert seen in own and not re.search(r"reqs\[|load_piece\(\);|issue\(\);|load_queries\(it", own[:own.index(seen)])
+    prologue = kernel("k_shared_prologue(")
+    assert prologue.index(wait) < prologue.index("relay_store(a.relay, a.call);") < prologue.index("pdl_launch_dependents();")
+    assert not re.search(r"reqs\[", prologue[:prologue.index(wait)])

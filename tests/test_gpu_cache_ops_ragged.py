@@ -4,7 +4,7 @@ test_gpu_cache_ops."""
 import numpy as np
 import pytest
 
-from test_gpu_cache_ops import _pool, _randn, _starts, _weights_case
+from test_gpu_cache_ops import _pool, _randn, _shared_case, _starts, _weights_case
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,36 @@ def test_key_weights_of_many_row_blocks_in_a_cluster(q, prefix):
     for b in range(n):
         got = float(w[0][int(co[b]):int(co[b + 1])].double().sum())
         assert abs(got - 4 * q[b]) <= 4 * q[b] * 2.0 ** -16
+
+
+@pytest.mark.parametrize("groups,prefix,own,q", [([4], [2600], [100, 60, 33, 90], [1] * 4),
+                                                  ([70], [900], [40] * 70, [1] * 70),
+                                                  ([3, 2], [200, 385], [0, 3, 300, 128, 1], [100, 130, 33, 150, 99])])
+def test_shared_prefix_behind_the_kernels_that_write_its_inputs(groups, prefix, own, q):
+    """Prefix, own rows and queries written by kernels just before the call on its
+    stream: the launches overlap at their ends, and every call reads this time's."""
+    import torch
+    L = 19 if sum(q) > 100 else 2
+    pool, args, _ = _shared_case(L, 8, 4, 128, "bf16", groups=groups, prefix=prefix, own=own, q=q, check=())
+    names = (3, 4, 8, 9, 10, 11, 12)
+    out = args[-1]
+    sets = []
+    for k in range(3):
+        x = [torch.randn_like(args[i]) for i in names]
+        for i, y in zip(names, x):
+            args[i].copy_(y)
+        torch.cuda.synchronize()
+        pool.shared_query_attention(*args)
+        torch.cuda.synchronize()
+        sets.append((x, out.clone()))
+    got = []
+    for k in range(30):
+        x = sets[k % 3][0]
+        for i, y in zip(names, x):
+            args[i].copy_(y)
+        pool.shared_query_attention(*args)
+        got.append(out.clone())
+    torch.cuda.synchronize()
+    pool.check()
+    for k, o in enumerate(got):
+        assert torch.equal(o, sets[k % 3][1]), k
