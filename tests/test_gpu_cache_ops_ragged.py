@@ -61,3 +61,22 @@ def test_shared_prefix_behind_the_kernels_that_write_its_inputs(groups, prefix, 
     pool.check()
     for k, o in enumerate(got):
         assert torch.equal(o, sets[k % 3][1]), k
+
+
+def test_shared_prefix_of_one_long_query_among_single_tokens():
+    """A prefill in a batch of decode steps, requests without tokens between them."""
+    q = [1] * 20 + [0, 300, 0, 0] + [1] * 10 + [130, 1, 0]
+    own = [(7 * i) % 150 for i in range(len(q))]
+    for L, H, G in ((1, 2, 4), (3, 1, 7)):
+        _shared_case(L, H, G, 128, "bf16", groups=[22, len(q) - 22], prefix=[300, 129], own=own, q=q)
+    n = 70   # a table in device memory
+    _shared_case(1, 1, 4, 128, "bf16", groups=[n], prefix=[260], own=[i % 40 for i in range(n)], q=[1] * 33 + [170] + [1] * (n - 34))
+
+
+def test_shared_prefix_grids_go_by_the_work():
+    """Requests x the longest one's work (33,000 x 16,500 tokens x 64 units, by 16)
+    is more CTAs than a grid holds; the work itself is small."""
+    n, long = 33000, 16500
+    q = [0] * n
+    q[10], q[11], q[20000], q[32998] = 1, long, 2, 1
+    _shared_case(8, 8, 1, 128, "bf16", groups=[n], prefix=[40], own=[0] * n, q=q, check=(10, 20000, 20001, 32998, 32999), spare=1)
