@@ -1302,7 +1302,6 @@ namespace {
 // tokens' keys and values.
 struct SharedPlan {
     std::vector<DevShared> rq;
-    int32_t max_lq = 0;
     SharedTable tab;
     AssembleTables atab;
     std::vector<DevGroup> gr;   // tensor-core path
@@ -1539,10 +1538,31 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         return st;
     pa.part = static_cast<float *>(p->part);
     pa.q_rot = p->q_rot;
-    int32_t max_own = 1;
-    for (const DevShared &r : pl.rq)
-        if (r.q_len > 0)
+    // Own rows: each request's kernel by its own rows.  For those of long queries the row
+    // groups of a (request, unit) that one CTA takes, as many as leave three CTAs per SM of
+    // all the call's groups (63 single tokens and one query of 2,048, 8 units: 0.30 ms a
+    // call, 7.1 where kernel and groups went by the longest query; 288 units: 10.6 and 17.0)
+    auto own_groups = [&](const DevShared &r) -> int64_t {
+        const int64_t rows = (int64_t)r.q_len * G;
+        return rows > kOwnFewRows ? (rows + kOwnRowsMax - 1) / kOwnRowsMax : 0;
+    };
+    int64_t groups = 0, most = 1;
+    int32_t few_rows = 0, max_own = 1;
+    for (const DevShared &r : pl.rq) {
+        const int64_t n = own_groups(r);
+        groups += n;
+        most = std::max(most, n);
+        if (n > 0)
             max_own = std::max(max_own, r.own + r.q_len);
+        else
+            few_rows = std::max(few_rows, r.q_len * G);
+    }
+    const int64_t per_cta = std::min(most, std::max<int64_t>(1, groups * lh_slice / (3 * (int64_t)p->n_sms)));
+    int64_t chunks = 0;
+    for (DevShared &r : pl.rq) {
+        r.chunk0 = (int32_t)chunks;   // (at most a chunk a query row: within 32 bits)
+        chunks += (own_groups(r) + per_cta - 1) / per_cta;
+    }
     CUtensorMap mq, mpk, mpv, mk, mv;
     if ((st = encode_rows_map(*p, p->q_rot, q_rows, 128, &mq)) != KVR_OK ||
         (any_prefix && ((st = encode_rows_map(*p, sa.prefix_k, pre_rows, 128, &mpk)) != KVR_OK ||
@@ -1568,7 +1588,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
         pa.groups = reinterpret_cast<const DevGroup *>(static_cast<const char *>(slot->dev) + off);
     }
     SharedTcArgs t{&sa, &pl.tab, &pa, &pl.gtab, &mq, any_prefix ? &mpk : nullptr, any_prefix ? &mpv : nullptr,
-                   &mk, &mv, p->n_sms, whole, max_own};
+                   &mk, &mv, p->n_sms, whole, few_rows, (int32_t)per_cta, (int32_t)chunks, max_own};
     p->mark(2, s);
     {
         NvtxRange r("kvr.k_shared_prologue");
@@ -1655,7 +1675,6 @@ extern "C" kvr_status kvr_shared_query_attention(kvr_pool_t p, int32_t n_groups,
                 r.q_off = q_offsets[b];
                 r.q_len = lq;
                 pl.rq.push_back(r);
-                pl.max_lq = std::max(pl.max_lq, lq);
             }
         if (T == 0)
             return KVR_OK;
@@ -1706,7 +1725,6 @@ extern "C" kvr_status kvr_shared_query_attention(kvr_pool_t p, int32_t n_groups,
         sa.n_q_heads = Hq;
         sa.n_kv_heads = H;
         sa.total_q = T;
-        sa.max_q_len = pl.max_lq;
         sa.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
         sa.interleaved = (p->d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
         sa.err = p->err;

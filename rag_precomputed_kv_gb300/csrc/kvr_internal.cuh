@@ -301,7 +301,8 @@ struct alignas(16) DevShared {
     int32_t pre_len;     // P_g; query token t sits at position P_g + own + t
     int32_t q_off, q_len;
     int32_t group;       // index into the group table (tensor-core path)
-    int32_t pad_[5];
+    int32_t chunk0;      // the request's first row chunk of a unit (k_shared_own_rows)
+    int32_t pad_[4];
 };
 static_assert(sizeof(DevShared) == 64, "shared-prefix request table layout");
 struct SharedTable {
@@ -317,7 +318,6 @@ struct SharedArgs {
     int32_t n_reqs;
     int32_t n_layers, n_q_heads, n_kv_heads;
     int32_t total_q;            // T
-    int32_t max_q_len;
     float scale_log2;
     int32_t interleaved;
     int *err;
@@ -347,6 +347,9 @@ static_assert(sizeof(DevGroup) == 64, "group table layout");
 struct GroupTable {
     DevGroup groups[kInlineEntries];
 };
+// Query rows of a request up to which k_shared_own_decode takes its own part, and those
+// that one row group of k_shared_own_rows holds.
+constexpr int kOwnFewRows = 16, kOwnRowsMax = 64;
 // Bytes of one partial result of the prefix part (a block's rows of one CTA:
 // 256 x 128 fp32 and 256 maxima and sums).
 constexpr int64_t kSharedPartBytes = 256 * 128 * 4 + 256 * 8;
@@ -379,7 +382,10 @@ struct SharedTcArgs {
     const void *tmap_q, *tmap_pk, *tmap_pv, *tmap_k, *tmap_v;
     int32_t n_sms;
     bool whole;                 // the prefix kernel takes whole blocks, and their rows' own keys too
-    int32_t max_own_keys;       // the longest own part (own rows and query tokens) of a request with tokens
+    int32_t few_rows;           // most query rows of a request that k_shared_own_decode takes (0: none)
+    int32_t own_per_cta;        // k_shared_own_rows: 64-row groups of a CTA
+    int32_t own_chunks;         // its CTAs of a unit (0: no request of more rows than the other takes)
+    int32_t max_own_keys;       // the longest own part (own rows and query tokens) of a request of k_shared_own_rows
 };
 
 // ---- attention weight per cached key ----

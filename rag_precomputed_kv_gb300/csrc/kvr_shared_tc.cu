@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kPrThreads)
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kOwThreads = 128;
-constexpr int kOwRowsMax = 64;
+constexpr int kOwRowsMax = kOwnRowsMax;
 constexpr int kOwTileMax = 128;   // keys per tile
 // Shared memory of k_shared_own_rows: K and V tile ([tile_keys][128], two
 // 128B-swizzled panels each), the barrier.
@@ -980,8 +980,8 @@ __device__ __forceinline__ void finish_rows(const SharedArgs &a, const SharedPre
 __global__ void __launch_bounds__(kOwThreads, 3)
     k_shared_own_rows(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                  const __grid_constant__ SharedArgs a, const __grid_constant__ SharedTable rt,
-                 const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt, const int n_chunks,
-                 const int tiles_per_cta, const int tile_keys)
+                 const __grid_constant__ SharedPrefixArgs pa, const __grid_constant__ GroupTable gt, const int tiles_per_cta,
+                 const int tile_keys)
 {
     using namespace dec;
     extern __shared__ uint8_t ow_smem_raw[];
@@ -994,15 +994,29 @@ __global__ void __launch_bounds__(kOwThreads, 3)
     const DevGroup *groups = pa.groups ? pa.groups : gt.groups;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = pa.group;
-    unsigned bi = blockIdx.x;
-    const int chunk = (int)(bi % (unsigned)n_chunks);
-    bi /= (unsigned)n_chunks;
-    const int lh_s = (int)(bi % (unsigned)pa.lh_count), lh = pa.lh_base + lh_s;
-    const DevShared rq = reqs[bi / (unsigned)pa.lh_count];
-    const int m_rows = rq.q_len * G;
-    const int r_first = chunk * tiles_per_cta * kOwRowsMax, r_last = min(m_rows, r_first + tiles_per_cta * kOwRowsMax);
-    if (r_first >= m_rows)
-        return;   // uniform over the CTA
+    if (a.reqs)
+        pdl_wait_prerequisites();   // (the table was uploaded)
+    // this CTA's request: the last one whose first chunk is at or before the CTA's (those
+    // behind it, without chunks, begin where the next one does); where requests have as many
+    // chunks as one another, the one that it would be then
+    const int rows_cta = tiles_per_cta * kOwRowsMax;
+    auto chunks_of = [&](const DevShared &r) { return r.q_len * G > kOwnFewRows ? (r.q_len * G + rows_cta - 1) / rows_cta : 0; };
+    int b = min((int)(((float)blockIdx.x + 0.5f) * __fdividef((float)a.n_reqs, (float)gridDim.x)), a.n_reqs - 1);
+    if (reqs[b].chunk0 * pa.lh_count > (int)blockIdx.x || (reqs[b].chunk0 + chunks_of(reqs[b])) * pa.lh_count <= (int)blockIdx.x) {
+        int last = a.n_reqs - 1;
+        b = 0;
+        while (b < last) {
+            const int mid = (b + last + 1) >> 1;
+            if (reqs[mid].chunk0 * pa.lh_count <= (int)blockIdx.x)
+                b = mid;
+            else
+                last = mid - 1;
+        }
+    }
+    const DevShared rq = reqs[b];
+    const int m_rows = rq.q_len * G, n_chunks = chunks_of(rq), in_req = (int)blockIdx.x - rq.chunk0 * pa.lh_count;
+    const int lh_s = in_req / n_chunks, lh = pa.lh_base + lh_s, r_first = (in_req - lh_s * n_chunks) * rows_cta;
+    const int r_last = min(m_rows, r_first + rows_cta);
     auto keys_to = [&](int r_end) { return rq.own + (r_end - 1) / G + 1; };   // keys of the rows before r_end
     const bool once = keys_to(r_last) <= kOwTile;
     const int64_t kv_row0 = rq.cache_row0 + (int64_t)lh * rq.cap;
@@ -1237,13 +1251,15 @@ __global__ void __launch_bounds__(kOdThreads, 1)
     if (waited)
         pdl_wait_prerequisites();
 
+    // (longer queries are k_shared_own_rows')
+    auto takes = [&](const DevShared &r) { return r.q_len > 0 && r.q_len * G <= kOwnFewRows; };
     // the next step to load: tile `lj` of piece `li`
     int li = it0, lj = 0, l_keys = 0, n_issued = 0;
     int64_t l_row0 = 0;
     auto load_piece = [&]() {   // the first piece from li on with keys to load
         for (; li < it1; ++li) {
             const DevShared &r = reqs[li / pa.lh_count];
-            if (r.q_len > 0) {
+            if (takes(r)) {
                 l_keys = r.own + r.q_len;
                 l_row0 = r.cache_row0 + (int64_t)(pa.lh_base + li % pa.lh_count) * r.cap;
                 return;
@@ -1302,7 +1318,7 @@ __global__ void __launch_bounds__(kOdThreads, 1)
     int k = 0;   // steps done
     bool ok = true;
     for (int it = it0; it < it1 && ok; ++it) {
-        if (rq.q_len == 0) {
+        if (!takes(rq)) {
             if (it + 1 < it1)
                 load_queries(it + 1);
             continue;
@@ -1474,26 +1490,21 @@ cudaError_t launch_shared_tc(const SharedTcArgs &t, bool pdl, cudaStream_t s)
         if (e != cudaSuccess)
             return e;
     }
-    const int rows = a.max_q_len * pa.group;
-    if (rows <= 16) {
+    if (t.few_rows > 0) {
         const int64_t items = (int64_t)a.n_reqs * pa.lh_count;
         if (items > 0x7fffffff)
             return cudaErrorInvalidValue;
-        return launch_pdl(rows <= 8 ? k_shared_own_decode<false> : k_shared_own_decode<true>, std::min<int64_t>(items, t.n_sms), kOdThreads, kOdSmem, pdl, s, map(t.tmap_k),
-                          map(t.tmap_v), a, *t.reqs, pa, *t.groups);
+        e = launch_pdl(t.few_rows <= 8 ? k_shared_own_decode<false> : k_shared_own_decode<true>, std::min<int64_t>(items, t.n_sms),
+                       kOdThreads, kOdSmem, pdl, s, map(t.tmap_k), map(t.tmap_v), a, *t.reqs, pa, *t.groups);
+        if (e != cudaSuccess || t.own_chunks == 0)
+            return e;
     }
     // tiles that just hold the longest own part, cut evenly (a smaller tile
     // leaves room for more CTAs per SM)
     const int n_tiles = (t.max_own_keys + kOwTileMax - 1) / kOwTileMax;
     const int tile_keys = ((t.max_own_keys + n_tiles - 1) / n_tiles + 31) & ~31;
-    // row groups per CTA: all of a (request, unit)'s, while that leaves three
-    // CTAs per SM
-    const int n_groups = (rows + kOwRowsMax - 1) / kOwRowsMax;
-    const int64_t units = (int64_t)a.n_reqs * pa.lh_count;
-    const int per_cta = (int)std::min<int64_t>(n_groups, std::max<int64_t>(1, units * n_groups / (3 * (int64_t)t.n_sms)));
-    const int n_chunks = (n_groups + per_cta - 1) / per_cta;
-    return launch_pdl(k_shared_own_rows, units * n_chunks, kOwThreads, ow_bytes(tile_keys), pdl, s, map(t.tmap_k), map(t.tmap_v),
-                      a, *t.reqs, pa, *t.groups, n_chunks, per_cta, tile_keys);
+    return launch_pdl(k_shared_own_rows, (int64_t)t.own_chunks * pa.lh_count, kOwThreads, ow_bytes(tile_keys), pdl, s,
+                      map(t.tmap_k), map(t.tmap_v), a, *t.reqs, pa, *t.groups, t.own_per_cta, tile_keys);
 }
 
 }  // namespace kvr

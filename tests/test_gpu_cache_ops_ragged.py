@@ -80,3 +80,27 @@ def test_shared_prefix_grids_go_by_the_work():
     q = [0] * n
     q[10], q[11], q[20000], q[32998] = 1, long, 2, 1
     _shared_case(8, 8, 1, 128, "bf16", groups=[n], prefix=[40], own=[0] * n, q=q, check=(10, 20000, 20001, 32998, 32999), spare=1)
+
+
+def _us(fn):
+    import torch
+    t = []
+    for k in range(8):
+        e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        torch.cuda._sleep(1000000)
+        e[0].record()
+        fn()
+        e[1].record()
+        torch.cuda.synchronize()
+        if k > 2:
+            t.append(1e3 * e[0].elapsed_time(e[1]))
+    return sorted(t)[len(t) // 2]
+
+
+def test_a_long_query_is_not_slower_for_the_single_tokens_beside_it():
+    """A batch takes no more than three times what its parts take alone (one whose
+    launches went by requests x the longest query took 27 times as long)."""
+    def us(q, own):
+        pool, args, _ = _shared_case(1, 8, 4, 128, "bf16", groups=[len(q)], prefix=[2592], own=own, q=q, check=())
+        return _us(lambda: pool.shared_query_attention(*args))
+    assert us([1] * 40 + [2048] + [1] * 23, [100] * 64) < 3 * (us([1] * 63, [100] * 63) + us([2048], [100]))
