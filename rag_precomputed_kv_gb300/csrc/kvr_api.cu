@@ -1813,6 +1813,15 @@ extern "C" kvr_status kvr_key_weights(kvr_pool_t p, int32_t batch, const int64_t
         CUtensorMap mk;
         if (tc && (st = encode_cache_map(*p, const_cast<void *>(cache_k), r1, &mk)) != KVR_OK)
             return st;
+        // On the tensor cores each request goes to the kernel for its own query rows, a
+        // launch for those of either (63 single tokens and a window of 64 on 1,200 keys, 288
+        // units: 1.00 ms, 1.48 with all in the window's kernel, which reads K twice; 15 and
+        // one on 16,000, 64 units: 0.89 and 1.65; 16 requests of 7 to 84 rows: 192 us, 187)
+        int32_t few = batch;
+        if (tc)
+            few = (int32_t)(std::stable_partition(rq.begin(), rq.end(),
+                                                  [&](const DevReq &r) { return (int64_t)r.q_len * (Hq / H) <= kWeightsFewRows; }) -
+                            rq.begin());
         ReqTable tab;
         Slot *slot = nullptr;
         if (inl) {
@@ -1822,10 +1831,20 @@ extern "C" kvr_status kvr_key_weights(kvr_pool_t p, int32_t batch, const int64_t
                 return st;
             a.reqs = static_cast<const DevReq *>(slot->dev);
         }
-        cudaError_t e;
-        {
-            NvtxRange r("kvr.k_key_weights");
-            e = tc ? launch_weights_tc(a, tab, &mk, p->n_sms, s) : launch_weights_simt(a, tab, p->d.dtype, D, p->n_sms, s);
+        cudaError_t e = cudaSuccess;
+        NvtxRange r("kvr.k_key_weights");
+        if (!tc)
+            e = launch_weights_simt(a, tab, p->d.dtype, D, p->n_sms, s);
+        for (int part = 0; tc && part < 2 && e == cudaSuccess; ++part) {
+            a.req0 = part ? few : 0;
+            a.n_reqs = part ? batch - few : few;
+            a.max_rows = a.max_q_len = 0;
+            for (int i = a.req0; i < a.req0 + a.n_reqs; ++i) {
+                a.max_rows = std::max(a.max_rows, rq[i].prefix + rq[i].q_len);
+                a.max_q_len = std::max(a.max_q_len, rq[i].q_len);
+            }
+            if (a.max_rows > 0)
+                e = launch_weights_tc(a, tab, &mk, p->n_sms, s);
         }
         if (slot)
             cudaEventRecord(slot->done, s);

@@ -389,17 +389,20 @@ struct SharedTcArgs {
 };
 
 // ---- attention weight per cached key ----
+// Query rows of a request up to which it goes to k_key_weights_tc, beyond to
+// k_key_weights_window.
+constexpr int kWeightsFewRows = 32;
 struct WeightsArgs {
     const DevReq *reqs;         // NULL: the ReqTable parameter
     const float2 *rope;
     const void *q;              // [L][T][Hq][D], not rotated
     const void *cache_k;
     float *weights;             // the cache's blocks, one float a row
-    int32_t n_reqs;
+    int32_t req0, n_reqs;       // this launch's requests of the table (CUDA cores: all)
     int32_t n_layers, n_q_heads, n_kv_heads;
     int32_t total_q;
-    int32_t max_rows;           // largest P_b + Lq_b of the batch
-    int32_t max_q_len;
+    int32_t max_rows;           // largest P_b + Lq_b of the launch's requests
+    int32_t max_q_len;          // and longest query
     float scale_log2;
     int32_t interleaved;
     int32_t accumulate;

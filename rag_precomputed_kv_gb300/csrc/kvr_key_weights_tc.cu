@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     pdl_wait_prerequisites();
 
     const DevReq *reqs = a.reqs ? a.reqs : rt.reqs;
-    const DevReq rq = reqs[unit_i / units];
+    const DevReq rq = reqs[a.req0 + unit_i / units];
     const int lh = unit_i % units;
     const int G = a.n_q_heads / a.n_kv_heads;
     const int m_rows = rq.q_len * G, n = rq.prefix + rq.q_len;
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
     pdl_wait_prerequisites();
 
     const DevReq *reqs = a.reqs ? a.reqs : rt.reqs;
-    const DevReq rq = reqs[unit_i / units];
+    const DevReq rq = reqs[a.req0 + unit_i / units];
     const int lh = unit_i % units;
     const int G = a.n_q_heads / a.n_kv_heads;
     const int m_rows = rq.q_len * G, n = rq.prefix + rq.q_len;
@@ -1007,6 +1007,7 @@ static cudaError_t launch_window(const WeightsArgs &a, const ReqTable &rt, const
     return launch_cluster(k_key_weights_window, units * c, kWtThreads, c > 1 ? kWwSmemCluster : kWwSmem, c, s, tmk, a, rt, c);
 }
 
+static_assert(kWeightsFewRows == 32, "the most rows of k_key_weights_tc");
 cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const void *tmap_k, int n_sms, cudaStream_t s)
 {
     const CUtensorMap &m = *static_cast<const CUtensorMap *>(tmap_k);
@@ -1017,7 +1018,7 @@ cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const vo
         return launch_nq<8>(a, rt, m, n_sms, s);
     if (rows <= 16)
         return launch_nq<16>(a, rt, m, n_sms, s);
-    if (rows <= 32)
+    if (rows <= kWeightsFewRows)
         return launch_nq<32>(a, rt, m, n_sms, s);
     return launch_window(a, rt, m, n_sms, s);
 }

@@ -104,3 +104,41 @@ def test_a_long_query_is_not_slower_for_the_single_tokens_beside_it():
         pool, args, _ = _shared_case(1, 8, 4, 128, "bf16", groups=[len(q)], prefix=[2592], own=own, q=q, check=())
         return _us(lambda: pool.shared_query_attention(*args))
     assert us([1] * 40 + [2048] + [1] * 23, [100] * 64) < 3 * (us([1] * 63, [100] * 63) + us([2048], [100]))
+
+
+def test_key_weights_of_one_window_among_single_tokens():
+    """Each request by the kernel for its own rows, whatever is beside it: the
+    batch's order, requests without tokens, a table in device memory."""
+    q = [1] * 5 + [0, 40, 8, 0, 200] + [1] * 6
+    prefix = [(97 * i) % 700 for i in range(len(q))]
+    for acc in (False, True):
+        _weights_case(2, 1, 4, 128, "bf16", prefix=prefix, q=q, accumulate=acc)
+    _weights_case(1, 2, 4, 128, "bf16", prefix=[30 + i for i in range(80)], q=[1] * 50 + [33] + [0] * 4 + [8] * 25)
+
+
+def test_key_weights_of_single_tokens_beside_a_window():
+    """Single tokens get the same weights bit for bit with and without a window in
+    their batch (either way a CTA a unit, and three query terms), and the batch
+    takes no longer than its parts."""
+    import torch
+    L, H, G, D, P = 8, 8, 4, 128, 1200
+    pool = _pool(L, H, G, D, "bf16")
+
+    def call(q):
+        co, qo = _starts([P + n for n in q]), _starts(q).astype(np.int32)
+        ck = _randn(1, (int(co[-1]) * L * H, D), "bf16", 2.0)
+        Q = _randn(2, (L, int(qo[-1]), H * G, D), "bf16", 2.0)
+        w = torch.empty(int(co[-1]) * L * H, device="cuda")
+        return w, ck, Q, lambda: pool.key_weights(co, [P] * len(q), qo, Q, ck, w)
+
+    w, ck, Q, run = call([1] * 6 + [64])
+    w1, ck1, Q1, run1 = call([1] * 6)
+    ck1.copy_(ck[:ck1.shape[0]])
+    Q1.copy_(Q[:, :6])
+    run()
+    run1()
+    torch.cuda.synchronize()
+    pool.check()
+    assert torch.equal(w[:w1.numel()], w1)
+    single, window, both = (_us(call(q)[3]) for q in ([1] * 63, [2048], [1] * 40 + [2048] + [1] * 23))
+    assert both < 1.5 * (single + window)
