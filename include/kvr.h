@@ -196,12 +196,14 @@ KVR_API kvr_status kvr_pool_unregister(kvr_pool_t pool);
  * kvr_pool_reserve -- bind the pool to the current device (if no call has
  * yet) and allocate, now, every buffer that calls within these limits need:
  * the 8 staging slots sized for the largest tables of a call with up to
- * max_batch requests, max_spans spans and max_locals local sources, and the
- * query scratch for up to max_query_tokens query tokens per call (tensor-core
- * path only).  It synchronizes (allocation and the wait for slots in use).
- * After it, kvr_assemble / kvr_query_attention / kvr_prefill calls within the
- * limits never allocate and never wait on the host, except on a staging slot
- * whose previous call is still queued (see the conventions above).  Calls
+ * max_batch requests (and no more groups of them), max_spans spans and
+ * max_locals local sources, and the query scratch for up to max_query_tokens
+ * query tokens per call (tensor-core path only).  It synchronizes (allocation
+ * and the wait for slots in use).  After it, calls of every entry point within
+ * the limits never allocate and never wait on the host, except on a staging
+ * slot whose previous call is still queued (see the conventions above) and,
+ * kvr_shared_query_attention on the tensor cores, for more partial results than
+ * a call before it had (its groups' sizes decide how many).  Calls
  * beyond the limits still work: they grow the buffers as described there.
  * Make it outside any stream capture.  Errors: KVR_ERR_INVALID_ARG (NULL pool,
  * a negative limit, max_query_tokens > 2^31 - 1), KVR_ERR_CUDA.

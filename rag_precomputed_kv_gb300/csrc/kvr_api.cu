@@ -388,11 +388,13 @@ extern "C" kvr_status kvr_pool_reserve(kvr_pool_t p, int32_t max_batch, int32_t 
         return st;
     DeviceGuard g(p->device);
     // the largest table a call within the limits uploads: an assemble's spans
-    // and local sources, or a query attention's request / append tables
+    // and local sources, or a request table with what goes beside it: append
+    // spans (CUDA-core attention), groups (shared prefixes: as many as requests)
+    constexpr size_t req = std::max({sizeof(DevReq), sizeof(DevShared), sizeof(DevEvict)});
     const size_t asm_bytes = align16((size_t)max_spans * sizeof(DevSpan)) + (size_t)max_locals * sizeof(DevLocal);
-    const size_t qa_bytes = align16((size_t)max_batch * sizeof(DevReq)) +
-                            align16((size_t)max_batch * sizeof(DevSpan)) + (size_t)max_batch * sizeof(DevLocal);
-    const size_t bytes = std::max(asm_bytes, qa_bytes);
+    const size_t append_bytes = align16((size_t)max_batch * sizeof(DevSpan)) + (size_t)max_batch * sizeof(DevLocal);
+    const size_t req_bytes = align16((size_t)max_batch * req) + std::max(append_bytes, (size_t)max_batch * sizeof(DevGroup));
+    const size_t bytes = std::max(asm_bytes, req_bytes);
     cudaError_t e;
     for (Slot &s : p->slots) {
         if (s.used && (e = cudaEventSynchronize(s.done)) != cudaSuccess)

@@ -142,3 +142,39 @@ def test_key_weights_of_single_tokens_beside_a_window():
     assert torch.equal(w[:w1.numel()], w1)
     single, window, both = (_us(call(q)[3]) for q in ([1] * 63, [2048], [1] * 40 + [2048] + [1] * 23))
     assert both < 1.5 * (single + window)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "fp32"), (128, "bf16")])
+def test_reserved_pool_takes_every_request_table(D, dtype):
+    """After kvr_pool_reserve no call within the limits waits for the GPU: each
+    returns while a kernel enqueued before it still runs."""
+    import torch
+    B, L, H, G = 1000, 1, 1, 2
+    pool = _pool(L, H, G, D, dtype)
+    pool.reserve(max_batch=B, max_query_tokens=B)
+    co, qo = np.arange(B + 1) * 6, np.arange(B + 1)
+    ck, cv = _randn(1, (6 * B, D), dtype), _randn(2, (6 * B, D), dtype)
+    q, kq, vq = _randn(3, (L, B, H * G, D), dtype), _randn(4, (L, B, H, D), dtype), _randn(5, (L, B, H, D), dtype)
+    out, w = torch.empty_like(q), torch.zeros(6 * B, device="cuda")
+    kept, own = torch.empty(2 * B, device="cuda", dtype=torch.int32), [3] * B
+
+    def calls(n):
+        c, o, t = co[:n + 1], own[:n], qo[:n + 1]
+        x = [y[:, :n].contiguous() for y in (q, kq, vq, out)]
+        # (a group of each request, nothing shared: no partial results)
+        yield lambda: pool.shared_query_attention(t, [0] * (n + 1), [0] * n, None, None, c, o, t, *x[:3], ck, cv, x[3])
+        yield lambda: pool.key_weights(c, o, t, x[0], ck, w)
+        yield lambda: pool.evict(c, [4] * n, [2] * n, w, ck, cv, kept)
+
+    for call in calls(3):     # (kernels are loaded)
+        call()
+    for call in calls(B):
+        for _ in range(3):
+            torch.cuda.synchronize()
+            torch.cuda._sleep(600_000_000)
+            done = torch.cuda.Event()
+            done.record()
+            call()
+            assert not done.query()
+    torch.cuda.synchronize()
+    pool.check()
