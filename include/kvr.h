@@ -372,7 +372,8 @@ KVR_API kvr_status kvr_prefill(kvr_pool_t pool, int32_t batch, const int32_t *sp
  * of that request's call (a weight of 0 times it is NaN), on other requests it
  * has no effect; neither has what a block holds behind its last row.
  * Errors: KVR_ERR_INVALID_ARG (also: the caches or `out` overlap the prefix or
- * each other), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;
+ * each other, the caches overlap q, kq or vq, or `out` overlaps q without being
+ * the same buffer), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;
  * kvr_check reports KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for
  * kvr_query_attention.
  */

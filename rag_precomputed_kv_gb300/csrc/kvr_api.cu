@@ -1702,6 +1702,15 @@ extern "C" kvr_status kvr_shared_query_attention(kvr_pool_t p, int32_t n_groups,
             for (int j = 0; j < i; ++j)
                 if (dst[i].meets(dst[j]))
                     return fail(KVR_ERR_INVALID_ARG, "the caches and the output overlap");
+        // the queries' keys and values are appended, and rows of the output written, while
+        // other rows of the inputs are still read (each row of q only before its own output)
+        const Range in[3] = {range_of(q, 0, (int64_t)L * T * Hq, row_bytes), range_of(kq, 0, (int64_t)L * T * H, row_bytes),
+                             range_of(vq, 0, (int64_t)L * T * H, row_bytes)};
+        for (const Range &x : in)
+            if (x.meets(dst[0]) || x.meets(dst[1]))
+                return fail(KVR_ERR_INVALID_ARG, "the caches overlap the query inputs");
+        if (in[0].meets(dst[2]) && in[0].lo != dst[2].lo)
+            return fail(KVR_ERR_INVALID_ARG, "the output overlaps the queries (it may only be the same buffer)");
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const bool may_tc = attention_tc_supported(p->d.dtype, D);
         if ((st = check_capture(*p, s, !may_tc && batch <= kInlineEntries,

@@ -200,3 +200,17 @@ def test_exchange_of_row_sums_between_ctas():
     assert _exchange_goes_wrong(3, 2, 1)
     for ctas, blocks in ((2, 5), (3, 4), (4, 3)):
         assert not _exchange_goes_wrong(ctas, blocks, 2)
+
+
+@pytest.mark.parametrize("kw", [dict(ck=C), dict(cv=C + 1024), dict(kq=Dp), dict(vq=E + 128 * 2 * 4 * 39),
+                                dict(q=F - 4096, out=F - 4096 + 2048), dict(q=F, out=F - 256)])
+def test_shared_query_attention_refuses_outputs_over_its_inputs(lib, pool, kw):
+    """Other rows of the inputs are read while rows are written."""
+    assert shared(lib, pool, **kw) == 1
+    assert "overlap" in lib.kvr_last_error().decode()
+
+
+def test_shared_query_attention_takes_its_queries_place(lib, pool):
+    """The output in the queries' own buffer: each row is read before it is written."""
+    if _no_gpu():
+        assert shared(lib, pool, q=F, out=F) == 4

@@ -178,3 +178,14 @@ def test_reserved_pool_takes_every_request_table(D, dtype):
             assert not done.query()
     torch.cuda.synchronize()
     pool.check()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "fp32"), (128, "bf16")])
+def test_shared_prefix_writes_the_output_over_the_queries(D, dtype):
+    import torch
+    pool, args, (ck0, cv0) = _shared_case(2, 2, 4, D, dtype, groups=[3], prefix=[300], own=[5, 40, 0], q=[1, 30, 2])
+    want, q = args[-1].clone(), args[8].clone()
+    pool.shared_query_attention(*args[:8], q, *args[9:-1], q)
+    torch.cuda.synchronize()
+    pool.check()
+    assert torch.equal(q, want)
