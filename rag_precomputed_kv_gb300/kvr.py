@@ -138,9 +138,12 @@ def _ints(name: str, a, code: str, n: Optional[int] = None):
         c = array(code, a)
         addr, m = c.buffer_info()
     else:
+        a = np.asarray(a)
         c = np.ascontiguousarray(a, dtype=np.int32 if code == "i" else np.int64)
         if c.ndim != 1:
             raise ValueError(f"{name} must be one-dimensional, got shape {c.shape}")
+        if a.dtype != c.dtype and a.size and (a.dtype.kind not in "iu" or (a != c).any()):
+            raise ValueError(f"{name} must hold {8 * c.itemsize}-bit integers")
         addr, m = c.ctypes.data, len(c)
     if n is not None and m != n:
         raise ValueError(f"{name} must hold {n} values, got {m}")
@@ -292,7 +295,9 @@ class Pool:
         read only) and the requests' own rows, to which the query K/V are
         appended; writes ``out``."""
         go = _ints("group_offsets", group_offsets, "i")
-        n, batch = go[2] - 1, int(group_offsets[-1])
+        if go[2] == 0:
+            raise ValueError("group_offsets must hold at least one value")
+        n, batch = go[2] - 1, max(0, int(go[0][-1]))   # (the library refuses a negative one)
         po, pl = _ints("prefix_offsets", prefix_offsets, "q", n + 1), _ints("prefix_len", prefix_len, "i", n)
         co, ol = _ints("cache_offsets", cache_offsets, "q", batch + 1), _ints("own_len", own_len, "i", batch)
         qo = _ints("q_offsets", q_offsets, "i", batch + 1)

@@ -214,3 +214,29 @@ def test_shared_query_attention_takes_its_queries_place(lib, pool):
     """The output in the queries' own buffer: each row is read before it is written."""
     if _no_gpu():
         assert shared(lib, pool, q=F, out=F) == 4
+
+
+def test_python_binding_refuses_lengths_that_are_not_integers():
+    """Nothing is cut to an integer or to 32 bits on the way."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    assert [list(kvr._ints("x", a, "i")[0]) for a in ([1, 2], (1, 2), np.array([1, 2], np.int64), torch.tensor([1, 2]))] == [[1, 2]] * 4
+    assert list(kvr._ints("x", np.array([1 << 40]), "q")[0]) == [1 << 40]
+    assert kvr._ints("x", np.array([]), "i")[2] == 0
+    for a in (np.array([1.5, 2.0]), np.array([1.0]), np.array([(1 << 32) + 5]), np.array([1 << 31], np.uint32), torch.tensor([0.5]),
+              np.array([True])):
+        with pytest.raises(ValueError, match="x must hold 32-bit integers"):
+            kvr._ints("x", a, "i")
+    for a in ([1.5], [1 << 31]):
+        with pytest.raises((TypeError, OverflowError)):
+            kvr._ints("x", a, "i")
+    k = torch.zeros((1, 1, 1, 8, 64))
+    p, x = kvr.Pool(k, k.clone(), 2, 1e4), torch.zeros(64)
+    try:
+        with pytest.raises(ValueError, match="group_offsets"):
+            p.shared_query_attention([], [0], [], x, x, [0], [], [0], x, x, x, x, x, x, stream=0)
+        with pytest.raises(kvr.KvrError) as e:
+            p.shared_query_attention([0, -1], [0, 4], [4], x, x, [0], [], [0], x, x, x, x, x, x, stream=0)
+        assert e.value.status == 1
+    finally:
+        p.close()
