@@ -108,12 +108,18 @@ def _raise(st: int):
         raise KvrError(st, load().kvr_last_error().decode())
 
 
+_raw_stream = None   # () -> the current stream's handle, once CUDA is initialised
+
+
 def _stream_ptr(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
+        if _raw_stream is not None:   # 3 us less than a Stream object
+            return _raw_stream()
         import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():   # 3 us less than a Stream object
-            return raw(torch.cuda.current_device())
+        raw, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw is not None and dev is not None and torch.cuda.is_initialized():
+            _raw_stream = lambda: raw(dev())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -150,10 +156,18 @@ def _ints(name: str, a, code: str, n: Optional[int] = None):
     return c, addr, m
 
 
-def _check_f32(t, name: str):
-    import torch
-    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous float32 tensor")
+def _data(name: str, t, dtype, n: int) -> Optional[int]:
+    """The address of a tensor that a call reads or writes as ``n`` elements of
+    ``dtype`` one behind the other (None: NULL, which the library judges)."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.is_contiguous() and t.numel() >= n and (t.is_cuda or t.is_pinned())):
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor")
+        if t.numel() < n:
+            raise ValueError(f"{name} must hold at least {n} values, got {t.numel()}")
+        raise ValueError(f"{name} must be in device or pinned host memory")
+    return t.data_ptr()
 
 
 def _np_ptr(a: Optional[np.ndarray]):
@@ -228,6 +242,8 @@ class Pool:
         self._keep = (k, v)
         self.n_layers, self.n_kv_heads, self.n_q_heads, self.head_dim = L, H, n_q_heads, D
         self.dtype = k.dtype
+        # elements of a cache row in every layer and kv head, and of a token's queries in a layer
+        self._row, self._heads, self._wide = L * H * D, H * D, n_q_heads * D
 
     def reserve(self, max_batch: int = 0, max_spans: int = 0, max_locals: int = 0, max_query_tokens: int = 0):
         """kvr_pool_reserve: bind the pool to the current device and allocate
@@ -301,22 +317,33 @@ class Pool:
         po, pl = _ints("prefix_offsets", prefix_offsets, "q", n + 1), _ints("prefix_len", prefix_len, "i", n)
         co, ol = _ints("cache_offsets", cache_offsets, "q", batch + 1), _ints("own_len", own_len, "i", batch)
         qo = _ints("q_offsets", q_offsets, "i", batch + 1)
-        _raise(load().kvr_shared_query_attention(self._h, n, go[1], po[1], pl[1], _ptr(prefix_k), _ptr(prefix_v), co[1],
-                                                 ol[1], qo[1], _ptr(q), _ptr(kq), _ptr(vq), _ptr(cache_k), _ptr(cache_v),
-                                                 _ptr(out), float(softmax_scale), _stream_ptr(stream)))
+        tokens = self.n_layers * int(qo[0][-1])
+        if tokens <= 0:   # nothing to do, or refused
+            pk, pv, q_, kq_, vq_, ck, cv, out_ = map(_ptr, (prefix_k, prefix_v, q, kq, vq, cache_k, cache_v, out))
+        else:
+            d, rows, wide = self.dtype, self._row * int(co[0][-1]), tokens * self._wide
+            heads, pre = tokens * self._heads, self._row * int(po[0][-1]) if any(pl[0]) else 0
+            pk, pv = _data("prefix_k", prefix_k, d, pre), _data("prefix_v", prefix_v, d, pre)
+            q_, kq_, vq_ = _data("q", q, d, wide), _data("kq", kq, d, heads), _data("vq", vq, d, heads)
+            ck, cv, out_ = _data("cache_k", cache_k, d, rows), _data("cache_v", cache_v, d, rows), _data("out", out, d, wide)
+        _raise(load().kvr_shared_query_attention(self._h, n, go[1], po[1], pl[1], pk, pv, co[1], ol[1], qo[1], q_, kq_, vq_,
+                                                 ck, cv, out_, float(softmax_scale), _stream_ptr(stream)))
 
     def key_weights(self, cache_offsets, prefix_len, q_offsets, q, cache_k, weights, softmax_scale: float = 0.0,
                     accumulate: bool = False, stream=None):
         """kvr_key_weights: the attention weight each cached key receives from
         the query tokens (fp32, one value per cache row), written to
         ``weights`` or, with ``accumulate``, added to it."""
-        _check_f32(weights, "weights")
+        import torch
         qo = _ints("q_offsets", q_offsets, "i")
         n = qo[2] - 1
         co, pl = _ints("cache_offsets", cache_offsets, "q", n + 1), _ints("prefix_len", prefix_len, "i", n)
-        _raise(load().kvr_key_weights(self._h, n, co[1], pl[1], qo[1], _ptr(q), _ptr(cache_k), _ptr(weights),
-                                      float(softmax_scale), KVR_WEIGHTS_ACCUMULATE if accumulate else 0,
-                                      _stream_ptr(stream)))
+        rows, tokens = (int(co[0][-1]), int(qo[0][-1])) if n >= 0 else (0, 0)
+        w = _data("weights", weights, torch.float32, self.n_layers * self.n_kv_heads * rows)
+        ck = _data("cache_k", cache_k, self.dtype, self._row * rows)
+        q_ = _data("q", q, self.dtype, self.n_layers * tokens * self._wide)
+        _raise(load().kvr_key_weights(self._h, n, co[1], pl[1], qo[1], q_, ck, w, float(softmax_scale),
+                                      KVR_WEIGHTS_ACCUMULATE if accumulate else 0, _stream_ptr(stream)))
 
     def evict(self, cache_offsets, kv_len, keep, weights, cache_k, cache_v, kept, dst_offsets=None, dst_k=None,
               dst_v=None, dst_weights=None, n_first: int = 0, n_recent: int = 0, keep_rotation: bool = False,
@@ -327,25 +354,25 @@ class Pool:
         rows.  Without ``dst_k`` the cache and the weights are evicted in
         place.  Returns the rows each request holds afterwards (numpy int32)."""
         import torch
-        _check_f32(weights, "weights")
         if dst_k is None:
             if dst_v is not None or dst_weights is not None or dst_offsets is not None:
                 raise ValueError("dst_offsets, dst_v and dst_weights go with dst_k")
             dst_offsets, dst_k, dst_v, dst_weights = cache_offsets, cache_k, cache_v, weights
         elif dst_offsets is None:
             raise ValueError("dst_k needs dst_offsets")
-        if dst_weights is not None:
-            _check_f32(dst_weights, "dst_weights")
-        if kept is not None and (kept.dtype != torch.int32 or not kept.is_contiguous()):
-            raise ValueError("kept must be a contiguous int32 tensor")
         kl = _ints("kv_len", kv_len, "i")
         n = kl[2]
         kp, co = _ints("keep", keep, "i", n), _ints("cache_offsets", cache_offsets, "q", n + 1)
         do = _ints("dst_offsets", dst_offsets, "q", n + 1)
-        _raise(load().kvr_evict(self._h, n, co[1], kl[1], kp[1], int(n_first), int(n_recent), _ptr(weights), _ptr(cache_k),
-                                _ptr(cache_v), do[1], _ptr(dst_k), _ptr(dst_v), _ptr(dst_weights), _ptr(kept),
-                                KVR_EVICT_KEEP_ROTATION if keep_rotation else 0, _stream_ptr(stream)))
-        return np.minimum(kl[0], kp[0], dtype=np.int32)
+        after = np.minimum(kl[0], kp[0], dtype=np.int32)
+        units, d, rows, d_rows = self.n_layers * self.n_kv_heads, self.dtype, int(co[0][-1]), int(do[0][-1])
+        kept_ = _data("kept", kept, torch.int32, units * sum(after.tolist()))
+        w, dw = _data("weights", weights, torch.float32, units * rows), _data("dst_weights", dst_weights, torch.float32, units * d_rows)
+        ck, cv = _data("cache_k", cache_k, d, self._row * rows), _data("cache_v", cache_v, d, self._row * rows)
+        dk, dv = _data("dst_k", dst_k, d, self._row * d_rows), _data("dst_v", dst_v, d, self._row * d_rows)
+        _raise(load().kvr_evict(self._h, n, co[1], kl[1], kp[1], int(n_first), int(n_recent), w, ck, cv, do[1], dk, dv, dw,
+                                kept_, KVR_EVICT_KEEP_ROTATION if keep_rotation else 0, _stream_ptr(stream)))
+        return after
 
     @property
     def attention_path(self) -> int:

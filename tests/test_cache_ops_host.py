@@ -240,3 +240,52 @@ def test_python_binding_refuses_lengths_that_are_not_integers():
         assert e.value.status == 1
     finally:
         p.close()
+
+
+def test_python_binding_refuses_tensors_that_a_call_would_leave():
+    """Another type, a strided view, too few values, pageable memory: refused by
+    name, for every tensor of the three calls."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D = 2, 2, 3, 64
+    k = torch.zeros((1, L, H, 8, D))
+    p = kvr.Pool(k, k.clone(), H * G, 1e4)
+    z = lambda n, dt=torch.float32: torch.zeros(n, dtype=dt)
+    row = L * H * D
+    shared = dict(prefix_k=z(30 * row), prefix_v=z(30 * row), q=z(3 * L * H * G * D), kq=z(3 * L * H * D), vq=z(3 * L * H * D),
+                  cache_k=z(20 * row), cache_v=z(20 * row), out=z(3 * L * H * G * D))
+    weights = dict(q=z(3 * L * H * G * D), cache_k=z(20 * row), weights=z(20 * L * H))
+    evict = dict(weights=z(20 * L * H), cache_k=z(20 * row), cache_v=z(20 * row), kept=z(9 * L * H, torch.int32), dst_k=z(12 * row),
+                 dst_v=z(12 * row), dst_weights=z(12 * L * H))
+    calls = ((shared, lambda **t: p.shared_query_attention([0, 2], [0, 30], [25], cache_offsets=[0, 10, 20], own_len=[2, 3],
+                                                           q_offsets=[0, 1, 3], stream=0, **t)),
+             (weights, lambda **t: p.key_weights([0, 10, 20], [2, 3], [0, 1, 3], stream=0, **t)),
+             (evict, lambda **t: p.evict([0, 10, 20], [8, 7], [5, 4], dst_offsets=[0, 6, 12], stream=0, **t)))
+    try:
+        for good, call in calls:
+            for name, t in good.items():
+                for bad, why in ((t.double(), "contiguous"), (torch.zeros(2 * t.numel(), dtype=t.dtype)[::2], "contiguous"),
+                                 (t[:-1].clone(), "at least")):
+                    pinned = {n: _Pinned(x) for n, x in good.items()}   # (no device here)
+                    with pytest.raises(ValueError, match=f"{name} must .*{why}"):
+                        call(**dict(pinned, **{name: _Pinned(bad)}))
+                if not t.is_pinned():
+                    with pytest.raises(ValueError, match=f"{name} must be in device or pinned"):
+                        call(**dict({n: _Pinned(x) for n, x in good.items()}, **{name: t}))
+        if _no_gpu():   # the tensors as they should be reach the library
+            for good, call in calls:
+                with pytest.raises(kvr.KvrError) as e:
+                    call(**{n: _Pinned(x) for n, x in good.items()})
+                assert e.value.status == 4
+    finally:
+        p.close()
+
+
+class _Pinned:
+    """A tensor that says it is in pinned memory."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return (lambda: True) if name == "is_pinned" else getattr(self.t, name)
