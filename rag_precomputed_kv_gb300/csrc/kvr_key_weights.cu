@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kWThreads)
                         s[r] = fmaf(sq[row0 + r][d + e], f[e], s[r]);
             }
             // rows that do not see the key: their token lies before it
-            const int r_min = (j - rq.prefix) * G - r0;
+            const int r_min = max(j - rq.prefix, 0) * G - r0;   // (a far prefix times G passes 32 bits)
 #pragma unroll
             for (int r = 0; r < kWPer; ++r)
                 s[r] = (row0 + r >= r_min && row0 + r < nr) ? s[r] * a.scale_log2 : -INFINITY;

@@ -189,3 +189,17 @@ def test_shared_prefix_writes_the_output_over_the_queries(D, dtype):
     torch.cuda.synchronize()
     pool.check()
     assert torch.equal(q, want)
+
+
+def test_key_weights_of_the_longest_cache_and_many_heads():
+    """2^24 rows, 130 query heads on one kv head: row numbers times heads pass 32
+    bits.  Every key weighs the same: 130 / 2^24, which fp32 holds exactly."""
+    import torch
+    n, G, D = 1 << 24, 130, 64
+    pool = _pool(1, 1, G, D, "bf16")
+    ck = torch.zeros((n, D), device="cuda", dtype=torch.bfloat16)
+    q, w = _randn(1, (1, 1, G, D), "bf16"), torch.empty(n, device="cuda")
+    pool.key_weights([0, n], [n - 1], [0, 1], q, ck, w)
+    torch.cuda.synchronize()
+    pool.check()
+    assert (w == G / n).all()
