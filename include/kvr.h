@@ -394,7 +394,14 @@ KVR_API kvr_status kvr_shared_query_attention(kvr_pool_t pool, int32_t n_groups,
  * the probabilities of kvr_query_attention with the same arguments, summed
  * over its query rows: after that call, with the same prefix_len, q_offsets
  * and q, the cache holds the keys these sums run over.  Queries are rotated in
- * fp32 and not rounded to the cache's type; sums are fp32.
+ * fp32 and not rounded to the cache's type; sums are fp32.  On the tensor cores
+ * (bf16, head_dim 128) a request of up to 32 query rows (tokens times G) is
+ * computed from all 24 bits of its rotated queries, one of more rows from 16: a
+ * score is then off by up to 2^-17 scale sum_i |q_i k_i|, and a probability by
+ * twice that part of itself (0.7e-7 and 3.7e-7 of the weights' norm for scores
+ * of order one; more for large scores).  Which of the two depends on the
+ * request alone; the order of a row's fp32 sums, and with it a weight's last
+ * bits, on the batch too.
  *
  *   weights  device fp32, one value per cache row: request b's block starts at
  *            element cache_offsets[b] * n_layers * n_kv_heads, inside it

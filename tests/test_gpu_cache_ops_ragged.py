@@ -203,3 +203,50 @@ def test_key_weights_of_the_longest_cache_and_many_heads():
     torch.cuda.synchronize()
     pool.check()
     assert (w == G / n).all()
+
+
+@pytest.mark.parametrize("up", [True, False])
+@pytest.mark.parametrize("q,prefix", [([12], [900]), ([60, 40], [2500, 300]), ([90], [700])])
+def test_key_weights_of_a_window_with_growing_and_falling_scores(q, prefix, up):
+    """More than 32 (and 128) query rows, keys of growing (falling) length: the
+    rows' references move in every tile, or never again.
+
+    Elementwise the bound of the other tests.  In the 2-norm: a score is off by the
+    query bits that two bf16 terms leave (independent, 2^-18 / sqrt 3 each: 17.3 *
+    2^-18 / sqrt 3 = 3.8e-5 for the longest keys' scores of deviation 17.3) and by 128
+    fp32 additions to sums of up to 64 (sqrt(128) * 64 * 2^-24 = 4.3e-5); numerator
+    and denominator: 1.2e-4, 2^-13."""
+    import oracle
+    import torch
+    from parity import to_np64
+    from test_gpu_cache_ops import THETA, _attention_ref, _block
+    L, H, G, D = 1, 2, 4, 128
+    B, LH, T = len(q), L * H, sum(q)
+    co, qo = _starts([a + b + 3 for a, b in zip(prefix, q)]), _starts(q).astype(np.int32)
+    ck = _randn(1, (int(co[-1]) * LH, D), "bf16", 1.7)
+    Q = _randn(2, (L, T, H * G, D), "bf16", 1.7)
+    for b in range(B):
+        blk = _block(ck, co, b, LH)
+        f = torch.linspace(0.01, 6.0, prefix[b] + q[b], device="cuda")
+        blk[:, :len(f)] *= (f if up else f.flip(0))[None, :, None].to(blk.dtype)
+        blk[:, len(f):] = float("nan")
+    pool, w = _pool(L, H, G, D, "bf16"), torch.full((int(co[-1]) * LH,), -1.0, device="cuda")
+    pool.key_weights(co, prefix, qo, Q, ck, w)
+    torch.cuda.synchronize()
+    pool.check()
+    e2 = n2 = 0.0
+    for b in range(B):
+        P, lq, a = prefix[b], q[b], int(qo[b])
+        n, sc = P + lq, D ** -0.5
+        got, K = to_np64(_block(w, co, b, LH)), to_np64(_block(ck, co, b, LH))
+        assert (got[:, n:] == -1).all()
+        qr = oracle.rope(to_np64(Q[:, a:a + lq]), P + np.arange(lq, dtype=np.float64)[None, :, None], THETA, False)
+        for u in range(LH):
+            _, _, qk, p = _attention_ref(K[u, :n], np.zeros((n, 1)), qr[0, :, u * G:(u + 1) * G], 0, P, sc)
+            d = qk.max(-1) * (2.0 ** -16 + (D + 8) * 2.0 ** -24)
+            ref = p.sum((0, 1))
+            bound = (p * (np.exp(2 * d)[..., None] * (1 + n * 2.0 ** -23) - 1)).sum((0, 1)) + (lq * G + 2) * 2.0 ** -24 * ref + 1e-37
+            err = np.abs(got[u, :n] - ref)
+            assert (err <= bound).all(), (b, u, float((err / bound).max()))
+            e2, n2 = e2 + (err ** 2).sum(), n2 + (ref ** 2).sum()
+    assert (e2 / n2) ** 0.5 <= 2.0 ** -13, (e2 / n2) ** 0.5
