@@ -468,6 +468,15 @@ enum { KVR_PATH_UNBOUND = -1, KVR_PATH_CUDA_CORES = 0, KVR_PATH_TCGEN05 = 1 };
  * call has bound it to a device; -2 for a NULL pool. */
 KVR_API int32_t kvr_attention_path(kvr_pool_t pool);
 
+/* Kernels of kvr_shared_query_attention (kvr_shared_path). */
+enum { KVR_SHARED_NONE = -1, KVR_SHARED_CUDA_CORES = 0, KVR_SHARED_PARTS = 1, KVR_SHARED_WHOLE = 2 };
+
+/* Which kernels the pool's last kvr_shared_query_attention that enqueued work
+ * ran: the CUDA-core kernel; on the tensor cores a prefix part and an own part
+ * that adds the partial results; or whole blocks of query rows with their own
+ * keys in one kernel.  KVR_SHARED_NONE before the first; -2 for a NULL pool. */
+KVR_API int32_t kvr_shared_path(kvr_pool_t pool);
+
 /* Timing hook.  With events non-NULL, later calls on this pool record, on the
  * caller's stream, events[0] / events[1] right before / after the assemble
  * kernel, events[2] / events[3] around the query-append kernel (nothing

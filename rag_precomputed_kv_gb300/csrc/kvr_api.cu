@@ -113,6 +113,7 @@ struct kvr_pool {
     float2 *rope_turns = nullptr;
     int *err = nullptr;       // device error word, then the shared-prefix calls' relay words
     uint32_t shared_calls = 0;   // shared-prefix calls on the tensor cores so far
+    int32_t shared_path = KVR_SHARED_NONE;   // kernels of the last shared-prefix call
     Slot slots[kSlots];
     int next = 0;
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -1423,6 +1424,7 @@ kvr_status shared_simt(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, cudaStream_t
         a.spans = reinterpret_cast<const DevSpan *>(dv + off_sp);
         a.locals = reinterpret_cast<const DevLocal *>(dv + off_lc);
     }
+    p->shared_path = KVR_SHARED_CUDA_CORES;
     p->mark(2, s);
     cudaError_t e = launch_assemble(a, p->d.dtype, D, (int)ap.size(), s, inl ? &pl.atab : nullptr);
     p->mark(3, s);
@@ -1591,6 +1593,7 @@ kvr_status shared_tc(kvr_pool *p, SharedPlan &pl, SharedArgs &sa, int32_t n_grou
     }
     SharedTcArgs t{&sa, &pl.tab, &pa, &pl.gtab, &mq, any_prefix ? &mpk : nullptr, any_prefix ? &mpv : nullptr,
                    &mk, &mv, p->n_sms, whole, few_rows, (int32_t)per_cta, (int32_t)chunks, max_own};
+    p->shared_path = whole ? KVR_SHARED_WHOLE : KVR_SHARED_PARTS;
     p->mark(2, s);
     {
         NvtxRange r("kvr.k_shared_prologue");
@@ -2068,3 +2071,5 @@ extern "C" int32_t kvr_attention_path(kvr_pool_t p)
         return KVR_PATH_UNBOUND;
     return use_tensor_cores(*p) ? KVR_PATH_TCGEN05 : KVR_PATH_CUDA_CORES;
 }
+
+extern "C" int32_t kvr_shared_path(kvr_pool_t p) { return p ? p->shared_path : -2; }

@@ -34,8 +34,9 @@ STATUS = {0: "KVR_OK", 1: "KVR_ERR_INVALID_ARG", 2: "KVR_ERR_OUT_OF_RANGE", 3: "
 EXPORTED = ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_query_attention",
             "kvr_prefill", "kvr_check", "kvr_status_string", "kvr_last_error", "kvr_attention_path",
             "kvr_set_timing_events", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
-            "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict")
+            "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict", "kvr_shared_path")
 PATH_UNBOUND, PATH_CUDA_CORES, PATH_TCGEN05 = -1, 0, 1
+SHARED_NONE, SHARED_CUDA_CORES, SHARED_PARTS, SHARED_WHOLE = -1, 0, 1, 2
 
 
 class KvrError(RuntimeError):
@@ -95,6 +96,8 @@ def load(path: str = LIB_PATH):
     lib.kvr_set_timing_events.restype = ctypes.c_int
     lib.kvr_attention_path.argtypes = [vp]
     lib.kvr_attention_path.restype = ctypes.c_int32
+    lib.kvr_shared_path.argtypes = [vp]
+    lib.kvr_shared_path.restype = ctypes.c_int32
     for name in ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_query_attention",
                  "kvr_prefill", "kvr_check", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
                  "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict"):
@@ -391,6 +394,12 @@ class Pool:
     def attention_path(self) -> int:
         """PATH_TCGEN05, PATH_CUDA_CORES, or PATH_UNBOUND before the first call."""
         return int(load().kvr_attention_path(self._h))
+
+    @property
+    def shared_path(self) -> int:
+        """Kernels of the last :meth:`shared_query_attention` that enqueued work:
+        SHARED_CUDA_CORES, SHARED_PARTS, SHARED_WHOLE, or SHARED_NONE before it."""
+        return int(load().kvr_shared_path(self._h))
 
     def set_timing_events(self, events):
         """Six torch.cuda.Event(enable_timing=True) recorded around the

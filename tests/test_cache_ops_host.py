@@ -305,3 +305,9 @@ def test_shared_tables_are_the_same_from_lists_and_arrays():
         kvr._shared_tables([0, 2], [0, 4], [4], [0, 1, 2], [1], [0, 1, 2])
     with pytest.raises((TypeError, OverflowError)):
         kvr._shared_tables([0, 1], [0, 4], [4.5], [0, 1], [1], [0, 1])
+
+
+def test_shared_path_before_any_call(lib, pool):
+    from rag_precomputed_kv_gb300 import kvr
+    assert lib.kvr_shared_path(None) == -2
+    assert lib.kvr_shared_path(pool) == kvr.SHARED_NONE

@@ -250,3 +250,72 @@ def test_key_weights_of_a_window_with_growing_and_falling_scores(q, prefix, up):
             assert (err <= bound).all(), (b, u, float((err / bound).max()))
             e2, n2 = e2 + (err ** 2).sum(), n2 + (ref ** 2).sum()
     assert (e2 / n2) ** 0.5 <= 2.0 ** -13, (e2 / n2) ** 0.5
+
+
+# what the cases of test_gpu_cache_ops.WHOLE run, whose blocks of one row are not well filled
+WHOLE_PATHS = {"two-groups": 2, "odd-heads": 2, "some-without-tokens": 2, "many-requests": 2, "one-row-blocks": 1}
+
+
+@pytest.mark.parametrize("name", WHOLE_PATHS)
+def test_which_kernels_the_cases_of_many_query_blocks_run(name):
+    from test_gpu_cache_ops import WHOLE
+    assert set(WHOLE) == set(WHOLE_PATHS)
+    c = dict(WHOLE[name])
+    pool = _shared_case(c.pop("L"), 8, c.pop("G"), 128, "bf16", check=(), **c)[0]
+    assert pool.shared_path == WHOLE_PATHS[name]
+
+
+def test_which_kernels_short_queries_run():
+    kw = dict(groups=[2], prefix=[100], own=[3, 4], check=())
+    assert _shared_case(1, 2, 2, 64, "fp32", q=[1, 1], **kw)[0].shared_path == 0
+    assert _shared_case(1, 2, 2, 128, "bf16", q=[1, 9], **kw)[0].shared_path == 1
+
+
+@pytest.mark.parametrize("own_scale", [0.02, 8.0])
+def test_shared_prefix_whole_blocks_with_moving_maxima(own_scale):
+    """Whole blocks of query rows whose prefix keys grow, and whose own keys are
+    far longer (a row's maximum moves in an own tile, which only some rows of a warp
+    see) or far shorter, against query attention on prefix and own rows in one cache.
+
+    Both round the same rotated queries and keys and each probability once, to a
+    reference of their own: with A = sum_j p_j |v_j| each is off by its output's
+    rounding, its probabilities' and n fp32 additions: 2 (2^-8 A + 2^-8 A + n 2^-23 A)
+    apart.  A comes from the rounded inputs, within 2^-7 of itself."""
+    import oracle
+    import torch
+    from parity import to_np64
+    from test_gpu_cache_ops import THETA, _attention_ref, _block
+    L, H, G, D, P, own, q = 19, 8, 4, 128, 200, [130, 60], [100, 130]
+    LH = L * H
+    pool, args, (ck0, cv0) = _shared_case(L, H, G, D, "bf16", groups=[2], prefix=[P], own=own, q=q, check=())
+    go, po, _, pk, pv, co, _, qo, Q, KQ, VQ, ck, cv, out = args
+    pk, kq = pk.clone(), KQ * own_scale
+    _block(pk, po, 0, LH)[:, :P] *= torch.linspace(0.05, 4.0, P, device="cuda")[None, :, None].to(pk.dtype)
+    ck.copy_(ck0)
+    for b in range(2):
+        _block(ck, co, b, LH)[:, :own[b]] *= own_scale
+    fo = _starts([P + a + b for a, b in zip(own, q)])
+    fk, fv = (torch.zeros((int(fo[-1]) * LH, D), device="cuda", dtype=ck.dtype) for _ in range(2))
+    for b in range(2):
+        for f, p, o in ((fk, pk, ck), (fv, pv, cv0)):
+            blk = _block(f, fo, b, LH)
+            blk[:, :P], blk[:, P:P + own[b]] = _block(p, po, 0, LH)[:, :P], _block(o, co, b, LH)[:, :own[b]]
+    pool.shared_query_attention(go, po, [P], pk, pv, co, own, qo, Q, kq, VQ, ck, cv, out)
+    assert pool.shared_path == 2
+    want = torch.empty_like(out)
+    pool.query_attention(fo, [P + a for a in own], qo, Q, kq, VQ, fk, fv, want)
+    torch.cuda.synchronize()
+    pool.check()
+    for b in range(2):
+        a, n = int(qo[b]), P + own[b] + q[b]
+        pos = P + own[b] + np.arange(q[b], dtype=np.float64)
+        qr = to_np64(torch.from_numpy(oracle.rope(to_np64(Q[:, a:a + q[b]]), pos[None, :, None], THETA, False)).to(Q.dtype))
+        K, V = to_np64(_block(fk, fo, b, LH)), to_np64(_block(fv, fo, b, LH))
+        x, y = to_np64(out[:, a:a + q[b]]), to_np64(want[:, a:a + q[b]])
+        for u in range(0, LH, 5):
+            l, h = divmod(u, H)
+            hs = slice(h * G, (h + 1) * G)
+            _, A, _, _ = _attention_ref(K[u], V[u], qr[l, :, hs], 0, P + own[b], D ** -0.5)
+            err = np.abs(x[l, :, hs] - y[l, :, hs])
+            bound = 2 * (2 * 2.0 ** -8 + n * 2.0 ** -23) * A * (1 + 2.0 ** -7)
+            assert (err <= bound).all(), (b, u, float((err / bound).max()))
