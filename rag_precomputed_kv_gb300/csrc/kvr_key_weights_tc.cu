@@ -34,7 +34,7 @@
 // panels: 128 keys x 64 dims); warp 5 the MMAs.  All waits are bounded.
 //
 // Bound by the one read of K where it is long: 4 rows, 33,281 keys, 512 units:
-// 715 us, 6.1 TB/s.  A short unit is latency: 7 rows, 2,657 keys, 112 units: 21
+// 721-745 us, 6.0-6.2 TB/s.  A short unit is latency: 7 rows, 2,657 keys, 112 units: 21
 // us a call, 3.7 TB/s (setup and rotation 4 us, then two passes and an exchange
 // that only the SM's other CTA overlaps).
 #include <cuda.h>
@@ -607,7 +607,8 @@ __global__ void __launch_bounds__(kWtThreads, 2)
 // memory is the same.  Two bf16 query terms: the weight of a key sums over all
 // the rows, which averages the 2^-17 that they leave.  Blocks of 128 rows; a
 // unit's tiles are split over a cluster only when there are too few units to
-// fill the SMs.  128 rows, 969 to 1,248 keys, 4,608 units: 483 us; the 2 x 2
+// fill the SMs.  128 rows, 969 to 1,248 keys, 4,608 units: 483 us in single
+// calls, 533-548 in runs long enough for the power cap; the 2 x 2
 // products are 340 us at the tensor rate, and a fifth of a CTA's time is setup,
 // rotation and exit, which only the SM's other CTA overlaps.  (32 rows cost it
 // 434 us on 16 requests of 1,300 keys, the kernel above 375; that one, with 128
