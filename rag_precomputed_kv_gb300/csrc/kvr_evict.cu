@@ -495,6 +495,8 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas<T, D>)
     k_evict_move(const __grid_constant__ EvictArgs a, const __grid_constant__ EvictTable rt)
 {
     const DevEvict *reqs = a.reqs ? a.reqs : rt.reqs;
+    if (a.reqs)
+        pdl_wait_prerequisites();   // (an uploaded table: promised to a grid that waited itself)
     int b, lh, c_first, c_end;
     if (a.in_place) {
         b = (int)(blockIdx.x / (unsigned)a.units);

@@ -91,3 +91,12 @@ def test_shared_prefix_kernels_read_what_they_may():
     prologue = kernel("k_shared_prologue(")
     assert prologue.index(wait) < prologue.index("relay_store(a.relay, a.call);") < prologue.index("pdl_launch_dependents();")
     assert not re.search(r"reqs\[", prologue[:prologue.index(wait)])
+
+
+def test_eviction_kernels_read_uploaded_tables_behind_their_own_wait():
+    text = _source("kvr_evict.cu")
+    for name in ("k_evict_select(", "k_evict_move(", "k_evict_unit("):
+        start = text.index("    " + name + "const __grid_constant__")
+        body = text[start:text.index("\n}\n", start)]
+        before = re.split(r"(?:if \(a\.reqs\)\s*)?pdl_wait_prerequisites\(\);", body, maxsplit=1)
+        assert len(before) == 2 and not re.search(r"reqs\)?\[", before[0]), name
