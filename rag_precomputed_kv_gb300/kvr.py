@@ -160,21 +160,23 @@ def _ints(name: str, a, code: str, n: Optional[int] = None):
 
 
 def _shared_tables(go, po, pl, co, ol, qo):
-    """`_ints` of a shared-prefix call's six tables.  Lists of the right lengths go
-    into one C array of either type (half the time of six)."""
+    """`_ints` of a shared-prefix call's six tables: (keep-alive, groups, query
+    tokens, rows of the caches, rows of the prefix or 0, the six addresses).  Lists
+    of the right lengths go into one C array of either type (half the time of six)."""
     if type(go) is type(po) is type(pl) is type(co) is type(ol) is type(qo) is list and go:
         n, b = len(go), go[-1]
         if len(pl) == n - 1 and len(po) == n and len(ol) == b and len(qo) == len(co) == b + 1:
             c32, c64 = array("i", go + pl + ol + qo), array("q", po + co)
             a32, a64 = c32.buffer_info()[0], c64.buffer_info()[0]
-            return ((go, a32, n, c32), (po, a64, n, c64), (pl, a32 + 4 * n, n - 1), (co, a64 + 8 * n, b + 1),
-                    (ol, a32 + 8 * n - 4, b), (qo, a32 + 8 * n - 4 + 4 * b, b + 1))
+            own = a32 + 8 * n - 4
+            return (c32, c64), n - 1, qo[-1], co[-1], po[-1] if any(pl) else 0, a32, a64, a32 + 4 * n, a64 + 8 * n, own, own + 4 * b
     g = _ints("group_offsets", go, "i")
     if g[2] == 0:
         raise ValueError("group_offsets must hold at least one value")
     n, b = g[2] - 1, max(0, int(g[0][-1]))   # (the library refuses a negative one)
-    return (g, _ints("prefix_offsets", po, "q", n + 1), _ints("prefix_len", pl, "i", n), _ints("cache_offsets", co, "q", b + 1),
-            _ints("own_len", ol, "i", b), _ints("q_offsets", qo, "i", b + 1))
+    t = (g, _ints("prefix_offsets", po, "q", n + 1), _ints("prefix_len", pl, "i", n), _ints("cache_offsets", co, "q", b + 1),
+         _ints("own_len", ol, "i", b), _ints("q_offsets", qo, "i", b + 1))
+    return (t, n, int(t[5][0][-1]), int(t[3][0][-1]), int(t[1][0][-1]) if any(t[2][0]) else 0, *(x[1] for x in t))
 
 
 def _data(name: str, t, dtype, n: int) -> Optional[int]:
@@ -331,19 +333,19 @@ class Pool:
         each over its group's shared prefix block (``prefix_k``, ``prefix_v``,
         read only) and the requests' own rows, to which the query K/V are
         appended; writes ``out``."""
-        go, po, pl, co, ol, qo = _shared_tables(group_offsets, prefix_offsets, prefix_len, cache_offsets, own_len, q_offsets)
-        n = go[2] - 1
-        tokens = self.n_layers * int(qo[0][-1])
+        keep, n, tokens, rows, pre, go, po, pl, co, ol, qo = _shared_tables(group_offsets, prefix_offsets, prefix_len,
+                                                                            cache_offsets, own_len, q_offsets)
         if tokens <= 0:   # nothing to do, or refused
-            pk, pv, q_, kq_, vq_, ck, cv, out_ = map(_ptr, (prefix_k, prefix_v, q, kq, vq, cache_k, cache_v, out))
+            ptrs = map(_ptr, (prefix_k, prefix_v, q, kq, vq, cache_k, cache_v, out))
         else:
-            d, rows, wide = self.dtype, self._row * int(co[0][-1]), tokens * self._wide
-            heads, pre = tokens * self._heads, self._row * int(po[0][-1]) if any(pl[0]) else 0
-            pk, pv = _data("prefix_k", prefix_k, d, pre), _data("prefix_v", prefix_v, d, pre)
-            q_, kq_, vq_ = _data("q", q, d, wide), _data("kq", kq, d, heads), _data("vq", vq, d, heads)
-            ck, cv, out_ = _data("cache_k", cache_k, d, rows), _data("cache_v", cache_v, d, rows), _data("out", out, d, wide)
-        _raise(load().kvr_shared_query_attention(self._h, n, go[1], po[1], pl[1], pk, pv, co[1], ol[1], qo[1], q_, kq_, vq_,
-                                                 ck, cv, out_, float(softmax_scale), _stream_ptr(stream)))
+            d, wide, heads = self.dtype, self._wide * self.n_layers * tokens, self._heads * self.n_layers * tokens
+            rows, pre = self._row * rows, self._row * pre
+            ptrs = (_data("prefix_k", prefix_k, d, pre), _data("prefix_v", prefix_v, d, pre), _data("q", q, d, wide),
+                    _data("kq", kq, d, heads), _data("vq", vq, d, heads), _data("cache_k", cache_k, d, rows),
+                    _data("cache_v", cache_v, d, rows), _data("out", out, d, wide))
+        pk, pv, q_, kq_, vq_, ck, cv, out_ = ptrs
+        _raise(load().kvr_shared_query_attention(self._h, n, go, po, pl, pk, pv, co, ol, qo, q_, kq_, vq_, ck, cv, out_,
+                                                 float(softmax_scale), _stream_ptr(stream)))
 
     def key_weights(self, cache_offsets, prefix_len, q_offsets, q, cache_k, weights, softmax_scale: float = 0.0,
                     accumulate: bool = False, stream=None):
@@ -380,15 +382,14 @@ class Pool:
         n = kl[2]
         kp, co = _ints("keep", keep, "i", n), _ints("cache_offsets", cache_offsets, "q", n + 1)
         do = _ints("dst_offsets", dst_offsets, "q", n + 1)
-        after = np.minimum(kl[0], kp[0], dtype=np.int32)
         units, d, rows, d_rows = self.n_layers * self.n_kv_heads, self.dtype, int(co[0][-1]), int(do[0][-1])
-        kept_ = _data("kept", kept, torch.int32, units * sum(after.tolist()))
+        kept_ = _data("kept", kept, torch.int32, units * sum(map(min, kl[0].tolist(), kp[0].tolist())))
         w, dw = _data("weights", weights, torch.float32, units * rows), _data("dst_weights", dst_weights, torch.float32, units * d_rows)
         ck, cv = _data("cache_k", cache_k, d, self._row * rows), _data("cache_v", cache_v, d, self._row * rows)
         dk, dv = _data("dst_k", dst_k, d, self._row * d_rows), _data("dst_v", dst_v, d, self._row * d_rows)
         _raise(load().kvr_evict(self._h, n, co[1], kl[1], kp[1], int(n_first), int(n_recent), w, ck, cv, do[1], dk, dv, dw,
                                 kept_, KVR_EVICT_KEEP_ROTATION if keep_rotation else 0, _stream_ptr(stream)))
-        return after
+        return np.minimum(kl[0], kp[0], dtype=np.int32)
 
     @property
     def attention_path(self) -> int:

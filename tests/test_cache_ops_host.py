@@ -293,14 +293,18 @@ class _Pinned:
 
 def test_shared_tables_are_the_same_from_lists_and_arrays():
     from rag_precomputed_kv_gb300 import kvr
-    read = lambda t, kind: np.ctypeslib.as_array((kind * t[2]).from_address(t[1])).tolist() if t[2] else []
+    read = lambda a, m, kind: np.ctypeslib.as_array((kind * m).from_address(a)).tolist() if m else []
     for tables in (([0, 2, 2, 5], [3, 10, 14, 1 << 40], [7, 0, 9], [0, 4, 9, 12, 15, 1 << 35], [1, 2, 3, 0, 5], [0, 1, 1, 4, 5, 9]),
                    ([0, 0], [0, 4], [4], [0], [], [0]), ([0], [0], [], [0], [], [0])):
         want = [list(x) for x in tables]
         for args in (tables, [np.array(x, np.int64) for x in tables], [tuple(x) for x in tables]):
-            got = kvr._shared_tables(*args)
-            assert [read(t, k) for t, k in zip(got, (ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
-                                                     ctypes.c_int32))] == want
+            keep, n, tokens, rows, pre, *addr = kvr._shared_tables(*args)
+            b = tables[0][-1]
+            assert (n, tokens, rows) == (len(tables[0]) - 1, tables[5][-1], tables[3][-1])
+            assert pre == (tables[1][-1] if any(tables[2]) else 0)
+            assert [read(a, m, k) for a, m, k in zip(addr, (n + 1, n + 1, n, b + 1, b, b + 1),
+                                                     (ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                                      ctypes.c_int32))] == want
     with pytest.raises(ValueError, match="own_len must hold 2"):
         kvr._shared_tables([0, 2], [0, 4], [4], [0, 1, 2], [1], [0, 1, 2])
     with pytest.raises((TypeError, OverflowError)):
