@@ -364,8 +364,8 @@ KVR_API kvr_status kvr_prefill(kvr_pool_t pool, int32_t batch, const int32_t *sp
  *   q_offsets, q, kq, vq, out, softmax_scale as in kvr_query_attention
  *
  * Requests without query tokens, and rows of a block behind its last query
- * row, are left as they are.  A batch of at most 64 requests passes its tables
- * inside the kernels' parameters.
+ * row, are left as they are.  A call of at most 64 requests and 64 groups passes
+ * its tables inside the kernels' parameters.
  * On a stream that is being captured the call returns KVR_ERR_UNSUPPORTED when
  * it would have to bind the pool, upload tables or use library scratch.
  * A NaN or an infinity among a request's new values may reach every query token
