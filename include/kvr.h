@@ -131,6 +131,10 @@ enum { KVR_DTYPE_BF16 = 0, KVR_DTYPE_FP32 = 1 };
  * i - r positions. */
 #define KVR_EVICT_KEEP_ROTATION 1u
 
+/* kvr_page_append flag: the keys are at their positions already (rows of a
+ * stitched prefix); they are copied bit for bit. */
+#define KVR_APPEND_TURNED 1u
+
 typedef struct kvr_pool *kvr_pool_t;
 
 /*
@@ -458,6 +462,131 @@ KVR_API kvr_status kvr_evict(kvr_pool_t pool, int32_t batch, const int64_t *cach
                              const int32_t *keep, int32_t n_first, int32_t n_recent, const float *weights,
                              const void *cache_k, const void *cache_v, const int64_t *dst_offsets, void *dst_k,
                              void *dst_v, float *dst_weights, int32_t *kept, uint32_t flags, void *stream);
+
+/*
+ * A paged cache: rows of many requests in pages of page_rows rows, in any order
+ * in memory.  Row r of request b is row r % page_rows of page
+ * table[b][r / page_rows]; that of page i, layer l, kv-head h, lies at element
+ *   i*stride[0] + l*stride[1] + h*stride[2] + (r % page_rows)*head_dim
+ * of k (and of v).  A row's number is its position.  A flat cache block
+ * [L][H_kv][R][D] is such pages too (page i: stride[0] = page_rows*head_dim,
+ * stride[1] = H_kv*R*head_dim, stride[2] = R*head_dim).
+ */
+typedef struct {
+    void *k;              /* device, 16-byte aligned */
+    void *v;
+    int64_t n_pages;
+    int32_t page_rows;    /* 1 .. 2^24 */
+    int64_t stride[3];    /* elements: page, layer, head; multiples of 16 bytes */
+} kvr_pages;
+
+/*
+ * Packed pages: rows in 4 bits (bf16 pools with head_dim 128).  Every 32 dims
+ * of a row share a scale, and a value stands for scale * code:
+ *   scale = max |x| / 7, rounded to bf16;  code = x / scale, rounded to the
+ *   nearest of -7 .. 7, halves to the even one
+ * (a group of zeros: all 0; one with a NaN or an infinity: all NaN).  Rows are
+ * packed in blocks of 32, of which a page of page_rows rows (a multiple of 32)
+ * has page_rows/32 per (layer, kv-head): [n_pages][L][H_kv][page_rows/32]
+ * blocks of 4,608 bytes (144 bytes a row for key and value, against 512), whose
+ * inside is the library's own.
+ */
+typedef struct {
+    void *data;           /* device, 16-byte aligned: n_pages * kvr_packed_page_bytes */
+    int64_t n_pages;
+} kvr_packed_pages;
+
+/* Bytes of one packed page; 0 where there are none (the pool's type, page_rows). */
+KVR_API int64_t kvr_packed_page_bytes(kvr_pool_t pool, int32_t page_rows);
+
+/*
+ * kvr_page_append -- append keys and values to a paged cache, turned to their
+ * positions (CoinRAG blog section 2.3: KV_M(q; C_ctx) follows the stitched
+ * prefix; TurboRAG blog, "Position ID").
+ *
+ * Token t of request b becomes row start[b] + t: its key is turned by
+ * start[b] + t positions (KVR_APPEND_TURNED: copied), its value copied bit for
+ * bit.  All other rows are left as they are.
+ *
+ *   table      host [batch][width] page numbers; only those of the new rows are
+ *              read.  A page that gets rows may be there once.
+ *   start      host [batch] first new row
+ *   q_offsets  host [batch+1]: request b's tokens on the token axis, T in all
+ *   k, v       device; layer l, token t, head h at element
+ *              l*stride[0] + t*stride[1] + h*stride[2]
+ *   stride     host [3] (multiples of 16 bytes), or NULL: [L][T][H_kv][D].  A
+ *              stitched block [L][H_kv][R][D] has (H_kv*R*D, D, R*D).
+ * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
+ * Errors: KVR_ERR_INVALID_ARG (also: pages that overlap each other, the new
+ * keys or the new values), KVR_ERR_OUT_OF_RANGE (a page outside the table or the
+ * pool, a row beyond 2^24), KVR_ERR_CUDA.
+ */
+KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int32_t batch, const int32_t *table,
+                                   int32_t width, const int32_t *start, const int32_t *q_offsets, const void *k,
+                                   const void *v, const int64_t *stride, uint32_t flags, void *stream);
+
+/*
+ * kvr_page_attention -- attention of query tokens over a paged cache.
+ *
+ * Query token t of request b sits at position p = q_pos[b] + t and sees row j if
+ *   j < kv_len[b], j <= p, and: window is 0, or j > p - window, or j < n_first
+ * (a sliding window, with a few first tokens that stay visible).  Its heads are
+ * turned by p;
+ *   O[l, q_offsets[b]+t, h] = sum_j softmax_j(scale * <q, k_j>) v_j
+ * over the rows that it sees, kv-head = h / (H_q / H_kv); 0 where it sees none.
+ * The call only reads the cache: append the tokens' own keys and values first
+ * (kvr_page_append).
+ *
+ *   table       host [batch][width]; only pages that hold rows some query of the
+ *               call sees are read, the others' numbers may be anything (pages
+ *               that a window left behind can be given away).  Requests may share
+ *               pages.
+ *   kv_len      host [batch] rows of the cache
+ *   q_pos       host [batch], or NULL: kv_len[b] minus the request's tokens
+ *   q_offsets, q, out, softmax_scale as in kvr_query_attention (device memory)
+ *   packed, packed_table, packed_width, packed_len   NULL, or: rows below
+ *               packed_len[b] (a multiple of 32) are read from packed pages, of
+ *               their own table; their pages in `table` are not read
+ *
+ * Rows behind kv_len, and those that no query of the request sees, have no
+ * effect, whatever they hold.  A NaN or an infinity in a value that some query
+ * token of a request sees may reach all query tokens of that request in the call
+ * (a weight of 0 times it is NaN).  On the tensor cores rotated queries and
+ * probabilities are rounded to bf16, as in kvr_query_attention.
+ * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
+ * Errors: KVR_ERR_INVALID_ARG (also: `out` overlaps the pages, or q without being
+ * the same buffer), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;
+ * kvr_check reports KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for
+ * kvr_query_attention (not for a query that sees no row).
+ */
+KVR_API kvr_status kvr_page_attention(kvr_pool_t pool, const kvr_pages *pages, int32_t batch, const int32_t *table,
+                                      int32_t width, const int32_t *kv_len, const int32_t *q_pos,
+                                      const int32_t *q_offsets, const void *q, void *out, int32_t window,
+                                      int32_t n_first, const kvr_packed_pages *packed, const int32_t *packed_table,
+                                      int32_t packed_width, const int32_t *packed_len, float softmax_scale,
+                                      void *stream);
+
+/*
+ * kvr_page_pack -- pack rows begin[b] .. end[b] - 1 of each request (multiples
+ * of 32) from its pages into its packed pages, at the same rows.  The pages are
+ * left as they are, as are the packed pages' other rows.
+ *   table, packed_table  host [batch][width], [batch][packed_width]: only pages
+ *                        of these rows are read; a packed page that gets rows may
+ *                        be there once
+ * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
+ * Errors: KVR_ERR_INVALID_ARG (also: packed pages that overlap the pages),
+ * KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED (the pool's type), KVR_ERR_CUDA.
+ */
+KVR_API kvr_status kvr_page_pack(kvr_pool_t pool, const kvr_pages *pages, int32_t batch, const int32_t *table,
+                                 int32_t width, const kvr_packed_pages *packed, const int32_t *packed_table,
+                                 int32_t packed_width, const int32_t *begin, const int32_t *end, void *stream);
+
+/* kvr_page_unpack -- the other way: scale * code, rounded to bf16, into the
+ * pages (each once in the call), for what works on bf16 rows. */
+KVR_API kvr_status kvr_page_unpack(kvr_pool_t pool, const kvr_packed_pages *packed, int32_t batch,
+                                   const int32_t *packed_table, int32_t packed_width, const kvr_pages *pages,
+                                   const int32_t *table, int32_t width, const int32_t *begin, const int32_t *end,
+                                   void *stream);
 
 /* Attention kernels a pool can select (kvr_attention_path). */
 enum { KVR_PATH_UNBOUND = -1, KVR_PATH_CUDA_CORES = 0, KVR_PATH_TCGEN05 = 1 };

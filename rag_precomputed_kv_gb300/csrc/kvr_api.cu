@@ -1995,6 +1995,451 @@ extern "C" kvr_status kvr_evict(kvr_pool_t p, int32_t batch, const int64_t *cach
 }
 
 // ---------------------------------------------------------------------------
+// paged cache
+// ---------------------------------------------------------------------------
+namespace {
+
+// One call: its requests and the page numbers that its kernels read.
+struct PagePlan {
+    std::vector<DevPageReq> rq;
+    std::vector<int32_t> ids;
+    PageTable tab;
+    PageArgs a{};
+    Slot *slot = nullptr;
+    bool inl() const { return rq.size() <= (size_t)kInlineEntries && ids.size() <= (size_t)kInlinePages; }
+};
+
+// Elements from a page pool's first element to behind its last row.
+int64_t page_extent(const kvr_pool &p, const kvr_pages &g)
+{
+    return (g.n_pages - 1) * g.stride[0] + (p.d.n_layers - 1) * g.stride[1] + (p.d.n_kv_heads - 1) * g.stride[2] +
+           (int64_t)g.page_rows * p.d.head_dim;
+}
+
+// `written`: the call writes rows, which must then not lie upon each other.
+kvr_status check_pages(const kvr_pool &p, const kvr_pages *pages, bool written)
+{
+    if (!pages)
+        return fail(KVR_ERR_INVALID_ARG, "pages is NULL");
+    const kvr_pages &g = *pages;
+    if (g.n_pages < 1 || g.n_pages > INT32_MAX || g.page_rows < 1 || g.page_rows > kMaxPosition)
+        return fail(KVR_ERR_INVALID_ARG, "n_pages %lld, page_rows %d", (long long)g.n_pages, g.page_rows);
+    if (!g.k || !g.v || !aligned16(g.k) || !aligned16(g.v))
+        return fail(KVR_ERR_INVALID_ARG, "pages: k / v NULL or not 16-byte aligned");
+    const int64_t count[3] = {g.n_pages, p.d.n_layers, p.d.n_kv_heads};
+    for (int i = 0; i < 3; ++i)
+        if (g.stride[i] < 0 || g.stride[i] % p.vec_elems() || g.stride[i] > (int64_t(1) << 58) / count[i])
+            return fail(KVR_ERR_INVALID_ARG, "pages: stride[%d] = %lld must be >= 0, a multiple of %d and within 2^58 elements", i,
+                        (long long)g.stride[i], p.vec_elems());
+    if (written) {
+        int o[3] = {0, 1, 2};
+        std::sort(o, o + 3, [&](int x, int y) { return g.stride[x] < g.stride[y]; });
+        int64_t need = (int64_t)g.page_rows * p.d.head_dim;
+        for (int i : o) {
+            if (count[i] > 1 && g.stride[i] < need)
+                return fail(KVR_ERR_INVALID_ARG, "pages: stride[%d] = %lld lays rows upon each other", i, (long long)g.stride[i]);
+            if (count[i] > 1)
+                need = (count[i] - 1) * g.stride[i] + need;
+        }
+    }
+    return KVR_OK;
+}
+
+kvr_status check_packed(const kvr_pool &p, const kvr_packed_pages *packed, int32_t page_rows)
+{
+    if (!packed)
+        return fail(KVR_ERR_INVALID_ARG, "packed is NULL");
+    if (p.d.dtype != KVR_DTYPE_BF16 || p.d.head_dim != 128)
+        return fail(KVR_ERR_UNSUPPORTED, "packed pages need a bf16 pool with head_dim 128");
+    if (!packed->data || !aligned16(packed->data))
+        return fail(KVR_ERR_INVALID_ARG, "packed: data NULL or not 16-byte aligned");
+    if (packed->n_pages < 1 || packed->n_pages > INT32_MAX)
+        return fail(KVR_ERR_INVALID_ARG, "packed: n_pages %lld", (long long)packed->n_pages);
+    if (page_rows % kPackRows)
+        return fail(KVR_ERR_INVALID_ARG, "packed pages: page_rows %d must be a multiple of %d", page_rows, kPackRows);
+    return KVR_OK;
+}
+
+int64_t packed_page_bytes(const kvr_pool &p, int32_t page_rows)
+{
+    return (int64_t)p.d.n_layers * p.d.n_kv_heads * (page_rows / kPackRows) * kPackBytes;
+}
+
+Range pages_range(const kvr_pool &p, const kvr_pages &g, bool values)
+{
+    return range_of(values ? g.v : g.k, 0, page_extent(p, g), p.elt());
+}
+Range packed_range(const kvr_pool &p, const kvr_packed_pages &k, int32_t page_rows)
+{
+    return range_of(k.data, 0, k.n_pages, packed_page_bytes(p, page_rows));
+}
+
+// Appends pages [g0, g1) of request b to the list.
+kvr_status take_pages(std::vector<int32_t> &ids, const int32_t *table, int64_t width, int b, int64_t g0, int64_t g1, int64_t n_pages,
+                      const char *what)
+{
+    if (g0 >= g1)
+        return KVR_OK;
+    if (!table)
+        return fail(KVR_ERR_INVALID_ARG, "%s table is NULL", what);
+    if (g1 > width)
+        return fail(KVR_ERR_OUT_OF_RANGE, "request %d: page %lld outside its %s table of %lld", b, (long long)(g1 - 1), what,
+                    (long long)width);
+    const int32_t *row = table + (int64_t)b * width;
+    for (int64_t g = g0; g < g1; ++g)
+        if (row[g] < 0 || row[g] >= n_pages)
+            return fail(KVR_ERR_OUT_OF_RANGE, "request %d: page %lld is %d, of %lld %s pages", b, (long long)g, row[g],
+                        (long long)n_pages, what);
+    ids.insert(ids.end(), row + g0, row + g1);
+    return KVR_OK;
+}
+
+// A page that a call writes must be in its list once.
+kvr_status check_distinct(const std::vector<int32_t> &ids, size_t from)
+{
+    std::vector<int32_t> x(ids.begin() + from, ids.end());
+    std::sort(x.begin(), x.end());
+    const auto d = std::adjacent_find(x.begin(), x.end());
+    if (d != x.end())
+        return fail(KVR_ERR_INVALID_ARG, "page %d is written for two requests, or twice for one", *d);
+    return KVR_OK;
+}
+
+void page_base(const kvr_pool &p, const kvr_pages &g, PagePlan &pl)
+{
+    PageArgs &a = pl.a;
+    a.n_reqs = (int32_t)pl.rq.size();
+    a.n_layers = p.d.n_layers;
+    a.n_q_heads = p.d.n_q_heads;
+    a.n_kv_heads = p.d.n_kv_heads;
+    a.interleaved = (p.d.flags & KVR_POOL_ROPE_INTERLEAVED) ? 1 : 0;
+    a.rope = p.rope;
+    a.err = p.err;
+    a.g.k = g.k;
+    a.g.v = g.v;
+    a.g.s_page = g.stride[0];
+    a.g.s_layer = g.stride[1];
+    a.g.s_head = g.stride[2];
+    a.g.rows = g.page_rows;
+}
+
+// The plan's tables into its kernels' parameters, or uploaded.
+kvr_status page_stage(kvr_pool *p, PagePlan &pl, cudaStream_t s)
+{
+    if (pl.inl()) {
+        std::memcpy(pl.tab.reqs, pl.rq.data(), pl.rq.size() * sizeof(DevPageReq));
+        if (!pl.ids.empty())
+            std::memcpy(pl.tab.ids, pl.ids.data(), pl.ids.size() * sizeof(int32_t));
+        return KVR_OK;
+    }
+    const size_t off = pl.rq.size() * sizeof(DevPageReq), bytes = off + pl.ids.size() * sizeof(int32_t);
+    kvr_status st;
+    if ((st = p->acquire(bytes, bytes, &pl.slot)) != KVR_OK)
+        return st;
+    char *h = static_cast<char *>(pl.slot->host);
+    std::memcpy(h, pl.rq.data(), off);
+    std::memcpy(h + off, pl.ids.data(), bytes - off);
+    const cudaError_t e = cudaMemcpyAsync(pl.slot->dev, h, bytes, cudaMemcpyHostToDevice, s);
+    cudaEventRecord(pl.slot->done, s);
+    pl.slot->used = true;
+    if (e != cudaSuccess)
+        return cuda_fail(e, "table upload");
+    pl.a.reqs = static_cast<const DevPageReq *>(pl.slot->dev);
+    pl.a.ids = reinterpret_cast<const int32_t *>(static_cast<const char *>(pl.slot->dev) + off);
+    return KVR_OK;
+}
+
+kvr_status page_ready(kvr_pool *p, const PagePlan &pl, cudaStream_t s)
+{
+    kvr_status st;
+    if ((st = check_capture(*p, s, pl.inl(), "the call uploads the tables of more than 64 requests or 1,024 pages")) != KVR_OK ||
+        (st = ensure_device(p)) != KVR_OK)
+        return st;
+    return KVR_OK;
+}
+
+// kvr_page_pack and kvr_page_unpack.
+kvr_status page_pack(kvr_pool_t p, const kvr_pages *pages, const int32_t *table, const kvr_packed_pages *packed,
+                     const int32_t *packed_table, int32_t batch, int32_t width, int32_t packed_width, const int32_t *begin,
+                     const int32_t *end, bool unpack, void *stream)
+{
+    if (!p)
+        return fail(KVR_ERR_INVALID_ARG, "pool is NULL");
+    if (batch < 0 || width < 0 || packed_width < 0)
+        return fail(KVR_ERR_INVALID_ARG, "batch %d, widths %d, %d", batch, width, packed_width);
+    NvtxRange call(unpack ? "kvr_page_unpack" : "kvr_page_pack");
+    return guarded([&]() -> kvr_status {
+        kvr_status st;
+        if ((st = check_pages(*p, pages, unpack)) != KVR_OK || (st = check_packed(*p, packed, pages->page_rows)) != KVR_OK)
+            return st;
+        if (batch > 0 && (!begin || !end))
+            return fail(KVR_ERR_INVALID_ARG, "begin / end is NULL");
+        const int32_t R = pages->page_rows;
+        PagePlan pl;
+        pl.rq.reserve(batch);
+        int64_t blocks = 0;
+        for (int b = 0; b < batch; ++b) {
+            if (begin[b] < 0 || end[b] < begin[b] || end[b] > kMaxPosition || begin[b] % kPackRows || end[b] % kPackRows)
+                return fail(KVR_ERR_INVALID_ARG, "request %d: rows %d to %d are not whole blocks of %d", b, begin[b], end[b], kPackRows);
+            DevPageReq r{};
+            r.pos0 = begin[b];
+            r.q_off = (int32_t)blocks;
+            r.q_len = (end[b] - begin[b]) / kPackRows;
+            blocks += r.q_len;
+            if (blocks > INT32_MAX)
+                return fail(KVR_ERR_OUT_OF_RANGE, "more than 2^31 blocks");
+            r.few = r.pfew = INT32_MAX;
+            pl.rq.push_back(r);
+        }
+        for (int which = 0; which < 2; ++which) {   // the pages, then the packed ones
+            const size_t from = pl.ids.size();
+            for (int b = 0; b < batch; ++b) {
+                const int64_t g0 = begin[b] / R, g1 = begin[b] < end[b] ? (end[b] + R - 1) / R : g0;
+                (which ? pl.rq[b].poff : pl.rq[b].off)[0] = (int32_t)((int64_t)pl.ids.size() - g0);
+                if ((st = which ? take_pages(pl.ids, packed_table, packed_width, b, g0, g1, packed->n_pages, "packed")
+                                : take_pages(pl.ids, table, width, b, g0, g1, pages->n_pages, "page")) != KVR_OK)
+                    return st;
+            }
+            if (which == (unpack ? 0 : 1) && (st = check_distinct(pl.ids, from)) != KVR_OK)
+                return st;
+        }
+        if (pl.ids.size() > INT32_MAX)
+            return fail(KVR_ERR_OUT_OF_RANGE, "too many pages");
+        const Range pr = packed_range(*p, *packed, R);
+        if (pr.meets(pages_range(*p, *pages, false)) || pr.meets(pages_range(*p, *pages, true)))
+            return fail(KVR_ERR_INVALID_ARG, "the packed pages overlap the pages");
+        if (blocks == 0)
+            return KVR_OK;
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if ((st = page_ready(p, pl, s)) != KVR_OK)
+            return st;
+        DeviceGuard g(p->device);
+        page_base(*p, *pages, pl);
+        pl.a.g.packed = static_cast<uint8_t *>(packed->data);
+        pl.a.g.packed_page = packed_page_bytes(*p, R);
+        if ((st = page_stage(p, pl, s)) != KVR_OK)
+            return st;
+        NvtxRange r("kvr.k_page_pack");
+        const cudaError_t e = launch_page_pack(pl.a, pl.tab, blocks, unpack, s);
+        if (pl.slot)
+            cudaEventRecord(pl.slot->done, s);
+        return e == cudaSuccess ? KVR_OK : cuda_fail(e, unpack ? "unpack launch" : "pack launch");
+    });
+}
+
+}  // namespace
+
+extern "C" int64_t kvr_packed_page_bytes(kvr_pool_t p, int32_t page_rows)
+{
+    return p && p->d.dtype == KVR_DTYPE_BF16 && p->d.head_dim == 128 && page_rows > 0 && page_rows <= kMaxPosition &&
+                   page_rows % kPackRows == 0
+               ? packed_page_bytes(*p, page_rows)
+               : 0;
+}
+
+extern "C" kvr_status kvr_page_append(kvr_pool_t p, const kvr_pages *pages, int32_t batch, const int32_t *table, int32_t width,
+                                      const int32_t *start, const int32_t *q_offsets, const void *k, const void *v,
+                                      const int64_t *stride, uint32_t flags, void *stream)
+{
+    if (!p)
+        return fail(KVR_ERR_INVALID_ARG, "pool is NULL");
+    if (batch < 0 || width < 0)
+        return fail(KVR_ERR_INVALID_ARG, "batch %d, width %d", batch, width);
+    if (flags & ~KVR_APPEND_TURNED)
+        return fail(KVR_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    NvtxRange call("kvr_page_append");
+    return guarded([&]() -> kvr_status {
+        kvr_status st;
+        if ((st = check_pages(*p, pages, true)) != KVR_OK || (st = check_offsets32(q_offsets, batch, "q_offsets")) != KVR_OK)
+            return st;
+        if (batch > 0 && !start)
+            return fail(KVR_ERR_INVALID_ARG, "start is NULL");
+        const int L = p->d.n_layers, H = p->d.n_kv_heads, D = p->d.head_dim;
+        const int32_t T = q_offsets[batch], R = pages->page_rows;
+        PagePlan pl;
+        pl.rq.reserve(batch);
+        for (int b = 0; b < batch; ++b) {
+            DevPageReq r{};
+            r.q_off = q_offsets[b];
+            r.q_len = q_offsets[b + 1] - q_offsets[b];
+            r.pos0 = start[b];
+            if (r.pos0 < 0 || (int64_t)r.pos0 + r.q_len > kMaxPosition)
+                return fail(KVR_ERR_OUT_OF_RANGE, "request %d: rows %d and %d more, of at most 2^24", b, r.pos0, r.q_len);
+            const int64_t g0 = r.pos0 / R, g1 = r.q_len > 0 ? ((int64_t)r.pos0 + r.q_len + R - 1) / R : g0;
+            r.few = INT32_MAX;
+            r.off[0] = (int32_t)((int64_t)pl.ids.size() - g0);
+            if ((st = take_pages(pl.ids, table, width, b, g0, g1, pages->n_pages, "page")) != KVR_OK)
+                return st;
+            pl.rq.push_back(r);
+        }
+        if ((st = check_distinct(pl.ids, 0)) != KVR_OK)
+            return st;
+        if (T == 0)
+            return KVR_OK;
+        if (!k || !v || !aligned16(k) || !aligned16(v))
+            return fail(KVR_ERR_INVALID_ARG, "k / v NULL or not 16-byte aligned");
+        const int64_t count[3] = {L, T, H};
+        const int64_t st3[3] = {stride ? stride[0] : (int64_t)T * H * D, stride ? stride[1] : (int64_t)H * D, stride ? stride[2] : D};
+        int64_t extent = D;
+        for (int i = 0; i < 3; ++i) {
+            if (st3[i] < 0 || st3[i] % p->vec_elems() || st3[i] > (int64_t(1) << 58) / count[i])
+                return fail(KVR_ERR_INVALID_ARG, "stride[%d] = %lld must be >= 0, a multiple of %d and within 2^58 elements", i,
+                            (long long)st3[i], p->vec_elems());
+            extent += (count[i] - 1) * st3[i];
+        }
+        const Range in[2] = {range_of(k, 0, extent, p->elt()), range_of(v, 0, extent, p->elt())};
+        for (const Range &x : in)
+            if (x.meets(pages_range(*p, *pages, false)) || x.meets(pages_range(*p, *pages, true)))
+                return fail(KVR_ERR_INVALID_ARG, "the pages overlap the new keys or values");
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if ((st = page_ready(p, pl, s)) != KVR_OK)
+            return st;
+        DeviceGuard g(p->device);
+        page_base(*p, *pages, pl);
+        PageArgs &a = pl.a;
+        a.total_q = T;
+        a.k = k;
+        a.v = v;
+        a.s_layer = st3[0];
+        a.s_tok = st3[1];
+        a.s_head = st3[2];
+        a.turned = (flags & KVR_APPEND_TURNED) ? 1 : 0;
+        if ((st = page_stage(p, pl, s)) != KVR_OK)
+            return st;
+        p->mark(2, s);
+        NvtxRange r("kvr.k_page_append");
+        const cudaError_t e = launch_page_append(a, pl.tab, p->d.dtype, D, p->n_sms, s);
+        p->mark(3, s);
+        if (pl.slot)
+            cudaEventRecord(pl.slot->done, s);
+        return e == cudaSuccess ? KVR_OK : cuda_fail(e, "page append launch");
+    });
+}
+
+extern "C" kvr_status kvr_page_pack(kvr_pool_t p, const kvr_pages *pages, int32_t batch, const int32_t *table, int32_t width,
+                                    const kvr_packed_pages *packed, const int32_t *packed_table, int32_t packed_width,
+                                    const int32_t *begin, const int32_t *end, void *stream)
+{
+    return page_pack(p, pages, table, packed, packed_table, batch, width, packed_width, begin, end, false, stream);
+}
+
+extern "C" kvr_status kvr_page_unpack(kvr_pool_t p, const kvr_packed_pages *packed, int32_t batch, const int32_t *packed_table,
+                                      int32_t packed_width, const kvr_pages *pages, const int32_t *table, int32_t width,
+                                      const int32_t *begin, const int32_t *end, void *stream)
+{
+    return page_pack(p, pages, table, packed, packed_table, batch, width, packed_width, begin, end, true, stream);
+}
+
+extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, int32_t batch, const int32_t *table, int32_t width,
+                                         const int32_t *kv_len, const int32_t *q_pos, const int32_t *q_offsets, const void *q,
+                                         void *out, int32_t window, int32_t n_first, const kvr_packed_pages *packed,
+                                         const int32_t *packed_table, int32_t packed_width, const int32_t *packed_len,
+                                         float softmax_scale, void *stream)
+{
+    if (!p)
+        return fail(KVR_ERR_INVALID_ARG, "pool is NULL");
+    if (batch < 0 || width < 0 || packed_width < 0)
+        return fail(KVR_ERR_INVALID_ARG, "batch %d, widths %d, %d", batch, width, packed_width);
+    if (window < 0 || n_first < 0)
+        return fail(KVR_ERR_INVALID_ARG, "window %d, n_first %d", window, n_first);
+    NvtxRange call("kvr_page_attention");
+    return guarded([&]() -> kvr_status {
+        kvr_status st;
+        if ((st = check_pages(*p, pages, false)) != KVR_OK || (st = check_offsets32(q_offsets, batch, "q_offsets")) != KVR_OK ||
+            (packed && (st = check_packed(*p, packed, pages->page_rows)) != KVR_OK))
+            return st;
+        if (batch > 0 && (!kv_len || (packed && !packed_len)))
+            return fail(KVR_ERR_INVALID_ARG, "kv_len / packed_len is NULL");
+        if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale))
+            return fail(KVR_ERR_INVALID_ARG, "softmax_scale %g", (double)softmax_scale);
+        const int L = p->d.n_layers, Hq = p->d.n_q_heads, D = p->d.head_dim;
+        const int32_t T = q_offsets[batch], R = pages->page_rows;
+        PagePlan pl;
+        pl.rq.reserve(batch);
+        for (int b = 0; b < batch; ++b) {
+            DevPageReq r{};
+            r.q_off = q_offsets[b];
+            r.q_len = q_offsets[b + 1] - q_offsets[b];
+            r.kv_len = kv_len[b];
+            if (r.kv_len < 0)
+                return fail(KVR_ERR_OUT_OF_RANGE, "request %d: kv_len %d", b, r.kv_len);
+            r.pos0 = q_pos ? q_pos[b] : r.kv_len - r.q_len;
+            if (r.pos0 < 0 || (int64_t)r.pos0 + r.q_len > kMaxPosition)
+                return fail(KVR_ERR_OUT_OF_RANGE, "request %d: positions %d and %d more, of at most 2^24", b, r.pos0, r.q_len);
+            if (packed) {
+                r.packed_len = packed_len[b];
+                if (r.packed_len < 0 || r.packed_len > r.kv_len || r.packed_len % kPackRows)
+                    return fail(KVR_ERR_OUT_OF_RANGE, "request %d: packed_len %d of %d rows, in whole blocks of %d", b, r.packed_len,
+                                r.kv_len, kPackRows);
+            }
+            if (r.q_len > 0) {
+                // rows that some query of the request sees: [0, few) and [lo, hi)
+                const int64_t hi = std::min<int64_t>(r.kv_len, (int64_t)r.pos0 + r.q_len);
+                const int64_t lo = std::min(hi, window > 0 ? std::max<int64_t>(0, (int64_t)r.pos0 - window + 1) : 0);
+                const int64_t few = std::min<int64_t>(n_first, lo), body = r.packed_len;
+                auto take = [&](int64_t a0, int64_t a1, int64_t b0, int64_t b1, bool pk, int32_t &nf, int32_t (&off)[2]) -> kvr_status {
+                    // pages of rows [a0, a1), then those of [b0, b1) that are not among them
+                    const int64_t p0 = a0 / R, p1 = a0 < a1 ? (a1 + R - 1) / R : p0;
+                    const int64_t q1 = b0 < b1 ? (b1 + R - 1) / R : 0, q0 = std::min(std::max(p1, b0 / R), std::max(p1, q1));
+                    nf = (int32_t)(a0 < a1 ? p1 : 0);
+                    for (int k = 0; k < 2; ++k) {
+                        const int64_t g0 = k ? q0 : p0, g1 = k ? q1 : p1;
+                        off[k] = (int32_t)((int64_t)pl.ids.size() - g0);
+                        kvr_status s2 = pk ? take_pages(pl.ids, packed_table, packed_width, b, g0, g1, packed->n_pages, "packed")
+                                           : take_pages(pl.ids, table, width, b, g0, g1, pages->n_pages, "page");
+                        if (s2 != KVR_OK)
+                            return s2;
+                    }
+                    return KVR_OK;
+                };
+                if ((st = take(body, few, std::max(lo, body), hi, false, r.few, r.off)) != KVR_OK ||
+                    (packed && (st = take(0, std::min(few, body), lo, std::min(hi, body), true, r.pfew, r.poff)) != KVR_OK))
+                    return st;
+            }
+            pl.rq.push_back(r);
+        }
+        if (pl.ids.size() > INT32_MAX)
+            return fail(KVR_ERR_OUT_OF_RANGE, "too many pages");
+        if (T == 0)
+            return KVR_OK;
+        if (!q || !out || !aligned16(q) || !aligned16(out))
+            return fail(KVR_ERR_INVALID_ARG, "q / out NULL or not 16-byte aligned");
+        const int64_t q_rows = (int64_t)L * T * Hq, row_bytes = (int64_t)D * p->elt();
+        const Range ro = range_of(out, 0, q_rows, row_bytes), rq = range_of(q, 0, q_rows, row_bytes);
+        if (ro.meets(pages_range(*p, *pages, false)) || ro.meets(pages_range(*p, *pages, true)) ||
+            (packed && ro.meets(packed_range(*p, *packed, R))))
+            return fail(KVR_ERR_INVALID_ARG, "the output overlaps the pages");
+        if (ro.meets(rq) && ro.lo != rq.lo)
+            return fail(KVR_ERR_INVALID_ARG, "the output overlaps the queries (it may only be the same buffer)");
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if ((st = page_ready(p, pl, s)) != KVR_OK)
+            return st;
+        DeviceGuard g(p->device);
+        page_base(*p, *pages, pl);
+        PageArgs &a = pl.a;
+        a.total_q = T;
+        a.q = q;
+        a.out = out;
+        a.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
+        a.window = window;
+        a.n_first = n_first;
+        if (packed) {
+            a.g.packed = static_cast<uint8_t *>(packed->data);
+            a.g.packed_page = packed_page_bytes(*p, R);
+        }
+        if ((st = page_stage(p, pl, s)) != KVR_OK)
+            return st;
+        p->mark(4, s);
+        NvtxRange r("kvr.k_page_attention");
+        const cudaError_t e = launch_page_simt(a, pl.tab, p->d.dtype, D, s);
+        p->mark(5, s);
+        if (pl.slot)
+            cudaEventRecord(pl.slot->done, s);
+        return e == cudaSuccess ? KVR_OK : cuda_fail(e, "paged attention launch");
+    });
+}
+
+// ---------------------------------------------------------------------------
 // status
 // ---------------------------------------------------------------------------
 extern "C" kvr_status kvr_check(kvr_pool_t p, void *stream)

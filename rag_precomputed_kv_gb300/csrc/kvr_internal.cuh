@@ -443,6 +443,63 @@ struct EvictArgs {
     int32_t in_place;
 };
 
+// ---- paged cache ----
+// Rows that are packed together, dims that share a scale, and the bytes of one
+// packed block of kPackRows rows (keys: codes, scales; values: codes, scales).
+constexpr int kPackRows = 32, kPackGroup = 32;
+constexpr int kPackHalf = kPackRows * 128 / 2 + kPackRows * (128 / kPackGroup) * 2;
+constexpr int kPackBytes = 2 * kPackHalf;
+static_assert(kPackBytes == 4608, "packed block layout");
+
+// Per-request data (48 bytes).  Page g of a request is entry g + off[0] of the
+// call's list of page numbers where g < few, else entry g + off[1] (a window's
+// list leaves out the pages between the first rows and the window).
+struct alignas(16) DevPageReq {
+    int32_t q_off, q_len;   // query (append: new) tokens; pack and unpack: blocks, numbered through the call
+    int32_t pos0;           // position of the first token; pack and unpack: first row
+    int32_t kv_len;         // rows that a query may see
+    int32_t packed_len;     // rows of them that are read from the packed pages
+    int32_t few, off[2];    // pages
+    int32_t pfew, poff[2];  // packed pages
+    int32_t item0;          // first work item of a unit (tensor-core kernel)
+};
+static_assert(sizeof(DevPageReq) == 48, "paged request table layout");
+constexpr int kInlinePages = 1024;
+struct PageTable {
+    DevPageReq reqs[kInlineEntries];
+    int32_t ids[kInlinePages];
+};
+// Where the rows are: row r of page i, (layer l, kv-head h), at element
+// i * s_page + l * s_layer + h * s_head + r * D.
+struct PageGeo {
+    void *k, *v;
+    int64_t s_page, s_layer, s_head;
+    int32_t rows;           // rows of a page
+    uint8_t *packed;        // or NULL: packed pages, block by block
+    int64_t packed_page;    // bytes of a packed page
+};
+struct PageArgs {
+    const DevPageReq *reqs;     // NULL: the PageTable parameter holds requests and page numbers
+    const int32_t *ids;
+    int32_t n_reqs;
+    int32_t n_layers, n_q_heads, n_kv_heads;
+    int32_t total_q;            // T
+    int32_t interleaved;
+    const float2 *rope;
+    PageGeo g;
+    // attention
+    const void *q;
+    void *out;
+    float scale_log2;
+    int32_t window, n_first;    // window 0: everything before the query
+    int *err;
+    // append
+    const void *k, *v;          // new keys and values
+    int64_t s_layer, s_tok, s_head;
+    int32_t turned;             // keys are at their positions already
+    int32_t per_cta;            // (layer, kv-head) units of a CTA
+};
+
 // ---- launchers (each returns the cudaGetLastError of its launch) ----
 cudaError_t launch_rope_tables(float2 *tab, int head_dim, double theta, cudaStream_t s);
 // `inl` (optional) carries the span and local tables; a.spans / a.locals are
@@ -529,6 +586,11 @@ cudaError_t launch_weights_tc(const WeightsArgs &a, const ReqTable &rt, const vo
 constexpr int kEvictChunk = 64;
 cudaError_t launch_rope_turns(float2 *turns, int head_dim, double theta, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, int head_dim, int n_sms, cudaStream_t s);
+// Paged cache: rotation and append; attention; rows packed, and packed rows
+// restored (bf16, head_dim 128; `n_blocks` of kPackRows rows in all).
+cudaError_t launch_page_append(const PageArgs &a, const PageTable &t, int dtype, int head_dim, int n_sms, cudaStream_t s);
+cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_page_pack(const PageArgs &a, const PageTable &t, int64_t n_blocks, bool unpack, cudaStream_t s);
 // Whether `n_sms` CTAs of the attention kernel (either variant) can be
 // resident at once as two-CTA clusters.
 bool attention_tc_pairs_fit(int n_sms);

@@ -1,0 +1,493 @@
+// kvr_page.cu -- the paged cache: rotation and append, packing to 4 bits and
+// back, and attention on the CUDA cores.
+//
+// A cache that grows token by token, or shrinks to a window, lives in pages:
+// row r of a request is row r % R of its page r / R, in any order in memory.
+// Rows are a query's positions: a token appended at row r has its key turned by
+// r (TurboRAG blog, "Position ID": contiguous positions).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kvr_page_common.cuh"
+
+namespace kvr {
+
+namespace {
+
+using namespace page;
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+constexpr int kApThreads = 128;
+
+template <typename T>
+struct Vec;   // 16 bytes of a row in fp32
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void get(const uint4 &u, float *f)
+    {
+        f[0] = __uint_as_float(u.x);
+        f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z);
+        f[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float *f)
+    {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void get(const uint4 &u, float *f)
+    {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 put(const float *f)
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// x, y: 16-byte vectors of a row's two halves; (c, s) per pair, ordered as
+// rope_pair says.
+template <typename T>
+__device__ __forceinline__ void rotate_halves(uint4 &x, uint4 &y, const float2 *cs, bool il)
+{
+    constexpr int N = Vec<T>::N;
+    float a[N], b[N];
+    Vec<T>::get(x, a);
+    Vec<T>::get(y, b);
+    if (!il) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float u = a[e], w = b[e];
+            a[e] = fmaf(u, cs[e].x, -(w * cs[e].y));
+            b[e] = fmaf(u, cs[e].y, w * cs[e].x);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+            float u = a[2 * e], w = a[2 * e + 1];
+            a[2 * e] = fmaf(u, cs[e].x, -(w * cs[e].y));
+            a[2 * e + 1] = fmaf(u, cs[e].y, w * cs[e].x);
+            u = b[2 * e], w = b[2 * e + 1];
+            b[2 * e] = fmaf(u, cs[N / 2 + e].x, -(w * cs[N / 2 + e].y));
+            b[2 * e + 1] = fmaf(u, cs[N / 2 + e].y, w * cs[N / 2 + e].x);
+        }
+    }
+    x = Vec<T>::put(a);
+    y = Vec<T>::put(b);
+}
+
+// The last request whose first token is <= t and that has tokens behind it.
+__device__ __forceinline__ int request_of(const DevPageReq *reqs, int n, int t)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (reqs[mid].q_off <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace
+
+// A group of D / 2 / N threads per token: each holds a 16-byte vector of both
+// halves of a row, its (cos, sin) once for all the units that its CTA takes.
+template <typename T, int D>
+__global__ void __launch_bounds__(kApThreads)
+    k_page_append(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t)
+{
+    constexpr int N = Vec<T>::N, kPer = D / 2 / N, kTokens = kApThreads / kPer;
+    const DevPageReq *reqs = a.reqs ? a.reqs : t.reqs;
+    const int32_t *ids = a.reqs ? a.ids : t.ids;
+    const int units = a.n_layers * a.n_kv_heads, unit_blocks = (units + a.per_cta - 1) / a.per_cta;
+    const int64_t tb = blockIdx.x / (unsigned)unit_blocks;
+    const int u0 = (int)(blockIdx.x % (unsigned)unit_blocks) * a.per_cta, u1 = min(units, u0 + a.per_cta);
+    const int j = threadIdx.x % kPer;
+    const int64_t tok = tb * kTokens + threadIdx.x / kPer;
+    if (tok >= a.total_q)
+        return;
+    const DevPageReq &rq = reqs[request_of(reqs, a.n_reqs, (int)tok)];
+    const int row = rq.pos0 + (int)(tok - rq.q_off), pg = row / a.g.rows;
+    const int64_t dst0 = (int64_t)page_id(rq, ids, pg) * a.g.s_page + (int64_t)(row - pg * a.g.rows) * D + N * j;
+    float2 cs[N];
+    const bool il = a.interleaved != 0;
+    if (!a.turned)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            cs[e] = rope_cs(a.rope, D / 2, row, rope_pair(il, D, N, j, e));
+    const T *k = static_cast<const T *>(a.k) + tok * a.s_tok + N * j, *v = static_cast<const T *>(a.v) + tok * a.s_tok + N * j;
+    T *pk = static_cast<T *>(a.g.k) + dst0, *pv = static_cast<T *>(a.g.v) + dst0;
+#pragma unroll 2
+    for (int u = u0; u < u1; ++u) {
+        const int l = u / a.n_kv_heads, h = u - l * a.n_kv_heads;
+        const int64_t src = l * a.s_layer + h * a.s_head, dst = l * a.g.s_layer + h * a.g.s_head;
+        uint4 x = *reinterpret_cast<const uint4 *>(k + src), y = *reinterpret_cast<const uint4 *>(k + src + D / 2);
+        const uint4 vx = *reinterpret_cast<const uint4 *>(v + src), vy = *reinterpret_cast<const uint4 *>(v + src + D / 2);
+        if (!a.turned)
+            rotate_halves<T>(x, y, cs, il);
+        *reinterpret_cast<uint4 *>(pk + dst) = x;
+        *reinterpret_cast<uint4 *>(pk + dst + D / 2) = y;
+        *reinterpret_cast<uint4 *>(pv + dst) = vx;
+        *reinterpret_cast<uint4 *>(pv + dst + D / 2) = vy;
+    }
+}
+
+template <typename T, int D>
+static cudaError_t append(PageArgs a, const PageTable &t, int n_sms, cudaStream_t s)
+{
+    constexpr int kTokens = kApThreads / (D / 2 / Vec<T>::N);
+    const int units = a.n_layers * a.n_kv_heads;
+    const int64_t tb = ((int64_t)a.total_q + kTokens - 1) / kTokens;
+    a.per_cta = (int32_t)std::clamp<int64_t>(tb * units / (16 * (int64_t)n_sms), 1, std::min(units, 16));
+    const int64_t grid = tb * ((units + a.per_cta - 1) / a.per_cta);
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    k_page_append<T, D><<<(unsigned)grid, kApThreads, 0, s>>>(a, t);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_page_append(const PageArgs &a, const PageTable &t, int dtype, int head_dim, int n_sms, cudaStream_t s)
+{
+    if (dtype == KVR_DTYPE_BF16)
+        return head_dim == 128 ? append<__nv_bfloat16, 128>(a, t, n_sms, s) : append<__nv_bfloat16, 64>(a, t, n_sms, s);
+    return head_dim == 128 ? append<float, 128>(a, t, n_sms, s) : append<float, 64>(a, t, n_sms, s);
+}
+
+// ---------------------------------------------------------------------------
+// packing
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kPkWarps = 4;
+
+// Eight values (dims 8 c .. 8 c + 7 of a group) as nibbles code + 8, and the scale of
+// the group, whose other values are in the other three lanes of the quad.
+// scale = bf16(max |x| / 7), code = round(x / scale), halves to even: x and scale
+// have 8 significant bits, so the fp32 quotient of a value that is not exactly
+// between two codes is at least 2^-10 away from the middle, and its rounding
+// (2^-22) changes no code.
+__device__ __forceinline__ uint32_t pack8(const uint4 &raw, uint16_t &scale_bits)
+{
+    float f[8];
+    Vec<__nv_bfloat16>::get(raw, f);
+    uint32_t top = 0;   // magnitudes as integers: a NaN or an infinity is above every number
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f));
+    const float scale = __bfloat162float(sb);
+    const bool finite = top < 0x7f800000u;
+    scale_bits = finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7fff;   // NaN
+    uint32_t w = 0x88888888u;
+    if (finite && scale > 0.f) {
+        w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float c = fminf(fmaxf(rintf(__fdiv_rn(f[e], scale)), -7.f), 7.f);
+            w |= (uint32_t)((int)c + 8) << (4 * e);
+        }
+    }
+    return w;
+}
+
+// nibbles 0..7 (dims in order) <-> the keys' order: dim 2 m at m, dim 2 m + 1 at m + 4
+__device__ __forceinline__ uint32_t spread_pairs(uint32_t w)
+{
+    uint32_t o = 0;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+        o |= ((w >> (8 * m)) & 0xfu) << (4 * m) | ((w >> (8 * m + 4)) & 0xfu) << (16 + 4 * m);
+    return o;
+}
+__device__ __forceinline__ uint32_t join_pairs(uint32_t w)
+{
+    uint32_t o = 0;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+        o |= ((w >> (4 * m)) & 0xfu) << (8 * m) | ((w >> (16 + 4 * m)) & 0xfu) << (8 * m + 4);
+    return o;
+}
+
+// Eight codes times their scale, rounded to bf16.
+__device__ __forceinline__ uint4 unpack8(uint32_t w, float scale)
+{
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = scale * (float)((int)((w >> (4 * e)) & 0xfu) - 8);
+    return Vec<__nv_bfloat16>::put(f);
+}
+
+}  // namespace
+
+// One warp: the keys or the values of one block of 32 rows.  Lane 4 n + c loads,
+// of row n of each 8, the 16 bytes 4 g + c of every group g.
+template <bool kUnpack>
+__global__ void __launch_bounds__(32 * kPkWarps)
+    k_page_pack(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t, int64_t n_items)
+{
+    const DevPageReq *reqs = a.reqs ? a.reqs : t.reqs;
+    const int32_t *ids = a.reqs ? a.ids : t.ids;
+    const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+    const int64_t item = (int64_t)blockIdx.x * kPkWarps + (threadIdx.x >> 5);
+    if (item >= n_items)
+        return;
+    const int which = (int)(item & 1), units = a.n_layers * a.n_kv_heads;
+    const int64_t blk = (item >> 1) / units;
+    const int u = (int)((item >> 1) - blk * units), l = u / a.n_kv_heads, h = u - l * a.n_kv_heads;
+    const DevPageReq &rq = reqs[request_of(reqs, a.n_reqs, (int)blk)];
+    const int row = rq.pos0 + (int)(blk - rq.q_off) * kPackRows, pg = row / a.g.rows, in = row - pg * a.g.rows;
+    __nv_bfloat16 *x = static_cast<__nv_bfloat16 *>(which ? a.g.v : a.g.k) + (int64_t)page_id(rq, ids, pg) * a.g.s_page +
+                       l * a.g.s_layer + h * a.g.s_head + (int64_t)in * 128;
+    uint8_t *p = a.g.packed + packed_block(a, rq, ids, u, row) + which * kPackHalf;
+    // the values' word of an octet's lane i (row 2 c' + i / 4 of octet c', ...) is, transposed,
+    // that of lane 4 i + c'
+    const int place = which ? 4 * (lane & 7) + (lane >> 3) : lane;
+    if constexpr (!kUnpack) {
+        uint4 raw[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                raw[i][g] = *reinterpret_cast<const uint4 *>(x + (8 * i + n) * 128 + 32 * g + 8 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+            uint16_t sc[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                w[g] = pack8(raw[i][g], sc[g]);
+                w[g] = which ? transpose_nibbles(w[g], lane) : spread_pairs(w[g]);
+            }
+            *reinterpret_cast<uint4 *>(p + 512 * i + 16 * place) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c == 0)
+                *reinterpret_cast<uint2 *>(p + 2048 + (8 * i + n) * 8) =
+                    make_uint2(sc[0] | (uint32_t)sc[1] << 16, sc[2] | (uint32_t)sc[3] << 16);
+        }
+    } else {
+        uint4 codes[4];
+        uint2 sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            codes[i] = *reinterpret_cast<const uint4 *>(p + 512 * i + 16 * place);
+            sc[i] = *reinterpret_cast<const uint2 *>(p + 2048 + (8 * i + n) * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            const uint32_t s2[2] = {sc[i].x, sc[i].y};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float scale = __uint_as_float((g & 1) ? s2[g >> 1] & 0xffff0000u : s2[g >> 1] << 16);
+                const uint32_t o = which ? transpose_nibbles(w[g], lane) : join_pairs(w[g]);
+                *reinterpret_cast<uint4 *>(x + (8 * i + n) * 128 + 32 * g + 8 * c) = unpack8(o, scale);
+            }
+        }
+    }
+}
+
+cudaError_t launch_page_pack(const PageArgs &a, const PageTable &t, int64_t n_blocks, bool unpack, cudaStream_t s)
+{
+    const int64_t items = 2 * n_blocks * a.n_layers * a.n_kv_heads, grid = (items + kPkWarps - 1) / kPkWarps;
+    if (grid == 0)
+        return cudaSuccess;
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    if (unpack)
+        k_page_pack<true><<<(unsigned)grid, 32 * kPkWarps, 0, s>>>(a, t, items);
+    else
+        k_page_pack<false><<<(unsigned)grid, 32 * kPkWarps, 0, s>>>(a, t, items);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// attention on the CUDA cores
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kSmHeads = 4;      // query heads of a CTA
+constexpr int kSmThreads = 128;
+constexpr int kSmTeams = kSmThreads / 8;
+}  // namespace
+
+// One CTA: one token, up to kSmHeads of the query heads of one kv head.  Teams of
+// 8 threads, D / 8 dims each, go through the visible keys by turns, every team
+// with its own running maximum, sum and output; they are joined at the end.
+template <typename T, int D>
+__global__ void __launch_bounds__(kSmThreads)
+    k_page_simt(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t)
+{
+    constexpr int N = D / 8, V = Vec<T>::N;   // dims of a thread: vectors 8 i + j of a row, i < N / V
+    __shared__ float qs[kSmHeads][D];
+    __shared__ float st_m[kSmTeams][kSmHeads], st_l[kSmTeams][kSmHeads];
+    __shared__ float st_o[kSmTeams][D];
+    const DevPageReq *reqs = a.reqs ? a.reqs : t.reqs;
+    const int32_t *ids = a.reqs ? a.ids : t.ids;
+    const int G = a.n_q_heads / a.n_kv_heads, hc = (G + kSmHeads - 1) / kSmHeads;
+    int64_t b = blockIdx.x;
+    const int g0 = (int)(b % hc) * kSmHeads, nh = min(kSmHeads, G - g0);
+    b /= hc;
+    const int h = (int)(b % a.n_kv_heads);
+    b /= a.n_kv_heads;
+    const int tok = (int)(b % a.total_q), l = (int)(b / a.total_q);
+    const DevPageReq &rq = reqs[request_of(reqs, a.n_reqs, tok)];
+    const int pos = rq.pos0 + tok - rq.q_off;
+    const int64_t q0 = (((int64_t)l * a.total_q + tok) * a.n_q_heads + h * G + g0) * D;
+    const T *q = static_cast<const T *>(a.q) + q0;
+    const bool il = a.interleaved != 0;
+    for (int i = threadIdx.x; i < nh * (D / 2); i += kSmThreads) {
+        const int g = i / (D / 2), pr = i % (D / 2), d0 = il ? 2 * pr : pr, d1 = il ? 2 * pr + 1 : pr + D / 2;
+        const float2 cs = rope_cs(a.rope, D / 2, pos, pr);
+        const float x = (float)q[g * D + d0], y = (float)q[g * D + d1];
+        qs[g][d0] = fmaf(x, cs.x, -(y * cs.y)) * a.scale_log2;
+        qs[g][d1] = fmaf(x, cs.y, y * cs.x) * a.scale_log2;
+    }
+    __syncthreads();
+    const int team = threadIdx.x >> 3, j = threadIdx.x & 7;
+    const Sees see = sees(a, rq, pos);
+    const int lo = min(see.lo, see.hi), few = min(see.few, see.hi), n_keys = few + see.hi - lo;
+    float qr[kSmHeads][N], o[kSmHeads][N], m[kSmHeads], ls[kSmHeads];
+#pragma unroll
+    for (int g = 0; g < kSmHeads; ++g) {
+        m[g] = -INFINITY;
+        ls[g] = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            o[g][e] = 0.f;
+            qr[g][e] = g < nh ? qs[g][(8 * (e / V) + j) * V + e % V] : 0.f;
+        }
+    }
+    const uint32_t team_mask = 0xffu << (8 * ((threadIdx.x >> 3) & 3));
+    for (int i = team; i < n_keys; i += kSmTeams) {
+        const int row = i < few ? i : lo + i - few;
+        float kf[N], vf[N];
+        if constexpr (sizeof(T) == 2 && D == 128) {
+            if (row < rq.packed_len) {
+                const int r = row % kPackRows;
+                const uint8_t *p = a.g.packed + packed_block(a, rq, ids, l * a.n_kv_heads + h, row - r);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const int d = (8 * (e / V) + j) * V + e % V, g = d / 32, x = d % 32;
+                    const uint32_t kw = *reinterpret_cast<const uint32_t *>(p + 512 * (r / 8) + 16 * (4 * (r % 8) + x / 8) + 4 * g);
+                    const uint32_t vw = *reinterpret_cast<const uint32_t *>(p + kPackHalf + 512 * (r / 8) + 16 * (4 * (x % 8) + (r % 8) / 2) + 4 * g);
+                    const int kn = (x % 8) / 2 + 4 * (x % 2), vn = x / 8 + 4 * (r % 2);
+                    const uint16_t ks = *reinterpret_cast<const uint16_t *>(p + 2048 + 8 * r + 2 * g);
+                    const uint16_t vs = *reinterpret_cast<const uint16_t *>(p + kPackHalf + 2048 + 8 * r + 2 * g);
+                    kf[e] = __uint_as_float((uint32_t)ks << 16) * (float)((int)((kw >> (4 * kn)) & 15u) - 8);
+                    vf[e] = __uint_as_float((uint32_t)vs << 16) * (float)((int)((vw >> (4 * vn)) & 15u) - 8);
+                }
+            }
+        }
+        if (sizeof(T) != 2 || D != 128 || row >= rq.packed_len) {
+            const int pg = row / a.g.rows;
+            const int64_t at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + l * a.g.s_layer + h * a.g.s_head +
+                               (int64_t)(row - pg * a.g.rows) * D;
+            const uint4 *kp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.k) + at);
+            const uint4 *vp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.v) + at);
+            uint4 kv[N / V], vv[N / V];
+#pragma unroll
+            for (int e = 0; e < N / V; ++e) {
+                kv[e] = __ldg(kp + 8 * e + j);
+                vv[e] = __ldg(vp + 8 * e + j);
+            }
+#pragma unroll
+            for (int e = 0; e < N / V; ++e) {
+                Vec<T>::get(kv[e], kf + V * e);
+                Vec<T>::get(vv[e], vf + V * e);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < kSmHeads; ++g) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                s = fmaf(qr[g][e], kf[e], s);
+            s += __shfl_xor_sync(team_mask, s, 1);
+            s += __shfl_xor_sync(team_mask, s, 2);
+            s += __shfl_xor_sync(team_mask, s, 4);
+            const float mn = fmaxf(m[g], s);
+            const float corr = mn == -INFINITY ? 1.f : exp2f(m[g] - mn), p = mn == -INFINITY ? 0.f : exp2f(s - mn);
+            m[g] = mn;
+            ls[g] = ls[g] * corr + p;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                o[g][e] = fmaf(p, vf[e], o[g][e] * corr);
+        }
+    }
+    if (j == 0) {
+#pragma unroll
+        for (int g = 0; g < kSmHeads; ++g) {
+            st_m[team][g] = m[g];
+            st_l[team][g] = ls[g];
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < kSmHeads; ++g) {
+        if (g >= nh)
+            break;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            st_o[team][(8 * (e / V) + j) * V + e % V] = o[g][e];
+        __syncthreads();
+        float M = -INFINITY, L = 0.f;
+        for (int w = 0; w < kSmTeams; ++w)
+            M = fmaxf(M, st_m[w][g]);
+        for (int d = threadIdx.x; d < D; d += kSmThreads) {
+            float x = 0.f;
+            L = 0.f;
+            for (int w = 0; w < kSmTeams; ++w) {
+                const float f = st_m[w][g] == -INFINITY ? 0.f : exp2f(st_m[w][g] - M);
+                L = fmaf(st_l[w][g], f, L);
+                x = fmaf(st_o[w][d], f, x);
+            }
+            // a row that sees no key is zero; one that does has a denominator of at least 1,
+            // or a NaN or an infinity in its query or a key
+            if (n_keys > 0 && !(L > 0.f && L < INFINITY) && d == 0)
+                atomicCAS(a.err, kDevOk, kDevBadInput);
+            T *out = static_cast<T *>(a.out) + q0 + g * D;
+            out[d] = (T)(n_keys > 0 ? x / L : 0.f);
+        }
+    }
+}
+
+template <typename T, int D>
+static cudaError_t simt(const PageArgs &a, const PageTable &t, cudaStream_t s)
+{
+    const int G = a.n_q_heads / a.n_kv_heads;
+    const int64_t grid = (int64_t)a.n_layers * a.total_q * a.n_kv_heads * ((G + kSmHeads - 1) / kSmHeads);
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidValue;
+    k_page_simt<T, D><<<(unsigned)grid, kSmThreads, 0, s>>>(a, t);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, int head_dim, cudaStream_t s)
+{
+    if (dtype == KVR_DTYPE_BF16)
+        return head_dim == 128 ? simt<__nv_bfloat16, 128>(a, t, s) : simt<__nv_bfloat16, 64>(a, t, s);
+    return head_dim == 128 ? simt<float, 128>(a, t, s) : simt<float, 64>(a, t, s);
+}
+
+}  // namespace kvr

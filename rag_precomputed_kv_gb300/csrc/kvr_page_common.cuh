@@ -1,0 +1,69 @@
+// kvr_page_common.cuh -- what the kernels of the paged cache share: page
+// look-up, which rows a query sees, and the packed rows' layout.
+//
+// A packed block holds kPackRows = 32 rows of one (layer, kv-head): keys, then
+// values, each as 2,048 bytes of 4-bit codes and 256 bytes of bf16 scales
+// [row][group of 32 dims].  A value is scale * (nibble - 8).  The codes lie as
+// the operands of mma.sync m16n8k16 want them, 512 bytes for 8 rows, 16 bytes
+// for each lane 4 n + c (n = 0..7, c = 0..3), one word per group g:
+//   keys    lane 4 n + c: row n, dims 32 g + 8 c + 0..7; nibble m holds the dim
+//           2 m, nibble m + 4 the dim 2 m + 1 (m = 0..3): a shift by 4 m and a
+//           mask leave two neighbouring dims in the two halves of the word.
+//   values  lane 4 n + c: nibbles t = 0..3 row 2 c, nibbles 4 + t row 2 c + 1, dim
+//           32 g + 8 t + n: a shift by 4 t and a mask leave two neighbouring
+//           rows' values of one dim.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kvr_internal.cuh"
+
+namespace kvr {
+namespace page {
+
+__device__ __forceinline__ int32_t page_id(const DevPageReq &r, const int32_t *ids, int pg)
+{
+    return ids[pg + (pg < r.few ? r.off[0] : r.off[1])];
+}
+__device__ __forceinline__ int32_t packed_id(const DevPageReq &r, const int32_t *ids, int pg)
+{
+    return ids[pg + (pg < r.pfew ? r.poff[0] : r.poff[1])];
+}
+
+// Rows that the query at position p sees: j < hi and (j >= lo or j < few).
+struct Sees {
+    int hi, lo, few;
+    __device__ __forceinline__ bool operator()(int j) const { return j < hi && (j >= lo || j < few); }
+};
+__device__ __forceinline__ Sees sees(const PageArgs &a, const DevPageReq &r, int p)
+{
+    Sees s;
+    s.hi = min(r.kv_len, p + 1);
+    s.lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    s.few = min(a.n_first, s.lo);
+    return s;
+}
+
+// Byte offset of packed row block `row / 32` in the packed pages.
+__device__ __forceinline__ int64_t packed_block(const PageArgs &a, const DevPageReq &r, const int32_t *ids, int lh, int row)
+{
+    const int pg = row / a.g.rows, in = row - pg * a.g.rows;
+    return (int64_t)packed_id(r, ids, pg) * a.g.packed_page + ((int64_t)lh * (a.g.rows / kPackRows) + in / kPackRows) * kPackBytes;
+}
+
+// 8x8 nibbles across the 8 lanes of an octet: lane i's nibble j becomes lane j's
+// nibble i.
+__device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane)
+{
+#pragma unroll
+    for (int b = 4; b >= 1; b >>= 1) {
+        // the halves that stay, and that change places with lane ^ b
+        const uint32_t mask = b == 4 ? 0x0000ffffu : b == 2 ? 0x00ff00ffu : 0x0f0f0f0fu;
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, w, b);
+        w = (lane & b) ? ((w & ~mask) | ((other >> (4 * b)) & mask)) : ((w & mask) | ((other << (4 * b)) & ~mask));
+    }
+    return w;
+}
+
+}  // namespace page
+}  // namespace kvr

@@ -25,6 +25,7 @@ KVR_POSITIONS_COMPOSITE = 1
 KVR_PREFILL_SKIP_PREFIX_CACHE = 2
 KVR_WEIGHTS_ACCUMULATE = 1
 KVR_EVICT_KEEP_ROTATION = 1
+KVR_APPEND_TURNED = 1
 KVR_POOL_KEYS_UNROTATED = 1
 KVR_POOL_ROPE_INTERLEAVED = 2
 
@@ -34,7 +35,8 @@ STATUS = {0: "KVR_OK", 1: "KVR_ERR_INVALID_ARG", 2: "KVR_ERR_OUT_OF_RANGE", 3: "
 EXPORTED = ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_query_attention",
             "kvr_prefill", "kvr_check", "kvr_status_string", "kvr_last_error", "kvr_attention_path",
             "kvr_set_timing_events", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
-            "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict", "kvr_shared_path")
+            "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict", "kvr_shared_path",
+            "kvr_packed_page_bytes", "kvr_page_append", "kvr_page_attention", "kvr_page_pack", "kvr_page_unpack")
 PATH_UNBOUND, PATH_CUDA_CORES, PATH_TCGEN05 = -1, 0, 1
 SHARED_NONE, SHARED_CUDA_CORES, SHARED_PARTS, SHARED_WHOLE = -1, 0, 1, 2
 
@@ -63,6 +65,15 @@ class LocalSrc(ctypes.Structure):
                 ("stride", ctypes.c_int64 * 3)]
 
 
+class PageDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_rows", ctypes.c_int32), ("stride", ctypes.c_int64 * 3)]
+
+
+class PackedDesc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -84,6 +95,12 @@ def load(path: str = LIB_PATH):
     lib.kvr_shared_query_attention.argtypes = [vp, i32] + [vp] * 14 + [ctypes.c_float, vp]
     lib.kvr_key_weights.argtypes = [vp, i32] + [vp] * 6 + [ctypes.c_float, ctypes.c_uint32, vp]
     lib.kvr_evict.argtypes = [vp, i32, vp, vp, vp, i32, i32] + [vp] * 8 + [ctypes.c_uint32, vp]
+    lib.kvr_packed_page_bytes.argtypes = [vp, i32]
+    lib.kvr_packed_page_bytes.restype = i64
+    lib.kvr_page_append.argtypes = [vp, vp, i32, vp, i32, vp, vp, vp, vp, vp, ctypes.c_uint32, vp]
+    lib.kvr_page_attention.argtypes = [vp, vp, i32, vp, i32] + [vp] * 5 + [i32, i32, vp, vp, i32, vp, ctypes.c_float, vp]
+    lib.kvr_page_pack.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, vp, vp, vp]
+    lib.kvr_page_unpack.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, vp, vp, vp]
     lib.kvr_check.argtypes = [vp, vp]
     lib.kvr_assemble_noalloc.argtypes = [ctypes.POINTER(PoolDesc), i32, vp, vp, vp, i32, vp, vp, vp, vp, vp,
                                          vp, ctypes.c_uint32, vp]
@@ -100,7 +117,8 @@ def load(path: str = LIB_PATH):
     lib.kvr_shared_path.restype = ctypes.c_int32
     for name in ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_query_attention",
                  "kvr_prefill", "kvr_check", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
-                 "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict"):
+                 "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict", "kvr_page_append", "kvr_page_attention",
+                 "kvr_page_pack", "kvr_page_unpack"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -191,6 +209,59 @@ def _data(name: str, t, dtype, n: int) -> Optional[int]:
             raise ValueError(f"{name} must hold at least {n} values, got {t.numel()}")
         raise ValueError(f"{name} must be in device or pinned host memory")
     return t.data_ptr()
+
+
+def _page_table(name: str, a, batch: int):
+    """``a`` as a C array of int32 [batch][width]: (keep-alive, address, width)."""
+    if a is None:
+        return None, None, 0
+    if hasattr(a, "is_cuda"):
+        if a.is_cuda:
+            raise ValueError(f"{name} must be in host memory")
+        if a.element_size() == 4 and not a.is_floating_point() and a.dim() == 2 and a.is_contiguous() and a.shape[0] == batch:
+            return a, a.data_ptr(), a.shape[1]
+        a = a.numpy()
+    elif not isinstance(a, np.ndarray):
+        a = [list(r) for r in a]
+        width = max(map(len, a), default=0)
+        a = np.array([r + [-1] * (width - len(r)) for r in a], np.int64).reshape(len(a), width)
+    c = np.ascontiguousarray(a, dtype=np.int32)
+    if c.ndim != 2 or c.shape[0] != batch:
+        raise ValueError(f"{name} must be [{batch}, pages], got shape {c.shape}")
+    if a.dtype != c.dtype and a.size and (a.dtype.kind not in "iu" or (a != c).any()):
+        raise ValueError(f"{name} must hold 32-bit integers")
+    return c, c.ctypes.data, c.shape[1]
+
+
+class Pages:
+    """The pages of a cache: ``k``, ``v`` ``[n_pages, layers, kv_heads, page_rows,
+    head_dim]``, of equal strides, whose rows are one behind the other (kvr_pages).
+    The tensors must outlive the calls that use them."""
+
+    def __init__(self, k, v):
+        if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype is not v.dtype:
+            raise ValueError("k and v must be alike, [n_pages, layers, kv_heads, page_rows, head_dim]")
+        if k.stride(4) != 1 or (k.shape[3] > 1 and k.stride(3) != k.shape[4]):
+            raise ValueError("the rows of a page must be contiguous")
+        if not (k.is_cuda and v.is_cuda):
+            raise ValueError("pages must be in device memory")
+        self.k, self.v = k, v
+        self.page_rows, self.shape = k.shape[3], (k.shape[1], k.shape[2], k.shape[4])
+        self._d = PageDesc(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[3], (ctypes.c_int64 * 3)(*k.stride()[:3]))
+        self._p = ctypes.addressof(self._d)
+
+
+class PackedPages:
+    """Packed pages: ``data`` ``[n_pages, bytes]`` (uint8), ``bytes`` those of
+    :meth:`Pool.packed_page_bytes` for ``page_rows`` (kvr_packed_pages)."""
+
+    def __init__(self, data, page_rows: int):
+        import torch
+        if data.dtype is not torch.uint8 or data.dim() != 2 or not data.is_contiguous() or not data.is_cuda:
+            raise ValueError("data must be a contiguous uint8 device tensor [n_pages, bytes]")
+        self.data, self.page_rows = data, int(page_rows)
+        self._d = PackedDesc(data.data_ptr(), data.shape[0])
+        self._p = ctypes.addressof(self._d)
 
 
 def _np_ptr(a: Optional[np.ndarray]):
@@ -390,6 +461,93 @@ class Pool:
         _raise(load().kvr_evict(self._h, n, co[1], kl[1], kp[1], int(n_first), int(n_recent), w, ck, cv, do[1], dk, dv, dw,
                                 kept_, KVR_EVICT_KEEP_ROTATION if keep_rotation else 0, _stream_ptr(stream)))
         return np.minimum(kl[0], kp[0], dtype=np.int32)
+
+    def _pages(self, pages: "Pages") -> int:
+        if pages.shape != (self.n_layers, self.n_kv_heads, self.head_dim) or pages.k.dtype is not self.dtype:
+            raise ValueError(f"pages of {pages.shape} (layers, kv heads, head dim), {pages.k.dtype} do not fit the pool")
+        return pages._p
+
+    def _packed(self, packed: "PackedPages", pages: "Pages") -> int:
+        if packed.page_rows != pages.page_rows:
+            raise ValueError(f"packed pages of {packed.page_rows} rows, pages of {pages.page_rows}")
+        n = self.packed_page_bytes(packed.page_rows)
+        if n and packed.data.shape[1] != n:   # (n 0: the library refuses the call)
+            raise ValueError(f"packed pages must have {n} bytes, got {packed.data.shape[1]}")
+        return packed._p
+
+    def packed_page_bytes(self, page_rows: int) -> int:
+        """kvr_packed_page_bytes: 0 where the pool's rows cannot be packed."""
+        return int(load().kvr_packed_page_bytes(self._h, int(page_rows)))
+
+    def packed_pages(self, n_pages: int, page_rows: int) -> "PackedPages":
+        """New packed pages (zeros: scales of 0) on the current device."""
+        import torch
+        n = self.packed_page_bytes(page_rows)
+        if n == 0:
+            raise ValueError("packed pages need a bf16 pool with head_dim 128 and page_rows a multiple of 32")
+        return PackedPages(torch.zeros((n_pages, n), dtype=torch.uint8, device="cuda"), page_rows)
+
+    def page_append(self, pages: "Pages", table, start, q_offsets, k, v, turned: bool = False, stream=None):
+        """kvr_page_append: token t of request b becomes row ``start[b] + t`` of
+        its pages (``table`` ``[batch, width]``, host memory), its key turned to
+        that position or, with ``turned``, copied.  ``k``, ``v``: ``[layers, T,
+        kv_heads, head_dim]``, of equal strides (a stitched block seen token by
+        token: ``block.view(L, H, R, D).transpose(1, 2)``)."""
+        qo = _ints("q_offsets", q_offsets, "i")
+        n = qo[2] - 1
+        st, tab, p = _ints("start", start, "i", n), _page_table("table", table, n), self._pages(pages)
+        tokens = int(qo[0][-1]) if n >= 0 else 0
+        for name, x in (("k", k), ("v", v)):
+            if x.dtype is not self.dtype or not x.is_cuda or x.dim() != 4:
+                raise ValueError(f"{name} must be a device tensor [layers, T, kv_heads, head_dim] of the pool's type")
+            if x.shape[0] != self.n_layers or x.shape[2:] != (self.n_kv_heads, self.head_dim) or x.shape[1] < tokens:
+                raise ValueError(f"{name} must hold {tokens} tokens of the pool's layout, got {tuple(x.shape)}")
+        s3 = k.stride()
+        if s3 != v.stride() or s3[3] != 1:
+            raise ValueError("k and v must have equal strides and contiguous rows")
+        _raise(load().kvr_page_append(self._h, p, n, tab[1], tab[2], st[1], qo[1], k.data_ptr(), v.data_ptr(),
+                                      (ctypes.c_int64 * 3)(*s3[:3]), KVR_APPEND_TURNED if turned else 0, _stream_ptr(stream)))
+
+    def page_attention(self, pages: "Pages", table, kv_len, q_offsets, q, out, q_pos=None, window: int = 0,
+                       n_first: int = 0, packed: Optional["PackedPages"] = None, packed_table=None, packed_len=None,
+                       softmax_scale: float = 0.0, stream=None):
+        """kvr_page_attention: attention of ``q`` over the paged cache, written to
+        ``out``; with ``window``, over the last ``window`` rows before each query
+        and the first ``n_first``.  ``packed``: rows below ``packed_len[b]`` are
+        read from these packed pages, through ``packed_table``."""
+        qo = _ints("q_offsets", q_offsets, "i")
+        n = qo[2] - 1
+        kl, tab, p = _ints("kv_len", kv_len, "i", n), _page_table("table", table, n), self._pages(pages)
+        qp = (None, None) if q_pos is None else _ints("q_pos", q_pos, "i", n)
+        pk, ptab, pl = None, (None, None, 0), (None, None)
+        if packed is not None:
+            if packed_len is None:
+                raise ValueError("packed goes with packed_table and packed_len")
+            pk, ptab, pl = self._packed(packed, pages), _page_table("packed_table", packed_table, n), _ints("packed_len", packed_len, "i", n)
+        elif packed_table is not None or packed_len is not None:
+            raise ValueError("packed_table and packed_len go with packed")
+        size = self.n_layers * (int(qo[0][-1]) if n >= 0 else 0) * self._wide
+        for name, x in (("q", q), ("out", out)):
+            if x is not None and not x.is_cuda:
+                raise ValueError(f"{name} must be in device memory")
+        q_, o_ = _data("q", q, self.dtype, size), _data("out", out, self.dtype, size)
+        _raise(load().kvr_page_attention(self._h, p, n, tab[1], tab[2], kl[1], qp[1], qo[1], q_, o_, int(window), int(n_first),
+                                         pk, ptab[1], ptab[2], pl[1], float(softmax_scale), _stream_ptr(stream)))
+
+    def page_pack(self, pages: "Pages", table, packed: "PackedPages", packed_table, begin, end, stream=None):
+        """kvr_page_pack: rows ``begin[b]`` .. ``end[b] - 1`` (multiples of 32) of
+        each request's pages into its packed pages."""
+        b = _ints("begin", begin, "i")
+        e, t, pt = _ints("end", end, "i", b[2]), _page_table("table", table, b[2]), _page_table("packed_table", packed_table, b[2])
+        _raise(load().kvr_page_pack(self._h, self._pages(pages), b[2], t[1], t[2], self._packed(packed, pages), pt[1], pt[2],
+                                    b[1], e[1], _stream_ptr(stream)))
+
+    def page_unpack(self, packed: "PackedPages", packed_table, pages: "Pages", table, begin, end, stream=None):
+        """kvr_page_unpack: the other way, rounded to bf16."""
+        b = _ints("begin", begin, "i")
+        e, t, pt = _ints("end", end, "i", b[2]), _page_table("table", table, b[2]), _page_table("packed_table", packed_table, b[2])
+        _raise(load().kvr_page_unpack(self._h, self._packed(packed, pages), b[2], pt[1], pt[2], self._pages(pages), t[1], t[2],
+                                      b[1], e[1], _stream_ptr(stream)))
 
     @property
     def attention_path(self) -> int:

@@ -1,0 +1,242 @@
+"""The paged cache on the CPU: every refused argument is refused with a status,
+before any GPU work; the binding's own checks; the packed format's rounding."""
+import ctypes
+from fractions import Fraction
+
+import numpy as np
+import pytest
+
+from rag_precomputed_kv_gb300 import build as B
+
+A, Bp, C, Dp, E, F = (0x10000000 * (i + 1) for i in range(6))   # far apart, aligned
+L, H, G, D = 2, 2, 4, 128
+ROW, UNIT = D, 64 * D
+TOP = 1 << 24
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    from rag_precomputed_kv_gb300 import kvr
+    return kvr.load()
+
+
+def _register(lib, dtype, d):
+    from rag_precomputed_kv_gb300 import kvr
+    desc = kvr.PoolDesc(L, H * G, H, d, dtype, 0, 4, 512, 0x10000, 0x20000, (ctypes.c_int64 * 4)(L * H * 512 * d, H * 512 * d, 512 * d, d), 1e6)
+    h = ctypes.c_void_p()
+    assert lib.kvr_pool_register(ctypes.byref(desc), ctypes.byref(h)) == 0
+    return h
+
+
+@pytest.fixture(scope="module")
+def pool(lib):
+    h = _register(lib, 0, 128)
+    yield h
+    lib.kvr_pool_unregister(h)
+
+
+@pytest.fixture(scope="module")
+def pool32(lib):
+    h = _register(lib, 1, 64)
+    yield h
+    lib.kvr_pool_unregister(h)
+
+
+def _no_gpu():
+    import torch
+    return not torch.cuda.is_available()
+
+
+def _p(x, dt=np.int32):
+    if x is None:
+        return None, None
+    a = np.ascontiguousarray(x, dt)
+    return a, a.ctypes.data_as(ctypes.c_void_p)
+
+
+def _pages(k=A, v=Bp, n=8, rows=64, stride=(L * H * UNIT, H * UNIT, UNIT)):
+    from rag_precomputed_kv_gb300 import kvr
+    return kvr.PageDesc(k, v, n, rows, (ctypes.c_int64 * 3)(*stride))
+
+
+def _packed(data=C, n=8):
+    from rag_precomputed_kv_gb300 import kvr
+    return kvr.PackedDesc(data, n)
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+BAD_PAGES = [
+    (dict(pages=None), 1), (dict(pages=dict(k=None)), 1), (dict(pages=dict(v=Bp + 8)), 1), (dict(pages=dict(n=0)), 1),
+    (dict(pages=dict(n=1 << 31)), 1), (dict(pages=dict(rows=0)), 1), (dict(pages=dict(rows=TOP + 1)), 1),
+    (dict(pages=dict(stride=(-64, H * UNIT, UNIT))), 1), (dict(pages=dict(stride=(L * H * UNIT + 4, H * UNIT, UNIT))), 1),
+    (dict(pages=dict(stride=(1 << 60, H * UNIT, UNIT))), 1),
+]
+ON_EACH_OTHER = [
+    (dict(pages=dict(stride=(0, H * UNIT, UNIT))), 1), (dict(pages=dict(stride=(L * H * UNIT, H * UNIT, UNIT - 128))), 1),
+    (dict(pages=dict(stride=(L * H * UNIT, UNIT, UNIT))), 1),
+]
+BAD_TABLE = [
+    (dict(n=-1), 1), (dict(width=-1), 1), (dict(table=None), 1), (dict(table=((8, 1), (2, 3))), 2), (dict(table=((-1, 1), (2, 3))), 2),
+]
+
+
+def append(lib, h, pages={}, table=((0, 1), (2, 3)), width=2, start=(10, 60), qo=(0, 1, 9), k=C, v=Dp, stride=None, flags=0, n=None):
+    pg = None if pages is None else _pages(**pages)
+    t, s, q, st = _p(table), _p(start), _p(qo), _p(stride, np.int64)
+    return lib.kvr_page_append(h, _ref(pg), 2 if n is None else n, t[1], width, s[1], q[1], k, v, st[1], flags, None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_PAGES + ON_EACH_OTHER + BAD_TABLE + [
+    (dict(start=None), 1), (dict(qo=None), 1), (dict(qo=(0, 2, 1)), 1), (dict(qo=(1, 2, 3)), 1), (dict(k=None), 1), (dict(v=Dp + 2), 1),
+    (dict(flags=2), 1), (dict(start=(-1, 0)), 2), (dict(start=(10, 121)), 2), (dict(start=(TOP, 0)), 2),
+    (dict(table=((0, 1), (0, 3))), 1),                       # one page, two requests
+    (dict(table=((0, 1), (2, 2))), 1),                       # twice in one
+    (dict(stride=(1024, 4, 128)), 1), (dict(stride=(-8, 256, 128)), 1), (dict(stride=(1 << 60, 256, 128)), 1),
+    (dict(k=A + 2 * UNIT), 1), (dict(v=Bp), 1),              # new rows among the pages
+])
+def test_append_refuses(lib, pool, kw, status):
+    assert append(lib, pool, **kw) == status
+    assert lib.kvr_last_error().decode()
+
+
+def test_append_with_nothing_to_do_and_pages_it_does_not_read(lib, pool):
+    assert append(lib, None) == 1
+    assert append(lib, pool, n=0, qo=(0,), start=None, table=None) == 0
+    assert append(lib, pool, qo=(0, 0, 0), k=None, v=None, table=None) == 0
+    if _no_gpu():
+        assert append(lib, pool) == 4
+        # pages without new rows are not looked at: one that another request writes, none at all
+        assert append(lib, pool, table=((0, -5), (2, 3))) == 4
+        assert append(lib, pool, start=(10, 64), table=((0, 3), (0, 3))) == 4
+        assert append(lib, pool, pages=dict(n=1, stride=(0, H * UNIT, UNIT)), table=((0, 0), (0, 0)), qo=(0, 1, 1)) == 4   # one page
+        # a flat block [L][H][256][D] as four pages
+        assert append(lib, pool, pages=dict(n=4, stride=(UNIT, H * 4 * UNIT, 4 * UNIT))) == 4
+
+
+def attend(lib, h, pages={}, table=((0, 1), (2, 3)), width=2, kv=(100, 128), pos=None, qo=(0, 1, 9), q=C, out=Dp, window=0, first=0,
+           packed=None, ptable=((0, 1), (2, 3)), pwidth=2, plen=(64, 96), scale=0.0, n=None):
+    pg = None if pages is None else _pages(**pages)
+    pk = None if packed is None else _packed(**packed)
+    t, kl, qp, qof = _p(table), _p(kv), _p(pos), _p(qo)
+    pt, pl = (_p(ptable), _p(plen)) if pk is not None else (_p(None), _p(None))
+    return lib.kvr_page_attention(h, _ref(pg), 2 if n is None else n, t[1], width, kl[1], qp[1], qof[1], q, out, window, first,
+                                  _ref(pk), pt[1], pwidth, pl[1], ctypes.c_float(scale), None)
+
+
+PACK = dict(data=E)
+
+
+@pytest.mark.parametrize("kw,status", BAD_PAGES + BAD_TABLE + [
+    (dict(kv=None), 1), (dict(kv=(-1, 5)), 2), (dict(kv=(129, 128)), 2), (dict(kv=(0, 128)), 2),   # (a token before row 0)
+    (dict(pos=(-1, 0)), 2), (dict(pos=(TOP, 0)), 2), (dict(qo=None), 1), (dict(qo=(0, 2, 1)), 1), (dict(q=None), 1),
+    (dict(q=C + 8), 1), (dict(out=None), 1), (dict(out=Dp + 2), 1), (dict(window=-1), 1), (dict(first=-1), 1),
+    (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(out=A + 64), 1), (dict(out=Bp), 1), (dict(out=C + 256), 1),
+    (dict(packed=dict(data=None)), 1), (dict(packed=dict(data=E + 8)), 1), (dict(packed=dict(data=E, n=0)), 1),
+    (dict(packed=PACK, plen=None), 1), (dict(packed=PACK, ptable=None), 1), (dict(packed=PACK, plen=(65, 0)), 2),
+    (dict(packed=PACK, plen=(-32, 0)), 2), (dict(packed=PACK, plen=(128, 0)), 2), (dict(packed=PACK, ptable=((0, 8), (2, 8))), 2),
+    (dict(packed=PACK, pwidth=0), 2), (dict(packed=PACK, pages=dict(rows=48)), 1), (dict(packed=dict(data=Dp)), 1),
+])
+def test_attention_refuses(lib, pool, kw, status):
+    assert attend(lib, pool, **kw) == status
+    assert lib.kvr_last_error().decode()
+
+
+def test_attention_with_nothing_to_do_and_pages_it_does_not_read(lib, pool, pool32):
+    assert attend(lib, None) == 1
+    assert attend(lib, pool, n=0, qo=(0,), kv=None, table=None) == 0
+    assert attend(lib, pool, qo=(0, 0, 0), q=None, out=None, table=None) == 0
+    assert attend(lib, pool32, packed=PACK, pages=dict(stride=(L * H * 64 * 64, H * 64 * 64, 64 * 64))) == 3   # fp32: not packed
+    if _no_gpu():
+        assert attend(lib, pool) == 4
+        assert attend(lib, pool, out=C) == 4                                                   # in place
+        assert attend(lib, pool, table=((0, 0), (0, 0))) == 4                                  # shared pages
+        assert attend(lib, pool, kv=(0, 0), pos=(0, 7), table=None) == 4                       # nothing to see
+        assert attend(lib, pool, window=36, table=((-1, 1), (7, 7))) == 4                      # rows 64 .. 99; 84 .. 127
+        assert attend(lib, pool, window=37, table=((-1, 1), (7, 7))) == 2
+        assert attend(lib, pool, window=30, first=1, table=((-1, 1), (7, 7))) == 2
+        assert attend(lib, pool, packed=PACK, table=((-1, 1), (-1, 3))) == 4                   # rows 0 .. 63 are packed
+        assert attend(lib, pool, packed=PACK, plen=(32, 96), table=((-1, 1), (-1, 3))) == 2
+        assert attend(lib, pool, pages=dict(stride=(0, 0, 0))) == 4                            # read only: rows may be shared
+
+
+def pack(lib, h, pages={}, table=((0, 1), (2, 3)), width=2, packed={}, ptable=((0, 1), (2, 3)), pwidth=2, begin=(0, 32), end=(64, 96),
+         n=None, unpack=False):
+    pg = None if pages is None else _pages(**pages)
+    pk = None if packed is None else _packed(**packed)
+    t, pt, b, e = _p(table), _p(ptable), _p(begin), _p(end)
+    n = 2 if n is None else n
+    if unpack:
+        return lib.kvr_page_unpack(h, _ref(pk), n, pt[1], pwidth, _ref(pg), t[1], width, b[1], e[1], None)
+    return lib.kvr_page_pack(h, _ref(pg), n, t[1], width, _ref(pk), pt[1], pwidth, b[1], e[1], None)
+
+
+@pytest.mark.parametrize("unpack", [False, True])
+@pytest.mark.parametrize("kw,status", BAD_PAGES + BAD_TABLE + [
+    (dict(packed=None), 1), (dict(packed=dict(data=None)), 1), (dict(packed=dict(data=C + 8)), 1), (dict(packed=dict(n=0)), 1),
+    (dict(pages=dict(rows=40)), 1), (dict(pwidth=-1), 1), (dict(ptable=None), 1), (dict(ptable=((9, 1), (2, 3))), 2),
+    (dict(begin=None), 1), (dict(end=None), 1), (dict(begin=(1, 32)), 1), (dict(end=(33, 96)), 1), (dict(end=(64, 0)), 1),
+    (dict(begin=(-32, 0)), 1), (dict(end=(160, 96)), 2), (dict(end=(TOP + 32, 96)), 1), (dict(packed=dict(data=A)), 1),
+    (dict(packed=dict(data=Bp + 4608)), 1),
+])
+def test_pack_refuses(lib, pool, kw, status, unpack):
+    assert pack(lib, pool, unpack=unpack, **kw) == status
+    assert lib.kvr_last_error().decode()
+
+
+def test_pack_writes_each_page_once(lib, pool, pool32):
+    twice = ((0, 1), (0, 3))
+    assert pack(lib, pool, ptable=twice) == 1 and pack(lib, pool, table=twice, unpack=True) == 1
+    for kw, status in ON_EACH_OTHER:
+        assert pack(lib, pool, unpack=True, **kw) == status
+    assert pack(lib, None) == 1 and pack(lib, pool, n=0) == 0 and pack(lib, pool, begin=(0, 32), end=(0, 32), table=None, ptable=None) == 0
+    assert pack(lib, pool32, pages=dict(stride=(L * H * 64 * 64, H * 64 * 64, 64 * 64))) == 3
+    if _no_gpu():
+        assert pack(lib, pool) == 4 and pack(lib, pool, unpack=True) == 4
+        assert pack(lib, pool, table=twice) == 4 and pack(lib, pool, ptable=twice, unpack=True) == 4   # read twice
+
+
+def test_packed_page_bytes(lib, pool, pool32):
+    assert lib.kvr_packed_page_bytes(pool, 64) == L * H * 2 * 4608
+    assert [lib.kvr_packed_page_bytes(pool, r) for r in (0, -32, 33, TOP + 32)] == [0] * 4
+    assert lib.kvr_packed_page_bytes(pool32, 64) == 0 and lib.kvr_packed_page_bytes(None, 64) == 0
+
+
+def test_no_code_depends_on_how_the_quotient_is_rounded():
+    """x and the scale have 8 significant bits: a quotient that is not exactly
+    between two codes is at least 2^-10 away from the middle, whatever the exponents."""
+    gap = Fraction(1)
+    for b in range(128, 256):
+        for a in range(128, 256):
+            for d in range(-4, 4):
+                x = Fraction(a, b) * Fraction(2) ** d
+                if x <= 8:
+                    away = abs(x - (x - Fraction(1, 2)).__round__() - Fraction(1, 2))
+                    if away:
+                        gap = min(gap, away)
+    assert gap >= Fraction(1, 1024)
+
+
+def test_binding_checks():
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    t = torch.zeros((2, 3), dtype=torch.int32)
+    assert kvr._page_table("t", t, 2)[1:] == (t.data_ptr(), 3)                     # as it is
+    assert kvr._page_table("t", [[1, 2], [3]], 2)[0].tolist() == [[1, 2], [3, -1]]
+    assert kvr._page_table("t", t[:, :2], 2)[0].tolist() == [[0, 0], [0, 0]]
+    assert kvr._page_table("t", None, 2) == (None, None, 0)
+    assert kvr._page_table("t", [], 0)[2] == 0
+    for bad, n in ((t, 3), (t[0], 2), (np.zeros((2, 2)) + 0.5, 2), (np.full((1, 1), 1 << 40), 1)):
+        with pytest.raises(ValueError):
+            kvr._page_table("t", bad, n)
+    k = torch.zeros((2, 1, 2, 16, 64))
+    for a, b in ((k, k[:1]), (k, k.bfloat16()), (k[0], k[0]), (k.transpose(3, 4), k.transpose(3, 4)), (k[..., :32], k[..., :32]), (k, k)):
+        with pytest.raises(ValueError):   # (the last: host memory)
+            kvr.Pages(a, b)
+    for d in (torch.zeros(4, dtype=torch.uint8), torch.zeros((2, 4)), torch.zeros((2, 4), dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            kvr.PackedPages(d, 32)
