@@ -2158,6 +2158,54 @@ kvr_status page_ready(kvr_pool *p, const PagePlan &pl, cudaStream_t s)
     return KVR_OK;
 }
 
+// The tensor-core kernel's items: 256-row blocks of the requests of more than
+// kPageFewRows query rows, each in `splits` stretches of its key tiles.
+kvr_status page_tc_plan(const kvr_pool *p, PagePlan &pl, const kvr_pages &g, int32_t window, int32_t n_first, PageTcArgs &tc)
+{
+    const int D = p->d.head_dim, G = p->d.n_q_heads / p->d.n_kv_heads;
+    const int64_t units = (int64_t)p->d.n_layers * p->d.n_kv_heads;
+    // boxes of the largest power of two of rows that no page boundary cuts
+    tc.box = 128;
+    while (g.page_rows % tc.box)
+        tc.box /= 2;
+    if (tc.box < 16 || g.stride[0] % D || g.stride[1] % D || g.stride[2] % D || page_extent(*p, g) / D > (int64_t)INT32_MAX - 256)
+        tc.box = 0;
+    int64_t blocks = 0, tiles = 0;
+    for (const DevPageReq &r : pl.rq) {
+        if (r.q_len * (int64_t)G <= kPageFewRows)
+            continue;
+        if (r.q_len * (int64_t)G > INT32_MAX - 256)
+            return fail(KVR_ERR_UNSUPPORTED, "too many query rows");
+        const int64_t n = (r.q_len * (int64_t)G + 255) / 256, hi = std::min<int64_t>(r.kv_len, (int64_t)r.pos0 + r.q_len);
+        const int64_t seen = window > 0 ? std::min<int64_t>(hi, (int64_t)window + n_first + 256 / G) : hi;
+        blocks += n;
+        tiles += n * ((seen + 127) / 128);
+    }
+    // The time of a call in units of a key tile (1.45 us): rounds of items, each its tiles
+    // and 3 more, and for partial results 4 more and their traffic (266 KB an item).
+    const double nt = (double)tiles / (double)std::max<int64_t>(1, blocks);
+    double best = 1e30;
+    for (int sp = 1; sp <= 32 && (sp == 1 || nt / sp >= 4.); ++sp) {
+        const double items = (double)(blocks * units) * sp;
+        const double t = std::ceil(items / p->n_sms) * (nt / sp + 3.) + (sp > 1 ? 4. + items * 266e3 / 6e6 / 1.45 : 0.);
+        if (t < 0.97 * best) {
+            best = t;
+            tc.splits = sp;
+        }
+    }
+    if (blocks * tc.splits > INT32_MAX)
+        return fail(KVR_ERR_UNSUPPORTED, "too many query rows");
+    int32_t item = 0;
+    for (DevPageReq &r : pl.rq) {
+        r.item0 = item;
+        if (r.q_len * (int64_t)G > kPageFewRows)
+            item += (int32_t)((r.q_len * (int64_t)G + 255) / 256) * tc.splits;
+    }
+    tc.unit_items = item;
+    tc.total = item * units;
+    return KVR_OK;
+}
+
 // kvr_page_pack and kvr_page_unpack.
 kvr_status page_pack(kvr_pool_t p, const kvr_pages *pages, const int32_t *table, const kvr_packed_pages *packed,
                      const int32_t *packed_table, int32_t batch, int32_t width, int32_t packed_width, const int32_t *begin,
@@ -2412,9 +2460,39 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
         if (ro.meets(rq) && ro.lo != rq.lo)
             return fail(KVR_ERR_INVALID_ARG, "the output overlaps the queries (it may only be the same buffer)");
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if ((st = page_ready(p, pl, s)) != KVR_OK)
+        const bool tensor = attention_tc_supported(p->d.dtype, D);
+        const int G = Hq / p->d.n_kv_heads;
+        bool few = false, many = false;   // requests for the kernel of few query rows, and for that of more
+        for (const DevPageReq &r : pl.rq) {
+            few = few || (r.q_len > 0 && r.q_len * (int64_t)G <= kPageFewRows);
+            many = many || (tensor && r.q_len * (int64_t)G > kPageFewRows);
+        }
+        if ((st = check_capture(*p, s, pl.inl() && !many, "the call uses library scratch (a request of more than 16 query rows), or "
+                                                          "uploads the tables of more than 64 requests or 1,024 pages")) != KVR_OK ||
+            (st = ensure_device(p)) != KVR_OK)
             return st;
         DeviceGuard g(p->device);
+        PageTcArgs tc{};
+        CUtensorMap mq, mk, mv;
+        if (many) {
+            if (!use_tensor_cores(*p))
+                return fail(KVR_ERR_UNSUPPORTED, "more than 16 query rows need the tensor-core kernel (sm_103)");
+            if (q_rows > (int64_t)INT32_MAX - 256)
+                return fail(KVR_ERR_UNSUPPORTED, "query rows exceed the int32 TMA coordinate range");
+            if ((st = page_tc_plan(p, pl, *pages, window, n_first, tc)) != KVR_OK || (st = p->grow_query_scratch((size_t)(q_rows * D) * 2)) != KVR_OK ||
+                (tc.splits > 1 && (st = p->grow_part_scratch((size_t)(tc.total * kPagePartBytes))) != KVR_OK) ||
+                (st = encode_rows_map(*p, p->q_rot, q_rows, 128, &mq)) != KVR_OK)
+                return st;
+            tc.part = static_cast<float *>(p->part);
+            const int64_t rows = page_extent(*p, *pages) / D;
+            if (tc.box && ((st = encode_rows_map(*p, pages->k, rows, tc.box, &mk)) != KVR_OK ||
+                           (st = encode_rows_map(*p, pages->v, rows, tc.box, &mv)) != KVR_OK))
+                return st;
+            // the previous call's attention must be done with the scratch
+            cudaError_t e;
+            if (p->q_rot_used && (e = cudaStreamWaitEvent(s, p->q_rot_done, 0)) != cudaSuccess)
+                return cuda_fail(e, "query scratch ordering");
+        }
         page_base(*p, *pages, pl);
         PageArgs &a = pl.a;
         a.total_q = T;
@@ -2431,7 +2509,14 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
             return st;
         p->mark(4, s);
         NvtxRange r("kvr.k_page_attention");
-        const cudaError_t e = launch_page_simt(a, pl.tab, p->d.dtype, D, s);
+        cudaError_t e = few && tensor ? launch_page_decode(a, pl.tab, pl.rq.data(), p->n_sms, s) : cudaSuccess;
+        if (e == cudaSuccess && !tensor)
+            e = launch_page_simt(a, pl.tab, p->d.dtype, D, s);
+        if (e == cudaSuccess && many) {
+            e = launch_page_tc(a, tc, pl.tab, p->q_rot, &mq, tc.box ? &mk : &mq, tc.box ? &mv : &mq, p->n_sms, s);
+            cudaEventRecord(p->q_rot_done, s);
+            p->q_rot_used = true;
+        }
         p->mark(5, s);
         if (pl.slot)
             cudaEventRecord(pl.slot->done, s);

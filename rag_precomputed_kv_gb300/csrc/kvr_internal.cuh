@@ -500,6 +500,17 @@ struct PageArgs {
     int32_t per_cta;            // (layer, kv-head) units of a CTA
 };
 
+// The tensor-core kernel of the paged attention: one (unit, request, 256-row block
+// of its query rows, stretch of its key tiles) an item.
+constexpr int64_t kPagePartBytes = 256 * 128 * 4 + 256 * 8;
+struct PageTcArgs {
+    int64_t total;          // items
+    int32_t unit_items;     // of one (layer, kv-head)
+    int32_t splits;         // stretches of a block
+    int32_t box;            // rows of a TMA box of the pages; 0: no tile is loaded by TMA
+    float *part;            // splits > 1: total partial results
+};
+
 // ---- launchers (each returns the cudaGetLastError of its launch) ----
 cudaError_t launch_rope_tables(float2 *tab, int head_dim, double theta, cudaStream_t s);
 // `inl` (optional) carries the span and local tables; a.spans / a.locals are
@@ -590,6 +601,12 @@ cudaError_t launch_evict(const EvictArgs &a, const EvictTable &rt, int dtype, in
 // restored (bf16, head_dim 128; `n_blocks` of kPackRows rows in all).
 cudaError_t launch_page_append(const PageArgs &a, const PageTable &t, int dtype, int head_dim, int n_sms, cudaStream_t s);
 cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, int head_dim, cudaStream_t s);
+// Query rows (tokens times query heads of a kv head) of a request up to which k_page_decode
+// takes it; `host_reqs` is the host's copy of the request table.
+constexpr int kPageFewRows = 16;
+cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevPageReq *host_reqs, int n_sms, cudaStream_t s);
+cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTable &t, void *q_rot, const void *tmap_q,
+                           const void *tmap_k, const void *tmap_v, int n_sms, cudaStream_t s);
 cudaError_t launch_page_pack(const PageArgs &a, const PageTable &t, int64_t n_blocks, bool unpack, cudaStream_t s);
 // Whether `n_sms` CTAs of the attention kernel (either variant) can be
 // resident at once as two-CTA clusters.

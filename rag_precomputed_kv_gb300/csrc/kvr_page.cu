@@ -382,40 +382,21 @@ __global__ void __launch_bounds__(kSmThreads)
     for (int i = team; i < n_keys; i += kSmTeams) {
         const int row = i < few ? i : lo + i - few;
         float kf[N], vf[N];
-        if constexpr (sizeof(T) == 2 && D == 128) {
-            if (row < rq.packed_len) {
-                const int r = row % kPackRows;
-                const uint8_t *p = a.g.packed + packed_block(a, rq, ids, l * a.n_kv_heads + h, row - r);
+        const int pg = row / a.g.rows;
+        const int64_t at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + l * a.g.s_layer + h * a.g.s_head +
+                           (int64_t)(row - pg * a.g.rows) * D;
+        const uint4 *kp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.k) + at);
+        const uint4 *vp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.v) + at);
+        uint4 kv[N / V], vv[N / V];
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const int d = (8 * (e / V) + j) * V + e % V, g = d / 32, x = d % 32;
-                    const uint32_t kw = *reinterpret_cast<const uint32_t *>(p + 512 * (r / 8) + 16 * (4 * (r % 8) + x / 8) + 4 * g);
-                    const uint32_t vw = *reinterpret_cast<const uint32_t *>(p + kPackHalf + 512 * (r / 8) + 16 * (4 * (x % 8) + (r % 8) / 2) + 4 * g);
-                    const int kn = (x % 8) / 2 + 4 * (x % 2), vn = x / 8 + 4 * (r % 2);
-                    const uint16_t ks = *reinterpret_cast<const uint16_t *>(p + 2048 + 8 * r + 2 * g);
-                    const uint16_t vs = *reinterpret_cast<const uint16_t *>(p + kPackHalf + 2048 + 8 * r + 2 * g);
-                    kf[e] = __uint_as_float((uint32_t)ks << 16) * (float)((int)((kw >> (4 * kn)) & 15u) - 8);
-                    vf[e] = __uint_as_float((uint32_t)vs << 16) * (float)((int)((vw >> (4 * vn)) & 15u) - 8);
-                }
-            }
+        for (int e = 0; e < N / V; ++e) {
+            kv[e] = __ldg(kp + 8 * e + j);
+            vv[e] = __ldg(vp + 8 * e + j);
         }
-        if (sizeof(T) != 2 || D != 128 || row >= rq.packed_len) {
-            const int pg = row / a.g.rows;
-            const int64_t at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + l * a.g.s_layer + h * a.g.s_head +
-                               (int64_t)(row - pg * a.g.rows) * D;
-            const uint4 *kp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.k) + at);
-            const uint4 *vp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.v) + at);
-            uint4 kv[N / V], vv[N / V];
 #pragma unroll
-            for (int e = 0; e < N / V; ++e) {
-                kv[e] = __ldg(kp + 8 * e + j);
-                vv[e] = __ldg(vp + 8 * e + j);
-            }
-#pragma unroll
-            for (int e = 0; e < N / V; ++e) {
-                Vec<T>::get(kv[e], kf + V * e);
-                Vec<T>::get(vv[e], vf + V * e);
-            }
+        for (int e = 0; e < N / V; ++e) {
+            Vec<T>::get(kv[e], kf + V * e);
+            Vec<T>::get(vv[e], vf + V * e);
         }
 #pragma unroll
         for (int g = 0; g < kSmHeads; ++g) {
@@ -485,8 +466,8 @@ static cudaError_t simt(const PageArgs &a, const PageTable &t, cudaStream_t s)
 
 cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, int head_dim, cudaStream_t s)
 {
-    if (dtype == KVR_DTYPE_BF16)
-        return head_dim == 128 ? simt<__nv_bfloat16, 128>(a, t, s) : simt<__nv_bfloat16, 64>(a, t, s);
+    if (dtype == KVR_DTYPE_BF16)   // (head_dim 128: the tensor-core kernels)
+        return head_dim == 64 ? simt<__nv_bfloat16, 64>(a, t, s) : cudaErrorInvalidValue;
     return head_dim == 128 ? simt<float, 128>(a, t, s) : simt<float, 64>(a, t, s);
 }
 

@@ -1,0 +1,809 @@
+// kvr_page_tc.cu -- attention of many query rows over a paged cache, on the
+// tensor cores (bf16, head_dim 128).
+//
+// The G query heads of a kv head are packed into the rows (row = token * G + g), as
+// in the query prefill; a request's rows of one (layer, kv-head) meet its cache in
+// blocks of up to 256, two 128-row tiles A and B per CTA with S, P and O in TMEM.
+// The key tiles of a block are the 128-row tiles that its queries see: the first
+// rows' and the window's.
+//
+//   warps 0-3, 4-7  softmax of tile A, B, a row a thread, and its output;
+//   warp 8          loads by TMA: a tile's pages are boxes of 16 to 128 rows, one a
+//                   lane, so that a tile of 16-row pages takes no longer to issue;
+//   warp 9          tcgen05 products; rows of V that no query of the block sees become
+//                   zeros first (their weight is 0, but 0 x NaN is NaN);
+//   warps 10, 11    tiles that a TMA box cannot bring: packed rows, and pages whose
+//                   rows are no multiple of 16 or lie at odd strides.  64 rows each; packed rows
+//                   become bf16 rows here (scale * code, rounded to bf16: the operand
+//                   of both products), a sub-block of 32 read ahead in registers.
+// A slot's barrier counts three arrivals whichever way it is filled: three of warp
+// 8, or one each of warps 8, 10 and 11.  Warps 10 and 11 wait for every slot in
+// turn, filled by them or not: a wait on a phase's parity holds only for a waiter
+// that has seen the phase before it.
+//
+// Few blocks (fewer than the SMs): each is cut in stretches of key tiles, whose
+// partial results (O relative to a maximum, the maximum, the sum) k_page_join adds.
+// Rounded to bf16 on the way: the turned queries, the probabilities, and what packed
+// rows stand for.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kvr_page_common.cuh"
+#include "kvr_tc_common.cuh"
+
+namespace kvr {
+
+namespace {
+
+using namespace page;
+using namespace tc;
+
+constexpr int kPtThreads = 384;
+constexpr int kPtRegsLaunch = 168, kPtRegsSoftmax = 200, kPtRegsOther = 104;
+static_assert(2 * 128 * kPtRegsSoftmax + 128 * kPtRegsOther <= kPtThreads * kPtRegsLaunch, "register split");
+constexpr int kPtTile = 128;                        // keys per tile, rows per query tile
+constexpr int kPtSlots = 5;                         // K/V ring
+constexpr int kPtTileBytes = kPtTile * 128 * 2;     // 32 KB
+constexpr int kPtPanel = kPtTileBytes / 2;
+constexpr int kPtTmemCols = 512;
+__host__ __device__ constexpr uint32_t pt_col_s(int x) { return 128u * (uint32_t)x; }
+__host__ __device__ constexpr uint32_t pt_col_o(int x) { return 256u + 128u * (uint32_t)x; }
+constexpr float kPtRescale = 8.0f;
+
+constexpr int kPtOffQ = 0;
+constexpr int kPtOffKV = 2 * kPtTileBytes;
+constexpr int kPtOffBar = kPtOffKV + kPtSlots * kPtTileBytes;
+constexpr int kTbFull = 0, kTbEmpty = kTbFull + kPtSlots, kTbS = kTbEmpty + kPtSlots, kTbP = kTbS + 2, kTbO = kTbP + 2,
+              kTbOEmpty = kTbO + 2, kTbQ = kTbOEmpty + 2, kTbQEmpty = kTbQ + 1, kTbDrain = kTbQEmpty + 1,
+              kTbNum = kTbDrain + 1;
+constexpr int kPtOffMisc = kPtOffBar + 8 * kTbNum;
+constexpr int kPtSmem = kPtOffMisc + 16 + 1024;     // + alignment slack
+static_assert(kPtSmem <= 227 * 1024, "shared memory budget");
+
+constexpr uint32_t kPtIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kPtTile >> 3) << 17) |
+                               ((uint32_t)(kPtTile >> 4) << 24);
+constexpr uint32_t kPtIdescPV = kPtIdescS | (1u << 16);   // V is MN-major
+
+// A partial result: per tile x, O as float4 [column / 4][row] (lanes are rows:
+// coalesced), then (max, sum) [row].
+constexpr int64_t kPartO = 2 * 128 * 128;                        // floats
+constexpr int64_t kPartFloats = kPartO + 2 * 128 * 2;
+static_assert(kPartFloats * 4 == kPagePartBytes, "partial result layout");
+__device__ __forceinline__ float4 *part_o(float *part, int64_t slot, int x)
+{
+    return reinterpret_cast<float4 *>(part + slot * kPartFloats) + x * (128 * 32);
+}
+__device__ __forceinline__ float2 *part_ml(float *part, int64_t slot, int x)
+{
+    return reinterpret_cast<float2 *>(part + slot * kPartFloats + kPartO) + x * 128;
+}
+
+// One block of query rows, and the key tiles of it that an item takes.
+struct Block {
+    DevPageReq rq;
+    int lh;
+    int row0, rows, nx;      // first packed row in the request, rows (<= 256), 128-row tiles
+    int hi, lo, few;         // rows that some query of the block sees: j < hi and (j >= lo or j < few)
+    int p0, p1;              // positions of its first and last token
+    int n_first, t_win;      // tiles of the first rows; the window's first tile
+    int jb, je;              // the item's tiles of the list
+
+    __device__ __forceinline__ int tile(int i) const { return i < n_first ? i : t_win + i - n_first; }
+    __device__ __forceinline__ bool seen(int j) const { return j < hi && (j >= lo || j < few); }
+    __device__ __forceinline__ bool all_seen(int j0, int j1) const { return j1 <= hi && (j0 >= lo || j1 <= few); }
+    __device__ __forceinline__ bool some_seen(int j0, int j1) const { return j0 < few || (j0 < hi && j1 > lo); }
+};
+
+__device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p, const DevPageReq *reqs, int64_t w)
+{
+    Block s;
+    s.lh = (int)(w / p.unit_items);
+    const int in_unit = (int)(w - (int64_t)s.lh * p.unit_items);
+    int lo = 0, hi = a.n_reqs - 1;
+    while (lo < hi) {   // the last request whose first item is <= it (one with items)
+        const int mid = (lo + hi + 1) >> 1;
+        if (reqs[mid].item0 <= in_unit)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    s.rq = reqs[lo];
+    const int G = a.n_q_heads / a.n_kv_heads, all = s.rq.q_len * G, mb = (all + 255) >> 8;
+    const int i = in_unit - s.rq.item0, blk = mb - 1 - i / p.splits, sp = i % p.splits;   // (the last blocks see most: first)
+    s.row0 = blk * 256;
+    s.rows = min(256, all - s.row0);
+    s.nx = s.rows > 128 ? 2 : 1;
+    s.p0 = s.rq.pos0 + s.row0 / G;
+    s.p1 = s.rq.pos0 + (s.row0 + s.rows - 1) / G;
+    s.hi = min(s.rq.kv_len, s.p1 + 1);
+    s.lo = min(s.hi, a.window > 0 ? max(0, s.p0 - a.window + 1) : 0);
+    s.few = min(a.n_first, s.lo);
+    s.n_first = (s.few + kPtTile - 1) / kPtTile;
+    s.t_win = max(s.n_first, s.lo / kPtTile);
+    const int n = s.n_first + max(0, (s.lo < s.hi ? (s.hi + kPtTile - 1) / kPtTile : 0) - s.t_win);
+    s.jb = (int)((int64_t)n * sp / p.splits);
+    s.je = (int)((int64_t)n * (sp + 1) / p.splits);
+    return s;
+}
+
+// A tile that TMA boxes bring.
+__device__ __forceinline__ bool by_tma(const PageTcArgs &p, const Block &s, int k)
+{
+    return p.box > 0 && k * kPtTile >= s.rq.packed_len;
+}
+
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// Nibbles 0 and 4 of w, less 8, as a bf16 pair (128 + nibble less 136: exact).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w)
+{
+    const uint32_t x = (w & 0x000f000fu) | 0x43004300u, c = 0x43084308u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+}  // namespace
+
+__global__ void __launch_bounds__(kPtThreads, 1)
+    k_page_attention(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PageArgs a,
+                     const __grid_constant__ PageTcArgs p, const __grid_constant__ PageTable pt)
+{
+    extern __shared__ uint8_t pt_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(pt_smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) { return sbase + kPtOffBar + 8u * (uint32_t)i; };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPtOffMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const DevPageReq *reqs = a.reqs ? a.reqs : pt.reqs;
+    const int32_t *ids = a.reqs ? a.ids : pt.ids;
+    const int G = a.n_q_heads / a.n_kv_heads;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kTbNum; ++i)
+            mbar_init(bar(i), i < kTbEmpty ? 3u
+                              : (i >= kTbP && i < kTbP + 2) || (i >= kTbOEmpty && i < kTbOEmpty + 2) ? 128u
+                                                                                                    : 1u);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9)
+        tmem_alloc(sbase + kPtOffMisc, kPtTmemCols);
+    if (warp == 8 && lane == 0) {
+        prefetch_tmap(&tmq);
+        prefetch_tmap(&tmk);
+        prefetch_tmap(&tmv);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kPtOffMisc);
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegsSoftmax));
+        pdl_wait_prerequisites();
+        pdl_launch_dependents();
+        const int x = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float sc = a.scale_log2;
+        int s_cnt = 0, o_cnt = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+            const Block b = block_at(a, p, reqs, w);
+            if (x >= b.nx)
+                continue;
+            const bool row_ok = x * 128 + r < b.rows;
+            // a warp without rows of its own only keeps the barriers going
+            const bool idle = x * 128 + (warp & 3) * 32 >= b.rows;
+            const int tok = (b.row0 + x * 128 + r) / G, pos = b.rq.pos0 + tok;
+            const Sees see = sees(a, b.rq, pos);
+            const int all_hi = min(b.rq.kv_len, b.p0 + 1), all_lo = a.window > 0 ? b.p1 - a.window + 1 : 0;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = b.jb; j < b.je; ++j) {
+                if (!mbar_wait_warp(bar(kTbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++s_cnt;
+                tc_fence_after();
+                if (idle) {
+                    tc_fence_before();
+                    mbar_arrive(bar(kTbP + x));
+                    continue;
+                }
+                float s[kPtTile];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    tmem_ld32(lane_base + pt_col_s(x) + 32 * q, s + 32 * q);
+                tmem_wait_ld();
+                const int k0 = b.tile(j) * kPtTile;
+                if (!(k0 + kPtTile <= all_hi && (k0 >= all_lo || k0 + kPtTile <= a.n_first))) {
+                    const int hi = see.hi - k0, lo = see.lo - k0, few = see.few - k0;
+#pragma unroll
+                    for (int c = 0; c < kPtTile; ++c)
+                        s[c] = (c < hi && (c >= lo || c < few)) ? s[c] : -INFINITY;
+                }
+                float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int c = 4; c + 4 < kPtTile; c += 8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        m4[k] = max3(m4[k], s[c + 2 * k], s[c + 2 * k + 1]);
+                }
+                const float mxs = max3(max3(m4[0], m4[1], m4[2]), m4[3],
+                                       max3(max3(s[kPtTile - 4], s[kPtTile - 3], s[kPtTile - 2]), s[kPtTile - 1], m4[0])) * sc;
+                // lazy maximum: O and l are rescaled only when it grows by more than the threshold
+                float corr = 1.f;
+                if (j == b.jb) {
+                    m_run = mxs;
+                } else if (mxs > m_run + kPtRescale) {
+                    corr = ex2(m_run - mxs);
+                    m_run = mxs;
+                }
+                // (all lanes together: tcgen05 loads and stores under a lane's own condition may never return)
+                const bool rescale = __any_sync(0xffffffffu, corr != 1.f);
+                const float nm = m_run == -INFINITY ? 0.f : -m_run;   // (no key seen yet)
+                const uint64_t sc2 = pk2(sc, sc), nm2 = pk2(nm, nm);
+                uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x0, x1;
+                        unpk2(fma2(pk2(s[32 * q + 2 * i], s[32 * q + 2 * i + 1]), sc2, nm2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        acc[i & 1] = add2(acc[i & 1], pk2(p0, p1));
+                        pk[i] = pack_bf16(p0, p1);
+                    }
+                    tmem_st16(lane_base + pt_col_s(x) + 16 * q, pk);
+                }
+                {
+                    float a0, a1, b0, b1;
+                    unpk2(acc[0], a0, a1);
+                    unpk2(acc[1], b0, b1);
+                    l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
+                }
+                if (rescale) {
+                    // the commit that signalled this S covers the P V before it: O is stable
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float o[32];
+                        tmem_ld32(lane_base + pt_col_o(x) + 32 * q, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] *= corr;
+                        tmem_st32(lane_base + pt_col_o(x) + 32 * q, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(kTbP + x));
+            }
+            if (!ok)
+                break;
+            const bool any = b.je > b.jb;   // (else no product was issued, O is not this item's)
+            if (any) {
+                if (!mbar_wait_warp(bar(kTbO + x), (uint32_t)o_cnt & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                ++o_cnt;
+                tc_fence_after();
+            }
+            if (p.splits == 1) {   // the row's output
+                const int l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
+                const int g = b.row0 + x * 128 + r - tok * G;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                       (((int64_t)l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + h * G + g) * 128);
+                const bool some = any && see.hi > 0 && (see.few > 0 || see.lo < see.hi);
+                if (row_ok && some && !(l_run > 0.f && l_run < INFINITY))
+                    atomicCAS(a.err, kDevOk, kDevBadInput);
+                const float inv = 1.f / l_run;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float o[32];
+                    if (any) {
+                        tmem_ld32(lane_base + pt_col_o(x) + 32 * q, o);
+                        tmem_wait_ld();
+                    }
+                    if (row_ok) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = some ? o[i] * inv : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[4 * q + i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                                        pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                    }
+                }
+            } else {
+                if (row_ok)
+                    part_ml(p.part, w, x)[r] = make_float2(m_run, l_run);
+                float4 *po = part_o(p.part, w, x) + r;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (!any)
+                        break;
+                    float o[32];
+                    tmem_ld32(lane_base + pt_col_o(x) + 32 * q, o);
+                    tmem_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            po[(8 * q + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+            }
+            if (any) {
+                tc_fence_before();
+                mbar_arrive(bar(kTbOEmpty + x));
+            }
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+    } else if (warp == 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
+        pdl_wait_prerequisites();
+        bool ok = true;
+        int tt = 0, nq = 0;
+        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+            const Block b = block_at(a, p, reqs, w);
+            const int n_loads = 2 * (b.je - b.jb);
+            if (n_loads == 0)
+                continue;
+            const int l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
+            const int64_t unit = (l * a.g.s_layer + h * a.g.s_head) / 128;
+            for (int i = 0; i <= n_loads; ++i) {
+                if (i == min(2, n_loads)) {   // the queries after the first K and V tile
+                    if (nq > 0 && !mbar_wait_warp(bar(kTbQEmpty), (uint32_t)(nq - 1) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const int q0 = (int)(((int64_t)b.lh * a.total_q + b.rq.q_off) * G + b.row0);
+                        mbar_expect_tx(bar(kTbQ), (uint32_t)(b.nx * kPtTileBytes));
+                        for (int x = 0; x < b.nx; ++x) {
+                            const uint32_t dst = sbase + (uint32_t)(kPtOffQ + x * kPtTileBytes);
+                            tma_load_2d(dst, &tmq, 0, q0 + x * kPtTile, bar(kTbQ));
+                            tma_load_2d(dst + kPtPanel, &tmq, 64, q0 + x * kPtTile, bar(kTbQ));
+                        }
+                    }
+                    ++nq;
+                }
+                if (i == n_loads)
+                    break;
+                const int slot = tt % kPtSlots, k = b.tile(b.jb + (i >> 1));
+                // lane: a box of the tile and a panel; its page is looked up while the slot is still used
+                int row = 0;
+                bool load = false;
+                const int at = (lane >> 1) * p.box, j0 = k * kPtTile + at;
+                const bool tma = by_tma(p, b, k);
+                if (tma && at < kPtTile && b.some_seen(j0, j0 + p.box)) {
+                    const int pg = j0 / a.g.rows;
+                    row = (int)((int64_t)page_id(b.rq, ids, pg) * (a.g.s_page / 128) + unit + (j0 - pg * a.g.rows));
+                    load = true;
+                }
+                const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
+                if (tt >= kPtSlots && !mbar_wait_warp(bar(kTbEmpty + slot), (uint32_t)(tt / kPtSlots - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (tma) {
+                        mbar_arrive(bar(kTbFull + slot));
+                        mbar_arrive(bar(kTbFull + slot));
+                        mbar_expect_tx(bar(kTbFull + slot), boxes * (uint32_t)p.box * 128u);
+                    } else {
+                        mbar_arrive(bar(kTbFull + slot));
+                    }
+                }
+                __syncwarp();   // (the bytes are expected before they land)
+                if (load)
+                    tma_load_2d(sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes + (lane & 1) * kPtPanel + at * 128), (i & 1) ? &tmv : &tmk,
+                                64 * (lane & 1), row, bar(kTbFull + slot));
+                ++tt;
+            }
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+        // copies in flight land before the CTA leaves
+        if (lane == 0) {
+            for (int k = tt > kPtSlots ? tt - kPtSlots : 0; k < tt; ++k)
+                mbar_drain(bar(kTbFull + k % kPtSlots), (uint32_t)(k / kPtSlots) & 1);
+            if (nq > 0)
+                mbar_drain(bar(kTbQ), (uint32_t)(nq - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
+        pdl_wait_prerequisites();
+        const uint32_t lead = elect_one();
+        int tt = 0, nq = 0, p_cnt[2] = {0, 0}, oe_cnt[2] = {0, 0};
+        bool o_used[2] = {false, false}, ok = true;
+        const uint64_t d_k = sdesc(sbase, 16, 1024), d_v = sdesc(sbase, kPtPanel, 1024);
+        const uint32_t lo_k = (uint32_t)d_k, hi_k = (uint32_t)(d_k >> 32), lo_v = (uint32_t)d_v, hi_v = (uint32_t)(d_v >> 32);
+        auto wait_kv = [&](int k) -> bool {
+            if (!mbar_wait_warp(bar(kTbFull + k % kPtSlots), (uint32_t)(k / kPtSlots) & 1, abort_flag))
+                return false;
+            tc_fence_after();
+            return true;
+        };
+        // S_x = Q_x K^T with K the ring's load k
+        auto issue_s = [&](int x, int k) {
+            const uint32_t qa = lo_k + ((uint32_t)(kPtOffQ + x * kPtTileBytes) >> 4);
+            const uint32_t kb = lo_k + ((uint32_t)(kPtOffKV + (k % kPtSlots) * kPtTileBytes) >> 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t off = (uint32_t)((i >> 2) * kPtPanel + (i & 3) * 32) >> 4;
+                mma_ss(lead, tmem + pt_col_s(x), desc_with_lo(qa + off, hi_k), desc_with_lo(kb + off, hi_k), kPtIdescS, i > 0);
+            }
+            umma_commit(lead, bar(kTbS + x));
+        };
+        auto issue_pv = [&](int x, int k, uint32_t acc0) {
+            const uint32_t vb = lo_v + ((uint32_t)(kPtOffKV + (k % kPtSlots) * kPtTileBytes) >> 4);
+#pragma unroll
+            for (int i = 0; i < kPtTile / 16; ++i)
+                mma_ts(lead, tmem + pt_col_o(x), tmem + pt_col_s(x) + 8 * i, desc_with_lo(vb + ((i * 2048) >> 4), hi_v), kPtIdescPV,
+                       i > 0 ? 1u : acc0);
+        };
+        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+            const Block b = block_at(a, p, reqs, w);
+            const int K = b.je - b.jb;
+            if (K == 0)
+                continue;
+            // V tile i of the item: landed, its rows that no query sees zeroed
+            auto wait_v = [&](int i) -> bool {
+                if (!wait_kv(tt + 2 * i + 1))
+                    return false;
+                const int k = b.tile(b.jb + i), k0 = k * kPtTile;
+                if (by_tma(p, b, k) && !b.all_seen(k0, k0 + kPtTile)) {
+                    const uint32_t v = sbase + (uint32_t)(kPtOffKV + ((tt + 2 * i + 1) % kPtSlots) * kPtTileBytes);
+                    for (int c = lane; c < kPtTile * 8; c += 32)
+                        if (!b.seen(k0 + (c >> 3))) {
+                            st_shared_v4(v + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
+                            st_shared_v4(v + kPtPanel + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
+                        }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                return true;
+            };
+            auto o_free = [&](int x) -> bool {
+                if (o_used[x]) {
+                    if (!mbar_wait_warp(bar(kTbOEmpty + x), (uint32_t)oe_cnt[x] & 1, abort_flag))
+                        return false;
+                    ++oe_cnt[x];
+                    o_used[x] = false;
+                }
+                return true;
+            };
+            if (!mbar_wait_warp(bar(kTbQ), (uint32_t)nq & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            ++nq;
+            tc_fence_after();
+            ok = wait_kv(tt);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                ok = ok && (x >= b.nx || o_free(x));
+                if (ok && x < b.nx)
+                    issue_s(x, tt);
+            }
+            if (!ok)
+                break;
+            umma_commit(lead, bar(kTbEmpty + tt % kPtSlots));
+            if (K == 1)
+                umma_commit(lead, bar(kTbQEmpty));
+            for (int i = 0; i < K && ok; ++i) {
+                const bool more = i + 1 < K;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x >= b.nx)
+                        break;
+                    if (!mbar_wait_warp(bar(kTbP + x), (uint32_t)p_cnt[x] & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    ++p_cnt[x];
+                    if (x == 0 && !wait_v(i)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    issue_pv(x, tt + 2 * i + 1, i > 0);
+                    if (!more) {
+                        umma_commit(lead, bar(kTbO + x));
+                        o_used[x] = true;
+                    } else {
+                        if (x == 0 && !wait_kv(tt + 2 * i + 2)) {
+                            ok = false;
+                            break;
+                        }
+                        issue_s(x, tt + 2 * i + 2);
+                    }
+                }
+                if (!ok)
+                    break;
+                if (i + 2 == K)
+                    umma_commit(lead, bar(kTbQEmpty));   // the item's last S is issued
+                umma_commit(lead, bar(kTbEmpty + (tt + 2 * i + 1) % kPtSlots));
+                if (more)
+                    umma_commit(lead, bar(kTbEmpty + (tt + 2 * i + 2) % kPtSlots));
+            }
+            tt += 2 * K;
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+        umma_commit(lead, bar(kTbDrain));
+        mbar_drain(bar(kTbDrain), 0);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
+        pdl_wait_prerequisites();
+        const int half = warp - 10, n = lane >> 2, c4 = lane & 3;
+        bool ok = true;
+        int tt = 0;
+        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
+            const Block b = block_at(a, p, reqs, w);
+            const int n_loads = 2 * (b.je - b.jb), l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
+            const int64_t unit = l * a.g.s_layer + h * a.g.s_head;
+            // Sub-block q of the item's loads (two of 32 rows a load): what it reads, ahead.
+            // Keys: lane 4 n + c: codes of row 8 i + n in r[4 i ..], its scales in r[16 + 2 i ..].
+            // Values: lane 16 i' + 4 c + g: in pass x, the words of rows 8 i + 2 c, + 1 (i = 2 x + i'),
+            // group g, n = 0..7, in r[8 x ..], the two scales in r[16 + x].
+            auto fetch = [&](int q, uint32_t (&r)[24]) {
+                if (q >= 2 * n_loads)
+                    return;
+                const int k = b.tile(b.jb + (q >> 2)), j0 = k * kPtTile + 64 * half + 32 * (q & 1);
+                if (by_tma(p, b, k) || j0 >= b.rq.packed_len || !b.some_seen(j0, j0 + 32))
+                    return;
+                const uint8_t *src = a.g.packed + packed_block(a, b.rq, ids, b.lh, j0);
+                if (!(q & 2)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 512 * i + 16 * lane));
+                        const uint2 s = __ldg(reinterpret_cast<const uint2 *>(src + 2048 + 64 * i + 8 * n));
+                        r[4 * i] = v.x;
+                        r[4 * i + 1] = v.y;
+                        r[4 * i + 2] = v.z;
+                        r[4 * i + 3] = v.w;
+                        r[16 + 2 * i] = s.x;
+                        r[16 + 2 * i + 1] = s.y;
+                    }
+                } else {
+                    src += kPackHalf;
+                    const int g = lane & 3, c = (lane >> 2) & 3;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int i = 2 * x + (lane >> 4);
+#pragma unroll
+                        for (int m = 0; m < 8; ++m)
+                            r[8 * x + m] = __ldg(reinterpret_cast<const uint32_t *>(src + 512 * i + 64 * m + 16 * c + 4 * g));
+                        const uint16_t *s = reinterpret_cast<const uint16_t *>(src + 2048 + 64 * i + 16 * c + 2 * g);
+                        r[16 + x] = (uint32_t)__ldg(s) | (uint32_t)__ldg(s + 4) << 16;
+                    }
+                }
+            };
+            auto put = [&](uint32_t tile, int row, int ch, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+                st_shared_v4(tile + (uint32_t)((ch >> 3) * kPtPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4)), v0, v1, v2, v3);
+            };
+            // the sub-block into its slot
+            auto store = [&](int q, const uint32_t (&r)[24], uint32_t tile) {
+                const int k = b.tile(b.jb + (q >> 2)), in = 64 * half + 32 * (q & 1), j0 = k * kPtTile + in;
+                const bool values = (q & 2) != 0, some = b.some_seen(j0, j0 + 32);
+                if (!some || j0 >= b.rq.packed_len) {   // bf16 rows, zeros where none is seen
+                    const int ch = lane & 15;
+                    if (!some && !values)
+                        return;
+#pragma unroll 4
+                    for (int x = 0; x < 16; ++x) {
+                        const int row = 2 * x + (lane >> 4), j = j0 + row;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (b.seen(j)) {
+                            const int pg = j / a.g.rows;
+                            const int64_t at = (int64_t)page_id(b.rq, ids, pg) * a.g.s_page + unit + (int64_t)(j - pg * a.g.rows) * 128;
+                            v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(values ? a.g.v : a.g.k) + at) + ch);
+                        }
+                        put(tile, in + row, ch, v.x, v.y, v.z, v.w);
+                    }
+                } else if (!values) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const uint32_t wd = r[4 * i + g], s = prmt(r[16 + 2 * i + (g >> 1)], 0u, (g & 1) ? 0x3232u : 0x1010u);
+                            put(tile, in + 8 * i + n, 4 * g + c4, hmul2_bf16(code_pair(wd), s), hmul2_bf16(code_pair(wd >> 4), s),
+                                hmul2_bf16(code_pair(wd >> 8), s), hmul2_bf16(code_pair(wd >> 12), s));
+                        }
+                } else {
+                    const int g = lane & 3, c = (lane >> 2) & 3;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int row = 8 * (2 * x + (lane >> 4)) + 2 * c;
+                        uint32_t s = r[16 + x];
+                        if (!b.seen(j0 + row))       // (its scale may be NaN)
+                            s &= 0xffff0000u;
+                        if (!b.seen(j0 + row + 1))
+                            s &= 0x0000ffffu;
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            uint32_t v[8];
+#pragma unroll
+                            for (int d = 0; d < 8; ++d)
+                                v[d] = hmul2_bf16(code_pair(r[8 * x + d] >> (4 * m)), s);
+                            put(tile, in + row, 4 * g + m, prmt(v[0], v[1], 0x5410), prmt(v[2], v[3], 0x5410), prmt(v[4], v[5], 0x5410),
+                                prmt(v[6], v[7], 0x5410));
+                            put(tile, in + row + 1, 4 * g + m, prmt(v[0], v[1], 0x7632), prmt(v[2], v[3], 0x7632),
+                                prmt(v[4], v[5], 0x7632), prmt(v[6], v[7], 0x7632));
+                        }
+                    }
+                }
+            };
+            uint32_t r0[24], r1[24];
+            fetch(0, r0);
+            for (int i = 0; i < n_loads; ++i, ++tt) {
+                const int slot = tt % kPtSlots;
+                if (tt >= kPtSlots && !mbar_wait_warp(bar(kTbEmpty + slot), (uint32_t)(tt / kPtSlots - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (by_tma(p, b, b.tile(b.jb + (i >> 1)))) {
+                    fetch(2 * (i + 1), r0);
+                    continue;
+                }
+                const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
+                fetch(2 * i + 1, r1);
+                store(2 * i, r0, tile);
+                fetch(2 * i + 2, r0);
+                store(2 * i + 1, r1, tile);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(kTbFull + slot));
+            }
+        }
+        if (!ok)
+            give_up(a.err, abort_flag);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kPtTmemCols);
+    }
+}
+
+// The partial results of a block's stretches, one after the other: a CTA a
+// 128-row tile, a thread a row.
+__global__ void __launch_bounds__(128)
+    k_page_join(const __grid_constant__ PageArgs a, const __grid_constant__ PageTcArgs p, const __grid_constant__ PageTable pt)
+{
+    pdl_wait_prerequisites();
+    const DevPageReq *reqs = a.reqs ? a.reqs : pt.reqs;
+    const int G = a.n_q_heads / a.n_kv_heads, x = (int)(blockIdx.x & 1u), r = threadIdx.x;
+    const int64_t w0 = (int64_t)(blockIdx.x >> 1) * p.splits;
+    const Block b = block_at(a, p, reqs, w0);
+    if (x * 128 + r >= b.rows)
+        return;
+    const int tok = (b.row0 + x * 128 + r) / G, g = b.row0 + x * 128 + r - tok * G;
+    const Sees see = sees(a, b.rq, b.rq.pos0 + tok);
+    const bool some = see.hi > 0 && (see.few > 0 || see.lo < see.hi);
+    float m = -INFINITY, L = 0.f;
+    for (int i = 0; i < p.splits; ++i)
+        m = fmaxf(m, part_ml(p.part, w0 + i, x)[r].x);
+    for (int i = 0; i < p.splits; ++i) {
+        const float2 ml = part_ml(p.part, w0 + i, x)[r];
+        L += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - m);   // (a stretch of NaN scores: a sum of NaN under -inf)
+    }
+    if (some && !(L > 0.f && L < INFINITY))
+        atomicCAS(a.err, kDevOk, kDevBadInput);
+    const float inv = some ? 1.f / L : 0.f;
+    const int l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
+    uint2 *dst = reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                           (((int64_t)l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + h * G + g) * 128);
+#pragma unroll 4
+    for (int c = 0; c < 32; ++c) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < p.splits; ++i) {
+            const float2 ml = part_ml(p.part, w0 + i, x)[r];
+            if (ml.x == -INFINITY && ml.y == 0.f)   // (nothing seen: its O is not written)
+                continue;
+            const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+            const float4 o = part_o(p.part, w0 + i, x)[c * 128 + r];
+            v.x = fmaf(o.x, f, v.x);
+            v.y = fmaf(o.y, f, v.y);
+            v.z = fmaf(o.z, f, v.z);
+            v.w = fmaf(o.w, f, v.w);
+        }
+        dst[c] = some ? make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)) : make_uint2(0u, 0u);
+    }
+}
+
+// The query heads of the requests of more than kPageFewRows rows, turned and packed:
+// [L][H_kv][T][G][D].  8 threads a (layer, token, kv-head), in the queries' order.
+__global__ void __launch_bounds__(128)
+    k_page_queries(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable pt, __nv_bfloat16 *__restrict__ q_rot)
+{
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    const DevPageReq *reqs = a.reqs ? a.reqs : pt.reqs;
+    const int G = a.n_q_heads / a.n_kv_heads, H = a.n_kv_heads, j = threadIdx.x & 7;
+    const int64_t item = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 3);
+    if (item >= (int64_t)a.n_layers * a.total_q * H)
+        return;
+    const int64_t lt = item / H;
+    const int h = (int)(item - lt * H), l = (int)(lt / a.total_q), tok = (int)(lt - (int64_t)l * a.total_q);
+    int lo = 0, hi = a.n_reqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (reqs[mid].q_off <= tok)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const DevPageReq &rq = reqs[lo];
+    if (rq.q_len * G <= kPageFewRows)
+        return;
+    const bool il = a.interleaved != 0;
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float2 v = rope_cs(a.rope, 64, rq.pos0 + tok - rq.q_off, rope_pair(il, 128, 8, j, e));
+        cs[e] = v.x;
+        sn[e] = v.y;
+    }
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) + item * G * 128 + 8 * j;
+    __nv_bfloat16 *dst = q_rot + (((int64_t)l * H + h) * a.total_q + tok) * G * 128 + 8 * j;
+#pragma unroll 4
+    for (int g = 0; g < G; ++g) {
+        uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + g * 128)), y = __ldg(reinterpret_cast<const uint4 *>(src + g * 128 + 64));
+        if (il)
+            rotate_bf16x8_il(x, y, cs, sn);
+        else
+            rotate_bf16x8(x, y, cs, sn);
+        *reinterpret_cast<uint4 *>(dst + g * 128) = x;
+        *reinterpret_cast<uint4 *>(dst + g * 128 + 64) = y;
+    }
+}
+
+cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTable &t, void *q_rot, const void *tmap_q,
+                           const void *tmap_k, const void *tmap_v, int n_sms, cudaStream_t s)
+{
+    static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+        cudaFuncAttributes fa{};
+        if ((e = cudaFuncGetAttributes(&fa, k_page_attention)) != cudaSuccess)
+            return e;
+        // the roles' register counts draw on what the launch holds: exactly this many
+        if (fa.numRegs != kPtRegsLaunch)
+            return cudaErrorInvalidConfiguration;
+        if ((e = cudaFuncSetAttribute(k_page_attention, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem)) != cudaSuccess)
+            return e;
+        if (dev < 64)
+            attr_set[dev].store(true, std::memory_order_release);
+    }
+    const int64_t triples = (int64_t)a.n_layers * a.total_q * a.n_kv_heads;
+    e = launch_pdl(k_page_queries, (triples + 15) / 16, 128, 0, true, s, a, t, static_cast<__nv_bfloat16 *>(q_rot));
+    if (e == cudaSuccess)
+        e = launch_pdl(k_page_attention, std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s,
+                       *static_cast<const CUtensorMap *>(tmap_q), *static_cast<const CUtensorMap *>(tmap_k),
+                       *static_cast<const CUtensorMap *>(tmap_v), a, p, t);
+    if (e == cudaSuccess && p.splits > 1)
+        e = launch_pdl(k_page_join, 2 * (p.total / p.splits), 128, 0, true, s, a, p, t);
+    return e;
+}
+
+}  // namespace kvr
