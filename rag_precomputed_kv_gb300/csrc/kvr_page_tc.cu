@@ -17,9 +17,11 @@
 //                   become bf16 rows here (scale * code, rounded to bf16: the operand
 //                   of both products), a sub-block of 32 read ahead in registers.
 // A slot's barrier counts three arrivals whichever way it is filled: three of warp
-// 8, or one each of warps 8, 10 and 11.  Warps 10 and 11 wait for every slot in
-// turn, filled by them or not: a wait on a phase's parity holds only for a waiter
-// that has seen the phase before it.
+// 8, or one each of warps 8, 10 and 11.  That a slot is free for them, warps 10 and
+// 11 learn from warp 8, over a barrier of the slot that completes a phase for each
+// of their tiles and no other: on the barrier that frees slots they could come two
+// phases late, past tiles that are none of theirs, and a wait for a parity would not
+// return.
 //
 // Few blocks (fewer than the SMs): each is cut in stretches of key tiles, whose
 // partial results (O relative to a maximum, the maximum, the sum) k_page_join adds.
@@ -58,7 +60,7 @@ constexpr int kPtOffKV = 2 * kPtTileBytes;
 constexpr int kPtOffBar = kPtOffKV + kPtSlots * kPtTileBytes;
 constexpr int kTbFull = 0, kTbEmpty = kTbFull + kPtSlots, kTbS = kTbEmpty + kPtSlots, kTbP = kTbS + 2, kTbO = kTbP + 2,
               kTbOEmpty = kTbO + 2, kTbQ = kTbOEmpty + 2, kTbQEmpty = kTbQ + 1, kTbDrain = kTbQEmpty + 1,
-              kTbNum = kTbDrain + 1;
+              kTbJob = kTbDrain + 1, kTbNum = kTbJob + kPtSlots;
 constexpr int kPtOffMisc = kPtOffBar + 8 * kTbNum;
 constexpr int kPtSmem = kPtOffMisc + 16 + 1024;     // + alignment slack
 static_assert(kPtSmem <= 227 * 1024, "shared memory budget");
@@ -404,6 +406,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         mbar_expect_tx(bar(kTbFull + slot), boxes * (uint32_t)p.box * 128u);
                     } else {
                         mbar_arrive(bar(kTbFull + slot));
+                        mbar_arrive(bar(kTbJob + slot));
                     }
                 }
                 __syncwarp();   // (the bytes are expected before they land)
@@ -552,6 +555,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int half = warp - 10, n = lane >> 2, c4 = lane & 3;
         bool ok = true;
         int tt = 0;
+        uint32_t jobs = 0;   // bit s: the parity of slot s's next job
         for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
             const Block b = block_at(a, p, reqs, w);
             const int n_loads = 2 * (b.je - b.jb), l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
@@ -652,14 +656,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             fetch(0, r0);
             for (int i = 0; i < n_loads; ++i, ++tt) {
                 const int slot = tt % kPtSlots;
-                if (tt >= kPtSlots && !mbar_wait_warp(bar(kTbEmpty + slot), (uint32_t)(tt / kPtSlots - 1) & 1, abort_flag)) {
-                    ok = false;
-                    break;
-                }
                 if (by_tma(p, b, b.tile(b.jb + (i >> 1)))) {
                     fetch(2 * (i + 1), r0);
                     continue;
                 }
+                if (!mbar_wait_warp(bar(kTbJob + slot), (jobs >> slot) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                jobs ^= 1u << slot;
                 const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
                 fetch(2 * i + 1, r1);
                 store(2 * i, r0, tile);
