@@ -15,8 +15,12 @@
 // memory and the cluster's.  Three CTAs of four warps are resident on an SM.
 //
 // Both products are warp MMAs (mma.sync m16n8k16; at 16 rows a tcgen05 MMA would
-// pass every tile through TMEM).  Packed rows are not restored to bf16 rows: a
-// nibble n under the exponent bits of 128 is the bf16 number 128 + n, and
+// pass every tile through TMEM), with keys and values as the 16-row operand and the
+// query rows, eight at a time, as the columns: S^T = K Q^T and O^T = V^T P^T, so that
+// a step of up to 8 query heads a kv head does half of what 16 rows would take.
+// The probabilities change from the one's layout to the other's by movmatrix.
+// Packed rows are not restored to bf16 rows: a nibble n under the exponent bits of
+// 128 is the bf16 number 128 + n, and
 //   keys    sum_d q_d (n_d + 128) - 136 sum_d q_d = sum_d q_d code_d: the second
 //           term is where the accumulator starts; the group's fp32 result is then
 //           scaled and added, so that a score has the codes' and scales' exact
@@ -51,7 +55,7 @@ constexpr int kPdStage = 2 * kPackBytes;             // 64 packed rows, or 16 bf
 constexpr int kPdRing = 2 * kPdStage;
 constexpr int kPdSmem = kPdWarps * kPdRing;
 constexpr int kPdCtas = 3;                           // resident on an SM
-constexpr int kPdPitch = 136;                        // floats of a row of a warp's output (no bank conflicts)
+constexpr int kPdPitch = 132;                        // floats of a row of a warp's output (two rows 8 banks apart)
 static_assert(16 * kPdPitch * 4 + 128 <= kPdStage && 16 * 128 * 4 + 128 <= kPdStage, "states over the ring");
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
@@ -107,14 +111,28 @@ __device__ __forceinline__ uint32_t less136(uint32_t w)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// d = a b + c
-__device__ __forceinline__ void mma_from(float *d, const uint32_t *a, uint32_t b0, uint32_t b1, float c0, float c2)
+// d = a b + c, c the same in every row
+__device__ __forceinline__ void mma_from(float *d, const uint32_t *a, uint32_t b0, uint32_t b1, const float *c)
 {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %11, %11};"
+        "{%10, %11, %10, %11};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c2));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]));
+}
+
+// The 8x8 matrix of a warp's bf16 pairs, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
 }
 
 // The tiles that some query of a request meets: packed ones of 64 rows, then bf16
@@ -157,6 +175,8 @@ struct TileList {
 
 }  // namespace
 
+// NR: octets of query rows (a call's largest request decides).
+template <int NR>
 __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     k_page_decode(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t, int n_ctas)
 {
@@ -223,15 +243,15 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     issue(it, 0);
     issue(it + step, 1);
 
-    // Q as the A operand: rows n and n + 8, of group g the dims 32 g + 8 c + 0..7, pair
-    // m at step m / 2; turned by the rows' positions
-    uint32_t qa[4][2][4];
-    float start[4][2];   // -136 times a group's sum
+    // Q^T as the B operand: of row 8 x + n and group g the dims 32 g + 8 c + 0..7, pair m
+    // at step m / 2; turned by the row's position
+    uint32_t qb[NR][4][4];
+    float start[NR][4][2];   // -136 times the group's sum, of rows 8 x + 2 c and + 1
     {
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
                                  (((int64_t)l * a.total_q + rq.q_off) * a.n_q_heads + h * G) * 128 + 8 * c;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < NR; ++x) {
             const int r = n + 8 * x, tok = r / G;
             const bool some = r < rows;
             uint4 v[4];
@@ -272,83 +292,29 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
                 float s = 0.f;
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    qa[g][m >> 1][2 * (m & 1) + x] = w[m];
+                    qb[x][g][m] = w[m];
                     s += bf_lo(w[m]) + bf_hi(w[m]);
                 }
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                start[g][x] = -136.f * s;
+                start[x][g][0] = -136.f * __shfl_sync(0xffffffffu, s, 8 * c);
+                start[x][g][1] = -136.f * __shfl_sync(0xffffffffu, s, 8 * c + 4);
             }
         }
     }
-    Sees see[2];
-    int p_last = rq.pos0 + rq.q_len - 1;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-        see[x] = sees(a, rq, min(p_last, rq.pos0 + (n + 8 * x) / G));
     // rows that every query sees: below, and from (or among the first) on
-    const int all_hi = min(rq.kv_len, rq.pos0 + 1), all_lo = a.window > 0 ? p_last - a.window + 1 : 0;
+    const int all_hi = min(rq.kv_len, rq.pos0 + 1), all_lo = a.window > 0 ? rq.pos0 + rq.q_len - a.window : 0;
 
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    float o[16][4];
+    float m_run[NR][2], l_run[NR][2];   // of query rows 8 x + 2 c and + 1; l over this lane's keys
+    float o[NR][8][4];                  // dims 16 j + n and + 8 of these two rows
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-
-    // scores of 8 NT rows from row0 on become probabilities, O and l are brought to the
-    // maximum they are relative to.  It moves only when it grows by more than 8 (log2),
-    // which bf16 and fp32 hold, and a row's quad agrees on it.
-    auto softmax = [&](float (*s)[4], auto nt, int row0) {
-        constexpr int NT = decltype(nt)::value;
-        const float sc = a.scale_log2;
-        if (row0 + 8 * NT <= all_hi && (row0 >= all_lo || row0 + 8 * NT <= a.n_first)) {
+    for (int x = 0; x < NR; ++x) {
+        m_run[x][0] = m_run[x][1] = -INFINITY;
+        l_run[x][0] = l_run[x][1] = 0.f;
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[i][e] *= sc;
-        } else {
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[i][e] = see[e >> 1](row0 + 8 * i + 2 * c + (e & 1)) ? s[i][e] * sc : -INFINITY;
-        }
-        float corr[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                mx = fmaxf(mx, fmaxf(s[i][2 * x], s[i][2 * x + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            corr[x] = 1.f;
-            if (mx > m_run[x] + 8.f) {
-                corr[x] = dec_ex2(m_run[x] - mx);
-                m_run[x] = mx;
-            }
-        }
-        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                o[j][0] *= corr[0];
-                o[j][1] *= corr[0];
-                o[j][2] *= corr[1];
-                o[j][3] *= corr[1];
-            }
-            l_run[0] *= corr[0];
-            l_run[1] *= corr[1];
-        }
-        const float nm[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[i][e] = dec_ex2(s[i][e] + nm[e >> 1]);
-                l_run[e >> 1] += s[i][e];
-            }
-    };
+        for (int j = 0; j < 8; ++j)
+            o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
+    }
 
     for (int stage = 0; it < n_t; it += step, stage ^= 1) {
         copies_wait<1>();
@@ -356,88 +322,153 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
         bool packed;
         const int row0 = tl.row(it, packed);
         const uint32_t st = ring + (uint32_t)(stage * kPdStage);
-        if (packed) {
+        // 16 keys at a time, in a loop that the instruction cache holds
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-                const int r = row0 + k * kPackRows;
-                if (!tl.block_seen(r))
-                    continue;
-                const uint32_t kb = st + (uint32_t)(k * kPackBytes), vb = kb + kPackHalf;
-                float s[4][4];
+        for (int k = 0; k < (packed ? kPdPacked / kPdKeys : 1); ++k) {
+            const int row = row0 + kPdKeys * k;
+            if (packed && !tl.block_seen(row & ~(kPackRows - 1)))
+                continue;   // (not loaded)
+            const uint32_t kb = st + (uint32_t)((k >> 1) * kPackBytes + (k & 1) * 1024 + 16 * lane);
+            const uint32_t sb = st + (uint32_t)((k >> 1) * kPackBytes + 2048 + (k & 1) * 128 + 8 * n);
+            // S^T: keys n and n + 8 of the 16, query rows 8 x + 2 c and + 1
+            float s[NR][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 code = lds128(kb + 512 * i + 16 * lane), sc = lds128(kb + 2048 + 64 * i + 16 * c);
-                    const uint32_t w[4] = {code.x, code.y, code.z, code.w}, s0[2] = {sc.x, sc.y}, s1[2] = {sc.z, sc.w};
-                    s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        float d[4];
-                        mma_from(d, qa[g][0], pair128(w[g]), pair128(w[g] >> 4), start[g][0], start[g][1]);
-                        mma_bf16(d, qa[g][1], pair128(w[g] >> 8), pair128(w[g] >> 12));
-                        const float x0 = (g & 1) ? bf_hi(s0[g >> 1]) : bf_lo(s0[g >> 1]);
-                        const float x1 = (g & 1) ? bf_hi(s1[g >> 1]) : bf_lo(s1[g >> 1]);
-                        s[i][0] = fmaf(x0, d[0], s[i][0]);
-                        s[i][1] = fmaf(x1, d[1], s[i][1]);
-                        s[i][2] = fmaf(x0, d[2], s[i][2]);
-                        s[i][3] = fmaf(x1, d[3], s[i][3]);
-                    }
-                }
-                softmax(s, std::integral_constant<int, 4>(), r);
-                // rows that no query sees may have scales of NaN
-                const bool whole = r + kPackRows <= tl.hi && (r >= tl.lo || r + kPackRows <= tl.few);
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const uint4 c0 = lds128(vb + 512 * i + 16 * lane), c1 = lds128(vb + 512 * i + 512 + 16 * lane);
-                    uint4 z0 = lds128(vb + 2048 + 64 * i + 16 * c), z1 = lds128(vb + 2048 + 64 * i + 64 + 16 * c);
-                    if (!whole) {
-                        const int j = r + 8 * i + 2 * c;
-                        if (!tl.seen(j))
-                            z0.x = z0.y = 0u;
-                        if (!tl.seen(j + 1))
-                            z0.z = z0.w = 0u;
-                        if (!tl.seen(j + 8))
-                            z1.x = z1.y = 0u;
-                        if (!tl.seen(j + 9))
-                            z1.z = z1.w = 0u;
-                    }
-                    const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
-                    const uint32_t s00[2] = {z0.x, z0.y}, s01[2] = {z0.z, z0.w}, s10[2] = {z1.x, z1.y}, s11[2] = {z1.z, z1.w};
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float x00 = (g & 1) ? bf_hi(s00[g >> 1]) : bf_lo(s00[g >> 1]);
-                        const float x01 = (g & 1) ? bf_hi(s01[g >> 1]) : bf_lo(s01[g >> 1]);
-                        const float x10 = (g & 1) ? bf_hi(s10[g >> 1]) : bf_lo(s10[g >> 1]);
-                        const float x11 = (g & 1) ? bf_hi(s11[g >> 1]) : bf_lo(s11[g >> 1]);
-                        const uint32_t pa[4] = {pack2(s[i][0] * x00, s[i][1] * x01), pack2(s[i][2] * x00, s[i][3] * x01),
-                                                pack2(s[i + 1][0] * x10, s[i + 1][1] * x11),
-                                                pack2(s[i + 1][2] * x10, s[i + 1][3] * x11)};
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            mma_bf16(o[4 * g + m], pa, less136(pair128(w0[g] >> (4 * m))), less136(pair128(w1[g] >> (4 * m))));
-                    }
-                }
-            }
-        } else {
-            float s[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            for (int x = 0; x < NR; ++x)
+                s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+            if (packed) {
+                const uint4 c0 = lds128(kb), c1 = lds128(kb + 512);
+                const uint2 z0 = lds64(sb), z1 = lds64(sb + 64);
+                const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint4 w = lds128(st + (uint32_t)((8 * i + n) * 256 + (((4 * g + c) ^ ((n & 1) << 2)) << 4)));
-                    mma_bf16(s[i], qa[g][0], w.x, w.y);
-                    mma_bf16(s[i], qa[g][1], w.z, w.w);
+                    const uint32_t y0 = g < 2 ? z0.x : z0.y, y1 = g < 2 ? z1.x : z1.y;
+                    const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
+                    const uint32_t a0[4] = {pair128(w0[g]), pair128(w1[g]), pair128(w0[g] >> 4), pair128(w1[g] >> 4)};
+                    const uint32_t a1[4] = {pair128(w0[g] >> 8), pair128(w1[g] >> 8), pair128(w0[g] >> 12), pair128(w1[g] >> 12)};
+#pragma unroll
+                    for (int x = 0; x < NR; ++x) {
+                        float d[4];
+                        mma_from(d, a0, qb[x][g][0], qb[x][g][1], start[x][g]);
+                        mma_bf16(d, a1, qb[x][g][2], qb[x][g][3]);
+                        s[x][0] = fmaf(x0, d[0], s[x][0]);
+                        s[x][1] = fmaf(x0, d[1], s[x][1]);
+                        s[x][2] = fmaf(x1, d[2], s[x][2]);
+                        s[x][3] = fmaf(x1, d[3], s[x][3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t at = st + (uint32_t)(n * 256 + (((4 * g + c) ^ ((n & 1) << 2)) << 4));
+                    const uint4 w0 = lds128(at), w1 = lds128(at + 2048);
+                    const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
+#pragma unroll
+                    for (int x = 0; x < NR; ++x) {
+                        mma_bf16(s[x], a0, qb[x][g][0], qb[x][g][1]);
+                        mma_bf16(s[x], a1, qb[x][g][2], qb[x][g][3]);
+                    }
                 }
             }
-            softmax(s, std::integral_constant<int, 2>(), row0);
-            const uint32_t pa[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]), pack2(s[1][2], s[1][3])};
-            const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
+            const bool all = row + kPdKeys <= all_hi && (row >= all_lo || row + kPdKeys <= a.n_first);
+            if (!all) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4_t(st + (uint32_t)(4096 + key * 256 + (((j + (lane >> 4)) ^ (key & 7)) << 4)), b0, b1, b2, b3);
-                mma_bf16(o[j], pa, b0, b1);
-                mma_bf16(o[j + 1], pa, b2, b3);
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const Sees see = sees(a, rq, min(rq.pos0 + rq.q_len - 1, rq.pos0 + (8 * x + 2 * c + (e & 1)) / G));
+                        if (!see(row + n + 8 * (e >> 1)))
+                            s[x][e] = -INFINITY;
+                    }
+            }
+            // Scores become probabilities relative to the row's maximum, which moves only when a
+            // score is more than 8 (log2) above it: bf16 and fp32 hold that, and most steps need
+            // no exchange between the lanes.
+            const float sc = a.scale_log2;
+            float t[NR][4];
+            bool over = false;
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float m = m_run[x][e & 1];
+                    t[x][e] = fmaf(s[x][e], sc, m == -INFINITY ? 0.f : -m);
+                    over = over || t[x][e] > (m == -INFINITY ? -INFINITY : 8.f);
+                }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(s[x][e], s[x][e + 2]) * sc;
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        mx = fmaxf(mx, m_run[x][e]);
+                        const float corr = mx == -INFINITY ? 1.f : dec_ex2(m_run[x][e] - mx), nm = mx == -INFINITY ? 0.f : -mx;
+                        m_run[x][e] = mx;
+                        l_run[x][e] *= corr;
+                        t[x][e] = fmaf(s[x][e], sc, nm);
+                        t[x][e + 2] = fmaf(s[x][e + 2], sc, nm);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            o[x][j][e] *= corr;
+                            o[x][j][e + 2] *= corr;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    t[x][e] = dec_ex2(t[x][e]);
+                    l_run[x][e & 1] += t[x][e];
+                }
+            // O^T += V^T P^T
+            if (packed) {
+                const uint4 c0 = lds128(kb + kPackHalf), c1 = lds128(kb + kPackHalf + 512);
+                uint2 z0 = lds64(sb + kPackHalf), z1 = lds64(sb + kPackHalf + 64);
+                if (!all) {   // rows that no query sees may have scales of NaN
+                    if (!tl.seen(row + n))
+                        z0 = make_uint2(0u, 0u);
+                    if (!tl.seen(row + n + 8))
+                        z1 = make_uint2(0u, 0u);
+                }
+                const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t y0 = g < 2 ? z0.x : z0.y, y1 = g < 2 ? z1.x : z1.y;
+                    const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
+                    uint32_t b0[NR], b1[NR];
+#pragma unroll
+                    for (int x = 0; x < NR; ++x) {
+                        b0[x] = transpose8(pack2(t[x][0] * x0, t[x][1] * x0));
+                        b1[x] = transpose8(pack2(t[x][2] * x1, t[x][3] * x1));
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t va[4] = {less136(pair128(w0[g] >> (8 * m))), less136(pair128(w0[g] >> (8 * m + 4))),
+                                                less136(pair128(w1[g] >> (8 * m))), less136(pair128(w1[g] >> (8 * m + 4)))};
+#pragma unroll
+                        for (int x = 0; x < NR; ++x)
+                            mma_bf16(o[x][2 * g + m], va, b0[x], b1[x]);
+                    }
+                }
+            } else {
+                uint32_t b0[NR], b1[NR];
+#pragma unroll
+                for (int x = 0; x < NR; ++x) {
+                    b0[x] = transpose8(pack2(t[x][0], t[x][1]));
+                    b1[x] = transpose8(pack2(t[x][2], t[x][3]));
+                }
+                const int key = (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t va[4];
+                    ldsm_x4_t(st + (uint32_t)(4096 + key * 256 + (((2 * j + ((lane >> 3) & 1)) ^ (key & 7)) << 4)), va[0], va[1], va[2], va[3]);
+#pragma unroll
+                    for (int x = 0; x < NR; ++x)
+                        mma_bf16(o[x][j], va, b0[x], b1[x]);
+                }
             }
         }
         __syncwarp();
@@ -451,19 +482,24 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     {
         float *f = area(warp);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            l_run[x] += __shfl_xor_sync(0xffffffffu, l_run[x], 1);
-            l_run[x] += __shfl_xor_sync(0xffffffffu, l_run[x], 2);
-            if (c == 0) {
-                f[16 * kPdPitch + n + 8 * x] = m_run[x];
-                f[16 * kPdPitch + 16 + n + 8 * x] = l_run[x];
-            }
-        }
+        for (int x = 0; x < NR; ++x)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            *reinterpret_cast<float2 *>(f + n * kPdPitch + 8 * j + 2 * c) = make_float2(o[j][0], o[j][1]);
-            *reinterpret_cast<float2 *>(f + (n + 8) * kPdPitch + 8 * j + 2 * c) = make_float2(o[j][2], o[j][3]);
-        }
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * x + 2 * c + e;
+                float v = l_run[x][e];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (n == 0) {
+                    f[16 * kPdPitch + r] = m_run[x][e];
+                    f[16 * kPdPitch + 16 + r] = v;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    f[r * kPdPitch + 16 * j + n] = o[x][j][e];
+                    f[r * kPdPitch + 16 * j + n + 8] = o[x][j][e + 2];
+                }
+            }
     }
     __syncthreads();
     // thread 32 k + i: rows k, k + 4, .., columns 4 i .. 4 i + 3
@@ -541,30 +577,41 @@ cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevP
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(k_page_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, kPdSmem);
-        if (e != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(k_page_decode<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPdSmem)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(k_page_decode<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPdSmem)) != cudaSuccess)
             return e;
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
     }
     const int units = a.n_layers * a.n_kv_heads, G = a.n_q_heads / a.n_kv_heads;
-    int64_t few = 0;
-    int most = 0;
+    int64_t few = 0, tiles = 0;
+    int rows = 0;
     for (int b = 0; b < a.n_reqs; ++b) {
-        if (host_reqs[b].q_len == 0 || host_reqs[b].q_len * (int64_t)G > kPageFewRows)
+        const int64_t r = host_reqs[b].q_len * (int64_t)G;
+        if (r == 0 || r > kPageFewRows)
             continue;
         TileList tl;
         tl.set(host_reqs[b], a.window, a.n_first);
-        most = std::max(most, tl.total());
+        tiles += tl.total();
+        rows = std::max(rows, (int)r);
         ++few;
     }
     if (few == 0)
         return cudaSuccess;
-    // as many CTAs of a (request, unit) as are resident at once, each warp with two tiles at least
+    // CTAs of a (request, unit): the largest share of an SM decides, its CTAs' tiles (0.2 us
+    // each when the SM is full, slower with one or two CTAs on it) and 1.5 us more for each.
+    // One request of 33,280 packed rows, 256 units: 819 us with one, 2.0 CTAs an SM.
     int c = 1;
-    while (c < 8 && few * units * c * 2 <= (int64_t)kPdCtas * n_sms && most >= 2 * kPdWarps * 2 * c)
-        c *= 2;
-    return launch_cluster(k_page_decode, (int64_t)a.n_reqs * units * c, kPdThreads, kPdSmem, c, s, a, t, c);
+    double best = 1e30;
+    for (int k = 1; k <= 8; k *= 2) {
+        const double load = (double)((few * units * k + n_sms - 1) / n_sms);
+        const double t1 = load * (0.2 * (double)tiles / (double)(few * k) + 1.5) * (load < 2. ? 2.2 : load < 3. ? 1.3 : 1.);
+        if (t1 < 0.97 * best) {
+            best = t1;
+            c = k;
+        }
+    }
+    return launch_cluster(rows <= 8 ? k_page_decode<1> : k_page_decode<2>, (int64_t)a.n_reqs * units * c, kPdThreads, kPdSmem, c, s, a, t, c);
 }
 
 }  // namespace kvr
