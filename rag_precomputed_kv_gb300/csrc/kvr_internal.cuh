@@ -444,11 +444,11 @@ struct EvictArgs {
 };
 
 // ---- paged cache ----
-// Rows that are packed together, dims that share a scale, and the bytes of one
-// packed block of kPackRows rows (keys: codes, scales; values: codes, scales).
+// Rows that are packed together, dims that share a scale, and the bytes of the
+// keys (or values) of 16 of these rows, of both, and of a packed block.
 constexpr int kPackRows = 32, kPackGroup = 32;
-constexpr int kPackHalf = kPackRows * 128 / 2 + kPackRows * (128 / kPackGroup) * 2;
-constexpr int kPackBytes = 2 * kPackHalf;
+constexpr int kPackPart = 16 * 128 / 2 + 16 * (128 / kPackGroup) * 2;
+constexpr int kPackStep = 2 * kPackPart, kPackBytes = kPackRows / 16 * kPackStep;
 static_assert(kPackBytes == 4608, "packed block layout");
 
 // Per-request data (48 bytes).  Page g of a request is entry g + off[0] of the

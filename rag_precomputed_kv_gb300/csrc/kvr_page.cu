@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(32 * kPkWarps)
     const int row = rq.pos0 + (int)(blk - rq.q_off) * kPackRows, pg = row / a.g.rows, in = row - pg * a.g.rows;
     __nv_bfloat16 *x = static_cast<__nv_bfloat16 *>(which ? a.g.v : a.g.k) + (int64_t)page_id(rq, ids, pg) * a.g.s_page +
                        l * a.g.s_layer + h * a.g.s_head + (int64_t)in * 128;
-    uint8_t *p = a.g.packed + packed_block(a, rq, ids, u, row) + which * kPackHalf;
+    uint8_t *p = a.g.packed + packed_block(a, rq, ids, u, row);
     // the values' word of an octet's lane i (row 2 c' + i / 4 of octet c', ...) is, transposed,
     // that of lane 4 i + c'
     const int place = which ? 4 * (lane & 7) + (lane >> 3) : lane;
@@ -281,9 +281,9 @@ __global__ void __launch_bounds__(32 * kPkWarps)
                 w[g] = pack8(raw[i][g], sc[g]);
                 w[g] = which ? transpose_nibbles(w[g], lane) : spread_pairs(w[g]);
             }
-            *reinterpret_cast<uint4 *>(p + 512 * i + 16 * place) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(p + codes_at(i, which) + 16 * place) = make_uint4(w[0], w[1], w[2], w[3]);
             if (c == 0)
-                *reinterpret_cast<uint2 *>(p + 2048 + (8 * i + n) * 8) =
+                *reinterpret_cast<uint2 *>(p + scales_at(8 * i + n, which)) =
                     make_uint2(sc[0] | (uint32_t)sc[1] << 16, sc[2] | (uint32_t)sc[3] << 16);
         }
     } else {
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(32 * kPkWarps)
         uint2 sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            codes[i] = *reinterpret_cast<const uint4 *>(p + 512 * i + 16 * place);
-            sc[i] = *reinterpret_cast<const uint2 *>(p + 2048 + (8 * i + n) * 8);
+            codes[i] = *reinterpret_cast<const uint4 *>(p + codes_at(i, which) + 16 * place);
+            sc[i] = *reinterpret_cast<const uint2 *>(p + scales_at(8 * i + n, which));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

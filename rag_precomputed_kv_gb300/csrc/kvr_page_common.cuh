@@ -1,11 +1,11 @@
 // kvr_page_common.cuh -- what the kernels of the paged cache share: page
 // look-up, which rows a query sees, and the packed rows' layout.
 //
-// A packed block holds kPackRows = 32 rows of one (layer, kv-head): keys, then
-// values, each as 2,048 bytes of 4-bit codes and 256 bytes of bf16 scales
-// [row][group of 32 dims].  A value is scale * (nibble - 8).  The codes lie as
-// the operands of mma.sync m16n8k16 want them, 512 bytes for 8 rows, 16 bytes
-// for each lane 4 n + c (n = 0..7, c = 0..3), one word per group g:
+// A packed block holds kPackRows = 32 rows of one (layer, kv-head), 16 at a time:
+// 1,024 bytes of the keys' 4-bit codes, 128 of their bf16 scales, then the values'.
+// A value is scale * (nibble - 8).  Scales lie [n][rows n, n + 8][group of 32 dims]
+// (n = 0..7).  Codes lie as the operands of mma.sync m16n8k16 want them, 512 bytes
+// for 8 rows, 16 bytes for each lane 4 n + c (c = 0..3), one word per group g:
 //   keys    lane 4 n + c: row n, dims 32 g + 8 c + 0..7; nibble m holds the dim
 //           2 m, nibble m + 4 the dim 2 m + 1 (m = 0..3): a shift by 4 m and a
 //           mask leave two neighbouring dims in the two halves of the word.
@@ -42,6 +42,14 @@ __device__ __forceinline__ Sees sees(const PageArgs &a, const DevPageReq &r, int
     s.lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
     s.few = min(a.n_first, s.lo);
     return s;
+}
+
+// Offsets in a block: the codes of rows 8 i .. 8 i + 7, the four scales of row r; of the
+// keys (part 0) or the values (1).
+__device__ __forceinline__ int codes_at(int i, int part) { return (i >> 1) * kPackStep + part * kPackPart + (i & 1) * 512; }
+__device__ __forceinline__ int scales_at(int r, int part)
+{
+    return (r >> 4) * kPackStep + part * kPackPart + 1024 + (r & 7) * 16 + (r & 8);
 }
 
 // Byte offset of packed row block `row / 32` in the packed pages.

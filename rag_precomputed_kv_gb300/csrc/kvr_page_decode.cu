@@ -58,6 +58,9 @@ constexpr int kPdCtas = 3;                           // resident on an SM
 constexpr int kPdPitch = 132;                        // floats of a row of a warp's output (two rows 8 banks apart)
 static_assert(16 * kPdPitch * 4 + 128 <= kPdStage && 16 * 128 * 4 + 128 <= kPdStage, "states over the ring");
 
+// The running maximum of a row that has seen no key: any score is above it.
+constexpr float kNothing = -3.4028234e38f;
+
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -127,12 +130,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
 }
 
 // The tiles that some query of a request meets: packed ones of 64 rows, then bf16
@@ -309,7 +306,7 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     float o[NR][8][4];                  // dims 16 j + n and + 8 of these two rows
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
-        m_run[x][0] = m_run[x][1] = -INFINITY;
+        m_run[x][0] = m_run[x][1] = kNothing;
         l_run[x][0] = l_run[x][1] = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -322,14 +319,15 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
         bool packed;
         const int row0 = tl.row(it, packed);
         const uint32_t st = ring + (uint32_t)(stage * kPdStage);
+        const int n_k = packed ? min(kPdPacked, tl.body - row0) / kPdKeys : 1, end = row0 + kPdKeys * n_k;
+        const bool all = end <= all_hi && (row0 >= all_lo || end <= a.n_first);   // every query sees every row
         // 16 keys at a time, in a loop that the instruction cache holds
 #pragma unroll 1
-        for (int k = 0; k < (packed ? kPdPacked / kPdKeys : 1); ++k) {
+        for (int k = 0; k < n_k; ++k) {
             const int row = row0 + kPdKeys * k;
-            if (packed && !tl.block_seen(row & ~(kPackRows - 1)))
+            if (!all && packed && !tl.block_seen(row & ~(kPackRows - 1)))
                 continue;   // (not loaded)
-            const uint32_t kb = st + (uint32_t)((k >> 1) * kPackBytes + (k & 1) * 1024 + 16 * lane);
-            const uint32_t sb = st + (uint32_t)((k >> 1) * kPackBytes + 2048 + (k & 1) * 128 + 8 * n);
+            const uint32_t kb = st + (uint32_t)(k * kPackStep + 16 * lane), sb = st + (uint32_t)(k * kPackStep + 1024 + 16 * n);
             // S^T: keys n and n + 8 of the 16, query rows 8 x + 2 c and + 1
             float s[NR][4];
 #pragma unroll
@@ -337,11 +335,11 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
                 s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
             if (packed) {
                 const uint4 c0 = lds128(kb), c1 = lds128(kb + 512);
-                const uint2 z0 = lds64(sb), z1 = lds64(sb + 64);
+                const uint4 z = lds128(sb);
                 const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint32_t y0 = g < 2 ? z0.x : z0.y, y1 = g < 2 ? z1.x : z1.y;
+                    const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
                     const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
                     const uint32_t a0[4] = {pair128(w0[g]), pair128(w1[g]), pair128(w0[g] >> 4), pair128(w1[g] >> 4)};
                     const uint32_t a1[4] = {pair128(w0[g] >> 8), pair128(w1[g] >> 8), pair128(w0[g] >> 12), pair128(w1[g] >> 12)};
@@ -369,7 +367,6 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
                     }
                 }
             }
-            const bool all = row + kPdKeys <= all_hi && (row >= all_lo || row + kPdKeys <= a.n_first);
             if (!all) {
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
@@ -385,16 +382,15 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
             // no exchange between the lanes.
             const float sc = a.scale_log2;
             float t[NR][4];
-            bool over = false;
+            float over = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < NR; ++x)
+            for (int x = 0; x < NR; ++x) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float m = m_run[x][e & 1];
-                    t[x][e] = fmaf(s[x][e], sc, m == -INFINITY ? 0.f : -m);
-                    over = over || t[x][e] > (m == -INFINITY ? -INFINITY : 8.f);
-                }
-            if (__any_sync(0xffffffffu, over)) {
+                for (int e = 0; e < 4; ++e)
+                    t[x][e] = fmaf(s[x][e], sc, -m_run[x][e & 1]);
+                over = fmaxf(over, fmaxf(fmaxf(t[x][0], t[x][1]), fmaxf(t[x][2], t[x][3])));
+            }
+            if (__any_sync(0xffffffffu, over > 8.f)) {
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -404,11 +400,11 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         mx = fmaxf(mx, m_run[x][e]);
-                        const float corr = mx == -INFINITY ? 1.f : dec_ex2(m_run[x][e] - mx), nm = mx == -INFINITY ? 0.f : -mx;
+                        const float corr = dec_ex2(m_run[x][e] - mx);
                         m_run[x][e] = mx;
                         l_run[x][e] *= corr;
-                        t[x][e] = fmaf(s[x][e], sc, nm);
-                        t[x][e + 2] = fmaf(s[x][e + 2], sc, nm);
+                        t[x][e] = fmaf(s[x][e], sc, -mx);
+                        t[x][e + 2] = fmaf(s[x][e + 2], sc, -mx);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             o[x][j][e] *= corr;
@@ -425,18 +421,18 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
                 }
             // O^T += V^T P^T
             if (packed) {
-                const uint4 c0 = lds128(kb + kPackHalf), c1 = lds128(kb + kPackHalf + 512);
-                uint2 z0 = lds64(sb + kPackHalf), z1 = lds64(sb + kPackHalf + 64);
+                const uint4 c0 = lds128(kb + kPackPart), c1 = lds128(kb + kPackPart + 512);
+                uint4 z = lds128(sb + kPackPart);
                 if (!all) {   // rows that no query sees may have scales of NaN
                     if (!tl.seen(row + n))
-                        z0 = make_uint2(0u, 0u);
+                        z.x = z.y = 0u;
                     if (!tl.seen(row + n + 8))
-                        z1 = make_uint2(0u, 0u);
+                        z.z = z.w = 0u;
                 }
                 const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint32_t y0 = g < 2 ? z0.x : z0.y, y1 = g < 2 ? z1.x : z1.y;
+                    const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
                     const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
                     uint32_t b0[NR], b1[NR];
 #pragma unroll
@@ -518,17 +514,16 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     const int col = 4 * lane;
     float *joined = reinterpret_cast<float *>(pd_smem + kPdStage);   // behind warp 0's state: [16][128], 16 maxima, 16 sums
     for (int r = warp; r < rows; r += kPdWarps) {
-        float M = -INFINITY, L = 0.f;
+        float M = kNothing, L = 0.f;
 #pragma unroll
         for (int w = 0; w < kPdWarps; ++w)
             M = fmaxf(M, area(w)[16 * kPdPitch + r]);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kPdWarps; ++w) {
-            const float mw = area(w)[16 * kPdPitch + r], f = mw == -INFINITY ? 0.f : dec_ex2(mw - M);
+            const float f = dec_ex2(area(w)[16 * kPdPitch + r] - M);
             const float4 x = *reinterpret_cast<const float4 *>(area(w) + r * kPdPitch + col);
-            // (a warp whose scores were NaN has a NaN sum under a maximum of -inf)
-            L += mw == -INFINITY ? area(w)[16 * kPdPitch + 16 + r] : area(w)[16 * kPdPitch + 16 + r] * f;
+            L = fmaf(area(w)[16 * kPdPitch + 16 + r], f, L);
             v.x = fmaf(x.x, f, v.x);
             v.y = fmaf(x.y, f, v.y);
             v.z = fmaf(x.z, f, v.z);
@@ -549,7 +544,7 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     cluster_meet();
     const uint32_t mine = dec_smem_u32(joined);
     for (int r = (int)rank + n_ctas * warp; r < rows; r += n_ctas * kPdWarps) {
-        float M = -INFINITY, L = 0.f;
+        float M = kNothing, L = 0.f;
         for (int k = 0; k < n_ctas; ++k)
             M = fmaxf(M, ld_cluster1(at_rank(mine + 4u * (uint32_t)(16 * 128 + r), (uint32_t)k)));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -557,8 +552,8 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
             const float mk = ld_cluster1(at_rank(mine + 4u * (uint32_t)(16 * 128 + r), (uint32_t)k));
             const float lk = ld_cluster1(at_rank(mine + 4u * (uint32_t)(16 * 128 + 16 + r), (uint32_t)k));
             const float4 x = ld_cluster(at_rank(mine + 4u * (uint32_t)(r * 128 + col), (uint32_t)k));
-            const float f = mk == -INFINITY ? 0.f : dec_ex2(mk - M);
-            L += mk == -INFINITY ? lk : lk * f;
+            const float f = dec_ex2(mk - M);
+            L = fmaf(lk, f, L);
             v.x = fmaf(x.x, f, v.x);
             v.y = fmaf(x.y, f, v.y);
             v.z = fmaf(x.z, f, v.z);

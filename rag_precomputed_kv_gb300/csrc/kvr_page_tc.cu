@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (!(q & 2)) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 512 * i + 16 * lane));
-                        const uint2 s = __ldg(reinterpret_cast<const uint2 *>(src + 2048 + 64 * i + 8 * n));
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + codes_at(i, 0) + 16 * lane));
+                        const uint2 s = __ldg(reinterpret_cast<const uint2 *>(src + scales_at(8 * i + n, 0)));
                         r[4 * i] = v.x;
                         r[4 * i + 1] = v.y;
                         r[4 * i + 2] = v.z;
@@ -584,16 +584,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         r[16 + 2 * i + 1] = s.y;
                     }
                 } else {
-                    src += kPackHalf;
                     const int g = lane & 3, c = (lane >> 2) & 3;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int i = 2 * x + (lane >> 4);
 #pragma unroll
                         for (int m = 0; m < 8; ++m)
-                            r[8 * x + m] = __ldg(reinterpret_cast<const uint32_t *>(src + 512 * i + 64 * m + 16 * c + 4 * g));
-                        const uint16_t *s = reinterpret_cast<const uint16_t *>(src + 2048 + 64 * i + 16 * c + 2 * g);
-                        r[16 + x] = (uint32_t)__ldg(s) | (uint32_t)__ldg(s + 4) << 16;
+                            r[8 * x + m] = __ldg(reinterpret_cast<const uint32_t *>(src + codes_at(i, 1) + 64 * m + 16 * c + 4 * g));
+                        const uint16_t *s = reinterpret_cast<const uint16_t *>(src + scales_at(8 * i + 2 * c, 1) + 2 * g);
+                        r[16 + x] = (uint32_t)__ldg(s) | (uint32_t)__ldg(s + 8) << 16;   // (the next row's)
                     }
                 }
             };

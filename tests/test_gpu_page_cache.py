@@ -314,13 +314,12 @@ def _attention_case(reqs, L=2, H=2, G=4, D=128, dtype="bf16", R=16, window=0, fi
         exact = [(_packed_ref(x.cpu())[0] * _packed_ref(x.cpu())[1]).reshape(x.shape).numpy() for x in (k, v)]
         kw = dict(packed=packed, packed_table=tp, packed_len=body)
         if poison:   # packed rows outside what is seen: scales of NaN again
-            blk = packed.data.view(npk, L, H, R // 32, 2, 2304)
+            # [pages, L, H, 16 rows, keys or values, rows n and n + 8 by turns, groups]
+            scales = packed.data.view(npk, L, H, R // 16, 2, 1152)[..., 1024:].view(torch.bfloat16).unflatten(-1, (8, 2, 4))
             for b in range(len(reqs)):
                 gone = np.setdiff1d(np.arange(body[b]), seen[b])
-                for half in (0, 1):
-                    sc = blk[:, :, :, :, half, 2048:].view(torch.bfloat16)          # [pages, L, H, blocks, 128]
-                    for r in gone:
-                        sc[int(tp[b, r // R]), :, :, r % R // 32, 4 * (r % 32):4 * (r % 32) + 4] = float("nan")
+                for r in gone:
+                    scales[int(tp[b, r // R]), :, :, r % R // 16, :, r % 8, r % 16 // 8] = float("nan")
     T, qo = sum(lq), _starts(lq).astype(np.int32)
     if poison:       # nothing may come of rows that no query sees, nor of pages without one
         mask = torch.ones((n, R), dtype=torch.bool)
