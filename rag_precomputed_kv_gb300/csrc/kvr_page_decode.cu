@@ -8,9 +8,8 @@
 //
 // One CTA, or a cluster of 2 to 8 where (request, unit) pairs are few, takes one
 // request's (layer, kv-head).  Its warps go through the visible key tiles by
-// turns, each with its own two-stage ring filled by cp.async (16 bf16 rows, or 64
-// packed ones, a stage: any page size and stride, rows that are not there are
-// zeros) and its own running maximum, sum and output in registers; no warp waits
+// turns, each with its own two-stage ring filled by cp.async (tiles of 16 bf16 or 32 packed rows: any page size and stride,
+// rows that are not there are zeros) and its own running maximum, sum and output in registers; no warp waits
 // for another before the states are joined, in a fixed order, through shared
 // memory and the cluster's.  Three CTAs of four warps are resident on an SM.
 //
@@ -50,13 +49,27 @@ using dec::pack2;
 
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
-constexpr int kPdKeys = 16, kPdPacked = 64;          // rows of a tile
-constexpr int kPdStage = 2 * kPackBytes;             // 64 packed rows, or 16 bf16 keys and values (8,192)
-constexpr int kPdRing = 2 * kPdStage;
-constexpr int kPdSmem = kPdWarps * kPdRing;
-constexpr int kPdCtas = 3;                           // resident on an SM
+constexpr int kPdKeys = 16, kPdPacked = kPackRows;   // rows of a tile
+constexpr int kPdKeyBytes = kPdKeys * 2 * 256;
 constexpr int kPdPitch = 132;                        // floats of a row of a warp's output (two rows 8 banks apart)
-static_assert(16 * kPdPitch * 4 + 128 <= kPdStage && 16 * 128 * 4 + 128 <= kPdStage, "states over the ring");
+
+// A warp's ring.  Calls without packed rows: two tiles of 16 rows, three CTAs on an
+// SM.  Calls with them: three packed tiles, in whose place the bf16 ones behind them come one
+// at a time; up to 8 query rows leave registers for four CTAs on an SM.
+template <int NR, bool kPack>
+struct Ring {
+    static constexpr int kCtas = kPack && NR == 1 ? 4 : 3;
+    static constexpr int kPackStages = 3, kKeyStages = kPack ? 1 : 2;
+    static constexpr int kBytes = kPack ? kPackStages * kPackBytes : kKeyStages * kPdKeyBytes;
+    static constexpr int kState = 8 * NR * kPdPitch * 4 + 64 * NR;          // a warp's state: O, maxima, sums
+    static constexpr int kJoined = 8 * NR * 128 * 4 + 64 * NR;              // a CTA's
+    // the joined state behind warp 0's where that leaves room, else behind the rings
+    static constexpr bool kInside = kState + kJoined <= kBytes;
+    static constexpr int kOffJoined = kInside ? kState : kPdWarps * kBytes;
+    static constexpr int kSmem = kPdWarps * kBytes + (kInside ? 0 : kJoined);
+    static_assert(kState <= kBytes, "states over the rings");
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
+};
 
 // The running maximum of a row that has seen no key: any score is above it.
 constexpr float kNothing = -3.4028234e38f;
@@ -132,7 +145,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
     return r;
 }
 
-// The tiles that some query of a request meets: packed ones of 64 rows, then bf16
+// The tiles that some query of a request meets: packed ones of 32 rows, then bf16
 // ones of 16; of each the first rows', then the window's.
 struct TileList {
     int t0[4], n[4];
@@ -158,25 +171,17 @@ struct TileList {
     }
     __host__ __device__ __forceinline__ int total() const { return n[0] + n[1] + n[2] + n[3]; }
     __device__ __forceinline__ bool seen(int j) const { return j < hi && (j >= lo || j < few); }
-    __device__ __forceinline__ bool block_seen(int j) const { return j < body && (j < few || (j < hi && j + kPackRows > lo)); }
-    // tile i: its first row, and whether it is packed
-    __device__ __forceinline__ int row(int i, bool &packed) const
-    {
-        const int p = n[0] + n[1];
-        packed = i < p;
-        if (packed)
-            return (i < n[0] ? t0[0] + i : t0[1] + i - n[0]) * kPdPacked;
-        return (i < p + n[2] ? t0[2] + i - p : t0[3] + i - p - n[2]) * kPdKeys;
-    }
 };
 
 }  // namespace
 
-// NR: octets of query rows (a call's largest request decides).
-template <int NR>
-__global__ void __launch_bounds__(kPdThreads, kPdCtas)
+// NR: octets of query rows (a call's largest request decides).  kPack: the call has
+// packed rows.
+template <int NR, bool kPack>
+__global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
     k_page_decode(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t, int n_ctas)
 {
+    using R = Ring<NR, kPack>;
     extern __shared__ __align__(128) uint8_t pd_smem[];
     pdl_wait_prerequisites();   // (also before leaving: the next kernel's wait stands for those before this one)
     pdl_launch_dependents();
@@ -195,50 +200,57 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     const int n_t = tl.total(), step = kPdWarps * n_ctas;
     const int64_t unit = l * a.g.s_layer + h * a.g.s_head;
     const __nv_bfloat16 *gk = static_cast<const __nv_bfloat16 *>(a.g.k), *gv = static_cast<const __nv_bfloat16 *>(a.g.v);
-    const uint32_t ring = dec_smem_u32(pd_smem) + (uint32_t)(warp * kPdRing);
+    const uint32_t ring = dec_smem_u32(pd_smem) + (uint32_t)(warp * R::kBytes);
     const bool one_page = a.g.rows % kPdKeys == 0;   // a tile's rows are in one page
 
+    const int n_p = kPack ? tl.n[0] + tl.n[1] : 0;
+    auto issue_packed = [&](int i, int stage) {
+        if (i < n_p) {
+            const int r0 = (i < tl.n[0] ? tl.t0[0] + i : tl.t0[1] + i - tl.n[0]) * kPdPacked;
+            const uint32_t dst = ring + (uint32_t)(stage * kPackBytes + 16 * lane);
+            const uint8_t *src = a.g.packed + packed_block(a, rq, ids, u, r0) + 16 * lane;
+#pragma unroll
+            for (int x = 0; x < kPackBytes / 512; ++x)
+                copy16(dst + 512 * x, src + 512 * x, true);
+        }
+        copies_end();
+    };
     auto issue = [&](int i, int stage) {
         if (i < n_t) {
-            bool packed;
-            const int r0 = tl.row(i, packed);
-            const uint32_t dst = ring + (uint32_t)(stage * kPdStage);
-            if (packed) {
+            const int r0 = (i < n_p + tl.n[2] ? tl.t0[2] + i - n_p : tl.t0[3] + i - n_p - tl.n[2]) * kPdKeys;
+            const uint32_t dst = ring + (uint32_t)(stage * kPdKeyBytes);
+            const int ch = lane & 15;
+            int64_t base = 0;
+            if (one_page) {
+                const int pg = r0 / a.g.rows;
+                base = (int64_t)page_id(rq, ids, pg) * a.g.s_page + unit + (int64_t)(r0 - pg * a.g.rows) * 128;
+            }
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (tl.block_seen(r0 + k * kPackRows)) {
-                        const uint8_t *src = a.g.packed + packed_block(a, rq, ids, u, r0 + k * kPackRows) + 16 * lane;
-#pragma unroll
-                        for (int x = 0; x < kPackBytes / 512; ++x)
-                            copy16(dst + (uint32_t)(k * kPackBytes + 16 * lane + 512 * x), src + 512 * x, true);
-                    }
-            } else {
-                const int ch = lane & 15;
-                int64_t base = 0;
-                if (one_page) {
-                    const int pg = r0 / a.g.rows;
-                    base = (int64_t)page_id(rq, ids, pg) * a.g.s_page + unit + (int64_t)(r0 - pg * a.g.rows) * 128;
+            for (int x = 0; x < 8; ++x) {
+                const int r = (lane >> 4) + 2 * x, j = r0 + r;
+                const bool there = tl.seen(j);
+                int64_t at = base + r * 128;
+                if (!one_page && there) {
+                    const int pg = j / a.g.rows;
+                    at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + unit + (int64_t)(j - pg * a.g.rows) * 128;
                 }
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const int r = (lane >> 4) + 2 * x, j = r0 + r;
-                    const bool there = tl.seen(j);
-                    int64_t at = base + r * 128;
-                    if (!one_page && there) {
-                        const int pg = j / a.g.rows;
-                        at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + unit + (int64_t)(j - pg * a.g.rows) * 128;
-                    }
-                    at = there ? at + 8 * ch : 0;
-                    copy16(dst + (uint32_t)(r * 256 + ((ch ^ ((r & 1) << 2)) << 4)), gk + at, there);
-                    copy16(dst + (uint32_t)(4096 + r * 256 + ((ch ^ (r & 7)) << 4)), gv + at, there);
-                }
+                at = there ? at + 8 * ch : 0;
+                copy16(dst + (uint32_t)(r * 256 + ((ch ^ ((r & 1) << 2)) << 4)), gk + at, there);
+                copy16(dst + (uint32_t)(4096 + r * 256 + ((ch ^ (r & 7)) << 4)), gv + at, there);
             }
         }
         copies_end();
     };
     int it = (int)rank * kPdWarps + warp;
-    issue(it, 0);
-    issue(it + step, 1);
+    if constexpr (kPack) {
+#pragma unroll
+        for (int k = 0; k < R::kPackStages; ++k)
+            issue_packed(it + k * step, k);
+    } else {
+#pragma unroll
+        for (int k = 0; k < R::kKeyStages; ++k)
+            issue(it + k * step, k);
+    }
 
     // Q^T as the B operand: of row 8 x + n and group g the dims 32 g + 8 c + 0..7, pair m
     // at step m / 2; turned by the row's position
@@ -313,168 +325,179 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
             o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
     }
 
-    for (int stage = 0; it < n_t; it += step, stage ^= 1) {
-        copies_wait<1>();
-        __syncwarp();
-        bool packed;
-        const int row0 = tl.row(it, packed);
-        const uint32_t st = ring + (uint32_t)(stage * kPdStage);
-        const int n_k = packed ? min(kPdPacked, tl.body - row0) / kPdKeys : 1, end = row0 + kPdKeys * n_k;
-        const bool all = end <= all_hi && (row0 >= all_lo || end <= a.n_first);   // every query sees every row
-        // 16 keys at a time, in a loop that the instruction cache holds
-#pragma unroll 1
-        for (int k = 0; k < n_k; ++k) {
-            const int row = row0 + kPdKeys * k;
-            if (!all && packed && !tl.block_seen(row & ~(kPackRows - 1)))
-                continue;   // (not loaded)
-            const uint32_t kb = st + (uint32_t)(k * kPackStep + 16 * lane), sb = st + (uint32_t)(k * kPackStep + 1024 + 16 * n);
-            // S^T: keys n and n + 8 of the 16, query rows 8 x + 2 c and + 1
-            float s[NR][4];
+    // One step: 16 rows from `row` on, packed at `st` (kThin) or as bf16 rows.  `all`: every
+    // query sees every row.
+    auto step16 = [&](auto thin, int row, uint32_t st, bool all) {
+        constexpr bool kThin = decltype(thin)::value;
+        const uint32_t kb = st + 16 * lane, sb = st + 1024 + 16 * n;
+        // S^T: keys n and n + 8 of the 16, query rows 8 x + 2 c and + 1
+        float s[NR][4];
 #pragma unroll
-            for (int x = 0; x < NR; ++x)
-                s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
-            if (packed) {
-                const uint4 c0 = lds128(kb), c1 = lds128(kb + 512);
-                const uint4 z = lds128(sb);
-                const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+        for (int x = 0; x < NR; ++x)
+            s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+        if constexpr (kThin) {
+            const uint4 c0 = lds128(kb), c1 = lds128(kb + 512);
+            const uint4 z = lds128(sb);
+            const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
-                    const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
-                    const uint32_t a0[4] = {pair128(w0[g]), pair128(w1[g]), pair128(w0[g] >> 4), pair128(w1[g] >> 4)};
-                    const uint32_t a1[4] = {pair128(w0[g] >> 8), pair128(w1[g] >> 8), pair128(w0[g] >> 12), pair128(w1[g] >> 12)};
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
+                const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
+                const uint32_t a0[4] = {pair128(w0[g]), pair128(w1[g]), pair128(w0[g] >> 4), pair128(w1[g] >> 4)};
+                const uint32_t a1[4] = {pair128(w0[g] >> 8), pair128(w1[g] >> 8), pair128(w0[g] >> 12), pair128(w1[g] >> 12)};
 #pragma unroll
-                    for (int x = 0; x < NR; ++x) {
-                        float d[4];
-                        mma_from(d, a0, qb[x][g][0], qb[x][g][1], start[x][g]);
-                        mma_bf16(d, a1, qb[x][g][2], qb[x][g][3]);
-                        s[x][0] = fmaf(x0, d[0], s[x][0]);
-                        s[x][1] = fmaf(x0, d[1], s[x][1]);
-                        s[x][2] = fmaf(x1, d[2], s[x][2]);
-                        s[x][3] = fmaf(x1, d[3], s[x][3]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t at = st + (uint32_t)(n * 256 + (((4 * g + c) ^ ((n & 1) << 2)) << 4));
-                    const uint4 w0 = lds128(at), w1 = lds128(at + 2048);
-                    const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
-#pragma unroll
-                    for (int x = 0; x < NR; ++x) {
-                        mma_bf16(s[x], a0, qb[x][g][0], qb[x][g][1]);
-                        mma_bf16(s[x], a1, qb[x][g][2], qb[x][g][3]);
-                    }
+                for (int x = 0; x < NR; ++x) {
+                    float d[4];
+                    mma_from(d, a0, qb[x][g][0], qb[x][g][1], start[x][g]);
+                    mma_bf16(d, a1, qb[x][g][2], qb[x][g][3]);
+                    s[x][0] = fmaf(x0, d[0], s[x][0]);
+                    s[x][1] = fmaf(x0, d[1], s[x][1]);
+                    s[x][2] = fmaf(x1, d[2], s[x][2]);
+                    s[x][3] = fmaf(x1, d[3], s[x][3]);
                 }
             }
-            if (!all) {
+        } else {
 #pragma unroll
-                for (int x = 0; x < NR; ++x)
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t at = st + (uint32_t)(n * 256 + (((4 * g + c) ^ ((n & 1) << 2)) << 4));
+                const uint4 w0 = lds128(at), w1 = lds128(at + 2048);
+                const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const Sees see = sees(a, rq, min(rq.pos0 + rq.q_len - 1, rq.pos0 + (8 * x + 2 * c + (e & 1)) / G));
-                        if (!see(row + n + 8 * (e >> 1)))
-                            s[x][e] = -INFINITY;
-                    }
+                for (int x = 0; x < NR; ++x) {
+                    mma_bf16(s[x], a0, qb[x][g][0], qb[x][g][1]);
+                    mma_bf16(s[x], a1, qb[x][g][2], qb[x][g][3]);
+                }
             }
-            // Scores become probabilities relative to the row's maximum, which moves only when a
-            // score is more than 8 (log2) above it: bf16 and fp32 hold that, and most steps need
-            // no exchange between the lanes.
-            const float sc = a.scale_log2;
-            float t[NR][4];
-            float over = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < NR; ++x) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    t[x][e] = fmaf(s[x][e], sc, -m_run[x][e & 1]);
-                over = fmaxf(over, fmaxf(fmaxf(t[x][0], t[x][1]), fmaxf(t[x][2], t[x][3])));
-            }
-            if (__any_sync(0xffffffffu, over > 8.f)) {
-#pragma unroll
-                for (int x = 0; x < NR; ++x)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(s[x][e], s[x][e + 2]) * sc;
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        mx = fmaxf(mx, m_run[x][e]);
-                        const float corr = dec_ex2(m_run[x][e] - mx);
-                        m_run[x][e] = mx;
-                        l_run[x][e] *= corr;
-                        t[x][e] = fmaf(s[x][e], sc, -mx);
-                        t[x][e + 2] = fmaf(s[x][e + 2], sc, -mx);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            o[x][j][e] *= corr;
-                            o[x][j][e + 2] *= corr;
-                        }
-                    }
-            }
+        }
+        if (!all) {
 #pragma unroll
             for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    t[x][e] = dec_ex2(t[x][e]);
-                    l_run[x][e & 1] += t[x][e];
+                    const Sees see = sees(a, rq, min(rq.pos0 + rq.q_len - 1, rq.pos0 + (8 * x + 2 * c + (e & 1)) / G));
+                    if (!see(row + n + 8 * (e >> 1)))
+                        s[x][e] = -INFINITY;
                 }
-            // O^T += V^T P^T
-            if (packed) {
-                const uint4 c0 = lds128(kb + kPackPart), c1 = lds128(kb + kPackPart + 512);
-                uint4 z = lds128(sb + kPackPart);
-                if (!all) {   // rows that no query sees may have scales of NaN
-                    if (!tl.seen(row + n))
-                        z.x = z.y = 0u;
-                    if (!tl.seen(row + n + 8))
-                        z.z = z.w = 0u;
-                }
-                const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+        }
+        // Scores become probabilities relative to the row's maximum, which moves only when a
+        // score is more than 8 (log2) above it: bf16 and fp32 hold that, and most steps need
+        // no exchange between the lanes.
+        const float sc = a.scale_log2;
+        float t[NR][4];
+        float over = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
-                    const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
-                    uint32_t b0[NR], b1[NR];
+        for (int x = 0; x < NR; ++x) {
 #pragma unroll
-                    for (int x = 0; x < NR; ++x) {
-                        b0[x] = transpose8(pack2(t[x][0] * x0, t[x][1] * x0));
-                        b1[x] = transpose8(pack2(t[x][2] * x1, t[x][3] * x1));
+            for (int e = 0; e < 4; ++e)
+                t[x][e] = fmaf(s[x][e], sc, -m_run[x][e & 1]);
+            over = fmaxf(over, fmaxf(fmaxf(t[x][0], t[x][1]), fmaxf(t[x][2], t[x][3])));
+        }
+        if (__any_sync(0xffffffffu, over > 8.f)) {
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(s[x][e], s[x][e + 2]) * sc;
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    mx = fmaxf(mx, m_run[x][e]);
+                    const float corr = dec_ex2(m_run[x][e] - mx);
+                    m_run[x][e] = mx;
+                    l_run[x][e] *= corr;
+                    t[x][e] = fmaf(s[x][e], sc, -mx);
+                    t[x][e + 2] = fmaf(s[x][e + 2], sc, -mx);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        o[x][j][e] *= corr;
+                        o[x][j][e + 2] *= corr;
                     }
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint32_t va[4] = {less136(pair128(w0[g] >> (8 * m))), less136(pair128(w0[g] >> (8 * m + 4))),
-                                                less136(pair128(w1[g] >> (8 * m))), less136(pair128(w1[g] >> (8 * m + 4)))};
-#pragma unroll
-                        for (int x = 0; x < NR; ++x)
-                            mma_bf16(o[x][2 * g + m], va, b0[x], b1[x]);
-                    }
                 }
-            } else {
+        }
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                t[x][e] = dec_ex2(t[x][e]);
+                l_run[x][e & 1] += t[x][e];
+            }
+        // O^T += V^T P^T
+        if constexpr (kThin) {
+            const uint4 c0 = lds128(kb + kPackPart), c1 = lds128(kb + kPackPart + 512);
+            uint4 z = lds128(sb + kPackPart);
+            if (!all) {   // rows that no query sees may have scales of NaN
+                if (!tl.seen(row + n))
+                    z.x = z.y = 0u;
+                if (!tl.seen(row + n + 8))
+                    z.z = z.w = 0u;
+            }
+            const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
+                const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
                 uint32_t b0[NR], b1[NR];
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
-                    b0[x] = transpose8(pack2(t[x][0], t[x][1]));
-                    b1[x] = transpose8(pack2(t[x][2], t[x][3]));
+                    b0[x] = transpose8(pack2(t[x][0] * x0, t[x][1] * x0));
+                    b1[x] = transpose8(pack2(t[x][2] * x1, t[x][3] * x1));
                 }
-                const int key = (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint32_t va[4];
-                    ldsm_x4_t(st + (uint32_t)(4096 + key * 256 + (((2 * j + ((lane >> 3) & 1)) ^ (key & 7)) << 4)), va[0], va[1], va[2], va[3]);
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t va[4] = {less136(pair128(w0[g] >> (8 * m))), less136(pair128(w0[g] >> (8 * m + 4))),
+                                            less136(pair128(w1[g] >> (8 * m))), less136(pair128(w1[g] >> (8 * m + 4)))};
 #pragma unroll
                     for (int x = 0; x < NR; ++x)
-                        mma_bf16(o[x][j], va, b0[x], b1[x]);
+                        mma_bf16(o[x][2 * g + m], va, b0[x], b1[x]);
                 }
             }
+        } else {
+            uint32_t b0[NR], b1[NR];
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                b0[x] = transpose8(pack2(t[x][0], t[x][1]));
+                b1[x] = transpose8(pack2(t[x][2], t[x][3]));
+            }
+            const int key = (lane & 7) + 8 * (lane >> 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t va[4];
+                ldsm_x4_t(st + (uint32_t)(4096 + key * 256 + (((2 * j + ((lane >> 3) & 1)) ^ (key & 7)) << 4)), va[0], va[1], va[2], va[3]);
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+                    mma_bf16(o[x][j], va, b0[x], b1[x]);
+            }
         }
+    };
+    auto all_see = [&](int row, int end) { return end <= all_hi && (row >= all_lo || end <= a.n_first); };
+    if constexpr (kPack) {
+        for (int stage = 0; it < n_p; it += step, stage = stage + 1 == R::kPackStages ? 0 : stage + 1) {
+            copies_wait<R::kPackStages - 1>();
+            __syncwarp();
+            const int row0 = (it < tl.n[0] ? tl.t0[0] + it : tl.t0[1] + it - tl.n[0]) * kPdPacked;
+            const bool all = all_see(row0, row0 + kPdPacked);
+            // (a loop, which the instruction cache holds)
+#pragma unroll 1
+            for (int k = 0; k < kPdPacked / kPdKeys; ++k)
+                step16(std::true_type(), row0 + kPdKeys * k, ring + (uint32_t)(stage * kPackBytes + k * kPackStep), all);
+            __syncwarp();
+            issue_packed(it + R::kPackStages * step, stage);
+        }
+        issue(it, 0);   // (the ring is free: what was in flight behind the last tile is nothing)
+    }
+    for (int stage = 0; it < n_t; it += step, stage = stage + 1 == R::kKeyStages ? 0 : stage + 1) {
+        copies_wait<R::kKeyStages - 1>();
         __syncwarp();
-        issue(it + 2 * step, stage);
+        const int row0 = (it < n_p + tl.n[2] ? tl.t0[2] + it - n_p : tl.t0[3] + it - n_p - tl.n[2]) * kPdKeys;
+        step16(std::false_type(), row0, ring + (uint32_t)(stage * kPdKeyBytes), all_see(row0, row0 + kPdKeys));
+        __syncwarp();
+        issue(it + R::kKeyStages * step, stage);
     }
     copies_wait<0>();
     __syncwarp();
 
     // the warp's state over its ring
-    auto area = [&](int w) { return reinterpret_cast<float *>(pd_smem + w * kPdRing); };
+    auto area = [&](int w) { return reinterpret_cast<float *>(pd_smem + w * R::kBytes); };
     {
         float *f = area(warp);
 #pragma unroll
@@ -487,8 +510,8 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 if (n == 0) {
-                    f[16 * kPdPitch + r] = m_run[x][e];
-                    f[16 * kPdPitch + 16 + r] = v;
+                    f[8 * NR * kPdPitch + r] = m_run[x][e];
+                    f[8 * NR * kPdPitch + 8 * NR + r] = v;
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -512,18 +535,18 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
     };
     const int col = 4 * lane;
-    float *joined = reinterpret_cast<float *>(pd_smem + kPdStage);   // behind warp 0's state: [16][128], 16 maxima, 16 sums
+    float *joined = reinterpret_cast<float *>(pd_smem + R::kOffJoined);   // [8 NR][128], maxima, sums
     for (int r = warp; r < rows; r += kPdWarps) {
         float M = kNothing, L = 0.f;
 #pragma unroll
         for (int w = 0; w < kPdWarps; ++w)
-            M = fmaxf(M, area(w)[16 * kPdPitch + r]);
+            M = fmaxf(M, area(w)[8 * NR * kPdPitch + r]);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kPdWarps; ++w) {
-            const float f = dec_ex2(area(w)[16 * kPdPitch + r] - M);
+            const float f = dec_ex2(area(w)[8 * NR * kPdPitch + r] - M);
             const float4 x = *reinterpret_cast<const float4 *>(area(w) + r * kPdPitch + col);
-            L = fmaf(area(w)[16 * kPdPitch + 16 + r], f, L);
+            L = fmaf(area(w)[8 * NR * kPdPitch + 8 * NR + r], f, L);
             v.x = fmaf(x.x, f, v.x);
             v.y = fmaf(x.y, f, v.y);
             v.z = fmaf(x.z, f, v.z);
@@ -534,8 +557,8 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
         } else {
             *reinterpret_cast<float4 *>(joined + r * 128 + col) = v;
             if (lane == 0) {
-                joined[16 * 128 + r] = M;
-                joined[16 * 128 + 16 + r] = L;
+                joined[8 * NR * 128 + r] = M;
+                joined[8 * NR * 128 + 8 * NR + r] = L;
             }
         }
     }
@@ -546,11 +569,11 @@ __global__ void __launch_bounds__(kPdThreads, kPdCtas)
     for (int r = (int)rank + n_ctas * warp; r < rows; r += n_ctas * kPdWarps) {
         float M = kNothing, L = 0.f;
         for (int k = 0; k < n_ctas; ++k)
-            M = fmaxf(M, ld_cluster1(at_rank(mine + 4u * (uint32_t)(16 * 128 + r), (uint32_t)k)));
+            M = fmaxf(M, ld_cluster1(at_rank(mine + 4u * (uint32_t)(8 * NR * 128 + r), (uint32_t)k)));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k = 0; k < n_ctas; ++k) {
-            const float mk = ld_cluster1(at_rank(mine + 4u * (uint32_t)(16 * 128 + r), (uint32_t)k));
-            const float lk = ld_cluster1(at_rank(mine + 4u * (uint32_t)(16 * 128 + 16 + r), (uint32_t)k));
+            const float mk = ld_cluster1(at_rank(mine + 4u * (uint32_t)(8 * NR * 128 + r), (uint32_t)k));
+            const float lk = ld_cluster1(at_rank(mine + 4u * (uint32_t)(8 * NR * 128 + 8 * NR + r), (uint32_t)k));
             const float4 x = ld_cluster(at_rank(mine + 4u * (uint32_t)(r * 128 + col), (uint32_t)k));
             const float f = dec_ex2(mk - M);
             L = fmaf(lk, f, L);
@@ -572,41 +595,55 @@ cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevP
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(k_page_decode<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPdSmem)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(k_page_decode<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPdSmem)) != cudaSuccess)
+        auto allow = [&](auto *k, int smem) {
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        };
+        allow(k_page_decode<1, false>, Ring<1, false>::kSmem);
+        allow(k_page_decode<2, false>, Ring<2, false>::kSmem);
+        allow(k_page_decode<1, true>, Ring<1, true>::kSmem);
+        allow(k_page_decode<2, true>, Ring<2, true>::kSmem);
+        if (e != cudaSuccess)
             return e;
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
     }
     const int units = a.n_layers * a.n_kv_heads, G = a.n_q_heads / a.n_kv_heads;
-    int64_t few = 0, tiles = 0;
+    int64_t few = 0, bytes = 0;   // of one unit's tiles
     int rows = 0;
+    bool packed = false;
     for (int b = 0; b < a.n_reqs; ++b) {
         const int64_t r = host_reqs[b].q_len * (int64_t)G;
         if (r == 0 || r > kPageFewRows)
             continue;
         TileList tl;
         tl.set(host_reqs[b], a.window, a.n_first);
-        tiles += tl.total();
+        bytes += (int64_t)(tl.n[0] + tl.n[1]) * kPackBytes + (int64_t)(tl.n[2] + tl.n[3]) * kPdKeyBytes;
+        packed = packed || tl.n[0] + tl.n[1] > 0;
         rows = std::max(rows, (int)r);
         ++few;
     }
     if (few == 0)
         return cudaSuccess;
-    // CTAs of a (request, unit): the largest share of an SM decides, its CTAs' tiles (0.2 us
-    // each when the SM is full, slower with one or two CTAs on it) and 1.5 us more for each.
-    // One request of 33,280 packed rows, 256 units: 819 us with one, 2.0 CTAs an SM.
+    // CTAs of a (request, unit): the largest share of an SM decides, its CTAs' bytes (44 GB/s
+    // when the SM is full, less with one or two CTAs on it) and 1.5 us more for each.  One
+    // request of 33,280 packed rows, 256 units: 819 us with one, 1.7 CTAs an SM.
     int c = 1;
     double best = 1e30;
     for (int k = 1; k <= 8; k *= 2) {
         const double load = (double)((few * units * k + n_sms - 1) / n_sms);
-        const double t1 = load * (0.2 * (double)tiles / (double)(few * k) + 1.5) * (load < 2. ? 2.2 : load < 3. ? 1.3 : 1.);
+        const double t1 = load * ((double)bytes / (double)(few * k) / 44e3 + 1.5) * (load < 2. ? 2.2 : load < 3. ? 1.3 : 1.);
         if (t1 < 0.97 * best) {
             best = t1;
             c = k;
         }
     }
-    return launch_cluster(rows <= 8 ? k_page_decode<1> : k_page_decode<2>, (int64_t)a.n_reqs * units * c, kPdThreads, kPdSmem, c, s, a, t, c);
+    auto launch = [&](auto *k, int smem) {
+        return launch_cluster(k, (int64_t)a.n_reqs * units * c, kPdThreads, smem, c, s, a, t, c);
+    };
+    if (packed)
+        return rows <= 8 ? launch(k_page_decode<1, true>, Ring<1, true>::kSmem) : launch(k_page_decode<2, true>, Ring<2, true>::kSmem);
+    return rows <= 8 ? launch(k_page_decode<1, false>, Ring<1, false>::kSmem) : launch(k_page_decode<2, false>, Ring<2, false>::kSmem);
 }
 
 }  // namespace kvr
