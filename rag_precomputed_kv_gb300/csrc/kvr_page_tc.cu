@@ -8,7 +8,9 @@
 // rows' and the window's.
 //
 //   warps 0-3, 4-7  softmax of tile A, B, a row a thread, and its output;
-//   warp 8          loads by TMA: a tile's pages are boxes of 16 to 128 rows, one a
+//   warp 8          works out each item's block of rows and its tiles, and passes them to
+//                   the others through a ring of three (each role on its own took 9 us at
+//                   every item boundary), then loads by TMA: a tile's pages are boxes of 16 to 128 rows, one a
 //                   lane, so that a tile of 16-row pages takes no longer to issue;
 //   warp 9          tcgen05 products; rows of V that no query of the block sees become
 //                   zeros first (their weight is 0, but 0 x NaN is NaN);
@@ -48,6 +50,7 @@ constexpr int kPtRegsLaunch = 168, kPtRegsSoftmax = 200, kPtRegsOther = 104;
 static_assert(2 * 128 * kPtRegsSoftmax + 128 * kPtRegsOther <= kPtThreads * kPtRegsLaunch, "register split");
 constexpr int kPtTile = 128;                        // keys per tile, rows per query tile
 constexpr int kPtSlots = 5;                         // K/V ring
+constexpr int kPtGeos = 3;                          // geometry ring
 constexpr int kPtTileBytes = kPtTile * 128 * 2;     // 32 KB
 constexpr int kPtPanel = kPtTileBytes / 2;
 constexpr int kPtTmemCols = 512;
@@ -60,9 +63,11 @@ constexpr int kPtOffKV = 2 * kPtTileBytes;
 constexpr int kPtOffBar = kPtOffKV + kPtSlots * kPtTileBytes;
 constexpr int kTbFull = 0, kTbEmpty = kTbFull + kPtSlots, kTbS = kTbEmpty + kPtSlots, kTbP = kTbS + 2, kTbO = kTbP + 2,
               kTbOEmpty = kTbO + 2, kTbQ = kTbOEmpty + 2, kTbQEmpty = kTbQ + 1, kTbDrain = kTbQEmpty + 1,
-              kTbJob = kTbDrain + 1, kTbNum = kTbJob + kPtSlots;
+              kTbJob = kTbDrain + 1, kTbGeo = kTbJob + kPtSlots, kTbGeoFree = kTbGeo + kPtGeos, kTbNum = kTbGeoFree + kPtGeos;
 constexpr int kPtOffMisc = kPtOffBar + 8 * kTbNum;
-constexpr int kPtSmem = kPtOffMisc + 16 + 1024;     // + alignment slack
+constexpr int kPtOffGeo = (kPtOffMisc + 16 + 15) & ~15;
+constexpr int kPtGeoBytes = 160;
+constexpr int kPtSmem = kPtOffGeo + kPtGeos * kPtGeoBytes + 1024;     // + alignment slack
 static_assert(kPtSmem <= 227 * 1024, "shared memory budget");
 
 constexpr uint32_t kPtIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kPtTile >> 3) << 17) |
@@ -84,20 +89,24 @@ __device__ __forceinline__ float2 *part_ml(float *part, int64_t slot, int x)
 }
 
 // One block of query rows, and the key tiles of it that an item takes.
-struct Block {
+struct alignas(16) Block {
     DevPageReq rq;
-    int lh;
+    int lh, l, h;
     int row0, rows, nx;      // first packed row in the request, rows (<= 256), 128-row tiles
     int hi, lo, few;         // rows that some query of the block sees: j < hi and (j >= lo or j < few)
     int p0, p1;              // positions of its first and last token
     int n_first, t_win;      // tiles of the first rows; the window's first tile
     int jb, je;              // the item's tiles of the list
 
+    int64_t unit;            // elements from a page's start to the (layer, kv-head)'s first row
+
     __device__ __forceinline__ int tile(int i) const { return i < n_first ? i : t_win + i - n_first; }
     __device__ __forceinline__ bool seen(int j) const { return j < hi && (j >= lo || j < few); }
     __device__ __forceinline__ bool all_seen(int j0, int j1) const { return j1 <= hi && (j0 >= lo || j1 <= few); }
     __device__ __forceinline__ bool some_seen(int j0, int j1) const { return j0 < few || (j0 < hi && j1 > lo); }
 };
+
+static_assert(sizeof(Block) <= kPtGeoBytes, "geometry ring");
 
 __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p, const DevPageReq *reqs, int64_t w)
 {
@@ -113,6 +122,9 @@ __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p
             hi = mid - 1;
     }
     s.rq = reqs[lo];
+    s.l = s.lh / a.n_kv_heads;
+    s.h = s.lh - s.l * a.n_kv_heads;
+    s.unit = s.l * a.g.s_layer + s.h * a.g.s_head;
     const int G = a.n_q_heads / a.n_kv_heads, all = s.rq.q_len * G, mb = (all + 255) >> 8;
     const int i = in_unit - s.rq.item0, blk = mb - 1 - i / p.splits, sp = i % p.splits;   // (the last blocks see most: first)
     s.row0 = blk * 256;
@@ -172,6 +184,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         for (int i = 0; i < kTbNum; ++i)
             mbar_init(bar(i), i < kTbEmpty ? 3u
                               : (i >= kTbP && i < kTbP + 2) || (i >= kTbOEmpty && i < kTbOEmpty + 2) ? 128u
+                              : i >= kTbGeoFree ? 11u
                                                                                                     : 1u);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -187,6 +200,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kPtOffMisc);
+    // the CTA's item i: its geometry, once it is there; at last free it for item i + kPtGeos
+    auto geo = [&](int i) -> const Block & { return *reinterpret_cast<const Block *>(smem + kPtOffGeo + i % kPtGeos * kPtGeoBytes); };
+    auto geo_wait = [&](int i) -> bool {
+        return mbar_wait_warp(bar(kTbGeo + i % kPtGeos), (uint32_t)(i / kPtGeos) & 1, abort_flag);
+    };
+    auto geo_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar(kTbGeoFree + i % kPtGeos));
+    };
+    const int n_items = (int)((p.total - blockIdx.x + gridDim.x - 1) / gridDim.x);
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPtRegsSoftmax));
@@ -197,16 +221,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const float sc = a.scale_log2;
         int s_cnt = 0, o_cnt = 0;
         bool ok = true;
-        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-            const Block b = block_at(a, p, reqs, w);
-            if (x >= b.nx)
+        for (int item = 0; item < n_items; ++item) {
+            if (!geo_wait(item)) {
+                ok = false;
+                break;
+            }
+            // (read where it is needed: the scores leave few registers)
+            const Block &b = geo(item);
+            if (x >= b.nx) {
+                geo_done(item);
                 continue;
-            const bool row_ok = x * 128 + r < b.rows;
+            }
             // a warp without rows of its own only keeps the barriers going
             const bool idle = x * 128 + (warp & 3) * 32 >= b.rows;
-            const int tok = (b.row0 + x * 128 + r) / G, pos = b.rq.pos0 + tok;
-            const Sees see = sees(a, b.rq, pos);
-            const int all_hi = min(b.rq.kv_len, b.p0 + 1), all_lo = a.window > 0 ? b.p1 - a.window + 1 : 0;
+            const int pos = b.rq.pos0 + (b.row0 + x * 128 + r) / G;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = b.jb; j < b.je; ++j) {
                 if (!mbar_wait_warp(bar(kTbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
@@ -225,12 +253,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 for (int q = 0; q < 4; ++q)
                     tmem_ld32(lane_base + pt_col_s(x) + 32 * q, s + 32 * q);
                 tmem_wait_ld();
-                const int k0 = b.tile(j) * kPtTile;
-                if (!(k0 + kPtTile <= all_hi && (k0 >= all_lo || k0 + kPtTile <= a.n_first))) {
+                const int k0 = b.tile(j) * kPtTile, k1 = k0 + kPtTile;
+                if (!(k1 <= min(b.rq.kv_len, b.p0 + 1) && (a.window == 0 || k0 > b.p1 - a.window || k1 <= a.n_first))) {
+                    const Sees see = sees(a, b.rq, pos);
                     const int hi = see.hi - k0, lo = see.lo - k0, few = see.few - k0;
+                    if (hi < kPtTile) {
 #pragma unroll
-                    for (int c = 0; c < kPtTile; ++c)
-                        s[c] = (c < hi && (c >= lo || c < few)) ? s[c] : -INFINITY;
+                        for (int c = 0; c < kPtTile; ++c)
+                            s[c] = c < hi ? s[c] : -INFINITY;
+                    }
+                    if (lo > 0) {
+#pragma unroll
+                        for (int c = 0; c < kPtTile; ++c)
+                            s[c] = (c >= lo || c < few) ? s[c] : -INFINITY;
+                    }
                 }
                 float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -301,13 +337,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 ++o_cnt;
                 tc_fence_after();
             }
+            const int row = b.row0 + x * 128 + r, tok = row / G;
+            const bool row_ok = x * 128 + r < b.rows;
+            const Sees see = sees(a, b.rq, pos);
+            const bool some = row_ok && any && see.hi > 0 && (see.few > 0 || see.lo < see.hi);
             if (p.splits == 1) {   // the row's output
-                const int l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
-                const int g = b.row0 + x * 128 + r - tok * G;
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                       (((int64_t)l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + h * G + g) * 128);
-                const bool some = any && see.hi > 0 && (see.few > 0 || see.lo < see.hi);
-                if (row_ok && some && !(l_run > 0.f && l_run < INFINITY))
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                       (((int64_t)b.l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + b.h * G + (row - tok * G)) * 128);
+                if (some && !(l_run > 0.f && l_run < INFINITY))
                     atomicCAS(a.err, kDevOk, kDevBadInput);
                 const float inv = 1.f / l_run;
 #pragma unroll
@@ -323,11 +360,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             o[i] = some ? o[i] * inv : 0.f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            dst[4 * q + i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                            out[4 * q + i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
                                                         pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
                     }
                 }
             } else {
+                const int64_t w = blockIdx.x + (int64_t)item * gridDim.x;
                 if (row_ok)
                     part_ml(p.part, w, x)[r] = make_float2(m_run, l_run);
                 float4 *po = part_o(p.part, w, x) + r;
@@ -349,6 +387,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 tc_fence_before();
                 mbar_arrive(bar(kTbOEmpty + x));
             }
+            geo_done(item);
         }
         if (!ok)
             give_up(a.err, abort_flag);
@@ -357,15 +396,47 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         pdl_wait_prerequisites();
         bool ok = true;
         int tt = 0, nq = 0;
-        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-            const Block b = block_at(a, p, reqs, w);
+        // item i's geometry into the ring, once the others are done with item i - kPtGeos'
+        auto publish = [&](int i) -> bool {
+            if (i >= n_items)
+                return true;
+            const Block b = block_at(a, p, reqs, blockIdx.x + (int64_t)i * gridDim.x);
+            const int slot = i % kPtGeos;
+            if (i >= kPtGeos && !mbar_wait_warp(bar(kTbGeoFree + slot), (uint32_t)(i / kPtGeos - 1) & 1, abort_flag))
+                return false;
+            if (lane == 0) {
+                *reinterpret_cast<Block *>(smem + kPtOffGeo + slot * kPtGeoBytes) = b;
+                mbar_arrive(bar(kTbGeo + slot));
+            }
+            __syncwarp();
+            return true;
+        };
+        ok = publish(0);
+        for (int item = 0; item < n_items && ok; ++item) {
+            const Block &b = geo(item);
+            if (!(ok = publish(item + 1)))
+                break;
             const int n_loads = 2 * (b.je - b.jb);
             if (n_loads == 0)
                 continue;
-            const int l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
-            const int64_t unit = (l * a.g.s_layer + h * a.g.s_head) / 128;
+            const int64_t unit = b.unit / 128;
+            // tile i of the item: the row of this lane's box (box lane / 2, panel lane & 1) and whether
+            // it is to be loaded; the same for keys and values
+            const int at = (lane >> 1) * p.box;
+            int row = 0;
+            bool tma = false, load = false;
+            auto find = [&](int i) {
+                const int k = b.tile(i), j0 = k * kPtTile + at;
+                tma = by_tma(p, b, k);
+                load = tma && at < kPtTile && b.some_seen(j0, j0 + p.box);
+                if (load) {
+                    const int pg = j0 / a.g.rows;
+                    row = (int)((int64_t)page_id(b.rq, ids, pg) * (a.g.s_page / 128) + unit + (j0 - pg * a.g.rows));
+                }
+            };
+            find(b.jb);
             for (int i = 0; i <= n_loads; ++i) {
-                if (i == min(2, n_loads)) {   // the queries after the first K and V tile
+                if (i == 2) {   // the queries after the first K and V tile
                     if (nq > 0 && !mbar_wait_warp(bar(kTbQEmpty), (uint32_t)(nq - 1) & 1, abort_flag)) {
                         ok = false;
                         break;
@@ -383,29 +454,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 if (i == n_loads)
                     break;
-                const int slot = tt % kPtSlots, k = b.tile(b.jb + (i >> 1));
-                // lane: a box of the tile and a panel; its page is looked up while the slot is still used
-                int row = 0;
-                bool load = false;
-                const int at = (lane >> 1) * p.box, j0 = k * kPtTile + at;
-                const bool tma = by_tma(p, b, k);
-                if (tma && at < kPtTile && b.some_seen(j0, j0 + p.box)) {
-                    const int pg = j0 / a.g.rows;
-                    row = (int)((int64_t)page_id(b.rq, ids, pg) * (a.g.s_page / 128) + unit + (j0 - pg * a.g.rows));
-                    load = true;
-                }
+                const int slot = tt % kPtSlots;
                 const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
                 if (tt >= kPtSlots && !mbar_wait_warp(bar(kTbEmpty + slot), (uint32_t)(tt / kPtSlots - 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
                 if (lane == 0) {
+                    mbar_arrive(bar(kTbFull + slot));
                     if (tma) {
-                        mbar_arrive(bar(kTbFull + slot));
                         mbar_arrive(bar(kTbFull + slot));
                         mbar_expect_tx(bar(kTbFull + slot), boxes * (uint32_t)p.box * 128u);
                     } else {
-                        mbar_arrive(bar(kTbFull + slot));
                         mbar_arrive(bar(kTbJob + slot));
                     }
                 }
@@ -413,6 +473,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (load)
                     tma_load_2d(sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes + (lane & 1) * kPtPanel + at * 128), (i & 1) ? &tmv : &tmk,
                                 64 * (lane & 1), row, bar(kTbFull + slot));
+                if ((i & 1) && i + 1 < n_loads)
+                    find(b.jb + (i >> 1) + 1);
                 ++tt;
             }
         }
@@ -458,11 +520,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 mma_ts(lead, tmem + pt_col_o(x), tmem + pt_col_s(x) + 8 * i, desc_with_lo(vb + ((i * 2048) >> 4), hi_v), kPtIdescPV,
                        i > 0 ? 1u : acc0);
         };
-        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-            const Block b = block_at(a, p, reqs, w);
+        for (int item = 0; item < n_items && ok; ++item) {
+            if (!geo_wait(item)) {
+                ok = false;
+                break;
+            }
+            const Block &b = geo(item);
             const int K = b.je - b.jb;
-            if (K == 0)
+            if (K == 0) {
+                geo_done(item);
                 continue;
+            }
             // V tile i of the item: landed, its rows that no query sees zeroed
             auto wait_v = [&](int i) -> bool {
                 if (!wait_kv(tt + 2 * i + 1))
@@ -544,6 +612,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     umma_commit(lead, bar(kTbEmpty + (tt + 2 * i + 2) % kPtSlots));
             }
             tt += 2 * K;
+            geo_done(item);
         }
         if (!ok)
             give_up(a.err, abort_flag);
@@ -556,21 +625,37 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         bool ok = true;
         int tt = 0;
         uint32_t jobs = 0;   // bit s: the parity of slot s's next job
-        for (int64_t w = blockIdx.x; w < p.total && ok; w += gridDim.x) {
-            const Block b = block_at(a, p, reqs, w);
-            const int n_loads = 2 * (b.je - b.jb), l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
-            const int64_t unit = l * a.g.s_layer + h * a.g.s_head;
+        for (int item = 0; item < n_items && ok; ++item) {
+            if (!geo_wait(item)) {
+                ok = false;
+                break;
+            }
+            const Block &b = geo(item);
+            const int n_loads = 2 * (b.je - b.jb);
+            // where the two sub-blocks of a packed tile are, one tile ahead of what reads them
+            const uint8_t *at[2] = {nullptr, nullptr}, *at_next[2] = {nullptr, nullptr};
+            auto find = [&](int i, const uint8_t *(&to)[2]) {
+                if (i >= b.je)
+                    return;
+                const int k = b.tile(i);
+                if (!by_tma(p, b, k))
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int j0 = k * kPtTile + 64 * half + 32 * y;
+                        if (j0 < b.rq.packed_len && b.some_seen(j0, j0 + 32))
+                            to[y] = a.g.packed + packed_block(a, b.rq, ids, b.lh, j0);
+                    }
+            };
             // Sub-block q of the item's loads (two of 32 rows a load): what it reads, ahead.
             // Keys: lane 4 n + c: codes of row 8 i + n in r[4 i ..], its scales in r[16 + 2 i ..].
             // Values: lane 16 i' + 4 c + g: in pass x, the words of rows 8 i + 2 c, + 1 (i = 2 x + i'),
             // group g, n = 0..7, in r[8 x ..], the two scales in r[16 + x].
-            auto fetch = [&](int q, uint32_t (&r)[24]) {
+            auto fetch = [&](int q, const uint8_t *src, uint32_t (&r)[24]) {
                 if (q >= 2 * n_loads)
                     return;
                 const int k = b.tile(b.jb + (q >> 2)), j0 = k * kPtTile + 64 * half + 32 * (q & 1);
                 if (by_tma(p, b, k) || j0 >= b.rq.packed_len || !b.some_seen(j0, j0 + 32))
                     return;
-                const uint8_t *src = a.g.packed + packed_block(a, b.rq, ids, b.lh, j0);
                 if (!(q & 2)) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -613,7 +698,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (b.seen(j)) {
                             const int pg = j / a.g.rows;
-                            const int64_t at = (int64_t)page_id(b.rq, ids, pg) * a.g.s_page + unit + (int64_t)(j - pg * a.g.rows) * 128;
+                            const int64_t at = (int64_t)page_id(b.rq, ids, pg) * a.g.s_page + b.unit + (int64_t)(j - pg * a.g.rows) * 128;
                             v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(values ? a.g.v : a.g.k) + at) + ch);
                         }
                         put(tile, in + row, ch, v.x, v.y, v.z, v.w);
@@ -652,28 +737,38 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
             };
             uint32_t r0[24], r1[24];
-            fetch(0, r0);
+            find(b.jb, at);
+            find(b.jb + 1, at_next);
+            fetch(0, at[0], r0);
             for (int i = 0; i < n_loads; ++i, ++tt) {
                 const int slot = tt % kPtSlots;
+                const bool last = (i & 1) != 0;   // the tile's values: what follows is the next tile
                 if (by_tma(p, b, b.tile(b.jb + (i >> 1)))) {
-                    fetch(2 * (i + 1), r0);
-                    continue;
+                    if (last)
+                        fetch(2 * (i + 1), at_next[0], r0);
+                } else {
+                    if (!mbar_wait_warp(bar(kTbJob + slot), (jobs >> slot) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    jobs ^= 1u << slot;
+                    const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
+                    fetch(2 * i + 1, at[1], r1);
+                    store(2 * i, r0, tile);
+                    fetch(2 * i + 2, last ? at_next[0] : at[0], r0);
+                    store(2 * i + 1, r1, tile);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar(kTbFull + slot));
                 }
-                if (!mbar_wait_warp(bar(kTbJob + slot), (jobs >> slot) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
+                if (last) {
+                    at[0] = at_next[0];
+                    at[1] = at_next[1];
+                    find(b.jb + (i >> 1) + 2, at_next);
                 }
-                jobs ^= 1u << slot;
-                const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
-                fetch(2 * i + 1, r1);
-                store(2 * i, r0, tile);
-                fetch(2 * i + 2, r0);
-                store(2 * i + 1, r1, tile);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(kTbFull + slot));
             }
+            geo_done(item);
         }
         if (!ok)
             give_up(a.err, abort_flag);
