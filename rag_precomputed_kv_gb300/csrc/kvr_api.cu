@@ -24,6 +24,7 @@
 #include <vector>
 
 #include "kvr_internal.cuh"
+#include "kvr_page_common.cuh"
 
 using namespace kvr;
 
@@ -2159,34 +2160,48 @@ kvr_status page_ready(kvr_pool *p, const PagePlan &pl, cudaStream_t s)
 }
 
 // The tensor-core kernel's items: 256-row blocks of the requests of more than
-// kPageFewRows query rows, each in `splits` stretches of its key tiles.
-kvr_status page_tc_plan(const kvr_pool *p, PagePlan &pl, const kvr_pages &g, int32_t window, int32_t n_first, PageTcArgs &tc)
+// kPageFewRows query rows, each in `splits` stretches of its key tiles; and the slices
+// of the units whose restored rows fit kMaxPartBytes.
+kvr_status page_tc_plan(const kvr_pool *p, PagePlan &pl, const kvr_pages &g, int32_t window, int32_t n_first, PageTcArgs &tc, int &lh_slice)
 {
-    const int D = p->d.head_dim, G = p->d.n_q_heads / p->d.n_kv_heads;
-    const int64_t units = (int64_t)p->d.n_layers * p->d.n_kv_heads;
+    const int D = p->d.head_dim, G = p->d.n_q_heads / p->d.n_kv_heads, LH = p->d.n_layers * p->d.n_kv_heads;
     // boxes of the largest power of two of rows that no page boundary cuts
     tc.box = 128;
     while (g.page_rows % tc.box)
         tc.box /= 2;
     if (tc.box < 16 || g.stride[0] % D || g.stride[1] % D || g.stride[2] % D || page_extent(*p, g) / D > (int64_t)INT32_MAX - 256)
         tc.box = 0;
-    int64_t blocks = 0, tiles = 0;
-    for (const DevPageReq &r : pl.rq) {
+    int64_t blocks = 0, tiles = 0, rest = 0;
+    for (DevPageReq &r : pl.rq) {
+        r.tile0 = (int32_t)rest;
         if (r.q_len * (int64_t)G <= kPageFewRows)
             continue;
         if (r.q_len * (int64_t)G > INT32_MAX - 256)
             return fail(KVR_ERR_UNSUPPORTED, "too many query rows");
-        const int64_t n = (r.q_len * (int64_t)G + 255) / 256, hi = std::min<int64_t>(r.kv_len, (int64_t)r.pos0 + r.q_len);
+        const int64_t n = (r.q_len * (int64_t)G + 255) / 256;
+        const int32_t hi = std::min<int32_t>(r.kv_len, r.pos0 + r.q_len);
+        const int32_t lo = std::min(hi, window > 0 ? std::max(0, r.pos0 - window + 1) : 0);
         const int64_t seen = window > 0 ? std::min<int64_t>(hi, (int64_t)window + n_first + 256 / G) : hi;
         blocks += n;
         tiles += n * ((seen + 127) / 128);
+        const page::RestTiles t = page::rest_tiles(hi, lo, std::min(n_first, lo), r.packed_len);
+        if (r.packed_len > 0)
+            rest += t.first + std::max(0, t.end - t.win);
+        if (rest > (INT32_MAX - 256) / 128)
+            return fail(KVR_ERR_UNSUPPORTED, "too many packed rows for queries of more than 16 rows");
     }
-    // The time of a call in units of a key tile (1.45 us): rounds of items, each its tiles
+    tc.unit_tiles = (int32_t)rest;
+    lh_slice = LH;
+    if (rest > 0) {
+        const int64_t fit = std::max<int64_t>(1, kMaxPartBytes / (rest * kPageTileBytes * 2)), n = (LH + fit - 1) / fit;
+        lh_slice = (int)((LH + n - 1) / n);
+    }
+    // The time of a slice in units of a key tile (1.45 us): rounds of items, each its tiles
     // and 3 more, and for partial results 4 more and their traffic (266 KB an item).
     const double nt = (double)tiles / (double)std::max<int64_t>(1, blocks);
     double best = 1e30;
     for (int sp = 1; sp <= 32 && (sp == 1 || nt / sp >= 4.); ++sp) {
-        const double items = (double)(blocks * units) * sp;
+        const double items = (double)(blocks * lh_slice) * sp;
         const double t = std::ceil(items / p->n_sms) * (nt / sp + 3.) + (sp > 1 ? 4. + items * 266e3 / 6e6 / 1.45 : 0.);
         if (t < 0.97 * best) {
             best = t;
@@ -2202,7 +2217,6 @@ kvr_status page_tc_plan(const kvr_pool *p, PagePlan &pl, const kvr_pages &g, int
             item += (int32_t)((r.q_len * (int64_t)G + 255) / 256) * tc.splits;
     }
     tc.unit_items = item;
-    tc.total = item * units;
     return KVR_OK;
 }
 
@@ -2473,21 +2487,36 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
             return st;
         DeviceGuard g(p->device);
         PageTcArgs tc{};
-        CUtensorMap mq, mk, mv;
+        PageTcMaps maps{};
+        CUtensorMap mq, mk, mv, mrk, mrv;
+        const int LH = L * p->d.n_kv_heads;
+        int lh_slice = LH;
         if (many) {
             if (!use_tensor_cores(*p))
                 return fail(KVR_ERR_UNSUPPORTED, "more than 16 query rows need the tensor-core kernel (sm_103)");
             if (q_rows > (int64_t)INT32_MAX - 256)
                 return fail(KVR_ERR_UNSUPPORTED, "query rows exceed the int32 TMA coordinate range");
-            if ((st = page_tc_plan(p, pl, *pages, window, n_first, tc)) != KVR_OK || (st = p->grow_query_scratch((size_t)(q_rows * D) * 2)) != KVR_OK ||
-                (tc.splits > 1 && (st = p->grow_part_scratch((size_t)(tc.total * kPagePartBytes))) != KVR_OK) ||
+            if ((st = page_tc_plan(p, pl, *pages, window, n_first, tc, lh_slice)) != KVR_OK)
+                return st;
+            // scratch: restored keys, restored values, partial results
+            const int64_t rest_rows = (int64_t)lh_slice * tc.unit_tiles * 128, rest_bytes = rest_rows * D * 2;
+            const int64_t part_bytes = tc.splits > 1 ? (int64_t)lh_slice * tc.unit_items * kPagePartBytes : 0;
+            if (rest_rows > (int64_t)INT32_MAX - 256)
+                return fail(KVR_ERR_UNSUPPORTED, "restored rows exceed the int32 TMA coordinate range");
+            if ((st = p->grow_query_scratch((size_t)(q_rows * D) * 2)) != KVR_OK ||
+                (st = p->grow_part_scratch((size_t)(2 * rest_bytes + part_bytes))) != KVR_OK ||
                 (st = encode_rows_map(*p, p->q_rot, q_rows, 128, &mq)) != KVR_OK)
                 return st;
-            tc.part = static_cast<float *>(p->part);
+            tc.rest_k = p->part;
+            tc.rest_v = static_cast<char *>(p->part) + rest_bytes;
+            tc.part = reinterpret_cast<float *>(static_cast<char *>(p->part) + 2 * rest_bytes);
             const int64_t rows = page_extent(*p, *pages) / D;
-            if (tc.box && ((st = encode_rows_map(*p, pages->k, rows, tc.box, &mk)) != KVR_OK ||
-                           (st = encode_rows_map(*p, pages->v, rows, tc.box, &mv)) != KVR_OK))
+            if ((tc.box && ((st = encode_rows_map(*p, pages->k, rows, tc.box, &mk)) != KVR_OK ||
+                            (st = encode_rows_map(*p, pages->v, rows, tc.box, &mv)) != KVR_OK)) ||
+                (rest_rows && ((st = encode_rows_map(*p, tc.rest_k, rest_rows, 128, &mrk)) != KVR_OK ||
+                               (st = encode_rows_map(*p, tc.rest_v, rest_rows, 128, &mrv)) != KVR_OK)))
                 return st;
+            maps = {&mq, tc.box ? &mk : &mq, tc.box ? &mv : &mq, rest_rows ? &mrk : &mq, rest_rows ? &mrv : &mq};
             // the previous call's attention must be done with the scratch
             cudaError_t e;
             if (p->q_rot_used && (e = cudaStreamWaitEvent(s, p->q_rot_done, 0)) != cudaSuccess)
@@ -2513,7 +2542,13 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
         if (e == cudaSuccess && !tensor)
             e = launch_page_simt(a, pl.tab, p->d.dtype, D, s);
         if (e == cudaSuccess && many) {
-            e = launch_page_tc(a, tc, pl.tab, p->q_rot, &mq, tc.box ? &mk : &mq, tc.box ? &mv : &mq, p->n_sms, s);
+            e = launch_page_queries(a, pl.tab, p->q_rot, s);
+            for (int lh = 0; lh < LH && e == cudaSuccess; lh += lh_slice) {
+                tc.lh_base = lh;
+                const int n = std::min(lh_slice, LH - lh);
+                tc.total = (int64_t)n * tc.unit_items;
+                e = launch_page_tc(a, tc, pl.tab, maps, n, p->n_sms, s);
+            }
             cudaEventRecord(p->q_rot_done, s);
             p->q_rot_used = true;
         }

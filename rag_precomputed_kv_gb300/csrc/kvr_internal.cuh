@@ -451,7 +451,7 @@ constexpr int kPackPart = 16 * 128 / 2 + 16 * (128 / kPackGroup) * 2;
 constexpr int kPackStep = 2 * kPackPart, kPackBytes = kPackRows / 16 * kPackStep;
 static_assert(kPackBytes == 4608, "packed block layout");
 
-// Per-request data (48 bytes).  Page g of a request is entry g + off[0] of the
+// Per-request data (64 bytes).  Page g of a request is entry g + off[0] of the
 // call's list of page numbers where g < few, else entry g + off[1] (a window's
 // list leaves out the pages between the first rows and the window).
 struct alignas(16) DevPageReq {
@@ -462,8 +462,10 @@ struct alignas(16) DevPageReq {
     int32_t few, off[2];    // pages
     int32_t pfew, poff[2];  // packed pages
     int32_t item0;          // first work item of a unit (tensor-core kernel)
+    int32_t tile0;          // first tile of a unit's restored rows (tensor-core kernel)
+    int32_t pad_[3];
 };
-static_assert(sizeof(DevPageReq) == 48, "paged request table layout");
+static_assert(sizeof(DevPageReq) == 64, "paged request table layout");
 constexpr int kInlinePages = 1024;
 struct PageTable {
     DevPageReq reqs[kInlineEntries];
@@ -501,14 +503,18 @@ struct PageArgs {
 };
 
 // The tensor-core kernel of the paged attention: one (unit, request, 256-row block
-// of its query rows, stretch of its key tiles) an item.
-constexpr int64_t kPagePartBytes = 256 * 128 * 4 + 256 * 8;
+// of its query rows, stretch of its key tiles) an item.  Packed rows are restored to
+// bf16 first, by k_page_restore, in tiles of 128 rows: [unit of the slice][tile][128][D].
+constexpr int64_t kPagePartBytes = 256 * 128 * 4 + 256 * 8, kPageTileBytes = 128 * 128 * 2;
 struct PageTcArgs {
     int64_t total;          // items
     int32_t unit_items;     // of one (layer, kv-head)
     int32_t splits;         // stretches of a block
     int32_t box;            // rows of a TMA box of the pages; 0: no tile is loaded by TMA
     float *part;            // splits > 1: total partial results
+    int32_t lh_base;        // first (layer, kv-head) unit of this launch's slice
+    int32_t unit_tiles;     // restored tiles of a unit
+    void *rest_k, *rest_v;  // restored rows
 };
 
 // ---- launchers (each returns the cudaGetLastError of its launch) ----
@@ -605,8 +611,15 @@ cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, i
 // takes it; `host_reqs` is the host's copy of the request table.
 constexpr int kPageFewRows = 16;
 cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevPageReq *host_reqs, int n_sms, cudaStream_t s);
-cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTable &t, void *q_rot, const void *tmap_q,
-                           const void *tmap_k, const void *tmap_v, int n_sms, cudaStream_t s);
+cudaError_t launch_page_queries(const PageArgs &a, const PageTable &t, void *q_rot, cudaStream_t s);
+// One slice of lh_count units: restore (unit_tiles > 0), attention, join (splits > 1).
+// Host CUtensorMaps: packed queries and restored rows with 64 x 128 boxes, pages with
+// 64 x box ones.
+struct PageTcMaps {
+    const void *q, *k, *v, *rest_k, *rest_v;
+};
+cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTable &t, const PageTcMaps &m, int lh_count, int n_sms,
+                           cudaStream_t s);
 cudaError_t launch_page_pack(const PageArgs &a, const PageTable &t, int64_t n_blocks, bool unpack, cudaStream_t s);
 // Whether `n_sms` CTAs of the attention kernel (either variant) can be
 // resident at once as two-CTA clusters.

@@ -94,20 +94,6 @@ __device__ __forceinline__ void rotate_halves(uint4 &x, uint4 &y, const float2 *
     y = Vec<T>::put(b);
 }
 
-// The last request whose first token is <= t and that has tokens behind it.
-__device__ __forceinline__ int request_of(const DevPageReq *reqs, int n, int t)
-{
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (reqs[mid].q_off <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
-}
-
 }  // namespace
 
 // A group of D / 2 / N threads per token: each holds a 16-byte vector of both

@@ -30,6 +30,20 @@ __device__ __forceinline__ int32_t packed_id(const DevPageReq &r, const int32_t 
     return ids[pg + (pg < r.pfew ? r.poff[0] : r.poff[1])];
 }
 
+// The last request whose first token is <= t and that has tokens behind it.
+__device__ __forceinline__ int request_of(const DevPageReq *reqs, int n, int t)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (reqs[mid].q_off <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
 // Rows that the query at position p sees: j < hi and (j >= lo or j < few).
 struct Sees {
     int hi, lo, few;
@@ -50,6 +64,34 @@ __device__ __forceinline__ int codes_at(int i, int part) { return (i >> 1) * kPa
 __device__ __forceinline__ int scales_at(int r, int part)
 {
     return (r >> 4) * kPackStep + part * kPackPart + 1024 + (r & 7) * 16 + (r & 8);
+}
+
+// Rows that some query of a request sees.
+__device__ __forceinline__ Sees sees_any(const PageArgs &a, const DevPageReq &r)
+{
+    Sees s;
+    s.hi = min(r.kv_len, r.pos0 + r.q_len);
+    s.lo = min(s.hi, a.window > 0 ? max(0, r.pos0 - a.window + 1) : 0);
+    s.few = min(a.n_first, s.lo);
+    return s;
+}
+
+// The 128-row tiles of a request that hold packed rows are restored: its first `first` ones and
+// those from `win` up to `end`, one behind the other.
+struct RestTiles {
+    int first, win, end;
+    __device__ __forceinline__ int count() const { return first + max(0, end - win); }
+    __device__ __forceinline__ int tile(int i) const { return i < first ? i : win + i - first; }
+    __device__ __forceinline__ int place(int t) const { return t < first ? t : first + t - win; }
+};
+__host__ __device__ __forceinline__ RestTiles rest_tiles(int hi, int lo, int few, int body)
+{
+    RestTiles r;
+    const int e = hi < body ? hi : body, a = (few + 127) / 128;
+    r.end = (e + 127) / 128;
+    r.first = a < r.end ? a : r.end;
+    r.win = a > lo / 128 ? a : lo / 128;
+    return r;
 }
 
 // Byte offset of packed row block `row / 32` in the packed pages.

@@ -9,26 +9,28 @@
 //
 //   warps 0-3, 4-7  softmax of tile A, B, a row a thread, and its output;
 //   warp 8          works out each item's block of rows and its tiles, and passes them to
-//                   the others through a ring of three (each role on its own took 9 us at
-//                   every item boundary), then loads by TMA: a tile's pages are boxes of 16 to 128 rows, one a
-//                   lane, so that a tile of 16-row pages takes no longer to issue;
-//   warp 9          tcgen05 products; rows of V that no query of the block sees become
+//                   the others through a ring of three, then loads by TMA: a tile's
+//                   pages are boxes of 16 to 128 rows, one and a panel a lane;
+//   warp 9          tcgen05 products; rows of V that no query of the request sees become
 //                   zeros first (their weight is 0, but 0 x NaN is NaN);
-//   warps 10, 11    tiles that a TMA box cannot bring: packed rows, and pages whose
-//                   rows are no multiple of 16 or lie at odd strides.  64 rows each; packed rows
-//                   become bf16 rows here (scale * code, rounded to bf16: the operand
-//                   of both products), a sub-block of 32 read ahead in registers.
-// A slot's barrier counts three arrivals whichever way it is filled: three of warp
-// 8, or one each of warps 8, 10 and 11.  That a slot is free for them, warps 10 and
-// 11 learn from warp 8, over a barrier of the slot that completes a phase for each
-// of their tiles and no other: on the barrier that frees slots they could come two
-// phases late, past tiles that are none of theirs, and a wait for a parity would not
-// return.
+//   warps 10, 11    tiles of pages that TMA boxes cannot bring (their rows are no multiple
+//                   of 16 or lie at odd strides), 64 rows each.
+// A slot's barrier counts two arrivals whichever way it is filled: two of warp 8, or
+// one each of warps 10 and 11.  That a slot is free for them, warps 10 and 11 learn from
+// warp 8, over a barrier of the slot that completes a phase for each of their tiles and
+// no other: on the barrier that frees slots they could come two phases late, past tiles
+// that are none of theirs, and a wait for a parity would not return.
+//
+// Packed rows are restored to bf16 first (k_page_restore: scale * code, rounded), slice by
+// slice of the (layer, kv-head) units as the scratch holds them, once for all blocks of a
+// request.  Restored by warps 10 and 11 on the way instead, for every block again, a step
+// of 128 keys took 8.8 us, 16 times what one warp reads and writes: 8 x 64 tokens on 2,592
+// packed rows, 112 units, 2,140 us.
 //
 // Few blocks (fewer than the SMs): each is cut in stretches of key tiles, whose
 // partial results (O relative to a maximum, the maximum, the sum) k_page_join adds.
 // Rounded to bf16 on the way: the turned queries, the probabilities, and what packed
-// rows stand for.
+// rows stand for (all operands of products with bf16 numbers).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -93,26 +95,29 @@ struct alignas(16) Block {
     DevPageReq rq;
     int lh, l, h;
     int row0, rows, nx;      // first packed row in the request, rows (<= 256), 128-row tiles
-    int hi, lo, few;         // rows that some query of the block sees: j < hi and (j >= lo or j < few)
+    int hi, lo;              // rows that some query of the block sees: j < hi and (j >= lo or a first one)
+    Sees any;                // ... and of the request
     int p0, p1;              // positions of its first and last token
     int n_first, t_win;      // tiles of the first rows; the window's first tile
     int jb, je;              // the item's tiles of the list
 
+    RestTiles rest;
+    int rest_row0;           // the request's first restored row of the unit
     int64_t unit;            // elements from a page's start to the (layer, kv-head)'s first row
 
     __device__ __forceinline__ int tile(int i) const { return i < n_first ? i : t_win + i - n_first; }
-    __device__ __forceinline__ bool seen(int j) const { return j < hi && (j >= lo || j < few); }
-    __device__ __forceinline__ bool all_seen(int j0, int j1) const { return j1 <= hi && (j0 >= lo || j1 <= few); }
-    __device__ __forceinline__ bool some_seen(int j0, int j1) const { return j0 < few || (j0 < hi && j1 > lo); }
+    __device__ __forceinline__ bool all_seen(int j0, int j1) const { return j1 <= any.hi && (j0 >= any.lo || j1 <= any.few); }
+    __device__ __forceinline__ bool some_seen(int j0, int j1) const { return j0 < any.few || (j0 < any.hi && j1 > any.lo); }
+    __device__ __forceinline__ bool restored(int k) const { return k * kPtTile < rq.packed_len; }
+    __device__ __forceinline__ int rest_row(int k) const { return rest_row0 + rest.place(k) * kPtTile; }
 };
-
 static_assert(sizeof(Block) <= kPtGeoBytes, "geometry ring");
 
 __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p, const DevPageReq *reqs, int64_t w)
 {
     Block s;
-    s.lh = (int)(w / p.unit_items);
-    const int in_unit = (int)(w - (int64_t)s.lh * p.unit_items);
+    const int lh_s = (int)(w / p.unit_items), in_unit = (int)(w - (int64_t)lh_s * p.unit_items);
+    s.lh = p.lh_base + lh_s;
     int lo = 0, hi = a.n_reqs - 1;
     while (lo < hi) {   // the last request whose first item is <= it (one with items)
         const int mid = (lo + hi + 1) >> 1;
@@ -134,8 +139,10 @@ __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p
     s.p1 = s.rq.pos0 + (s.row0 + s.rows - 1) / G;
     s.hi = min(s.rq.kv_len, s.p1 + 1);
     s.lo = min(s.hi, a.window > 0 ? max(0, s.p0 - a.window + 1) : 0);
-    s.few = min(a.n_first, s.lo);
-    s.n_first = (s.few + kPtTile - 1) / kPtTile;
+    s.any = sees_any(a, s.rq);
+    s.rest = rest_tiles(s.any.hi, s.any.lo, s.any.few, s.rq.packed_len);
+    s.rest_row0 = (lh_s * p.unit_tiles + s.rq.tile0) * kPtTile;
+    s.n_first = (min(a.n_first, s.lo) + kPtTile - 1) / kPtTile;
     s.t_win = max(s.n_first, s.lo / kPtTile);
     const int n = s.n_first + max(0, (s.lo < s.hi ? (s.hi + kPtTile - 1) / kPtTile : 0) - s.t_win);
     s.jb = (int)((int64_t)n * sp / p.splits);
@@ -143,12 +150,7 @@ __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p
     return s;
 }
 
-// A tile that TMA boxes bring.
-__device__ __forceinline__ bool by_tma(const PageTcArgs &p, const Block &s, int k)
-{
-    return p.box > 0 && k * kPtTile >= s.rq.packed_len;
-}
-
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b)
 {
     const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
@@ -161,13 +163,16 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w)
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&c));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+// A tile that warps 10 and 11 fill.
+__device__ __forceinline__ bool by_hand(const PageTcArgs &p, const Block &s, int k) { return p.box == 0 && !s.restored(k); }
 
 }  // namespace
 
 __global__ void __launch_bounds__(kPtThreads, 1)
     k_page_attention(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ PageArgs a,
+                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmrk,
+                     const __grid_constant__ CUtensorMap tmrv, const __grid_constant__ PageArgs a,
                      const __grid_constant__ PageTcArgs p, const __grid_constant__ PageTable pt)
 {
     extern __shared__ uint8_t pt_smem_raw[];
@@ -182,7 +187,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTbNum; ++i)
-            mbar_init(bar(i), i < kTbEmpty ? 3u
+            mbar_init(bar(i), i < kTbEmpty ? 2u
                               : (i >= kTbP && i < kTbP + 2) || (i >= kTbOEmpty && i < kTbOEmpty + 2) ? 128u
                               : i >= kTbGeoFree ? 11u
                                                                                                     : 1u);
@@ -195,6 +200,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         prefetch_tmap(&tmq);
         prefetch_tmap(&tmk);
         prefetch_tmap(&tmv);
+        prefetch_tmap(&tmrk);
+        prefetch_tmap(&tmrv);
     }
     tc_fence_before();
     __syncthreads();
@@ -237,6 +244,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int pos = b.rq.pos0 + (b.row0 + x * 128 + r) / G;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = b.jb; j < b.je; ++j) {
+                const int k0 = b.tile(j) * kPtTile, k1 = k0 + kPtTile;
+                const bool all = k1 <= min(b.rq.kv_len, b.p0 + 1) && (a.window == 0 || k0 > b.p1 - a.window || k1 <= a.n_first);
                 if (!mbar_wait_warp(bar(kTbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
                     ok = false;
                     break;
@@ -253,8 +262,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 for (int q = 0; q < 4; ++q)
                     tmem_ld32(lane_base + pt_col_s(x) + 32 * q, s + 32 * q);
                 tmem_wait_ld();
-                const int k0 = b.tile(j) * kPtTile, k1 = k0 + kPtTile;
-                if (!(k1 <= min(b.rq.kv_len, b.p0 + 1) && (a.window == 0 || k0 > b.p1 - a.window || k1 <= a.n_first))) {
+                if (!all) {
                     const Sees see = sees(a, b.rq, pos);
                     const int hi = see.hi - k0, lo = see.lo - k0, few = see.few - k0;
                     if (hi < kPtTile) {
@@ -422,16 +430,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int64_t unit = b.unit / 128;
             // tile i of the item: the row of this lane's box (box lane / 2, panel lane & 1) and whether
             // it is to be loaded; the same for keys and values
-            const int at = (lane >> 1) * p.box;
-            int row = 0;
-            bool tma = false, load = false;
+            int row = 0, at = 0, rows = 0;
+            bool hand = false, load = false, rest = false;
             auto find = [&](int i) {
-                const int k = b.tile(i), j0 = k * kPtTile + at;
-                tma = by_tma(p, b, k);
-                load = tma && at < kPtTile && b.some_seen(j0, j0 + p.box);
+                const int k = b.tile(i);
+                rest = b.restored(k);
+                hand = by_hand(p, b, k);
+                rows = rest ? kPtTile : p.box;
+                at = (lane >> 1) * rows;
+                const int j0 = k * kPtTile + at;
+                load = !hand && at < kPtTile && (rest || b.some_seen(j0, j0 + rows));
                 if (load) {
                     const int pg = j0 / a.g.rows;
-                    row = (int)((int64_t)page_id(b.rq, ids, pg) * (a.g.s_page / 128) + unit + (j0 - pg * a.g.rows));
+                    row = rest ? b.rest_row(k)
+                               : (int)((int64_t)page_id(b.rq, ids, pg) * (a.g.s_page / 128) + unit + (j0 - pg * a.g.rows));
                 }
             };
             find(b.jb);
@@ -461,18 +473,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     break;
                 }
                 if (lane == 0) {
-                    mbar_arrive(bar(kTbFull + slot));
-                    if (tma) {
+                    if (!hand) {
                         mbar_arrive(bar(kTbFull + slot));
-                        mbar_expect_tx(bar(kTbFull + slot), boxes * (uint32_t)p.box * 128u);
+                        mbar_expect_tx(bar(kTbFull + slot), boxes * (uint32_t)rows * 128u);
                     } else {
                         mbar_arrive(bar(kTbJob + slot));
                     }
                 }
                 __syncwarp();   // (the bytes are expected before they land)
                 if (load)
-                    tma_load_2d(sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes + (lane & 1) * kPtPanel + at * 128), (i & 1) ? &tmv : &tmk,
-                                64 * (lane & 1), row, bar(kTbFull + slot));
+                    tma_load_2d(sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes + (lane & 1) * kPtPanel + at * 128),
+                                (i & 1) ? (rest ? &tmrv : &tmv) : (rest ? &tmrk : &tmk), 64 * (lane & 1), row, bar(kTbFull + slot));
                 if ((i & 1) && i + 1 < n_loads)
                     find(b.jb + (i >> 1) + 1);
                 ++tt;
@@ -536,10 +547,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (!wait_kv(tt + 2 * i + 1))
                     return false;
                 const int k = b.tile(b.jb + i), k0 = k * kPtTile;
-                if (by_tma(p, b, k) && !b.all_seen(k0, k0 + kPtTile)) {
+                if (!by_hand(p, b, k) && !b.restored(k) && !b.all_seen(k0, k0 + kPtTile)) {
                     const uint32_t v = sbase + (uint32_t)(kPtOffKV + ((tt + 2 * i + 1) % kPtSlots) * kPtTileBytes);
                     for (int c = lane; c < kPtTile * 8; c += 32)
-                        if (!b.seen(k0 + (c >> 3))) {
+                        if (!b.any(k0 + (c >> 3))) {
                             st_shared_v4(v + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
                             st_shared_v4(v + kPtPanel + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
                         }
@@ -621,7 +632,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
         pdl_wait_prerequisites();
-        const int half = warp - 10, n = lane >> 2, c4 = lane & 3;
         bool ok = true;
         int tt = 0;
         uint32_t jobs = 0;   // bit s: the parity of slot s's next job
@@ -632,141 +642,33 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             const Block &b = geo(item);
             const int n_loads = 2 * (b.je - b.jb);
-            // where the two sub-blocks of a packed tile are, one tile ahead of what reads them
-            const uint8_t *at[2] = {nullptr, nullptr}, *at_next[2] = {nullptr, nullptr};
-            auto find = [&](int i, const uint8_t *(&to)[2]) {
-                if (i >= b.je)
-                    return;
-                const int k = b.tile(i);
-                if (!by_tma(p, b, k))
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int j0 = k * kPtTile + 64 * half + 32 * y;
-                        if (j0 < b.rq.packed_len && b.some_seen(j0, j0 + 32))
-                            to[y] = a.g.packed + packed_block(a, b.rq, ids, b.lh, j0);
-                    }
-            };
-            // Sub-block q of the item's loads (two of 32 rows a load): what it reads, ahead.
-            // Keys: lane 4 n + c: codes of row 8 i + n in r[4 i ..], its scales in r[16 + 2 i ..].
-            // Values: lane 16 i' + 4 c + g: in pass x, the words of rows 8 i + 2 c, + 1 (i = 2 x + i'),
-            // group g, n = 0..7, in r[8 x ..], the two scales in r[16 + x].
-            auto fetch = [&](int q, const uint8_t *src, uint32_t (&r)[24]) {
-                if (q >= 2 * n_loads)
-                    return;
-                const int k = b.tile(b.jb + (q >> 2)), j0 = k * kPtTile + 64 * half + 32 * (q & 1);
-                if (by_tma(p, b, k) || j0 >= b.rq.packed_len || !b.some_seen(j0, j0 + 32))
-                    return;
-                if (!(q & 2)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + codes_at(i, 0) + 16 * lane));
-                        const uint2 s = __ldg(reinterpret_cast<const uint2 *>(src + scales_at(8 * i + n, 0)));
-                        r[4 * i] = v.x;
-                        r[4 * i + 1] = v.y;
-                        r[4 * i + 2] = v.z;
-                        r[4 * i + 3] = v.w;
-                        r[16 + 2 * i] = s.x;
-                        r[16 + 2 * i + 1] = s.y;
-                    }
-                } else {
-                    const int g = lane & 3, c = (lane >> 2) & 3;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int i = 2 * x + (lane >> 4);
-#pragma unroll
-                        for (int m = 0; m < 8; ++m)
-                            r[8 * x + m] = __ldg(reinterpret_cast<const uint32_t *>(src + codes_at(i, 1) + 64 * m + 16 * c + 4 * g));
-                        const uint16_t *s = reinterpret_cast<const uint16_t *>(src + scales_at(8 * i + 2 * c, 1) + 2 * g);
-                        r[16 + x] = (uint32_t)__ldg(s) | (uint32_t)__ldg(s + 8) << 16;   // (the next row's)
-                    }
-                }
-            };
-            auto put = [&](uint32_t tile, int row, int ch, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
-                st_shared_v4(tile + (uint32_t)((ch >> 3) * kPtPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4)), v0, v1, v2, v3);
-            };
-            // the sub-block into its slot
-            auto store = [&](int q, const uint32_t (&r)[24], uint32_t tile) {
-                const int k = b.tile(b.jb + (q >> 2)), in = 64 * half + 32 * (q & 1), j0 = k * kPtTile + in;
-                const bool values = (q & 2) != 0, some = b.some_seen(j0, j0 + 32);
-                if (!some || j0 >= b.rq.packed_len) {   // bf16 rows, zeros where none is seen
-                    const int ch = lane & 15;
-                    if (!some && !values)
-                        return;
-#pragma unroll 4
-                    for (int x = 0; x < 16; ++x) {
-                        const int row = 2 * x + (lane >> 4), j = j0 + row;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (b.seen(j)) {
-                            const int pg = j / a.g.rows;
-                            const int64_t at = (int64_t)page_id(b.rq, ids, pg) * a.g.s_page + b.unit + (int64_t)(j - pg * a.g.rows) * 128;
-                            v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(values ? a.g.v : a.g.k) + at) + ch);
-                        }
-                        put(tile, in + row, ch, v.x, v.y, v.z, v.w);
-                    }
-                } else if (!values) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint32_t wd = r[4 * i + g], s = prmt(r[16 + 2 * i + (g >> 1)], 0u, (g & 1) ? 0x3232u : 0x1010u);
-                            put(tile, in + 8 * i + n, 4 * g + c4, hmul2_bf16(code_pair(wd), s), hmul2_bf16(code_pair(wd >> 4), s),
-                                hmul2_bf16(code_pair(wd >> 8), s), hmul2_bf16(code_pair(wd >> 12), s));
-                        }
-                } else {
-                    const int g = lane & 3, c = (lane >> 2) & 3;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int row = 8 * (2 * x + (lane >> 4)) + 2 * c;
-                        uint32_t s = r[16 + x];
-                        if (!b.seen(j0 + row))       // (its scale may be NaN)
-                            s &= 0xffff0000u;
-                        if (!b.seen(j0 + row + 1))
-                            s &= 0x0000ffffu;
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            uint32_t v[8];
-#pragma unroll
-                            for (int d = 0; d < 8; ++d)
-                                v[d] = hmul2_bf16(code_pair(r[8 * x + d] >> (4 * m)), s);
-                            put(tile, in + row, 4 * g + m, prmt(v[0], v[1], 0x5410), prmt(v[2], v[3], 0x5410), prmt(v[4], v[5], 0x5410),
-                                prmt(v[6], v[7], 0x5410));
-                            put(tile, in + row + 1, 4 * g + m, prmt(v[0], v[1], 0x7632), prmt(v[2], v[3], 0x7632),
-                                prmt(v[4], v[5], 0x7632), prmt(v[6], v[7], 0x7632));
-                        }
-                    }
-                }
-            };
-            uint32_t r0[24], r1[24];
-            find(b.jb, at);
-            find(b.jb + 1, at_next);
-            fetch(0, at[0], r0);
             for (int i = 0; i < n_loads; ++i, ++tt) {
-                const int slot = tt % kPtSlots;
-                const bool last = (i & 1) != 0;   // the tile's values: what follows is the next tile
-                if (by_tma(p, b, b.tile(b.jb + (i >> 1)))) {
-                    if (last)
-                        fetch(2 * (i + 1), at_next[0], r0);
-                } else {
-                    if (!mbar_wait_warp(bar(kTbJob + slot), (jobs >> slot) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
+                const int slot = tt % kPtSlots, k = b.tile(b.jb + (i >> 1));
+                if (!by_hand(p, b, k))
+                    continue;
+                if (!mbar_wait_warp(bar(kTbJob + slot), (jobs >> slot) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                jobs ^= 1u << slot;
+                const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>((i & 1) ? a.g.v : a.g.k) + b.unit;
+                const int ch = lane & 15;
+#pragma unroll 8
+                for (int y = 0; y < 32; ++y) {
+                    const int row = 64 * (warp - 10) + 2 * y + (lane >> 4), j = k * kPtTile + row;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (b.any(j)) {
+                        const int pg = j / a.g.rows;
+                        v = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)page_id(b.rq, ids, pg) * a.g.s_page +
+                                                                  (int64_t)(j - pg * a.g.rows) * 128) + ch);
                     }
-                    jobs ^= 1u << slot;
-                    const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
-                    fetch(2 * i + 1, at[1], r1);
-                    store(2 * i, r0, tile);
-                    fetch(2 * i + 2, last ? at_next[0] : at[0], r0);
-                    store(2 * i + 1, r1, tile);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar(kTbFull + slot));
+                    st_shared_v4(tile + (uint32_t)((ch >> 3) * kPtPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4)), v.x, v.y, v.z, v.w);
                 }
-                if (last) {
-                    at[0] = at_next[0];
-                    at[1] = at_next[1];
-                    find(b.jb + (i >> 1) + 2, at_next);
-                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(kTbFull + slot));
             }
             geo_done(item);
         }
@@ -778,6 +680,82 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, kPtTmemCols);
+    }
+}
+
+// Packed rows of the slice's units as bf16 rows, for the requests of more than
+// kPageFewRows query rows.  One CTA: the keys or the values of one tile of 128 rows, a
+// warp a block of 32.  Rows behind packed_len in the last tile are copied from the pages,
+// rows that no query sees are zeros.
+__global__ void __launch_bounds__(128)
+    k_page_restore(const __grid_constant__ PageArgs a, const __grid_constant__ PageTcArgs p, const __grid_constant__ PageTable pt)
+{
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    const DevPageReq *reqs = a.reqs ? a.reqs : pt.reqs;
+    const int32_t *ids = a.reqs ? a.ids : pt.ids;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+    const int part = (int)(blockIdx.x & 1u), tile = (int)((blockIdx.x >> 1) % (unsigned)p.unit_tiles);
+    const int lh_s = (int)((blockIdx.x >> 1) / (unsigned)p.unit_tiles), lh = p.lh_base + lh_s;
+    int lo = 0, hi = a.n_reqs - 1;
+    while (lo < hi) {   // the last request whose first tile is <= it (one with tiles)
+        const int mid = (lo + hi + 1) >> 1;
+        if (reqs[mid].tile0 <= tile)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const DevPageReq rq = reqs[lo];
+    const Sees any = sees_any(a, rq);
+    const int j0 = rest_tiles(any.hi, any.lo, any.few, rq.packed_len).tile(tile - rq.tile0) * kPtTile + 32 * warp;
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(part ? p.rest_v : p.rest_k) +
+                                           ((int64_t)(lh_s * p.unit_tiles + tile) * kPtTile + 32 * warp) * 128);
+    if (j0 < rq.packed_len && (j0 < any.few || (j0 < any.hi && j0 + 32 > any.lo))) {
+        const uint8_t *src = a.g.packed + packed_block(a, rq, ids, lh, j0);
+        const int place = part ? 4 * (lane & 7) + (lane >> 3) : lane;
+        uint4 codes[4];
+        uint2 sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            codes[i] = __ldg(reinterpret_cast<const uint4 *>(src + codes_at(i, part) + 16 * place));
+            sc[i] = __ldg(reinterpret_cast<const uint2 *>(src + scales_at(8 * i + n, part)));
+            if (!any(j0 + 8 * i + n))   // (its scales may be NaN)
+                sc[i] = make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t s = prmt(g < 2 ? sc[i].x : sc[i].y, 0u, (g & 1) ? 0x3232u : 0x1010u);
+                uint32_t v[4];
+                if (part) {
+                    const uint32_t o = transpose_nibbles(w[g], lane);   // dims in order
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        v[m] = code_pair(prmt(o, o >> 4, 0x0400u + 0x0101u * (uint32_t)m));
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        v[m] = code_pair(w[g] >> (4 * m));
+                }
+                dst[(8 * i + n) * 16 + 4 * g + c] = make_uint4(hmul2_bf16(v[0], s), hmul2_bf16(v[1], s), hmul2_bf16(v[2], s), hmul2_bf16(v[3], s));
+            }
+        }
+        return;
+    }
+    const int l = lh / a.n_kv_heads, h = lh - l * a.n_kv_heads;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(part ? a.g.v : a.g.k) + l * a.g.s_layer + h * a.g.s_head;
+    const int ch = lane & 15;
+#pragma unroll 4
+    for (int y = 0; y < 16; ++y) {
+        const int row = 2 * y + (lane >> 4), j = j0 + row;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (any(j) && j >= rq.packed_len) {
+            const int pg = j / a.g.rows;
+            v = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)page_id(rq, ids, pg) * a.g.s_page + (int64_t)(j - pg * a.g.rows) * 128) + ch);
+        }
+        dst[row * 16 + ch] = v;
     }
 }
 
@@ -874,8 +852,14 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTable &t, void *q_rot, const void *tmap_q,
-                           const void *tmap_k, const void *tmap_v, int n_sms, cudaStream_t s)
+cudaError_t launch_page_queries(const PageArgs &a, const PageTable &t, void *q_rot, cudaStream_t s)
+{
+    const int64_t triples = (int64_t)a.n_layers * a.total_q * a.n_kv_heads;
+    return launch_pdl(k_page_queries, (triples + 15) / 16, 128, 0, true, s, a, t, static_cast<__nv_bfloat16 *>(q_rot));
+}
+
+cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTable &t, const PageTcMaps &m, int lh_count, int n_sms,
+                           cudaStream_t s)
 {
     static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
     int dev = 0;
@@ -894,12 +878,12 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
     }
-    const int64_t triples = (int64_t)a.n_layers * a.total_q * a.n_kv_heads;
-    e = launch_pdl(k_page_queries, (triples + 15) / 16, 128, 0, true, s, a, t, static_cast<__nv_bfloat16 *>(q_rot));
+    auto map = [](const void *x) -> const CUtensorMap & { return *static_cast<const CUtensorMap *>(x); };
+    if (p.unit_tiles > 0)
+        e = launch_pdl(k_page_restore, 2 * (int64_t)lh_count * p.unit_tiles, 128, 0, true, s, a, p, t);
     if (e == cudaSuccess)
-        e = launch_pdl(k_page_attention, std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s,
-                       *static_cast<const CUtensorMap *>(tmap_q), *static_cast<const CUtensorMap *>(tmap_k),
-                       *static_cast<const CUtensorMap *>(tmap_v), a, p, t);
+        e = launch_pdl(k_page_attention, std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q), map(m.k), map(m.v),
+                       map(m.rest_k), map(m.rest_v), a, p, t);
     if (e == cudaSuccess && p.splits > 1)
         e = launch_pdl(k_page_join, 2 * (p.total / p.splits), 128, 0, true, s, a, p, t);
     return e;
