@@ -2172,6 +2172,7 @@ kvr_status page_tc_plan(const kvr_pool *p, PagePlan &pl, const kvr_pages &g, int
     if (tc.box < 16 || g.stride[0] % D || g.stride[1] % D || g.stride[2] % D || page_extent(*p, g) / D > (int64_t)INT32_MAX - 256)
         tc.box = 0;
     int64_t blocks = 0, tiles = 0, rest = 0;
+    tc.one_tile = 1;
     for (DevPageReq &r : pl.rq) {
         r.tile0 = (int32_t)rest;
         if (r.q_len * (int64_t)G <= kPageFewRows)
@@ -2179,6 +2180,7 @@ kvr_status page_tc_plan(const kvr_pool *p, PagePlan &pl, const kvr_pages &g, int
         if (r.q_len * (int64_t)G > INT32_MAX - 256)
             return fail(KVR_ERR_UNSUPPORTED, "too many query rows");
         const int64_t n = (r.q_len * (int64_t)G + 255) / 256;
+        tc.one_tile = tc.one_tile && r.q_len * (int64_t)G <= 128;
         const int32_t hi = std::min<int32_t>(r.kv_len, r.pos0 + r.q_len);
         const int32_t lo = std::min(hi, window > 0 ? std::max(0, r.pos0 - window + 1) : 0);
         const int64_t seen = window > 0 ? std::min<int64_t>(hi, (int64_t)window + n_first + 256 / G) : hi;
@@ -2516,6 +2518,7 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
                 (rest_rows && ((st = encode_rows_map(*p, tc.rest_k, rest_rows, 128, &mrk)) != KVR_OK ||
                                (st = encode_rows_map(*p, tc.rest_v, rest_rows, 128, &mrv)) != KVR_OK)))
                 return st;
+            tc.out32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             maps = {&mq, tc.box ? &mk : &mq, tc.box ? &mv : &mq, rest_rows ? &mrk : &mq, rest_rows ? &mrv : &mq};
             // the previous call's attention must be done with the scratch
             cudaError_t e;

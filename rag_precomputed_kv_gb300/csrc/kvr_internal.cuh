@@ -514,6 +514,8 @@ struct PageTcArgs {
     float *part;            // splits > 1: total partial results
     int32_t lh_base;        // first (layer, kv-head) unit of this launch's slice
     int32_t unit_tiles;     // restored tiles of a unit
+    int32_t one_tile;       // no request has more than 128 of the kernel's rows
+    int32_t out32;          // `out` is 32-byte aligned
     void *rest_k, *rest_v;  // restored rows
 };
 

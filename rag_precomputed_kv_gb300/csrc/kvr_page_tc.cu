@@ -48,7 +48,7 @@ using namespace page;
 using namespace tc;
 
 constexpr int kPtThreads = 384;
-constexpr int kPtRegsLaunch = 168, kPtRegsSoftmax = 200, kPtRegsOther = 104;
+constexpr int kPtRegsLaunch = 168, kPtRegsSoftmax = 208, kPtRegsOther = 88;
 static_assert(2 * 128 * kPtRegsSoftmax + 128 * kPtRegsOther <= kPtThreads * kPtRegsLaunch, "register split");
 constexpr int kPtTile = 128;                        // keys per tile, rows per query tile
 constexpr int kPtSlots = 5;                         // K/V ring
@@ -64,7 +64,7 @@ constexpr int kPtOffQ = 0;
 constexpr int kPtOffKV = 2 * kPtTileBytes;
 constexpr int kPtOffBar = kPtOffKV + kPtSlots * kPtTileBytes;
 constexpr int kTbFull = 0, kTbEmpty = kTbFull + kPtSlots, kTbS = kTbEmpty + kPtSlots, kTbP = kTbS + 2, kTbO = kTbP + 2,
-              kTbOEmpty = kTbO + 2, kTbQ = kTbOEmpty + 2, kTbQEmpty = kTbQ + 1, kTbDrain = kTbQEmpty + 1,
+              kTbOEmpty = kTbO + 2, kTbPv = kTbOEmpty + 2, kTbQ = kTbPv + 1, kTbQEmpty = kTbQ + 1, kTbDrain = kTbQEmpty + 1,
               kTbJob = kTbDrain + 1, kTbGeo = kTbJob + kPtSlots, kTbGeoFree = kTbGeo + kPtGeos, kTbNum = kTbGeoFree + kPtGeos;
 constexpr int kPtOffMisc = kPtOffBar + 8 * kTbNum;
 constexpr int kPtOffGeo = (kPtOffMisc + 16 + 15) & ~15;
@@ -164,11 +164,22 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // A tile that warps 10 and 11 fill.
 __device__ __forceinline__ bool by_hand(const PageTcArgs &p, const Block &s, int k) { return p.box == 0 && !s.restored(k); }
 
 }  // namespace
 
+// kOne: every block of the call has one 128-row tile.  The S of its next key tile then
+// goes into tile B's buffer, ahead of the softmax (32 tokens x 4 heads on 33,000 rows, 64
+// units: 253 -> 231 us; as a branch of the kernel for two tiles it cost those 10 %).
+template <bool kOne>
 __global__ void __launch_bounds__(kPtThreads, 1)
     k_page_attention(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmrk,
@@ -226,7 +237,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int x = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float sc = a.scale_log2;
-        int s_cnt = 0, o_cnt = 0;
+        int s_cnt = 0, alt_cnt = 0, o_cnt = 0, pv_cnt = 0;   // phases seen of S, of the second buffer's S, of O, of single P V's
         bool ok = true;
         for (int item = 0; item < n_items; ++item) {
             if (!geo_wait(item)) {
@@ -246,21 +257,40 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             for (int j = b.jb; j < b.je; ++j) {
                 const int k0 = b.tile(j) * kPtTile, k1 = k0 + kPtTile;
                 const bool all = k1 <= min(b.rq.kv_len, b.p0 + 1) && (a.window == 0 || k0 > b.p1 - a.window || k1 <= a.n_first);
-                if (!mbar_wait_warp(bar(kTbS + x), (uint32_t)s_cnt & 1, abort_flag)) {
+                // (one tile uses both S buffers by turns)
+                const bool odd = kOne && ((j - b.jb) & 1);
+                const int sb = odd ? 1 : x;
+                if (!mbar_wait_warp(bar(kTbS + sb), (uint32_t)(odd ? alt_cnt : s_cnt) & 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
-                ++s_cnt;
+                if (odd)
+                    ++alt_cnt;
+                else
+                    ++s_cnt;
                 tc_fence_after();
+                // (one tile) the P V before is done, O stable: the commit that signalled S does not
+                // cover it then, as it does with two tiles
+                auto pv_done = [&]() -> bool {
+                    if (!kOne || j == b.jb)
+                        return true;
+                    const bool r = mbar_wait_warp(bar(kTbPv), (uint32_t)pv_cnt & 1u, abort_flag);
+                    ++pv_cnt;
+                    tc_fence_after();
+                    return r;
+                };
                 if (idle) {
+                    if (!(ok = pv_done()))
+                        break;
                     tc_fence_before();
-                    mbar_arrive(bar(kTbP + x));
+                    mbar_arrive(bar(kTbP + sb));
                     continue;
                 }
+                const uint32_t s_cols = lane_base + pt_col_s(sb);
                 float s[kPtTile];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    tmem_ld32(lane_base + pt_col_s(x) + 32 * q, s + 32 * q);
+                    tmem_ld32(s_cols + 32 * q, s + 32 * q);
                 tmem_wait_ld();
                 if (!all) {
                     const Sees see = sees(a, b.rq, pos);
@@ -309,7 +339,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         acc[i & 1] = add2(acc[i & 1], pk2(p0, p1));
                         pk[i] = pack_bf16(p0, p1);
                     }
-                    tmem_st16(lane_base + pt_col_s(x) + 16 * q, pk);
+                    tmem_st16(s_cols + 16 * q, pk);
                 }
                 {
                     float a0, a1, b0, b1;
@@ -317,8 +347,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     unpk2(acc[1], b0, b1);
                     l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
                 }
+                if (!(ok = pv_done()))
+                    break;
                 if (rescale) {
-                    // the commit that signalled this S covers the P V before it: O is stable
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float o[32];
@@ -332,13 +363,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(kTbP + x));
+                mbar_arrive(bar(kTbP + sb));
             }
             if (!ok)
                 break;
             const bool any = b.je > b.jb;   // (else no product was issued, O is not this item's)
             if (any) {
-                if (!mbar_wait_warp(bar(kTbO + x), (uint32_t)o_cnt & 1, abort_flag)) {
+                if (!mbar_wait_warp(bar(kTbO + x), (uint32_t)o_cnt & 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -367,9 +398,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             o[i] = some ? o[i] * inv : 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            out[4 * q + i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                                                        pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                v[k] = pack_bf16(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
+                            if (p.out32) {   // (whole sectors: a row a thread)
+                                st_global_v8(out + 4 * q + 2 * i, v);
+                            } else {
+                                out[4 * q + 2 * i] = make_uint4(v[0], v[1], v[2], v[3]);
+                                out[4 * q + 2 * i + 1] = make_uint4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
                     }
                 }
             } else {
@@ -503,7 +543,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
         pdl_wait_prerequisites();
         const uint32_t lead = elect_one();
-        int tt = 0, nq = 0, p_cnt[2] = {0, 0}, oe_cnt[2] = {0, 0};
+        int tt = 0, nq = 0, oe_cnt[2] = {0, 0};
+        uint32_t p_par = 0;   // bit i: the parity of P barrier i's next phase
         bool o_used[2] = {false, false}, ok = true;
         const uint64_t d_k = sdesc(sbase, 16, 1024), d_v = sdesc(sbase, kPtPanel, 1024);
         const uint32_t lo_k = (uint32_t)d_k, hi_k = (uint32_t)(d_k >> 32), lo_v = (uint32_t)d_v, hi_v = (uint32_t)(d_v >> 32);
@@ -513,22 +554,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             tc_fence_after();
             return true;
         };
-        // S_x = Q_x K^T with K the ring's load k
-        auto issue_s = [&](int x, int k) {
+        // S = Q_x K^T, with K the ring's load k, into buffer sb
+        auto issue_s = [&](int x, int k, int sb) {
             const uint32_t qa = lo_k + ((uint32_t)(kPtOffQ + x * kPtTileBytes) >> 4);
             const uint32_t kb = lo_k + ((uint32_t)(kPtOffKV + (k % kPtSlots) * kPtTileBytes) >> 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t off = (uint32_t)((i >> 2) * kPtPanel + (i & 3) * 32) >> 4;
-                mma_ss(lead, tmem + pt_col_s(x), desc_with_lo(qa + off, hi_k), desc_with_lo(kb + off, hi_k), kPtIdescS, i > 0);
+                mma_ss(lead, tmem + pt_col_s(sb), desc_with_lo(qa + off, hi_k), desc_with_lo(kb + off, hi_k), kPtIdescS, i > 0);
             }
-            umma_commit(lead, bar(kTbS + x));
+            umma_commit(lead, bar(kTbS + sb));
         };
-        auto issue_pv = [&](int x, int k, uint32_t acc0) {
+        auto issue_pv = [&](int x, int k, uint32_t acc0, int sb) {
             const uint32_t vb = lo_v + ((uint32_t)(kPtOffKV + (k % kPtSlots) * kPtTileBytes) >> 4);
 #pragma unroll
             for (int i = 0; i < kPtTile / 16; ++i)
-                mma_ts(lead, tmem + pt_col_o(x), tmem + pt_col_s(x) + 8 * i, desc_with_lo(vb + ((i * 2048) >> 4), hi_v), kPtIdescPV,
+                mma_ts(lead, tmem + pt_col_o(x), tmem + pt_col_s(sb) + 8 * i, desc_with_lo(vb + ((i * 2048) >> 4), hi_v), kPtIdescPV,
                        i > 0 ? 1u : acc0);
         };
         for (int item = 0; item < n_items && ok; ++item) {
@@ -574,15 +615,40 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             ++nq;
             tc_fence_after();
+            if constexpr (kOne) {
+                auto s_of = [&](int i) -> bool {   // S of key tile i into buffer i & 1
+                    if (!wait_kv(tt + 2 * i))
+                        return false;
+                    issue_s(0, tt + 2 * i, i & 1);
+                    umma_commit(lead, bar(kTbEmpty + (tt + 2 * i) % kPtSlots));
+                    if (i + 1 == K)
+                        umma_commit(lead, bar(kTbQEmpty));
+                    return true;
+                };
+                ok = s_of(0) && (K == 1 || s_of(1)) && o_free(0);
+                for (int i = 0; i < K && ok; ++i) {
+                    const int sb = i & 1;
+                    if (!mbar_wait_warp(bar(kTbP + sb), (p_par >> sb) & 1u, abort_flag) || !wait_v(i)) {
+                        ok = false;
+                        break;
+                    }
+                    p_par ^= 1u << sb;
+                    tc_fence_after();
+                    issue_pv(0, tt + 2 * i + 1, i > 0, sb);
+                    umma_commit(lead, bar(i + 1 < K ? kTbPv : kTbO));
+                    umma_commit(lead, bar(kTbEmpty + (tt + 2 * i + 1) % kPtSlots));
+                    ok = i + 2 >= K || s_of(i + 2);
+                }
+                o_used[0] = true;
+            } else {
             ok = wait_kv(tt);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                ok = ok && (x >= b.nx || o_free(x));
-                if (ok && x < b.nx)
-                    issue_s(x, tt);
-            }
             if (!ok)
                 break;
+            // (into S at once: O, which the epilogue before may still read, is the first P V's affair)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (x < b.nx)
+                    issue_s(x, tt, x);
             umma_commit(lead, bar(kTbEmpty + tt % kPtSlots));
             if (K == 1)
                 umma_commit(lead, bar(kTbQEmpty));
@@ -592,17 +658,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     if (x >= b.nx)
                         break;
-                    if (!mbar_wait_warp(bar(kTbP + x), (uint32_t)p_cnt[x] & 1, abort_flag)) {
+                    if (!mbar_wait_warp(bar(kTbP + x), (p_par >> x) & 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    ++p_cnt[x];
-                    if (x == 0 && !wait_v(i)) {
+                    p_par ^= 1u << x;
+                    if ((x == 0 && !wait_v(i)) || (i == 0 && !o_free(x))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    issue_pv(x, tt + 2 * i + 1, i > 0);
+                    issue_pv(x, tt + 2 * i + 1, i > 0, x);
                     if (!more) {
                         umma_commit(lead, bar(kTbO + x));
                         o_used[x] = true;
@@ -611,7 +677,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             ok = false;
                             break;
                         }
-                        issue_s(x, tt + 2 * i + 2);
+                        issue_s(x, tt + 2 * i + 2, x);
                     }
                 }
                 if (!ok)
@@ -621,6 +687,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 umma_commit(lead, bar(kTbEmpty + (tt + 2 * i + 1) % kPtSlots));
                 if (more)
                     umma_commit(lead, bar(kTbEmpty + (tt + 2 * i + 2) % kPtSlots));
+            }
             }
             tt += 2 * K;
             geo_done(item);
@@ -867,14 +934,16 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        cudaFuncAttributes fa{};
-        if ((e = cudaFuncGetAttributes(&fa, k_page_attention)) != cudaSuccess)
-            return e;
-        // the roles' register counts draw on what the launch holds: exactly this many
-        if (fa.numRegs != kPtRegsLaunch)
-            return cudaErrorInvalidConfiguration;
-        if ((e = cudaFuncSetAttribute(k_page_attention, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem)) != cudaSuccess)
-            return e;
+        for (auto *k : {k_page_attention<false>, k_page_attention<true>}) {
+            cudaFuncAttributes fa{};
+            if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess)
+                return e;
+            // the roles' register counts draw on what the launch holds: exactly this many
+            if (fa.numRegs != kPtRegsLaunch)
+                return cudaErrorInvalidConfiguration;
+            if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPtSmem)) != cudaSuccess)
+                return e;
+        }
         if (dev < 64)
             attr_set[dev].store(true, std::memory_order_release);
     }
@@ -882,7 +951,7 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
     if (p.unit_tiles > 0)
         e = launch_pdl(k_page_restore, 2 * (int64_t)lh_count * p.unit_tiles, 128, 0, true, s, a, p, t);
     if (e == cudaSuccess)
-        e = launch_pdl(k_page_attention, std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q), map(m.k), map(m.v),
+        e = launch_pdl(p.one_tile ? k_page_attention<true> : k_page_attention<false>, std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q), map(m.k), map(m.v),
                        map(m.rest_k), map(m.rest_v), a, p, t);
     if (e == cudaSuccess && p.splits > 1)
         e = launch_pdl(k_page_join, 2 * (p.total / p.splits), 128, 0, true, s, a, p, t);
