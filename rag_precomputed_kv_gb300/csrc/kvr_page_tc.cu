@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTbNum; ++i)
             mbar_init(bar(i), i < kTbEmpty ? 2u
-                              : (i >= kTbP && i < kTbP + 2) || (i >= kTbOEmpty && i < kTbOEmpty + 2) ? 128u
+                              : (i >= kTbP && i < kTbP + 2) || (i >= kTbOEmpty && i < kTbOEmpty + 2) ? 4u
                               : i >= kTbGeoFree ? 11u
                                                                                                     : 1u);
         *abort_flag = 0;
@@ -227,6 +227,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         __syncwarp();
         if (lane == 0)
             mbar_arrive(bar(kTbGeoFree + i % kPtGeos));
+    };
+    // one arrival of a warp, behind what its lanes did to TMEM
+    auto warp_arrive = [&](int i) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar(i));
     };
     const int n_items = (int)((p.total - blockIdx.x + gridDim.x - 1) / gridDim.x);
 
@@ -280,10 +287,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     return r;
                 };
                 if (idle) {
-                    if (!(ok = pv_done()))
+                    ok = pv_done();
+                    if (!ok)
                         break;
-                    tc_fence_before();
-                    mbar_arrive(bar(kTbP + sb));
+                    warp_arrive(kTbP + sb);
                     continue;
                 }
                 const uint32_t s_cols = lane_base + pt_col_s(sb);
@@ -347,7 +354,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     unpk2(acc[1], b0, b1);
                     l_run = l_run * corr + ((a0 + a1) + (b0 + b1));
                 }
-                if (!(ok = pv_done()))
+                ok = pv_done();
+                if (!ok)
                     break;
                 if (rescale) {
 #pragma unroll
@@ -362,8 +370,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     }
                 }
                 tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(bar(kTbP + sb));
+                warp_arrive(kTbP + sb);
             }
             if (!ok)
                 break;
@@ -432,8 +439,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
             }
             if (any) {
-                tc_fence_before();
-                mbar_arrive(bar(kTbOEmpty + x));
+                warp_arrive(kTbOEmpty + x);
             }
             geo_done(item);
         }
@@ -470,7 +476,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int64_t unit = b.unit / 128;
             // tile i of the item: the row of this lane's box (box lane / 2, panel lane & 1) and whether
             // it is to be loaded; the same for keys and values
-            int row = 0, at = 0, rows = 0;
+            // (a page's number is asked for a tile ahead of its use)
+            int row = 0, at = 0, rows = 0, id = 0, in = 0;
             bool hand = false, load = false, rest = false;
             auto find = [&](int i) {
                 const int k = b.tile(i);
@@ -482,8 +489,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 load = !hand && at < kPtTile && (rest || b.some_seen(j0, j0 + rows));
                 if (load) {
                     const int pg = j0 / a.g.rows;
-                    row = rest ? b.rest_row(k)
-                               : (int)((int64_t)page_id(b.rq, ids, pg) * (a.g.s_page / 128) + unit + (j0 - pg * a.g.rows));
+                    in = rest ? b.rest_row(k) : j0 - pg * a.g.rows;
+                    if (!rest)
+                        id = page_id(b.rq, ids, pg);
                 }
             };
             find(b.jb);
@@ -507,6 +515,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (i == n_loads)
                     break;
                 const int slot = tt % kPtSlots;
+                if (!(i & 1))
+                    row = rest ? in : (int)((int64_t)id * (a.g.s_page / 128) + unit + in);
                 const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load));
                 if (tt >= kPtSlots && !mbar_wait_warp(bar(kTbEmpty + slot), (uint32_t)(tt / kPtSlots - 1) & 1, abort_flag)) {
                     ok = false;
@@ -826,15 +836,16 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// The partial results of a block's stretches, one after the other: a CTA a
-// 128-row tile, a thread a row.
+// The partial results of a block's stretches, one after the other.  A CTA: 16 columns of a
+// 128-row tile, a thread a row.  (128 columns a CTA: 50 us for 64 blocks of 7 stretches,
+// one load after the other; 16: 14 us.)
 __global__ void __launch_bounds__(128)
     k_page_join(const __grid_constant__ PageArgs a, const __grid_constant__ PageTcArgs p, const __grid_constant__ PageTable pt)
 {
     pdl_wait_prerequisites();
     const DevPageReq *reqs = a.reqs ? a.reqs : pt.reqs;
-    const int G = a.n_q_heads / a.n_kv_heads, x = (int)(blockIdx.x & 1u), r = threadIdx.x;
-    const int64_t w0 = (int64_t)(blockIdx.x >> 1) * p.splits;
+    const int G = a.n_q_heads / a.n_kv_heads, part = (int)(blockIdx.x & 7u), x = (int)(blockIdx.x >> 3 & 1u), r = threadIdx.x;
+    const int64_t w0 = (int64_t)(blockIdx.x >> 4) * p.splits;
     const Block b = block_at(a, p, reqs, w0);
     if (x * 128 + r >= b.rows)
         return;
@@ -844,31 +855,36 @@ __global__ void __launch_bounds__(128)
     float m = -INFINITY, L = 0.f;
     for (int i = 0; i < p.splits; ++i)
         m = fmaxf(m, part_ml(p.part, w0 + i, x)[r].x);
+    float4 v[4] = {};
+#pragma unroll 2
     for (int i = 0; i < p.splits; ++i) {
         const float2 ml = part_ml(p.part, w0 + i, x)[r];
-        L += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - m);   // (a stretch of NaN scores: a sum of NaN under -inf)
+        if (ml.x == -INFINITY && ml.y == 0.f)   // (nothing seen: its O may not be written)
+            continue;
+        const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);   // (a stretch of NaN scores: a sum of NaN under -inf)
+        L = fmaf(ml.y, f, L);
+        const float4 *o = part_o(p.part, w0 + i, x) + 4 * part * 128 + r;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 y = o[c * 128];
+            v[c].x = fmaf(y.x, f, v[c].x);
+            v[c].y = fmaf(y.y, f, v[c].y);
+            v[c].z = fmaf(y.z, f, v[c].z);
+            v[c].w = fmaf(y.w, f, v[c].w);
+        }
     }
-    if (some && !(L > 0.f && L < INFINITY))
+    if (some && part == 0 && !(L > 0.f && L < INFINITY))
         atomicCAS(a.err, kDevOk, kDevBadInput);
     const float inv = some ? 1.f / L : 0.f;
     const int l = b.lh / a.n_kv_heads, h = b.lh - l * a.n_kv_heads;
-    uint2 *dst = reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                           (((int64_t)l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + h * G + g) * 128);
-#pragma unroll 4
-    for (int c = 0; c < 32; ++c) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < p.splits; ++i) {
-            const float2 ml = part_ml(p.part, w0 + i, x)[r];
-            if (ml.x == -INFINITY && ml.y == 0.f)   // (nothing seen: its O is not written)
-                continue;
-            const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-            const float4 o = part_o(p.part, w0 + i, x)[c * 128 + r];
-            v.x = fmaf(o.x, f, v.x);
-            v.y = fmaf(o.y, f, v.y);
-            v.z = fmaf(o.z, f, v.z);
-            v.w = fmaf(o.w, f, v.w);
-        }
-        dst[c] = some ? make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)) : make_uint2(0u, 0u);
+    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                           (((int64_t)l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + h * G + g) * 128) + 2 * part;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const float4 y = v[2 * c], z = v[2 * c + 1];
+        dst[c] = some ? make_uint4(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv), pack_bf16(z.x * inv, z.y * inv),
+                                   pack_bf16(z.z * inv, z.w * inv))
+                      : make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -954,7 +970,7 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
         e = launch_pdl(p.one_tile ? k_page_attention<true> : k_page_attention<false>, std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q), map(m.k), map(m.v),
                        map(m.rest_k), map(m.rest_v), a, p, t);
     if (e == cudaSuccess && p.splits > 1)
-        e = launch_pdl(k_page_join, 2 * (p.total / p.splits), 128, 0, true, s, a, p, t);
+        e = launch_pdl(k_page_join, 16 * (p.total / p.splits), 128, 0, true, s, a, p, t);
     return e;
 }
 
