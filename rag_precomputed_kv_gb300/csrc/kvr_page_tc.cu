@@ -593,12 +593,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 geo_done(item);
                 continue;
             }
-            // V tile i of the item: landed, its rows that no query sees zeroed
-            auto wait_v = [&](int i) -> bool {
+            // V tile i of the item has rows that no query sees, which have to be zeroed (worked out
+            // while the tile's probabilities are: nothing stands between them and the product)
+            auto holes = [&](int i) -> bool {
+                const int k = b.tile(b.jb + i), k0 = k * kPtTile;
+                return !by_hand(p, b, k) && !b.restored(k) && !b.all_seen(k0, k0 + kPtTile);
+            };
+            // V tile i: landed, such rows zeroed
+            auto wait_v = [&](int i, bool zero) -> bool {
                 if (!wait_kv(tt + 2 * i + 1))
                     return false;
-                const int k = b.tile(b.jb + i), k0 = k * kPtTile;
-                if (!by_hand(p, b, k) && !b.restored(k) && !b.all_seen(k0, k0 + kPtTile)) {
+                if (zero) {
+                    const int k0 = b.tile(b.jb + i) * kPtTile;
                     const uint32_t v = sbase + (uint32_t)(kPtOffKV + ((tt + 2 * i + 1) % kPtSlots) * kPtTileBytes);
                     for (int c = lane; c < kPtTile * 8; c += 32)
                         if (!b.any(k0 + (c >> 3))) {
@@ -638,7 +644,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 ok = s_of(0) && (K == 1 || s_of(1)) && o_free(0);
                 for (int i = 0; i < K && ok; ++i) {
                     const int sb = i & 1;
-                    if (!mbar_wait_warp(bar(kTbP + sb), (p_par >> sb) & 1u, abort_flag) || !wait_v(i)) {
+                    const bool zero = holes(i);
+                    if (!mbar_wait_warp(bar(kTbP + sb), (p_par >> sb) & 1u, abort_flag) || !wait_v(i, zero)) {
                         ok = false;
                         break;
                     }
@@ -662,18 +669,19 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             umma_commit(lead, bar(kTbEmpty + tt % kPtSlots));
             if (K == 1)
                 umma_commit(lead, bar(kTbQEmpty));
+            const bool two = b.nx == 2;
             for (int i = 0; i < K && ok; ++i) {
-                const bool more = i + 1 < K;
+                const bool more = i + 1 < K, zero = holes(i);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (x >= b.nx)
+                    if (x == 1 && !two)
                         break;
                     if (!mbar_wait_warp(bar(kTbP + x), (p_par >> x) & 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
                     p_par ^= 1u << x;
-                    if ((x == 0 && !wait_v(i)) || (i == 0 && !o_free(x))) {
+                    if ((x == 0 && !wait_v(i, zero)) || (i == 0 && !o_free(x))) {
                         ok = false;
                         break;
                     }
