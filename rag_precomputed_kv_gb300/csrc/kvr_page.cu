@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(kApThreads)
     k_page_append(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t)
 {
     constexpr int N = Vec<T>::N, kPer = D / 2 / N, kTokens = kApThreads / kPer;
+    pdl_wait_prerequisites();   // (uploaded tables too are read behind it)
+    pdl_launch_dependents();
     const DevPageReq *reqs = a.reqs ? a.reqs : t.reqs;
     const int32_t *ids = a.reqs ? a.ids : t.ids;
     const int units = a.n_layers * a.n_kv_heads, unit_blocks = (units + a.per_cta - 1) / a.per_cta;
@@ -146,10 +148,7 @@ static cudaError_t append(PageArgs a, const PageTable &t, int n_sms, cudaStream_
     const int64_t tb = ((int64_t)a.total_q + kTokens - 1) / kTokens;
     a.per_cta = (int32_t)std::clamp<int64_t>(tb * units / (16 * (int64_t)n_sms), 1, std::min(units, 16));
     const int64_t grid = tb * ((units + a.per_cta - 1) / a.per_cta);
-    if (grid > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    k_page_append<T, D><<<(unsigned)grid, kApThreads, 0, s>>>(a, t);
-    return cudaGetLastError();
+    return launch_pdl(k_page_append<T, D>, grid, kApThreads, 0, true, s, a, t);
 }
 
 cudaError_t launch_page_append(const PageArgs &a, const PageTable &t, int dtype, int head_dim, int n_sms, cudaStream_t s)
@@ -166,74 +165,77 @@ namespace {
 
 constexpr int kPkWarps = 4;
 
-// Eight values (dims 8 c .. 8 c + 7 of a group) as nibbles code + 8, and the scale of
-// the group, whose other values are in the other three lanes of the quad.
-// scale = bf16(max |x| / 7), code = round(x / scale), halves to even: x and scale
-// have 8 significant bits, so the fp32 quotient of a value that is not exactly
-// between two codes is at least 2^-10 away from the middle, and its rounding
-// (2^-22) changes no code.
-__device__ __forceinline__ uint32_t pack8(const uint4 &raw, uint16_t &scale_bits)
+// For scales near or below the smallest normal numbers, whose reciprocal may be no fp32 number.
+__device__ __noinline__ uint32_t pack8_small(uint4 raw, float scale)
 {
     float f[8];
     Vec<__nv_bfloat16>::get(raw, f);
-    uint32_t top = 0;   // magnitudes as integers: a NaN or an infinity is above every number
+    uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f));
-    const float scale = __bfloat162float(sb);
-    const bool finite = top < 0x7f800000u;
-    scale_bits = finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7fff;   // NaN
-    uint32_t w = 0x88888888u;
-    if (finite && scale > 0.f) {
-        w = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float c = fminf(fmaxf(rintf(__fdiv_rn(f[e], scale)), -7.f), 7.f);
-            w |= (uint32_t)((int)c + 8) << (4 * e);
-        }
-    }
+        w |= (uint32_t)((int)fminf(fmaxf(rintf(__fdiv_rn(f[e], scale)), -7.f), 7.f) + 8) << (4 * e);
     return w;
 }
 
-// nibbles 0..7 (dims in order) <-> the keys' order: dim 2 m at m, dim 2 m + 1 at m + 4
-__device__ __forceinline__ uint32_t spread_pairs(uint32_t w)
+// Eight values (dims 8 c .. 8 c + 7 of a group) as nibbles code + 8, dims in order, and the
+// scale of the group, whose other values are in the other three lanes of the quad.
+//
+// scale = bf16(max |x| / 7), code = x / scale rounded, halves to even.  x and scale have 8
+// significant bits, so that a quotient is a half, or at least 2^-10 away from one: rounded
+// to a multiple of 2^-11 first, x times the reciprocal (off by 2^-21 at most) is exactly
+// the half or on the right side of it.  The codes are joined as fp32 integers (up to 2^16),
+// which leaves the integer pipes to the loads: 8 instead of 20 instructions a value.
+__device__ __forceinline__ uint32_t pack8(const uint4 &raw, uint16_t &scale_bits)
 {
-    uint32_t o = 0;
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-        o |= ((w >> (8 * m)) & 0xfu) << (4 * m) | ((w >> (8 * m + 4)) & 0xfu) << (16 + 4 * m);
-    return o;
-}
-__device__ __forceinline__ uint32_t join_pairs(uint32_t w)
-{
-    uint32_t o = 0;
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-        o |= ((w >> (4 * m)) & 0xfu) << (8 * m) | ((w >> (16 + 4 * m)) & 0xfu) << (8 * m + 4);
-    return o;
-}
-
-// Eight codes times their scale, rounded to bf16.
-__device__ __forceinline__ uint4 unpack8(uint32_t w, float scale)
-{
+    const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+    // magnitudes as integers: a NaN or an infinity is above every number
+    uint32_t top2 = __vmaxu2(__vmaxu2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu), __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu));
+    top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, 1));
+    top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, 2));
+    const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    // (a seventh of an 8-bit number is nowhere near the middle of two: the product rounds as the quotient)
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top << 16) * (1.f / 7.f));
+    const float scale = __bfloat162float(sb);
+    const bool finite = top < 0x7f80u;
+    scale_bits = finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7fff;   // NaN
+    if (!finite || !(scale > 0.f))
+        return 0x88888888u;
+    if (scale < 1e-36f)
+        return pack8_small(raw, scale);
     float f[8];
+    Vec<__nv_bfloat16>::get(raw, f);
+    const float inv = __frcp_rn(scale);
+    constexpr float kGrid = 6144.f, kWhole = 12582912.f;   // 1.5 * 2^12, 2^23: a sum with them is rounded to 2^-11, to 1
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        f[e] = scale * (float)((int)((w >> (4 * e)) & 0xfu) - 8);
-    return Vec<__nv_bfloat16>::put(f);
+        f[e] = __fadd_rn(__fadd_rn(__fmaf_rn(f[e], inv, kGrid), kWhole - kGrid), -kWhole);
+    // sum of 16^e (code + 8), four at a time
+    const float a = fmaf(fmaf(f[3], 16.f, f[2]), 256.f, fmaf(f[1], 16.f, f[0])) + (34952.f + 8388608.f);
+    const float b = fmaf(fmaf(f[7], 16.f, f[6]), 256.f, fmaf(f[5], 16.f, f[4])) + (34952.f + 8388608.f);
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
+}
+
+// nibbles 0..7 (dims in order) -> the keys' order: dim 2 m at m, dim 2 m + 1 at m + 4
+__device__ __forceinline__ uint32_t spread_pairs(uint32_t w)
+{
+    // each step takes the middle two of four neighbours: halves of bytes, then bytes, ..
+    uint32_t t = (w ^ (w >> 4)) & 0x00f000f0u;
+    w ^= t ^ (t << 4);
+    t = (w ^ (w >> 8)) & 0x0000ff00u;
+    return w ^ t ^ (t << 8);
 }
 
 }  // namespace
 
-// One warp: the keys or the values of one block of 32 rows.  Lane 4 n + c loads,
-// of row n of each 8, the 16 bytes 4 g + c of every group g.
+// One warp: the keys or the values of one block of 32 rows, 8 at a time (a loop, which the
+// instruction cache holds), the next 8 asked for ahead.  Lane 4 n + c holds, of row n of
+// the 8, the dims 32 g + 8 c .. of every group g.
 template <bool kUnpack>
 __global__ void __launch_bounds__(32 * kPkWarps)
     k_page_pack(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t, int64_t n_items)
 {
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
     const DevPageReq *reqs = a.reqs ? a.reqs : t.reqs;
     const int32_t *ids = a.reqs ? a.ids : t.ids;
     const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
@@ -245,29 +247,34 @@ __global__ void __launch_bounds__(32 * kPkWarps)
     const int u = (int)((item >> 1) - blk * units), l = u / a.n_kv_heads, h = u - l * a.n_kv_heads;
     const DevPageReq &rq = reqs[request_of(reqs, a.n_reqs, (int)blk)];
     const int row = rq.pos0 + (int)(blk - rq.q_off) * kPackRows, pg = row / a.g.rows, in = row - pg * a.g.rows;
-    __nv_bfloat16 *x = static_cast<__nv_bfloat16 *>(which ? a.g.v : a.g.k) + (int64_t)page_id(rq, ids, pg) * a.g.s_page +
-                       l * a.g.s_layer + h * a.g.s_head + (int64_t)in * 128;
+    uint4 *x = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(which ? a.g.v : a.g.k) + (int64_t)page_id(rq, ids, pg) * a.g.s_page +
+                                         l * a.g.s_layer + h * a.g.s_head + (int64_t)in * 128) + 16 * n + c;
     uint8_t *p = a.g.packed + packed_block(a, rq, ids, u, row);
-    // the values' word of an octet's lane i (row 2 c' + i / 4 of octet c', ...) is, transposed,
-    // that of lane 4 i + c'
-    const int place = which ? 4 * (lane & 7) + (lane >> 3) : lane;
+    // a value word of octet c' is, transposed, that of lane 4 (lane & 7) + c'
+    const int place = 16 * (which ? 4 * (lane & 7) + (lane >> 3) : lane);
     if constexpr (!kUnpack) {
-        uint4 raw[4][4];
+        uint4 next[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int g = 0; g < 4; ++g)
+            next[g] = x[4 * g];
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            uint4 raw[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                raw[i][g] = *reinterpret_cast<const uint4 *>(x + (8 * i + n) * 128 + 32 * g + 8 * c);
+                raw[g] = next[g];
+            if (i < 3)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+                for (int g = 0; g < 4; ++g)
+                    next[g] = x[128 * (i + 1) + 4 * g];
             uint32_t w[4];
             uint16_t sc[4];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                w[g] = pack8(raw[i][g], sc[g]);
+                w[g] = pack8(raw[g], sc[g]);
                 w[g] = which ? transpose_nibbles(w[g], lane) : spread_pairs(w[g]);
             }
-            *reinterpret_cast<uint4 *>(p + codes_at(i, which) + 16 * place) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(p + codes_at(i, which) + place) = make_uint4(w[0], w[1], w[2], w[3]);
             if (c == 0)
                 *reinterpret_cast<uint2 *>(p + scales_at(8 * i + n, which)) =
                     make_uint2(sc[0] | (uint32_t)sc[1] << 16, sc[2] | (uint32_t)sc[3] << 16);
@@ -277,19 +284,15 @@ __global__ void __launch_bounds__(32 * kPkWarps)
         uint2 sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            codes[i] = *reinterpret_cast<const uint4 *>(p + codes_at(i, which) + 16 * place);
+            codes[i] = *reinterpret_cast<const uint4 *>(p + codes_at(i, which) + place);
             sc[i] = *reinterpret_cast<const uint2 *>(p + scales_at(8 * i + n, which));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-            const uint32_t s2[2] = {sc[i].x, sc[i].y};
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float scale = __uint_as_float((g & 1) ? s2[g >> 1] & 0xffff0000u : s2[g >> 1] << 16);
-                const uint32_t o = which ? transpose_nibbles(w[g], lane) : join_pairs(w[g]);
-                *reinterpret_cast<uint4 *>(x + (8 * i + n) * 128 + 32 * g + 8 * c) = unpack8(o, scale);
-            }
+            for (int g = 0; g < 4; ++g)
+                x[128 * i + 4 * g] = restore8(w[g], which, prmt(g < 2 ? sc[i].x : sc[i].y, 0u, (g & 1) ? 0x3232u : 0x1010u), lane);
         }
     }
 }
@@ -299,13 +302,7 @@ cudaError_t launch_page_pack(const PageArgs &a, const PageTable &t, int64_t n_bl
     const int64_t items = 2 * n_blocks * a.n_layers * a.n_kv_heads, grid = (items + kPkWarps - 1) / kPkWarps;
     if (grid == 0)
         return cudaSuccess;
-    if (grid > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    if (unpack)
-        k_page_pack<true><<<(unsigned)grid, 32 * kPkWarps, 0, s>>>(a, t, items);
-    else
-        k_page_pack<false><<<(unsigned)grid, 32 * kPkWarps, 0, s>>>(a, t, items);
-    return cudaGetLastError();
+    return launch_pdl(unpack ? k_page_pack<true> : k_page_pack<false>, grid, 32 * kPkWarps, 0, true, s, a, t, items);
 }
 
 // ---------------------------------------------------------------------------
@@ -328,6 +325,8 @@ __global__ void __launch_bounds__(kSmThreads)
     __shared__ float qs[kSmHeads][D];
     __shared__ float st_m[kSmTeams][kSmHeads], st_l[kSmTeams][kSmHeads];
     __shared__ float st_o[kSmTeams][D];
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
     const DevPageReq *reqs = a.reqs ? a.reqs : t.reqs;
     const int32_t *ids = a.reqs ? a.ids : t.ids;
     const int G = a.n_q_heads / a.n_kv_heads, hc = (G + kSmHeads - 1) / kSmHeads;
@@ -444,10 +443,7 @@ static cudaError_t simt(const PageArgs &a, const PageTable &t, cudaStream_t s)
 {
     const int G = a.n_q_heads / a.n_kv_heads;
     const int64_t grid = (int64_t)a.n_layers * a.total_q * a.n_kv_heads * ((G + kSmHeads - 1) / kSmHeads);
-    if (grid > 0x7fffffff)
-        return cudaErrorInvalidValue;
-    k_page_simt<T, D><<<(unsigned)grid, kSmThreads, 0, s>>>(a, t);
-    return cudaGetLastError();
+    return launch_pdl(k_page_simt<T, D>, grid, kSmThreads, 0, true, s, a, t);
 }
 
 cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, int head_dim, cudaStream_t s)

@@ -115,5 +115,38 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t w, int lane)
     return w;
 }
 
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// Nibbles 0 and 4 of w, less 8, as a bf16 pair (128 + nibble less 136: exact).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w)
+{
+    const uint32_t x = (w & 0x000f000fu) | 0x43004300u, c = 0x43084308u;
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Eight values of a packed word (dims 32 g + 8 c .. of the lane's row), times their scale
+// (in both halves of s), each rounded once.  part 1: a value word, of the lane that its
+// octet's transposition puts in this lane's place.
+__device__ __forceinline__ uint4 restore8(uint32_t w, int part, uint32_t s, int lane)
+{
+    uint32_t v[4];
+    if (part) {
+        w = transpose_nibbles(w, lane);   // dims in order
+#pragma unroll
+        for (int m = 0; m < 4; ++m)       // (nibbles 2 m and 2 m + 1 into bytes 0 and 2)
+            v[m] = code_pair(prmt(w, w >> 4, 0x0400u + 0x0101u * (uint32_t)m));
+    } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            v[m] = code_pair(w >> (4 * m));
+    }
+    return make_uint4(hmul2_bf16(v[0], s), hmul2_bf16(v[1], s), hmul2_bf16(v[2], s), hmul2_bf16(v[3], s));
+}
+
 }  // namespace page
 }  // namespace kvr

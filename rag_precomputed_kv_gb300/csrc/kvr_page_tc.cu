@@ -150,20 +150,6 @@ __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p
     return s;
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
-__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b)
-{
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-// Nibbles 0 and 4 of w, less 8, as a bf16 pair (128 + nibble less 136: exact).
-__device__ __forceinline__ uint32_t code_pair(uint32_t w)
-{
-    const uint32_t x = (w & 0x000f000fu) | 0x43004300u, c = 0x43084308u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&c));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8])
 {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
@@ -813,18 +799,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const uint32_t s = prmt(g < 2 ? sc[i].x : sc[i].y, 0u, (g & 1) ? 0x3232u : 0x1010u);
-                uint32_t v[4];
-                if (part) {
-                    const uint32_t o = transpose_nibbles(w[g], lane);   // dims in order
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        v[m] = code_pair(prmt(o, o >> 4, 0x0400u + 0x0101u * (uint32_t)m));
-                } else {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        v[m] = code_pair(w[g] >> (4 * m));
-                }
-                dst[(8 * i + n) * 16 + 4 * g + c] = make_uint4(hmul2_bf16(v[0], s), hmul2_bf16(v[1], s), hmul2_bf16(v[2], s), hmul2_bf16(v[3], s));
+                dst[(8 * i + n) * 16 + 4 * g + c] = restore8(w[g], part, s, lane);
             }
         }
         return;

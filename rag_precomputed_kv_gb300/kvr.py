@@ -218,8 +218,10 @@ def _page_table(name: str, a, batch: int):
     if hasattr(a, "is_cuda"):
         if a.is_cuda:
             raise ValueError(f"{name} must be in host memory")
-        if a.element_size() == 4 and not a.is_floating_point() and a.dim() == 2 and a.is_contiguous() and a.shape[0] == batch:
-            return a, a.data_ptr(), a.shape[1]
+        import torch
+        shape = a.shape
+        if a.dtype is torch.int32 and len(shape) == 2 and shape[0] == batch and a.is_contiguous():
+            return a, a.data_ptr(), shape[1]
         a = a.numpy()
     elif not isinstance(a, np.ndarray):
         a = [list(r) for r in a]
@@ -246,7 +248,7 @@ class Pages:
         if not (k.is_cuda and v.is_cuda):
             raise ValueError("pages must be in device memory")
         self.k, self.v = k, v
-        self.page_rows, self.shape = k.shape[3], (k.shape[1], k.shape[2], k.shape[4])
+        self.page_rows, self.shape, self.dtype = k.shape[3], (k.shape[1], k.shape[2], k.shape[4]), k.dtype
         self._d = PageDesc(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[3], (ctypes.c_int64 * 3)(*k.stride()[:3]))
         self._p = ctypes.addressof(self._d)
 
@@ -336,6 +338,7 @@ class Pool:
         self._keep = (k, v)
         self.n_layers, self.n_kv_heads, self.n_q_heads, self.head_dim = L, H, n_q_heads, D
         self.dtype = k.dtype
+        self._layout = (L, H, D)
         # elements of a cache row in every layer and kv head, and of a token's queries in a layer
         self._row, self._heads, self._wide = L * H * D, H * D, n_q_heads * D
 
@@ -463,8 +466,8 @@ class Pool:
         return np.minimum(kl[0], kp[0], dtype=np.int32)
 
     def _pages(self, pages: "Pages") -> int:
-        if pages.shape != (self.n_layers, self.n_kv_heads, self.head_dim) or pages.k.dtype is not self.dtype:
-            raise ValueError(f"pages of {pages.shape} (layers, kv heads, head dim), {pages.k.dtype} do not fit the pool")
+        if pages.shape != self._layout or pages.dtype is not self.dtype:
+            raise ValueError(f"pages of {pages.shape} (layers, kv heads, head dim), {pages.dtype} do not fit the pool")
         return pages._p
 
     def _packed(self, packed: "PackedPages", pages: "Pages") -> int:
@@ -497,16 +500,16 @@ class Pool:
         n = qo[2] - 1
         st, tab, p = _ints("start", start, "i", n), _page_table("table", table, n), self._pages(pages)
         tokens = int(qo[0][-1]) if n >= 0 else 0
-        for name, x in (("k", k), ("v", v)):
-            if x.dtype is not self.dtype or not x.is_cuda or x.dim() != 4:
-                raise ValueError(f"{name} must be a device tensor [layers, T, kv_heads, head_dim] of the pool's type")
-            if x.shape[0] != self.n_layers or x.shape[2:] != (self.n_kv_heads, self.head_dim) or x.shape[1] < tokens:
-                raise ValueError(f"{name} must hold {tokens} tokens of the pool's layout, got {tuple(x.shape)}")
-        s3 = k.stride()
-        if s3 != v.stride() or s3[3] != 1:
-            raise ValueError("k and v must have equal strides and contiguous rows")
+        d, s3, shape = self.dtype, k.stride(), k.shape
+        if not (k.dtype is d and v.dtype is d and k.is_cuda and v.is_cuda and v.stride() == s3 and v.shape == shape):
+            raise ValueError("k and v must be alike, device tensors [layers, T, kv_heads, head_dim] of the pool's type and of equal strides")
+        if len(shape) != 4 or shape[0] != self.n_layers or shape[1] < tokens or shape[2] != self.n_kv_heads or shape[3] != self.head_dim:
+            raise ValueError(f"k and v must hold {tokens} tokens of the pool's layout, got {tuple(shape)}")
+        if s3[3] != 1:
+            raise ValueError("the rows of k and v must be contiguous")
+        strides = array("q", s3)
         _raise(load().kvr_page_append(self._h, p, n, tab[1], tab[2], st[1], qo[1], k.data_ptr(), v.data_ptr(),
-                                      (ctypes.c_int64 * 3)(*s3[:3]), KVR_APPEND_TURNED if turned else 0, _stream_ptr(stream)))
+                                      strides.buffer_info()[0], KVR_APPEND_TURNED if turned else 0, _stream_ptr(stream)))
 
     def page_attention(self, pages: "Pages", table, kv_len, q_offsets, q, out, q_pos=None, window: int = 0,
                        n_first: int = 0, packed: Optional["PackedPages"] = None, packed_table=None, packed_len=None,
