@@ -288,15 +288,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (!all) {
                     const Sees see = sees(a, b.rq, pos);
                     const int hi = see.hi - k0, lo = see.lo - k0, few = see.few - k0;
-                    if (hi < kPtTile) {
+                    // (as bits: a compare and a select for each column cost as much as the rest of the
+                    // softmax)
+                    auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
 #pragma unroll
-                        for (int c = 0; c < kPtTile; ++c)
-                            s[c] = c < hi ? s[c] : -INFINITY;
-                    }
-                    if (lo > 0) {
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t m = below(hi - 32 * q) & (~below(lo - 32 * q) | below(few - 32 * q));
+                        if (m != ~0u) {
 #pragma unroll
-                        for (int c = 0; c < kPtTile; ++c)
-                            s[c] = (c >= lo || c < few) ? s[c] : -INFINITY;
+                            for (int c = 0; c < 32; ++c)
+                                s[32 * q + c] = (m >> c & 1u) ? s[32 * q + c] : -INFINITY;
+                        }
                     }
                 }
                 float m4[4] = {s[0], s[1], s[2], s[3]};
