@@ -552,7 +552,9 @@ KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int3
  * effect, whatever they hold.  A NaN or an infinity in a value that some query
  * token of a request sees may reach all query tokens of that request in the call
  * (a weight of 0 times it is NaN).  On the tensor cores rotated queries and
- * probabilities are rounded to bf16, as in kvr_query_attention.
+ * probabilities are rounded to bf16, as in kvr_query_attention; queries of more
+ * than 16 rows (tokens times G) a request see packed rows rounded to bf16.
+ * Queries above 2^63 in magnitude give no finite result on packed rows.
  * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
  * Errors: KVR_ERR_INVALID_ARG (also: `out` overlaps the pages, or q without being
  * the same buffer), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;

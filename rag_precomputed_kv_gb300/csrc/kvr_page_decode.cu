@@ -18,14 +18,16 @@
 // query rows, eight at a time, as the columns: S^T = K Q^T and O^T = V^T P^T, so that
 // a step of up to 8 query heads a kv head does half of what 16 rows would take.
 // The probabilities change from the one's layout to the other's by movmatrix.
-// Packed rows are not restored to bf16 rows: a nibble n under the exponent bits of
-// 128 is the bf16 number 128 + n, and
-//   keys    sum_d q_d (n_d + 128) - 136 sum_d q_d = sum_d q_d code_d: the second
-//           term is where the accumulator starts; the group's fp32 result is then
-//           scaled and added, so that a score has the codes' and scales' exact
-//           values in it;
-//   values  the (row, group) scale goes to the probability, rounded to bf16 once
-//           with it, and 136 is subtracted from the operand, which is exact.
+// Packed rows are not restored to bf16 rows:
+//   keys    as bf16 bits a nibble n is the number n 2^-133, and 16 n 2^-133 four bits
+//           higher (bf16 numbers are their bits' multiples of 2^-133 up to 255), which the
+//           MMA takes exactly; queries are scaled by 2^64.  sum_d q_d n_d - 8 sum_d q_d
+//           = sum_d q_d code_d: the second term is where the accumulator starts.  The
+//           group's fp32 result is then scaled and added, so that a score has the codes'
+//           and scales' exact values in it;
+//   values  a nibble n under the exponent bits of 128 is 128 + n, and 136 is subtracted,
+//           which is exact; the (row, group) scale goes to the probability, rounded to
+//           bf16 once with it (scaled as the queries are, large values would overflow).
 // Rounded to bf16: the turned queries and the (scaled) probabilities, because
 // they are operands of products with bf16 numbers.
 #include <cuda_bf16.h>
@@ -70,6 +72,11 @@ struct Ring {
     static_assert(kState <= kBytes, "states over the rings");
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
+
+// What queries that meet packed keys are scaled by, and what the bit patterns of small
+// integers stand for as bf16 numbers.  (A query above 2^63 becomes infinite.)
+constexpr float kLift = 18446744073709551616.f;          // 2^64
+constexpr float kTiny = 1.f / kLift / kLift / 32.f;      // 2^-133
 
 // The running maximum of a row that has seen no key: any score is above it.
 constexpr float kNothing = -3.4028234e38f;
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
     // Q^T as the B operand: of row 8 x + n and group g the dims 32 g + 8 c + 0..7, pair m
     // at step m / 2; turned by the row's position
     uint32_t qb[NR][4][4];
-    float start[NR][4][2];   // -136 times the group's sum, of rows 8 x + 2 c and + 1
+    float start[NR][4][2];   // -8 times the group's sum, of rows 8 x + 2 c and + 1
     {
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
                                  (((int64_t)l * a.total_q + rq.q_off) * a.n_q_heads + h * G) * 128 + 8 * c;
@@ -301,13 +308,14 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
                 float s = 0.f;
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    qb[x][g][m] = w[m];
-                    s += bf_lo(w[m]) + bf_hi(w[m]);
+                    qb[x][g][m] = kPack ? pack2(bf_lo(w[m]) * kLift, bf_hi(w[m]) * kLift) : w[m];   // (exact)
+                    s += bf_lo(qb[x][g][m]) + bf_hi(qb[x][g][m]);
                 }
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                start[x][g][0] = -136.f * __shfl_sync(0xffffffffu, s, 8 * c);
-                start[x][g][1] = -136.f * __shfl_sync(0xffffffffu, s, 8 * c + 4);
+                s *= -8.f * kTiny;
+                start[x][g][0] = __shfl_sync(0xffffffffu, s, 8 * c);
+                start[x][g][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
             }
         }
     }
@@ -343,17 +351,19 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
             for (int g = 0; g < 4; ++g) {
                 const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
                 const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
-                const uint32_t a0[4] = {pair128(w0[g]), pair128(w1[g]), pair128(w0[g] >> 4), pair128(w1[g] >> 4)};
-                const uint32_t a1[4] = {pair128(w0[g] >> 8), pair128(w1[g] >> 8), pair128(w0[g] >> 12), pair128(w1[g] >> 12)};
+                // pairs 0 and 2 of the words; pairs 1 and 3, which count 16 times
+                const uint32_t v0 = w0[g] >> 8, v1 = w1[g] >> 8;
+                const uint32_t a0[4] = {w0[g] & 0x000f000fu, w1[g] & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu};
+                const uint32_t a1[4] = {w0[g] & 0x00f000f0u, w1[g] & 0x00f000f0u, v0 & 0x00f000f0u, v1 & 0x00f000f0u};
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
-                    float d[4];
-                    mma_from(d, a0, qb[x][g][0], qb[x][g][1], start[x][g]);
-                    mma_bf16(d, a1, qb[x][g][2], qb[x][g][3]);
-                    s[x][0] = fmaf(x0, d[0], s[x][0]);
-                    s[x][1] = fmaf(x0, d[1], s[x][1]);
-                    s[x][2] = fmaf(x1, d[2], s[x][2]);
-                    s[x][3] = fmaf(x1, d[3], s[x][3]);
+                    const float zero[2] = {0.f, 0.f};
+                    float d[4], d16[4];
+                    mma_from(d, a0, qb[x][g][0], qb[x][g][2], start[x][g]);
+                    mma_from(d16, a1, qb[x][g][1], qb[x][g][3], zero);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[x][e] = fmaf(e < 2 ? x0 : x1, fmaf(d16[e], 0.0625f, d[e]), s[x][e]);
                 }
             }
         } else {
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
         // Scores become probabilities relative to the row's maximum, which moves only when a
         // score is more than 8 (log2) above it: bf16 and fp32 hold that, and most steps need
         // no exchange between the lanes.
-        const float sc = a.scale_log2;
+        const float sc = kThin ? a.scale_log2 * (1.f / (kLift * kTiny)) : kPack ? a.scale_log2 * (1.f / kLift) : a.scale_log2;
         float t[NR][4];
         float over = -INFINITY;
 #pragma unroll
