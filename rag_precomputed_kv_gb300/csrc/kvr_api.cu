@@ -2122,6 +2122,7 @@ void page_base(const kvr_pool &p, const kvr_pages &g, PagePlan &pl)
     a.g.s_layer = g.stride[1];
     a.g.s_head = g.stride[2];
     a.g.rows = g.page_rows;
+    a.g.shift = (g.page_rows & (g.page_rows - 1)) == 0 ? __builtin_ctz((unsigned)g.page_rows) : -1;
 }
 
 // The plan's tables into its kernels' parameters, or uploaded.

@@ -477,6 +477,7 @@ struct PageGeo {
     void *k, *v;
     int64_t s_page, s_layer, s_head;
     int32_t rows;           // rows of a page
+    int32_t shift;          // their logarithm to base 2, or -1: no power of two
     uint8_t *packed;        // or NULL: packed pages, block by block
     int64_t packed_page;    // bytes of a packed page
 };

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kApThreads)
     if (tok >= a.total_q)
         return;
     const DevPageReq &rq = reqs[request_of(reqs, a.n_reqs, (int)tok)];
-    const int row = rq.pos0 + (int)(tok - rq.q_off), pg = row / a.g.rows;
+    const int row = rq.pos0 + (int)(tok - rq.q_off), pg = page_of(a, row);
     const int64_t dst0 = (int64_t)page_id(rq, ids, pg) * a.g.s_page + (int64_t)(row - pg * a.g.rows) * D + N * j;
     float2 cs[N];
     const bool il = a.interleaved != 0;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(32 * kPkWarps)
     const int64_t blk = (item >> 1) / units;
     const int u = (int)((item >> 1) - blk * units), l = u / a.n_kv_heads, h = u - l * a.n_kv_heads;
     const DevPageReq &rq = reqs[request_of(reqs, a.n_reqs, (int)blk)];
-    const int row = rq.pos0 + (int)(blk - rq.q_off) * kPackRows, pg = row / a.g.rows, in = row - pg * a.g.rows;
+    const int row = rq.pos0 + (int)(blk - rq.q_off) * kPackRows, pg = page_of(a, row), in = row - pg * a.g.rows;
     uint4 *x = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(which ? a.g.v : a.g.k) + (int64_t)page_id(rq, ids, pg) * a.g.s_page +
                                          l * a.g.s_layer + h * a.g.s_head + (int64_t)in * 128) + 16 * n + c;
     uint8_t *p = a.g.packed + packed_block(a, rq, ids, u, row);
@@ -310,7 +310,7 @@ cudaError_t launch_page_pack(const PageArgs &a, const PageTable &t, int64_t n_bl
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kSmHeads = 4;      // query heads of a CTA
-constexpr int kSmThreads = 128;
+constexpr int kSmThreads = 256;
 constexpr int kSmTeams = kSmThreads / 8;
 }  // namespace
 
@@ -364,25 +364,31 @@ __global__ void __launch_bounds__(kSmThreads)
         }
     }
     const uint32_t team_mask = 0xffu << (8 * ((threadIdx.x >> 3) & 3));
-    for (int i = team; i < n_keys; i += kSmTeams) {
-        const int row = i < few ? i : lo + i - few;
-        float kf[N], vf[N];
-        const int pg = row / a.g.rows;
+    // a team's next row is asked for before this one is used
+    uint4 kv[N / V], vv[N / V];
+    auto ask = [&](int i) {
+        if (i >= n_keys)
+            return;
+        const int row = i < few ? i : lo + i - few, pg = page_of(a, row);
         const int64_t at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + l * a.g.s_layer + h * a.g.s_head +
                            (int64_t)(row - pg * a.g.rows) * D;
         const uint4 *kp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.k) + at);
         const uint4 *vp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.v) + at);
-        uint4 kv[N / V], vv[N / V];
 #pragma unroll
         for (int e = 0; e < N / V; ++e) {
             kv[e] = __ldg(kp + 8 * e + j);
             vv[e] = __ldg(vp + 8 * e + j);
         }
+    };
+    ask(team);
+    for (int i = team; i < n_keys; i += kSmTeams) {
+        float kf[N], vf[N];
 #pragma unroll
         for (int e = 0; e < N / V; ++e) {
             Vec<T>::get(kv[e], kf + V * e);
             Vec<T>::get(vv[e], vf + V * e);
         }
+        ask(i + kSmTeams);
 #pragma unroll
         for (int g = 0; g < kSmHeads; ++g) {
             float s = 0.f;

@@ -21,6 +21,8 @@
 namespace kvr {
 namespace page {
 
+// The page of a row (a division is 25 instructions).
+__device__ __forceinline__ int page_of(const PageArgs &a, int row) { return a.g.shift >= 0 ? row >> a.g.shift : row / a.g.rows; }
 __device__ __forceinline__ int32_t page_id(const DevPageReq &r, const int32_t *ids, int pg)
 {
     return ids[pg + (pg < r.few ? r.off[0] : r.off[1])];
@@ -97,7 +99,7 @@ __host__ __device__ __forceinline__ RestTiles rest_tiles(int hi, int lo, int few
 // Byte offset of packed row block `row / 32` in the packed pages.
 __device__ __forceinline__ int64_t packed_block(const PageArgs &a, const DevPageReq &r, const int32_t *ids, int lh, int row)
 {
-    const int pg = row / a.g.rows, in = row - pg * a.g.rows;
+    const int pg = page_of(a, row), in = row - pg * a.g.rows;
     return (int64_t)packed_id(r, ids, pg) * a.g.packed_page + ((int64_t)lh * (a.g.rows / kPackRows) + in / kPackRows) * kPackBytes;
 }
 

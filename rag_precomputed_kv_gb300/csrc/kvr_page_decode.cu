@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
             const int ch = lane & 15;
             int64_t base = 0;
             if (one_page) {
-                const int pg = r0 / a.g.rows;
+                const int pg = page_of(a, r0);
                 base = (int64_t)page_id(rq, ids, pg) * a.g.s_page + unit + (int64_t)(r0 - pg * a.g.rows) * 128;
             }
 #pragma unroll
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
                 const bool there = tl.seen(j);
                 int64_t at = base + r * 128;
                 if (!one_page && there) {
-                    const int pg = j / a.g.rows;
+                    const int pg = page_of(a, j);
                     at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + unit + (int64_t)(j - pg * a.g.rows) * 128;
                 }
                 at = there ? at + 8 * ch : 0;

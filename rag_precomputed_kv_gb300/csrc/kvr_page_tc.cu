@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const int j0 = k * kPtTile + at;
                 load = !hand && at < kPtTile && (rest || b.some_seen(j0, j0 + rows));
                 if (load) {
-                    const int pg = j0 / a.g.rows;
+                    const int pg = page_of(a, j0);
                     in = rest ? b.rest_row(k) : j0 - pg * a.g.rows;
                     if (!rest)
                         id = page_id(b.rq, ids, pg);
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     const int row = 64 * (warp - 10) + 2 * y + (lane >> 4), j = k * kPtTile + row;
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (b.any(j)) {
-                        const int pg = j / a.g.rows;
+                        const int pg = page_of(a, j);
                         v = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)page_id(b.rq, ids, pg) * a.g.s_page +
                                                                   (int64_t)(j - pg * a.g.rows) * 128) + ch);
                     }
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(128)
         const int row = 2 * y + (lane >> 4), j = j0 + row;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (any(j) && j >= rq.packed_len) {
-            const int pg = j / a.g.rows;
+            const int pg = page_of(a, j);
             v = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)page_id(rq, ids, pg) * a.g.s_page + (int64_t)(j - pg * a.g.rows) * 128) + ch);
         }
         dst[row * 16 + ch] = v;
