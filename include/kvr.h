@@ -34,7 +34,8 @@
  *          synchronously.
  *       3. Staging slots.  A call whose span, local-source or request tables
  *          do not fit inside its kernels' parameters (more than 64 spans,
- *          local sources or requests) copies them up from one of the pool's
+ *          local sources or requests; in a paged cache's call more than 64
+ *          requests or 1,024 pages) copies them up from one of the pool's
  *          8 pinned staging slots, taken in turn.  A slot is allocated on
  *          first use, and freed and allocated larger when a call needs more
  *          (cudaFreeHost / cudaFree synchronize the device).  If the slot's
@@ -49,6 +50,11 @@
  *          to 1 GiB for partial results, grown the same way (133 KB for each
  *          256 query rows of a group and (layer, kv-head), and for each SM;
  *          more than 1 GiB only where one (layer, kv-head) needs it).
+ *          kvr_page_attention uses both for requests of more than 16 query
+ *          rows: the queries, and up to 1 GiB for packed rows restored to
+ *          bf16 (512 bytes a row and (layer, kv-head); more only where one
+ *          (layer, kv-head) needs it) beside partial results (133 KB for each
+ *          256 query rows, (layer, kv-head) and stretch of their keys).
  *       5. A pool in pinned host memory: the first kvr_prefill on it creates
  *          an internal stream and its events (kept until unregister).
  *     kvr_pool_reserve makes 3 and 4 happen up front, but for the partial
@@ -200,14 +206,15 @@ KVR_API kvr_status kvr_pool_unregister(kvr_pool_t pool);
  * kvr_pool_reserve -- bind the pool to the current device (if no call has
  * yet) and allocate, now, every buffer that calls within these limits need:
  * the 8 staging slots sized for the largest tables of a call with up to
- * max_batch requests (and no more groups of them), max_spans spans and
- * max_locals local sources, and the query scratch for up to max_query_tokens
+ * max_batch requests (and no more groups of them), max_spans spans (or pages)
+ * and max_locals local sources, and the query scratch for up to max_query_tokens
  * query tokens per call (tensor-core path only).  It synchronizes (allocation
  * and the wait for slots in use).  After it, calls of every entry point within
  * the limits never allocate and never wait on the host, except on a staging
  * slot whose previous call is still queued (see the conventions above) and,
- * kvr_shared_query_attention on the tensor cores, for more partial results than
- * a call before it had (its groups' sizes decide how many).  Calls
+ * kvr_shared_query_attention and kvr_page_attention on the tensor cores, for
+ * more partial results or restored rows than a call before it had (its
+ * requests' sizes decide how many).  Calls
  * beyond the limits still work: they grow the buffers as described there.
  * Make it outside any stream capture.  Errors: KVR_ERR_INVALID_ARG (NULL pool,
  * a negative limit, max_query_tokens > 2^31 - 1), KVR_ERR_CUDA.

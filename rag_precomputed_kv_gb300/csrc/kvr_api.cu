@@ -396,7 +396,8 @@ extern "C" kvr_status kvr_pool_reserve(kvr_pool_t p, int32_t max_batch, int32_t 
     const size_t asm_bytes = align16((size_t)max_spans * sizeof(DevSpan)) + (size_t)max_locals * sizeof(DevLocal);
     const size_t append_bytes = align16((size_t)max_batch * sizeof(DevSpan)) + (size_t)max_batch * sizeof(DevLocal);
     const size_t req_bytes = align16((size_t)max_batch * req) + std::max(append_bytes, (size_t)max_batch * sizeof(DevGroup));
-    const size_t bytes = std::max(asm_bytes, req_bytes);
+    const size_t page_bytes = align16((size_t)max_batch * sizeof(DevPageReq)) + (size_t)max_spans * sizeof(int32_t);
+    const size_t bytes = std::max({asm_bytes, req_bytes, page_bytes});
     cudaError_t e;
     for (Slot &s : p->slots) {
         if (s.used && (e = cudaEventSynchronize(s.done)) != cudaSuccess)
@@ -2058,6 +2059,8 @@ kvr_status check_packed(const kvr_pool &p, const kvr_packed_pages *packed, int32
         return fail(KVR_ERR_INVALID_ARG, "packed: n_pages %lld", (long long)packed->n_pages);
     if (page_rows % kPackRows)
         return fail(KVR_ERR_INVALID_ARG, "packed pages: page_rows %d must be a multiple of %d", page_rows, kPackRows);
+    if ((double)packed->n_pages * p.d.n_layers * p.d.n_kv_heads * (page_rows / kPackRows) * kPackBytes > 1e18)
+        return fail(KVR_ERR_INVALID_ARG, "packed: %lld pages of %d rows", (long long)packed->n_pages, page_rows);
     return KVR_OK;
 }
 

@@ -100,3 +100,26 @@ def test_eviction_kernels_read_uploaded_tables_behind_their_own_wait():
         body = text[start:text.index("\n}\n", start)]
         before = re.split(r"(?:if \(a\.reqs\)\s*)?pdl_wait_prerequisites\(\);", body, maxsplit=1)
         assert len(before) == 2 and not re.search(r"reqs\)?\[", before[0]), name
+
+
+def test_paged_attention_warps_wait_with_one_answer():
+    """k_page_attention and k_page_decode: every wait of a role is voted on or one
+    lane's own, the filling warps wait on barriers of their own (on the ones that free
+    slots they could come two phases late), and a grid reads behind its own wait."""
+    text = _source("kvr_page_tc.cu")
+    body = text[text.index("    k_page_attention("):text.index("\n}\n", text.index("    k_page_attention("))]
+    assert not PLAIN.search(body) and "mbar_wait_warp(" in body
+    fill = body[body.rindex("uint32_t jobs = 0;"):]
+    assert re.findall(r"mbar_wait_warp\(bar\((\w+)", fill) == ["kTbJob"] and "geo_wait(item)" in fill
+    roles = dict(reversed(_roles(text)))
+    for cond in (("<", "8"), ("==", "8"), ("==", "9")):
+        before = roles[cond].split("pdl_wait_prerequisites();", 1)[0]
+        assert "geo" not in before and "block_at" not in before and "tma_load_2d" not in before
+    assert body.count("pdl_wait_prerequisites();") == 4
+    for name, kernels in (("kvr_page_tc.cu", ("k_page_restore(", "k_page_join(", "k_page_queries(")),
+                          ("kvr_page_decode.cu", ("k_page_decode(",)), ("kvr_page.cu", ("k_page_append(", "k_page_pack(", "k_page_simt("))):
+        text = _source(name)
+        for k in kernels:
+            start = text.index("    " + k + "const __grid_constant__")
+            before = text[start:].split("pdl_wait_prerequisites();", 1)[0]
+            assert not re.search(r"reqs|ids\b|__ldg|return", before), k

@@ -288,7 +288,7 @@ def _attention_ref(K, V, q, rows, pos, hi, window, first, scale):
 
 
 def _attention_case(reqs, L=2, H=2, G=4, D=128, dtype="bf16", R=16, window=0, first=0, il=False, scale=0.0, spread=1.0, seed=1,
-                    stream=None, pool=None, default_pos=False, in_place=False, theta=THETA, poison=True, twice=False):
+                    stream=None, pool=None, default_pos=False, in_place=False, theta=THETA, poison=True, twice=False, pad=0):
     """reqs: (kv_len, first query's position, query tokens, packed rows) of each request."""
     import torch
     from rag_precomputed_kv_gb300 import kvr
@@ -299,6 +299,12 @@ def _attention_case(reqs, L=2, H=2, G=4, D=128, dtype="bf16", R=16, window=0, fi
     seen = [np.r_[0:f, a:h] if n else np.r_[0:0] for f, a, h, n in zip(few, lo, hi, lq)]
     t, n = _table([max(k, 1) for k in kv], R, seed)
     k, v = (_randn(seed + i, (n, L, H, R, D), dtype, spread) for i in (2, 3))
+    if pad:          # pages, layers and heads at odd distances
+        strides = ((L * H * (R * D + pad) + pad) + pad, H * (R * D + pad) + pad, R * D + pad, D, 1)
+        for x in (k, v):
+            y = torch.empty(n * strides[0] + L * strides[1], device="cuda", dtype=x.dtype).as_strided(x.shape, strides)
+            y.copy_(x)
+            x.set_(y)
     pool = pool or _pool(L, H, G, D, dtype, il, theta)
     kw = {}
     held = [to_np64(x) for x in (k, v)]
@@ -459,6 +465,248 @@ def test_attention_default_positions_and_in_place():
     for q in (1, 3, 30):
         _attention_case(_plain(80, 60, q=q), default_pos=True, in_place=True)
         _attention_case(_plain(80, 60, q=q), in_place=True, D=64, dtype="fp32")
+
+
+@pytest.mark.parametrize("q", [1, 20, 50])
+def test_attention_over_padded_pages(q):
+    _attention_case(_plain(300, 170, q=q), pad=8, R=16, L=2)
+    _attention_case(_plain(300, 170, q=q), pad=256, R=64, L=2, window=90, first=5)
+    _attention_case([(300, 300 - q, q, 256), (90, 90 - q, q, 32)], pad=24, R=32, L=2)
+    _attention_case(_plain(200, q=q), pad=8, R=20, dtype="fp32", D=64)
+
+
+def test_attention_of_one_and_two_tiles_of_rows():
+    """Blocks of up to 128 rows beside larger ones, and alone; both orders."""
+    for R in (16, 20):
+        _attention_case(_plain(300, q=20) + _plain(400, q=40) + _plain(500, q=64) + _plain(260, q=33) + _plain(90, q=70), R=R, L=1)
+        _attention_case(_plain(300, q=20) + _plain(1400, q=32) + _plain(130, q=5) + _plain(31, q=31), R=R, L=3, H=2)
+    _attention_case([(300, 236, 64, 288), (700, 620, 80, 32), (40, 20, 20, 32)], R=32, L=1, window=150, first=10)
+
+
+def test_attention_is_deterministic_and_leaves_the_cache():
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    for reqs in (_plain(2000, 77), _plain(2000, 300, q=40), [(1500, 1470, 30, 1472), (900, 899, 1, 864)]):
+        a = _attention_case(reqs, R=32, seed=7)
+        for _ in range(3):
+            assert torch.equal(a, _attention_case(reqs, R=32, seed=7, twice=True))
+    pool = _pool(2, 2, 4, 128, "bf16")
+    k, v = _randn(1, (9, 2, 2, 16, 128), "bf16"), _randn(2, (9, 2, 2, 16, 128), "bf16")
+    k0, v0 = k.clone(), v.clone()
+    for q in (1, 30):
+        Q = _randn(3, (2, q, 8, 128), "bf16")
+        pool.page_attention(kvr.Pages(k, v), [list(range(9))], [130], [0, q], Q, torch.empty_like(Q))
+    torch.cuda.synchronize()
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+
+
+def test_requests_that_share_pages():
+    """Two requests on one prefix's pages, each with its own last page: as each alone."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D, R = 2, 2, 4, 128, 32
+    pool = _pool(L, H, G, D, "bf16")
+    pages = kvr.Pages(_randn(1, (8, L, H, R, D), "bf16"), _randn(2, (8, L, H, R, D), "bf16"))
+    t = [[5, 2, 0, 7, 4], [5, 2, 0, 1, 3]]
+    for q in (1, 3, 30):
+        Q = _randn(3, (L, 2 * q, H * G, D), "bf16")
+        both, alone = torch.empty_like(Q), torch.empty_like(Q)
+        pool.page_attention(pages, t, [110, 99 + q], [0, q, 2 * q], Q, both)
+        for b, n in enumerate((110, 99 + q)):
+            o = torch.empty((L, q, H * G, D), device="cuda", dtype=torch.bfloat16)
+            pool.page_attention(pages, [t[b]], [n], [0, q], Q[:, b * q:(b + 1) * q].contiguous(), o)
+            alone[:, b * q:(b + 1) * q] = o
+        torch.cuda.synchronize()
+        d = (both.double() - alone.double()).norm() / alone.double().norm()
+        assert d <= np.sqrt(2 * 3) * 2.0 ** -8, float(d)
+
+
+def test_restored_rows_in_slices():
+    """Packed rows that the scratch holds in two slices of the units only: bit for bit what their
+    unpacked pages give, which meet the same products."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D, R, n = 9, 8, 1, 128, 128, 33152
+    pool = _pool(L, H, G, D, "bf16")
+    k, v = (_randn(i, (n // R, L, H, R, D), "bf16") for i in (1, 2))
+    t = np.random.default_rng(0).permutation(n // R).astype(np.int32)[None]
+    packed = pool.packed_pages(n // R, R)
+    pool.page_pack(kvr.Pages(k, v), t, packed, t, [0], [n])
+    pool.page_unpack(packed, t, kvr.Pages(k, v), t, [0], [n])
+    Q = _randn(3, (L, 40, H * G, D), "bf16")
+    a, b = torch.empty_like(Q), torch.empty_like(Q)
+    pool.page_attention(kvr.Pages(k, v), t, [n], [0, 40], Q, a, packed=packed, packed_table=t, packed_len=[n])
+    pool.page_attention(kvr.Pages(k, v), t, [n], [0, 40], Q, b)
+    torch.cuda.synchronize()
+    pool.check()
+    # (another number of stretches may be taken: the order of sums)
+    d = (a.double() - b.double()).norm() / b.double().norm()
+    assert d <= np.sqrt(2 * 3) * 2.0 ** -8, float(d)
+    assert (a.view(-1, D).double() - b.view(-1, D).double()).norm(dim=1).max() <= 2.0 ** -5 * b.double().view(-1, D).norm(dim=1).max()
+
+
+def test_pages_beyond_32_bit_offsets():
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D, R = 2, 2, 4, 128, 128
+    n = (1 << 31) // (L * H * R * D) + 40                     # elements of k alone pass 2^31
+    pool = _pool(L, H, G, D, "bf16")
+    k, v = (torch.empty((n, L, H, R, D), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    packed = kvr.PackedPages(torch.empty(((1 << 32) // pool.packed_page_bytes(R) + 40, pool.packed_page_bytes(R)), device="cuda", dtype=torch.uint8), R)
+    small = [_randn(i, (3, L, H, R, D), "bf16") for i in (1, 2)]
+    hi = [n - 1, n - 30, n - 2]
+    for x, y in zip((k, v), small):
+        for i, p in enumerate(hi):
+            x[p] = y[i]
+    far, near = kvr.Pages(k, v), kvr.Pages(*small)
+    tp = [[packed.data.shape[0] - 1, packed.data.shape[0] - 20, packed.data.shape[0] - 3]]
+    near_packed = pool.packed_pages(3, R)
+    nk, nv = _randn(5, (L, 70, H, D), "bf16"), _randn(6, (L, 70, H, D), "bf16")
+    for pages, t, pk, pt in ((far, [hi], packed, tp), (near, [[0, 1, 2]], near_packed, [[0, 1, 2]])):
+        pool.page_append(pages, t, [300], [0, 70], nk, nv)
+        pool.page_pack(pages, t, pk, pt, [0], [256])
+    for q in (1, 4, 40):
+        Q = _randn(7, (L, q, H * G, D), "bf16")
+        o = [torch.empty_like(Q) for _ in range(4)]
+        pool.page_attention(far, [hi], [370], [0, q], Q, o[0])
+        pool.page_attention(near, [[0, 1, 2]], [370], [0, q], Q, o[1])
+        pool.page_attention(far, [hi], [370], [0, q], Q, o[2], packed=packed, packed_table=tp, packed_len=[256])
+        pool.page_attention(near, [[0, 1, 2]], [370], [0, q], Q, o[3], packed=near_packed, packed_table=[[0, 1, 2]], packed_len=[256])
+        torch.cuda.synchronize()
+        pool.check()
+        assert torch.equal(o[0], o[1]) and torch.equal(o[2], o[3]) and not torch.equal(o[0], o[2])
+    u = [torch.zeros_like(x) for x in small]
+    pool.page_unpack(packed, tp, kvr.Pages(*u), [[0, 1, 2]], [0], [256])
+    w = [torch.zeros_like(x) for x in small]
+    pool.page_unpack(near_packed, [[0, 1, 2]], kvr.Pages(*w), [[0, 1, 2]], [0], [256])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(u, w))
+
+
+def test_streams_and_graphs():
+    """A decode step (append, attention, the packing of a full page) captured once and replayed on
+    new inputs, on two streams at once; what needs scratch or uploads is refused in a capture."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D, R, n = 2, 2, 4, 128, 32, 129
+    pool = _pool(L, H, G, D, "bf16")
+    pool.reserve(max_batch=128, max_spans=4096, max_query_tokens=256)
+    t, tp = [[0, 1, 2, 3, 4]], [[0, 1, 2, 3]]
+
+    def state(seed):
+        k, v = _randn(seed, (5, L, H, R, D), "bf16"), _randn(seed + 1, (5, L, H, R, D), "bf16")
+        s = dict(k=k, v=v, pages=kvr.Pages(k, v), packed=pool.packed_pages(4, R), q=_randn(seed + 2, (L, 1, H * G, D), "bf16"),
+                 nk=_randn(seed + 3, (L, 1, H, D), "bf16"), nv=_randn(seed + 4, (L, 1, H, D), "bf16"))
+        s["out"] = torch.empty_like(s["q"])
+        return s
+
+    def step(s):
+        pool.page_append(s["pages"], t, [n - 1], [0, 1], s["nk"], s["nv"])
+        pool.page_pack(s["pages"], t, s["packed"], tp, [0], [128])
+        pool.page_attention(s["pages"], t, [n], [0, 1], s["q"], s["out"], packed=s["packed"], packed_table=tp, packed_len=[128],
+                            window=100, n_first=3)
+
+    states, graphs, streams = [state(10), state(20)], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for s, st in zip(states, streams):
+        with torch.cuda.stream(st):
+            step(s)                       # warm
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            step(s)
+        graphs.append(g)
+    for seed in (30, 50):
+        fresh = [state(seed), state(seed + 10)]
+        want = []
+        for s, f in zip(states, fresh):
+            for x in ("k", "v", "q", "nk", "nv"):
+                s[x].copy_(f[x])
+            step(f)
+            want.append(f["out"])
+        torch.cuda.synchronize()
+        for _ in range(20):               # both at once
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for s, w in zip(states, want):
+            assert torch.equal(s["out"], w)
+    pool.check()
+
+    def refused(call):
+        g = torch.cuda.CUDAGraph()
+        st = torch.cuda.Stream()
+        with pytest.raises(kvr.KvrError) as e, torch.cuda.graph(g, stream=st):
+            call()
+        assert e.value.status == 3
+        torch.cuda.synchronize()
+
+    s, Q = states[0], _randn(1, (L, 20, H * G, D), "bf16")
+    refused(lambda: pool.page_attention(s["pages"], t, [n], [0, 20], Q, Q))
+    many = [[i % 5] for i in range(70)]
+    Q70 = _randn(1, (L, 70, H * G, D), "bf16")
+    refused(lambda: pool.page_attention(s["pages"], many, [20] * 70, list(range(71)), Q70, Q70))
+    step(s)                               # and all goes on
+    pool.page_attention(s["pages"], t, [n], [0, 20], Q, Q)
+    torch.cuda.synchronize()
+    pool.check()
+
+
+def test_calls_on_several_streams_share_the_scratch_in_turn():
+    """Query prefills of one pool on two streams, enqueued alternately."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D, R = 2, 2, 4, 128, 32
+    pool = _pool(L, H, G, D, "bf16")
+    jobs = []
+    for i in range(6):
+        n, q = 400 + 77 * i, 20 + 9 * i
+        k, v = _randn(10 * i, (30, L, H, R, D), "bf16"), _randn(10 * i + 1, (30, L, H, R, D), "bf16")
+        Q = _randn(10 * i + 2, (L, q, H * G, D), "bf16")
+        jobs.append((kvr.Pages(k, v), [list(range(30))], [n], [0, q], Q, torch.empty_like(Q), torch.empty_like(Q), pool.packed_pages(30, R)))
+    torch.cuda.synchronize()
+    for pages, t, n, qo, Q, o, w, pk in jobs:
+        pool.page_pack(pages, t, pk, t, [0], [320])
+        pool.page_attention(pages, t, n, qo, Q, w, packed=pk, packed_table=t, packed_len=[320])
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, (pages, t, n, qo, Q, o, w, pk) in enumerate(jobs * 3):
+        pool.page_attention(pages, t, n, qo, Q, o, packed=pk, packed_table=t, packed_len=[320], stream=streams[i % 2])
+    torch.cuda.synchronize()
+    pool.check()
+    assert all(torch.equal(o, w) for *_, o, w, _ in jobs)
+
+
+def test_bad_queries_are_reported_and_only_they():
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    for dtype, D in (("bf16", 128), ("fp32", 64)):
+        pool = _pool(1, 1, 4, D, dtype)
+        pages = kvr.Pages(_randn(1, (4, 1, 1, 32, D), dtype), _randn(2, (4, 1, 1, 32, D), dtype))
+        t = [[0, 1], [2, 3]]
+        for q in (1, 30):
+            Q = _randn(3, (1, 2 * q, 4, D), dtype)
+            good = torch.empty_like(Q)
+            args = (pages, t, [60, 30 + q], [0, q, 2 * q])
+            kw = dict(q_pos=[60 - q, 30])
+            pool.page_attention(*args, Q, good, **kw)
+            torch.cuda.synchronize()
+            pool.check()
+            Q[0, 0, 1, 5] = float("nan")
+            bad = torch.empty_like(Q)
+            pool.page_attention(*args, Q, bad, **kw)
+            with pytest.raises(kvr.KvrError) as e:
+                pool.check()
+            assert e.value.status == 6
+            same = (bad == good).all(-1)
+            same[0, 0, 1] = True
+            assert same.all() and not torch.isfinite(bad[0, 0, 1]).any()
+            # a query of NaN that sees nothing gives zeros, and no error
+            pool.page_attention(pages, t, [0, 0], [0, q, 2 * q], Q, bad, q_pos=[5, 9])
+            torch.cuda.synchronize()
+            pool.check()
+            assert (bad == 0).all()
 
 
 def test_a_cache_as_it_is_used():

@@ -179,6 +179,7 @@ def pack(lib, h, pages={}, table=((0, 1), (2, 3)), width=2, packed={}, ptable=((
 @pytest.mark.parametrize("kw,status", BAD_PAGES + BAD_TABLE + [
     (dict(packed=None), 1), (dict(packed=dict(data=None)), 1), (dict(packed=dict(data=C + 8)), 1), (dict(packed=dict(n=0)), 1),
     (dict(pages=dict(rows=40)), 1), (dict(pwidth=-1), 1), (dict(ptable=None), 1), (dict(ptable=((9, 1), (2, 3))), 2),
+    (dict(packed=dict(n=(1 << 31) - 1), pages=dict(rows=TOP, stride=(1 << 27, 1 << 27, 1 << 27), n=1)), 1),   # more bytes than there are
     (dict(begin=None), 1), (dict(end=None), 1), (dict(begin=(1, 32)), 1), (dict(end=(33, 96)), 1), (dict(end=(64, 0)), 1),
     (dict(begin=(-32, 0)), 1), (dict(end=(160, 96)), 2), (dict(end=(TOP + 32, 96)), 1), (dict(packed=dict(data=A)), 1),
     (dict(packed=dict(data=Bp + 4608)), 1),
