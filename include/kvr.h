@@ -558,10 +558,11 @@ KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int3
  * Rows behind kv_len, and those that no query of the request sees, have no
  * effect, whatever they hold.  A NaN or an infinity in a value that some query
  * token of a request sees may reach all query tokens of that request in the call
- * (a weight of 0 times it is NaN).  On the tensor cores rotated queries and
- * probabilities are rounded to bf16, as in kvr_query_attention; queries of more
- * than 16 rows (tokens times G) a request see packed rows rounded to bf16.
- * Queries above 2^63 in magnitude give no finite result on packed rows.
+ * (a weight of 0 times it is NaN).  On the tensor cores (bf16, head_dim 128) a
+ * request of up to 16 query rows (tokens times G) is computed from 11 bits of
+ * its rotated queries and 16 of its probabilities, 8 where these meet packed
+ * values; one of more rows from 8 bits of both, as in kvr_query_attention, and of
+ * what packed rows stand for.
  * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
  * Errors: KVR_ERR_INVALID_ARG (also: `out` overlaps the pages, or q without being
  * the same buffer), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;

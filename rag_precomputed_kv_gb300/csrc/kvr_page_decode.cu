@@ -19,18 +19,22 @@
 // a step of up to 8 query heads a kv head does half of what 16 rows would take.
 // The probabilities change from the one's layout to the other's by movmatrix.
 // Packed rows are not restored to bf16 rows:
-//   keys    as bf16 bits a nibble n is the number n 2^-133, and 16 n 2^-133 four bits
-//           higher (bf16 numbers are their bits' multiples of 2^-133 up to 255), which the
-//           MMA takes exactly; queries are scaled by 2^64.  sum_d q_d n_d - 8 sum_d q_d
-//           = sum_d q_d code_d: the second term is where the accumulator starts.  The
-//           group's fp32 result is then scaled and added, so that a score has the codes'
-//           and scales' exact values in it;
-//   values  a nibble n under the exponent bits of 128 is 128 + n, and 136 is subtracted,
-//           which is exact; the (row, group) scale goes to the probability, rounded to
-//           bf16 once with it (scaled as the queries are, large values would overflow).
-// Rounded to bf16: the turned queries and the (scaled) probabilities, because
-// they are operands of products with bf16 numbers.
+//   keys    as fp16 bits a nibble n is the number n 2^-24, and 16 n 2^-24 four bits
+//           higher (fp16 numbers are their bits' multiples of 2^-24 up to 2,047), which
+//           the MMA takes exactly.  sum_d q_d n_d - 8 sum_d q_d = sum_d q_d code_d: the
+//           second term is where the accumulator starts.  The group's fp32 result is then
+//           scaled and added, so that a score has the codes' and scales' exact values;
+//   values  a nibble n under the exponent bits of 128 is 128 + n in bf16, and 136 is
+//           subtracted, which is exact; the (row, group) scale goes to the probability,
+//           rounded to bf16 once with it.
+// Queries and probabilities that meet bf16 rows are two bf16 terms each (16 bits): the
+// memory's pace leaves room for that, and the output is off by its own rounding alone
+// (0.0017 of its norm; 0.0029 with one term each).  Queries that meet packed rows are fp16
+// times a power of two of their row, the largest element between 2^12 and 2^13 (11 bits of
+// an element, fewer only below 2^-26 of the largest); probabilities there are rounded to
+// bf16 (0.0024): the step is bound by instructions, a second term would be a tenth more.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 #include <atomic>
@@ -68,15 +72,14 @@ struct Ring {
     // the joined state behind warp 0's where that leaves room, else behind the rings
     static constexpr bool kInside = kState + kJoined <= kBytes;
     static constexpr int kOffJoined = kInside ? kState : kPdWarps * kBytes;
-    static constexpr int kSmem = kPdWarps * kBytes + (kInside ? 0 : kJoined);
+    // queries behind the rings (their place is the joined state's at the end): fp16, or two
+    // bf16 terms
+    static constexpr int kTerms = kPack ? 1 : 2, kQ = NR * kTerms * 2048;
+    static constexpr bool kQRegs = kPack && NR == 1;    // every warp keeps them in registers
+    static constexpr int kSmem = kPdWarps * kBytes + (kInside || kQ > kJoined ? kQ : kJoined);
     static_assert(kState <= kBytes, "states over the rings");
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
-
-// What queries that meet packed keys are scaled by, and what the bit patterns of small
-// integers stand for as bf16 numbers.  (A query above 2^63 becomes infinite.)
-constexpr float kLift = 18446744073709551616.f;          // 2^64
-constexpr float kTiny = 1.f / kLift / kLift / 32.f;      // 2^-133
 
 // The running maximum of a row that has seen no key: any score is above it.
 constexpr float kNothing = -3.4028234e38f;
@@ -134,14 +137,28 @@ __device__ __forceinline__ uint32_t less136(uint32_t w)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// d = a b + c, c the same in every row
-__device__ __forceinline__ void mma_from(float *d, const uint32_t *a, uint32_t b0, uint32_t b1, const float *c)
+// d = a b + c in fp16, c the same in every row
+__device__ __forceinline__ void mma_f16_from(float *d, const uint32_t *a, uint32_t b0, uint32_t b1, const float *c)
 {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%10, %11, %10, %11};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]));
+}
+
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float2 unpack2_f16(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+// x and y as two bf16 terms each
+__device__ __forceinline__ void two_terms(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack2(x, y);
+    lo = pack2(x - bf_lo(hi), y - bf_hi(hi));
 }
 
 // The 8x8 matrix of a warp's bf16 pairs, transposed.
@@ -259,65 +276,127 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
             issue(it + k * step, k);
     }
 
-    // Q^T as the B operand: of row 8 x + n and group g the dims 32 g + 8 c + 0..7, pair m
-    // at step m / 2; turned by the row's position
-    uint32_t qb[NR][4][4];
-    float start[NR][4][2];   // -8 times the group's sum, of rows 8 x + 2 c and + 1
+    // Q^T as the B operand: of row 8 x + n and group g the dims 32 g + 8 c + 0..7, turned by the
+    // row's position, pair m in word m of what lane 4 n + c reads.  A warp turns a quarter:
+    // dims 4 y .. of the groups gp and gp + 2.
+    const uint32_t q_base = dec_smem_u32(pd_smem) + (uint32_t)(kPdWarps * R::kBytes);
+    auto q_at = [&](int x, int term, int g) { return q_base + (uint32_t)(((x * R::kTerms + term) * 4 + g) * 512 + 16 * lane); };
+    float rs[NR][2];         // what scores of the rows 8 x + 2 c and + 1 are scaled by
     {
+        const int gp = warp & 1, y = warp >> 1;
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) +
-                                 (((int64_t)l * a.total_q + rq.q_off) * a.n_q_heads + h * G) * 128 + 8 * c;
+                                 (((int64_t)l * a.total_q + rq.q_off) * a.n_q_heads + h * G) * 128 + 32 * gp + 8 * c + 4 * y;
+        float f[NR][2][4];
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int r = n + 8 * x, tok = r / G;
             const bool some = r < rows;
-            uint4 v[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                v[g] = some ? *reinterpret_cast<const uint4 *>(q + ((int64_t)tok * a.n_q_heads + (r - tok * G)) * 128 + 32 * g)
-                            : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 2; ++k) {
+                const uint2 v = some ? *reinterpret_cast<const uint2 *>(q + ((int64_t)tok * a.n_q_heads + (r - tok * G)) * 128 + 64 * k)
+                                     : make_uint2(0, 0);
+                f[x][k][0] = bf_lo(v.x);
+                f[x][k][1] = bf_hi(v.x);
+                f[x][k][2] = bf_lo(v.y);
+                f[x][k][3] = bf_hi(v.y);
+            }
+            auto turn = [](float &p, float &q2, float2 cs) {
+                const float v = fmaf(p, cs.x, -(q2 * cs.y));
+                q2 = fmaf(p, cs.y, q2 * cs.x);
+                p = v;
+            };
             if (some) {
                 const int pos = rq.pos0 + tok;
-                float cs[8], sn[8];
-                if (a.interleaved) {
 #pragma unroll
-                    for (int g = 0; g < 4; g += 2) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 w = rope_cs(a.rope, 64, pos, 16 * (g + (e >> 2)) + 4 * c + (e & 3));
-                            cs[e] = w.x;
-                            sn[e] = w.y;
-                        }
-                        rotate_bf16x8_il(v[g], v[g + 1], cs, sn);
-                    }
-                } else {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 w = rope_cs(a.rope, 64, pos, 32 * g + 8 * c + e);
-                            cs[e] = w.x;
-                            sn[e] = w.y;
-                        }
-                        rotate_bf16x8(v[g], v[g + 2], cs, sn);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    if (a.interleaved)   // pairs e & 1 of either group
+                        turn(f[x][e >> 1][2 * (e & 1)], f[x][e >> 1][2 * (e & 1) + 1],
+                             rope_cs(a.rope, 64, pos, 16 * (gp + 2 * (e >> 1)) + 4 * c + 2 * y + (e & 1)));
+                    else
+                        turn(f[x][0][e], f[x][1][e], rope_cs(a.rope, 64, pos, 32 * gp + 8 * c + 4 * y + e));
                 }
             }
+        }
+        if constexpr (kPack) {
+            // the rows' largest elements, over the lanes' quads and the warps
+            float *tops = reinterpret_cast<float *>(pd_smem + kPdWarps * R::kBytes);   // [row][warp]
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                float top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = fmaxf(top, fmaxf(fabsf(f[x][0][e]), fabsf(f[x][1][e])));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if (c == 0)
+                    tops[4 * (8 * x + n) + warp] = top;
+            }
+            __syncthreads();
+            // 2^k times the largest is in [2^12, 2^13)
+            auto power = [&](int row) -> int {
+                const float4 v = *reinterpret_cast<const float4 *>(tops + 4 * row);
+                return min(126, 12 + 127 - (int)(__float_as_uint(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))) >> 23));
+            };
+            float up[NR];
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                up[x] = __uint_as_float((uint32_t)(127 + power(8 * x + n)) << 23);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    rs[x][e] = a.scale_log2 * __uint_as_float((uint32_t)(127 - power(8 * x + 2 * c + e)) << 23);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at(x, 0, gp + 2 * k) + 8u * (uint32_t)y),
+                                 "r"(pack2_f16(f[x][k][0] * up[x], f[x][k][1] * up[x])),
+                                 "r"(pack2_f16(f[x][k][2] * up[x], f[x][k][3] * up[x]))
+                                 : "memory");
+        } else {
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                rs[x][0] = rs[x][1] = a.scale_log2;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t hi[2], lo[2];
+                    two_terms(f[x][k][0], f[x][k][1], hi[0], lo[0]);
+                    two_terms(f[x][k][2], f[x][k][3], hi[1], lo[1]);
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at(x, 0, gp + 2 * k) + 8u * (uint32_t)y), "r"(hi[0]), "r"(hi[1]) : "memory");
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at(x, 1, gp + 2 * k) + 8u * (uint32_t)y), "r"(lo[0]), "r"(lo[1]) : "memory");
+                }
+            }
+        }
+        __syncthreads();
+    }
+    uint4 qr[R::kQRegs ? 4 : 1];
+    if constexpr (R::kQRegs) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            qr[g] = lds128(q_at(0, 0, g));
+    }
+    auto query = [&](int x, int term, int g) -> uint4 {
+        if constexpr (R::kQRegs)
+            return qr[g];
+        else
+            return lds128(q_at(x, term, g));
+    };
+    float start[kPack ? NR : 1][4][2];   // -8 times a group's sum, of rows 8 x + 2 c and + 1
+    if constexpr (kPack) {
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint32_t w[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
-                float s = 0.f;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    qb[x][g][m] = kPack ? pack2(bf_lo(w[m]) * kLift, bf_hi(w[m]) * kLift) : w[m];   // (exact)
-                    s += bf_lo(qb[x][g][m]) + bf_hi(qb[x][g][m]);
-                }
+                const uint4 q = query(x, 0, g);
+                const float2 v[4] = {unpack2_f16(q.x), unpack2_f16(q.y), unpack2_f16(q.z), unpack2_f16(q.w)};
+                float s = ((v[0].x + v[0].y) + (v[1].x + v[1].y)) + ((v[2].x + v[2].y) + (v[3].x + v[3].y));
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                s *= -8.f * kTiny;
+                s *= -8.f / 16777216.f;
                 start[x][g][0] = __shfl_sync(0xffffffffu, s, 8 * c);
                 start[x][g][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
             }
-        }
     }
     // rows that every query sees: below, and from (or among the first) on
     const int all_hi = min(rq.kv_len, rq.pos0 + 1), all_lo = a.window > 0 ? rq.pos0 + rq.q_len - a.window : 0;
@@ -359,8 +438,9 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
                 for (int x = 0; x < NR; ++x) {
                     const float zero[2] = {0.f, 0.f};
                     float d[4], d16[4];
-                    mma_from(d, a0, qb[x][g][0], qb[x][g][2], start[x][g]);
-                    mma_from(d16, a1, qb[x][g][1], qb[x][g][3], zero);
+                    const uint4 q = query(x, 0, g);
+                    mma_f16_from(d, a0, q.x, q.z, start[x][g]);
+                    mma_f16_from(d16, a1, q.y, q.w, zero);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         s[x][e] = fmaf(e < 2 ? x0 : x1, fmaf(d16[e], 0.0625f, d[e]), s[x][e]);
@@ -374,8 +454,24 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
                 const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
-                    mma_bf16(s[x], a0, qb[x][g][0], qb[x][g][1]);
-                    mma_bf16(s[x], a1, qb[x][g][2], qb[x][g][3]);
+                    uint32_t hi[4], lo[4];
+                    if constexpr (kPack) {   // (the few rows behind the packed ones: exactly, 8 and 3 bits)
+                        const uint4 q = query(x, 0, g);
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const float2 v = unpack2_f16(w[m]);
+                            two_terms(v.x, v.y, hi[m], lo[m]);
+                        }
+                    } else {
+                        const uint4 p = query(x, 0, g), q = query(x, 1, g);
+                        hi[0] = p.x, hi[1] = p.y, hi[2] = p.z, hi[3] = p.w;
+                        lo[0] = q.x, lo[1] = q.y, lo[2] = q.z, lo[3] = q.w;
+                    }
+                    mma_bf16(s[x], a0, lo[0], lo[1]);
+                    mma_bf16(s[x], a1, lo[2], lo[3]);
+                    mma_bf16(s[x], a0, hi[0], hi[1]);
+                    mma_bf16(s[x], a1, hi[2], hi[3]);
                 }
             }
         }
@@ -392,14 +488,14 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
         // Scores become probabilities relative to the row's maximum, which moves only when a
         // score is more than 8 (log2) above it: bf16 and fp32 hold that, and most steps need
         // no exchange between the lanes.
-        const float sc = kThin ? a.scale_log2 * (1.f / (kLift * kTiny)) : kPack ? a.scale_log2 * (1.f / kLift) : a.scale_log2;
+        constexpr float kUnit = kThin ? 16777216.f : 1.f;   // (packed keys' scores are in 2^-24)
         float t[NR][4];
         float over = -INFINITY;
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                t[x][e] = fmaf(s[x][e], sc, -m_run[x][e & 1]);
+                t[x][e] = fmaf(s[x][e], rs[x][e & 1] * kUnit, -m_run[x][e & 1]);
             over = fmaxf(over, fmaxf(fmaxf(t[x][0], t[x][1]), fmaxf(t[x][2], t[x][3])));
         }
         if (__any_sync(0xffffffffu, over > 8.f)) {
@@ -407,6 +503,7 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
             for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const float sc = rs[x][e] * kUnit;
                     float mx = fmaxf(s[x][e], s[x][e + 2]) * sc;
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -462,11 +559,16 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
                 }
             }
         } else {
-            uint32_t b0[NR], b1[NR];
+            uint32_t b0[NR][2], b1[NR][2];   // two terms
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
-                b0[x] = transpose8(pack2(t[x][0], t[x][1]));
-                b1[x] = transpose8(pack2(t[x][2], t[x][3]));
+                two_terms(t[x][0], t[x][1], b0[x][0], b0[x][1]);
+                two_terms(t[x][2], t[x][3], b1[x][0], b1[x][1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    b0[x][e] = transpose8(b0[x][e]);
+                    b1[x][e] = transpose8(b1[x][e]);
+                }
             }
             const int key = (lane & 7) + 8 * (lane >> 4);
 #pragma unroll
@@ -474,8 +576,10 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
                 uint32_t va[4];
                 ldsm_x4_t(st + (uint32_t)(4096 + key * 256 + (((2 * j + ((lane >> 3) & 1)) ^ (key & 7)) << 4)), va[0], va[1], va[2], va[3]);
 #pragma unroll
-                for (int x = 0; x < NR; ++x)
-                    mma_bf16(o[x][j], va, b0[x], b1[x]);
+                for (int x = 0; x < NR; ++x) {
+                    mma_bf16(o[x][j], va, b0[x][1], b1[x][1]);
+                    mma_bf16(o[x][j], va, b0[x][0], b1[x][0]);
+                }
             }
         }
     };
