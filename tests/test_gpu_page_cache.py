@@ -23,6 +23,8 @@ value:
   k = 1.1, 1.1, 2.2, 3 and 5 in bf16 (1.1, 2.2: with what the others leave); in fp32
   2^-17 ||o_ref|| (scores off by up to 2^-17).
 """
+import gc
+
 import numpy as np
 import pytest
 
@@ -610,6 +612,8 @@ def test_streams_and_graphs():
         s["out"] = torch.empty_like(s["q"])
         return s
 
+    gc.collect()      # (an older test's pool that is released during a capture ends the capture)
+
     def step(s):
         pool.page_append(s["pages"], t, [n - 1], [0, 1], s["nk"], s["nv"])
         pool.page_pack(s["pages"], t, s["packed"], tp, [0], [128])
@@ -645,12 +649,16 @@ def test_streams_and_graphs():
     pool.check()
 
     def refused(call):
+        """... and the capture stays usable."""
         g = torch.cuda.CUDAGraph()
-        st = torch.cuda.Stream()
-        with pytest.raises(kvr.KvrError) as e, torch.cuda.graph(g, stream=st):
-            call()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            states[0]["out"].zero_()
+            with pytest.raises(kvr.KvrError) as e:
+                call()
         assert e.value.status == 3
+        g.replay()
         torch.cuda.synchronize()
+        assert (states[0]["out"] == 0).all()
 
     s, Q = states[0], _randn(1, (L, 20, H * G, D), "bf16")
     refused(lambda: pool.page_attention(s["pages"], t, [n], [0, 20], Q, Q))
