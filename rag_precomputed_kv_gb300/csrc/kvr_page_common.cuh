@@ -21,7 +21,8 @@
 namespace kvr {
 namespace page {
 
-// The page of a row (a division is 25 instructions).
+// The page of a row (a power of two of rows without a division: 33,280 packed rows, 256
+// units, 286 -> 273 us).
 __device__ __forceinline__ int page_of(const PageArgs &a, int row) { return a.g.shift >= 0 ? row >> a.g.shift : row / a.g.rows; }
 __device__ __forceinline__ int32_t page_id(const DevPageReq &r, const int32_t *ids, int pg)
 {

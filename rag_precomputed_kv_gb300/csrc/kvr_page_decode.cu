@@ -7,11 +7,12 @@
 // bound by these reads, 512 bytes a row and (layer, kv-head), 144 where packed.
 //
 // One CTA, or a cluster of 2 to 8 where (request, unit) pairs are few, takes one
-// request's (layer, kv-head).  Its warps go through the visible key tiles by
-// turns, each with its own two-stage ring filled by cp.async (tiles of 16 bf16 or 32 packed rows: any page size and stride,
-// rows that are not there are zeros) and its own running maximum, sum and output in registers; no warp waits
-// for another before the states are joined, in a fixed order, through shared
-// memory and the cluster's.  Three CTAs of four warps are resident on an SM.
+// request's (layer, kv-head).  Its warps go through the visible key tiles by turns, each
+// with its own ring filled by cp.async (tiles of 16 bf16 or 32 packed rows: any page size
+// and stride, rows that are not there are zeros) and its own running maximum, sum and
+// output in registers; no warp waits for another before the states are joined, in a
+// fixed order, through shared memory and the cluster's.  Three CTAs of four warps are
+// resident on an SM, four in calls with packed rows.
 //
 // Both products are warp MMAs (mma.sync m16n8k16; at 16 rows a tcgen05 MMA would
 // pass every tile through TMEM), with keys and values as the 16-row operand and the
@@ -32,7 +33,16 @@
 // (0.0017 of its norm; 0.0029 with one term each).  Queries that meet packed rows are fp16
 // times a power of two of their row, the largest element between 2^12 and 2^13 (11 bits of
 // an element, fewer only below 2^-26 of the largest); probabilities there are rounded to
-// bf16 (0.0024): the step is bound by instructions, a second term would be a tenth more.
+// bf16 (0.0024), as the step is bound by instructions.
+//
+// Measured: 4 x 2,656 bf16 rows, 112 units 97 us (6.3 TB/s); 8 windows of 4,100 rows, 256
+// units 605 us (7.1 TB/s; reads alone run above the copy rate).  33,280 packed rows, 256
+// units 285 us, 4.3 TB/s; the integer pipe is busy 0.6 of the time, half of it with
+// extracting codes.  On the way there (33,280 packed rows): the 16 query rows as the MMA's
+// rows 699 us; as columns, eight at a time 374; steps of 16 rows in a loop that the
+// instruction cache holds, scales of a step together 348; four CTAs an SM 317; keys as
+// subnormal numbers (one shift a word instead of three) 286; shifts as high products of
+// the multiplier, which is idle, 299.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -701,26 +711,59 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
     cluster_meet();   // a CTA's state is read by the others until here
 }
 
+namespace {
+
+struct Variant {
+    void (*kernel)(PageArgs, PageTable, int);
+    int smem, ctas;
+};
+template <int NR, bool kPack>
+Variant variant()
+{
+    return {k_page_decode<NR, kPack>, Ring<NR, kPack>::kSmem, Ring<NR, kPack>::kCtas};
+}
+
+// Clusters of 1, 2, 4 and 8 CTAs that the device holds at once.
+cudaError_t capacities(const Variant &v, int (&cap)[4])
+{
+    cudaError_t e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(8u << i);
+        cfg.blockDim = dim3(kPdThreads);
+        cfg.dynamicSmemBytes = (size_t)v.smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1u << i;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&cap[i], v.kernel, &cfg);
+    }
+    return e;
+}
+
+}  // namespace
+
 cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevPageReq *host_reqs, int n_sms, cudaStream_t s)
 {
-    static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
+    const Variant variants[4] = {variant<1, false>(), variant<2, false>(), variant<1, true>(), variant<2, true>()};
+    static std::atomic<bool> known[64] = {};   // per device (host threads may race: same values)
+    static int caps[64][4][4];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        auto allow = [&](auto *k, int smem) {
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        };
-        allow(k_page_decode<1, false>, Ring<1, false>::kSmem);
-        allow(k_page_decode<2, false>, Ring<2, false>::kSmem);
-        allow(k_page_decode<1, true>, Ring<1, true>::kSmem);
-        allow(k_page_decode<2, true>, Ring<2, true>::kSmem);
-        if (e != cudaSuccess)
-            return e;
-        if (dev < 64)
-            attr_set[dev].store(true, std::memory_order_release);
+    int own[4][4], (*cap)[4] = dev < 64 ? caps[dev] : own;
+    if (dev >= 64 || !known[dev].load(std::memory_order_acquire)) {
+        for (int i = 0; i < 4; ++i)
+            if ((e = capacities(variants[i], own[i])) != cudaSuccess)
+                return e;
+        if (dev < 64) {
+            for (int i = 0; i < 16; ++i)
+                caps[dev][i / 4][i % 4] = own[i / 4][i % 4];
+            known[dev].store(true, std::memory_order_release);
+        }
     }
     const int units = a.n_layers * a.n_kv_heads, G = a.n_q_heads / a.n_kv_heads;
     int64_t few = 0, bytes = 0;   // of one unit's tiles
@@ -739,25 +782,37 @@ cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevP
     }
     if (few == 0)
         return cudaSuccess;
-    // CTAs of a (request, unit): the largest share of an SM decides, its CTAs' bytes (44 GB/s
-    // when the SM is full, less with one or two CTAs on it) and 1.5 us more for each.  One
-    // request of 33,280 packed rows, 256 units: 819 us with one, 1.7 CTAs an SM.
+    const int which = (packed ? 2 : 0) + (rows > 8 ? 1 : 0);
+    // CTAs of a (request, unit), by an estimate of the call's time in us: 6 to start and end;
+    // the bytes at the card's pace (6.4 TB/s, on packed rows at the instructions', 4.1); where all
+    // clusters are resident at once the fullest SM's share at that SM's pace (36, 54, 60
+    // GB/s for one, two, three CTAs; 19 and 27 packed); else 5 for each round behind the
+    // first and half a CTA's time for the last ones.  Measured with 1, 2, 4, 8 CTAs:
+    //   bf16, 2,656 rows: 112 units 45, 31, 42, 44 us; 32 units 43, 26, 17, 15; 336
+    //     (request, unit) pairs 72, 80, 88, 103; 4,100 rows, 256 units: 90, 115, 98, 113
+    //   packed, 33,280 rows: 256 units 355, 320, 301, 288 us; 16 units 255, 136, 75, 50;
+    //     1,216 rows, 288 units 20, 20, 25, 38
+    const double pace[2][3] = {{36e3, 54e3, 60e3}, {19e3, 27e3, 27e3}}, total = (double)bytes * units;
     int c = 1;
     double best = 1e30;
-    for (int k = 1; k <= 8; k *= 2) {
-        const double load = (double)((few * units * k + n_sms - 1) / n_sms);
-        const double t1 = load * ((double)bytes / (double)(few * k) / 44e3 + 1.5) * (load < 2. ? 2.2 : load < 3. ? 1.3 : 1.);
-        if (t1 < 0.97 * best) {
-            best = t1;
-            c = k;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t n = few * units << i, room = std::max<int64_t>(1, (int64_t)cap[which][i] << i);
+        const double cta = (double)bytes / (double)(few << i);   // bytes of one
+        double us = total / (packed ? 4.1e6 : 6.4e6);
+        if (n <= room) {
+            const int64_t k = (n + n_sms - 1) / n_sms;
+            us = std::max(us, (double)k * cta / pace[packed][std::min<int64_t>(k, 3) - 1]);
+        } else {
+            us += 5. * (double)((n - 1) / room) + 0.5 * cta / pace[packed][0];
+        }
+        us += i ? 1. : 0.;
+        if (us < 0.97 * best) {
+            best = us;
+            c = 1 << i;
         }
     }
-    auto launch = [&](auto *k, int smem) {
-        return launch_cluster(k, (int64_t)a.n_reqs * units * c, kPdThreads, smem, c, s, a, t, c);
-    };
-    if (packed)
-        return rows <= 8 ? launch(k_page_decode<1, true>, Ring<1, true>::kSmem) : launch(k_page_decode<2, true>, Ring<2, true>::kSmem);
-    return rows <= 8 ? launch(k_page_decode<1, false>, Ring<1, false>::kSmem) : launch(k_page_decode<2, false>, Ring<2, false>::kSmem);
+    const Variant &v = variants[which];
+    return launch_cluster(v.kernel, (int64_t)a.n_reqs * units * c, kPdThreads, v.smem, c, s, a, t, c);
 }
 
 }  // namespace kvr
