@@ -32,17 +32,19 @@
 // memory's pace leaves room for that, and the output is off by its own rounding alone
 // (0.0017 of its norm; 0.0029 with one term each).  Queries that meet packed rows are fp16
 // times a power of two of their row, the largest element between 2^12 and 2^13 (11 bits of
-// an element, fewer only below 2^-26 of the largest); probabilities there are rounded to
+// an element, fewer only below 2^-22 of the largest); probabilities there are rounded to
 // bf16 (0.0024), as the step is bound by instructions.
 //
 // Measured: 4 x 2,656 bf16 rows, 112 units 97 us (6.3 TB/s); 8 windows of 4,100 rows, 256
 // units 605 us (7.1 TB/s; reads alone run above the copy rate).  33,280 packed rows, 256
-// units 285 us, 4.3 TB/s; the integer pipe is busy 0.6 of the time, half of it with
+// units 269 us, 4.6 TB/s; the integer pipe is busy 0.6 of the time, half of it with
 // extracting codes.  On the way there (33,280 packed rows): the 16 query rows as the MMA's
 // rows 699 us; as columns, eight at a time 374; steps of 16 rows in a loop that the
-// instruction cache holds, scales of a step together 348; four CTAs an SM 317; keys as
-// subnormal numbers (one shift a word instead of three) 286; shifts as high products of
-// the multiplier, which is idle, 299.
+// instruction cache holds, scales of a step together 348 (not a loop, 16 x 1,216 rows take
+// 240 us, 197 as one); four CTAs an SM 317; keys as subnormal numbers (one shift a word
+// instead of three) 286; both products of a group in one accumulator, the upper nibbles'
+// queries a sixteenth 269.  Shifts as high products of the multiplier, which is idle: 299
+// against 286.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -155,6 +157,16 @@ __device__ __forceinline__ void mma_f16_from(float *d, const uint32_t *a, uint32
         "{%10, %11, %10, %11};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]));
+}
+
+// d += a b in fp16
+__device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi)
@@ -360,9 +372,10 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
             for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
+                    // (the pairs that meet the nibbles four bits higher are a sixteenth)
                     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at(x, 0, gp + 2 * k) + 8u * (uint32_t)y),
                                  "r"(pack2_f16(f[x][k][0] * up[x], f[x][k][1] * up[x])),
-                                 "r"(pack2_f16(f[x][k][2] * up[x], f[x][k][3] * up[x]))
+                                 "r"(pack2_f16(f[x][k][2] * up[x] * 0.0625f, f[x][k][3] * up[x] * 0.0625f))
                                  : "memory");
         } else {
 #pragma unroll
@@ -400,7 +413,7 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
             for (int g = 0; g < 4; ++g) {
                 const uint4 q = query(x, 0, g);
                 const float2 v[4] = {unpack2_f16(q.x), unpack2_f16(q.y), unpack2_f16(q.z), unpack2_f16(q.w)};
-                float s = ((v[0].x + v[0].y) + (v[1].x + v[1].y)) + ((v[2].x + v[2].y) + (v[3].x + v[3].y));
+                float s = fmaf(16.f, (v[1].x + v[1].y) + (v[3].x + v[3].y), (v[0].x + v[0].y) + (v[2].x + v[2].y));
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
                 s *= -8.f / 16777216.f;
@@ -440,20 +453,19 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
             for (int g = 0; g < 4; ++g) {
                 const uint32_t y0 = g < 2 ? z.x : z.y, y1 = g < 2 ? z.z : z.w;
                 const float x0 = (g & 1) ? bf_hi(y0) : bf_lo(y0), x1 = (g & 1) ? bf_hi(y1) : bf_lo(y1);
-                // pairs 0 and 2 of the words; pairs 1 and 3, which count 16 times
+                // pairs 0 and 2 of the words; pairs 1 and 3, which are 16 times as much
                 const uint32_t v0 = w0[g] >> 8, v1 = w1[g] >> 8;
                 const uint32_t a0[4] = {w0[g] & 0x000f000fu, w1[g] & 0x000f000fu, v0 & 0x000f000fu, v1 & 0x000f000fu};
                 const uint32_t a1[4] = {w0[g] & 0x00f000f0u, w1[g] & 0x00f000f0u, v0 & 0x00f000f0u, v1 & 0x00f000f0u};
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
-                    const float zero[2] = {0.f, 0.f};
-                    float d[4], d16[4];
                     const uint4 q = query(x, 0, g);
+                    float d[4];
                     mma_f16_from(d, a0, q.x, q.z, start[x][g]);
-                    mma_f16_from(d16, a1, q.y, q.w, zero);
+                    mma_f16(d, a1, q.y, q.w);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        s[x][e] = fmaf(e < 2 ? x0 : x1, fmaf(d16[e], 0.0625f, d[e]), s[x][e]);
+                        s[x][e] = fmaf(e < 2 ? x0 : x1, d[e], s[x][e]);
                 }
             }
         } else {
@@ -471,7 +483,7 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             const float2 v = unpack2_f16(w[m]);
-                            two_terms(v.x, v.y, hi[m], lo[m]);
+                            two_terms(v.x * ((m & 1) ? 16.f : 1.f), v.y * ((m & 1) ? 16.f : 1.f), hi[m], lo[m]);
                         }
                     } else {
                         const uint4 p = query(x, 0, g), q = query(x, 1, g);
