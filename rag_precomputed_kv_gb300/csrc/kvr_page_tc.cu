@@ -372,7 +372,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             if (!ok)
                 break;
+            // the row's place, before its output is waited for
             const bool any = b.je > b.jb;   // (else no product was issued, O is not this item's)
+            const int row = b.row0 + x * 128 + r, tok = row / G;
+            const bool row_ok = x * 128 + r < b.rows;
+            const Sees see = sees(a, b.rq, pos);
+            const bool some = row_ok && any && see.hi > 0 && (see.few > 0 || see.lo < see.hi);
+            const int out_row = row_ok ? (b.l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + b.h * G + (row - tok * G) : -1;
             if (any) {
                 if (!mbar_wait_warp(bar(kTbO + x), (uint32_t)o_cnt & 1u, abort_flag)) {
                     ok = false;
@@ -381,16 +387,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 ++o_cnt;
                 tc_fence_after();
             }
-            const int row = b.row0 + x * 128 + r, tok = row / G;
-            const bool row_ok = x * 128 + r < b.rows;
-            const Sees see = sees(a, b.rq, pos);
-            const bool some = row_ok && any && see.hi > 0 && (see.few > 0 || see.lo < see.hi);
             if (p.splits == 1) {   // the row's output
-                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                       (((int64_t)b.l * a.total_q + b.rq.q_off + tok) * a.n_q_heads + b.h * G + (row - tok * G)) * 128);
                 if (some && !(l_run > 0.f && l_run < INFINITY))
                     atomicCAS(a.err, kDevOk, kDevBadInput);
                 const float inv = 1.f / l_run;
+                // packed first: the next item's first P V is let into O before the stores
+                uint32_t v[64];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float o[32];
@@ -398,22 +400,43 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         tmem_ld32(lane_base + pt_col_o(x) + 32 * q, o);
                         tmem_wait_ld();
                     }
-                    if (row_ok) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = some ? o[i] * inv : 0.f;
+                    for (int i = 0; i < 16; ++i)
+                        v[16 * q + i] = some ? pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
+                }
+                if (any)
+                    warp_arrive(kTbOEmpty + x);
+                geo_done(item);
+                if (idle)
+                    continue;
+                // four lanes change their rows' 32-byte pieces so that they write whole lines
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t v[8];
+                for (int m = 1; m <= 2; m <<= 1)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                v[k] = pack_bf16(o[16 * i + 2 * k], o[16 * i + 2 * k + 1]);
-                            if (p.out32) {   // (whole sectors: a row a thread)
-                                st_global_v8(out + 4 * q + 2 * i, v);
-                            } else {
-                                out[4 * q + 2 * i] = make_uint4(v[0], v[1], v[2], v[3]);
-                                out[4 * q + 2 * i + 1] = make_uint4(v[4], v[5], v[6], v[7]);
-                            }
+                    for (int i = 0; i < 64; ++i)
+                        if (!(i >> 3 & m)) {
+                            const int k = i + 8 * m;
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & m) ? v[i] : v[k], m);
+                            v[i] = (lane & m) ? got : v[i];
+                            v[k] = (lane & m) ? v[k] : got;
+                        }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + i);
+                    if (at < 0)
+                        continue;
+                    uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (int64_t)at * 128) + 2 * (lane & 3);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = v[32 * hf + 8 * i + k];
+                        if (p.out32) {
+                            st_global_v8(out + 8 * hf, w);
+                        } else {
+                            out[8 * hf] = make_uint4(w[0], w[1], w[2], w[3]);
+                            out[8 * hf + 1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
                     }
                 }
@@ -435,11 +458,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             po[(8 * q + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
+                if (any)
+                    warp_arrive(kTbOEmpty + x);
+                geo_done(item);
             }
-            if (any) {
-                warp_arrive(kTbOEmpty + x);
-            }
-            geo_done(item);
         }
         if (!ok)
             give_up(a.err, abort_flag);
