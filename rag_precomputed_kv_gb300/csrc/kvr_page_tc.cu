@@ -107,19 +107,21 @@ struct alignas(16) Block {
     int row0, rows, nx;      // first packed row in the request, rows (<= 256), 128-row tiles
     int hi, lo;              // rows that some query of the block sees: j < hi and (j >= lo or a first one)
     Sees any;                // ... and of the request
-    int p0, p1;              // positions of its first and last token
-    int n_first, t_win;      // tiles of the first rows; the window's first tile
-    int jb, je;              // the item's tiles of the list
+    int all_hi, all_lo;      // rows that all its queries see: j < all_hi and (j >= all_lo or a first one)
+    int first, shift;        // place v of the list of rows is row v, from `first` on row v + shift
+    int jb, je;              // the item's 128-row tiles of the list
 
-    RestTiles rest;
-    int rest_row0;           // the request's first restored row of the unit
+    int rest_first, rest_row[2];   // row j is restored row rest_row[j >= rest_first] + j
     int64_t unit;            // elements from a page's start to the (layer, kv-head)'s first row
 
-    __device__ __forceinline__ int tile(int i) const { return i < n_first ? i : t_win + i - n_first; }
+    __device__ __forceinline__ int row(int v) const { return v < first ? v : v + shift; }
+    // tile j has first rows and others
+    __device__ __forceinline__ bool cut(int j) const { return shift > 0 && j * kPtTile < first && j * kPtTile + kPtTile > first; }
     __device__ __forceinline__ bool all_seen(int j0, int j1) const { return j1 <= any.hi && (j0 >= any.lo || j1 <= any.few); }
     __device__ __forceinline__ bool some_seen(int j0, int j1) const { return j0 < any.few || (j0 < any.hi && j1 > any.lo); }
-    __device__ __forceinline__ bool restored(int k) const { return k * kPtTile < rq.packed_len; }
-    __device__ __forceinline__ int rest_row(int k) const { return rest_row0 + rest.place(k) * kPtTile; }
+    // tile j is one of restored rows (a request's that has packed ones are whole tiles of its cache)
+    __device__ __forceinline__ bool restored(int j) const { return rq.packed_len > 0 && row(j * kPtTile) < rq.packed_len; }
+    __device__ __forceinline__ int place(int j) const { return j + (j < rest_first ? rest_row[0] : rest_row[1]); }
 };
 static_assert(sizeof(Block) <= kPtGeoBytes, "geometry ring");
 
@@ -145,16 +147,22 @@ __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p
     s.row0 = blk * 256;
     s.rows = min(256, all - s.row0);
     s.nx = s.rows > 128 ? 2 : 1;
-    s.p0 = s.rq.pos0 + s.row0 / G;
-    s.p1 = s.rq.pos0 + (s.row0 + s.rows - 1) / G;
-    s.hi = min(s.rq.kv_len, s.p1 + 1);
-    s.lo = min(s.hi, a.window > 0 ? max(0, s.p0 - a.window + 1) : 0);
+    const int p0 = s.rq.pos0 + s.row0 / G, p1 = s.rq.pos0 + (s.row0 + s.rows - 1) / G;   // its first and last token
+    s.hi = min(s.rq.kv_len, p1 + 1);
+    s.lo = min(s.hi, a.window > 0 ? max(0, p0 - a.window + 1) : 0);
+    s.all_hi = min(s.rq.kv_len, p0 + 1);
+    s.all_lo = a.window > 0 ? p1 - a.window + 1 : 0;
     s.any = sees_any(a, s.rq);
-    s.rest = rest_tiles(s.any.hi, s.any.lo, s.any.few, s.rq.packed_len);
-    s.rest_row0 = (lh_s * p.unit_tiles + s.rq.tile0) * kPtTile;
-    s.n_first = (min(a.n_first, s.lo) + kPtTile - 1) / kPtTile;
-    s.t_win = max(s.n_first, s.lo / kPtTile);
-    const int n = s.n_first + max(0, (s.lo < s.hi ? (s.hi + kPtTile - 1) / kPtTile : 0) - s.t_win);
+    const RestTiles rest = rest_tiles(s.any.hi, s.any.lo, s.any.few, s.rq.packed_len);
+    s.rest_first = rest.first * kPtTile;
+    s.rest_row[0] = (lh_s * p.unit_tiles + s.rq.tile0) * kPtTile;
+    s.rest_row[1] = s.rest_row[0] + (rest.first - rest.win) * kPtTile;
+    // the rows listed: the first ones and those from s.lo on, both rounded out to whole boxes
+    const int g = s.rq.packed_len > 0 ? kPtTile : p.box ? p.box : 16;
+    s.first = (min(a.n_first, s.lo) + g - 1) / g * g;
+    const int w0 = max(s.first, s.lo / g * g);
+    s.shift = w0 - s.first;
+    const int n = (s.first + (s.lo < s.hi ? max(0, s.hi - w0) : 0) + kPtTile - 1) / kPtTile;
     s.jb = (int)((int64_t)n * sp / p.splits);
     s.je = (int)((int64_t)n * (sp + 1) / p.splits);
     return s;
@@ -168,7 +176,7 @@ __device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8])
 }
 
 // A tile that warps 10 and 11 fill.
-__device__ __forceinline__ bool by_hand(const PageTcArgs &p, const Block &s, int k) { return p.box == 0 && !s.restored(k); }
+__device__ __forceinline__ bool by_hand(const PageTcArgs &p, const Block &s, int j) { return p.box == 0 && !s.restored(j); }
 
 }  // namespace
 
@@ -258,8 +266,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int pos = b.rq.pos0 + (b.row0 + x * 128 + r) / G;
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = b.jb; j < b.je; ++j) {
-                const int k0 = b.tile(j) * kPtTile, k1 = k0 + kPtTile;
-                const bool all = k1 <= min(b.rq.kv_len, b.p0 + 1) && (a.window == 0 || k0 > b.p1 - a.window || k1 <= a.n_first);
+                const int k0 = b.row(j * kPtTile), k1 = k0 + kPtTile;
+                const bool all = !b.cut(j) && k1 <= b.all_hi && (k0 >= b.all_lo || k1 <= a.n_first);
                 // (one tile uses both S buffers by turns)
                 const bool odd = kOne && ((j - b.jb) & 1);
                 const int sb = odd ? 1 : x;
@@ -290,27 +298,41 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     continue;
                 }
                 const uint32_t s_cols = lane_base + pt_col_s(sb);
+                if (!all) {
+                    // scores of rows that this query does not see go, in TMEM: a loop over 32 columns (in
+                    // place of 128 selects in registers: the code of an item's tiles and its end stays
+                    // within what the instruction cache holds)
+                    const Sees see = sees(a, b.rq, pos);
+                    const bool cut = b.cut(j);
+                    const int f = cut ? b.first - j * kPtTile : kPtTile;
+                    auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+                    auto seen = [&](int k) -> uint32_t {   // of rows k .. k + 31
+                        return below(see.hi - k) & (~below(see.lo - k) | below(see.few - k));
+                    };
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t m = seen(k0 + 32 * q);
+                        if (cut) {
+                            const uint32_t n = below(f - 32 * q);
+                            m = (m & n) | (seen(k0 + 32 * q + b.shift) & ~n);
+                        }
+                        if (__all_sync(0xffffffffu, m == ~0u))
+                            continue;
+                        float t[32];
+                        tmem_ld32(s_cols + 32 * q, t);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            t[c] = (m >> c & 1u) ? t[c] : -INFINITY;
+                        tmem_st32(s_cols + 32 * q, t);
+                    }
+                    tmem_wait_st();
+                }
                 float s[kPtTile];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     tmem_ld32(s_cols + 32 * q, s + 32 * q);
                 tmem_wait_ld();
-                if (!all) {
-                    const Sees see = sees(a, b.rq, pos);
-                    const int hi = see.hi - k0, lo = see.lo - k0, few = see.few - k0;
-                    // (as bits: a compare and a select for each column cost as much as the rest of the
-                    // softmax)
-                    auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t m = below(hi - 32 * q) & (~below(lo - 32 * q) | below(few - 32 * q));
-                        if (m != ~0u) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                s[32 * q + c] = (m >> c & 1u) ? s[32 * q + c] : -INFINITY;
-                        }
-                    }
-                }
                 float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int c = 4; c + 4 < kPtTile; c += 8) {
@@ -356,7 +378,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (!ok)
                     break;
                 if (rescale) {
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         float o[32];
                         tmem_ld32(lane_base + pt_col_o(x) + 32 * q, o);
@@ -391,55 +413,57 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (some && !(l_run > 0.f && l_run < INFINITY))
                     atomicCAS(a.err, kDevOk, kDevBadInput);
                 const float inv = 1.f / l_run;
-                // packed first: the next item's first P V is let into O before the stores
-                uint32_t v[64];
+                // half a row at a time; four lanes change their rows' 32-byte pieces so that they write
+                // whole lines
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t v[32];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float o[32];
-                    if (any) {
-                        tmem_ld32(lane_base + pt_col_o(x) + 32 * q, o);
-                        tmem_wait_ld();
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        v[16 * q + i] = some ? pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
-                }
-                if (any)
-                    warp_arrive(kTbOEmpty + x);
-                geo_done(item);
-                if (idle)
-                    continue;
-                // four lanes change their rows' 32-byte pieces so that they write whole lines
-#pragma unroll
-                for (int m = 1; m <= 2; m <<= 1)
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (!(i >> 3 & m)) {
-                            const int k = i + 8 * m;
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & m) ? v[i] : v[k], m);
-                            v[i] = (lane & m) ? got : v[i];
-                            v[k] = (lane & m) ? v[k] : got;
+                    for (int q = 0; q < 2; ++q) {
+                        float o[32];
+                        if (any) {
+                            tmem_ld32(lane_base + pt_col_o(x) + 64 * hf + 32 * q, o);
+                            tmem_wait_ld();
                         }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + i);
-                    if (at < 0)
+                        for (int i = 0; i < 16; ++i)
+                            v[16 * q + i] = some ? pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
+                    }
+                    // O is read: the next item's first P V is let into it
+                    if (any && hf == 1)
+                        warp_arrive(kTbOEmpty + x);
+                    if (idle)
                         continue;
-                    uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (int64_t)at * 128) + 2 * (lane & 3);
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
+                    for (int m = 1; m <= 2; m <<= 1)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(i >> 3 & m)) {
+                                const int k = i + 8 * m;
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & m) ? v[i] : v[k], m);
+                                v[i] = (lane & m) ? got : v[i];
+                                v[k] = (lane & m) ? v[k] : got;
+                            }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + i);
+                        if (at < 0)
+                            continue;
+                        uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (int64_t)at * 128) + 8 * hf +
+                                     2 * (lane & 3);
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            w[k] = v[32 * hf + 8 * i + k];
+                            w[k] = v[8 * i + k];
                         if (p.out32) {
-                            st_global_v8(out + 8 * hf, w);
+                            st_global_v8(out, w);
                         } else {
-                            out[8 * hf] = make_uint4(w[0], w[1], w[2], w[3]);
-                            out[8 * hf + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            out[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
                     }
                 }
+                geo_done(item);
             } else {
                 const int64_t w = blockIdx.x + (int64_t)item * gridDim.x;
                 if (row_ok)
@@ -494,24 +518,26 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (n_loads == 0)
                 continue;
             const int64_t unit = b.unit / 128;
-            // tile i of the item: the row of this lane's box (box lane / 2, panel lane & 1) and whether
+            // tile i of the list: the row of this lane's box (box lane / 2, panel lane & 1) and whether
             // it is to be loaded; the same for keys and values
             // (a page's number is asked for a tile ahead of its use)
             int row = 0, at = 0, rows = 0, id = 0, in = 0;
             bool hand = false, load = false, rest = false;
             auto find = [&](int i) {
-                const int k = b.tile(i);
-                rest = b.restored(k);
-                hand = by_hand(p, b, k);
+                rest = b.restored(i);
+                hand = by_hand(p, b, i);
                 rows = rest ? kPtTile : p.box;
                 at = (lane >> 1) * rows;
-                const int j0 = k * kPtTile + at;
+                const int j0 = b.row(i * kPtTile + at);
                 load = !hand && at < kPtTile && (rest || b.some_seen(j0, j0 + rows));
                 if (load) {
-                    const int pg = page_of(a, j0);
-                    in = rest ? b.rest_row(k) : j0 - pg * a.g.rows;
-                    if (!rest)
+                    if (rest) {
+                        in = b.place(j0);
+                    } else {
+                        const int pg = page_of(a, j0);
+                        in = j0 - pg * a.g.rows;
                         id = page_id(b.rq, ids, pg);
+                    }
                 }
             };
             find(b.jb);
@@ -573,9 +599,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
         pdl_wait_prerequisites();
         const uint32_t lead = elect_one();
-        int tt = 0, nq = 0, oe_cnt[2] = {0, 0};
-        uint32_t p_par = 0;   // bit i: the parity of P barrier i's next phase
-        bool o_used[2] = {false, false}, ok = true;
+        int tt = 0, nq = 0;
+        // bit x: the parity of P (O) barrier x's next phase; O x holds an output
+        uint32_t p_par = 0, o_par = 0, o_used = 0;
+        bool ok = true;
         const uint64_t d_k = sdesc(sbase, 16, 1024), d_v = sdesc(sbase, kPtPanel, 1024);
         const uint32_t lo_k = (uint32_t)d_k, hi_k = (uint32_t)(d_k >> 32), lo_v = (uint32_t)d_v, hi_v = (uint32_t)(d_v >> 32);
         auto wait_kv = [&](int k) -> bool {
@@ -613,21 +640,26 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 geo_done(item);
                 continue;
             }
-            // V tile i of the item has rows that no query sees, which have to be zeroed (worked out
-            // while the tile's probabilities are: nothing stands between them and the product)
+            // V tile i of the item has rows that no query sees, which have to be zeroed: only one where the
+            // first rows or the window begin or end
+            const int j_cut = b.first / kPtTile, j_end = (b.any.hi - b.shift) / kPtTile;
             auto holes = [&](int i) -> bool {
-                const int k = b.tile(b.jb + i), k0 = k * kPtTile;
-                return !by_hand(p, b, k) && !b.restored(k) && !b.all_seen(k0, k0 + kPtTile);
+                const int j = b.jb + i, v0 = j * kPtTile, v1 = v0 + kPtTile;
+                if (j > j_cut && j < j_end)
+                    return false;
+                const bool all = b.cut(j) ? b.all_seen(v0, b.first) && b.all_seen(b.first + b.shift, v1 + b.shift)
+                                          : b.all_seen(b.row(v0), b.row(v0) + kPtTile);
+                return !all && !by_hand(p, b, j) && !b.restored(j);
             };
             // V tile i: landed, such rows zeroed
             auto wait_v = [&](int i, bool zero) -> bool {
                 if (!wait_kv(tt + 2 * i + 1))
                     return false;
                 if (zero) {
-                    const int k0 = b.tile(b.jb + i) * kPtTile;
+                    const int v0 = (b.jb + i) * kPtTile;
                     const uint32_t v = sbase + (uint32_t)(kPtOffKV + ((tt + 2 * i + 1) % kPtSlots) * kPtTileBytes);
                     for (int c = lane; c < kPtTile * 8; c += 32)
-                        if (!b.any(k0 + (c >> 3))) {
+                        if (!b.any(b.row(v0 + (c >> 3)))) {
                             st_shared_v4(v + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
                             st_shared_v4(v + kPtPanel + 16u * (uint32_t)c, 0u, 0u, 0u, 0u);
                         }
@@ -637,11 +669,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 return true;
             };
             auto o_free = [&](int x) -> bool {
-                if (o_used[x]) {
-                    if (!mbar_wait_warp(bar(kTbOEmpty + x), (uint32_t)oe_cnt[x] & 1, abort_flag))
+                if (o_used >> x & 1u) {
+                    if (!mbar_wait_warp(bar(kTbOEmpty + x), o_par >> x & 1u, abort_flag))
                         return false;
-                    ++oe_cnt[x];
-                    o_used[x] = false;
+                    o_par ^= 1u << x;
+                    o_used ^= 1u << x;
                 }
                 return true;
             };
@@ -676,7 +708,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     umma_commit(lead, bar(kTbEmpty + (tt + 2 * i + 1) % kPtSlots));
                     ok = i + 2 >= K || s_of(i + 2);
                 }
-                o_used[0] = true;
+                o_used = 1u;
             } else {
             ok = wait_kv(tt);
             if (!ok)
@@ -696,20 +728,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     if (x == 1 && !two)
                         break;
-                    if (!mbar_wait_warp(bar(kTbP + x), (p_par >> x) & 1u, abort_flag)) {
+                    // (the probabilities last: nothing stands between them and the product)
+                    if ((x == 0 && !wait_v(i, zero)) || (i == 0 && !o_free(x)) ||
+                        !mbar_wait_warp(bar(kTbP + x), (p_par >> x) & 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
                     p_par ^= 1u << x;
-                    if ((x == 0 && !wait_v(i, zero)) || (i == 0 && !o_free(x))) {
-                        ok = false;
-                        break;
-                    }
                     tc_fence_after();
                     issue_pv(x, tt + 2 * i + 1, i > 0, x);
                     if (!more) {
                         umma_commit(lead, bar(kTbO + x));
-                        o_used[x] = true;
+                        o_used |= 1u << x;
                     } else {
                         if (x == 0 && !wait_kv(tt + 2 * i + 2)) {
                             ok = false;
@@ -748,8 +778,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const Block &b = geo(item);
             const int n_loads = 2 * (b.je - b.jb);
             for (int i = 0; i < n_loads; ++i, ++tt) {
-                const int slot = tt % kPtSlots, k = b.tile(b.jb + (i >> 1));
-                if (!by_hand(p, b, k))
+                const int slot = tt % kPtSlots, t = b.jb + (i >> 1);
+                if (!by_hand(p, b, t))
                     continue;
                 if (!mbar_wait_warp(bar(kTbJob + slot), (jobs >> slot) & 1u, abort_flag)) {
                     ok = false;
@@ -761,7 +791,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const int ch = lane & 15;
 #pragma unroll 8
                 for (int y = 0; y < 32; ++y) {
-                    const int row = 64 * (warp - 10) + 2 * y + (lane >> 4), j = k * kPtTile + row;
+                    const int row = 64 * (warp - 10) + 2 * y + (lane >> 4), j = b.row(t * kPtTile + row);
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (b.any(j)) {
                         const int pg = page_of(a, j);
