@@ -2513,6 +2513,7 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
                 (st = p->grow_part_scratch((size_t)(2 * rest_bytes + part_bytes))) != KVR_OK ||
                 (st = encode_rows_map(*p, p->q_rot, q_rows, 128, &mq)) != KVR_OK)
                 return st;
+            tc.q_rot = p->q_rot;
             tc.rest_k = p->part;
             tc.rest_v = static_cast<char *>(p->part) + rest_bytes;
             tc.part = reinterpret_cast<float *>(static_cast<char *>(p->part) + 2 * rest_bytes);

@@ -518,6 +518,7 @@ struct PageTcArgs {
     int32_t one_tile;       // no request has more than 128 of the kernel's rows
     int32_t out32;          // `out` is 32-byte aligned
     void *rest_k, *rest_v;  // restored rows
+    const void *q_rot;      // the turned queries
 };
 
 // ---- launchers (each returns the cudaGetLastError of its launch) ----

@@ -74,7 +74,7 @@ constexpr int kPtOffQ = 0;
 constexpr int kPtOffKV = 2 * kPtTileBytes;
 constexpr int kPtOffBar = kPtOffKV + kPtSlots * kPtTileBytes;
 constexpr int kTbFull = 0, kTbEmpty = kTbFull + kPtSlots, kTbS = kTbEmpty + kPtSlots, kTbP = kTbS + 2, kTbO = kTbP + 2,
-              kTbOEmpty = kTbO + 2, kTbPv = kTbOEmpty + 2, kTbQ = kTbPv + 1, kTbQEmpty = kTbQ + 1, kTbDrain = kTbQEmpty + 1,
+              kTbOEmpty = kTbO + 2, kTbPv = kTbOEmpty + 2, kTbQ = kTbPv + 1, kTbQEmpty = kTbQ + 2, kTbDrain = kTbQEmpty + 1,
               kTbJob = kTbDrain + 1, kTbGeo = kTbJob + kPtSlots, kTbGeoFree = kTbGeo + kPtGeos, kTbNum = kTbGeoFree + kPtGeos;
 constexpr int kPtOffMisc = kPtOffBar + 8 * kTbNum;
 constexpr int kPtOffGeo = (kPtOffMisc + 16 + 15) & ~15;
@@ -157,10 +157,11 @@ __device__ __forceinline__ Block block_at(const PageArgs &a, const PageTcArgs &p
     s.rest_first = rest.first * kPtTile;
     s.rest_row[0] = (lh_s * p.unit_tiles + s.rq.tile0) * kPtTile;
     s.rest_row[1] = s.rest_row[0] + (rest.first - rest.win) * kPtTile;
-    // the rows listed: the first ones and those from s.lo on, both rounded out to whole boxes
-    const int g = s.rq.packed_len > 0 ? kPtTile : p.box ? p.box : 16;
-    s.first = (min(a.n_first, s.lo) + g - 1) / g * g;
-    const int w0 = max(s.first, s.lo / g * g);
+    // the rows listed: the first ones and those from s.lo on, both rounded out to whole boxes; 32 places
+    // in a row hold rows in a row
+    const int g = s.rq.packed_len > 0 ? kPtTile : p.box ? p.box : 16, g32 = max(g, 32);   // (powers of two)
+    s.first = (min(a.n_first, s.lo) + g32 - 1) & -g32;
+    const int w0 = max(s.first, s.lo & -g);
     s.shift = w0 - s.first;
     const int n = (s.first + (s.lo < s.hi ? max(0, s.hi - w0) : 0) + kPtTile - 1) / kPtTile;
     s.jb = (int)((int64_t)n * sp / p.splits);
@@ -303,19 +304,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     // place of 128 selects in registers: the code of an item's tiles and its end stays
                     // within what the instruction cache holds)
                     const Sees see = sees(a, b.rq, pos);
-                    const bool cut = b.cut(j);
-                    const int f = cut ? b.first - j * kPtTile : kPtTile;
-                    auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-                    auto seen = [&](int k) -> uint32_t {   // of rows k .. k + 31
-                        return below(see.hi - k) & (~below(see.lo - k) | below(see.few - k));
+                    auto below = [](int n) -> uint32_t {
+                        uint32_t r;
+                        asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(max(n, 0)));
+                        return r;
                     };
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t m = seen(k0 + 32 * q);
-                        if (cut) {
-                            const uint32_t n = below(f - 32 * q);
-                            m = (m & n) | (seen(k0 + 32 * q + b.shift) & ~n);
-                        }
+                        const int k = b.row(j * kPtTile + 32 * q);
+                        const uint32_t m = below(see.hi - k) & (~below(see.lo - k) | below(see.few - k));
                         if (__all_sync(0xffffffffu, m == ~0u))
                             continue;
                         float t[32];
@@ -421,10 +418,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float o[32];
-                        if (any) {
-                            tmem_ld32(lane_base + pt_col_o(x) + 64 * hf + 32 * q, o);
-                            tmem_wait_ld();
-                        }
+                        tmem_ld32(lane_base + pt_col_o(x) + 64 * hf + 32 * q, o);   // (not this item's without a tile: then `some` is not set)
+                        tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             v[16 * q + i] = some ? pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
@@ -435,31 +430,31 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     if (idle)
                         continue;
 #pragma unroll
-                    for (int m = 1; m <= 2; m <<= 1)
+                    for (int i = 0; i < 32; ++i)
+                        if (!(i >> 3 & 1)) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[i] : v[i + 8], 1);
+                            v[i] = (lane & 1) ? got : v[i];
+                            v[i + 8] = (lane & 1) ? v[i + 8] : got;
+                        }
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(i >> 3 & m)) {
-                                const int k = i + 8 * m;
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & m) ? v[i] : v[k], m);
-                                v[i] = (lane & m) ? got : v[i];
-                                v[k] = (lane & m) ? v[k] : got;
-                            }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int at = __shfl_sync(0xffffffffu, out_row, (lane & ~3) + i);
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = __shfl_sync(0xffffffffu, out_row, (lane & ~1) + i);
                         if (at < 0)
                             continue;
                         uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (int64_t)at * 128) + 8 * hf +
-                                     2 * (lane & 3);
-                        uint32_t w[8];
+                                     2 * (lane & 1);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            w[k] = v[8 * i + k];
-                        if (p.out32) {
-                            st_global_v8(out, w);
-                        } else {
-                            out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                w[k] = v[16 * c + 8 * i + k];
+                            if (p.out32) {
+                                st_global_v8(out + 4 * c, w);
+                            } else {
+                                out[4 * c] = make_uint4(w[0], w[1], w[2], w[3]);
+                                out[4 * c + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
                         }
                     }
                 }
@@ -493,7 +488,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
         pdl_wait_prerequisites();
         bool ok = true;
-        int tt = 0, nq = 0;
+        int tt = 0, nq[2] = {0, 0};   // loads into the ring, into either query tile
         // item i's geometry into the ring, once the others are done with item i - kPtGeos'
         auto publish = [&](int i) -> bool {
             if (i >= n_items)
@@ -505,6 +500,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (lane == 0) {
                 *reinterpret_cast<Block *>(smem + kPtOffGeo + slot * kPtGeoBytes) = b;
                 mbar_arrive(bar(kTbGeo + slot));
+                // its queries, contiguous rows, on their way to L2
+                if (b.je > b.jb)
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                     static_cast<const __nv_bfloat16 *>(p.q_rot) +
+                                     ((((int64_t)b.lh * a.total_q + b.rq.q_off) * G + b.row0) << 7)),
+                                 "r"(b.rows * 256)
+                                 : "memory");
             }
             __syncwarp();
             return true;
@@ -521,14 +523,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // tile i of the list: the row of this lane's box (box lane / 2, panel lane & 1) and whether
             // it is to be loaded; the same for keys and values
             // (a page's number is asked for a tile ahead of its use)
+            const int first = b.first, shift = b.shift, body = b.rq.packed_len;
             int row = 0, at = 0, rows = 0, id = 0, in = 0;
             bool hand = false, load = false, rest = false;
             auto find = [&](int i) {
-                rest = b.restored(i);
-                hand = by_hand(p, b, i);
+                auto row_of = [&](int v) -> int { return v < first ? v : v + shift; };
+                rest = body > 0 && row_of(i * kPtTile) < body;
+                hand = p.box == 0 && !rest;
                 rows = rest ? kPtTile : p.box;
                 at = (lane >> 1) * rows;
-                const int j0 = b.row(i * kPtTile + at);
+                const int j0 = row_of(i * kPtTile + at);
                 load = !hand && at < kPtTile && (rest || b.some_seen(j0, j0 + rows));
                 if (load) {
                     if (rest) {
@@ -543,20 +547,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             find(b.jb);
             for (int i = 0; i <= n_loads; ++i) {
                 if (i == 2) {   // the queries after the first K and V tile
-                    if (nq > 0 && !mbar_wait_warp(bar(kTbQEmpty), (uint32_t)(nq - 1) & 1, abort_flag)) {
+                    if (nq[0] > 0 && !mbar_wait_warp(bar(kTbQEmpty), (uint32_t)(nq[0] - 1) & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
                     if (lane == 0) {
                         const int q0 = (int)(((int64_t)b.lh * a.total_q + b.rq.q_off) * G + b.row0);
-                        mbar_expect_tx(bar(kTbQ), (uint32_t)(b.nx * kPtTileBytes));
                         for (int x = 0; x < b.nx; ++x) {
                             const uint32_t dst = sbase + (uint32_t)(kPtOffQ + x * kPtTileBytes);
-                            tma_load_2d(dst, &tmq, 0, q0 + x * kPtTile, bar(kTbQ));
-                            tma_load_2d(dst + kPtPanel, &tmq, 64, q0 + x * kPtTile, bar(kTbQ));
+                            mbar_expect_tx(bar(kTbQ + x), (uint32_t)kPtTileBytes);
+                            tma_load_2d(dst, &tmq, 0, q0 + x * kPtTile, bar(kTbQ + x));
+                            tma_load_2d(dst + kPtPanel, &tmq, 64, q0 + x * kPtTile, bar(kTbQ + x));
                         }
                     }
-                    ++nq;
+                    ++nq[0];
+                    nq[1] += b.nx - 1;
                 }
                 if (i == n_loads)
                     break;
@@ -591,17 +596,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (lane == 0) {
             for (int k = tt > kPtSlots ? tt - kPtSlots : 0; k < tt; ++k)
                 mbar_drain(bar(kTbFull + k % kPtSlots), (uint32_t)(k / kPtSlots) & 1);
-            if (nq > 0)
-                mbar_drain(bar(kTbQ), (uint32_t)(nq - 1) & 1);
+            for (int x = 0; x < 2; ++x)
+                if (nq[x] > 0)
+                    mbar_drain(bar(kTbQ + x), (uint32_t)(nq[x] - 1) & 1);
         }
         __syncwarp();
     } else if (warp == 9) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPtRegsOther));
         pdl_wait_prerequisites();
         const uint32_t lead = elect_one();
-        int tt = 0, nq = 0;
-        // bit x: the parity of P (O) barrier x's next phase; O x holds an output
-        uint32_t p_par = 0, o_par = 0, o_used = 0;
+        int tt = 0;
+        // bit x: the parity of the next phase of P (O, Q) barrier x; O x holds an output
+        uint32_t p_par = 0, o_par = 0, q_par = 0, o_used = 0;
         bool ok = true;
         const uint64_t d_k = sdesc(sbase, 16, 1024), d_v = sdesc(sbase, kPtPanel, 1024);
         const uint32_t lo_k = (uint32_t)d_k, hi_k = (uint32_t)(d_k >> 32), lo_v = (uint32_t)d_v, hi_v = (uint32_t)(d_v >> 32);
@@ -677,11 +683,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 return true;
             };
-            if (!mbar_wait_warp(bar(kTbQ), (uint32_t)nq & 1, abort_flag)) {
+            if (!mbar_wait_warp(bar(kTbQ), q_par & 1u, abort_flag)) {
                 ok = false;
                 break;
             }
-            ++nq;
+            q_par ^= 1u;
             tc_fence_after();
             if constexpr (kOne) {
                 auto s_of = [&](int i) -> bool {   // S of key tile i into buffer i & 1
@@ -716,8 +722,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // (into S at once: O, which the epilogue before may still read, is the first P V's affair)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                if (x < b.nx)
+                if (x < b.nx) {
+                    if (x == 1) {   // (its queries land behind tile A's)
+                        if (!(ok = mbar_wait_warp(bar(kTbQ + 1), q_par >> 1, abort_flag)))
+                            break;
+                        q_par ^= 2u;
+                        tc_fence_after();
+                    }
                     issue_s(x, tt, x);
+                }
+            if (!ok)
+                break;
             umma_commit(lead, bar(kTbEmpty + tt % kPtSlots));
             if (K == 1)
                 umma_commit(lead, bar(kTbQEmpty));
