@@ -524,8 +524,8 @@ KVR_API int64_t kvr_packed_page_bytes(kvr_pool_t pool, int32_t page_rows);
  *   stride     host [3] (multiples of 16 bytes), or NULL: [L][T][H_kv][D].  A
  *              stitched block [L][H_kv][R][D] has (H_kv*R*D, D, R*D).
  * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
- * Errors: KVR_ERR_INVALID_ARG (also: pages that overlap each other, the new
- * keys or the new values), KVR_ERR_OUT_OF_RANGE (a page outside the table or the
+ * Errors: KVR_ERR_INVALID_ARG (also: pages that overlap each other, keys that are
+ * the values, pages that overlap the new keys or values), KVR_ERR_OUT_OF_RANGE (a page outside the table or the
  * pool, a row beyond 2^24), KVR_ERR_CUDA.
  */
 KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int32_t batch, const int32_t *table,

@@ -2034,6 +2034,8 @@ kvr_status check_pages(const kvr_pool &p, const kvr_pages *pages, bool written)
             return fail(KVR_ERR_INVALID_ARG, "pages: stride[%d] = %lld must be >= 0, a multiple of %d and within 2^58 elements", i,
                         (long long)g.stride[i], p.vec_elems());
     if (written) {
+        if (g.k == g.v)
+            return fail(KVR_ERR_INVALID_ARG, "pages: k and v are the same rows, of which the call writes both");
         int o[3] = {0, 1, 2};
         std::sort(o, o + 3, [&](int x, int y) { return g.stride[x] < g.stride[y]; });
         int64_t need = (int64_t)g.page_rows * p.d.head_dim;
@@ -2169,8 +2171,11 @@ kvr_status page_ready(kvr_pool *p, const PagePlan &pl, cudaStream_t s)
 kvr_status page_tc_plan(const kvr_pool *p, PagePlan &pl, const kvr_pages &g, int32_t window, int32_t n_first, PageTcArgs &tc, int &lh_slice)
 {
     const int D = p->d.head_dim, G = p->d.n_q_heads / p->d.n_kv_heads, LH = p->d.n_layers * p->d.n_kv_heads;
-    // boxes of the largest power of two of rows that no page boundary cuts
-    tc.box = 128;
+    // boxes of the largest power of two of rows that no page boundary cuts; with a window at most 64, as
+    // the first rows and the window's are rounded out to boxes (pages of 256 rows, 4,096-token prompt, 64
+    // units: window 1,024 with 64 first rows 506 us, 550 with boxes of 128; with none 519 and 512; window
+    // 200 with 4 first rows 326 and 382.  Boxes of 32 take the first to 529)
+    tc.box = window > 0 ? 64 : 128;
     while (g.page_rows % tc.box)
         tc.box /= 2;
     if (tc.box < 16 || g.stride[0] % D || g.stride[1] % D || g.stride[2] % D || page_extent(*p, g) / D > (int64_t)INT32_MAX - 256)

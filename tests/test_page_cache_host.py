@@ -241,3 +241,13 @@ def test_binding_checks():
     for d in (torch.zeros(4, dtype=torch.uint8), torch.zeros((2, 4)), torch.zeros((2, 4), dtype=torch.uint8)):
         with pytest.raises(ValueError):
             kvr.PackedPages(d, 32)
+
+
+def test_keys_that_are_the_values_are_read_but_not_written(lib, pool):
+    same = dict(pages=dict(v=A))
+    assert append(lib, pool, **same) == 1
+    assert "same rows" in lib.kvr_last_error().decode()
+    assert pack(lib, pool, unpack=True, **same) == 1
+    if _no_gpu():
+        assert attend(lib, pool, **same) == 4
+        assert pack(lib, pool, **same) == 4
