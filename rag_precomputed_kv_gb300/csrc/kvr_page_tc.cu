@@ -4,8 +4,9 @@
 // The G query heads of a kv head are packed into the rows (row = token * G + g), as
 // in the query prefill; a request's rows of one (layer, kv-head) meet its cache in
 // blocks of up to 256, two 128-row tiles A and B per CTA with S, P and O in TMEM.
-// The key tiles of a block are the 128-row tiles that its queries see: the first
-// rows' and the window's.
+// The key tiles of a block are 128 rows each of a list: the first rows and the window's that its
+// queries see, rounded out to TMA boxes (4 first rows and a window of 1,024 are 9 tiles for 64 tokens;
+// with tiles aligned in the cache 10).
 //
 //   warps 0-3, 4-7  softmax of tile A, B, a row a thread, and its output;
 //   warp 8          works out each item's block of rows and its tiles, and passes them to
@@ -25,7 +26,7 @@
 // slice of the (layer, kv-head) units as the scratch holds them, once for all blocks of a
 // request.  (8 x 64 tokens x 7 heads on 2,592 packed rows, 112 units: restored by warps 10
 // and 11 on the way instead, for every block again, a step of 128 keys took 8.8 us and the
-// call 2,140; with k_page_restore 820 at once, 740 now.)
+// call 2,140; with k_page_restore 820 at once, 735 now.)
 //
 // Few blocks (fewer than the SMs): each is cut in stretches of key tiles, whose
 // partial results (O relative to a maximum, the maximum, the sum) k_page_join adds.
@@ -35,12 +36,18 @@
 // probabilities would add half of all products).
 //
 // Bound by the tensor pipe and the chain S, softmax, P V of each tile: a step of 128 keys and
-// 256 rows takes 1.87 us, its products 1.35 at cuBLAS's rate.  A 4,096-token prompt x 4 heads,
-// 256 units: 923 us / 8 layers without a window, 0.62 of the measured peak; with a window
-// of 1,024 (9 key tiles a block) 5 us of every 20 are the block's start and end.  What
-// mattered: registers without spills (28 bytes spilled in the softmax: 586 -> 631 us),
-// masks as bits, item geometry and page numbers worked out ahead of their use, the next
-// item's S ahead of the epilogue, 32-byte stores.
+// 256 rows takes 1.5 us, its products 1.35 at cuBLAS's rate (pages of 16 rows 2.1: 32 boxes a
+// step).  A 4,096-token prompt x 4 heads, 256 units: 889 us / 8 layers without a window, 0.64 of
+// the measured peak; with a window of 1,024 and 64 first rows (9 key tiles a block) 1,985 us, where 5
+// of a block's 18 us are its start and end.  What mattered (that prompt): registers without
+// spills (28 bytes spilled in the softmax: 8 %), masks as bits, item geometry and page numbers
+// worked out ahead of their use, the next item's S ahead of the epilogue (2,460 then); whole lines
+// written by lanes together (a row a thread: 12 bytes a clock; 4 %); one tile for first rows and
+// window (9 %); little code in an item's start and end, by loops (7 %: rescale, masks and output are
+// executed once a block, and their code has to come from far); V waited for before the probabilities,
+// queries of either tile on a barrier of their own.  Not kept: the next item's S between the last two
+// products (its softmax then runs beside the other tile's output, 10 % slower), the next geometry
+// behind the queries' load (8 %).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -410,15 +417,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (some && !(l_run > 0.f && l_run < INFINITY))
                     atomicCAS(a.err, kDevOk, kDevBadInput);
                 const float inv = 1.f / l_run;
-                // half a row at a time; four lanes change their rows' 32-byte pieces so that they write
-                // whole lines
+                // half a row at a time, in a loop; two lanes change their rows' 32-byte pieces so that they
+                // write 64 bytes in a row
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
                     uint32_t v[32];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         float o[32];
-                        tmem_ld32(lane_base + pt_col_o(x) + 64 * hf + 32 * q, o);   // (not this item's without a tile: then `some` is not set)
+                        // (an item without a tile: something, which `some` leaves out)
+                        tmem_ld32(lane_base + pt_col_o(x) + 64 * hf + 32 * q, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; ++i)

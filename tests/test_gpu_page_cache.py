@@ -495,6 +495,42 @@ def test_attention_of_one_and_two_tiles_of_rows():
     _attention_case([(300, 236, 64, 288), (700, 620, 80, 32), (40, 20, 20, 32)], R=32, L=1, window=150, first=10)
 
 
+@pytest.mark.parametrize("R", [16, 32, 48, 64, 128, 256, 20])
+def test_first_rows_and_window_in_one_tile(R):
+    """First rows that fill a part of a 128-row tile, whose rest is the window's: by boxes of 16 to 64 rows
+    and by hand; blocks of one and of two tiles, cut in stretches too."""
+    for first, window in ((4, 100), (40, 64), (64, 300), (70, 33), (129, 257)):
+        _attention_case(_plain(900, 515, q=70), R=R, L=1, H=1, window=window, first=first)
+        _attention_case(_plain(700, q=20) + _plain(390, q=32), R=R, L=1, H=1, window=window, first=first, seed=6)
+    _attention_case(_plain(5000, q=40), R=R, L=1, H=1, window=4000, first=5)
+    if R % 32 == 0:
+        _attention_case([(900, 830, 70, 512), (900, 830, 70, 32), (900, 830, 70, 0)], R=R, L=1, H=1, window=300, first=40)
+
+
+def test_outputs_at_16_bytes():
+    """Rows of an output that starts 16 bytes behind a 32-byte boundary, for both kernels."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D, R = 1, 2, 4, 128, 32
+    pool = _pool(L, H, G, D, "bf16")
+    t, n = _table([300, 90], R, 3)
+    pages = kvr.Pages(_randn(1, (n, L, H, R, D), "bf16"), _randn(2, (n, L, H, R, D), "bf16"))
+    for lq in ((70, 40), (1, 3)):
+        T = sum(lq)
+        q = _randn(3, (L, T, H * G, D), "bf16")
+        outs = []
+        for off in (0, 8):
+            buf = torch.zeros(q.numel() + 16, device="cuda", dtype=q.dtype)
+            out = buf[off:off + q.numel()].view(q.shape)
+            assert out.data_ptr() % 32 == 2 * off
+            pool.page_attention(pages, t, [300, 90], _starts(lq).astype(np.int32), q, out)
+            torch.cuda.synchronize()
+            pool.check()
+            assert not buf[:off].any() and not buf[off + q.numel():].any()
+            outs.append(out)
+        assert torch.equal(*outs) and outs[0].any()
+
+
 def test_attention_is_deterministic_and_leaves_the_cache():
     import torch
     from rag_precomputed_kv_gb300 import kvr
