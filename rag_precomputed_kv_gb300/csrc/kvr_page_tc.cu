@@ -41,8 +41,8 @@
 // the measured peak; with a window of 1,024 and 64 first rows (9 key tiles a block) 1,985 us, where 5
 // of a block's 18 us are its start and end.  What mattered (that prompt): registers without
 // spills (28 bytes spilled in the softmax: 8 %), masks as bits, item geometry and page numbers
-// worked out ahead of their use, the next item's S ahead of the epilogue (2,460 then); whole lines
-// written by lanes together (a row a thread: 12 bytes a clock; 4 %); one tile for first rows and
+// worked out ahead of their use, the next item's S ahead of the epilogue (2,460 then); 64 bytes
+// written at once by lanes in pairs (a row a thread: 12 bytes a clock; 4 %); one tile for first rows and
 // window (9 %); little code in an item's start and end, by loops (7 %: rescale, masks and output are
 // executed once a block, and their code has to come from far); V waited for before the probabilities,
 // queries of either tile on a barrier of their own.  Not kept: the next item's S between the last two
