@@ -51,7 +51,7 @@
  *          256 query rows of a group and (layer, kv-head), and for each SM;
  *          more than 1 GiB only where one (layer, kv-head) needs it).
  *          kvr_page_attention uses both for requests of more than 16 query
- *          rows: the queries, and up to 1 GiB for packed rows restored to
+ *          rows (three times as many where they see packed rows): the queries, and up to 1 GiB for packed rows restored to
  *          bf16 (512 bytes a row and (layer, kv-head); more only where one
  *          (layer, kv-head) needs it) beside partial results (133 KB for each
  *          256 query rows, (layer, kv-head) and stretch of their keys).
@@ -559,7 +559,8 @@ KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int3
  * effect, whatever they hold.  A NaN or an infinity in a value that some query
  * token of a request sees may reach all query tokens of that request in the call
  * (a weight of 0 times it is NaN).  On the tensor cores (bf16, head_dim 128) a
- * request of up to 16 query rows (tokens times G) is computed from 11 bits of
+ * request of up to 16 query rows (tokens times G; one that sees packed rows, of
+ * up to three times as many whole tokens, in parts) is computed from 11 bits of
  * its rotated queries and 16 of its probabilities, 8 where these meet packed
  * values; one of more rows from 8 bits of both, as in kvr_query_attention, and of
  * what packed rows stand for.

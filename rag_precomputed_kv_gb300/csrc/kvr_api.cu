@@ -396,7 +396,7 @@ extern "C" kvr_status kvr_pool_reserve(kvr_pool_t p, int32_t max_batch, int32_t 
     const size_t asm_bytes = align16((size_t)max_spans * sizeof(DevSpan)) + (size_t)max_locals * sizeof(DevLocal);
     const size_t append_bytes = align16((size_t)max_batch * sizeof(DevSpan)) + (size_t)max_batch * sizeof(DevLocal);
     const size_t req_bytes = align16((size_t)max_batch * req) + std::max(append_bytes, (size_t)max_batch * sizeof(DevGroup));
-    const size_t page_bytes = align16((size_t)max_batch * sizeof(DevPageReq)) + (size_t)max_spans * sizeof(int32_t);
+    const size_t page_bytes = align16((size_t)max_batch * kPagePackedParts * sizeof(DevPageReq)) + (size_t)max_spans * sizeof(int32_t);
     const size_t bytes = std::max({asm_bytes, req_bytes, page_bytes});
     cudaError_t e;
     for (Slot &s : p->slots) {
@@ -2425,7 +2425,7 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
             return fail(KVR_ERR_INVALID_ARG, "kv_len / packed_len is NULL");
         if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale))
             return fail(KVR_ERR_INVALID_ARG, "softmax_scale %g", (double)softmax_scale);
-        const int L = p->d.n_layers, Hq = p->d.n_q_heads, D = p->d.head_dim;
+        const int L = p->d.n_layers, Hq = p->d.n_q_heads, D = p->d.head_dim, G = Hq / p->d.n_kv_heads;
         const int32_t T = q_offsets[batch], R = pages->page_rows;
         PagePlan pl;
         pl.rq.reserve(batch);
@@ -2434,6 +2434,7 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
             r.q_off = q_offsets[b];
             r.q_len = q_offsets[b + 1] - q_offsets[b];
             r.kv_len = kv_len[b];
+            int32_t step = std::max(1, r.q_len);   // tokens that are a request to the kernels
             if (r.kv_len < 0)
                 return fail(KVR_ERR_OUT_OF_RANGE, "request %d: kv_len %d", b, r.kv_len);
             r.pos0 = q_pos ? q_pos[b] : r.kv_len - r.q_len;
@@ -2468,8 +2469,20 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
                 if ((st = take(body, few, std::max(lo, body), hi, false, r.few, r.off)) != KVR_OK ||
                     (packed && (st = take(0, std::min(few, body), lo, std::min(hi, body), true, r.pfew, r.poff)) != KVR_OK))
                     return st;
+                // a few more query rows than k_page_decode takes, on packed rows: it reads these up to three
+                // times, rather than k_page_attention bf16 rows restored from them (33,280 packed rows, 256
+                // units: 32 query rows in two parts 755 us, 1,657 there; 48 in three 1,132, 1,661 there; 16 x
+                // 1,216, 288 units, 32 rows 650 and 1,109; four parts would be 1,300 there, for 1,120)
+                const int n = G <= kPageFewRows ? (r.q_len + kPageFewRows / G - 1) / (kPageFewRows / G) : INT32_MAX;
+                if (n <= kPagePackedParts && (std::min(few, body) > 0 || lo < std::min(hi, body)))
+                    step = (r.q_len + n - 1) / n;
             }
-            pl.rq.push_back(r);
+            for (int32_t t = 0, n = r.q_len, pos = r.pos0; t == 0 || t < n; t += step) {
+                r.q_off = q_offsets[b] + t;
+                r.q_len = std::min(step, n - t);
+                r.pos0 = pos + t;
+                pl.rq.push_back(r);
+            }
         }
         if (pl.ids.size() > INT32_MAX)
             return fail(KVR_ERR_OUT_OF_RANGE, "too many pages");
@@ -2486,14 +2499,14 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
             return fail(KVR_ERR_INVALID_ARG, "the output overlaps the queries (it may only be the same buffer)");
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         const bool tensor = attention_tc_supported(p->d.dtype, D);
-        const int G = Hq / p->d.n_kv_heads;
         bool few = false, many = false;   // requests for the kernel of few query rows, and for that of more
         for (const DevPageReq &r : pl.rq) {
             few = few || (r.q_len > 0 && r.q_len * (int64_t)G <= kPageFewRows);
             many = many || (tensor && r.q_len * (int64_t)G > kPageFewRows);
         }
-        if ((st = check_capture(*p, s, pl.inl() && !many, "the call uses library scratch (a request of more than 16 query rows), or "
-                                                          "uploads the tables of more than 64 requests or 1,024 pages")) != KVR_OK ||
+        if ((st = check_capture(*p, s, pl.inl() && !many, "the call uses library scratch (a request of more than 16 query rows, three times "
+                                                          "as many on packed rows), or uploads the tables of more than 64 "
+                                                          "requests (or parts of them) or 1,024 pages")) != KVR_OK ||
             (st = ensure_device(p)) != KVR_OK)
             return st;
         DeviceGuard g(p->device);

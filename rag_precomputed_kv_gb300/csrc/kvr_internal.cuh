@@ -614,6 +614,8 @@ cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, i
 // Query rows (tokens times query heads of a kv head) of a request up to which k_page_decode
 // takes it; `host_reqs` is the host's copy of the request table.
 constexpr int kPageFewRows = 16;
+// Parts of at most as many rows that a request which sees packed rows is taken in.
+constexpr int kPagePackedParts = 3;
 cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevPageReq *host_reqs, int n_sms, cudaStream_t s);
 cudaError_t launch_page_queries(const PageArgs &a, const PageTable &t, void *q_rot, cudaStream_t s);
 // One slice of lh_count units: restore (unit_tiles > 0), attention, join (splits > 1).

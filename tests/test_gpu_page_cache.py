@@ -15,7 +15,7 @@ value:
   4 roundings each way in fp32):
       fp32, and bf16 with head_dim 64              e = 0        r = 0
       bf16, up to 16 rows a request                e = 2^-11    r = 2^-8 (16 bits)
-        that see packed rows                       e = 2^-11    r = 1
+        that see packed rows (up to three parts)   e = 2^-11    r = 1
       more rows                                    e = u        r = 1
         that see packed rows (rounded to bf16)     e = 2 u      r = 2
   In the 2-norm the roundings are independent and add in squares: of the output,
@@ -294,7 +294,7 @@ def _attention_ref(K, V, q, rows, pos, hi, window, first, scale):
 
 
 def _attention_case(reqs, L=2, H=2, G=4, D=128, dtype="bf16", R=16, window=0, first=0, il=False, scale=0.0, spread=1.0, seed=1,
-                    stream=None, pool=None, default_pos=False, in_place=False, theta=THETA, poison=True, twice=False, pad=0):
+                    stream=None, pool=None, default_pos=False, in_place=False, theta=THETA, poison=True, twice=False, pad=0, parts=1):
     """reqs: (kv_len, first query's position, query tokens, packed rows) of each request."""
     import torch
     from rag_precomputed_kv_gb300 import kvr
@@ -370,7 +370,7 @@ def _attention_case(reqs, L=2, H=2, G=4, D=128, dtype="bf16", R=16, window=0, fi
         thin = bool((seen[b] < body[b]).any())
         if dtype == "fp32" or D == 64:
             e_q, r, k = 0.0, 0.0, 1.1
-        elif lq[b] * G <= 16:
+        elif lq[b] * G <= 16 or parts > 1 and thin and -(-lq[b] // (16 // G)) <= parts:
             e_q, r, k = 2.0 ** -11, (1.0 if thin else u), (2.2 if thin else 1.1)
         else:
             e_q, r, k = u * (1 + thin), 1.0 + thin, (5.0 if thin else 3.0)
@@ -434,6 +434,43 @@ def test_attention_packed(q):
     _attention_case([(200, 200 - q, q, 192), (300, 300 - q, q, 32), (96, 96 - q, q, 96), (130, 130 - q, q, 0), (700, 700 - q, q, 640)], R=64)
     _attention_case([(500, 500 - q, q, 480), (288, 288 - q, q, 288)], R=96, il=True, seed=2)
     _attention_case([(500, 500 - q, q, 480), (288, 288 - q, q, 288)], R=32, G=7, seed=2)
+
+
+@pytest.mark.parametrize("G,q", [(4, 5), (4, 8), (4, 9), (4, 12), (5, 7), (5, 9), (7, 6), (16, 3), (1, 48), (2, 20), (4, 13), (16, 4)])
+def test_packed_rows_for_a_few_parts(G, q):
+    """Requests of up to three times 16 query rows that see packed rows keep the accuracy of one of 16, beside
+    others that see none, of one token and of more."""
+    _attention_case([(200, 200 - q, q, 192), (700, 700 - q, q, 640), (300, 299, 1, 256), (96, 96 - q, q, 96), (90, 90 - q, q, 0),
+                     (400, 340, 60, 320)], R=64, L=1, G=G, parts=3)
+    _attention_case([(500, 500 - q, q, 480), (300, 300 - q, q, 32), (300, 310, q, 288)], R=32, L=1, G=G, parts=3, window=150, first=5, il=True)
+
+
+def test_packed_parts_are_captured_and_in_place():
+    """A call that takes packed rows in parts uses no scratch: it can be captured, and write over its queries."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, G, D, R, q = 1, 2, 4, 128, 32, 10
+    pool = _pool(L, H, G, D, "bf16")
+    t, n = _table([300], R, 3)
+    pages = kvr.Pages(_randn(1, (n, L, H, R, D), "bf16"), _randn(2, (n, L, H, R, D), "bf16"))
+    packed = pool.packed_pages(n, R)
+    pool.page_pack(pages, t, packed, t, [0], [256])
+    first = _randn(3, (L, q, H * G, D), "bf16")
+    kw = dict(packed=packed, packed_table=t, packed_len=[256])
+    want = torch.empty_like(first)
+    pool.page_attention(pages, t, [300], [0, q], first, want, **kw)
+    x = first.clone()
+    torch.cuda.synchronize()
+    gc.collect()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pool.page_attention(pages, t, [300], [0, q], x, x, **kw)
+    for _ in range(2):
+        x.copy_(first)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x, want)
+    pool.check()
 
 
 @pytest.mark.parametrize("q", [1, 6, 50])
