@@ -11,10 +11,11 @@
 //   warps 0-3, 4-7  softmax of tile A, B, a row a thread, and its output;
 //   warp 8          works out each item's block of rows and its tiles, and passes them to
 //                   the others through a ring of three, then loads by TMA: a tile's
-//                   pages are boxes of 16 to 128 rows, one and a panel a lane;
+//                   pages are boxes of 16 to 128 rows, one and a panel a lane (small ones
+//                   together with warp 10);
 //   warp 9          tcgen05 products; rows of V that no query of the request sees become
 //                   zeros first (their weight is 0, but 0 x NaN is NaN);
-//   warps 10, 11    tiles of pages that TMA boxes cannot bring (their rows are no multiple
+//   warps 10, 11    else tiles of pages that TMA boxes cannot bring (their rows are no multiple
 //                   of 16 or lie at odd strides), 64 rows each.
 // A slot's barrier counts two arrivals whichever way it is filled: two of warp 8, or
 // one each of warps 10 and 11.  That a slot is free for them, warps 10 and 11 learn from
@@ -36,8 +37,7 @@
 // probabilities would add half of all products).
 //
 // Bound by the tensor pipe and the chain S, softmax, P V of each tile: a step of 128 keys and
-// 256 rows takes 1.5 us, its products 1.35 at cuBLAS's rate (pages of 16 rows 2.1: 32 boxes a
-// step).  A 4,096-token prompt x 4 heads, 256 units: 889 us / 8 layers without a window, 0.64 of
+// 256 rows takes 1.5 us, its products 1.35 at cuBLAS's rate.  A 4,096-token prompt x 4 heads, 256 units: 889 us / 8 layers without a window, 0.64 of
 // the measured peak; with a window of 1,024 and 64 first rows (9 key tiles a block) 1,985 us, where 5
 // of a block's 18 us are its start and end.  What mattered (that prompt): registers without
 // spills (28 bytes spilled in the softmax: 8 %), masks as bits, item geometry and page numbers
@@ -191,7 +191,12 @@ __device__ __forceinline__ bool by_hand(const PageTcArgs &p, const Block &s, int
 // kOne: every block of the call has one 128-row tile.  The S of its next key tile then
 // goes into tile B's buffer, ahead of the softmax (32 tokens x 4 heads on 33,000 rows, 64
 // units: 253 -> 231 us; as a branch of the kernel for two tiles it cost those 10 %).
-template <bool kOne>
+// kTwo: warp 10 loads by TMA beside warp 8, a 64-column panel each.  A load of 16- or 32-row boxes
+// takes one warp longer than a step (4,096-token prompt, window 1,024, 4 first rows, 64 units: pages of
+// 16 rows 638 -> 545 us, of 32 537 -> 527; without a window of 96 997 -> 898; 8 windows of 4,100 rows of
+// pages of 16, 8 tokens 969 -> 781).  Of 64 rows only blocks of one tile gain (185 -> 183; the prompt 505 ->
+// 518).
+template <bool kOne, bool kTwo>
 __global__ void __launch_bounds__(kPtThreads, 1)
     k_page_attention(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmrk,
@@ -203,7 +208,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return sbase + kPtOffBar + 8u * (uint32_t)i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPtOffMisc + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool second = kTwo && threadIdx.x >> 5 == 10;   // a second warp 8
+    const int warp = second ? 8 : (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const DevPageReq *reqs = a.reqs ? a.reqs : pt.reqs;
     const int32_t *ids = a.reqs ? a.ids : pt.ids;
     const int G = a.n_q_heads / a.n_kv_heads;
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
     if (warp == 9)
         tmem_alloc(sbase + kPtOffMisc, kPtTmemCols);
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && !second && lane == 0) {
         prefetch_tmap(&tmq);
         prefetch_tmap(&tmk);
         prefetch_tmap(&tmv);
@@ -519,17 +525,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             __syncwarp();
             return true;
         };
-        ok = publish(0);
+        const int at_lane = kTwo ? lane : lane >> 1, panel = kTwo ? (int)second : lane & 1;
+        ok = second || publish(0);
         for (int item = 0; item < n_items && ok; ++item) {
-            const Block &b = geo(item);
-            if (!(ok = publish(item + 1)))
+            if (!(ok = second ? geo_wait(item) : publish(item + 1)))
                 break;
+            const Block &b = geo(item);
             const int n_loads = 2 * (b.je - b.jb);
-            if (n_loads == 0)
+            if (n_loads == 0) {
+                if (second)
+                    geo_done(item);
                 continue;
+            }
             const int64_t unit = b.unit / 128;
-            // tile i of the list: the row of this lane's box (box lane / 2, panel lane & 1) and whether
-            // it is to be loaded; the same for keys and values
+            // tile i of the list: the row of this lane's box and whether it is to be loaded; the same for
+            // keys and values
             // (a page's number is asked for a tile ahead of its use)
             const int first = b.first, shift = b.shift, body = b.rq.packed_len;
             int row = 0, at = 0, rows = 0, id = 0, in = 0;
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 rest = body > 0 && row_of(i * kPtTile) < body;
                 hand = p.box == 0 && !rest;
                 rows = rest ? kPtTile : p.box;
-                at = (lane >> 1) * rows;
+                at = at_lane * rows;
                 const int j0 = row_of(i * kPtTile + at);
                 load = !hand && at < kPtTile && (rest || b.some_seen(j0, j0 + rows));
                 if (load) {
@@ -554,7 +564,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             };
             find(b.jb);
             for (int i = 0; i <= n_loads; ++i) {
-                if (i == 2) {   // the queries after the first K and V tile
+                if (i == 2 && !second) {   // the queries after the first K and V tile
                     if (nq[0] > 0 && !mbar_wait_warp(bar(kTbQEmpty), (uint32_t)(nq[0] - 1) & 1, abort_flag)) {
                         ok = false;
                         break;
@@ -583,7 +593,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 if (lane == 0) {
                     if (!hand) {
-                        mbar_arrive(bar(kTbFull + slot));
+                        if (!kTwo)
+                            mbar_arrive(bar(kTbFull + slot));
                         mbar_expect_tx(bar(kTbFull + slot), boxes * (uint32_t)rows * 128u);
                     } else {
                         mbar_arrive(bar(kTbJob + slot));
@@ -591,12 +602,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 __syncwarp();   // (the bytes are expected before they land)
                 if (load)
-                    tma_load_2d(sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes + (lane & 1) * kPtPanel + at * 128),
-                                (i & 1) ? (rest ? &tmrv : &tmv) : (rest ? &tmrk : &tmk), 64 * (lane & 1), row, bar(kTbFull + slot));
+                    tma_load_2d(sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes + panel * kPtPanel + at * 128),
+                                (i & 1) ? (rest ? &tmrv : &tmv) : (rest ? &tmrk : &tmk), 64 * panel, row, bar(kTbFull + slot));
                 if ((i & 1) && i + 1 < n_loads)
                     find(b.jb + (i >> 1) + 1);
                 ++tt;
             }
+            if (ok && second)
+                geo_done(item);
         }
         if (!ok)
             give_up(a.err, abort_flag);
@@ -1015,12 +1028,14 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
                            cudaStream_t s)
 {
     static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
+    decltype(&k_page_attention<false, false>) const kernels[4] = {k_page_attention<false, false>, k_page_attention<false, true>,
+                                                                  k_page_attention<true, false>, k_page_attention<true, true>};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        for (auto *k : {k_page_attention<false>, k_page_attention<true>}) {
+        for (auto *k : kernels) {
             cudaFuncAttributes fa{};
             if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess)
                 return e;
@@ -1036,9 +1051,10 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
     auto map = [](const void *x) -> const CUtensorMap & { return *static_cast<const CUtensorMap *>(x); };
     if (p.unit_tiles > 0)
         e = launch_pdl(k_page_restore, 2 * (int64_t)lh_count * p.unit_tiles, 128, 0, true, s, a, p, t);
+    const bool two = p.box > 0 && (p.one_tile || p.box <= 32);
     if (e == cudaSuccess)
-        e = launch_pdl(p.one_tile ? k_page_attention<true> : k_page_attention<false>, std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q), map(m.k), map(m.v),
-                       map(m.rest_k), map(m.rest_v), a, p, t);
+        e = launch_pdl(kernels[2 * (p.one_tile != 0) + two], std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q),
+                       map(m.k), map(m.v), map(m.rest_k), map(m.rest_v), a, p, t);
     if (e == cudaSuccess && p.splits > 1)
         e = launch_pdl(k_page_join, 16 * (p.total / p.splits), 128, 0, true, s, a, p, t);
     return e;
