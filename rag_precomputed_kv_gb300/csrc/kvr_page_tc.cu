@@ -183,20 +183,39 @@ __device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8])
                  : "memory");
 }
 
+// 16 bytes to shared memory, on the way until the thread waits for its copies; or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kLoadOne = 0, kLoadTwo = 1, kLoadByHand = 2;
 // A tile that warps 10 and 11 fill.
-__device__ __forceinline__ bool by_hand(const PageTcArgs &p, const Block &s, int j) { return p.box == 0 && !s.restored(j); }
+template <int kLoad>
+__device__ __forceinline__ bool by_hand(const Block &s, int j)
+{
+    return kLoad == kLoadByHand && !s.restored(j);
+}
 
 }  // namespace
 
 // kOne: every block of the call has one 128-row tile.  The S of its next key tile then
 // goes into tile B's buffer, ahead of the softmax (32 tokens x 4 heads on 33,000 rows, 64
 // units: 253 -> 231 us; as a branch of the kernel for two tiles it cost those 10 %).
-// kTwo: warp 10 loads by TMA beside warp 8, a 64-column panel each.  A load of 16- or 32-row boxes
-// takes one warp longer than a step (4,096-token prompt, window 1,024, 4 first rows, 64 units: pages of
-// 16 rows 638 -> 545 us, of 32 537 -> 527; without a window of 96 997 -> 898; 8 windows of 4,100 rows of
-// pages of 16, 8 tokens 969 -> 781).  Of 64 rows only blocks of one tile gain (185 -> 183; the prompt 505 ->
-// 518).
-template <bool kOne, bool kTwo>
+// kLoad, who brings the pages: warp 8 by TMA; kLoadTwo: warp 10 beside it, a 64-column panel each;
+// kLoadByHand: warps 10 and 11 (branches of one kernel for these cost the first 2 %).  A load of 16-
+// or 32-row boxes takes one warp longer than a step: 4,096-token prompt, window 1,024, 4 first rows, 64
+// units, pages of 16 rows 638 -> 532 us, of 32 540 -> 519; 8 windows of 4,100 rows in pages of 16, 8
+// tokens 971 -> 780.  Boxes of 64: the prompt 507, by two warps 518; blocks of one tile gain (185 -> 182).
+// By hand three tiles are in flight (pages of 20 rows, 4 x 8 tokens on 2,656 rows, 32 units: 94 us; 946
+// with loads that the warps wait for).
+template <bool kOne, int kLoad>
 __global__ void __launch_bounds__(kPtThreads, 1)
     k_page_attention(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmrk,
@@ -208,6 +227,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) { return sbase + kPtOffBar + 8u * (uint32_t)i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kPtOffMisc + 4);
+    constexpr bool kTwo = kLoad == kLoadTwo;
     const bool second = kTwo && threadIdx.x >> 5 == 10;   // a second warp 8
     const int warp = second ? 8 : (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const DevPageReq *reqs = a.reqs ? a.reqs : pt.reqs;
@@ -547,7 +567,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             auto find = [&](int i) {
                 auto row_of = [&](int v) -> int { return v < first ? v : v + shift; };
                 rest = body > 0 && row_of(i * kPtTile) < body;
-                hand = p.box == 0 && !rest;
+                hand = kLoad == kLoadByHand && !rest;
                 rows = rest ? kPtTile : p.box;
                 at = at_lane * rows;
                 const int j0 = row_of(i * kPtTile + at);
@@ -676,7 +696,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     return false;
                 const bool all = b.cut(j) ? b.all_seen(v0, b.first) && b.all_seen(b.first + b.shift, v1 + b.shift)
                                           : b.all_seen(b.row(v0), b.row(v0) + kPtTile);
-                return !all && !by_hand(p, b, j) && !b.restored(j);
+                return !all && !by_hand<kLoad>(b, j) && !b.restored(j);
             };
             // V tile i: landed, such rows zeroed
             auto wait_v = [&](int i, bool zero) -> bool {
@@ -806,6 +826,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         bool ok = true;
         int tt = 0;
         uint32_t jobs = 0;   // bit s: the parity of slot s's next job
+        // Up to three tiles' copies are in flight: their slots, the oldest in the lowest byte.  One is passed
+        // on when a fourth is asked for, or as soon as there is nothing to do: the products may wait for it.
+        uint32_t flight = 0;
+        int n_flight = 0;
+        auto landed = [&](int keep) {
+            if (keep == 0)
+                copies_wait<0>();
+            else
+                copies_wait<2>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            for (; n_flight > keep; --n_flight, flight >>= 8)
+                if (lane == 0)
+                    mbar_arrive(bar(kTbFull + (int)(flight & 255u)));
+        };
+        int64_t at[2] = {-1, -1};   // of this lane's rows of the tile: elements from the unit's start; < 0: zeros
         for (int item = 0; item < n_items && ok; ++item) {
             if (!geo_wait(item)) {
                 ok = false;
@@ -815,34 +851,48 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int n_loads = 2 * (b.je - b.jb);
             for (int i = 0; i < n_loads; ++i, ++tt) {
                 const int slot = tt % kPtSlots, t = b.jb + (i >> 1);
-                if (!by_hand(p, b, t))
+                if (!by_hand<kLoad>(b, t))
                     continue;
+                if (n_flight > 0 && !mbar_test_warp(bar(kTbJob + slot), (jobs >> slot) & 1u))
+                    landed(0);
                 if (!mbar_wait_warp(bar(kTbJob + slot), (jobs >> slot) & 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
                 jobs ^= 1u << slot;
-                const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
-                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>((i & 1) ? a.g.v : a.g.k) + b.unit;
-                const int ch = lane & 15;
-#pragma unroll 8
-                for (int y = 0; y < 32; ++y) {
-                    const int row = 64 * (warp - 10) + 2 * y + (lane >> 4), j = b.row(t * kPtTile + row);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (b.any(j)) {
-                        const int pg = page_of(a, j);
-                        v = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)page_id(b.rq, ids, pg) * a.g.s_page +
-                                                                  (int64_t)(j - pg * a.g.rows) * 128) + ch);
+                if (!(i & 1)) {   // (a row's place once, for its key and its value)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = b.row(t * kPtTile + 64 * (warp - 10) + 32 * k + lane);
+                        at[k] = -1;
+                        if (b.any(j)) {
+                            const int pg = page_of(a, j);
+                            at[k] = (int64_t)page_id(b.rq, ids, pg) * a.g.s_page + (int64_t)(j - pg * a.g.rows) * 128;
+                        }
                     }
-                    st_shared_v4(tile + (uint32_t)((ch >> 3) * kPtPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4)), v.x, v.y, v.z, v.w);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(kTbFull + slot));
+                const uint32_t tile = sbase + (uint32_t)(kPtOffKV + slot * kPtTileBytes);
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>((i & 1) ? a.g.v : a.g.k);
+                const int ch = lane & 15;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll 4
+                    for (int y = 0; y < 16; ++y) {
+                        const int row = 64 * (warp - 10) + 32 * k + 2 * y + (lane >> 4);
+                        const int64_t o = __shfl_sync(0xffffffffu, at[k], 2 * y + (lane >> 4));
+                        copy16(tile + (uint32_t)((ch >> 3) * kPtPanel + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                               src + (o >= 0 ? b.unit + o + 8 * ch : 0), o >= 0);
+                    }
+                copies_end();
+                flight |= (uint32_t)slot << 8 * n_flight;
+                if (++n_flight == 3)
+                    landed(2);
             }
+            if (ok)
+                landed(0);
             geo_done(item);
         }
+        copies_wait<0>();
         if (!ok)
             give_up(a.err, abort_flag);
     }
@@ -1028,8 +1078,9 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
                            cudaStream_t s)
 {
     static std::atomic<bool> attr_set[64] = {};   // per device (host threads may race: same value)
-    decltype(&k_page_attention<false, false>) const kernels[4] = {k_page_attention<false, false>, k_page_attention<false, true>,
-                                                                  k_page_attention<true, false>, k_page_attention<true, true>};
+    decltype(&k_page_attention<false, 0>) const kernels[5] = {
+        k_page_attention<false, kLoadOne>, k_page_attention<false, kLoadTwo>, k_page_attention<false, kLoadByHand>,
+        k_page_attention<true, kLoadTwo>, k_page_attention<true, kLoadByHand>};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -1051,9 +1102,9 @@ cudaError_t launch_page_tc(const PageArgs &a, const PageTcArgs &p, const PageTab
     auto map = [](const void *x) -> const CUtensorMap & { return *static_cast<const CUtensorMap *>(x); };
     if (p.unit_tiles > 0)
         e = launch_pdl(k_page_restore, 2 * (int64_t)lh_count * p.unit_tiles, 128, 0, true, s, a, p, t);
-    const bool two = p.box > 0 && (p.one_tile || p.box <= 32);
+    const int load = p.box == 0 ? kLoadByHand : p.one_tile || p.box <= 32 ? kLoadTwo : kLoadOne;
     if (e == cudaSuccess)
-        e = launch_pdl(kernels[2 * (p.one_tile != 0) + two], std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q),
+        e = launch_pdl(kernels[load + (p.one_tile ? 2 : 0)], std::min<int64_t>(n_sms, p.total), kPtThreads, kPtSmem, true, s, map(m.q),
                        map(m.k), map(m.v), map(m.rest_k), map(m.rest_v), a, p, t);
     if (e == cudaSuccess && p.splits > 1)
         e = launch_pdl(k_page_join, 16 * (p.total / p.splits), 128, 0, true, s, a, p, t);
