@@ -314,21 +314,24 @@ cudaError_t launch_page_pack(const PageArgs &a, const PageTable &t, int64_t n_bl
 // attention on the CUDA cores
 // ---------------------------------------------------------------------------
 namespace {
-constexpr int kSmHeads = 4;      // query heads of a CTA
 constexpr int kSmThreads = 256;
 constexpr int kSmTeams = kSmThreads / 8;
 }  // namespace
 
-// One CTA: one token, up to kSmHeads of the query heads of one kv head.  Teams of
-// 8 threads, D / 8 dims each, go through the visible keys by turns, every team
-// with its own running maximum, sum and output; they are joined at the end.  (fp32, head_dim
-// 64, 16 tokens on 193 rows: 8.5 us a call, 12.3 with half the teams and rows asked for
-// when they are needed.)
-template <typename T, int D>
+// One CTA: one token, up to kSmHeads (2 or 4) of the query heads of one kv head.  Teams of 8
+// threads, D / 8 dims each, go through the visible keys by turns, every team with its own
+// running maximum, sum and output; they are joined at the end.  Few CTAs are bound by a team's
+// chain of loads, sums over its threads and exponentials, so a team takes four rows (of 128 fp32
+// dims two) at once; many by instructions: without empty heads.  fp32, head_dim 64, 2 heads a kv
+// head, 8 units: 4 x 1 token on 2,000 rows 22 us, 49 with a row at a time; 4 x 24 tokens 80 us,
+// 150 with places for 4 heads, 171 with a row at a time too (bf16 81, 191 and 173); 16 tokens on
+// 193 rows, 2 units, the host's call.
+template <typename T, int D, int kSmHeads>
 __global__ void __launch_bounds__(kSmThreads)
     k_page_simt(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t)
 {
     constexpr int N = D / 8, V = Vec<T>::N;   // dims of a thread: vectors 8 i + j of a row, i < N / V
+    constexpr int kKeys = N / V > 2 ? 2 : 4;
     __shared__ float qs[kSmHeads][D];
     __shared__ float st_m[kSmTeams][kSmHeads], st_l[kSmTeams][kSmHeads];
     __shared__ float st_o[kSmTeams][D];
@@ -371,47 +374,77 @@ __global__ void __launch_bounds__(kSmThreads)
         }
     }
     const uint32_t team_mask = 0xffu << (8 * ((threadIdx.x >> 3) & 3));
-    // a team's next row is asked for before this one is used
-    uint4 kv[N / V], vv[N / V];
-    auto ask = [&](int i) {
-        if (i >= n_keys)
-            return;
-        const int row = i < few ? i : lo + i - few, pg = page_of(a, row);
-        const int64_t at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + l * a.g.s_layer + h * a.g.s_head +
-                           (int64_t)(row - pg * a.g.rows) * D;
-        const uint4 *kp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.k) + at);
-        const uint4 *vp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.v) + at);
+    // kKeys rows at a time: their loads and their scores' sums do not wait for each other
+    for (int i = team; i < n_keys; i += kKeys * kSmTeams) {
+        uint4 kv[kKeys][N / V], vv[kKeys][N / V];
 #pragma unroll
-        for (int e = 0; e < N / V; ++e) {
-            kv[e] = __ldg(kp + 8 * e + j);
-            vv[e] = __ldg(vp + 8 * e + j);
-        }
-    };
-    ask(team);
-    for (int i = team; i < n_keys; i += kSmTeams) {
-        float kf[N], vf[N];
+        for (int u = 0; u < kKeys; ++u) {
+            const int r = min(i + u * kSmTeams, n_keys - 1), row = r < few ? r : lo + r - few, pg = page_of(a, row);
+            const int64_t at = (int64_t)page_id(rq, ids, pg) * a.g.s_page + l * a.g.s_layer + h * a.g.s_head +
+                               (int64_t)(row - pg * a.g.rows) * D;
+            const uint4 *kp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.k) + at);
+            const uint4 *vp = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.g.v) + at);
 #pragma unroll
-        for (int e = 0; e < N / V; ++e) {
-            Vec<T>::get(kv[e], kf + V * e);
-            Vec<T>::get(vv[e], vf + V * e);
+            for (int e = 0; e < N / V; ++e) {
+                kv[u][e] = __ldg(kp + 8 * e + j);
+                vv[u][e] = __ldg(vp + 8 * e + j);
+            }
         }
-        ask(i + kSmTeams);
+        float s[kSmHeads][kKeys];
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            float f[N];
+#pragma unroll
+            for (int e = 0; e < N / V; ++e)
+                Vec<T>::get(kv[u][e], f + V * e);
+#pragma unroll
+            for (int g = 0; g < kSmHeads; ++g) {
+                float x = 0.f;
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    x = fmaf(qr[g][e], f[e], x);
+                s[g][u] = x;
+            }
+        }
+#pragma unroll
+        for (int d = 1; d <= 4; d <<= 1)
+#pragma unroll
+            for (int u = 0; u < kKeys; ++u)
+#pragma unroll
+                for (int g = 0; g < kSmHeads; ++g)
+                    s[g][u] += __shfl_xor_sync(team_mask, s[g][u], d);
 #pragma unroll
         for (int g = 0; g < kSmHeads; ++g) {
-            float s = 0.f;
+            float mn = m[g];
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                s = fmaf(qr[g][e], kf[e], s);
-            s += __shfl_xor_sync(team_mask, s, 1);
-            s += __shfl_xor_sync(team_mask, s, 2);
-            s += __shfl_xor_sync(team_mask, s, 4);
-            const float mn = fmaxf(m[g], s);
-            const float corr = mn == -INFINITY ? 1.f : exp2f(m[g] - mn), p = mn == -INFINITY ? 0.f : exp2f(s - mn);
+            for (int u = 0; u < kKeys; ++u) {
+                if (i + u * kSmTeams >= n_keys)   // (the last row again)
+                    s[g][u] = -INFINITY;
+                mn = fmaxf(mn, s[g][u]);
+            }
+            const float corr = mn == -INFINITY ? 1.f : exp2f(m[g] - mn);
             m[g] = mn;
-            ls[g] = ls[g] * corr + p;
+            ls[g] *= corr;
 #pragma unroll
             for (int e = 0; e < N; ++e)
-                o[g][e] = fmaf(p, vf[e], o[g][e] * corr);
+                o[g][e] *= corr;
+#pragma unroll
+            for (int u = 0; u < kKeys; ++u) {
+                s[g][u] = mn == -INFINITY ? 0.f : exp2f(s[g][u] - mn);
+                ls[g] += s[g][u];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            float f[N];
+#pragma unroll
+            for (int e = 0; e < N / V; ++e)
+                Vec<T>::get(vv[u][e], f + V * e);
+#pragma unroll
+            for (int g = 0; g < kSmHeads; ++g)
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    o[g][e] = fmaf(s[g][u], f[e], o[g][e]);
         }
     }
     if (j == 0) {
@@ -454,9 +487,9 @@ __global__ void __launch_bounds__(kSmThreads)
 template <typename T, int D>
 static cudaError_t simt(const PageArgs &a, const PageTable &t, cudaStream_t s)
 {
-    const int G = a.n_q_heads / a.n_kv_heads;
-    const int64_t grid = (int64_t)a.n_layers * a.total_q * a.n_kv_heads * ((G + kSmHeads - 1) / kSmHeads);
-    return launch_pdl(k_page_simt<T, D>, grid, kSmThreads, 0, true, s, a, t);
+    const int G = a.n_q_heads / a.n_kv_heads, heads = G <= 2 ? 2 : 4;
+    const int64_t grid = (int64_t)a.n_layers * a.total_q * a.n_kv_heads * ((G + heads - 1) / heads);
+    return launch_pdl(heads == 2 ? k_page_simt<T, D, 2> : k_page_simt<T, D, 4>, grid, kSmThreads, 0, true, s, a, t);
 }
 
 cudaError_t launch_page_simt(const PageArgs &a, const PageTable &t, int dtype, int head_dim, cudaStream_t s)
