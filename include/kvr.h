@@ -564,6 +564,8 @@ KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int3
  * its rotated queries and 16 of its probabilities, 8 where these meet packed
  * values; one of more rows from 8 bits of both, as in kvr_query_attention, and of
  * what packed rows stand for.
+ * On packed rows a query element of 2^115 or more may be reported as an infinity
+ * is; so may, everywhere, scores of 2^30 or more, whose steps in fp32 are above 2^6.
  * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
  * Errors: KVR_ERR_INVALID_ARG (also: `out` overlaps the pages, or q without being
  * the same buffer), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;

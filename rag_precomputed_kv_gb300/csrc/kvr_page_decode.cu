@@ -32,7 +32,7 @@
 // memory's pace leaves room for that, and the output is off by its own rounding alone
 // (0.0017 of its norm; 0.0029 with one term each).  Queries that meet packed rows are fp16
 // times a power of two of their row, the largest element between 2^12 and 2^13 (11 bits of
-// an element, fewer only below 2^-22 of the largest); probabilities there are rounded to
+// an element, fewer below 2^-22 of the largest or 2^-114); probabilities there are rounded to
 // bf16 (0.0024), as the step is bound by instructions.
 //
 // Measured: 4 x 2,656 bf16 rows, 112 units 97 us (6.3 TB/s); 8 windows of 4,100 rows, 256
@@ -354,18 +354,19 @@ __global__ void __launch_bounds__(kPdThreads, (Ring<NR, kPack>::kCtas))
                     tops[4 * (8 * x + n) + warp] = top;
             }
             __syncthreads();
-            // 2^k times the largest is in [2^12, 2^13)
+            // 2^k times the largest is in [2^12, 2^13); a row of less than 2^-88 is taken times 2^100, as 2^-k
+            // times the scale has to be a number
             auto power = [&](int row) -> int {
                 const float4 v = *reinterpret_cast<const float4 *>(tops + 4 * row);
-                return min(126, 12 + 127 - (int)(__float_as_uint(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))) >> 23));
+                return min(100, 12 + 127 - (int)(__float_as_uint(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w))) >> 23));
             };
             float up[NR];
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
                 up[x] = __uint_as_float((uint32_t)(127 + power(8 * x + n)) << 23);
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    rs[x][e] = a.scale_log2 * __uint_as_float((uint32_t)(127 - power(8 * x + 2 * c + e)) << 23);
+                for (int e = 0; e < 2; ++e)   // (never 0, which would make the -inf of a hidden row's score a NaN)
+                    rs[x][e] = fmaxf(a.scale_log2 * __uint_as_float((uint32_t)(127 - power(8 * x + 2 * c + e)) << 23), 1.40129846e-45f);
             }
             __syncthreads();
 #pragma unroll
