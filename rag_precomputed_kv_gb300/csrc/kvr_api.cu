@@ -2018,6 +2018,20 @@ int64_t page_extent(const kvr_pool &p, const kvr_pages &g)
            (int64_t)g.page_rows * p.d.head_dim;
 }
 
+// Whether runs of `run` bytes at the sums of `n` strides (ascending, each at least what the ones before
+// it span) meet the same ones `d` bytes further on.  Within its stride's multiples an outer distance is
+// made good by the nearest two: what the inner ones span is at most one stride.
+bool runs_meet(int64_t d, const int64_t *stride, const int64_t *count, int n, int64_t run)
+{
+    if (n == 0)
+        return -run < d && d < run;
+    const int64_t s = stride[n - 1], j0 = d / s;
+    for (int64_t j = j0 - 1; j <= j0 + 1; ++j)
+        if (-count[n - 1] < j && j < count[n - 1] && runs_meet(d - j * s, stride, count, n - 1, run))
+            return true;
+    return false;
+}
+
 // `written`: the call writes rows, which must then not lie upon each other.
 kvr_status check_pages(const kvr_pool &p, const kvr_pages *pages, bool written)
 {
@@ -2045,6 +2059,18 @@ kvr_status check_pages(const kvr_pool &p, const kvr_pages *pages, bool written)
             if (count[i] > 1)
                 need = (count[i] - 1) * g.stride[i] + need;
         }
+        int64_t stride[3], number[3];
+        int n = 0;
+        for (int i : o)
+            if (count[i] > 1) {
+                stride[n] = g.stride[i] * p.elt();
+                number[n++] = count[i];
+            }
+        // (apart as a whole, as in most caches: their distance may be beyond 2^63)
+        if (range_of(g.k, 0, need, p.elt()).meets(range_of(g.v, 0, need, p.elt())) &&
+            runs_meet((int64_t)(reinterpret_cast<uintptr_t>(g.v) - reinterpret_cast<uintptr_t>(g.k)), stride, number, n,
+                      (int64_t)g.page_rows * p.d.head_dim * p.elt()))
+            return fail(KVR_ERR_INVALID_ARG, "pages: rows of v lie upon rows of k, and the call writes both");
     }
     return KVR_OK;
 }

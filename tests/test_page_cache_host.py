@@ -251,3 +251,45 @@ def test_keys_that_are_the_values_are_read_but_not_written(lib, pool):
     if _no_gpu():
         assert attend(lib, pool, **same) == 4
         assert pack(lib, pool, **same) == 4
+
+
+def test_keys_and_values_that_lie_upon_each_other_are_read_but_not_written(lib, pool):
+    """v some elements, rows, pages, heads or layers behind k (or before it) in one dense pool; and side by
+    side in one tensor, which is fine."""
+    page, layer = L * H * UNIT, H * UNIT
+    for d in (8, 64, ROW, UNIT - ROW, UNIT, UNIT + 64, 2 * UNIT, layer, layer + UNIT, page - ROW, page, 7 * page, 8 * page - 64):
+        for a, b in ((A, A + 2 * d), (A + 2 * d, A)):
+            kw = dict(pages=dict(k=a, v=b))
+            assert append(lib, pool, k=E, v=F, **kw) == 1 and "lie upon" in lib.kvr_last_error().decode(), d
+            assert pack(lib, pool, unpack=True, **kw) == 1, d
+            if _no_gpu():
+                assert attend(lib, pool, q=E, out=F, **kw) == 4 and pack(lib, pool, **kw) == 4
+    beside = [((2 * page, layer, UNIT), page), ((2 * page, 2 * layer, UNIT), layer), ((2 * page, 2 * layer, 2 * UNIT), UNIT),
+              ((page, layer, UNIT), 8 * page), ((2 * UNIT, 16 * layer, 16 * UNIT), UNIT)]
+    if _no_gpu():
+        for stride, d in beside:
+            for a, b in ((A, A + 2 * d), (A + 2 * d, A)):
+                assert append(lib, pool, k=E, v=F, pages=dict(k=a, v=b, stride=stride)) == 4, (stride, d)
+    for stride, d in beside[:3]:      # a row further on they meet
+        assert append(lib, pool, k=E, v=F, pages=dict(k=A, v=A + 2 * (d + ROW), stride=stride)) == 1
+
+
+@pytest.mark.skipif("not _no_gpu()")
+def test_where_rows_lie_is_found_as_by_trying_all(lib, pool):
+    rng = np.random.default_rng(1)
+    seen = [0, 0]
+    for _ in range(400):
+        n, rows = int(rng.integers(1, 5)), int(rng.integers(1, 3))
+        run, stride = rows * ROW, [0, 0, 0]
+        need = run
+        for i in rng.permutation(3):
+            stride[i] = need * int(rng.integers(1, 5)) + 8 * int(rng.integers(0, 20))
+            need += ((n, L, H)[i] - 1) * stride[i]
+        d = 8 * int(rng.integers(-need // 8 - 2, need // 8 + 3))
+        starts = (np.arange(n)[:, None, None] * stride[0] + np.arange(L)[:, None] * stride[1] + np.arange(H) * stride[2]).ravel()
+        meet = bool((np.abs(starts[:, None] - starts[None] - d) < run).any())
+        seen[meet] += 1
+        got = append(lib, pool, pages=dict(k=A + (1 << 20), v=A + (1 << 20) + 2 * d, n=n, rows=rows, stride=tuple(stride)), table=((0,), (0,)),
+                     width=1, start=(0, 0), qo=(0, 1, 1), k=E, v=F)
+        assert got == (1 if meet else 4), (n, rows, stride, d)
+    assert min(seen) > 50
