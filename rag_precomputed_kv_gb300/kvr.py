@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from array import array
+from operator import index
 from typing import Optional, Sequence
 
 import numpy as np
@@ -211,6 +212,14 @@ def _data(name: str, t, dtype, n: int) -> Optional[int]:
     return t.data_ptr()
 
 
+def _int32(name: str, x) -> int:
+    """``x``, an integer that fits 32 bits."""
+    i = index(x)
+    if not -(1 << 31) <= i < 1 << 31:
+        raise ValueError(f"{name} must be a 32-bit integer, got {i}")
+    return i
+
+
 def _page_table(name: str, a, batch: int):
     """``a`` as a C array of int32 [batch][width]: (keep-alive, address, width)."""
     if a is None:
@@ -226,7 +235,7 @@ def _page_table(name: str, a, batch: int):
     elif not isinstance(a, np.ndarray):
         a = [list(r) for r in a]
         width = max(map(len, a), default=0)
-        a = np.array([r + [-1] * (width - len(r)) for r in a], np.int64).reshape(len(a), width)
+        a = np.array(array("i", [x for r in a for x in r + [-1] * (width - len(r))]), np.int32).reshape(len(a), width)
     c = np.ascontiguousarray(a, dtype=np.int32)
     if c.ndim != 2 or c.shape[0] != batch:
         raise ValueError(f"{name} must be [{batch}, pages], got shape {c.shape}")
@@ -261,7 +270,7 @@ class PackedPages:
         import torch
         if data.dtype is not torch.uint8 or data.dim() != 2 or not data.is_contiguous() or not data.is_cuda:
             raise ValueError("data must be a contiguous uint8 device tensor [n_pages, bytes]")
-        self.data, self.page_rows = data, int(page_rows)
+        self.data, self.page_rows = data, _int32("page_rows", page_rows)
         self._d = PackedDesc(data.data_ptr(), data.shape[0])
         self._p = ctypes.addressof(self._d)
 
@@ -480,7 +489,7 @@ class Pool:
 
     def packed_page_bytes(self, page_rows: int) -> int:
         """kvr_packed_page_bytes: 0 where the pool's rows cannot be packed."""
-        return int(load().kvr_packed_page_bytes(self._h, int(page_rows)))
+        return int(load().kvr_packed_page_bytes(self._h, _int32("page_rows", page_rows)))
 
     def packed_pages(self, n_pages: int, page_rows: int) -> "PackedPages":
         """New packed pages (zeros: scales of 0) on the current device."""
@@ -534,8 +543,9 @@ class Pool:
             if x is not None and not x.is_cuda:
                 raise ValueError(f"{name} must be in device memory")
         q_, o_ = _data("q", q, self.dtype, size), _data("out", out, self.dtype, size)
-        _raise(load().kvr_page_attention(self._h, p, n, tab[1], tab[2], kl[1], qp[1], qo[1], q_, o_, int(window), int(n_first),
-                                         pk, ptab[1], ptab[2], pl[1], float(softmax_scale), _stream_ptr(stream)))
+        _raise(load().kvr_page_attention(self._h, p, n, tab[1], tab[2], kl[1], qp[1], qo[1], q_, o_,
+                                         _int32("window", window), _int32("n_first", n_first), pk, ptab[1], ptab[2], pl[1],
+                                         float(softmax_scale), _stream_ptr(stream)))
 
     def page_pack(self, pages: "Pages", table, packed: "PackedPages", packed_table, begin, end, stream=None):
         """kvr_page_pack: rows ``begin[b]`` .. ``end[b] - 1`` (multiples of 32) of

@@ -293,3 +293,35 @@ def test_where_rows_lie_is_found_as_by_trying_all(lib, pool):
                      width=1, start=(0, 0), qo=(0, 1, 1), k=E, v=F)
         assert got == (1 if meet else 4), (n, rows, stride, d)
     assert min(seen) > 50
+
+
+def test_binding_refuses_numbers_that_it_would_have_to_cut(lib, pool):
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    own, pages = object.__new__(kvr.Pool), object.__new__(kvr.Pages)
+    own.__dict__.update(_h=pool, n_layers=L, n_kv_heads=H, n_q_heads=H * G, head_dim=D, dtype=torch.bfloat16, _layout=(L, H, D), _wide=H * G * D)
+    desc = _pages()
+    pages.__dict__.update(shape=(L, H, D), dtype=torch.bfloat16, page_rows=64, _d=desc, _p=ctypes.addressof(desc))
+    try:
+        def call(**kw):
+            own.page_attention(pages, [[0]], [0], [0, 0], None, None, stream=0, **kw)
+
+        for name in ("window", "n_first"):
+            for x in (0, 5, np.int64(7), (1 << 31) - 1):
+                call(**{name: x})
+            for x in (2.5, 1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 33), "3"):
+                with pytest.raises((TypeError, ValueError)):
+                    call(**{name: x})
+            with pytest.raises(kvr.KvrError):
+                call(**{name: -1})
+        assert own.packed_page_bytes(64) == lib.kvr_packed_page_bytes(pool, 64)
+        for x in ((1 << 32) + 64, 64.5):
+            with pytest.raises((TypeError, ValueError)):
+                own.packed_page_bytes(x)
+    finally:
+        own._h = None
+    for bad in ([[1.5, 2]], [[1, 2.0]], [[1 << 40]], [[1], [None]]):
+        with pytest.raises((TypeError, ValueError, OverflowError)):
+            kvr._page_table("t", bad, len(bad))
+    assert kvr._page_table("t", [(np.int32(4), 2), []], 2)[0].tolist() == [[4, 2], [-1, -1]]
+    assert kvr._page_table("t", [[], []], 2)[2] == 0
