@@ -762,19 +762,22 @@ cudaError_t launch_page_decode(const PageArgs &a, const PageTable &t, const DevP
 {
     const Variant variants[4] = {variant<1, false>(), variant<2, false>(), variant<1, true>(), variant<2, true>()};
     static std::atomic<bool> known[64] = {};   // per device (host threads may race: same values)
-    static int caps[64][4][4];
+    static std::atomic<int> caps[64][4][4];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    int own[4][4], (*cap)[4] = dev < 64 ? caps[dev] : own;
-    if (dev >= 64 || !known[dev].load(std::memory_order_acquire)) {
+    int cap[4][4];
+    if (dev < 64 && known[dev].load(std::memory_order_acquire)) {
+        for (int i = 0; i < 16; ++i)
+            cap[i / 4][i % 4] = caps[dev][i / 4][i % 4].load(std::memory_order_relaxed);
+    } else {
         for (int i = 0; i < 4; ++i)
-            if ((e = capacities(variants[i], own[i])) != cudaSuccess)
+            if ((e = capacities(variants[i], cap[i])) != cudaSuccess)
                 return e;
         if (dev < 64) {
             for (int i = 0; i < 16; ++i)
-                caps[dev][i / 4][i % 4] = own[i / 4][i % 4];
+                caps[dev][i / 4][i % 4].store(cap[i / 4][i % 4], std::memory_order_relaxed);
             known[dev].store(true, std::memory_order_release);
         }
     }

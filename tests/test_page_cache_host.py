@@ -1,6 +1,9 @@
 """The paged cache on the CPU: every refused argument is refused with a status,
 before any GPU work; the binding's own checks; the packed format's rounding."""
 import ctypes
+import glob
+import os
+import re
 from fractions import Fraction
 
 import numpy as np
@@ -325,3 +328,15 @@ def test_binding_refuses_numbers_that_it_would_have_to_cut(lib, pool):
             kvr._page_table("t", bad, len(bad))
     assert kvr._page_table("t", [(np.int32(4), 2), []], 2)[0].tolist() == [[4, 2], [-1, -1]]
     assert kvr._page_table("t", [[], []], 2)[2] == 0
+
+
+def test_what_host_threads_share_is_atomic():
+    """Two pools may be called by two threads at once: what a launcher keeps between calls is constant or atomic."""
+    kept = re.compile(r"^\s+static (?!const\b|constexpr\b|std::atomic<)[^(;={]*(?:;|=|\{)", re.M)
+    found = {}
+    for path in glob.glob(os.path.join(B.CSRC, "*.cu*")):
+        with open(path) as f:
+            found[os.path.basename(path)] = kept.findall(re.sub(r"//[^\n]*", "", f.read()))
+    assert len(found) > 10 and not {k: v for k, v in found.items() if v}
+    assert kept.findall("    static int caps[64];\n    static bool x = 1;\n    static std::atomic<int> y;\n    static kvr_status f(int a);\n") == [
+        "    static int caps[64];", "    static bool x ="]
