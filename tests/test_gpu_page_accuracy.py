@@ -1,11 +1,34 @@
-"""Paged attention at the ends of fp32's range: queries of zeros and scales near zero, large and
-small queries, against fp64."""
+"""How near the paged attention's kernels come to fp64, each by its own precision, and
+queries and scales at the ends of fp32's range.
+
+A result rounded to bf16 is off by r = ||round(o) - o|| / ||o||, which is taken from the
+fp64 result itself.  Each operand that a kernel rounds to bf16 on the way (the turned
+query, the probability, a restored key, a restored value) is off by as much in the rms
+and independently of the others: with queries and keys of unit variance a score's error
+is r times its own spread of 1, and so is the probability's.  n roundings give r sqrt(n):
+    up to 16 query rows, bf16 rows             n = 1   the output alone
+    up to 16, or in parts, on packed rows      n = 2   and the probability times its scale
+    more query rows                            n = 3   the output, the query, the probability
+    more query rows on packed rows             n = 5   and keys and values, restored
+(fp16 queries, 11 bits, add 1/64.)  The limit is half a rounding above, r sqrt(n + 1/2):
+one rounding more does not pass.
+"""
 import numpy as np
 import pytest
 
-from test_gpu_page_cache import _packed_ref, _pool, _randn, _table
+from test_gpu_page_cache import THETA, _packed_ref, _pool, _randn, _starts, _table
 
 pytestmark = pytest.mark.gpu
+
+
+def _turn64(x, pos, theta=THETA):
+    """x [..., T, heads, D] fp64 on the GPU, token t turned by pos[t]."""
+    import torch
+    h = x.shape[-1] // 2
+    w = theta ** (-torch.arange(h, dtype=torch.float64, device=x.device) / h)
+    a = torch.as_tensor(np.asarray(pos), dtype=torch.float64, device=x.device)[:, None, None] * w
+    lo, hi = x[..., :h], x[..., h:]
+    return torch.cat([lo * a.cos() - hi * a.sin(), lo * a.sin() + hi * a.cos()], -1)
 
 
 def _rows64(x, ids, n, R):
@@ -18,6 +41,84 @@ def _thin64(x):
     """What the packed form of bf16 rows stands for, exactly."""
     code, scale = _packed_ref(x.to("cpu"))
     return (code * scale).reshape(x.shape).to("cuda")
+
+
+def _attend64(q, K, V, pos, scale):
+    """q [L, T, Hq, D] turned, K, V [L, H, n, D]; every token sees rows <= its position."""
+    import torch
+    L, T, Hq, D = q.shape
+    H, n = K.shape[1], K.shape[2]
+    x = q.view(L, T, H, Hq // H, D)
+    hide = torch.arange(n, device="cuda") > torch.as_tensor(np.asarray(pos), device="cuda")[:, None]
+    out = torch.empty_like(x)
+    for l in range(L):
+        for h in range(H):
+            s = torch.einsum("tgd,nd->tgn", x[l, :, h], K[l, h]) * scale
+            s.masked_fill_(hide[:, None], -float("inf"))
+            out[l, :, h] = torch.einsum("tgn,nd->tgd", torch.softmax(s, -1), V[l, h])
+    return out.view(L, T, Hq, D)
+
+
+def _off(got, want):
+    """||got - want|| / ||want|| and the same of want rounded to bf16."""
+    import torch
+    n = want.norm()
+    return float((got.double() - want).norm() / n), float((want.to(torch.bfloat16).double() - want).norm() / n)
+
+
+def _case(reqs, G, L=2, H=4, R=64, seed=1):
+    """reqs: (rows, query tokens, packed rows, roundings).  Each request against its own limit."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    D = 128
+    kv, lq, body, roundings = (list(x) for x in zip(*reqs))
+    t, n = _table(kv, R, seed)
+    k, v = (_randn(seed + i, (n, L, H, R, D), "bf16") for i in (1, 2))
+    Q = _randn(seed + 3, (L, sum(lq), H * G, D), "bf16")
+    out = torch.full_like(Q, float("nan"))
+    pool, kw = _pool(L, H, G, D, "bf16"), {}
+    if any(body):
+        packed = pool.packed_pages(n, R)
+        pool.page_pack(kvr.Pages(k, v), t, packed, t, [0] * len(body), body)
+        kw = dict(packed=packed, packed_table=t, packed_len=body)
+    qo = _starts(lq)
+    pool.page_attention(kvr.Pages(k, v), t, kv, qo.astype(np.int32), Q, out, **kw)
+    pool.check()
+    for b, (m, T, p, roundings) in enumerate(reqs):
+        a, e = int(qo[b]), int(qo[b + 1])
+        pos = m - T + np.arange(T)
+        K, V = _rows64(k, t[b], m, R), _rows64(v, t[b], m, R)
+        if p:
+            K[:, :, :p], V[:, :, :p] = (_thin64(_rows64(x, t[b], p, R).to(torch.bfloat16)) for x in (k, v))
+        want = _attend64(_turn64(Q[:, a:e].double(), pos), K, V, pos, D ** -0.5)
+        off, r = _off(out[:, a:e], want)
+        assert 0.8 * r <= off <= r * np.sqrt(roundings + 0.5), (b, off, r, off * off / (r * r))
+    return pool
+
+
+@pytest.mark.parametrize("G,q", [(1, 16), (4, 1), (4, 4), (7, 2), (8, 1), (16, 1)])
+def test_few_query_rows_are_off_by_their_rounding(G, q):
+    _case([(700, q, 0, 1), (333, q, 0, 1), (1500, 1, 0, 1)], G)
+
+
+@pytest.mark.parametrize("G,q", [(1, 16), (4, 1), (4, 4), (7, 2), (16, 1), (1, 17), (1, 48), (4, 12), (7, 6), (16, 3)])
+def test_few_query_rows_and_parts_on_packed_rows(G, q):
+    """... in parts as alone, and one that sees no packed row beside them as without them."""
+    _case([(700, q, 640, 2), (333, q, 320, 2), (900, 1, 0, 1), (1500, 1, 1472, 2)], G)
+
+
+@pytest.mark.parametrize("G,q", [(1, 17), (4, 40), (7, 64), (16, 2), (20, 1)])
+def test_many_query_rows(G, q):
+    _case([(700, q, 0, 3), (333, q, 0, 3), (1500, q, 0, 3)], G)
+
+
+@pytest.mark.parametrize("G,q", [(1, 49), (4, 13), (7, 64), (16, 4), (20, 1)])
+def test_many_query_rows_on_packed_rows(G, q):
+    _case([(700, q, 640, 5), (333, q, 320, 5), (1500, q, 1408, 5)], G)
+
+
+def test_each_request_of_a_call_keeps_its_own_precision():
+    _case([(700, 60, 640, 5), (700, 60, 0, 3), (700, 1, 640, 2), (700, 12, 640, 2), (700, 1, 0, 1)], 4)
 
 
 # ---------------------------------------------------------------------------

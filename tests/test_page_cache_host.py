@@ -340,3 +340,38 @@ def test_what_host_threads_share_is_atomic():
     assert len(found) > 10 and not {k: v for k, v in found.items() if v}
     assert kept.findall("    static int caps[64];\n    static bool x = 1;\n    static std::atomic<int> y;\n    static kvr_status f(int a);\n") == [
         "    static int caps[64];", "    static bool x ="]
+
+
+def test_limits_of_the_accuracy_tests_tell_the_roundings_apart():
+    """The model behind the limits of the GPU tests' norms, in fp64 with operands rounded to bf16 here: an error
+    in units of the output's own rounding, squared, is the number of roundings, and one more passes no limit."""
+    import torch
+    bf = lambda x: x.to(torch.bfloat16).double()
+
+    def roundings(packed):
+        g = torch.Generator().manual_seed(3)
+        off = dict.fromkeys(("none", "q", "p", "qp", "qpkv"), 0.0)
+        own = 0.0
+        for _ in range(8):
+            q = torch.randn((32, 128), generator=g).double()
+            k, v = (bf(torch.randn((700, 128), generator=g)) for _ in range(2))
+            if packed:
+                k, v = ((torch.round(y / s).clamp(-7, 7) * s).view(700, 128)
+                        for y, s in ((x.view(700, 4, 32), bf(x.view(700, 4, 32).abs().amax(-1, keepdim=True) / 7)) for x in (k, v)))
+
+            def out(r=""):
+                a, b, c = (bf(x) if y in r else x for x, y in ((q, "q"), (k, "k"), (v, "v")))
+                s = a @ b.T * 128 ** -0.5
+                p = torch.exp(s - s.amax(-1, keepdim=True))
+                return (bf(p) if "p" in r else p) @ c / p.sum(-1, keepdim=True)
+
+            want = out()
+            own += float((bf(want) - want).norm() ** 2)
+            for r in off:
+                off[r] += float((bf(out(r.replace("none", ""))) - want).norm() ** 2)
+        return {r: x / own for r, x in off.items()}
+
+    n = roundings(False)      # limits: 1 + 1/2, 3 + 1/2
+    assert n["none"] < 1.01 and 1.5 < n["q"] < 2.5 and 1.5 < n["p"] < 2.5 and 2.5 < n["qp"] < 3.5, n
+    n = roundings(True)       # 2 + 1/2, 5 + 1/2
+    assert 1.5 < n["p"] < 2.5 < n["qp"] < 3.5 < n["qpkv"] < 5.5, n
