@@ -619,6 +619,22 @@ enum { KVR_SHARED_NONE = -1, KVR_SHARED_CUDA_CORES = 0, KVR_SHARED_PARTS = 1, KV
  * keys in one kernel.  KVR_SHARED_NONE before the first; -2 for a NULL pool. */
 KVR_API int32_t kvr_shared_path(kvr_pool_t pool);
 
+/* Kernels of kvr_page_attention (kvr_page_path): bits, and above the lowest eight the
+ * number of launches that the kernel of many query rows took, each for a slice of the
+ * (layer, kv-head) units whose restored rows fit the scratch. */
+enum {
+    KVR_PAGE_NONE = -1,
+    KVR_PAGE_CUDA_CORES = 1,   /* fp32, or head_dim 64 */
+    KVR_PAGE_FEW = 2,          /* up to 16 query rows a request, or parts of so many on packed rows */
+    KVR_PAGE_MANY = 4,         /* more of them (tcgen05) */
+    KVR_PAGE_RESTORED = 8,     /* ... on packed rows, restored to bf16 first */
+    KVR_PAGE_JOINED = 16       /* ... in stretches of the cache, whose results were joined */
+};
+
+/* Which kernels the pool's last kvr_page_attention that enqueued work ran;
+ * KVR_PAGE_NONE before the first, -2 for a NULL pool. */
+KVR_API int32_t kvr_page_path(kvr_pool_t pool);
+
 /* Timing hook.  With events non-NULL, later calls on this pool record, on the
  * caller's stream, events[0] / events[1] right before / after the assemble
  * kernel, events[2] / events[3] around the query-append kernel (nothing

@@ -115,6 +115,7 @@ struct kvr_pool {
     int *err = nullptr;       // device error word, then the shared-prefix calls' relay words
     uint32_t shared_calls = 0;   // shared-prefix calls on the tensor cores so far
     int32_t shared_path = KVR_SHARED_NONE;   // kernels of the last shared-prefix call
+    int32_t page_path = KVR_PAGE_NONE;       // ... of the last paged attention
     Slot slots[kSlots];
     int next = 0;
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -2590,20 +2591,25 @@ extern "C" kvr_status kvr_page_attention(kvr_pool_t p, const kvr_pages *pages, i
             return st;
         p->mark(4, s);
         NvtxRange r("kvr.k_page_attention");
+        int32_t path = tensor ? (few ? KVR_PAGE_FEW : 0) : KVR_PAGE_CUDA_CORES;
         cudaError_t e = few && tensor ? launch_page_decode(a, pl.tab, pl.rq.data(), p->n_sms, s) : cudaSuccess;
         if (e == cudaSuccess && !tensor)
             e = launch_page_simt(a, pl.tab, p->d.dtype, D, s);
         if (e == cudaSuccess && many) {
             e = launch_page_queries(a, pl.tab, p->q_rot, s);
+            int slices = 0;
             for (int lh = 0; lh < LH && e == cudaSuccess; lh += lh_slice) {
                 tc.lh_base = lh;
                 const int n = std::min(lh_slice, LH - lh);
                 tc.total = (int64_t)n * tc.unit_items;
                 e = launch_page_tc(a, tc, pl.tab, maps, n, p->n_sms, s);
+                ++slices;
             }
+            path |= KVR_PAGE_MANY | (tc.unit_tiles > 0 ? KVR_PAGE_RESTORED : 0) | (tc.splits > 1 ? KVR_PAGE_JOINED : 0) | slices << 8;
             cudaEventRecord(p->q_rot_done, s);
             p->q_rot_used = true;
         }
+        p->page_path = path;
         p->mark(5, s);
         if (pl.slot)
             cudaEventRecord(pl.slot->done, s);
@@ -2690,3 +2696,4 @@ extern "C" int32_t kvr_attention_path(kvr_pool_t p)
 }
 
 extern "C" int32_t kvr_shared_path(kvr_pool_t p) { return p ? p->shared_path : -2; }
+extern "C" int32_t kvr_page_path(kvr_pool_t p) { return p ? p->page_path : -2; }

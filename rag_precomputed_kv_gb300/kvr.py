@@ -37,9 +37,11 @@ EXPORTED = ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_que
             "kvr_prefill", "kvr_check", "kvr_status_string", "kvr_last_error", "kvr_attention_path",
             "kvr_set_timing_events", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
             "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict", "kvr_shared_path",
-            "kvr_packed_page_bytes", "kvr_page_append", "kvr_page_attention", "kvr_page_pack", "kvr_page_unpack")
+            "kvr_packed_page_bytes", "kvr_page_append", "kvr_page_attention", "kvr_page_pack", "kvr_page_unpack",
+            "kvr_page_path")
 PATH_UNBOUND, PATH_CUDA_CORES, PATH_TCGEN05 = -1, 0, 1
 SHARED_NONE, SHARED_CUDA_CORES, SHARED_PARTS, SHARED_WHOLE = -1, 0, 1, 2
+PAGE_NONE, PAGE_CUDA_CORES, PAGE_FEW, PAGE_MANY, PAGE_RESTORED, PAGE_JOINED = -1, 1, 2, 4, 8, 16
 
 
 class KvrError(RuntimeError):
@@ -116,6 +118,8 @@ def load(path: str = LIB_PATH):
     lib.kvr_attention_path.restype = ctypes.c_int32
     lib.kvr_shared_path.argtypes = [vp]
     lib.kvr_shared_path.restype = ctypes.c_int32
+    lib.kvr_page_path.argtypes = [vp]
+    lib.kvr_page_path.restype = ctypes.c_int32
     for name in ("kvr_pool_register", "kvr_pool_unregister", "kvr_assemble", "kvr_query_attention",
                  "kvr_prefill", "kvr_check", "kvr_selftest_wait", "kvr_assemble_noalloc", "kvr_pool_reserve",
                  "kvr_shared_query_attention", "kvr_key_weights", "kvr_evict", "kvr_page_append", "kvr_page_attention",
@@ -572,6 +576,12 @@ class Pool:
         """Kernels of the last :meth:`shared_query_attention` that enqueued work:
         SHARED_CUDA_CORES, SHARED_PARTS, SHARED_WHOLE, or SHARED_NONE before it."""
         return int(load().kvr_shared_path(self._h))
+
+    @property
+    def page_path(self) -> int:
+        """Kernels of the last :meth:`page_attention` that enqueued work: PAGE_ bits, and 256
+        times the launches that many query rows took; or PAGE_NONE before it."""
+        return int(load().kvr_page_path(self._h))
 
     def set_timing_events(self, events):
         """Six torch.cuda.Event(enable_timing=True) recorded around the

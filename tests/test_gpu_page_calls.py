@@ -1,9 +1,11 @@
 """Paged cache: what a call uses beside its arguments."""
 import threading
 
+import numpy as np
 import pytest
 
-from test_gpu_page_cache import _pool, _randn, _table
+from test_gpu_page_accuracy import _attend64, _off, _turn64
+from test_gpu_page_cache import _pool, _randn, _starts, _table
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +58,64 @@ def test_two_threads_with_a_pool_each():
         assert len(got[i]) == 5
         for out in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+def test_restored_rows_in_slices_of_units():
+    """64 query rows on packed rows, whose restored form passes the scratch's 1 GiB: two slices of
+    the (layer, kv-head) units, the second a unit shorter, against fp64 unit by unit."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    L, H, D, R, n, q = 13, 5, 128, 128, 33152, 64
+    pool = _pool(L, H, 1, D, "bf16")
+    k, v = (_randn(i, (n // R, L, H, R, D), "bf16") for i in (1, 2))
+    t = np.random.default_rng(0).permutation(n // R).astype(np.int32)[None]
+    packed = pool.packed_pages(n // R, R)
+    pages = kvr.Pages(k, v)
+    pool.page_pack(pages, t, packed, t, [0], [n])
+    Q = _randn(3, (L, q, H, D), "bf16")
+    out = torch.full_like(Q, float("nan"))
+    for _ in range(2):      # the second call meets the first one's scratch
+        pool.page_attention(pages, t, [n], [0, q], Q, out, packed=packed, packed_table=t, packed_len=[n])
+        pool.check()
+    path = pool.page_path
+    assert path & kvr.PAGE_RESTORED and path & kvr.PAGE_MANY and path >> 8 == 2
+    # what the restoring kernel gives for each row, rounded to bf16: three roundings are left
+    pool.page_unpack(packed, t, pages, t, [0], [n])
+    pos = n - q + np.arange(q)
+    turned = _turn64(Q.double(), pos)
+    for l in range(L):
+        K, V = (torch.cat([x[int(i), l] for i in t[0]], 1)[None].double() for x in (k, v))
+        want = _attend64(turned[l:l + 1], K, V, pos, D ** -0.5)
+        for h in range(H):
+            off, r = _off(out[l, :, h], want[0, :, h])
+            assert off <= r * np.sqrt(3 + 1), (l, h, off, r)
+
+
+def test_which_kernels_ran():
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    R = 32
+
+    def path(reqs, G=4, D=128, dtype="bf16"):
+        pool = _pool(1, 2, G, D, dtype)
+        assert pool.page_path == kvr.PAGE_NONE
+        kv, lq, body = (list(x) for x in zip(*reqs))
+        t, n = _table(kv, R, 3)
+        pages = kvr.Pages(*(_randn(i, (n, 1, 2, R, D), dtype) for i in (1, 2)))
+        kw = {}
+        if any(body):
+            packed = pool.packed_pages(n, R)
+            pool.page_pack(pages, t, packed, t, [0] * len(kv), body)
+            kw = dict(packed=packed, packed_table=t, packed_len=body)
+        Q = _randn(3, (1, sum(lq), 2 * G, D), dtype)
+        pool.page_attention(pages, t, kv, _starts(lq).astype(np.int32), Q, Q, **kw)
+        pool.check()
+        return pool.page_path & 255, pool.page_path >> 8
+
+    few, many, rest = kvr.PAGE_FEW, kvr.PAGE_MANY, kvr.PAGE_RESTORED
+    assert path([(90, 4, 0)], D=64) == path([(90, 4, 0)], dtype="fp32") == (kvr.PAGE_CUDA_CORES, 0)
+    assert path([(90, 4, 0)]) == path([(90, 4, 64), (90, 1, 0)]) == path([(90, 12, 64)]) == (few, 0)
+    assert path([(90, 5, 0)]) == (many, 1) and path([(90, 5, 0), (90, 12, 64)]) == (few | many, 1)
+    assert path([(90, 13, 64)]) == (many | rest, 1) and path([(90, 13, 64), (90, 1, 0)]) == (few | many | rest, 1)
+    assert path([(90, 1, 64)], G=20) == (many | rest, 1) and path([(90, 1, 0)], G=20) == (many, 1)
+    assert path([(4000, 20, 0)], G=1) == (many | kvr.PAGE_JOINED, 1)

@@ -375,3 +375,9 @@ def test_limits_of_the_accuracy_tests_tell_the_roundings_apart():
     assert n["none"] < 1.01 and 1.5 < n["q"] < 2.5 and 1.5 < n["p"] < 2.5 and 2.5 < n["qp"] < 3.5, n
     n = roundings(True)       # 2 + 1/2, 5 + 1/2
     assert 1.5 < n["p"] < 2.5 < n["qp"] < 3.5 < n["qpkv"] < 5.5, n
+
+
+def test_page_path_before_any_call(lib, pool):
+    from rag_precomputed_kv_gb300 import kvr
+    assert lib.kvr_page_path(None) == -2
+    assert lib.kvr_page_path(pool) == kvr.PAGE_NONE
