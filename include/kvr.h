@@ -35,7 +35,8 @@
  *       3. Staging slots.  A call whose span, local-source or request tables
  *          do not fit inside its kernels' parameters (more than 64 spans,
  *          local sources or requests; in a paged cache's call more than 64
- *          requests or 1,024 pages) copies them up from one of the pool's
+ *          requests, those taken in parts counted by parts, or 1,024 page
+ *          numbers, of both its tables) copies them up from one of the pool's
  *          8 pinned staging slots, taken in turn.  A slot is allocated on
  *          first use, and freed and allocated larger when a call needs more
  *          (cudaFreeHost / cudaFree synchronize the device).  If the slot's
@@ -50,11 +51,11 @@
  *          to 1 GiB for partial results, grown the same way (133 KB for each
  *          256 query rows of a group and (layer, kv-head), and for each SM;
  *          more than 1 GiB only where one (layer, kv-head) needs it).
- *          kvr_page_attention uses both for requests of more than 16 query
- *          rows (three times as many where they see packed rows): the queries, and up to 1 GiB for packed rows restored to
- *          bf16 (512 bytes a row and (layer, kv-head); more only where one
- *          (layer, kv-head) needs it) beside partial results (133 KB for each
- *          256 query rows, (layer, kv-head) and stretch of their keys).
+ *          kvr_page_attention uses both for calls with a request of many query
+ *          rows (as said there): the queries, and up to 1 GiB for packed rows
+ *          restored to bf16 (512 bytes a row and (layer, kv-head); more only
+ *          where one (layer, kv-head) needs it) beside partial results (133 KB
+ *          for each 256 query rows, (layer, kv-head) and stretch of their keys).
  *       5. A pool in pinned host memory: the first kvr_prefill on it creates
  *          an internal stream and its events (kept until unregister).
  *     kvr_pool_reserve makes 3 and 4 happen up front, but for the partial
@@ -206,8 +207,8 @@ KVR_API kvr_status kvr_pool_unregister(kvr_pool_t pool);
  * kvr_pool_reserve -- bind the pool to the current device (if no call has
  * yet) and allocate, now, every buffer that calls within these limits need:
  * the 8 staging slots sized for the largest tables of a call with up to
- * max_batch requests (and no more groups of them), max_spans spans (or pages)
- * and max_locals local sources, and the query scratch for up to max_query_tokens
+ * max_batch requests (and no more groups of them), max_spans spans (or page
+ * numbers, of both tables of a paged cache's call together) and max_locals local sources, and the query scratch for up to max_query_tokens
  * query tokens per call (tensor-core path only).  It synchronizes (allocation
  * and the wait for slots in use).  After it, calls of every entry point within
  * the limits never allocate and never wait on the host, except on a staging
@@ -524,9 +525,9 @@ KVR_API int64_t kvr_packed_page_bytes(kvr_pool_t pool, int32_t page_rows);
  *   stride     host [3] (multiples of 16 bytes), or NULL: [L][T][H_kv][D].  A
  *              stitched block [L][H_kv][R][D] has (H_kv*R*D, D, R*D).
  * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
- * Errors: KVR_ERR_INVALID_ARG (also: pages that overlap each other, keys that are
- * the values, pages that overlap the new keys or values), KVR_ERR_OUT_OF_RANGE (a page outside the table or the
- * pool, a row beyond 2^24), KVR_ERR_CUDA.
+ * Errors: KVR_ERR_INVALID_ARG (also: pages that overlap each other, values that lie
+ * upon keys, pages that overlap the new keys or values), KVR_ERR_OUT_OF_RANGE (a
+ * page outside the table or the pool, a row beyond 2^24), KVR_ERR_CUDA.
  */
 KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int32_t batch, const int32_t *table,
                                    int32_t width, const int32_t *start, const int32_t *q_offsets, const void *k,
@@ -558,15 +559,22 @@ KVR_API kvr_status kvr_page_append(kvr_pool_t pool, const kvr_pages *pages, int3
  * Rows behind kv_len, and those that no query of the request sees, have no
  * effect, whatever they hold.  A NaN or an infinity in a value that some query
  * token of a request sees may reach all query tokens of that request in the call
- * (a weight of 0 times it is NaN).  On the tensor cores (bf16, head_dim 128) a
- * request of up to 16 query rows (tokens times G; one that sees packed rows, of
- * up to three times as many whole tokens, in parts) is computed from 11 bits of
- * its rotated queries and 16 of its probabilities, 8 where these meet packed
- * values; one of more rows from 8 bits of both, as in kvr_query_attention, and of
- * what packed rows stand for.
+ * (a weight of 0 times it is NaN).
+ *
+ * On the tensor cores (bf16, head_dim 128) a request has few query rows, or many.
+ * Few are up to 16, tokens times G.  A request that sees packed rows is taken in up
+ * to three parts of as many: up to 3 * floor(16 / G) tokens; for G > 16 there is
+ * no such part, and one token has many rows.  Few rows are computed from 11 bits of
+ * their rotated queries (16 in calls whose few rows see no packed ones) and 16 of
+ * their probabilities, 8 where these meet packed values; many from 8 bits of both,
+ * as in kvr_query_attention, and of what packed rows stand for.
  * On packed rows a query element of 2^115 or more may be reported as an infinity
  * is; so may, everywhere, scores of 2^30 or more, whose steps in fp32 are above 2^6.
- * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
+ * Capture: a call is refused with KVR_ERR_UNSUPPORTED if one of its requests has
+ * many query rows (it takes the library's scratch), or if its tables are uploaded:
+ * more than 64 requests, each part of one counted, or more than 1,024 page numbers,
+ * of both tables, each request's own.  Lengths and page numbers are the captured
+ * call's in every replay.
  * Errors: KVR_ERR_INVALID_ARG (also: `out` overlaps the pages, or q without being
  * the same buffer), KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED, KVR_ERR_CUDA;
  * kvr_check reports KVR_ERR_TIMEOUT and KVR_ERR_DEVICE_CHECK as for
@@ -586,9 +594,11 @@ KVR_API kvr_status kvr_page_attention(kvr_pool_t pool, const kvr_pages *pages, i
  *   table, packed_table  host [batch][width], [batch][packed_width]: only pages
  *                        of these rows are read; a packed page that gets rows may
  *                        be there once
- * Capture: as kvr_key_weights (more than 64 requests or 1,024 pages are uploaded).
- * Errors: KVR_ERR_INVALID_ARG (also: packed pages that overlap the pages),
- * KVR_ERR_OUT_OF_RANGE, KVR_ERR_UNSUPPORTED (the pool's type), KVR_ERR_CUDA.
+ * Capture: as kvr_key_weights (more than 64 requests, or 1,024 pages of both tables,
+ * are uploaded).
+ * Errors: KVR_ERR_INVALID_ARG (also: packed pages that overlap the pages, and for
+ * kvr_page_unpack pages as in kvr_page_append), KVR_ERR_OUT_OF_RANGE,
+ * KVR_ERR_UNSUPPORTED (the pool's type), KVR_ERR_CUDA.
  */
 KVR_API kvr_status kvr_page_pack(kvr_pool_t pool, const kvr_pages *pages, int32_t batch, const int32_t *table,
                                  int32_t width, const kvr_packed_pages *packed, const int32_t *packed_table,

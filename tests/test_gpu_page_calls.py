@@ -119,3 +119,52 @@ def test_which_kernels_ran():
     assert path([(90, 13, 64)]) == (many | rest, 1) and path([(90, 13, 64), (90, 1, 0)]) == (few | many | rest, 1)
     assert path([(90, 1, 64)], G=20) == (many | rest, 1) and path([(90, 1, 0)], G=20) == (many, 1)
     assert path([(4000, 20, 0)], G=1) == (many | kvr.PAGE_JOINED, 1)
+
+
+@pytest.mark.parametrize("G,reqs,fits", [
+    (4, [(90, 4, 0)], True), (4, [(90, 5, 0)], False),                  # 16 query rows, and 20
+    (4, [(90, 12, 64)], True), (4, [(90, 13, 64)], False),              # three parts, and four
+    (7, [(90, 6, 64)], True), (7, [(90, 7, 64)], False),                # of two tokens each
+    (16, [(90, 3, 32)], True), (20, [(90, 1, 0)], False), (20, [(90, 1, 32)], False),
+    (4, [(40, 1, 0)] * 64, True), (4, [(40, 1, 0)] * 65, False),
+    (4, [(40, 8, 32)] * 32, True), (4, [(40, 8, 32)] * 33, False),      # two parts each
+    (4, [(512 * 32, 1, 512 * 32)] * 2, True), (4, [(512 * 32 + 1, 1, 512 * 32)] * 2, False),   # 1,024 page numbers; 2 more
+    (4, [(1024 * 32, 1, 0)], True), (4, [(1025 * 32, 1, 0)], False),
+])
+def test_which_calls_can_be_captured(G, reqs, fits):
+    import gc
+
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    H, D, R = 1, 128, 32
+    pool = _pool(1, H, G, D, "bf16")
+    pool.reserve(max_batch=128, max_spans=4096, max_query_tokens=256)
+    kv, lq, body = (list(x) for x in zip(*reqs))
+    n = max(-(-x // R) for x in kv)
+    t = np.stack([np.roll(np.arange(n, dtype=np.int32), i) for i in range(len(kv))])      # (shared pages)
+    pages = kvr.Pages(*(_randn(i, (n, 1, H, R, D), "bf16") for i in (1, 2)))
+    kw = {}
+    if any(body):
+        packed = pool.packed_pages(n, R)
+        pool.page_pack(pages, t[:1], packed, t[:1], [0], [max(body)])
+        kw = dict(packed=packed, packed_table=t, packed_len=body)
+    Q = _randn(3, (1, sum(lq), H * G, D), "bf16")
+    want, out = torch.empty_like(Q), torch.zeros_like(Q)
+    args = (pages, t, kv, _starts(lq).astype(np.int32), Q)
+    pool.page_attention(*args, want, **kw)
+    torch.cuda.synchronize()
+    pool.check()
+    gc.collect()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Q.add_(0)
+        if fits:
+            pool.page_attention(*args, out, **kw)
+        else:
+            with pytest.raises(kvr.KvrError) as e:
+                pool.page_attention(*args, out, **kw)
+            assert e.value.status == 3
+    g.replay()
+    torch.cuda.synchronize()
+    pool.check()
+    assert torch.equal(out, want) if fits else not out.any()
