@@ -98,8 +98,10 @@ __device__ __forceinline__ void rotate_halves(uint4 &x, uint4 &y, const float2 *
 
 // A group of D / 2 / N threads per token: each holds a 16-byte vector of both
 // halves of a row, its (cos, sin) once for all the units that its CTA takes.  Bound by
-// HBM: 2,592 rows, 112 units, 47 us = 6.3 TB/s read and written, 0.94 of the copy rate; a
-// serving batch's 64 rows, 288 units (19 MB), by the host's call of 10 us.
+// HBM: 2,592 rows, 112 units, 47 us = 6.3 TB/s read and written, 0.94 of the copy rate (50 us
+// turned).  A serving batch's 64 rows, 288 units (19 MB): 7.1 us in a replayed graph of calls on
+// eight caches, 2.8 at the copy rate, of which a thread's chain (its request by bisection, a page
+// number, the rotation, a row) is the larger part; a call by itself takes the host 10 to 13 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(kApThreads)
     k_page_append(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t)
@@ -324,8 +326,10 @@ constexpr int kSmTeams = kSmThreads / 8;
 // chain of loads, sums over its threads and exponentials, so a team takes four rows (of 128 fp32
 // dims two) at once; many by instructions: without empty heads.  fp32, head_dim 64, 2 heads a kv
 // head, 8 units: 4 x 1 token on 2,000 rows 22 us, 49 with a row at a time; 4 x 24 tokens 80 us,
-// 150 with places for 4 heads, 171 with a row at a time too (bf16 81, 191 and 173); 16 tokens on
-// 193 rows, 2 units, the host's call.
+// 150 with places for 4 heads, 171 with a row at a time too (bf16 81, 191 and 173): the reads alone
+// are 5 us, but each token takes the whole cache again, and every product is an FMA (issue slots
+// 57 % busy).  head_dim 128 32 and 172 us, its reads 10.  16 tokens on 193 rows, 2 units: 5.3 us in a
+// replayed graph, the host's call 8 to 10.
 template <typename T, int D, int kSmHeads>
 __global__ void __launch_bounds__(kSmThreads)
     k_page_simt(const __grid_constant__ PageArgs a, const __grid_constant__ PageTable t)

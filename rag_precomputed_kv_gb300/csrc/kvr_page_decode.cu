@@ -33,12 +33,13 @@
 // (0.0017 of its norm; 0.0029 with one term each).  Queries that meet packed rows are fp16
 // times a power of two of their row, the largest element between 2^12 and 2^13 (11 bits of
 // an element, fewer below 2^-22 of the largest or 2^-114); probabilities there are rounded to
-// bf16 (0.0024), as the step is bound by instructions.
+// bf16 (0.0024), as a second term would be half as many products again in the step's chain.
 //
-// Measured: 4 x 2,656 bf16 rows, 112 units 97 us (6.3 TB/s); 8 windows of 4,100 rows, 256
-// units 605 us (7.1 TB/s; reads alone run above the copy rate).  33,280 packed rows, 256
-// units 269 us, 4.6 TB/s; the integer pipe is busy 0.6 of the time, half of it with
-// extracting codes.  On the way there (33,280 packed rows): the 16 query rows as the MMA's
+// Measured: 4 x 2,656 bf16 rows, 112 units 93 us (6.5 TB/s); 8 windows of 4,100 rows, 256
+// units 600 us (7.1 TB/s; reads alone run above the copy rate).  33,280 packed rows, 256
+// units 271 to 293 us, 4.2 to 4.6 TB/s: no pipe is full (issue slots and ALU 0.58 of the time, half
+// of it with extracting codes, DRAM 0.49); what bounds it is the length of a step's chain, codes,
+// products, exponentials, products, at a fifth of the warps that an SM can hold.  On the way there (33,280 packed rows): the 16 query rows as the MMA's
 // rows 699 us; as columns, eight at a time 374; steps of 16 rows in a loop that the
 // instruction cache holds, scales of a step together 348 (not a loop, 16 x 1,216 rows take
 // 240 us, 197 as one); four CTAs an SM 317; keys as subnormal numbers (one shift a word

@@ -37,9 +37,9 @@
 // probabilities would add half of all products).
 //
 // Bound by the tensor pipe and the chain S, softmax, P V of each tile: a step of 128 keys and
-// 256 rows takes 1.5 us, its products 1.35 at cuBLAS's rate.  A 4,096-token prompt x 4 heads, 256 units: 889 us / 8 layers without a window, 0.64 of
-// the measured peak; with a window of 1,024 and 64 first rows (9 key tiles a block) 1,985 us, where 5
-// of a block's 18 us are its start and end.  What mattered (that prompt): registers without
+// 256 rows takes 1.5 us, its products 1.35 at cuBLAS's rate.  A 4,096-token prompt x 4 heads, 64 units, 880 to 889 us without a window, 0.64 of
+// the measured peak; 256 units with a window of 1,024 and 64 first rows (9 key tiles a block) 1,965 to
+// 2,030 us, where 5 of a block's 18 us are its start and end.  What mattered (that prompt): registers without
 // spills (28 bytes spilled in the softmax: 8 %), masks as bits, item geometry and page numbers
 // worked out ahead of their use, the next item's S ahead of the epilogue (2,460 then); 64 bytes
 // written at once by lanes in pairs (a row a thread: 12 bytes a clock; 4 %); one tile for first rows and
