@@ -527,10 +527,11 @@ class Pool:
     def page_attention(self, pages: "Pages", table, kv_len, q_offsets, q, out, q_pos=None, window: int = 0,
                        n_first: int = 0, packed: Optional["PackedPages"] = None, packed_table=None, packed_len=None,
                        softmax_scale: float = 0.0, stream=None):
-        """kvr_page_attention: attention of ``q`` over the paged cache, written to
-        ``out``; with ``window``, over the last ``window`` rows before each query
-        and the first ``n_first``.  ``packed``: rows below ``packed_len[b]`` are
-        read from these packed pages, through ``packed_table``."""
+        """kvr_page_attention: attention of ``q`` ``[layers, T, q_heads, head_dim]``
+        (T: ``q_offsets[-1]``) over the paged cache, written to ``out``; with
+        ``window``, over the last ``window`` rows before each query and the first
+        ``n_first``.  ``packed``: rows below ``packed_len[b]`` are read from these
+        packed pages, through ``packed_table``."""
         qo = _ints("q_offsets", q_offsets, "i")
         n = qo[2] - 1
         kl, tab, p = _ints("kv_len", kv_len, "i", n), _page_table("table", table, n), self._pages(pages)
@@ -542,7 +543,11 @@ class Pool:
             pk, ptab, pl = self._packed(packed, pages), _page_table("packed_table", packed_table, n), _ints("packed_len", packed_len, "i", n)
         elif packed_table is not None or packed_len is not None:
             raise ValueError("packed_table and packed_len go with packed")
-        size = self.n_layers * (int(qo[0][-1]) if n >= 0 else 0) * self._wide
+        tokens = int(qo[0][-1]) if n >= 0 else 0
+        size = self.n_layers * tokens * self._wide
+        for name, x in (("q", q), ("out", out)):   # (the layers lie as many tokens apart as there are)
+            if x is not None and self.n_layers > 1 and x.dim() == 4 and x.shape[0] == self.n_layers and x.shape[1] != tokens:
+                raise ValueError(f"{name} must hold {tokens} tokens in each layer, got {x.shape[1]}")
         for name, x in (("q", q), ("out", out)):
             if x is not None and not x.is_cuda:
                 raise ValueError(f"{name} must be in device memory")

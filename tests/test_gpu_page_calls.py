@@ -168,3 +168,29 @@ def test_which_calls_can_be_captured(G, reqs, fits):
     torch.cuda.synchronize()
     pool.check()
     assert torch.equal(out, want) if fits else not out.any()
+
+
+def test_a_padded_batch():
+    """One layer: tokens behind the last request's are left as they were.  More layers: refused where the token
+    axis is longer than the offsets, taken when cut to it."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    H, G, D, R = 2, 4, 128, 32
+    for L in (1, 3):
+        pool = _pool(L, H, G, D, "bf16")
+        t, n = _table([90, 50], R, 3)
+        pages = kvr.Pages(*(_randn(i, (n, L, H, R, D), "bf16") for i in (1, 2)))
+        for lq in ((1, 1), (2, 3), (30, 9)):
+            T, qo = sum(lq), _starts(lq).astype(np.int32)
+            wide = _randn(3, (L, T + 5, H * G, D), "bf16")
+            q, want, out = wide[:, :T].contiguous(), torch.empty_like(wide[:, :T]), torch.full_like(wide, 7.0)
+            pool.page_attention(pages, t, [90, 50], qo, q, want)
+            if L == 1:
+                pool.page_attention(pages, t, [90, 50], qo, wide, out)
+                torch.cuda.synchronize()
+                assert torch.equal(out[:, :T], want) and (out[:, T:] == 7.0).all()
+            else:
+                for a, b in ((wide, out), (q, out), (wide, want.clone())):
+                    with pytest.raises(ValueError, match="tokens in each layer"):
+                        pool.page_attention(pages, t, [90, 50], qo, a, b)
+            pool.check()

@@ -381,3 +381,26 @@ def test_page_path_before_any_call(lib, pool):
     from rag_precomputed_kv_gb300 import kvr
     assert lib.kvr_page_path(None) == -2
     assert lib.kvr_page_path(pool) == kvr.PAGE_NONE
+
+
+def test_binding_refuses_queries_padded_on_the_token_axis(lib, pool):
+    """[layers, more tokens than the offsets say, heads, head_dim]: its layers are not where the library takes them."""
+    import torch
+    from rag_precomputed_kv_gb300 import kvr
+    own, pages = object.__new__(kvr.Pool), object.__new__(kvr.Pages)
+    own.__dict__.update(_h=pool, n_layers=L, n_kv_heads=H, n_q_heads=H * G, head_dim=D, dtype=torch.bfloat16, _layout=(L, H, D), _wide=H * G * D)
+    desc = _pages()
+    pages.__dict__.update(shape=(L, H, D), dtype=torch.bfloat16, page_rows=64, _d=desc, _p=ctypes.addressof(desc))
+    right, wide = (torch.zeros((L, n, H * G, D), dtype=torch.bfloat16) for n in (3, 5))
+    try:
+        for q, out in ((wide, right), (right, wide), (wide, wide)):
+            with pytest.raises(ValueError, match="must hold 3 tokens in each layer"):
+                own.page_attention(pages, [[0]], [9], [0, 3], q, out, stream=0)
+        for q in (right, wide.view(-1), wide.view(L, -1)):      # (as it should be, and buffers without a token axis: on to the next check)
+            with pytest.raises(ValueError, match="device memory"):
+                own.page_attention(pages, [[0]], [9], [0, 3], q, right, stream=0)
+        own.n_layers = 1                                        # one layer: tokens behind the last are left alone
+        with pytest.raises(ValueError, match="device memory"):
+            own.page_attention(pages, [[0]], [9], [0, 3], wide[:1], right[:1], stream=0)
+    finally:
+        own._h = None
